@@ -404,7 +404,8 @@ def _handles(s):
     if "k_pool" in s:
         own_["cache"] = kvq.BlockKVCache(s["k_pool"], s["v_pool"], s["scales"])
     if "n_max" in s:
-        own_["ws"] = kvq.block_workspace(s["n_max"], case["hq"], case["hkv"], case["d"])
+        own_["ws"] = kvq.block_workspace(case["b"], s["n_max"], case["hq"], case["hkv"],
+                                         case["d"])
     return own_
 
 
