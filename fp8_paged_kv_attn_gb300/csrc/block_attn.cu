@@ -1,0 +1,1044 @@
+// kvq_block_attn: causal attention of one or several query rows a request over
+// the block-scaled paged cache.
+//
+// Mathematics (include/kvq.h): with the page's scales ks, vs of the kv head,
+//     x_j = sm_scale log2(e) ks (q . code_j),  out = sum_j 2^(x_j - m) vs code'_j / sum_j 2^(x_j - m)
+// in one pass over the tokens.  Each row keeps two running references: m, the
+// maximum of x, for the denominator l, and n, the maximum of x + log2(vs),
+// for the accumulators o.  The weights of a tile are w_j = 2^(x_j - m) for l and
+// w_j vs 2^(m - n) for o, so the f16 operand of p.v is at most 2^8 (lazy
+// rescaling) however the scales of the V blocks differ, and a block of large
+// values with a small softmax weight keeps its precision beside a block of
+// small values with a large one.  out = 2^(n - m) o / l.
+//
+// Bound: HBM.  A request's K and V are read once for all query heads of a kv
+// head and all its rows (up to 128 rows x heads a kv head).
+//
+//   split   persistent CTAs; the requests' (kv-head group, row block) rows, in
+//           units of 16 tokens, are laid end to end and cut into equal runs
+//           (find_run: every CTA works out its own start, so the call needs no
+//           plan kernel at any batch size).  A producer warp walks the run, stages
+//           16 tokens of a group of HG heads per TMA copy into a ring (the pool
+//           layout makes them one box) and the blocks' scales by 8-byte async
+//           copies that count on the same barrier.  Eight consumer warps: HG
+//           heads x RT 16-row tiles x TW teams that take the ring's stages in
+//           turn, so that few heads or few rows still occupy every warp.  At
+//           the end of a segment the teams' partials meet in shared memory.
+//   combine merges rows that were cut across CTAs.
+//
+// q.k and p.v run on mma.sync m16n8k16 (f16 in, fp32 sums): at up to 16 rows a
+// tile the tensor work is about half of what the memory time allows, and the
+// operands come from registers in the layout that the byte conversion leaves
+// them in.  e4m3 is exact in f16; a row of q is scaled by a power of two into
+// f16's range (exact down to 2^-39 of its largest value); weights are split
+// into an f16 and its f16 remainder (relative error 2^-22), because one f16
+// alone (2^-11) would be visible in an fp32 output.
+//
+// Every wait is bounded; one that gives up raises KVQ_ERRBIT_TIMEOUT, and the
+// CTA leaves after its copies have landed.
+#include <atomic>
+
+#include "block_common.cuh"
+#include "decode_common.cuh"
+#include "decode_attn_mma.cuh"
+
+namespace kvq {
+
+constexpr int kBaWarps = 8;                      // consumer warps
+constexpr int kBaThreads = 32 * (kBaWarps + 1);
+constexpr int kBaMaxStages = 24;
+constexpr int kBaSegs = 4;                       // segment descriptors in flight
+constexpr int kBaSmem = 220 * 1024;              // ring + merge area + control, per CTA
+constexpr int kStat = 4;                         // floats after a row's accumulators: m, l, n, -
+
+// Row tiles: 4 (one MMA column block carries the weights and their remainders),
+// 8 or 16 rows a warp; larger row counts take RT tiles of 16.
+struct BaShape {
+  int rk, rt, hg, tw;   // rows a warp, row tiles, heads a stage, teams
+  int rows;             // rows a row block holds: rk * rt
+  int row_blocks;       // row blocks of a request of max_q rows
+  int groups;           // head groups
+  int warps() const { return hg * rt * tw; }
+};
+
+inline BaShape ba_shape(int max_q, int G, int Hkv) {
+  BaShape s;
+  const int64_t rows = static_cast<int64_t>(max_q) * G;
+  s.rk = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
+  s.rt = 1;
+  while (s.rt < kBaWarps && s.rk * s.rt < rows) s.rt *= 2;
+  s.rows = s.rk * s.rt;
+  s.row_blocks = static_cast<int>((rows + s.rows - 1) / s.rows);
+  s.hg = 1;
+  for (int h = 1; h <= kBaWarps / s.rt; ++h)
+    if (Hkv % h == 0) s.hg = h;
+  s.groups = Hkv / s.hg;
+  s.tw = kBaWarps / (s.hg * s.rt);
+  return s;
+}
+
+// One segment: a run of units of one row, of one CTA.
+struct BaSeg {
+  int b, grp, rb;      // request (-1: no more segments), head group, row block
+  int row0, n, L;      // the request's first row, rows, length
+  int t_begin, t_end;  // tokens
+  int stages;
+  int part;            // -1: the row is this segment alone; else the partial slot
+};
+
+struct BaCtl {
+  BaSeg seg[kBaSegs];
+  uint64_t full[kBaMaxStages], empty[kBaMaxStages];
+  uint64_t segfull[kBaSegs], segempty[kBaSegs];
+  uint64_t mfull[kBaWarps], mempty[kBaWarps];  // per (head, row tile): the teams' merge
+  float2 sc[kBaMaxStages][kBaWarps];           // (K, V) scale of the stage's heads
+  int bad[kBaMaxStages];
+  RunScan<kBaThreads> scan;
+  int fail;
+};
+
+struct BaArgs {
+  const uint16_t *q;
+  int64_t q_stride;
+  Ragged rg;
+  const int32_t *block_table;
+  const uint8_t *abort_mask;
+  const float2 *scales;  // [num_pages][Hkv]
+  int2 *desc;            // [B][row_blocks][groups]: (first CTA, parts) of every row of work
+  float *part;           // [2 CTAs][hg * rt][rk][D + kStat]
+  float *out;
+  uint32_t *err_word;
+  int32_t num_pages, P, Hkv, Hq, G, MP, max_q;
+  int32_t hg, rt, tw, row_blocks, groups, stages;
+  float q_scale;  // sm_scale * log2(e)
+};
+
+// Request b's rows, with what attention refuses; `live`: it has work.
+__device__ __forceinline__ Rows ba_rows(const BaArgs &a, int b, bool &live) {
+  Rows r = request_rows<true>(a.rg, b);
+  if (!r.err && r.n > a.max_q) r.err = KVQ_ERRBIT_SEQLEN;
+  live = r.n > 0 && !r.err && !(a.abort_mask && __ldg(a.abort_mask + b) != 0);
+  return r;
+}
+
+// Units of one row of work and row blocks of a live request.
+__device__ __forceinline__ int ba_units(const Rows &r) { return (r.p0 + r.n + kTile - 1) / kTile; }
+__device__ __forceinline__ int ba_blocks(const BaArgs &a, const Rows &r, int rows) {
+  return (r.n * a.G + rows - 1) / rows;
+}
+
+__device__ __forceinline__ bool ba_wait(BaCtl &ctl, uint64_t *bar, uint32_t parity,
+                                        uint32_t *err_word) {
+  volatile int *fail = &ctl.fail;
+  if (*fail) return false;
+  if (mbar_wait(bar, parity)) return true;
+  if (atomicExch(&ctl.fail, 1) == 0) report(err_word, KVQ_ERRBIT_TIMEOUT);
+  return false;
+}
+
+// The same for a whole warp, which leaves or stays together.
+__device__ __forceinline__ bool ba_wait_warp(BaCtl &ctl, uint64_t *bar, uint32_t parity,
+                                             uint32_t *err_word) {
+  return __all_sync(0xffffffffu, ba_wait(ctl, bar, parity, err_word));
+}
+
+__device__ __forceinline__ void cp_async8(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src)
+               : "memory");
+}
+
+// Arrives on the barrier once this thread's async copies so far have landed
+// (the arrival is one of the barrier's expected count).
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+
+// Byte offset of 16-byte chunk c of row r in a head's swizzled 16-row block.
+template <int D>
+__device__ __forceinline__ int swz(int r, int c) {
+  return D == 128 ? r * 128 + ((c ^ (r & 7)) * 16) : r * 64 + ((c ^ ((r >> 1) & 3)) * 16);
+}
+
+// A consumer warp's state: RK rows of one kv head.
+template <int D, int RK>
+struct BaState {
+  static constexpr int KS = D / 16;            // k-steps of q.k, 16-dim tiles of p.v
+  static constexpr int NG = RK == 16 ? 2 : 1;  // 8-row groups
+  uint32_t qa[NG][2][KS];                      // A fragments: rows gq (+8), words 0 and 2
+  float o[KS][NG][4];
+  float m[NG], l[NG], n[NG], qk[NG];
+  int lim[NG];                                 // tokens that the lane's row sees
+};
+
+// The row of lane group gq in 8-row group g (copies of rows 0..3 in 4..7 for RK 4).
+template <int RK>
+__device__ __forceinline__ int lane_row(int gq, int g) {
+  return RK == 4 ? (gq & 3) : gq + 8 * g;
+}
+
+template <int D, int RK>
+__device__ __forceinline__ void ba_load_q(BaState<D, RK> &st, const BaArgs &a, const BaSeg &sg,
+                                          int kvh, int row_base, int gq, int tq) {
+  constexpr int KS = BaState<D, RK>::KS, NG = BaState<D, RK>::NG, W = D / 4;  // dims a lane
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const int r = row_base + lane_row<RK>(gq, g);
+    const int i = r / a.G;
+    float x[W];
+    const bool ok = i < sg.n;
+    st.lim[g] = ok ? sg.L - sg.n + 1 + i : sg.L;
+    if (ok) {
+      const uint16_t *p = a.q + (sg.row0 + i) * a.q_stride +
+                          static_cast<int64_t>(kvh * a.G + r - i * a.G) * D + W * tq;
+#pragma unroll
+      for (int c = 0; c < W / 8; ++c)
+        unpack8(__ldg(reinterpret_cast<const uint4 *>(p) + c), x + 8 * c);
+    } else {
+#pragma unroll
+      for (int c = 0; c < W; ++c) x[c] = 0.f;
+    }
+    float mx = 0.f;
+#pragma unroll
+    for (int c = 0; c < W; ++c) mx = fmaxf(mx, fabsf(x[c]));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    // 2^e puts the row's largest value into [2^14, 2^15)
+    int e = mx > 0.f && mx < INFINITY ? 14 - ilogbf(mx) : 0;
+    e = min(e, 126);
+    const float up = pow2(e);  // e >= 14 - 127
+    st.qk[g] = a.q_scale * pow2(-e);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      st.qa[g][0][s] = f32x2_to_f16x2(x[4 * s] * up, x[4 * s + 1] * up);
+      st.qa[g][1][s] = f32x2_to_f16x2(x[4 * s + 2] * up, x[4 * s + 3] * up);
+    }
+    st.m[g] = st.n[g] = -INFINITY;
+    st.l[g] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) st.o[k][g][0] = st.o[k][g][1] = st.o[k][g][2] = st.o[k][g][3] = 0.f;
+  }
+}
+
+// p.v of one tile: words wa..wd are V rows 2t, 2t+1, 2t+8, 2t+9 at the lane's
+// D / 8 dims; hi / lo the weights' f16 and remainders per row group and n-tile.
+template <int D, int RK>
+__device__ __forceinline__ void ba_pv(float (&o)[D / 16][BaState<D, RK>::NG][4],
+                                      const uint32_t (&wa)[D / 32], const uint32_t (&wb)[D / 32],
+                                      const uint32_t (&wc)[D / 32], const uint32_t (&wd)[D / 32],
+                                      const uint32_t (&hi)[BaState<D, RK>::NG][2],
+                                      const uint32_t (&lo)[BaState<D, RK>::NG][2]) {
+  constexpr int KS = D / 16, NG = BaState<D, RK>::NG;
+#pragma unroll
+  for (int i = 0; i < KS; ++i) {
+    const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;  // bytes (a.b, b.b, a.b+1, b.b+1)
+    const uint32_t x = prmt(wa[i >> 1], wb[i >> 1], sel);
+    const uint32_t y = prmt(wc[i >> 1], wd[i >> 1], sel);
+    const uint32_t a0 = e4m3x2_to_f16x2(x & 0xFFFFu), a1 = e4m3x2_to_f16x2(x >> 16);
+    const uint32_t a2 = e4m3x2_to_f16x2(y & 0xFFFFu), a3 = e4m3x2_to_f16x2(y >> 16);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      mma_16816(o[i][g], a0, a1, a2, a3, hi[g][0], hi[g][1]);
+      if constexpr (RK > 4) mma_16816(o[i][g], a0, a1, a2, a3, lo[g][0], lo[g][1]);
+    }
+  }
+}
+
+// NaN codes anywhere in a word of four
+__device__ __forceinline__ bool has_nan(uint32_t w) {
+  return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
+}
+
+// A tile where some row does not see every token, and V holds a NaN code: a
+// weight of 0 does not stop a NaN, so every row's sum must leave the tokens out
+// that it does not see.  Once for each of the tile's visibility limits, V
+// rows beyond it zeroed, into sums of their own that only the rows with that
+// limit take.  Rare (a NaN has been cached), so out of line.
+template <int D, int RK>
+struct BaMasked {
+  static constexpr int KS = D / 16, NG = BaState<D, RK>::NG, W = D / 32;
+  float o[KS][NG][4];
+  uint32_t v[4][W], hi[NG][2], lo[NG][2];
+  int lim[NG], tok0, tq;
+};
+
+template <int D, int RK>
+__device__ __noinline__ void ba_pv_masked(BaMasked<D, RK> &x) {
+  constexpr int KS = D / 16, NG = BaState<D, RK>::NG, W = D / 32;
+  for (int seen = 1; seen <= kTile; ++seen) {
+    uint32_t w[4][W];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int c = 0; c < W; ++c)
+        w[k][c] = 2 * x.tq + (k & 1) + 8 * (k >> 1) < seen ? x.v[k][c] : 0u;
+    float tmp[KS][NG][4];
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int g = 0; g < NG; ++g) tmp[i][g][0] = tmp[i][g][1] = tmp[i][g][2] = tmp[i][g][3] = 0.f;
+    ba_pv<D, RK>(tmp, w[0], w[1], w[2], w[3], x.hi, x.lo);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int mine = min(x.lim[g] - x.tok0, kTile);  // the lane's row; its columns are rows 2t, 2t+1
+      const int sa = __shfl_sync(0xffffffffu, mine, 8 * x.tq);
+      const int sb = __shfl_sync(0xffffffffu, mine, 8 * x.tq + 4);
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        if (sa == seen) {
+          x.o[i][g][0] += tmp[i][g][0];
+          x.o[i][g][2] += tmp[i][g][2];
+        }
+        if (sb == seen) {
+          x.o[i][g][1] += tmp[i][g][1];
+          x.o[i][g][3] += tmp[i][g][3];
+        }
+      }
+    }
+  }
+}
+
+// One 16-token tile: ks / vs the head's swizzled blocks, tok0 its first token,
+// min_lim the fewest tokens that a row of the row block sees, L the length.
+template <int D, int RK>
+__device__ __forceinline__ void ba_tile(BaState<D, RK> &st, const uint8_t *ks, const uint8_t *vs,
+                                        float2 sc, int tok0, int min_lim, int L, int gq, int tq) {
+  constexpr int KS = BaState<D, RK>::KS, NG = BaState<D, RK>::NG, W = D / 32;
+  uint32_t kw[2][KS];  // rows gq and 8 + gq, the lane's D / 4 dims
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      const uint4 x = lds128(ks + swz<D>(gq + 8 * j, (D / 64) * tq + c));
+      kw[j][4 * c] = x.x;
+      kw[j][4 * c + 1] = x.y;
+      kw[j][4 * c + 2] = x.z;
+      kw[j][4 * c + 3] = x.w;
+    }
+  uint32_t v[4][W];  // V rows 2t, 2t+1, 2t+8, 2t+9 at dims (D / 8) gq ..
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = 2 * tq + (k & 1) + 8 * (k >> 1);
+    if constexpr (D == 128) {
+      const uint4 x = lds128(vs + swz<D>(r, gq));
+      v[k][0] = x.x;
+      v[k][1] = x.y;
+      v[k][2] = x.z;
+      v[k][3] = x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2 *>(vs + swz<D>(r, gq >> 1) + 8 * (gq & 1));
+      v[k][0] = x.x;
+      v[k][1] = x.y;
+    }
+  }
+  // q.k: even and odd k-steps in sums of their own (shorter dependency chains)
+  float s[2][2][4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) s[j][e][0] = s[j][e][1] = s[j][e][2] = s[j][e][3] = 0.f;
+#pragma unroll
+  for (int k = 0; k < KS; ++k)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      mma_16816(s[j][k & 1], st.qa[0][0][k], NG == 2 ? st.qa[NG - 1][0][k] : 0u, st.qa[0][1][k],
+                NG == 2 ? st.qa[NG - 1][1][k] : 0u, e4m3x2_to_f16x2(kw[j][k] & 0xFFFFu),
+                e4m3x2_to_f16x2(kw[j][k] >> 16));
+  const bool partial = tok0 + kTile > min_lim;  // uniform over the warp
+  // log2 of the V scale, rounded up: exact for a power of two
+  const uint32_t vu = __float_as_uint(sc.y);
+  const int ve = static_cast<int>(vu >> 23) - 127 + ((vu & 0x7FFFFFu) ? 1 : 0);
+  const float lv = static_cast<float>(ve);
+  float x[NG][2][2];
+  float mx[NG], mv[NG];
+  bool grow_l[NG], grow_o[NG];
+  bool any = false;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const float f = st.qk[g] * sc.x;
+    const int seen = st.lim[g] - tok0;
+    mx[g] = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        x[g][j][e] = (s[j][0][2 * g + e] + s[j][1][2 * g + e]) * f;
+        if (partial && 8 * j + 2 * tq + e >= seen) x[g][j][e] = -INFINITY;
+        mx[g] = fmaxf(mx[g], x[g][j][e]);
+      }
+    mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], 1));
+    mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], 2));
+    mv[g] = mx[g] + lv;
+    grow_l[g] = mx[g] > st.m[g] + kRescaleThreshold;
+    grow_o[g] = mv[g] > st.n[g] + kRescaleThreshold;
+    any |= grow_l[g] | grow_o[g];
+  }
+  if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      if (grow_l[g]) {
+        st.l[g] *= exp2f(st.m[g] - mx[g]);  // 0 when m is -inf
+        st.m[g] = mx[g];
+      }
+      const float f = grow_o[g] ? exp2f(st.n[g] - mv[g]) : 1.f;
+      if (grow_o[g]) st.n[g] = mv[g];
+      const float fa = __shfl_sync(0xffffffffu, f, 8 * tq);
+      const float fb = __shfl_sync(0xffffffffu, f, 8 * tq + 4);
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        st.o[i][g][0] *= fa;
+        st.o[i][g][1] *= fb;
+        st.o[i][g][2] *= fa;
+        st.o[i][g][3] *= fb;
+      }
+    }
+  }
+  uint32_t hi[NG][2], lo[NG][2];
+  const float vm = sc.y * pow2(max(-126, min(127, -ve)));  // the V scale's fraction, (0.5, 1]
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    // vs 2^(m - n), with kPScale (2^7) so that the largest weights sit high in
+    // f16's range; the clamp only meets rows whose weights here are below
+    // 2^-112 of their largest
+    const float d = st.n[g] == -INFINITY
+                        ? 0.f
+                        : vm * kPScale * fast_exp2(fminf(st.m[g] - st.n[g] + lv, 112.f));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float p0 = x[g][j][0] == -INFINITY ? 0.f : fast_exp2(x[g][j][0] - st.m[g]);
+      const float p1 = x[g][j][1] == -INFINITY ? 0.f : fast_exp2(x[g][j][1] - st.m[g]);
+      st.l[g] += p0 + p1;
+      const float w0 = p0 * d, w1 = p1 * d;
+      const uint32_t h = f32x2_to_f16x2(w0, w1);
+      const float2 hf = f16x2_to_f32x2(h);
+      const uint32_t r = f32x2_to_f16x2(w0 - hf.x, w1 - hf.y);
+      hi[g][j] = RK == 4 && gq >= 4 ? r : h;
+      lo[g][j] = r;
+    }
+  }
+  if (partial) {
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int c = 0; c < W; ++c) {
+        // cached bytes past the sequence may be anything
+        if (tok0 + 2 * tq + (k & 1) + 8 * (k >> 1) >= L) v[k][c] = 0u;
+        bad |= has_nan(v[k][c]);
+      }
+    if (__any_sync(0xffffffffu, bad)) {
+      BaMasked<D, RK> x2;  // copies: the state's own registers keep no address
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x2.o[i][g][k] = st.o[i][g][k];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int c = 0; c < W; ++c) x2.v[k][c] = v[k][c];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          x2.hi[g][j] = hi[g][j];
+          x2.lo[g][j] = lo[g][j];
+        }
+        x2.lim[g] = st.lim[g];
+      }
+      x2.tok0 = tok0;
+      x2.tq = tq;
+      ba_pv_masked<D, RK>(x2);
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) st.o[i][g][k] = x2.o[i][g][k];
+      return;
+    }
+  }
+  ba_pv<D, RK>(st.o, v[0], v[1], v[2], v[3], hi, lo);
+}
+
+// ---------------------------------------------------------------------------
+// the split kernel
+// ---------------------------------------------------------------------------
+
+// Shared memory: K ring, V ring, merge area (teams only), control.
+template <int D>
+__host__ __device__ constexpr size_t ba_stage_bytes(int hg) {
+  return static_cast<size_t>(hg) * kTile * D;
+}
+
+inline size_t ba_merge_floats(const BaShape &s, int D) {
+  return s.tw > 1 ? static_cast<size_t>(s.warps()) * s.rk * (D + kStat) : 0;
+}
+
+inline int ba_stages(const BaShape &s, int D) {
+  const size_t stage = 2 * static_cast<size_t>(s.hg) * kTile * D;
+  const size_t room = kBaSmem - 1024 - sizeof(BaCtl) - ba_merge_floats(s, D) * sizeof(float);
+  const size_t n = room / stage;
+  return static_cast<int>(n < kBaMaxStages ? n : kBaMaxStages);
+}
+
+// Row r (of the request) as an output row's address.
+template <int D>
+__device__ __forceinline__ float *ba_out_row(const BaArgs &a, const BaSeg &sg, int kvh, int r) {
+  const int i = r / a.G;
+  return a.out + ((static_cast<int64_t>(sg.row0) + i) * a.Hq + kvh * a.G + r - i * a.G) * D;
+}
+
+template <int D, int RK>
+__global__ void __launch_bounds__(kBaThreads, 1)
+    block_split_kernel(const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap, BaArgs a) {
+  using St = BaState<D, RK>;
+  constexpr int KS = St::KS, NG = St::NG, RF = D + kStat;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);  // for the swizzle
+  const uint32_t stage_bytes = static_cast<uint32_t>(ba_stage_bytes<D>(a.hg));
+  const int NS = a.stages;
+  uint8_t *kbuf = smem;
+  uint8_t *vbuf = smem + static_cast<size_t>(NS) * stage_bytes;
+  float *area = reinterpret_cast<float *>(smem + 2 * static_cast<size_t>(NS) * stage_bytes);
+  const int ngrp = a.hg * a.rt;  // (head, row tile) pairs
+  BaCtl &ctl = *reinterpret_cast<BaCtl *>(area + (a.tw > 1 ? ngrp * a.tw * RK * RF : 0));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = RK * a.rt;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&ctl.full[i], 1 + a.hg);
+      mbar_init(&ctl.empty[i], ngrp);
+    }
+    for (int i = 0; i < kBaSegs; ++i) {
+      mbar_init(&ctl.segfull[i], 1);
+      mbar_init(&ctl.segempty[i], ngrp * a.tw);
+    }
+    for (int i = 0; i < ngrp; ++i) {
+      mbar_init(&ctl.mfull[i], a.tw);
+      mbar_init(&ctl.mempty[i], a.tw);
+    }
+    ctl.fail = 0;
+    fence_barrier_init();
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  const RunStart run = find_run<kBaThreads>(
+      a.rg.B, gridDim.x, blockIdx.x, ctl.scan, [&](int b) -> int64_t {
+        bool live;
+        const Rows r = ba_rows(a, b, live);
+        if (r.err && blockIdx.x == 0) report(a.err_word, r.err);
+        return live ? static_cast<int64_t>(ba_units(r)) * a.groups * ba_blocks(a, r, rows) : 0;
+      });
+  allow_dependents();
+  const int64_t u0 = blockIdx.x * run.per;
+  const int64_t u1 = min(u0 + run.per, run.total);
+
+  if (warp == kBaWarps) {
+    // ------------------------------------------------------------ producer
+    const uint64_t pol = policy_evict_first();
+    int64_t u = u0, in = run.in;
+    int b = run.b;
+    uint32_t g = 0, nseg = 0;  // stages and segments issued
+    bool ok = true;
+    int win_b = -1, win = 0, cur = -1, nxt = -1;  // block-table window (two of 32 entries)
+    const int32_t *bt = a.block_table;
+    auto bt_load = [&](int lp) -> int { return lp < a.MP ? __ldg(bt + lp) : -1; };
+    while (ok && u < u1) {
+      bool live;
+      const Rows rq = ba_rows(a, b, live);
+      const int units = live ? ba_units(rq) : 0;
+      const int64_t have = live ? static_cast<int64_t>(units) * a.groups * ba_blocks(a, rq, rows) : 0;
+      if (in >= have) {
+        ++b;
+        in = 0;
+        continue;
+      }
+      const int64_t rw = in / units;  // row of work: row block major
+      const int s = static_cast<int>(in - rw * units);
+      const int rb = static_cast<int>(rw / a.groups), grp = static_cast<int>(rw - static_cast<int64_t>(rb) * a.groups);
+      const int take = static_cast<int>(min(static_cast<int64_t>(units - s), u1 - u));
+      const int L = rq.p0 + rq.n;
+      const int t_begin = s * kTile, t_end = min((s + take) * kTile, L);
+      const int64_t ur = u - s;  // the row's first unit
+      const int64_t c_lo = ur / run.per;
+      const int nparts = static_cast<int>((ur + units - 1) / run.per - c_lo) + 1;
+      const int ss = nseg % kBaSegs;
+      bool w = true;
+      if (lane == 0 && nseg >= kBaSegs)
+        w = ba_wait(ctl, &ctl.segempty[ss], ((nseg / kBaSegs) - 1) & 1, a.err_word);
+      ok = __shfl_sync(0xffffffffu, w ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      if (lane == 0) {
+        if (s == 0)
+          a.desc[(static_cast<int64_t>(b) * a.row_blocks + rb) * a.groups + grp] =
+              make_int2(static_cast<int>(c_lo), nparts);
+        ctl.seg[ss] = {b, grp, rb, rq.row, rq.n, L, t_begin, t_end, take,
+                       nparts == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (s == 0 ? 1 : 0)};
+        mbar_arrive(&ctl.segfull[ss]);
+      }
+      ++nseg;
+      const int lp0 = t_begin / a.P;
+      if (b != win_b || lp0 < win || lp0 >= win + 32) {
+        win_b = b;
+        win = lp0;
+        bt = a.block_table + static_cast<int64_t>(b) * a.MP;
+        cur = bt_load(win + lane);
+        nxt = bt_load(win + 32 + lane);
+      }
+      for (int st = 0; st < take; ++st, ++g) {
+        const int slot = g % NS;
+        bool waited = true;
+        if (lane == 0 && g >= NS)
+          waited = ba_wait(ctl, &ctl.empty[slot], ((g / NS) - 1) & 1, a.err_word);
+        ok = __shfl_sync(0xffffffffu, waited ? 1 : 0, 0) != 0 &&
+             !*reinterpret_cast<volatile int *>(&ctl.fail);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int tok = t_begin + st * kTile;
+        const int lp = tok / a.P;
+        while (lp >= win + 32) {
+          win += 32;
+          cur = nxt;
+          nxt = bt_load(win + 32 + lane);
+        }
+        const int page = __shfl_sync(0xffffffffu, cur, lp - win);
+        const bool bad = page < 0 || page >= a.num_pages;
+        if (lane == 0) {
+          ctl.bad[slot] = bad;
+          if (bad) report(a.err_word, KVQ_ERRBIT_PAGE);
+          mbar_arrive_expect_tx(&ctl.full[slot], bad ? 0u : 2u * stage_bytes);
+          if (!bad) {
+            const int y = tok % a.P;
+            tma_load_4d(kbuf + slot * stage_bytes, &kmap, 0, y, grp * a.hg, page, &ctl.full[slot],
+                        pol);
+            tma_load_4d(vbuf + slot * stage_bytes, &vmap, 0, y, grp * a.hg, page, &ctl.full[slot],
+                        pol);
+          }
+        }
+        if (lane < a.hg) {
+          if (!bad)
+            cp_async8(&ctl.sc[slot][lane],
+                      a.scales + static_cast<int64_t>(page) * a.Hkv + grp * a.hg + lane);
+          cp_async_arrive(&ctl.full[slot]);
+        }
+        __syncwarp();
+      }
+      u += take;
+      in += take;
+    }
+    if (ok) {  // nothing more
+      const int ss = nseg % kBaSegs;
+      if (lane == 0 && (nseg < kBaSegs ||
+                        ba_wait(ctl, &ctl.segempty[ss], ((nseg / kBaSegs) - 1) & 1, a.err_word))) {
+        ctl.seg[ss].b = -1;
+        mbar_arrive(&ctl.segfull[ss]);
+      }
+    }
+    if (*reinterpret_cast<volatile int *>(&ctl.fail)) {
+      // a wait gave up: let the copies in flight land before the CTA's shared
+      // memory goes to another one
+      if (lane == 0)
+        for (uint32_t k = g > NS ? g - NS : 0; k < g; ++k)
+          mbar_wait(&ctl.full[k % NS], (k / NS) & 1);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  // rows of requests without work (aborted, bad lengths) are zeros
+  for (int b = blockIdx.x; b < a.rg.B; b += gridDim.x) {
+    bool live;
+    const Rows r = ba_rows(a, b, live);
+    if (live || r.n == 0) continue;
+    float4 *o = reinterpret_cast<float4 *>(a.out + static_cast<int64_t>(r.row) * a.Hq * D);
+    const int64_t n4 = static_cast<int64_t>(r.n) * a.Hq * (D / 4);
+    for (int64_t k = threadIdx.x; k < n4; k += 32 * kBaWarps) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const int pair = warp % ngrp, team = warp / ngrp;  // (head, row tile), team
+  if (team >= a.tw) return;
+  const int head = pair / a.rt, tile = pair % a.rt;
+  const int gq = lane >> 2, tq = lane & 3;
+  St st;
+  uint32_t g0 = 0, nseg = 0;
+  while (true) {
+    const int ss = nseg % kBaSegs;
+    if (!ba_wait_warp(ctl, &ctl.segfull[ss], (nseg / kBaSegs) & 1, a.err_word)) return;
+    const BaSeg sg = ctl.seg[ss];
+    if (sg.b < 0) return;
+    const int kvh = sg.grp * a.hg + head;
+    const int row_base = sg.rb * rows + tile * RK;  // this warp's first row of the request
+    ba_load_q<D, RK>(st, a, sg, kvh, row_base, gq, tq);
+    const int min_lim = min(sg.L, sg.L - sg.n + 1 + (sg.rb * rows) / a.G);
+    bool seg_bad = false;
+    for (int k = team; k < sg.stages; k += a.tw) {
+      const uint32_t g = g0 + k;
+      const int slot = g % NS;
+      if (!ba_wait_warp(ctl, &ctl.full[slot], (g / NS) & 1, a.err_word)) return;
+      if (ctl.bad[slot])
+        seg_bad = true;
+      else
+        ba_tile<D, RK>(st, kbuf + slot * stage_bytes + head * (kTile * D),
+                       vbuf + slot * stage_bytes + head * (kTile * D), ctl.sc[slot][head],
+                       sg.t_begin + k * kTile, min_lim, sg.L, gq, tq);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.empty[slot]);
+    }
+    g0 += sg.stages;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl.segempty[ss]);
+
+    // ---- the segment's end
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      if constexpr (RK == 4) {  // columns 4..7 hold the remainders' sums
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            st.o[i][g][k] += __shfl_down_sync(0xffffffffu, st.o[i][g][k], 2);
+      }
+      st.l[g] += __shfl_xor_sync(0xffffffffu, st.l[g], 1);
+      st.l[g] += __shfl_xor_sync(0xffffffffu, st.l[g], 2);
+      if (seg_bad) st.l[g] = -1.f;  // marks a part that met a page outside the pool
+    }
+    const bool many = a.tw > 1;
+    const int used = min(RK, sg.n * a.G - row_base);  // rows of this warp that exist
+    float *to = many ? area + static_cast<int64_t>(warp) * RK * RF
+                     : a.part + (static_cast<int64_t>(sg.part) * ngrp + pair) * (RK * RF);
+    const bool direct = !many && sg.part < 0;
+    if (many && nseg > 0 && !ba_wait_warp(ctl, &ctl.mempty[pair], (nseg - 1) & 1, a.err_word)) return;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const float la = __shfl_sync(0xffffffffu, st.l[g], 8 * tq);
+      const float lb = __shfl_sync(0xffffffffu, st.l[g], 8 * tq + 4);
+      const float ma = __shfl_sync(0xffffffffu, st.m[g], 8 * tq);
+      const float mb = __shfl_sync(0xffffffffu, st.m[g], 8 * tq + 4);
+      const float na = __shfl_sync(0xffffffffu, st.n[g], 8 * tq);
+      const float nb = __shfl_sync(0xffffffffu, st.n[g], 8 * tq + 4);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 2 * tq + e + 8 * g;
+        if (r >= used || r >= RK) continue;
+        const float l = e ? lb : la, m = e ? mb : ma, n = e ? nb : na;
+        if (direct) {
+          // 2^(n - m) / (l 2^7); a bad row is zeros, selected and not scaled
+          const float f = l < 0.f ? 0.f : exp2f(n - m - 7.f) / l;
+          float *o = ba_out_row<D>(a, sg, kvh, row_base + r) + (D / 8) * gq;
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+            *reinterpret_cast<float2 *>(o + 2 * i) =
+                l < 0.f ? make_float2(0.f, 0.f)
+                        : make_float2(st.o[i][g][e] * f, st.o[i][g][2 + e] * f);
+        } else {
+          float *o = to + r * RF;
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+            *reinterpret_cast<float2 *>(o + (D / 8) * gq + 2 * i) =
+                make_float2(st.o[i][g][e], st.o[i][g][2 + e]);
+          if (gq == 0) *reinterpret_cast<float4 *>(o + D) = make_float4(m, l, n, 0.f);
+        }
+      }
+    }
+    if (many) {
+      // ---- the teams' partials of each row: team t merges rows t, t + tw, ...
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.mfull[pair]);
+      if (!ba_wait_warp(ctl, &ctl.mfull[pair], nseg & 1, a.err_word)) return;
+      for (int r = team; r < used; r += a.tw) {
+        float M = -INFINITY, N = -INFINITY;
+        bool bad = false;
+        for (int t = 0; t < a.tw; ++t) {
+          const float *p = area + (static_cast<int64_t>(t * ngrp + pair) * RK + r) * RF;
+          const float4 s = *reinterpret_cast<const float4 *>(p + D);
+          M = fmaxf(M, s.x);
+          N = fmaxf(N, s.z);
+          bad |= s.y < 0.f;
+        }
+        float l = 0.f;
+        float acc[D / 32];
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
+        for (int t = 0; t < a.tw; ++t) {
+          const float *p = area + (static_cast<int64_t>(t * ngrp + pair) * RK + r) * RF;
+          const float4 s = *reinterpret_cast<const float4 *>(p + D);
+          if (s.y == 0.f) continue;  // saw nothing
+          l += exp2f(s.x - M) * s.y;
+          const float f = exp2f(s.z - N);
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) acc[k] += f * p[lane + 32 * k];
+        }
+        if (sg.part < 0) {
+          const float f = bad ? 0.f : exp2f(N - M - 7.f) / l;
+          float *o = ba_out_row<D>(a, sg, kvh, row_base + r);
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) o[lane + 32 * k] = bad ? 0.f : acc[k] * f;
+        } else {
+          float *o = a.part + ((static_cast<int64_t>(sg.part) * ngrp + pair) * RK + r) * RF;
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) o[lane + 32 * k] = acc[k];
+          if (lane == 0) *reinterpret_cast<float4 *>(o + D) = make_float4(M, bad ? -1.f : l, N, 0.f);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.mempty[pair]);
+    }
+    ++nseg;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// combine: rows cut across CTAs
+// ---------------------------------------------------------------------------
+
+constexpr int kBcbWarps = 8;
+
+// Output rows (request, row block, head group, head, row tile, row), one a
+// warp (kWide false) or one a CTA whose warps take every eighth part (kWide
+// true, for batches of so few rows that one is cut into many parts).
+//   out = 2^(N - M) sum_p 2^(n_p - N) o_p / sum_p 2^(m_p - M) l_p
+template <int D, bool kWide>
+__global__ void __launch_bounds__(32 * kBcbWarps) block_combine_kernel(BaArgs a, int rk) {
+  constexpr int V = D / 32, RF = D + kStat, kBatch = 4;
+  __shared__ float s_acc[kWide ? kBcbWarps : 1][D];
+  __shared__ float4 s_st[kWide ? kBcbWarps : 1];
+  grid_dependency_wait();
+  allow_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ngrp = a.hg * a.rt, rows = rk * a.rt;
+  const int64_t total = static_cast<int64_t>(a.rg.B) * a.row_blocks * a.groups * ngrp * rk;
+  const int64_t step = kWide ? gridDim.x : static_cast<int64_t>(gridDim.x) * kBcbWarps;
+  for (int64_t it = kWide ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kBcbWarps + warp;
+       it < total; it += step) {
+    const int rr = static_cast<int>(it % rk);
+    const int64_t t1 = it / rk;
+    const int pair = static_cast<int>(t1 % ngrp);
+    const int64_t work = t1 / ngrp;  // (request, row block, group)
+    const int grp = static_cast<int>(work % a.groups);
+    const int64_t t2 = work / a.groups;
+    const int rb = static_cast<int>(t2 % a.row_blocks), b = static_cast<int>(t2 / a.row_blocks);
+    bool live;
+    const Rows rq = ba_rows(a, b, live);
+    const int r = rb * rows + (pair % a.rt) * rk + rr;
+    if (!live || r >= rq.n * a.G) continue;
+    const int2 d = __ldcg(a.desc + work);
+    if (d.y < 2) continue;
+    float M = -INFINITY, N = -INFINITY, l = 0.f, acc[V];
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+    // part p lies in CTA d.x + p's slot 0, the first one in slot 1 of CTA d.x
+    for (int p0 = kWide ? warp : 0; p0 < d.y; p0 += kBatch * (kWide ? kBcbWarps : 1)) {
+      float4 s[kBatch];
+      float v[kBatch][V];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int p = p0 + j * (kWide ? kBcbWarps : 1);
+        s[j] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        if (p < d.y) {
+          const float *q = a.part + ((static_cast<int64_t>(2 * (d.x + p) + (p == 0)) * ngrp + pair) * rk + rr) * RF;
+          s[j] = __ldcg(reinterpret_cast<const float4 *>(q + D));
+#pragma unroll
+          for (int k = 0; k < V; ++k) v[j][k] = __ldcg(q + lane + 32 * k);
+        }
+      }
+      float Mb = M, Nb = N;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        Mb = fmaxf(Mb, s[j].x);
+        Nb = fmaxf(Nb, s[j].z);
+        bad |= s[j].y < 0.f;
+      }
+      const float fl = M == -INFINITY ? 0.f : exp2f(M - Mb), fo = N == -INFINITY ? 0.f : exp2f(N - Nb);
+      l *= fl;
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[k] *= fo;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (s[j].y == 0.f) continue;  // saw nothing
+        l = fmaf(exp2f(s[j].x - Mb), s[j].y, l);
+        const float f = exp2f(s[j].z - Nb);
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = fmaf(f, v[j][k], acc[k]);
+      }
+      M = Mb;
+      N = Nb;
+    }
+    const int i = r / a.G;
+    float *out = a.out + ((static_cast<int64_t>(rq.row) + i) * a.Hq + (grp * a.hg + pair / a.rt) * a.G + r - i * a.G) * D;
+    if constexpr (!kWide) {
+      const float f = bad ? 0.f : exp2f(N - M - 7.f) / l;
+#pragma unroll
+      for (int k = 0; k < V; ++k) out[lane + 32 * k] = bad ? 0.f : acc[k] * f;
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) s_acc[warp][lane + 32 * k] = acc[k];
+      if (lane == 0) s_st[warp] = make_float4(M, bad ? -1.f : l, N, 0.f);
+      __syncthreads();
+      if (threadIdx.x < D) {
+        float Mr = -INFINITY, Nr = -INFINITY, lr = 0.f, o = 0.f;
+        bool rbad = false;
+#pragma unroll
+        for (int w = 0; w < kBcbWarps; ++w) {
+          Mr = fmaxf(Mr, s_st[w].x);
+          Nr = fmaxf(Nr, s_st[w].z);
+          rbad |= s_st[w].y < 0.f;
+        }
+#pragma unroll
+        for (int w = 0; w < kBcbWarps; ++w) {
+          if (s_st[w].y == 0.f) continue;
+          lr = fmaf(exp2f(s_st[w].x - Mr), s_st[w].y, lr);
+          o = fmaf(exp2f(s_st[w].z - Nr), s_acc[w][threadIdx.x], o);
+        }
+        out[threadIdx.x] = rbad ? 0.f : o * (exp2f(Nr - Mr - 7.f) / lr);
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+namespace {
+
+using BaFn = void (*)(CUtensorMap, CUtensorMap, BaArgs);
+
+template <int D>
+BaFn ba_kernel(int rk) {
+  return rk == 4 ? block_split_kernel<D, 4>
+                 : rk == 8 ? block_split_kernel<D, 8> : block_split_kernel<D, 16>;
+}
+
+// Opt a kernel into its shared memory, once per device.
+bool ba_opt_in(BaFn fn, int variant) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<bool> done[kMaxDev][6];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return false;
+  if (done[dev][variant].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kBaSmem) !=
+      cudaSuccess)
+    return false;
+  done[dev][variant].store(true, std::memory_order_release);
+  return true;
+}
+
+size_t ba_desc_bytes(int64_t B, const BaShape &s) {
+  return (static_cast<size_t>(B) * s.row_blocks * s.groups * sizeof(int2) + 255) & ~size_t(255);
+}
+
+size_t ba_part_bytes(const BaShape &s, int D, int ctas) {
+  return 2ull * ctas * s.hg * s.rt * s.rk * (D + kStat) * sizeof(float);
+}
+
+// [page][head][slot][dim] as a 4-D map; a box is 16 slots of hg heads.
+bool ba_map(CUtensorMap *map, const void *pool, const kvq_block_cache &c, int hg) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t D = c.head_dim, P = c.page_size, H = c.num_kv_heads, NP = c.num_pages;
+  const cuuint64_t dims[4] = {D, P, H, NP};
+  const cuuint64_t strides[3] = {D, P * D, H * P * D};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(kTile),
+                             static_cast<cuuint32_t>(hg), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(pool), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" size_t kvq_block_attn_workspace_size(int32_t B, int32_t max_q, int32_t Hq,
+                                                int32_t num_kv_heads, int32_t head_dim) {
+  if (B < 0 || max_q <= 0 || Hq <= 0 || num_kv_heads <= 0 || Hq % num_kv_heads) return 0;
+  if (head_dim != 64 && head_dim != 128) return 0;
+  if (static_cast<int64_t>(max_q) * (Hq / num_kv_heads) > INT32_MAX / 2) return 0;
+  int sms = 0;
+  if (device_sm_count(&sms) != KVQ_OK) return 0;
+  const BaShape s = ba_shape(max_q, Hq / num_kv_heads, num_kv_heads);
+  return ba_desc_bytes(B, s) + ba_part_bytes(s, head_dim, sms);
+}
+
+extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q, int64_t q_stride,
+                                     int32_t Hq, const int32_t *tok_start, int32_t n_tokens,
+                                     int32_t max_q, const int32_t *seq_lens,
+                                     const int32_t *block_table, int32_t B, int32_t MP,
+                                     const uint8_t *abort_mask, float sm_scale, float *out,
+                                     void *workspace, size_t workspace_bytes, uint32_t *err_word,
+                                     kvq_stream_t stream) {
+  kvq_status st = validate_block_cache(cache);
+  if (st != KVQ_OK) return st;
+  const int D = cache->head_dim, Hkv = cache->num_kv_heads;
+  st = validate_ragged(tok_start, n_tokens, block_table, B, MP, cache->page_size);
+  if (st != KVQ_OK) return st;
+  if (Hq <= 0 || Hq % Hkv || max_q <= 0 || !std::isfinite(sm_scale)) return KVQ_ERR_INVALID_ARG;
+  const int G = Hq / Hkv;
+  if (static_cast<int64_t>(max_q) * G > INT32_MAX / 2) return KVQ_ERR_INVALID_ARG;
+  if (n_tokens == 0 || B == 0) return KVQ_OK;
+  if (!seq_lens || !out || !workspace || !aligned16(out) || !rows_ok(q, q_stride, Hq, D))
+    return KVQ_ERR_INVALID_ARG;
+  int sms = 0;
+  if (device_sm_count(&sms) != KVQ_OK) return KVQ_ERR_CUDA;
+  const BaShape s = ba_shape(max_q, G, Hkv);
+  const size_t db = ba_desc_bytes(B, s);
+  if (!aligned256(workspace) || workspace_bytes < db + ba_part_bytes(s, D, sms))
+    return KVQ_ERR_WORKSPACE;
+  BaArgs a;
+  a.q = static_cast<const uint16_t *>(q);
+  a.q_stride = q_stride;
+  a.rg = {tok_start, seq_lens, B, n_tokens, static_cast<int64_t>(MP) * cache->page_size};
+  a.block_table = block_table;
+  a.abort_mask = abort_mask;
+  a.scales = reinterpret_cast<const float2 *>(cache->scales);
+  a.desc = static_cast<int2 *>(workspace);
+  a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + db);
+  a.out = out;
+  a.err_word = err_word;
+  a.num_pages = cache->num_pages;
+  a.P = cache->page_size;
+  a.Hkv = Hkv;
+  a.Hq = Hq;
+  a.G = G;
+  a.MP = MP;
+  a.max_q = max_q;
+  a.hg = s.hg;
+  a.rt = s.rt;
+  a.tw = s.tw;
+  a.row_blocks = s.row_blocks;
+  a.groups = s.groups;
+  a.stages = ba_stages(s, D);
+  a.q_scale = sm_scale * kLog2e;
+  const BaFn fn = D == 128 ? ba_kernel<128>(s.rk) : ba_kernel<64>(s.rk);
+  if (!ba_opt_in(fn, (D == 128 ? 3 : 0) + (s.rk == 4 ? 0 : s.rk == 8 ? 1 : 2))) return KVQ_ERR_CUDA;
+  CUtensorMap kmap, vmap;
+  if (!ba_map(&kmap, cache->k_pool, *cache, s.hg) || !ba_map(&vmap, cache->v_pool, *cache, s.hg))
+    return KVQ_ERR_CUDA;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (launch_dependent(fn, sms, kBaThreads, kBaSmem, cs, kmap, vmap, a) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  // rows of work a CTA: with fewer than one in three, a row is cut into four
+  // parts or more, and a CTA merges each of its output rows
+  const int64_t work = static_cast<int64_t>(B) * s.row_blocks * s.groups;
+  const int64_t outs = work * s.hg * s.rt * s.rk;
+  const bool wide = work * 3 < sms;
+  const int64_t want = wide ? outs : (outs + kBcbWarps - 1) / kBcbWarps;
+  const int64_t most = 8LL * sms;
+  const int grid = static_cast<int>(want < most ? want : most);
+  const auto cfn = D == 128 ? (wide ? block_combine_kernel<128, true> : block_combine_kernel<128, false>)
+                            : (wide ? block_combine_kernel<64, true> : block_combine_kernel<64, false>);
+  if (launch_dependent(cfn, grid, 32 * kBcbWarps, 0, cs, a, s.rk) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  return KVQ_OK;
+}

@@ -31,6 +31,14 @@ KV_BF16 = 1
 W_INT4 = 0
 W_E4M3 = 1
 
+ROPE_HALF = 0
+ROPE_INTERLEAVED = 1
+ROPE_PLAIN = 0
+ROPE_LINEAR = 1
+ROPE_BASE = 2
+ROPE_RAMP = 3
+ROPE_BANDS = 4
+
 ERRBIT_PAGE = 1 << 0
 ERRBIT_SEQLEN = 1 << 1
 ERRBIT_POS = 1 << 2
@@ -44,7 +52,9 @@ STATUS = {0: "KVQ_OK", 1: "KVQ_ERR_INVALID_ARG", 2: "KVQ_ERR_WORKSPACE", 3: "KVQ
 # every symbol include/kvq.h declares
 EXPORTS = ("kvq_append", "kvq_append_check", "kvq_handoff_pages", "kvq_check_tags",
            "kvq_pages_update", "kvq_decode_attn_workspace_size", "kvq_decode_attn",
-           "kvq_decode_attn_static", "kvq_wq_gemm", "kvq_selftest_wait", "kvq_status_string")
+           "kvq_decode_attn_static", "kvq_wq_gemm", "kvq_selftest_wait", "kvq_status_string",
+           "kvq_rope_inv_freq", "kvq_rope", "kvq_block_append", "kvq_rope_block_append",
+           "kvq_block_read", "kvq_block_attn_workspace_size", "kvq_block_attn")
 STATIC_SCRATCH_BYTES = 64 << 20
 
 
@@ -60,6 +70,18 @@ class CCache(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("k_scale", ctypes.c_float),
                 ("v_scale", ctypes.c_float)]
+
+
+class CBlockCache(ctypes.Structure):
+    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class CRope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("mscale", ctypes.c_float)]
 
 
 _lib = None
@@ -102,6 +124,24 @@ def load(build_if_missing: bool = True):
     L.kvq_decode_attn.restype = ctypes.c_int
     L.kvq_decode_attn_static.argtypes = [cp, vp, i32, i32, vp, i32, vp, vp, f32, vp, vp, vp]
     L.kvq_decode_attn_static.restype = ctypes.c_int
+    i64, f64, bp, rp = ctypes.c_int64, ctypes.c_double, ctypes.POINTER(CBlockCache), \
+        ctypes.POINTER(CRope)
+    L.kvq_rope_inv_freq.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp, vp]
+    L.kvq_rope_inv_freq.restype = ctypes.c_int
+    L.kvq_rope.argtypes = [rp, vp, i32, i32, vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, vp]
+    L.kvq_rope.restype = ctypes.c_int
+    L.kvq_block_append.argtypes = [bp, vp, i64, vp, i64, vp, i32, vp, vp, i32, i32, vp, vp]
+    L.kvq_block_append.restype = ctypes.c_int
+    L.kvq_rope_block_append.argtypes = [bp, rp, vp, i64, vp, i64, i32, vp, i64, vp, i64, vp, i32,
+                                        vp, vp, i32, i32, vp, vp]
+    L.kvq_rope_block_append.restype = ctypes.c_int
+    L.kvq_block_read.argtypes = [bp, vp, i32, vp, vp, i32, i32, vp, i64, vp, i64, vp, vp]
+    L.kvq_block_read.restype = ctypes.c_int
+    L.kvq_block_attn_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    L.kvq_block_attn_workspace_size.restype = sz
+    L.kvq_block_attn.argtypes = [bp, vp, i64, i32, vp, i32, i32, vp, vp, i32, i32, vp, f32, vp,
+                                 vp, sz, vp, vp]
+    L.kvq_block_attn.restype = ctypes.c_int
     L.kvq_status_string.argtypes = [ctypes.c_int]
     L.kvq_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -391,3 +431,217 @@ def kvq_decode_attn_static(cache: KVCache, q, block_table, seq_lens, out, abort_
                                   _dev(out, "out", (torch.float32,), 3),
                                   _dev(err_word, "err_word", U32), _stream(stream))
     _check("kvq_decode_attn_static", st)
+
+
+# ----------------------------------------------------------------------------
+# the block-scaled cache (include/kvq.h): rotary positions, append, read-back
+# and attention over ragged steps.  Request b's rows are tok_start[b] ..
+# tok_start[b + 1] - 1 (int32 [B + 1]; None: one row a request) and seq_lens[b]
+# its length after the step.  q, k and v are [rows, heads, D] bf16 whose
+# last two dims are contiguous; the rows may be slices of a wider projection.
+# Every tensor of a call lies on one device; without `stream` the call runs on
+# that device's current stream.
+# ----------------------------------------------------------------------------
+
+_F8 = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _arr(t, name, dtype, shape):
+    """Pointer of a contiguous device array of the given dtype and shape."""
+    if t.dtype is not dtype and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{name}: dtype {t.dtype} is not {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, is {list(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+def _rows(t, name, n, heads, D):
+    """(pointer, token stride) of a bf16 [n, heads, D] tensor strided by token."""
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name}: dtype {t.dtype} is not bfloat16")
+    if t.shape != (n, heads, D):
+        raise ValueError(f"{name} must be [{n}, {heads}, {D}], is {list(t.shape)}")
+    st = t.stride()
+    if not t.is_cuda or st[2] != 1 or (st[1] != D and heads > 1):
+        raise ValueError(f"{name} must be a CUDA tensor with contiguous rows of heads")
+    return t.data_ptr(), (st[0] if n > 1 else heads * D)
+
+
+def _launch(fn, name, dev, tensors, stream, args):
+    """Calls the library with `dev` current, on `stream` or its current stream."""
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: tensors lie on {t.device} and {dev}")
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream))
+    else:
+        st = fn(*args, _stream(stream))
+    if st != 0:
+        raise KvqError(name, st)
+
+
+@dataclass
+class BlockKVCache:
+    """Caller-owned e4m3 pools [num_pages, Hkv, P, D] and the scale of each
+    (page, kv head) block of K and of V: scales fp32 [num_pages, Hkv, 2]."""
+    k_pool: torch.Tensor
+    v_pool: torch.Tensor
+    scales: torch.Tensor
+
+    def c(self) -> CBlockCache:
+        shape = self.k_pool.shape
+        if len(shape) != 4:
+            raise ValueError("k_pool must have 4 dims")
+        NP, H, P, D = shape
+        return CBlockCache(_arr(self.k_pool, "k_pool", _F8, shape),
+                           _arr(self.v_pool, "v_pool", _F8, shape),
+                           _arr(self.scales, "scales", torch.float32, (NP, H, 2)), NP, P, H, D)
+
+    @staticmethod
+    def empty(num_pages, num_kv_heads, page_size, head_dim, device="cuda"):
+        shape = (num_pages, num_kv_heads, page_size, head_dim)
+        return BlockKVCache(torch.empty(shape, dtype=torch.uint8, device=device),
+                            torch.empty(shape, dtype=torch.uint8, device=device),
+                            torch.ones((num_pages, num_kv_heads, 2), device=device))
+
+
+@dataclass
+class Rope:
+    """Rotary positions: inv_freq float64 [rotary_dim / 2] on the device
+    (radians per position), the pairs' layout and the factor on the result."""
+    inv_freq: torch.Tensor
+    layout: int = ROPE_HALF
+    mscale: float = 1.0
+
+    def c(self) -> CRope:
+        n = self.inv_freq.shape[0] if self.inv_freq.dim() == 1 else -1
+        return CRope(_arr(self.inv_freq, "inv_freq", torch.float64, (n,)), 2 * n,
+                     int(self.layout), float(self.mscale))
+
+
+def kvq_rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: int = ROPE_PLAIN,
+                      factor: float = 1.0, orig_len: float = 0.0, low: float = 1.0,
+                      high: float = 32.0):
+    """(float64 tensor [rotary_dim / 2] on the host, mscale) of a frequency
+    scheme (include/kvq.h): move the tensor to the device once and keep it."""
+    out = torch.empty(max(rotary_dim, 0) // 2, dtype=torch.float64)
+    m = ctypes.c_float()
+    st = load().kvq_rope_inv_freq(int(rotary_dim), float(base), int(scaling), float(factor),
+                                  float(orig_len), float(low), float(high),
+                                  ctypes.c_void_p(out.data_ptr()), ctypes.byref(m))
+    _check("kvq_rope_inv_freq", st)
+    return out, m.value
+
+
+def kvq_rope(rope: Rope, pos, q, q_out, k=None, k_out=None, stream=None) -> None:
+    """Rotate rows of q into q_out (and of k into k_out); row t stands at
+    position pos[t] (int32).  An output may be its input."""
+    L = load()
+    N, Hq, D = q.shape
+    qa, qb = _rows(q, "q", N, Hq, D), _rows(q_out, "q_out", N, Hq, D)
+    Hk, ka, kb = 0, (None, 0), (None, 0)
+    if k is not None:
+        Hk = k.shape[1]
+        ka, kb = _rows(k, "k", N, Hk, D), _rows(k_out, "k_out", N, Hk, D)
+    _launch(L.kvq_rope, "kvq_rope", q.device, (pos, q_out, k, k_out, rope.inv_freq), stream,
+            (rope.c(), _arr(pos, "pos", torch.int32, (N,)), N, D, *qa, *qb, Hq, *ka, *kb, Hk))
+
+
+def _step(tok_start, seq_lens, block_table, name="seq_lens"):
+    B, MP = block_table.shape
+    return (None if tok_start is None else _arr(tok_start, "tok_start", torch.int32, (B + 1,)),
+            None if seq_lens is None else _arr(seq_lens, name, torch.int32, (B,)),
+            _arr(block_table, "block_table", torch.int32, (B, MP)), B, MP)
+
+
+def _err(err_word):
+    return None if err_word is None else _arr(err_word, "err_word", U32, (1,))
+
+
+def kvq_block_append(cache: BlockKVCache, k_new, v_new, tok_start, seq_lens, block_table,
+                     err_word=None, stream=None) -> None:
+    """Quantise rows of k_new / v_new [rows, Hkv, D] into their requests' pages
+    and set the blocks' scales (include/kvq.h)."""
+    L = load()
+    c = cache.c()
+    N = k_new.shape[0]
+    ka = _rows(k_new, "k_new", N, c.num_kv_heads, c.head_dim)
+    va = _rows(v_new, "v_new", N, c.num_kv_heads, c.head_dim)
+    ts, sl, bt, B, MP = _step(tok_start, seq_lens, block_table)
+    _launch(L.kvq_block_append, "kvq_block_append", k_new.device,
+            (cache.k_pool, cache.v_pool, cache.scales, v_new, tok_start, seq_lens, block_table,
+             err_word), stream, (c, *ka, *va, ts, N, sl, bt, B, MP, _err(err_word)))
+
+
+def kvq_rope_block_append(cache: BlockKVCache, rope: Rope, q, q_out, k_new, v_new, tok_start,
+                          seq_lens, block_table, err_word=None, stream=None) -> None:
+    """kvq_block_append with K rotated on the way in, and q rotated into q_out
+    (q and q_out may be None), in one launch."""
+    L = load()
+    c = cache.c()
+    N = k_new.shape[0]
+    D = c.head_dim
+    ka = _rows(k_new, "k_new", N, c.num_kv_heads, D)
+    va = _rows(v_new, "v_new", N, c.num_kv_heads, D)
+    Hq, qa, qb = 0, (None, 0), (None, 0)
+    if q is not None:
+        Hq = q.shape[1]
+        qa, qb = _rows(q, "q", N, Hq, D), _rows(q_out, "q_out", N, Hq, D)
+    ts, sl, bt, B, MP = _step(tok_start, seq_lens, block_table)
+    _launch(L.kvq_rope_block_append, "kvq_rope_block_append", k_new.device,
+            (cache.k_pool, cache.v_pool, cache.scales, v_new, q, q_out, rope.inv_freq, tok_start,
+             seq_lens, block_table, err_word), stream,
+            (c, rope.c(), *qa, *qb, Hq, *ka, *va, ts, N, sl, bt, B, MP, _err(err_word)))
+
+
+def kvq_block_read(cache: BlockKVCache, tok_start, first, block_table, k_out, v_out,
+                   err_word=None, stream=None) -> None:
+    """Read cached tokens back into k_out / v_out [rows, Hkv, D] bf16: row i of
+    request b is its position first[b] + i (first None: from position 0)."""
+    L = load()
+    c = cache.c()
+    N = k_out.shape[0]
+    ka = _rows(k_out, "k_out", N, c.num_kv_heads, c.head_dim)
+    va = _rows(v_out, "v_out", N, c.num_kv_heads, c.head_dim)
+    ts, fi, bt, B, MP = _step(tok_start, first, block_table, "first")
+    _launch(L.kvq_block_read, "kvq_block_read", k_out.device,
+            (cache.k_pool, cache.v_pool, cache.scales, v_out, tok_start, first, block_table,
+             err_word), stream, (c, ts, N, fi, bt, B, MP, *ka, *va, _err(err_word)))
+
+
+def kvq_block_attn_workspace_size(B: int, max_q: int, Hq: int, num_kv_heads: int,
+                                  head_dim: int) -> int:
+    return int(load().kvq_block_attn_workspace_size(B, max_q, Hq, num_kv_heads, head_dim))
+
+
+def block_workspace(B: int, max_q: int, Hq: int, num_kv_heads: int, head_dim: int,
+                    device="cuda") -> torch.Tensor:
+    """Allocate (with torch) a workspace of the size kvq_block_attn needs."""
+    with torch.cuda.device(device):
+        n = kvq_block_attn_workspace_size(B, max_q, Hq, num_kv_heads, head_dim)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def kvq_block_attn(cache: BlockKVCache, q, tok_start, seq_lens, block_table, out, workspace,
+                   max_q: int = 1, abort_mask=None, sm_scale: Optional[float] = None,
+                   err_word=None, stream=None) -> None:
+    """Causal attention of each request's rows (at most max_q a request) over
+    its cached tokens: q [rows, Hq, D] bf16, out [rows, Hq, D] fp32."""
+    L = load()
+    c = cache.c()
+    N, Hq, D = q.shape
+    qa = _rows(q, "q", N, Hq, c.head_dim)
+    ts, sl, bt, B, MP = _step(tok_start, seq_lens, block_table)
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(D)
+    _launch(L.kvq_block_attn, "kvq_block_attn", q.device,
+            (cache.k_pool, cache.v_pool, cache.scales, out, workspace, tok_start, seq_lens,
+             block_table, abort_mask, err_word), stream,
+            (c, *qa, Hq, ts, N, int(max_q), sl, bt, B, MP,
+             None if abort_mask is None else _arr(abort_mask, "abort_mask", U8, (B,)),
+             float(sm_scale), _arr(out, "out", torch.float32, (N, Hq, D)),
+             _arr(workspace, "workspace", torch.uint8, workspace.shape), workspace.numel(),
+             _err(err_word)))

@@ -301,6 +301,173 @@ KVQ_API kvq_status kvq_decode_attn_static(const kvq_cache *cache, const void *q,
                                           float sm_scale, float *out, uint32_t *err_word,
                                           kvq_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The block-scaled cache: e4m3 pools whose scales belong to blocks of tokens,
+ * written and calibrated in one step, with rotary positions on the way in and
+ * attention of one or several query tokens a request over it.
+ *
+ * Pools as in kvq_cache (e4m3, same layout); `scales` fp32
+ * [num_pages][num_kv_heads][2] holds, for each (page, kv head), the scale of
+ * its K block ([0]) and of its V block ([1]): a cached value is
+ * e4m3(code) * scale.  The scales that the library writes are powers of two,
+ * so that quantising and reading back round at most once and a block whose
+ * scale grows is requantised by exponent shifts.
+ * Supported: page_size in {16, 32, 64}; head_dim in {64, 128}; pools 16-byte
+ * and scales 8-byte aligned.  A page belongs to one request while a call
+ * writes it (two requests that write one page: unspecified).
+ *
+ * Ragged steps: a call handles B requests with n_tokens rows in all, request
+ * b owning rows tok_start[b] .. tok_start[b+1]-1 (tok_start int32 [B+1],
+ * non-decreasing, within [0, n_tokens]; NULL = one row a request, row b, and
+ * then n_tokens == B).  seq_lens[b] is the request's length AFTER the step, so its
+ * row i stands at position seq_lens[b] - n_b + i.  Rows behind tok_start[B]
+ * belong to nobody and are neither read nor written.  A request with a bad
+ * tok_start pair raises KVQ_ERRBIT_REQ, one whose length is negative, over
+ * MP * page_size or below its own row count KVQ_ERRBIT_SEQLEN; it is left
+ * out (nothing written; rows of an attention output are zeroed where the
+ * tok_start pair is good).  A request without rows is skipped.
+ * Token strides are in elements (multiples of 8, at least heads * head_dim),
+ * so q, k and v may be slices of one projection's output; base pointers are
+ * 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    void *k_pool;
+    void *v_pool;
+    float *scales;
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+} kvq_block_cache;
+
+typedef enum {
+    KVQ_ROPE_HALF = 0,       /* pair i: dims i and i + rotary_dim/2 */
+    KVQ_ROPE_INTERLEAVED = 1 /* pair i: dims 2i and 2i + 1 */
+} kvq_rope_layout;
+
+/* Rotary positions on the first rotary_dim dims of a head: pair i of a token
+ * at position p, (a, b), becomes
+ *     mscale * (a cos t - b sin t, b cos t + a sin t),  t = p * inv_freq[i];
+ * the other dims pass unchanged.  inv_freq: device fp64 [rotary_dim / 2],
+ * radians per position, >= 0 (kvq_rope_inv_freq computes the usual tables);
+ * rotary_dim a multiple of 16, at most head_dim.  Angles are reduced exactly
+ * in 64-bit fixed point (a turn = 2^64), so far positions keep fp32-accurate
+ * sines; products are fp32 and rounded once. */
+typedef struct {
+    const double *inv_freq;
+    int32_t rotary_dim;
+    int32_t layout; /* kvq_rope_layout */
+    float mscale;
+} kvq_rope_desc;
+
+typedef enum {
+    KVQ_ROPE_PLAIN = 0,  /* f_i = base^(-2i / rotary_dim) */
+    KVQ_ROPE_LINEAR = 1, /* f_i / factor: positions interpolated */
+    KVQ_ROPE_BASE = 2,   /* base * factor^(rd / (rd - 2)) in place of base: the lowest
+                            frequency is divided by factor, the highest kept */
+    KVQ_ROPE_RAMP = 3,   /* f_i / factor below `low` turns within orig_len, f_i above
+                            `high` turns, a linear ramp over i between (its ends rounded
+                            outwards to whole pairs); mscale = 0.1 ln(factor) + 1 */
+    KVQ_ROPE_BANDS = 4   /* the same ends, the ramp linear in the number of turns;
+                            mscale = 1 */
+} kvq_rope_scaling;
+
+/* Fills inv_freq_host (host fp64 [rotary_dim / 2]) and *mscale_host for a
+ * scheme; factor >= 1 (all but PLAIN), orig_len > 0 and 0 < low < high (RAMP
+ * and BANDS) are the model's long-context settings.  Host work only. */
+KVQ_API kvq_status kvq_rope_inv_freq(int32_t rotary_dim, double base, int32_t scaling,
+                                     double factor, double orig_len, double low, double high,
+                                     double *inv_freq_host, float *mscale_host);
+
+/* Rotates n_tokens rows of q (bf16, n_q_heads heads of head_dim) into q_out and of
+ * k (n_k_heads) into k_out; row t stands at position pos[t] (device int32,
+ * any value).  k may be NULL (with n_k_heads 0).  An output may be its input
+ * (same pointer and stride); otherwise they must not overlap. */
+KVQ_API kvq_status kvq_rope(const kvq_rope_desc *rope, const int32_t *pos, int32_t n_tokens,
+                            int32_t head_dim, const void *q, int64_t q_stride, void *q_out,
+                            int64_t q_out_stride, int32_t n_q_heads, const void *k,
+                            int64_t k_stride, void *k_out, int64_t k_out_stride,
+                            int32_t n_k_heads, kvq_stream_t stream);
+
+/* Quantise-and-append into the block-scaled cache: request b's rows of k_new /
+ * v_new (bf16 [n_tokens][num_kv_heads][head_dim], strided by token) are
+ * stored at its positions.  For every block (page, kv head, K or V) that gets
+ * tokens, with amax the largest finite magnitude among them,
+ *     s = max(2^ceil(log2(amax / 448)), the block's old scale if it holds
+ *         tokens before this step's), at least 2^-126;
+ * the block's scale becomes s, each new value e4m3_rne_satfinite(x / s) (inf
+ * saturates, NaN becomes a NaN code) and, where s grew, each old code
+ * e4m3_rne_satfinite(e4m3(code) * s_old / s).  Whether a block holds earlier
+ * tokens follows from the positions (slot 0 written in this step = a new
+ * block, whose old scale is not read).  Slots past the request's length are
+ * not written.  A table entry outside the pool raises KVQ_ERRBIT_PAGE and
+ * its tokens are not written.  Appending the same rows again at the same
+ * positions changes nothing. */
+KVQ_API kvq_status kvq_block_append(const kvq_block_cache *cache, const void *k_new,
+                                    int64_t k_stride, const void *v_new, int64_t v_stride,
+                                    const int32_t *tok_start, int32_t n_tokens,
+                                    const int32_t *seq_lens, const int32_t *block_table,
+                                    int32_t B, int32_t MP, uint32_t *err_word,
+                                    kvq_stream_t stream);
+
+/* kvq_block_append of K rotated by `rope` (quantised from the fp32 rotation:
+ * rounded once), and q rotated into q_out, in one launch.  q (bf16
+ * [n_tokens][n_q_heads][head_dim]) may be NULL with n_q_heads 0; q_out may be
+ * q.  q's rows of a request that is left out, or of a token whose page is
+ * bad, are not written. */
+KVQ_API kvq_status kvq_rope_block_append(const kvq_block_cache *cache, const kvq_rope_desc *rope,
+                                         const void *q, int64_t q_stride, void *q_out,
+                                         int64_t q_out_stride, int32_t n_q_heads,
+                                         const void *k_new, int64_t k_stride, const void *v_new,
+                                         int64_t v_stride, const int32_t *tok_start,
+                                         int32_t n_tokens, const int32_t *seq_lens,
+                                         const int32_t *block_table, int32_t B, int32_t MP,
+                                         uint32_t *err_word, kvq_stream_t stream);
+
+/* Reads cached tokens back: row i of request b is its position first[b] + i
+ * (first int32 [B], NULL = zeros), k_out / v_out bf16
+ * [n_tokens][num_kv_heads][head_dim] strided by token:
+ *     bf16_rne( e4m3(code) * scale )   (exact for the library's own scales
+ * unless the value is below bf16's normal range).  A range that is negative
+ * or reaches past MP * page_size raises KVQ_ERRBIT_POS and its rows are not
+ * written; a page outside the pool KVQ_ERRBIT_PAGE (its tokens' rows are not
+ * written). */
+KVQ_API kvq_status kvq_block_read(const kvq_block_cache *cache, const int32_t *tok_start,
+                                  int32_t n_tokens, const int32_t *first,
+                                  const int32_t *block_table, int32_t B, int32_t MP, void *k_out,
+                                  int64_t k_stride, void *v_out, int64_t v_stride,
+                                  uint32_t *err_word, kvq_stream_t stream);
+
+/* Bytes of device workspace kvq_block_attn needs on the current device, for
+ * at most B requests of at most max_q rows each (0: bad sizes). */
+KVQ_API size_t kvq_block_attn_workspace_size(int32_t B, int32_t max_q, int32_t Hq,
+                                             int32_t num_kv_heads, int32_t head_dim);
+
+/* Causal attention of each request's last rows over its cached tokens.  Row i
+ * of request b (n_b rows, length L) attends to tokens j <= L - n_b + i:
+ *     s_j = sm_scale * sum_d q[row][h][d] * k_scale(page_j, g) * e4m3(k_code_j[d])
+ *     out[row][h][:] = sum_j softmax(s)_j * v_scale(page_j, g) * e4m3(v_code_j[:])
+ * with g = h / (Hq / num_kv_heads); q bf16 strided by token, out fp32
+ * [n_tokens][Hq][head_dim], contiguous; sums and softmax statistics fp32.
+ * max_q (>= 1): no request has more rows; one that does is treated as having
+ * a bad length (KVQ_ERRBIT_SEQLEN).  Any number of rows is computed; the
+ * kernel is built for decode and drafted tokens (up to 128 rows times heads
+ * a kv head share one read of the cache).  abort_mask (uint8 [B], nullable):
+ * an aborted request's pages are not read and its rows are zero.  A page
+ * outside the pool raises KVQ_ERRBIT_PAGE and zeroes the request's rows that
+ * would read it.  A scale is any positive finite fp32.  Values at positions
+ * that a row does not see (NaN codes among them) do not reach it.
+ * workspace: 256-byte aligned, kvq_block_attn_workspace_size() bytes, not
+ * shared by calls that can run at the same time; its contents need no
+ * preparation. */
+KVQ_API kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q, int64_t q_stride,
+                                  int32_t Hq, const int32_t *tok_start, int32_t n_tokens,
+                                  int32_t max_q, const int32_t *seq_lens,
+                                  const int32_t *block_table, int32_t B, int32_t MP,
+                                  const uint8_t *abort_mask, float sm_scale, float *out,
+                                  void *workspace, size_t workspace_bytes, uint32_t *err_word,
+                                  kvq_stream_t stream);
+
 /* Self-test of a kernel failure path (no fault, no hang): one CTA starts a
  * real bulk copy of 64 bytes from src (device, 16-byte aligned) into shared
  * memory, then waits on an mbarrier that nothing ever arrives at, with the
