@@ -20,7 +20,7 @@
 //           plan kernel at any batch size).  A producer warp walks the run, stages
 //           16 tokens of a group of HG heads per TMA copy into a ring (the pool
 //           layout makes them one box) and the blocks' scales by 8-byte async
-//           copies that count on the same barrier.  Eight consumer warps: HG
+//           copies that count on the same barrier.  Consumer warps: HG
 //           heads x RT 16-row tiles x TW teams that take the ring's stages in
 //           turn, so that few heads or few rows still occupy every warp.  At
 //           the end of a segment the teams' partials meet in shared memory.
@@ -46,19 +46,21 @@ namespace kvq {
 
 constexpr int kBaWarps = 8;                      // consumer warps
 constexpr int kBaThreads = 32 * (kBaWarps + 1);
-constexpr int kBaMaxStages = 24;
+constexpr int kBaMaxStages = 48;
 constexpr int kBaSegs = 4;                       // segment descriptors in flight
-constexpr int kBaSmem = 220 * 1024;              // ring + merge area + control, per CTA
+constexpr int kBaSmem = 225 * 1024;              // ring + merge slots + control, per CTA
 constexpr int kStat = 4;                         // floats after a row's accumulators: m, l, n, -
 
 // Row tiles: 4 (one MMA column block carries the weights and their remainders),
-// 8 or 16 rows a warp; larger row counts take RT tiles of 16.
+// 8 or 16 rows a warp; larger row counts take RT tiles of 16.  The warps that
+// the (head, row tile) pairs leave free are further teams.
 struct BaShape {
   int rk, rt, hg, tw;   // rows a warp, row tiles, heads a stage, teams
   int rows;             // rows a row block holds: rk * rt
   int row_blocks;       // row blocks of a request of max_q rows
   int groups;           // head groups
-  int warps() const { return hg * rt * tw; }
+  int pairs() const { return hg * rt; }
+  int slots() const { return pairs() * (tw - 1); }
 };
 
 inline BaShape ba_shape(int max_q, int G, int Hkv) {
@@ -73,7 +75,7 @@ inline BaShape ba_shape(int max_q, int G, int Hkv) {
   for (int h = 1; h <= kBaWarps / s.rt; ++h)
     if (Hkv % h == 0) s.hg = h;
   s.groups = Hkv / s.hg;
-  s.tw = kBaWarps / (s.hg * s.rt);
+  s.tw = kBaWarps / s.pairs();
   return s;
 }
 
@@ -109,7 +111,7 @@ struct BaArgs {
   float *out;
   uint32_t *err_word;
   int32_t num_pages, P, Hkv, Hq, G, MP, max_q;
-  int32_t hg, rt, tw, row_blocks, groups, stages;
+  int32_t hg, rt, tw, rounds, row_blocks, groups, stages;  // rounds: of the teams' merge
   float q_scale;  // sm_scale * log2(e)
 };
 
@@ -177,42 +179,50 @@ __device__ __forceinline__ int lane_row(int gq, int g) {
   return RK == 4 ? (gq & 3) : gq + 8 * g;
 }
 
+// The lane's D / 4 dims of row r (of the request), scaled by 2^e so that the
+// row's largest value lies in [2^14, 2^15), as f16 pairs; the scale that undoes it.
 template <int D, int RK>
-__device__ __forceinline__ void ba_load_q(BaState<D, RK> &st, const BaArgs &a, const BaSeg &sg,
-                                          int kvh, int row_base, int gq, int tq) {
-  constexpr int KS = BaState<D, RK>::KS, NG = BaState<D, RK>::NG, W = D / 4;  // dims a lane
+__device__ __forceinline__ float ba_q_row(const BaArgs &a, const BaSeg &sg, int kvh, int r, int tq,
+                                          uint32_t (&lo)[D / 16], uint32_t (&hi)[D / 16]) {
+  constexpr int W = D / 4;
+  const int i = r / a.G;
+  float x[W];
+  if (i < sg.n) {
+    const uint16_t *p = a.q + (static_cast<int64_t>(sg.row0) + i) * a.q_stride +
+                        static_cast<int64_t>(kvh * a.G + r - i * a.G) * D + W * tq;
+#pragma unroll
+    for (int c = 0; c < W / 8; ++c) unpack8(__ldg(reinterpret_cast<const uint4 *>(p) + c), x + 8 * c);
+  } else {
+#pragma unroll
+    for (int c = 0; c < W; ++c) x[c] = 0.f;
+  }
+  float mx = 0.f;
+#pragma unroll
+  for (int c = 0; c < W; ++c) mx = fmaxf(mx, fabsf(x[c]));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  int e = mx > 0.f && mx < INFINITY ? 14 - ilogbf(mx) : 0;
+  e = min(e, 126);
+  const float up = pow2(e);  // e >= 14 - 127
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) {
+    lo[s] = f32x2_to_f16x2(x[4 * s] * up, x[4 * s + 1] * up);
+    hi[s] = f32x2_to_f16x2(x[4 * s + 2] * up, x[4 * s + 3] * up);
+  }
+  return a.q_scale * pow2(-e);
+}
+
+// A segment's start: q, limits and empty sums.
+template <int D, int RK>
+__device__ __forceinline__ void ba_begin(BaState<D, RK> &st, const BaArgs &a, const BaSeg &sg,
+                                         int kvh, int row_base, int gq, int tq) {
+  constexpr int KS = BaState<D, RK>::KS, NG = BaState<D, RK>::NG;
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     const int r = row_base + lane_row<RK>(gq, g);
     const int i = r / a.G;
-    float x[W];
-    const bool ok = i < sg.n;
-    st.lim[g] = ok ? sg.L - sg.n + 1 + i : sg.L;
-    if (ok) {
-      const uint16_t *p = a.q + (sg.row0 + i) * a.q_stride +
-                          static_cast<int64_t>(kvh * a.G + r - i * a.G) * D + W * tq;
-#pragma unroll
-      for (int c = 0; c < W / 8; ++c)
-        unpack8(__ldg(reinterpret_cast<const uint4 *>(p) + c), x + 8 * c);
-    } else {
-#pragma unroll
-      for (int c = 0; c < W; ++c) x[c] = 0.f;
-    }
-    float mx = 0.f;
-#pragma unroll
-    for (int c = 0; c < W; ++c) mx = fmaxf(mx, fabsf(x[c]));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    // 2^e puts the row's largest value into [2^14, 2^15)
-    int e = mx > 0.f && mx < INFINITY ? 14 - ilogbf(mx) : 0;
-    e = min(e, 126);
-    const float up = pow2(e);  // e >= 14 - 127
-    st.qk[g] = a.q_scale * pow2(-e);
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      st.qa[g][0][s] = f32x2_to_f16x2(x[4 * s] * up, x[4 * s + 1] * up);
-      st.qa[g][1][s] = f32x2_to_f16x2(x[4 * s + 2] * up, x[4 * s + 3] * up);
-    }
+    st.lim[g] = i < sg.n ? sg.L - sg.n + 1 + i : sg.L;
+    st.qk[g] = ba_q_row<D, RK>(a, sg, kvh, r, tq, st.qa[g][0], st.qa[g][1]);
     st.m[g] = st.n[g] = -INFINITY;
     st.l[g] = 0.f;
 #pragma unroll
@@ -298,24 +308,9 @@ __device__ __noinline__ void ba_pv_masked(BaMasked<D, RK> &x) {
   }
 }
 
-// One 16-token tile: ks / vs the head's swizzled blocks, tok0 its first token,
-// min_lim the fewest tokens that a row of the row block sees, L the length.
-template <int D, int RK>
-__device__ __forceinline__ void ba_tile(BaState<D, RK> &st, const uint8_t *ks, const uint8_t *vs,
-                                        float2 sc, int tok0, int min_lim, int L, int gq, int tq) {
-  constexpr int KS = BaState<D, RK>::KS, NG = BaState<D, RK>::NG, W = D / 32;
-  uint32_t kw[2][KS];  // rows gq and 8 + gq, the lane's D / 4 dims
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-      const uint4 x = lds128(ks + swz<D>(gq + 8 * j, (D / 64) * tq + c));
-      kw[j][4 * c] = x.x;
-      kw[j][4 * c + 1] = x.y;
-      kw[j][4 * c + 2] = x.z;
-      kw[j][4 * c + 3] = x.w;
-    }
-  uint32_t v[4][W];  // V rows 2t, 2t+1, 2t+8, 2t+9 at dims (D / 8) gq ..
+// V^T operand words of a tile: rows 2t, 2t+1, 2t+8, 2t+9 at dims (D / 8) gq ..
+template <int D>
+__device__ __forceinline__ void ba_load_v(uint32_t (&v)[4][D / 32], const uint8_t *vs, int gq, int tq) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int r = 2 * tq + (k & 1) + 8 * (k >> 1);
@@ -331,57 +326,108 @@ __device__ __forceinline__ void ba_tile(BaState<D, RK> &st, const uint8_t *ks, c
       v[k][1] = x.y;
     }
   }
-  // q.k: even and odd k-steps in sums of their own (shorter dependency chains)
-  float s[2][2][4];
+}
+
+// NT consecutive 16-token tiles of a segment: ks / vs the head's swizzled
+// blocks, sc the blocks' scales, tok0 the first token, min_lim the fewest tokens that a
+// row of the row block sees, L the length.  Two tiles share one softmax update:
+// a warp is bound by the latency of its dependency chain (max, vote, exponential,
+// conversion), which the second tile's work fills.
+template <int D, int RK, int NT>
+__device__ __forceinline__ void ba_tiles(BaState<D, RK> &st, const uint8_t *const (&ks)[NT],
+                                         const uint8_t *const (&vs)[NT], const float2 (&sc)[NT],
+                                         int tok0, int min_lim, int L, int gq, int tq) {
+  constexpr int KS = BaState<D, RK>::KS, NG = BaState<D, RK>::NG, W = D / 32;
+  constexpr int CH = NT == 1 ? 2 : 1;  // sums a score tile: independent chains of MMAs
+  float s[NT][2][CH][4];
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) s[j][e][0] = s[j][e][1] = s[j][e][2] = s[j][e][3] = 0.f;
-#pragma unroll
-  for (int k = 0; k < KS; ++k)
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      mma_16816(s[j][k & 1], st.qa[0][0][k], NG == 2 ? st.qa[NG - 1][0][k] : 0u, st.qa[0][1][k],
-                NG == 2 ? st.qa[NG - 1][1][k] : 0u, e4m3x2_to_f16x2(kw[j][k] & 0xFFFFu),
-                e4m3x2_to_f16x2(kw[j][k] >> 16));
-  const bool partial = tok0 + kTile > min_lim;  // uniform over the warp
-  // log2 of the V scale, rounded up: exact for a power of two
-  const uint32_t vu = __float_as_uint(sc.y);
-  const int ve = static_cast<int>(vu >> 23) - 127 + ((vu & 0x7FFFFFu) ? 1 : 0);
-  const float lv = static_cast<float>(ve);
-  float x[NG][2][2];
-  float mx[NG], mv[NG];
-  bool grow_l[NG], grow_o[NG];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) s[t][j][c][0] = s[t][j][c][1] = s[t][j][c][2] = s[t][j][c][3] = 0.f;
+  {
+    uint32_t kw[NT][2][KS];  // rows gq and 8 + gq, the lane's D / 4 dims
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          const uint4 x = lds128(ks[t] + swz<D>(gq + 8 * j, (D / 64) * tq + c));
+          kw[t][j][4 * c] = x.x;
+          kw[t][j][4 * c + 1] = x.y;
+          kw[t][j][4 * c + 2] = x.z;
+          kw[t][j][4 * c + 3] = x.w;
+        }
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          mma_16816(s[t][j][k % CH], st.qa[0][0][k], NG == 2 ? st.qa[NG - 1][0][k] : 0u,
+                    st.qa[0][1][k], NG == 2 ? st.qa[NG - 1][1][k] : 0u,
+                    e4m3x2_to_f16x2(kw[t][j][k] & 0xFFFFu), e4m3x2_to_f16x2(kw[t][j][k] >> 16));
+  }
+  const bool partial = tok0 + NT * kTile > min_lim;  // uniform over the warp
+  // log2 of the V scales, rounded up (exact for a power of two), and the
+  // scales' fractions, in (0.5, 1]
+  float lv[NT], vm[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const uint32_t u = __float_as_uint(sc[t].y);
+    const int e = static_cast<int>(u >> 23) - 127 + ((u & 0x7FFFFFu) ? 1 : 0);
+    lv[t] = static_cast<float>(e);
+    vm[t] = sc[t].y * pow2(max(-126, min(127, -e)));
+  }
+  float x[NG][NT][2][2], mx[NG], mv[NG];
   bool any = false;
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    const float f = st.qk[g] * sc.x;
     const int seen = st.lim[g] - tok0;
-    mx[g] = -INFINITY;
+    mx[g] = mv[g] = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int t = 0; t < NT; ++t) {
+      const float f = st.qk[g] * sc[t].x;
+      float mt = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        x[g][j][e] = (s[j][0][2 * g + e] + s[j][1][2 * g + e]) * f;
-        if (partial && 8 * j + 2 * tq + e >= seen) x[g][j][e] = -INFINITY;
-        mx[g] = fmaxf(mx[g], x[g][j][e]);
-      }
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float y = s[t][j][0][2 * g + e];
+          if constexpr (CH == 2) y += s[t][j][CH - 1][2 * g + e];
+          y *= f;
+          if (partial && kTile * t + 8 * j + 2 * tq + e >= seen) y = -INFINITY;
+          x[g][t][j][e] = y;
+          mt = fmaxf(mt, y);
+        }
+      mx[g] = fmaxf(mx[g], mt);
+      mv[g] = fmaxf(mv[g], mt + lv[t]);
+    }
     mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], 1));
     mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], 2));
-    mv[g] = mx[g] + lv;
-    grow_l[g] = mx[g] > st.m[g] + kRescaleThreshold;
-    grow_o[g] = mv[g] > st.n[g] + kRescaleThreshold;
-    any |= grow_l[g] | grow_o[g];
+    if constexpr (NT == 1) {
+      mv[g] = mx[g] + lv[0];
+    } else {
+      mv[g] = fmaxf(mv[g], __shfl_xor_sync(0xffffffffu, mv[g], 1));
+      mv[g] = fmaxf(mv[g], __shfl_xor_sync(0xffffffffu, mv[g], 2));
+    }
+    any |= mx[g] > st.m[g] + kRescaleThreshold || mv[g] > st.n[g] + kRescaleThreshold;
   }
   if (__any_sync(0xffffffffu, any)) {
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      if (grow_l[g]) {
+      if (mx[g] > st.m[g] + kRescaleThreshold) {
         st.l[g] *= exp2f(st.m[g] - mx[g]);  // 0 when m is -inf
         st.m[g] = mx[g];
       }
-      const float f = grow_o[g] ? exp2f(st.n[g] - mv[g]) : 1.f;
-      if (grow_o[g]) st.n[g] = mv[g];
+      float f = 1.f;
+      if (mv[g] > st.n[g] + kRescaleThreshold) {
+        f = exp2f(st.n[g] - mv[g]);
+        st.n[g] = mv[g];
+      }
+      // columns 2t and 2t + 1 of O^T are the rows of lanes 8t and 8t + 4
       const float fa = __shfl_sync(0xffffffffu, f, 8 * tq);
       const float fb = __shfl_sync(0xffffffffu, f, 8 * tq + 4);
 #pragma unroll
@@ -393,94 +439,108 @@ __device__ __forceinline__ void ba_tile(BaState<D, RK> &st, const uint8_t *ks, c
       }
     }
   }
-  uint32_t hi[NG][2], lo[NG][2];
-  const float vm = sc.y * pow2(max(-126, min(127, -ve)));  // the V scale's fraction, (0.5, 1]
+  uint32_t hi[NT][NG][2], lo[NT][NG][2];
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    // vs 2^(m - n), with kPScale (2^7) so that the largest weights sit high in
-    // f16's range; the clamp only meets rows whose weights here are below
-    // 2^-112 of their largest
-    const float d = st.n[g] == -INFINITY
-                        ? 0.f
-                        : vm * kPScale * fast_exp2(fminf(st.m[g] - st.n[g] + lv, 112.f));
+    // a row that has seen nothing yet (m, n = -inf) has only x = -inf here:
+    // its weights come out 0 with any finite reference
+    const bool none = st.n[g] == -INFINITY;
+    const float m = none ? 0.f : st.m[g];
+    const float mn = none ? 0.f : st.m[g] - st.n[g];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float p0 = x[g][j][0] == -INFINITY ? 0.f : fast_exp2(x[g][j][0] - st.m[g]);
-      const float p1 = x[g][j][1] == -INFINITY ? 0.f : fast_exp2(x[g][j][1] - st.m[g]);
-      st.l[g] += p0 + p1;
-      const float w0 = p0 * d, w1 = p1 * d;
-      const uint32_t h = f32x2_to_f16x2(w0, w1);
-      const float2 hf = f16x2_to_f32x2(h);
-      const uint32_t r = f32x2_to_f16x2(w0 - hf.x, w1 - hf.y);
-      hi[g][j] = RK == 4 && gq >= 4 ? r : h;
-      lo[g][j] = r;
+    for (int t = 0; t < NT; ++t) {
+      // vs 2^(m - n), with kPScale (2^7) so that the largest weights sit high in
+      // f16's range; the clamp only meets rows whose weights here are below
+      // 2^-112 of their largest
+      const float d = vm[t] * kPScale * fast_exp2(fminf(mn + lv[t], 112.f));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float p0 = fast_exp2(x[g][t][j][0] - m), p1 = fast_exp2(x[g][t][j][1] - m);
+        st.l[g] += p0 + p1;
+        const float w0 = p0 * d, w1 = p1 * d;
+        const uint32_t h = f32x2_to_f16x2(w0, w1);
+        const float2 hf = f16x2_to_f32x2(h);
+        const uint32_t r = f32x2_to_f16x2(w0 - hf.x, w1 - hf.y);
+        hi[t][g][j] = RK == 4 && gq >= 4 ? r : h;
+        lo[t][g][j] = r;
+      }
     }
   }
-  if (partial) {
-    bool bad = false;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int c = 0; c < W; ++c) {
-        // cached bytes past the sequence may be anything
-        if (tok0 + 2 * tq + (k & 1) + 8 * (k >> 1) >= L) v[k][c] = 0u;
-        bad |= has_nan(v[k][c]);
-      }
-    if (__any_sync(0xffffffffu, bad)) {
-      BaMasked<D, RK> x2;  // copies: the state's own registers keep no address
-#pragma unroll
-      for (int i = 0; i < KS; ++i)
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x2.o[i][g][k] = st.o[i][g][k];
+  for (int t = 0; t < NT; ++t) {
+    uint32_t v[4][W];
+    ba_load_v<D>(v, vs[t], gq, tq);
+    if (partial) {
+      bool bad = false;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int c = 0; c < W; ++c) x2.v[k][c] = v[k][c];
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          x2.hi[g][j] = hi[g][j];
-          x2.lo[g][j] = lo[g][j];
+        for (int c = 0; c < W; ++c) {
+          // cached bytes past the sequence may be anything
+          if (tok0 + kTile * t + 2 * tq + (k & 1) + 8 * (k >> 1) >= L) v[k][c] = 0u;
+          bad |= has_nan(v[k][c]);
         }
-        x2.lim[g] = st.lim[g];
+      if (__any_sync(0xffffffffu, bad)) {
+        BaMasked<D, RK> x2;  // copies: the state's own registers keep no address
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x2.o[i][g][k] = st.o[i][g][k];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int c = 0; c < W; ++c) x2.v[k][c] = v[k][c];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            x2.hi[g][j] = hi[t][g][j];
+            x2.lo[g][j] = lo[t][g][j];
+          }
+          x2.lim[g] = st.lim[g];
+        }
+        x2.tok0 = tok0 + kTile * t;
+        x2.tq = tq;
+        ba_pv_masked<D, RK>(x2);
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) st.o[i][g][k] = x2.o[i][g][k];
+        continue;
       }
-      x2.tok0 = tok0;
-      x2.tq = tq;
-      ba_pv_masked<D, RK>(x2);
-#pragma unroll
-      for (int i = 0; i < KS; ++i)
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) st.o[i][g][k] = x2.o[i][g][k];
-      return;
     }
+    ba_pv<D, RK>(st.o, v[0], v[1], v[2], v[3], hi[t], lo[t]);
   }
-  ba_pv<D, RK>(st.o, v[0], v[1], v[2], v[3], hi, lo);
 }
 
 // ---------------------------------------------------------------------------
 // the split kernel
 // ---------------------------------------------------------------------------
 
-// Shared memory: K ring, V ring, merge area (teams only), control.
-template <int D>
-__host__ __device__ constexpr size_t ba_stage_bytes(int hg) {
-  return static_cast<size_t>(hg) * kTile * D;
+// A merge slot holds a warp's sums register by register: [KS * NG * 4 + 3 NG]
+// words of 32 lanes.
+template <int D, int RK>
+constexpr int kBaSlotWords = (D / 16 * BaState<D, RK>::NG * 4 + 3 * BaState<D, RK>::NG) * 32;
+
+inline size_t ba_slot_bytes(const BaShape &s, int D) {
+  return (D / 16 * 4 + 3) * (s.rk == 16 ? 2 : 1) * 128;
 }
 
-inline size_t ba_merge_floats(const BaShape &s, int D) {
-  return s.tw > 1 ? static_cast<size_t>(s.warps()) * s.rk * (D + kStat) : 0;
-}
-
+// Shared memory: K ring, V ring, merge slots, control.  Teams take turns of two
+// stages; the stage count is a multiple of a round of turns, so that within a
+// segment every ring slot belongs to one team and its phases are waited for
+// in order (a team that ran ahead of another on a shared slot could take the
+// parity of the phase before last for its own).
 inline int ba_stages(const BaShape &s, int D) {
   const size_t stage = 2 * static_cast<size_t>(s.hg) * kTile * D;
-  const size_t room = kBaSmem - 1024 - sizeof(BaCtl) - ba_merge_floats(s, D) * sizeof(float);
-  const size_t n = room / stage;
-  return static_cast<int>(n < kBaMaxStages ? n : kBaMaxStages);
+  const size_t room = kBaSmem - 1024 - sizeof(BaCtl) - s.slots() * ba_slot_bytes(s, D);
+  const size_t fit = room / stage < kBaMaxStages ? room / stage : kBaMaxStages;
+  const int n = static_cast<int>(fit);
+  return s.tw > 1 ? n / (2 * s.tw) * (2 * s.tw) : n;
 }
 
 // Row r (of the request) as an output row's address.
@@ -498,13 +558,13 @@ __global__ void __launch_bounds__(kBaThreads, 1)
   constexpr int KS = St::KS, NG = St::NG, RF = D + kStat;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);  // for the swizzle
-  const uint32_t stage_bytes = static_cast<uint32_t>(ba_stage_bytes<D>(a.hg));
+  const uint32_t stage_bytes = static_cast<uint32_t>(a.hg) * kTile * D;
   const int NS = a.stages;
+  const int ngrp = a.hg * a.rt;  // (head, row tile) pairs
   uint8_t *kbuf = smem;
   uint8_t *vbuf = smem + static_cast<size_t>(NS) * stage_bytes;
-  float *area = reinterpret_cast<float *>(smem + 2 * static_cast<size_t>(NS) * stage_bytes);
-  const int ngrp = a.hg * a.rt;  // (head, row tile) pairs
-  BaCtl &ctl = *reinterpret_cast<BaCtl *>(area + (a.tw > 1 ? ngrp * a.tw * RK * RF : 0));
+  float *slots = reinterpret_cast<float *>(smem + 2 * static_cast<size_t>(NS) * stage_bytes);
+  BaCtl &ctl = *reinterpret_cast<BaCtl *>(slots + (a.tw - 1) * ngrp * kBaSlotWords<D, RK>);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = RK * a.rt;
   if (threadIdx.x == 0) {
@@ -665,7 +725,7 @@ __global__ void __launch_bounds__(kBaThreads, 1)
   const int head = pair / a.rt, tile = pair % a.rt;
   const int gq = lane >> 2, tq = lane & 3;
   St st;
-  uint32_t g0 = 0, nseg = 0;
+  uint32_t g0 = 0, nseg = 0, nmerge = 0;
   while (true) {
     const int ss = nseg % kBaSegs;
     if (!ba_wait_warp(ctl, &ctl.segfull[ss], (nseg / kBaSegs) & 1, a.err_word)) return;
@@ -673,27 +733,108 @@ __global__ void __launch_bounds__(kBaThreads, 1)
     if (sg.b < 0) return;
     const int kvh = sg.grp * a.hg + head;
     const int row_base = sg.rb * rows + tile * RK;  // this warp's first row of the request
-    ba_load_q<D, RK>(st, a, sg, kvh, row_base, gq, tq);
+    ba_begin<D, RK>(st, a, sg, kvh, row_base, gq, tq);
     const int min_lim = min(sg.L, sg.L - sg.n + 1 + (sg.rb * rows) / a.G);
     bool seg_bad = false;
-    for (int k = team; k < sg.stages; k += a.tw) {
-      const uint32_t g = g0 + k;
-      const int slot = g % NS;
-      if (!ba_wait_warp(ctl, &ctl.full[slot], (g / NS) & 1, a.err_word)) return;
-      if (ctl.bad[slot])
-        seg_bad = true;
-      else
-        ba_tile<D, RK>(st, kbuf + slot * stage_bytes + head * (kTile * D),
-                       vbuf + slot * stage_bytes + head * (kTile * D), ctl.sc[slot][head],
-                       sg.t_begin + k * kTile, min_lim, sg.L, gq, tq);
+    for (int k = 2 * team; k < sg.stages; k += 2 * a.tw) {  // a turn: two stages
+      const int s0 = (g0 + k) % NS, s1 = (g0 + k + 1) % NS;
+      const bool two = k + 1 < sg.stages;
+      if (!ba_wait_warp(ctl, &ctl.full[s0], ((g0 + k) / NS) & 1, a.err_word)) return;
+      if (two && !ba_wait_warp(ctl, &ctl.full[s1], ((g0 + k + 1) / NS) & 1, a.err_word)) return;
+      const int tok = sg.t_begin + k * kTile;
+      const uint32_t off0 = s0 * stage_bytes + head * (kTile * D), off1 = s1 * stage_bytes + head * (kTile * D);
+      // a row that meets a bad page is zeros: its other tiles are skipped with it
+      const bool bad = ctl.bad[s0] || (two && ctl.bad[s1]);
+      seg_bad |= bad;
+      if (!bad) {
+        if (two) {
+          const uint8_t *kp[2] = {kbuf + off0, kbuf + off1}, *vp[2] = {vbuf + off0, vbuf + off1};
+          const float2 sc[2] = {ctl.sc[s0][head], ctl.sc[s1][head]};
+          ba_tiles<D, RK, 2>(st, kp, vp, sc, tok, min_lim, sg.L, gq, tq);
+        } else {
+          const uint8_t *kp[1] = {kbuf + off0}, *vp[1] = {vbuf + off0};
+          const float2 sc[1] = {ctl.sc[s0][head]};
+          ba_tiles<D, RK, 1>(st, kp, vp, sc, tok, min_lim, sg.L, gq, tq);
+        }
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.empty[slot]);
+      if (lane == 0) {
+        mbar_arrive(&ctl.empty[s0]);
+        if (two) mbar_arrive(&ctl.empty[s1]);
+      }
     }
     g0 += sg.stages;
     __syncwarp();
     if (lane == 0) mbar_arrive(&ctl.segempty[ss]);
+    ++nseg;
 
-    // ---- the segment's end
+    // ---- the segment's end: the row's denominator, marked if a page was bad
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      st.l[g] += __shfl_xor_sync(0xffffffffu, st.l[g], 1);
+      st.l[g] += __shfl_xor_sync(0xffffffffu, st.l[g], 2);
+      if (seg_bad) st.l[g] = -1.f;
+    }
+    if (a.tw > 1) {
+      // The teams' sums go to team 0, halving the teams each round.  Every round
+      // has slots of its own, so one barrier a round orders its writes before
+      // its reads, and one after the last keeps the next segment's writes off.
+      if (nmerge > 0 && !ba_wait_warp(ctl, &ctl.mempty[pair], (nmerge - 1) & 1, a.err_word)) return;
+      int alive = a.tw, slot0 = 0, round = 0;
+      while (alive > 1) {
+        const int half = (alive + 1) / 2;
+        if (team >= half && team < alive) {
+          float *w = slots + static_cast<int64_t>((slot0 + team - half) * ngrp + pair) * kBaSlotWords<D, RK> + lane;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) w[32 * ((g * KS + i) * 4 + k)] = st.o[i][g][k];
+            w[32 * (KS * NG * 4 + 3 * g)] = st.m[g];
+            w[32 * (KS * NG * 4 + 3 * g + 1)] = st.l[g];
+            w[32 * (KS * NG * 4 + 3 * g + 2)] = st.n[g];
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.mfull[pair]);
+        if (!ba_wait_warp(ctl, &ctl.mfull[pair], (nmerge * a.rounds + round) & 1, a.err_word)) return;
+        if (team < alive - half) {
+          const float *w = slots + static_cast<int64_t>((slot0 + team) * ngrp + pair) * kBaSlotWords<D, RK> + lane;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const float m2 = w[32 * (KS * NG * 4 + 3 * g)], l2 = w[32 * (KS * NG * 4 + 3 * g + 1)];
+            const float n2 = w[32 * (KS * NG * 4 + 3 * g + 2)];
+            const bool bad = st.l[g] < 0.f || l2 < 0.f;
+            // a side that saw nothing (l = 0) has no maximum and no weight
+            const float M = fmaxf(st.m[g], m2), N = fmaxf(st.n[g], n2);
+            const float fl = st.l[g] == 0.f ? 0.f : exp2f(st.m[g] - M), f2 = l2 == 0.f ? 0.f : exp2f(m2 - M);
+            const float fo = st.l[g] == 0.f ? 0.f : exp2f(st.n[g] - N), o2 = l2 == 0.f ? 0.f : exp2f(n2 - N);
+            st.l[g] = bad ? -1.f : st.l[g] * fl + l2 * f2;
+            st.m[g] = M;
+            st.n[g] = N;
+            // columns 2t and 2t + 1 of O^T are the rows of lanes 8t and 8t + 4
+            const float fa = __shfl_sync(0xffffffffu, fo, 8 * tq), fb = __shfl_sync(0xffffffffu, fo, 8 * tq + 4);
+            const float ga = __shfl_sync(0xffffffffu, o2, 8 * tq), gb = __shfl_sync(0xffffffffu, o2, 8 * tq + 4);
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                st.o[i][g][k] = st.o[i][g][k] * ((k & 1) ? fb : fa) +
+                                w[32 * ((g * KS + i) * 4 + k)] * ((k & 1) ? gb : ga);
+          }
+        }
+        slot0 += alive - half;
+        alive = half;
+        ++round;
+      }
+      ++nmerge;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.mempty[pair]);
+      if (team > 0) continue;
+    }
+    const int used = min(RK, sg.n * a.G - row_base);  // rows of this warp that exist
+    float *to = a.part + (static_cast<int64_t>(sg.part) * ngrp + pair) * (RK * RF);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       if constexpr (RK == 4) {  // columns 4..7 hold the remainders' sums
@@ -703,18 +844,6 @@ __global__ void __launch_bounds__(kBaThreads, 1)
           for (int k = 0; k < 4; ++k)
             st.o[i][g][k] += __shfl_down_sync(0xffffffffu, st.o[i][g][k], 2);
       }
-      st.l[g] += __shfl_xor_sync(0xffffffffu, st.l[g], 1);
-      st.l[g] += __shfl_xor_sync(0xffffffffu, st.l[g], 2);
-      if (seg_bad) st.l[g] = -1.f;  // marks a part that met a page outside the pool
-    }
-    const bool many = a.tw > 1;
-    const int used = min(RK, sg.n * a.G - row_base);  // rows of this warp that exist
-    float *to = many ? area + static_cast<int64_t>(warp) * RK * RF
-                     : a.part + (static_cast<int64_t>(sg.part) * ngrp + pair) * (RK * RF);
-    const bool direct = !many && sg.part < 0;
-    if (many && nseg > 0 && !ba_wait_warp(ctl, &ctl.mempty[pair], (nseg - 1) & 1, a.err_word)) return;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
       const float la = __shfl_sync(0xffffffffu, st.l[g], 8 * tq);
       const float lb = __shfl_sync(0xffffffffu, st.l[g], 8 * tq + 4);
       const float ma = __shfl_sync(0xffffffffu, st.m[g], 8 * tq);
@@ -726,7 +855,7 @@ __global__ void __launch_bounds__(kBaThreads, 1)
         const int r = 2 * tq + e + 8 * g;
         if (r >= used || r >= RK) continue;
         const float l = e ? lb : la, m = e ? mb : ma, n = e ? nb : na;
-        if (direct) {
+        if (sg.part < 0) {
           // 2^(n - m) / (l 2^7); a bad row is zeros, selected and not scaled
           const float f = l < 0.f ? 0.f : exp2f(n - m - 7.f) / l;
           float *o = ba_out_row<D>(a, sg, kvh, row_base + r) + (D / 8) * gq;
@@ -745,50 +874,6 @@ __global__ void __launch_bounds__(kBaThreads, 1)
         }
       }
     }
-    if (many) {
-      // ---- the teams' partials of each row: team t merges rows t, t + tw, ...
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.mfull[pair]);
-      if (!ba_wait_warp(ctl, &ctl.mfull[pair], nseg & 1, a.err_word)) return;
-      for (int r = team; r < used; r += a.tw) {
-        float M = -INFINITY, N = -INFINITY;
-        bool bad = false;
-        for (int t = 0; t < a.tw; ++t) {
-          const float *p = area + (static_cast<int64_t>(t * ngrp + pair) * RK + r) * RF;
-          const float4 s = *reinterpret_cast<const float4 *>(p + D);
-          M = fmaxf(M, s.x);
-          N = fmaxf(N, s.z);
-          bad |= s.y < 0.f;
-        }
-        float l = 0.f;
-        float acc[D / 32];
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
-        for (int t = 0; t < a.tw; ++t) {
-          const float *p = area + (static_cast<int64_t>(t * ngrp + pair) * RK + r) * RF;
-          const float4 s = *reinterpret_cast<const float4 *>(p + D);
-          if (s.y == 0.f) continue;  // saw nothing
-          l += exp2f(s.x - M) * s.y;
-          const float f = exp2f(s.z - N);
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) acc[k] += f * p[lane + 32 * k];
-        }
-        if (sg.part < 0) {
-          const float f = bad ? 0.f : exp2f(N - M - 7.f) / l;
-          float *o = ba_out_row<D>(a, sg, kvh, row_base + r);
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) o[lane + 32 * k] = bad ? 0.f : acc[k] * f;
-        } else {
-          float *o = a.part + ((static_cast<int64_t>(sg.part) * ngrp + pair) * RK + r) * RF;
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) o[lane + 32 * k] = acc[k];
-          if (lane == 0) *reinterpret_cast<float4 *>(o + D) = make_float4(M, bad ? -1.f : l, N, 0.f);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.mempty[pair]);
-    }
-    ++nseg;
   }
 }
 
@@ -1016,6 +1101,8 @@ extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q
   a.hg = s.hg;
   a.rt = s.rt;
   a.tw = s.tw;
+  a.rounds = 0;
+  for (int t = s.tw; t > 1; t = (t + 1) / 2) ++a.rounds;
   a.row_blocks = s.row_blocks;
   a.groups = s.groups;
   a.stages = ba_stages(s, D);
