@@ -110,7 +110,7 @@ struct BaArgs {
   float *part;           // [2 CTAs][hg * rt][rk][D + kStat]
   float *out;
   uint32_t *err_word;
-  int32_t num_pages, P, Hkv, Hq, G, MP, max_q;
+  int32_t num_pages, p_shift, Hkv, Hq, G, MP, max_q;  // page size 1 << p_shift
   int32_t hg, rt, tw, rounds, row_blocks, groups, stages;  // rounds: of the teams' merge
   float q_scale;  // sm_scale * log2(e)
 };
@@ -603,7 +603,12 @@ __global__ void __launch_bounds__(kBaThreads, 1)
     const uint64_t pol = policy_evict_first();
     int64_t u = u0, in = run.in;
     int b = run.b;
-    uint32_t g = 0, nseg = 0;  // stages and segments issued
+    // stages and segments issued; the next stage's ring slot and the parity of
+    // its empty barrier's phase (kept by steps: a division by the ring's
+    // length each stage cost the warp more than the copies)
+    uint32_t g = 0, nseg = 0;
+    int slot = 0;
+    uint32_t par = 1;
     bool ok = true;
     int win_b = -1, win = 0, cur = -1, nxt = -1;  // block-table window (two of 32 entries)
     const int32_t *bt = a.block_table;
@@ -642,7 +647,7 @@ __global__ void __launch_bounds__(kBaThreads, 1)
         mbar_arrive(&ctl.segfull[ss]);
       }
       ++nseg;
-      const int lp0 = t_begin / a.P;
+      const int lp0 = t_begin >> a.p_shift;
       if (b != win_b || lp0 < win || lp0 >= win + 32) {
         win_b = b;
         win = lp0;
@@ -650,18 +655,13 @@ __global__ void __launch_bounds__(kBaThreads, 1)
         cur = bt_load(win + lane);
         nxt = bt_load(win + 32 + lane);
       }
-      for (int st = 0; st < take; ++st, ++g) {
-        const int slot = g % NS;
-        bool waited = true;
-        if (lane == 0 && g >= NS)
-          waited = ba_wait(ctl, &ctl.empty[slot], ((g / NS) - 1) & 1, a.err_word);
-        ok = __shfl_sync(0xffffffffu, waited ? 1 : 0, 0) != 0 &&
-             !*reinterpret_cast<volatile int *>(&ctl.fail);
-        ok = __all_sync(0xffffffffu, ok);
+      for (int st = 0, tok = t_begin; st < take; ++st, tok += kTile) {
+        // on a ring's first round the wait returns at once: the phase before a
+        // barrier's first counts as completed
+        ok = ba_wait_warp(ctl, &ctl.empty[slot], par, a.err_word);
         if (!ok) break;
-        const int tok = t_begin + st * kTile;
-        const int lp = tok / a.P;
-        while (lp >= win + 32) {
+        const int lp = tok >> a.p_shift;
+        if (lp >= win + 32) {  // at most one window a stage
           win += 32;
           cur = nxt;
           nxt = bt_load(win + 32 + lane);
@@ -670,14 +670,15 @@ __global__ void __launch_bounds__(kBaThreads, 1)
         const bool bad = page < 0 || page >= a.num_pages;
         if (lane == 0) {
           ctl.bad[slot] = bad;
-          if (bad) report(a.err_word, KVQ_ERRBIT_PAGE);
           mbar_arrive_expect_tx(&ctl.full[slot], bad ? 0u : 2u * stage_bytes);
           if (!bad) {
-            const int y = tok % a.P;
+            const int y = tok & ((1 << a.p_shift) - 1);
             tma_load_4d(kbuf + slot * stage_bytes, &kmap, 0, y, grp * a.hg, page, &ctl.full[slot],
                         pol);
             tma_load_4d(vbuf + slot * stage_bytes, &vmap, 0, y, grp * a.hg, page, &ctl.full[slot],
                         pol);
+          } else {
+            report(a.err_word, KVQ_ERRBIT_PAGE);
           }
         }
         if (lane < a.hg) {
@@ -685,6 +686,11 @@ __global__ void __launch_bounds__(kBaThreads, 1)
             cp_async8(&ctl.sc[slot][lane],
                       a.scales + static_cast<int64_t>(page) * a.Hkv + grp * a.hg + lane);
           cp_async_arrive(&ctl.full[slot]);
+        }
+        ++g;
+        if (++slot == NS) {
+          slot = 0;
+          par ^= 1;
         }
         __syncwarp();
       }
@@ -736,11 +742,14 @@ __global__ void __launch_bounds__(kBaThreads, 1)
     ba_begin<D, RK>(st, a, sg, kvh, row_base, gq, tq);
     const int min_lim = min(sg.L, sg.L - sg.n + 1 + (sg.rb * rows) / a.G);
     bool seg_bad = false;
+    // the ring slot and phase parity of the team's first stage
+    int s0 = static_cast<int>((g0 + 2 * team) % NS);
+    uint32_t p0 = ((g0 + 2 * team) / NS) & 1;
     for (int k = 2 * team; k < sg.stages; k += 2 * a.tw) {  // a turn: two stages
-      const int s0 = (g0 + k) % NS, s1 = (g0 + k + 1) % NS;
       const bool two = k + 1 < sg.stages;
-      if (!ba_wait_warp(ctl, &ctl.full[s0], ((g0 + k) / NS) & 1, a.err_word)) return;
-      if (two && !ba_wait_warp(ctl, &ctl.full[s1], ((g0 + k + 1) / NS) & 1, a.err_word)) return;
+      const int s1 = s0 + 1 == NS ? 0 : s0 + 1;
+      if (!ba_wait_warp(ctl, &ctl.full[s0], p0, a.err_word)) return;
+      if (two && !ba_wait_warp(ctl, &ctl.full[s1], s1 == 0 ? p0 ^ 1 : p0, a.err_word)) return;
       const int tok = sg.t_begin + k * kTile;
       const uint32_t off0 = s0 * stage_bytes + head * (kTile * D), off1 = s1 * stage_bytes + head * (kTile * D);
       // a row that meets a bad page is zeros: its other tiles are skipped with it
@@ -761,6 +770,11 @@ __global__ void __launch_bounds__(kBaThreads, 1)
       if (lane == 0) {
         mbar_arrive(&ctl.empty[s0]);
         if (two) mbar_arrive(&ctl.empty[s1]);
+      }
+      s0 += 2 * a.tw;
+      if (s0 >= NS) {  // 2 tw <= NS
+        s0 -= NS;
+        p0 ^= 1;
       }
     }
     g0 += sg.stages;
@@ -1092,7 +1106,7 @@ extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q
   a.out = out;
   a.err_word = err_word;
   a.num_pages = cache->num_pages;
-  a.P = cache->page_size;
+  a.p_shift = cache->page_size == 16 ? 4 : cache->page_size == 32 ? 5 : 6;
   a.Hkv = Hkv;
   a.Hq = Hq;
   a.G = G;
