@@ -79,13 +79,26 @@ inline BaShape ba_shape(int max_q, int G, int Hkv) {
   return s;
 }
 
-// One segment: a run of units of one row, of one CTA.
+// Units that a row of work counts beside its tiles: its start (q, the first
+// block-table entries, the pipeline's fill) and end, in tiles' times.  Without
+// them a CTA whose run holds many short rows ends long after the others.
+constexpr int kRowCost = 4;
+
+// One segment: a run of tiles of one row, of one CTA.
 struct BaSeg {
   int b, grp, rb;      // request (-1: no more segments), head group, row block
   int row0, n, L;      // the request's first row, rows, length
   int t_begin, t_end;  // tokens
   int stages;
   int part;            // -1: the row is this segment alone; else the partial slot
+};
+
+// The row of work that starts in a CTA and goes on past its end, if any: the
+// rows that combine has to merge (a CTA's end cuts one row at most).
+struct BaCut {
+  int parts;             // 0: none; its parts lie in this CTA and the next ones
+  int grp, rb, row0, n;
+  int pad[3];
 };
 
 struct BaCtl {
@@ -106,12 +119,12 @@ struct BaArgs {
   const int32_t *block_table;
   const uint8_t *abort_mask;
   const float2 *scales;  // [num_pages][Hkv]
-  int2 *desc;            // [B][row_blocks][groups]: (first CTA, parts) of every row of work
+  BaCut *cut;            // [CTAs]
   float *part;           // [2 CTAs][hg * rt][rk][D + kStat]
   float *out;
   uint32_t *err_word;
   int32_t num_pages, p_shift, Hkv, Hq, G, MP, max_q;  // page size 1 << p_shift
-  int32_t hg, rt, tw, rounds, row_blocks, groups, stages;  // rounds: of the teams' merge
+  int32_t hg, rt, tw, rounds, groups, stages;  // rounds: of the teams' merge
   float q_scale;  // sm_scale * log2(e)
 };
 
@@ -123,8 +136,8 @@ __device__ __forceinline__ Rows ba_rows(const BaArgs &a, int b, bool &live) {
   return r;
 }
 
-// Units of one row of work and row blocks of a live request.
-__device__ __forceinline__ int ba_units(const Rows &r) { return (r.p0 + r.n + kTile - 1) / kTile; }
+// 16-token tiles of one row of work, and row blocks, of a live request.
+__device__ __forceinline__ int ba_tiles_of(const Rows &r) { return (r.p0 + r.n + kTile - 1) / kTile; }
 __device__ __forceinline__ int ba_blocks(const BaArgs &a, const Rows &r, int rows) {
   return (r.n * a.G + rows - 1) / rows;
 }
@@ -239,17 +252,33 @@ __device__ __forceinline__ void ba_pv(float (&o)[D / 16][BaState<D, RK>::NG][4],
                                       const uint32_t (&hi)[BaState<D, RK>::NG][2],
                                       const uint32_t (&lo)[BaState<D, RK>::NG][2]) {
   constexpr int KS = D / 16, NG = BaState<D, RK>::NG;
+  // the two MMAs on one accumulator lie four MMAs apart (their latency)
+  constexpr int BI = 4 / NG;
 #pragma unroll
-  for (int i = 0; i < KS; ++i) {
-    const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;  // bytes (a.b, b.b, a.b+1, b.b+1)
-    const uint32_t x = prmt(wa[i >> 1], wb[i >> 1], sel);
-    const uint32_t y = prmt(wc[i >> 1], wd[i >> 1], sel);
-    const uint32_t a0 = e4m3x2_to_f16x2(x & 0xFFFFu), a1 = e4m3x2_to_f16x2(x >> 16);
-    const uint32_t a2 = e4m3x2_to_f16x2(y & 0xFFFFu), a3 = e4m3x2_to_f16x2(y >> 16);
+  for (int i0 = 0; i0 < KS; i0 += BI) {
+    uint32_t f[BI][4];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      mma_16816(o[i][g], a0, a1, a2, a3, hi[g][0], hi[g][1]);
-      if constexpr (RK > 4) mma_16816(o[i][g], a0, a1, a2, a3, lo[g][0], lo[g][1]);
+    for (int j = 0; j < BI; ++j) {
+      const int i = i0 + j;
+      const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;  // bytes (a.b, b.b, a.b+1, b.b+1)
+      const uint32_t x = prmt(wa[i >> 1], wb[i >> 1], sel);
+      const uint32_t y = prmt(wc[i >> 1], wd[i >> 1], sel);
+      f[j][0] = e4m3x2_to_f16x2(x & 0xFFFFu);
+      f[j][1] = e4m3x2_to_f16x2(x >> 16);
+      f[j][2] = e4m3x2_to_f16x2(y & 0xFFFFu);
+      f[j][3] = e4m3x2_to_f16x2(y >> 16);
+    }
+#pragma unroll
+    for (int j = 0; j < BI; ++j)
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+        mma_16816(o[i0 + j][g], f[j][0], f[j][1], f[j][2], f[j][3], hi[g][0], hi[g][1]);
+    if constexpr (RK > 4) {
+#pragma unroll
+      for (int j = 0; j < BI; ++j)
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          mma_16816(o[i0 + j][g], f[j][0], f[j][1], f[j][2], f[j][3], lo[g][0], lo[g][1]);
     }
   }
 }
@@ -592,7 +621,7 @@ __global__ void __launch_bounds__(kBaThreads, 1)
         bool live;
         const Rows r = ba_rows(a, b, live);
         if (r.err && blockIdx.x == 0) report(a.err_word, r.err);
-        return live ? static_cast<int64_t>(ba_units(r)) * a.groups * ba_blocks(a, r, rows) : 0;
+        return live ? static_cast<int64_t>(ba_tiles_of(r) + kRowCost) * a.groups * ba_blocks(a, r, rows) : 0;
       });
   allow_dependents();
   const int64_t u0 = blockIdx.x * run.per;
@@ -603,6 +632,7 @@ __global__ void __launch_bounds__(kBaThreads, 1)
     const uint64_t pol = policy_evict_first();
     int64_t u = u0, in = run.in;
     int b = run.b;
+    BaCut cut = {0, 0, 0, 0, 0, {0, 0, 0}};
     // stages and segments issued; the next stage's ring slot and the parity of
     // its empty barrier's phase (kept by steps: a division by the ring's
     // length each stage cost the warp more than the copies)
@@ -616,7 +646,7 @@ __global__ void __launch_bounds__(kBaThreads, 1)
     while (ok && u < u1) {
       bool live;
       const Rows rq = ba_rows(a, b, live);
-      const int units = live ? ba_units(rq) : 0;
+      const int tiles = live ? ba_tiles_of(rq) : 0, units = tiles + kRowCost;
       const int64_t have = live ? static_cast<int64_t>(units) * a.groups * ba_blocks(a, rq, rows) : 0;
       if (in >= have) {
         ++b;
@@ -626,12 +656,17 @@ __global__ void __launch_bounds__(kBaThreads, 1)
       const int64_t rw = in / units;  // row of work: row block major
       const int s = static_cast<int>(in - rw * units);
       const int rb = static_cast<int>(rw / a.groups), grp = static_cast<int>(rw - static_cast<int64_t>(rb) * a.groups);
-      const int take = static_cast<int>(min(static_cast<int64_t>(units - s), u1 - u));
+      const int span = static_cast<int>(min(static_cast<int64_t>(units - s), u1 - u));
+      // units [0, kRowCost) of a row stand for its start; tile t is unit kRowCost + t
+      const int t0 = max(0, s - kRowCost), take = s + span - kRowCost - t0;
+      const int64_t ut = u - s + kRowCost;  // the row's first tile
+      u += span;
+      in += span;
+      if (take <= 0) continue;
       const int L = rq.p0 + rq.n;
-      const int t_begin = s * kTile, t_end = min((s + take) * kTile, L);
-      const int64_t ur = u - s;  // the row's first unit
-      const int64_t c_lo = ur / run.per;
-      const int nparts = static_cast<int>((ur + units - 1) / run.per - c_lo) + 1;
+      const int t_begin = t0 * kTile, t_end = min((t0 + take) * kTile, L);
+      const int64_t c_lo = ut / run.per;
+      const int nparts = static_cast<int>((ut + tiles - 1) / run.per - c_lo) + 1;
       const int ss = nseg % kBaSegs;
       bool w = true;
       if (lane == 0 && nseg >= kBaSegs)
@@ -639,11 +674,9 @@ __global__ void __launch_bounds__(kBaThreads, 1)
       ok = __shfl_sync(0xffffffffu, w ? 1 : 0, 0) != 0;
       if (!ok) break;
       if (lane == 0) {
-        if (s == 0)
-          a.desc[(static_cast<int64_t>(b) * a.row_blocks + rb) * a.groups + grp] =
-              make_int2(static_cast<int>(c_lo), nparts);
+        if (t0 == 0 && nparts > 1) cut = {nparts, grp, rb, rq.row, rq.n, {0, 0, 0}};
         ctl.seg[ss] = {b, grp, rb, rq.row, rq.n, L, t_begin, t_end, take,
-                       nparts == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (s == 0 ? 1 : 0)};
+                       nparts == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (t0 == 0 ? 1 : 0)};
         mbar_arrive(&ctl.segfull[ss]);
       }
       ++nseg;
@@ -694,9 +727,8 @@ __global__ void __launch_bounds__(kBaThreads, 1)
         }
         __syncwarp();
       }
-      u += take;
-      in += take;
     }
+    if (lane == 0) a.cut[blockIdx.x] = cut;
     if (ok) {  // nothing more
       const int ss = nseg % kBaSegs;
       if (lane == 0 && (nseg < kBaSegs ||
@@ -897,106 +929,121 @@ __global__ void __launch_bounds__(kBaThreads, 1)
 
 constexpr int kBcbWarps = 8;
 
-// Output rows (request, row block, head group, head, row tile, row), one a
-// warp (kWide false) or one a CTA whose warps take every eighth part (kWide
-// true, for batches of so few rows that one is cut into many parts).
+// blockIdx.x: which of the cut rows, in the order of their CTAs (there are at
+// most as many as rows of work, and fewer than CTAs); blockIdx.y: which of its output
+// rows, eight a CTA and one a warp (kWide false), or one whose parts the eight
+// warps share (kWide true: batches of so few rows that one has many parts).
 //   out = 2^(N - M) sum_p 2^(n_p - N) o_p / sum_p 2^(m_p - M) l_p
 template <int D, bool kWide>
-__global__ void __launch_bounds__(32 * kBcbWarps) block_combine_kernel(BaArgs a, int rk) {
+__global__ void __launch_bounds__(32 * kBcbWarps) block_combine_kernel(BaArgs a, int rk_shift,
+                                                                      int ctas) {
   constexpr int V = D / 32, RF = D + kStat, kBatch = 4;
   __shared__ float s_acc[kWide ? kBcbWarps : 1][D];
   __shared__ float4 s_st[kWide ? kBcbWarps : 1];
+  __shared__ int s_cnt[kBcbWarps], s_cta;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int idx = kWide ? blockIdx.y : blockIdx.y * kBcbWarps + warp;  // (pair, row)
+  const int ngrp = a.hg * a.rt, rk = 1 << rk_shift;
+  const int pair = idx >> rk_shift, rr = idx & (rk - 1);
+  const int head = pair / a.rt, tile = pair - head * a.rt;
   grid_dependency_wait();
   allow_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ngrp = a.hg * a.rt, rows = rk * a.rt;
-  const int64_t total = static_cast<int64_t>(a.rg.B) * a.row_blocks * a.groups * ngrp * rk;
-  const int64_t step = kWide ? gridDim.x : static_cast<int64_t>(gridDim.x) * kBcbWarps;
-  for (int64_t it = kWide ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kBcbWarps + warp;
-       it < total; it += step) {
-    const int rr = static_cast<int>(it % rk);
-    const int64_t t1 = it / rk;
-    const int pair = static_cast<int>(t1 % ngrp);
-    const int64_t work = t1 / ngrp;  // (request, row block, group)
-    const int grp = static_cast<int>(work % a.groups);
-    const int64_t t2 = work / a.groups;
-    const int rb = static_cast<int>(t2 % a.row_blocks), b = static_cast<int>(t2 / a.row_blocks);
-    bool live;
-    const Rows rq = ba_rows(a, b, live);
-    const int r = rb * rows + (pair % a.rt) * rk + rr;
-    if (!live || r >= rq.n * a.G) continue;
-    const int2 d = __ldcg(a.desc + work);
-    if (d.y < 2) continue;
-    float M = -INFINITY, N = -INFINITY, l = 0.f, acc[V];
-    bool bad = false;
+  // the CTA that holds cut row blockIdx.x's first part
+  int before = 0;
+  if (threadIdx.x == 0) s_cta = -1;
+  for (int c = threadIdx.x; c - static_cast<int>(threadIdx.x) < ctas; c += 32 * kBcbWarps) {
+    const bool is_cut = c < ctas && __ldcg(&a.cut[c].parts) > 0;
+    const unsigned in_warp = __ballot_sync(0xffffffffu, is_cut);
+    __syncthreads();
+    if (lane == 0) s_cnt[warp] = __popc(in_warp);
+    __syncthreads();
+    int rank = before + __popc(in_warp & ((1u << lane) - 1));
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = 0.f;
-    // part p lies in CTA d.x + p's slot 0, the first one in slot 1 of CTA d.x
-    for (int p0 = kWide ? warp : 0; p0 < d.y; p0 += kBatch * (kWide ? kBcbWarps : 1)) {
-      float4 s[kBatch];
-      float v[kBatch][V];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int p = p0 + j * (kWide ? kBcbWarps : 1);
-        s[j] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-        if (p < d.y) {
-          const float *q = a.part + ((static_cast<int64_t>(2 * (d.x + p) + (p == 0)) * ngrp + pair) * rk + rr) * RF;
-          s[j] = __ldcg(reinterpret_cast<const float4 *>(q + D));
-#pragma unroll
-          for (int k = 0; k < V; ++k) v[j][k] = __ldcg(q + lane + 32 * k);
-        }
-      }
-      float Mb = M, Nb = N;
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        Mb = fmaxf(Mb, s[j].x);
-        Nb = fmaxf(Nb, s[j].z);
-        bad |= s[j].y < 0.f;
-      }
-      const float fl = M == -INFINITY ? 0.f : exp2f(M - Mb), fo = N == -INFINITY ? 0.f : exp2f(N - Nb);
-      l *= fl;
-#pragma unroll
-      for (int k = 0; k < V; ++k) acc[k] *= fo;
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        if (s[j].y == 0.f) continue;  // saw nothing
-        l = fmaf(exp2f(s[j].x - Mb), s[j].y, l);
-        const float f = exp2f(s[j].z - Nb);
-#pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] = fmaf(f, v[j][k], acc[k]);
-      }
-      M = Mb;
-      N = Nb;
+    for (int w = 0; w < kBcbWarps; ++w) {
+      if (w < warp) rank += s_cnt[w];
+      before += s_cnt[w];
     }
-    const int i = r / a.G;
-    float *out = a.out + ((static_cast<int64_t>(rq.row) + i) * a.Hq + (grp * a.hg + pair / a.rt) * a.G + r - i * a.G) * D;
-    if constexpr (!kWide) {
-      const float f = bad ? 0.f : exp2f(N - M - 7.f) / l;
+    if (is_cut && rank == static_cast<int>(blockIdx.x)) s_cta = c;
+  }
+  __syncthreads();
+  const int cta = s_cta;
+  if (cta < 0) return;
+  const int4 c0 = __ldcg(reinterpret_cast<const int4 *>(a.cut + cta));
+  const int n = __ldcg(&a.cut[cta].n);
+  const int parts = c0.x, grp = c0.y, rb = c0.z, row0 = c0.w;
+  const int r = (rb * a.rt + tile) * rk + rr;
+  if (pair >= ngrp || r >= n * a.G) return;
+  float M = -INFINITY, N = -INFINITY, l = 0.f, acc[V];
+  bool bad = false;
 #pragma unroll
-      for (int k = 0; k < V; ++k) out[lane + 32 * k] = bad ? 0.f : acc[k] * f;
-    } else {
+  for (int k = 0; k < V; ++k) acc[k] = 0.f;
+  // part p lies in the p-th CTA from here on: the first in slot 1, others in slot 0
+  const float *base = a.part + ((static_cast<int64_t>(2 * cta) * ngrp + pair) * rk + rr) * RF;
+  const int64_t slot = static_cast<int64_t>(ngrp) * rk * RF;
+  constexpr int kStep = kWide ? kBcbWarps : 1;
+  for (int p0 = kWide ? warp : 0; p0 < parts; p0 += kBatch * kStep) {
+    float4 s[kBatch];
+    float v[kBatch][V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) s_acc[warp][lane + 32 * k] = acc[k];
-      if (lane == 0) s_st[warp] = make_float4(M, bad ? -1.f : l, N, 0.f);
-      __syncthreads();
-      if (threadIdx.x < D) {
-        float Mr = -INFINITY, Nr = -INFINITY, lr = 0.f, o = 0.f;
-        bool rbad = false;
+    for (int j = 0; j < kBatch; ++j) {
+      const int p = p0 + j * kStep;
+      s[j] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+      if (p < parts) {
+        const float *q = base + (2 * p + (p == 0)) * slot;
+        s[j] = __ldcg(reinterpret_cast<const float4 *>(q + D));
 #pragma unroll
-        for (int w = 0; w < kBcbWarps; ++w) {
-          Mr = fmaxf(Mr, s_st[w].x);
-          Nr = fmaxf(Nr, s_st[w].z);
-          rbad |= s_st[w].y < 0.f;
-        }
-#pragma unroll
-        for (int w = 0; w < kBcbWarps; ++w) {
-          if (s_st[w].y == 0.f) continue;
-          lr = fmaf(exp2f(s_st[w].x - Mr), s_st[w].y, lr);
-          o = fmaf(exp2f(s_st[w].z - Nr), s_acc[w][threadIdx.x], o);
-        }
-        out[threadIdx.x] = rbad ? 0.f : o * (exp2f(Nr - Mr - 7.f) / lr);
+        for (int k = 0; k < V; ++k) v[j][k] = __ldcg(q + lane + 32 * k);
       }
-      __syncthreads();
+    }
+    float Mb = M, Nb = N;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      Mb = fmaxf(Mb, s[j].x);
+      Nb = fmaxf(Nb, s[j].z);
+      bad |= s[j].y < 0.f;
+    }
+    const float fl = M == -INFINITY ? 0.f : exp2f(M - Mb), fo = N == -INFINITY ? 0.f : exp2f(N - Nb);
+    l *= fl;
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] *= fo;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (s[j].y == 0.f) continue;  // saw nothing
+      l = fmaf(exp2f(s[j].x - Mb), s[j].y, l);
+      const float f = exp2f(s[j].z - Nb);
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[k] = fmaf(f, v[j][k], acc[k]);
+    }
+    M = Mb;
+    N = Nb;
+  }
+  const int i = r / a.G;
+  float *out = a.out + ((static_cast<int64_t>(row0) + i) * a.Hq + (grp * a.hg + head) * a.G + r - i * a.G) * D;
+  if constexpr (!kWide) {
+    const float f = bad ? 0.f : exp2f(N - M - 7.f) / l;
+#pragma unroll
+    for (int k = 0; k < V; ++k) out[lane + 32 * k] = bad ? 0.f : acc[k] * f;
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) s_acc[warp][lane + 32 * k] = acc[k];
+    if (lane == 0) s_st[warp] = make_float4(M, bad ? -1.f : l, N, 0.f);
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float Mr = -INFINITY, Nr = -INFINITY, lr = 0.f, o = 0.f;
+      bool rbad = false;
+#pragma unroll
+      for (int w = 0; w < kBcbWarps; ++w) {
+        Mr = fmaxf(Mr, s_st[w].x);
+        Nr = fmaxf(Nr, s_st[w].z);
+        rbad |= s_st[w].y < 0.f;
+      }
+#pragma unroll
+      for (int w = 0; w < kBcbWarps; ++w) {
+        if (s_st[w].y == 0.f) continue;
+        lr = fmaf(exp2f(s_st[w].x - Mr), s_st[w].y, lr);
+        o = fmaf(exp2f(s_st[w].z - Nr), s_acc[w][threadIdx.x], o);
+      }
+      out[threadIdx.x] = rbad ? 0.f : o * (exp2f(Nr - Mr - 7.f) / lr);
     }
   }
 }
@@ -1029,8 +1076,8 @@ bool ba_opt_in(BaFn fn, int variant) {
   return true;
 }
 
-size_t ba_desc_bytes(int64_t B, const BaShape &s) {
-  return (static_cast<size_t>(B) * s.row_blocks * s.groups * sizeof(int2) + 255) & ~size_t(255);
+size_t ba_cut_bytes(int ctas) {
+  return (static_cast<size_t>(ctas) * sizeof(BaCut) + 255) & ~static_cast<size_t>(255);
 }
 
 size_t ba_part_bytes(const BaShape &s, int D, int ctas) {
@@ -1067,7 +1114,7 @@ extern "C" size_t kvq_block_attn_workspace_size(int32_t B, int32_t max_q, int32_
   int sms = 0;
   if (device_sm_count(&sms) != KVQ_OK) return 0;
   const BaShape s = ba_shape(max_q, Hq / num_kv_heads, num_kv_heads);
-  return ba_desc_bytes(B, s) + ba_part_bytes(s, head_dim, sms);
+  return ba_cut_bytes(sms) + ba_part_bytes(s, head_dim, sms);
 }
 
 extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q, int64_t q_stride,
@@ -1091,8 +1138,8 @@ extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q
   int sms = 0;
   if (device_sm_count(&sms) != KVQ_OK) return KVQ_ERR_CUDA;
   const BaShape s = ba_shape(max_q, G, Hkv);
-  const size_t db = ba_desc_bytes(B, s);
-  if (!aligned256(workspace) || workspace_bytes < db + ba_part_bytes(s, D, sms))
+  const size_t cb = ba_cut_bytes(sms);
+  if (!aligned256(workspace) || workspace_bytes < cb + ba_part_bytes(s, D, sms))
     return KVQ_ERR_WORKSPACE;
   BaArgs a;
   a.q = static_cast<const uint16_t *>(q);
@@ -1101,8 +1148,8 @@ extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q
   a.block_table = block_table;
   a.abort_mask = abort_mask;
   a.scales = reinterpret_cast<const float2 *>(cache->scales);
-  a.desc = static_cast<int2 *>(workspace);
-  a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + db);
+  a.cut = static_cast<BaCut *>(workspace);
+  a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + cb);
   a.out = out;
   a.err_word = err_word;
   a.num_pages = cache->num_pages;
@@ -1117,7 +1164,6 @@ extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q
   a.tw = s.tw;
   a.rounds = 0;
   for (int t = s.tw; t > 1; t = (t + 1) / 2) ++a.rounds;
-  a.row_blocks = s.row_blocks;
   a.groups = s.groups;
   a.stages = ba_stages(s, D);
   a.q_scale = sm_scale * kLog2e;
@@ -1129,17 +1175,16 @@ extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (launch_dependent(fn, sms, kBaThreads, kBaSmem, cs, kmap, vmap, a) != cudaSuccess)
     return KVQ_ERR_CUDA;
-  // rows of work a CTA: with fewer than one in three, a row is cut into four
-  // parts or more, and a CTA merges each of its output rows
+  // fewer than a row of work for three CTAs: a row is cut into four parts or
+  // more, and a CTA merges each of its output rows
   const int64_t work = static_cast<int64_t>(B) * s.row_blocks * s.groups;
-  const int64_t outs = work * s.hg * s.rt * s.rk;
   const bool wide = work * 3 < sms;
-  const int64_t want = wide ? outs : (outs + kBcbWarps - 1) / kBcbWarps;
-  const int64_t most = 8LL * sms;
-  const int grid = static_cast<int>(want < most ? want : most);
+  const int outs = s.pairs() * s.rk;  // output rows of a row of work
+  const dim3 grid(static_cast<unsigned>(work < sms - 1 ? work : sms - 1), wide ? outs : (outs + kBcbWarps - 1) / kBcbWarps);
   const auto cfn = D == 128 ? (wide ? block_combine_kernel<128, true> : block_combine_kernel<128, false>)
                             : (wide ? block_combine_kernel<64, true> : block_combine_kernel<64, false>);
-  if (launch_dependent(cfn, grid, 32 * kBcbWarps, 0, cs, a, s.rk) != cudaSuccess)
+  const int rk_shift = s.rk == 4 ? 2 : s.rk == 8 ? 3 : 4;
+  if (launch_dependent(cfn, grid, 32 * kBcbWarps, 0, cs, a, rk_shift, sms) != cudaSuccess)
     return KVQ_ERR_CUDA;
   return KVQ_OK;
 }
