@@ -444,61 +444,79 @@ def kvq_decode_attn_static(cache: KVCache, q, block_table, seq_lens, out, abort_
 # ----------------------------------------------------------------------------
 
 _F8 = (torch.uint8, torch.float8_e4m3fn)
+_F32 = (torch.float32,)
+_F64 = (torch.float64,)
+_BYTES = (torch.uint8,)
 
 
-def _arr(t, name, dtype, shape):
-    """Pointer of a contiguous device array of the given dtype and shape."""
-    if t.dtype is not dtype and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise ValueError(f"{name}: dtype {t.dtype} is not {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, is {list(t.shape)}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+# The checks below run on every call of a decode step, so they are written for
+# few attribute look-ups: a decode step's kernels take a few microseconds.
+
+def _arr(t, name, dtypes, shape, dev):
+    """Pointer of a contiguous array of the given dtypes and shape on device dev."""
+    if t.dtype not in dtypes or t.shape != shape or t.get_device() != dev or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtypes[0]} tensor {list(shape)} on "
+                         f"cuda:{dev}; it is {t.dtype} {list(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
     return t.data_ptr()
 
 
-def _rows(t, name, n, heads, D):
+def _rows(t, name, n, heads, D, dev):
     """(pointer, token stride) of a bf16 [n, heads, D] tensor strided by token."""
-    if t.dtype is not torch.bfloat16:
-        raise ValueError(f"{name}: dtype {t.dtype} is not bfloat16")
-    if t.shape != (n, heads, D):
-        raise ValueError(f"{name} must be [{n}, {heads}, {D}], is {list(t.shape)}")
     st = t.stride()
-    if not t.is_cuda or st[2] != 1 or (st[1] != D and heads > 1):
-        raise ValueError(f"{name} must be a CUDA tensor with contiguous rows of heads")
+    if t.dtype is not torch.bfloat16 or t.shape != (n, heads, D) or t.get_device() != dev or \
+            st[2] != 1 or (st[1] != D and heads > 1):
+        raise ValueError(f"{name} must be a bfloat16 tensor {[n, heads, D]} on cuda:{dev} with "
+                         f"contiguous rows of heads; it is {t.dtype} {list(t.shape)}, strides "
+                         f"{list(st)}, on {t.device}")
     return t.data_ptr(), (st[0] if n > 1 else heads * D)
 
 
-def _launch(fn, name, dev, tensors, stream, args):
-    """Calls the library with `dev` current, on `stream` or its current stream."""
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: tensors lie on {t.device} and {dev}")
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
-            st = fn(*args, _stream(stream))
+def _device(t, name) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _launch(fn, name, dev, stream, args):
+    """Calls the library with device `dev` current, on `stream` or that device's
+    current stream."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
     else:
-        st = fn(*args, _stream(stream))
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
     if st != 0:
         raise KvqError(name, st)
 
 
-@dataclass
+@dataclass(frozen=True)
 class BlockKVCache:
     """Caller-owned e4m3 pools [num_pages, Hkv, P, D] and the scale of each
-    (page, kv head) block of K and of V: scales fp32 [num_pages, Hkv, 2]."""
+    (page, kv head) block of K and of V: scales fp32 [num_pages, Hkv, 2].  A
+    handle: the tensors are checked once, here, and held."""
     k_pool: torch.Tensor
     v_pool: torch.Tensor
     scales: torch.Tensor
 
-    def c(self) -> CBlockCache:
-        shape = self.k_pool.shape
+    def __post_init__(self):
+        shape, dev = tuple(self.k_pool.shape), _device(self.k_pool, "k_pool")
         if len(shape) != 4:
             raise ValueError("k_pool must have 4 dims")
         NP, H, P, D = shape
-        return CBlockCache(_arr(self.k_pool, "k_pool", _F8, shape),
-                           _arr(self.v_pool, "v_pool", _F8, shape),
-                           _arr(self.scales, "scales", torch.float32, (NP, H, 2)), NP, P, H, D)
+        c = CBlockCache(_arr(self.k_pool, "k_pool", _F8, shape, dev),
+                        _arr(self.v_pool, "v_pool", _F8, shape, dev),
+                        _arr(self.scales, "scales", _F32, (NP, H, 2), dev), NP, P, H, D)
+        object.__setattr__(self, "_c", (ctypes.byref(c), dev, H, D))
+
+    def c(self):
+        """(reference to the C descriptor, device, kv heads, head_dim)"""
+        return self._c
 
     @staticmethod
     def empty(num_pages, num_kv_heads, page_size, head_dim, device="cuda"):
@@ -508,18 +526,25 @@ class BlockKVCache:
                             torch.ones((num_pages, num_kv_heads, 2), device=device))
 
 
-@dataclass
+@dataclass(frozen=True)
 class Rope:
     """Rotary positions: inv_freq float64 [rotary_dim / 2] on the device
-    (radians per position), the pairs' layout and the factor on the result."""
+    (radians per position), the pairs' layout and the factor on the result.  A
+    handle, like BlockKVCache."""
     inv_freq: torch.Tensor
     layout: int = ROPE_HALF
     mscale: float = 1.0
 
-    def c(self) -> CRope:
-        n = self.inv_freq.shape[0] if self.inv_freq.dim() == 1 else -1
-        return CRope(_arr(self.inv_freq, "inv_freq", torch.float64, (n,)), 2 * n,
-                     int(self.layout), float(self.mscale))
+    def __post_init__(self):
+        dev = _device(self.inv_freq, "inv_freq")
+        n = self.inv_freq.numel()
+        c = CRope(_arr(self.inv_freq, "inv_freq", _F64, (n,), dev), 2 * n, int(self.layout),
+                  float(self.mscale))
+        object.__setattr__(self, "_c", (ctypes.byref(c), dev))
+
+    def c(self):
+        """(reference to the C descriptor, device)"""
+        return self._c
 
 
 def kvq_rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: int = ROPE_PLAIN,
@@ -536,80 +561,80 @@ def kvq_rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: int = ROP
     return out, m.value
 
 
+def _rope(rope, dev):
+    r, d = rope.c()
+    if d != dev:
+        raise ValueError(f"inv_freq lies on cuda:{d}, the call's tensors on cuda:{dev}")
+    return r
+
+
 def kvq_rope(rope: Rope, pos, q, q_out, k=None, k_out=None, stream=None) -> None:
     """Rotate rows of q into q_out (and of k into k_out); row t stands at
     position pos[t] (int32).  An output may be its input."""
-    L = load()
+    L = _lib or load()
     N, Hq, D = q.shape
-    qa, qb = _rows(q, "q", N, Hq, D), _rows(q_out, "q_out", N, Hq, D)
+    dev = _device(q, "q")
+    qa, qb = _rows(q, "q", N, Hq, D, dev), _rows(q_out, "q_out", N, Hq, D, dev)
     Hk, ka, kb = 0, (None, 0), (None, 0)
     if k is not None:
         Hk = k.shape[1]
-        ka, kb = _rows(k, "k", N, Hk, D), _rows(k_out, "k_out", N, Hk, D)
-    _launch(L.kvq_rope, "kvq_rope", q.device, (pos, q_out, k, k_out, rope.inv_freq), stream,
-            (rope.c(), _arr(pos, "pos", torch.int32, (N,)), N, D, *qa, *qb, Hq, *ka, *kb, Hk))
+        ka, kb = _rows(k, "k", N, Hk, D, dev), _rows(k_out, "k_out", N, Hk, D, dev)
+    _launch(L.kvq_rope, "kvq_rope", dev, stream,
+            (_rope(rope, dev), _arr(pos, "pos", I32, (N,), dev), N, D, *qa, *qb, Hq, *ka, *kb, Hk))
 
 
-def _step(tok_start, seq_lens, block_table, name="seq_lens"):
+def _step(tok_start, seq_lens, block_table, dev, name="seq_lens"):
     B, MP = block_table.shape
-    return (None if tok_start is None else _arr(tok_start, "tok_start", torch.int32, (B + 1,)),
-            None if seq_lens is None else _arr(seq_lens, name, torch.int32, (B,)),
-            _arr(block_table, "block_table", torch.int32, (B, MP)), B, MP)
+    return (None if tok_start is None else _arr(tok_start, "tok_start", I32, (B + 1,), dev),
+            None if seq_lens is None else _arr(seq_lens, name, I32, (B,), dev),
+            _arr(block_table, "block_table", I32, (B, MP), dev), B, MP)
 
 
-def _err(err_word):
-    return None if err_word is None else _arr(err_word, "err_word", U32, (1,))
+def _err(err_word, dev):
+    return None if err_word is None else _arr(err_word, "err_word", U32, (1,), dev)
 
 
 def kvq_block_append(cache: BlockKVCache, k_new, v_new, tok_start, seq_lens, block_table,
                      err_word=None, stream=None) -> None:
     """Quantise rows of k_new / v_new [rows, Hkv, D] into their requests' pages
     and set the blocks' scales (include/kvq.h)."""
-    L = load()
-    c = cache.c()
+    L = _lib or load()
+    c, dev, H, D = cache.c()
     N = k_new.shape[0]
-    ka = _rows(k_new, "k_new", N, c.num_kv_heads, c.head_dim)
-    va = _rows(v_new, "v_new", N, c.num_kv_heads, c.head_dim)
-    ts, sl, bt, B, MP = _step(tok_start, seq_lens, block_table)
-    _launch(L.kvq_block_append, "kvq_block_append", k_new.device,
-            (cache.k_pool, cache.v_pool, cache.scales, v_new, tok_start, seq_lens, block_table,
-             err_word), stream, (c, *ka, *va, ts, N, sl, bt, B, MP, _err(err_word)))
+    ts, sl, bt, B, MP = _step(tok_start, seq_lens, block_table, dev)
+    _launch(L.kvq_block_append, "kvq_block_append", dev, stream,
+            (c, *_rows(k_new, "k_new", N, H, D, dev), *_rows(v_new, "v_new", N, H, D, dev), ts, N,
+             sl, bt, B, MP, _err(err_word, dev)))
 
 
 def kvq_rope_block_append(cache: BlockKVCache, rope: Rope, q, q_out, k_new, v_new, tok_start,
                           seq_lens, block_table, err_word=None, stream=None) -> None:
     """kvq_block_append with K rotated on the way in, and q rotated into q_out
     (q and q_out may be None), in one launch."""
-    L = load()
-    c = cache.c()
+    L = _lib or load()
+    c, dev, H, D = cache.c()
     N = k_new.shape[0]
-    D = c.head_dim
-    ka = _rows(k_new, "k_new", N, c.num_kv_heads, D)
-    va = _rows(v_new, "v_new", N, c.num_kv_heads, D)
     Hq, qa, qb = 0, (None, 0), (None, 0)
     if q is not None:
         Hq = q.shape[1]
-        qa, qb = _rows(q, "q", N, Hq, D), _rows(q_out, "q_out", N, Hq, D)
-    ts, sl, bt, B, MP = _step(tok_start, seq_lens, block_table)
-    _launch(L.kvq_rope_block_append, "kvq_rope_block_append", k_new.device,
-            (cache.k_pool, cache.v_pool, cache.scales, v_new, q, q_out, rope.inv_freq, tok_start,
-             seq_lens, block_table, err_word), stream,
-            (c, rope.c(), *qa, *qb, Hq, *ka, *va, ts, N, sl, bt, B, MP, _err(err_word)))
+        qa, qb = _rows(q, "q", N, Hq, D, dev), _rows(q_out, "q_out", N, Hq, D, dev)
+    ts, sl, bt, B, MP = _step(tok_start, seq_lens, block_table, dev)
+    _launch(L.kvq_rope_block_append, "kvq_rope_block_append", dev, stream,
+            (c, _rope(rope, dev), *qa, *qb, Hq, *_rows(k_new, "k_new", N, H, D, dev),
+             *_rows(v_new, "v_new", N, H, D, dev), ts, N, sl, bt, B, MP, _err(err_word, dev)))
 
 
 def kvq_block_read(cache: BlockKVCache, tok_start, first, block_table, k_out, v_out,
                    err_word=None, stream=None) -> None:
     """Read cached tokens back into k_out / v_out [rows, Hkv, D] bf16: row i of
     request b is its position first[b] + i (first None: from position 0)."""
-    L = load()
-    c = cache.c()
+    L = _lib or load()
+    c, dev, H, D = cache.c()
     N = k_out.shape[0]
-    ka = _rows(k_out, "k_out", N, c.num_kv_heads, c.head_dim)
-    va = _rows(v_out, "v_out", N, c.num_kv_heads, c.head_dim)
-    ts, fi, bt, B, MP = _step(tok_start, first, block_table, "first")
-    _launch(L.kvq_block_read, "kvq_block_read", k_out.device,
-            (cache.k_pool, cache.v_pool, cache.scales, v_out, tok_start, first, block_table,
-             err_word), stream, (c, ts, N, fi, bt, B, MP, *ka, *va, _err(err_word)))
+    ts, fi, bt, B, MP = _step(tok_start, first, block_table, dev, "first")
+    _launch(L.kvq_block_read, "kvq_block_read", dev, stream,
+            (c, ts, N, fi, bt, B, MP, *_rows(k_out, "k_out", N, H, D, dev),
+             *_rows(v_out, "v_out", N, H, D, dev), _err(err_word, dev)))
 
 
 def kvq_block_attn_workspace_size(B: int, max_q: int, Hq: int, num_kv_heads: int,
@@ -622,6 +647,8 @@ def block_workspace(B: int, max_q: int, Hq: int, num_kv_heads: int, head_dim: in
     """Allocate (with torch) a workspace of the size kvq_block_attn needs."""
     with torch.cuda.device(device):
         n = kvq_block_attn_workspace_size(B, max_q, Hq, num_kv_heads, head_dim)
+    if n == 0:
+        raise ValueError("kvq_block_attn does not support these sizes")
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
@@ -630,18 +657,14 @@ def kvq_block_attn(cache: BlockKVCache, q, tok_start, seq_lens, block_table, out
                    err_word=None, stream=None) -> None:
     """Causal attention of each request's rows (at most max_q a request) over
     its cached tokens: q [rows, Hq, D] bf16, out [rows, Hq, D] fp32."""
-    L = load()
-    c = cache.c()
-    N, Hq, D = q.shape
-    qa = _rows(q, "q", N, Hq, c.head_dim)
-    ts, sl, bt, B, MP = _step(tok_start, seq_lens, block_table)
-    if sm_scale is None:
-        sm_scale = 1.0 / math.sqrt(D)
-    _launch(L.kvq_block_attn, "kvq_block_attn", q.device,
-            (cache.k_pool, cache.v_pool, cache.scales, out, workspace, tok_start, seq_lens,
-             block_table, abort_mask, err_word), stream,
-            (c, *qa, Hq, ts, N, int(max_q), sl, bt, B, MP,
-             None if abort_mask is None else _arr(abort_mask, "abort_mask", U8, (B,)),
-             float(sm_scale), _arr(out, "out", torch.float32, (N, Hq, D)),
-             _arr(workspace, "workspace", torch.uint8, workspace.shape), workspace.numel(),
-             _err(err_word)))
+    L = _lib or load()
+    c, dev, _, D = cache.c()
+    N, Hq = q.shape[0], q.shape[1]
+    ts, sl, bt, B, MP = _step(tok_start, seq_lens, block_table, dev)
+    _launch(L.kvq_block_attn, "kvq_block_attn", dev, stream,
+            (c, *_rows(q, "q", N, Hq, D, dev), Hq, ts, N, max_q, sl, bt, B, MP,
+             None if abort_mask is None else _arr(abort_mask, "abort_mask", U8, (B,), dev),
+             D ** -0.5 if sm_scale is None else sm_scale,
+             _arr(out, "out", _F32, (N, Hq, D), dev),
+             _arr(workspace, "workspace", _BYTES, workspace.shape, dev), workspace.numel(),
+             _err(err_word, dev)))

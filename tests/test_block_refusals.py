@@ -153,15 +153,15 @@ def test_inv_freq_refusals(args):
 def test_binding_refuses_host_and_misshapen_tensors():
     pool = torch.zeros(4, 2, 16, 64, dtype=torch.uint8)
     with pytest.raises(ValueError):
-        kvq.BlockKVCache(pool, pool, torch.ones(4, 2, 2)).c()  # host memory
+        kvq.BlockKVCache(pool, pool, torch.ones(4, 2, 2))  # host memory
     with pytest.raises(ValueError):
-        kvq.BlockKVCache(pool, pool[:2], torch.ones(4, 2, 2)).c()
+        kvq.BlockKVCache(pool, pool[:2], torch.ones(4, 2, 2))
     with pytest.raises(ValueError):
-        kvq.Rope(torch.zeros(8)).c()  # not float64
+        kvq.Rope(torch.zeros(8, dtype=torch.float64))
     x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
-    with pytest.raises(ValueError):
-        kvq._rows(x, "q", 3, 2, 64)
-    with pytest.raises(ValueError):
-        kvq._rows(x.float(), "q", 3, 2, 64)
-    with pytest.raises(ValueError):
-        kvq._rows(x, "q", 3, 4, 64)
+    for bad in (x, x.float(), x[:, :1], x.transpose(0, 1)):
+        with pytest.raises(ValueError):
+            kvq._rows(bad, "q", 3, 2, 64, 0)
+    for bad in (torch.zeros(3, dtype=torch.int32), torch.zeros(3), torch.zeros(4, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            kvq._arr(bad, "pos", (torch.int32,), (3,), 0)
