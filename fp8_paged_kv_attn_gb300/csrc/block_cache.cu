@@ -7,13 +7,22 @@
 // equal run of items (find_run), so that one prompt among decode tokens
 // does not leave the other SMs idle.
 //
-// Append: a warp takes 16 rows (tokens) of one head's K or V in one page, so
-// the 16 x D values stay in registers between the maximum that sets the scale
-// and the conversion: K and V are read once.  A 64-token page's block is four
-// warps, which exchange their maxima through shared memory.  The page's
-// angles are computed once into shared memory for all heads and q.
-// Bandwidth-bound on prompts (2 D (2 + 1) bytes a token and kv head);
-// latency-bound on a decode step.
+// Append has three kernels, all with the maximum that sets a block's scale and
+// the conversion in one visit:
+//   short  decode and draft steps: latency counts.  K, V and q of a page go to
+//          CTAs of their own, a warp takes one head's rows, four (head_dim 128)
+//          at a time; further rows are read twice, the second time from L1.
+//   ring   prompts with enough kv heads: bandwidth counts (2 D (2 + 1) bytes a
+//          token and kv head, 4 D a query head).  A producer warp stages the
+//          rows of a page and a group of heads with one TMA copy each into a
+//          shared-memory ring; a consumer warp takes 16 rows of one head.
+//   wide   prompts with few kv heads: the same without the ring, a warp's 16
+//          rows loaded by itself.
+// In 32- and 64-token pages the warps of a block exchange their maxima through
+// shared memory.  The page's angles are computed once into shared memory and
+// used by all heads.
+#include <atomic>
+
 #include "block_common.cuh"
 
 namespace kvq {
@@ -45,7 +54,7 @@ __device__ __forceinline__ int64_t pages_touched(const Rows &r, int P) {
   return r.n == 0 || r.err ? 0 : (r.p0 + r.n - 1) / P - r.p0 / P + 1;
 }
 
-// Old codes of a block whose scale grew: rows [0, n_old) of this warp's 16.
+// Old codes of a block whose scale grew: rows [0, n_old) from `block` on.
 template <int D>
 __device__ __forceinline__ void requantise_rows(uint8_t *block, int n_old, float ratio, int lane) {
   constexpr int kLanes = D / 16;  // lanes a row, 16 codes each
@@ -64,121 +73,293 @@ __device__ __forceinline__ void requantise_rows(uint8_t *block, int n_old, float
   }
 }
 
+// The next page of a CTA's run.
+struct PageWalk {
+  int64_t left, in;
+  int b;
+};
+
+struct PageItem {
+  int page;          // -1: outside the pool
+  int first;         // position of the first row
+  int slot0, nrow;   // slots [slot0, slot0 + nrow) of the page
+  int64_t row0;
+  int part;          // share of the page (short kernel)
+};
+
+template <bool kLens>
+__device__ __forceinline__ bool next_page(const Ragged &rg, const int32_t *block_table, int MP,
+                                          int P, int num_pages, int parts, PageWalk &w,
+                                          PageItem &it) {
+  if (w.left <= 0) return false;
+  Rows rq = request_rows<kLens>(rg, w.b);
+  while (w.in >= pages_touched(rq, P) * parts) {
+    ++w.b;
+    w.in = 0;
+    rq = request_rows<kLens>(rg, w.b);
+  }
+  const int pg = parts == 1 ? static_cast<int>(w.in) : static_cast<int>(w.in / parts);
+  it.part = static_cast<int>(w.in - static_cast<int64_t>(pg) * parts);
+  ++w.in;
+  --w.left;
+  const int lp = rq.p0 / P + pg;
+  const int page = __ldg(block_table + static_cast<int64_t>(w.b) * MP + lp);
+  it.page = page >= 0 && page < num_pages ? page : -1;
+  it.first = max(rq.p0, lp * P);
+  it.slot0 = it.first - lp * P;
+  it.nrow = min(rq.p0 + rq.n, lp * P + P) - it.first;
+  it.row0 = static_cast<int64_t>(rq.row) + (it.first - rq.p0);
+  return true;
+}
+
+// The CTA's run of pages (every thread calls it).
+template <int NT, bool kLens>
+__device__ __forceinline__ PageWalk page_run(const Ragged &rg, int P, int parts, uint32_t *err_word,
+                                             RunScan<NT> &scan) {
+  const RunStart run = find_run<NT>(rg.B, gridDim.x, blockIdx.x, scan, [&](int b) -> int64_t {
+    const Rows r = request_rows<kLens>(rg, b);
+    if (r.err && blockIdx.x == 0) report(err_word, r.err);
+    return pages_touched(r, P) * parts;
+  });
+  return {min(run.per, run.total - blockIdx.x * run.per), run.in, run.b};
+}
+
+// Angles of rows 0 .. nrow - 1, at positions first + row, into tab: threads
+// tid, tid + nt, ... of those that call.
+__device__ __forceinline__ void fill_angles(float4 *tab, const uint64_t *freq, int first, int nrow,
+                                            int rd, bool half, float mscale, int tid, int nt) {
+  const int nq = rd / 4;
+  for (int j = tid; j < nrow * nq; j += nt) {
+    const int r = j / nq, q = j - r * nq;
+    const float2 x = rotation(first + r, freq[2 * q], mscale);
+    const float2 y = rotation(first + r, freq[2 * q + 1], mscale);
+    tab[r * nq + angle_slot(q, rd, half)] = make_float4(x.x, x.y, y.x, y.y);
+  }
+}
+
+// 16 values (an item) -> codes at the two chunks of a row.
+__device__ __forceinline__ void store_codes(uint8_t *row, ItemChunks ch, const float (&y)[16],
+                                            float inv) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t o[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float *v = y + 8 * c + 4 * j;
+      o[j] = static_cast<uint32_t>(f32x2_to_e4m3x2(v[0] * inv, v[1] * inv)) |
+             (static_cast<uint32_t>(f32x2_to_e4m3x2(v[2] * inv, v[3] * inv)) << 16);
+    }
+    *reinterpret_cast<uint2 *>(row + (c ? ch.c1 : ch.c0) * 8) = make_uint2(o[0], o[1]);
+  }
+}
+
+// A rotated item -> bf16 at the two chunks; a chunk past rotary_dim as it came.
+__device__ __forceinline__ void store_rotated(uint16_t *row, ItemChunks ch, const float (&y)[16],
+                                              uint4 w0, uint4 w1, int i, int D, int rd, bool half) {
+  const int lim = half ? (i < rd / 16 ? D / 8 : 0) : rd / 8;
+  *reinterpret_cast<uint4 *>(row + ch.c0 * 8) = ch.c0 < lim ? pack8(y) : w0;
+  *reinterpret_cast<uint4 *>(row + ch.c1 * 8) = ch.c1 < lim ? pack8(y + 8) : w1;
+}
+
+__device__ __forceinline__ float item_amax(const float (&y)[16]) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) m = fmaxf(m, finite_abs(y[j]));
+  return m;
+}
+
+__device__ __forceinline__ float warp_max(float m) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+// ---- short steps
+
 template <int D, bool kRope>
-__global__ void __launch_bounds__(kBcThreads, 2) block_append_kernel(BlockAppendArgs a) {
-  constexpr int kItems = D / 16;           // lanes a row (two 8-dim chunks each)
-  constexpr int kRpp = 32 / kItems;        // rows a pass of a warp
-  constexpr int kPasses = kRowsPerWarp / kRpp;
-  extern __shared__ float4 tab[];          // kRope: [P][rd / 4] angles of the page's rows
+__global__ void __launch_bounds__(kBcThreads, 4) block_append_short(BlockAppendArgs a, int parts) {
+  constexpr int kItems = D / 16;      // lanes a row (two 8-dim chunks each)
+  constexpr int kRpp = 32 / kItems;   // rows a warp pass
+  extern __shared__ float4 tab[];     // kRope: [P][rd / 4] angles of the page's rows
   __shared__ RunScan<kBcThreads> scan;
   __shared__ uint64_t s_freq[kRope ? D / 2 : 1];
-  __shared__ float s_amax[2][kBcWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int P = a.c.P, H = a.c.H;
-  const int team = P / kRowsPerWarp;       // warps a block: 1, 2 or 4
-  const int sub = warp % team;             // this warp's 16 rows of the block
   const int i = lane % kItems, r0 = lane / kItems;
   const bool half = !kRope || a.rope.layout == KVQ_ROPE_HALF;
   const int rd = kRope ? a.rope.rd : D;
   const ItemChunks ch = item_chunks(i, D, rd, half);
   grid_dependency_wait();
   allow_dependents();
-  if constexpr (kRope) {
-    for (int j = threadIdx.x; j < rd / 2; j += kBcThreads)
-      s_freq[j] = turns_per_token(a.rope.inv_freq[j]);
-  }
-  const RunStart run = find_run<kBcThreads>(
-      a.rg.B, gridDim.x, blockIdx.x, scan, [&](int b) -> int64_t {
-        const Rows r = request_rows<true>(a.rg, b);
-        if (r.err && blockIdx.x == 0) report(a.err_word, r.err);
-        return pages_touched(r, P);
-      });
-  int64_t left = min(run.per, run.total - blockIdx.x * run.per);
-  int b = run.b;
-  int64_t in = run.in;
-  uint32_t round = 0;
-  while (left > 0) {  // uniform over the CTA
-    const Rows rq = request_rows<true>(a.rg, b);
-    const int64_t have = pages_touched(rq, P);
-    if (in >= have) {
-      ++b;
-      in = 0;
+  double freq = 0.0;  // in flight while the requests are scanned (rd / 2 <= blockDim)
+  if constexpr (kRope)
+    if (threadIdx.x < rd / 2) freq = a.rope.inv_freq[threadIdx.x];
+  PageWalk walk = page_run<kBcThreads, true>(a.rg, P, parts, a.err_word, scan);
+  if constexpr (kRope)
+    if (threadIdx.x < rd / 2) s_freq[threadIdx.x] = turns_per_token(freq);
+  PageItem it;
+  while (next_page<true>(a.rg, a.block_table, a.MP, P, a.c.num_pages, parts, walk, it)) {
+    const bool is_v = it.part == 1;
+    if (kRope && !is_v) {  // uniform over the CTA
+      __syncthreads();  // the previous item's angles are no longer read (and s_freq is set)
+      fill_angles(tab, s_freq, it.first, it.nrow, rd, half, a.rope.mscale, threadIdx.x, kBcThreads);
+      __syncthreads();
+    }
+    auto rotate = [&](float (&y)[16], int r) {
+      if constexpr (kRope)
+        if (!is_v && r < it.nrow) rotate_item(y, tab + r * (rd / 4), i, rd, half, ch);
+    };
+    if (it.part == 2) {  // q: rows of (token, head)
+      if (it.page < 0) continue;
+      const int total = it.nrow * a.Hq;
+      for (int base = warp * kRpp; base < total; base += 2 * kBcWarps * kRpp) {
+        uint4 w[2][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int e = base + j * kBcWarps * kRpp + r0, r = e / a.Hq;
+          if (e < total) {
+            const uint16_t *s = a.q + (it.row0 + r) * a.q_stride + static_cast<int64_t>(e - r * a.Hq) * D;
+            w[j][0] = *reinterpret_cast<const uint4 *>(s + ch.c0 * 8);
+            w[j][1] = *reinterpret_cast<const uint4 *>(s + ch.c1 * 8);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int e = base + j * kBcWarps * kRpp + r0, r = e / a.Hq;
+          if (e < total) {
+            float y[16];
+            unpack8(w[j][0], y);
+            unpack8(w[j][1], y + 8);
+            rotate(y, r);
+            store_rotated(a.q_out + (it.row0 + r) * a.q_out_stride + static_cast<int64_t>(e - r * a.Hq) * D,
+                          ch, y, w[j][0], w[j][1], i, D, rd, half);
+          }
+        }
+      }
       continue;
     }
-    const int lp = rq.p0 / P + static_cast<int>(in);
-    ++in;
-    --left;
-    const int first = max(rq.p0, lp * P);              // the item's positions
-    const int last = min(rq.p0 + rq.n, lp * P + P);    // [first, last)
-    const int row0 = rq.row + (first - rq.p0);
-    const int slot0 = first - lp * P, nrow = last - first;
-    const int page = __ldg(a.block_table + static_cast<int64_t>(b) * a.MP + lp);
-    if (page < 0 || page >= a.c.num_pages) {
+    for (int h = warp; h < H; h += kBcWarps) {
+      const uint16_t *src = (is_v ? a.v_new : a.k_new) + static_cast<int64_t>(h) * D;
+      const int64_t stride = is_v ? a.v_stride : a.k_stride;
+      auto load = [&](int r, float (&y)[16]) {
+        uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+        if (r < it.nrow) {
+          const uint16_t *s = src + (it.row0 + r) * stride;
+          w0 = __ldg(reinterpret_cast<const uint4 *>(s + ch.c0 * 8));
+          w1 = __ldg(reinterpret_cast<const uint4 *>(s + ch.c1 * 8));
+        }
+        unpack8(w0, y);
+        unpack8(w1, y + 8);
+        rotate(y, r);
+      };
+      float y[16];
+      load(r0, y);  // its addresses do not need the page
+      if (it.page < 0) {
+        if (lane == 0) report(a.err_word, KVQ_ERRBIT_PAGE);
+        break;
+      }
+      const int64_t blk = static_cast<int64_t>(it.page) * H + h;
+      float *scale = a.c.scales + 2 * blk + is_v;
+      const float s_old = it.slot0 > 0 ? *scale : 0.f;
+      float amax = item_amax(y);
+      for (int r = kRpp + r0; r - r0 < it.nrow; r += kRpp) {
+        load(r, y);
+        amax = fmaxf(amax, item_amax(y));
+      }
+      amax = warp_max(amax);
+      const float s_new = fmaxf(pow2(block_exponent(amax)), s_old);
+      const float inv = 1.0f / s_new;  // exact: a power of two
+      uint8_t *block = (is_v ? a.c.v : a.c.k) + blk * P * D;
+      if (s_new > s_old && it.slot0 > 0)
+        requantise_rows<D>(block, it.slot0, s_old / s_new, lane);
+      if (lane == 0) *scale = s_new;
+      for (int r = r0; r - r0 < it.nrow; r += kRpp) {
+        if (it.nrow > kRpp) load(r, y);
+        if (r < it.nrow) store_codes(block + (it.slot0 + r) * D, ch, y, inv);
+      }
+    }
+  }
+}
+
+// ---- prompts, a warp's rows loaded by itself
+
+template <int D, bool kRope>
+__global__ void __launch_bounds__(kBcThreads, kRope ? 2 : 3) block_append_wide(BlockAppendArgs a) {
+  constexpr int kItems = D / 16;
+  constexpr int kRpp = 32 / kItems;
+  constexpr int kPasses = kRowsPerWarp / kRpp;
+  extern __shared__ float4 tab[];
+  __shared__ RunScan<kBcThreads> scan;
+  __shared__ uint64_t s_freq[kRope ? D / 2 : 1];
+  __shared__ float s_amax[2][kBcWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int P = a.c.P, H = a.c.H;
+  const int i = lane % kItems, r0 = lane / kItems;
+  const bool half = !kRope || a.rope.layout == KVQ_ROPE_HALF;
+  const int rd = kRope ? a.rope.rd : D;
+  const ItemChunks ch = item_chunks(i, D, rd, half);
+  grid_dependency_wait();
+  allow_dependents();
+  if constexpr (kRope)
+    if (threadIdx.x < rd / 2) s_freq[threadIdx.x] = turns_per_token(a.rope.inv_freq[threadIdx.x]);
+  PageWalk walk = page_run<kBcThreads, true>(a.rg, P, 1, a.err_word, scan);
+  PageItem it;
+  uint32_t round = 0;
+  while (next_page<true>(a.rg, a.block_table, a.MP, P, a.c.num_pages, 1, walk, it)) {  // uniform
+    if (it.page < 0) {
       if (threadIdx.x == 0) report(a.err_word, KVQ_ERRBIT_PAGE);
       continue;
     }
     if constexpr (kRope) {
       __syncthreads();  // the previous item's angles are no longer read (and s_freq is set)
-      for (int j = threadIdx.x; j < nrow * (rd / 4); j += kBcThreads) {
-        const int r = j / (rd / 4), q = j % (rd / 4);
-        const float2 x = rotation(first + r, s_freq[2 * q], a.rope.mscale);
-        const float2 y = rotation(first + r, s_freq[2 * q + 1], a.rope.mscale);
-        tab[r * (rd / 4) + angle_slot(q, rd, half)] = make_float4(x.x, x.y, y.x, y.y);
-      }
+      fill_angles(tab, s_freq, it.first, it.nrow, rd, half, a.rope.mscale, threadIdx.x, kBcThreads);
       __syncthreads();
     }
-    // this warp's rows of the page: slots [16 sub, 16 sub + 16)
-    const int lo = max(slot0, kRowsPerWarp * sub), hi = min(slot0 + nrow, kRowsPerWarp * (sub + 1));
-    const int units = 2 * H, step = kBcWarps / team;
-    for (int u0 = 0; u0 < units; u0 += step, ++round) {
+    // warps a block: one takes up to 16 rows, more rows take one for each 16 slots
+    const int team = it.nrow <= kRowsPerWarp ? 1 : P / kRowsPerWarp;
+    const int sub = team == 1 ? 0 : warp % team;
+    const int wbase = team == 1 ? it.slot0 : kRowsPerWarp * sub;
+    const int lo = max(it.slot0, wbase), hi = min(it.slot0 + it.nrow, wbase + kRowsPerWarp);
+    for (int u0 = 0; u0 < 2 * H; u0 += kBcWarps / team, ++round) {
       const int u = u0 + warp / team;  // (head, K or V)
-      const bool live = u < units;
+      const bool live = u < 2 * H;
       const int h = u >> 1, is_v = u & 1;
       uint4 w[kPasses][2];
-      float amax = 0.f;
       if (live) {
         const uint16_t *src = (is_v ? a.v_new : a.k_new) + static_cast<int64_t>(h) * D;
         const int64_t stride = is_v ? a.v_stride : a.k_stride;
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
-          const int slot = kRowsPerWarp * sub + p * kRpp + r0;
+          const int slot = wbase + p * kRpp + r0;
           w[p][0] = w[p][1] = make_uint4(0, 0, 0, 0);
           if (slot >= lo && slot < hi) {
-            const uint16_t *s = src + (row0 + slot - slot0) * stride;
+            const uint16_t *s = src + (it.row0 + slot - it.slot0) * stride;
             w[p][0] = __ldg(reinterpret_cast<const uint4 *>(s + ch.c0 * 8));
             w[p][1] = __ldg(reinterpret_cast<const uint4 *>(s + ch.c1 * 8));
           }
         }
       }
-      const int64_t blk = static_cast<int64_t>(page) * H + h;
-      const float s_old = live && slot0 > 0 ? a.c.scales[2 * blk + is_v] : 0.f;
-      // rotated K values are needed twice (maximum, conversion): kept in fp32
-      float x[kRope ? kPasses : 1][16];
-      if constexpr (kRope) {
+      const int64_t blk = static_cast<int64_t>(it.page) * H + h;
+      const float s_old = live && it.slot0 > 0 ? a.c.scales[2 * blk + is_v] : 0.f;
+      auto item = [&](int p, float (&y)[16]) {
+        const int slot = wbase + p * kRpp + r0;
+        unpack8(w[p][0], y);
+        unpack8(w[p][1], y + 8);
+        if constexpr (kRope)
+          if (!is_v && slot >= lo && slot < hi)
+            rotate_item(y, tab + (slot - it.slot0) * (rd / 4), i, rd, half, ch);
+      };
+      float amax = 0.f;
+      if (live) {
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
-          const int slot = kRowsPerWarp * sub + p * kRpp + r0;
-          unpack8(w[p][0], x[p]);
-          unpack8(w[p][1], x[p] + 8);
-          if (!is_v && slot >= lo && slot < hi)
-            rotate_item(x[p], tab + (slot - slot0) * (rd / 4), i, rd, half, ch);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) amax = fmaxf(amax, finite_abs(x[p][j]));
+          float y[16];
+          item(p, y);
+          amax = fmaxf(amax, item_amax(y));
         }
-      } else {
-#pragma unroll
-        for (int p = 0; p < kPasses; ++p)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float y[8];
-            unpack8(w[p][c], y);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(y[j]));
-          }
+        amax = warp_max(amax);
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      if (team > 1) {  // uniform over the grid
+      if (team > 1) {  // uniform over the CTA
         float *m = s_amax[round & 1];
         if (lane == 0) m[warp] = amax;
         __syncthreads();
@@ -188,57 +369,270 @@ __global__ void __launch_bounds__(kBcThreads, 2) block_append_kernel(BlockAppend
       }
       if (!live) continue;
       const float s_new = fmaxf(pow2(block_exponent(amax)), s_old);
-      const float inv = 1.0f / s_new;  // exact: a power of two
+      const float inv = 1.0f / s_new;
       uint8_t *block = (is_v ? a.c.v : a.c.k) + blk * P * D;
-      if (s_new > s_old && slot0 > kRowsPerWarp * sub)
-        requantise_rows<D>(block + static_cast<int64_t>(kRowsPerWarp * sub) * D,
-                           min(slot0 - kRowsPerWarp * sub, kRowsPerWarp), s_old / s_new, lane);
-      if (sub == 0 && lane == 0) a.c.scales[2 * blk + is_v] = s_new;
+      if (s_new > s_old && it.slot0 > 0) {  // this warp's old rows: its 16's, or all of them
+        const int from = team == 1 ? 0 : wbase;
+        requantise_rows<D>(block + from * D, min(it.slot0 - from, team == 1 ? P : kRowsPerWarp),
+                           s_old / s_new, lane);
+      }
+      if (lane == 0 && sub == 0) a.c.scales[2 * blk + is_v] = s_new;
 #pragma unroll
       for (int p = 0; p < kPasses; ++p) {
-        const int slot = kRowsPerWarp * sub + p * kRpp + r0;
-        if (slot >= lo && slot < hi) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float y[8];
-            if constexpr (kRope) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) y[j] = x[p][8 * c + j];
-            } else {
-              unpack8(w[p][c], y);
-            }
-            uint32_t o[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              o[j] = static_cast<uint32_t>(f32x2_to_e4m3x2(y[4 * j] * inv, y[4 * j + 1] * inv)) |
-                     (static_cast<uint32_t>(f32x2_to_e4m3x2(y[4 * j + 2] * inv,
-                                                            y[4 * j + 3] * inv))
-                      << 16);
-            *reinterpret_cast<uint2 *>(block + slot * D + (c ? ch.c1 : ch.c0) * 8) =
-                make_uint2(o[0], o[1]);
-          }
-        }
+        const int slot = wbase + p * kRpp + r0;
+        float y[16];
+        item(p, y);
+        if (slot >= lo && slot < hi) store_codes(block + slot * D, ch, y, inv);
       }
     }
     if constexpr (kRope) {
-      // q: rows of (token, head), kRpp a warp pass
-      const int total = nrow * a.Hq;
+      const int total = it.nrow * a.Hq;
       for (int base = warp * kRpp; base < total; base += kBcWarps * kRpp) {
-        const int e = base + r0;
+        const int e = base + r0, r = e / a.Hq;
         if (e >= total) continue;
-        const int r = e / a.Hq, h = e % a.Hq;
-        const uint16_t *s = a.q + (row0 + r) * a.q_stride + static_cast<int64_t>(h) * D;
-        uint16_t *d = a.q_out + (row0 + r) * a.q_out_stride + static_cast<int64_t>(h) * D;
+        const int64_t col = static_cast<int64_t>(e - r * a.Hq) * D;
+        const uint16_t *s = a.q + (it.row0 + r) * a.q_stride + col;
         const uint4 w0 = *reinterpret_cast<const uint4 *>(s + ch.c0 * 8);
         const uint4 w1 = *reinterpret_cast<const uint4 *>(s + ch.c1 * 8);
-        float x[16];
-        unpack8(w0, x);
-        unpack8(w1, x + 8);
-        rotate_item(x, tab + r * (rd / 4), i, rd, half, ch);
-        const int lim = half ? (i < rd / 16 ? D / 8 : 0) : rd / 8;
-        *reinterpret_cast<uint4 *>(d + ch.c0 * 8) = ch.c0 < lim ? pack8(x) : w0;
-        *reinterpret_cast<uint4 *>(d + ch.c1 * 8) = ch.c1 < lim ? pack8(x + 8) : w1;
+        float y[16];
+        unpack8(w0, y);
+        unpack8(w1, y + 8);
+        rotate_item(y, tab + r * (rd / 4), i, rd, half, ch);
+        store_rotated(a.q_out + (it.row0 + r) * a.q_out_stride + col, ch, y, w0, w1, i, D, rd, half);
       }
+    }
+  }
+}
+
+// ---- prompts, staged by TMA
+
+constexpr int kRingMaxStages = 6;
+
+// Ring stage: `rows` rows of heads h0 .. h0 + hg - 1 of K (0), V (1) or q (2).
+struct RingStage {
+  PageItem it;
+  int what, h0;
+};
+
+struct RingCtl {
+  RingStage st[kRingMaxStages];
+  uint64_t full[kRingMaxStages], empty[kRingMaxStages];
+  uint64_t sync;  // the consumer warps among themselves
+  RunScan<kBcThreads + 32> scan;
+  float amax[2][kBcWarps];
+  int fail;
+};
+
+// A stage is what eight warps take at once: 16 rows of a head each.
+template <int D>
+struct RingCfg {
+  static constexpr int STAGE = kBcWarps * kRowsPerWarp * D * 2;
+};
+
+// Stages that fit half an SM's shared memory beside the angles.
+inline int ring_stages(int D, size_t angle_bytes) {
+  const size_t stage = static_cast<size_t>(kBcWarps) * kRowsPerWarp * D * 2;
+  const size_t n = (110 * 1024 - angle_bytes) / stage;
+  return static_cast<int>(n < kRingMaxStages ? n : kRingMaxStages);
+}
+
+__device__ __forceinline__ bool ring_wait(RingCtl &ctl, uint64_t *bar, uint32_t parity,
+                                          uint32_t *err_word) {
+  bool ok = false;
+  if (!*reinterpret_cast<volatile int *>(&ctl.fail)) {
+    ok = mbar_wait(bar, parity);
+    if (!ok && atomicExch(&ctl.fail, 1) == 0) report(err_word, KVQ_ERRBIT_TIMEOUT);
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                            uint64_t *bar, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(pol)
+      : "memory");
+}
+
+// A barrier of the consumer warps, bounded like every wait.
+__device__ __forceinline__ bool consumers_sync(RingCtl &ctl, uint32_t &phase, int lane,
+                                               uint32_t *err_word) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&ctl.sync);
+  const bool ok = ring_wait(ctl, &ctl.sync, phase, err_word);
+  phase ^= 1;
+  return ok;
+}
+
+// hg heads of P rows make a stage (hg P = 128).  Dynamic shared memory: the
+// ring of NS stages, then the angles.
+template <int D, bool kRope>
+__global__ void __launch_bounds__(kBcThreads + 32, 2)
+    block_append_ring(const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap,
+                      const __grid_constant__ CUtensorMap qmap, BlockAppendArgs a, int NS) {
+  using C = RingCfg<D>;
+  constexpr int kItems = D / 16, kRpp = 32 / kItems, kPasses = kRowsPerWarp / kRpp;
+  extern __shared__ __align__(128) uint8_t ring[];
+  float4 *tab = reinterpret_cast<float4 *>(ring + NS * C::STAGE);
+  __shared__ RingCtl ctl;
+  __shared__ uint64_t s_freq[kRope ? D / 2 : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int P = a.c.P, H = a.c.H;
+  const int team = P / kRowsPerWarp, hg = kBcWarps / team;
+  const int rd = kRope ? a.rope.rd : D;
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < NS; ++k) {
+      mbar_init(&ctl.full[k], 1);
+      mbar_init(&ctl.empty[k], kBcWarps);
+    }
+    mbar_init(&ctl.sync, kBcWarps);
+    ctl.fail = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  allow_dependents();
+  if constexpr (kRope)
+    if (threadIdx.x < rd / 2) s_freq[threadIdx.x] = turns_per_token(a.rope.inv_freq[threadIdx.x]);
+  PageWalk walk = page_run<kBcThreads + 32, true>(a.rg, P, 1, a.err_word, ctl.scan);  // syncs
+
+  if (warp == kBcWarps) {
+    // ------------------------------------------------------------ producer
+    const uint64_t pol = policy_evict_first();
+    uint32_t g = 0, par = 1;
+    int slot = 0;
+    bool ok = true;
+    PageItem it;
+    while (ok && next_page<true>(a.rg, a.block_table, a.MP, P, a.c.num_pages, 1, walk, it)) {
+      if (it.page < 0) {
+        if (lane == 0) report(a.err_word, KVQ_ERRBIT_PAGE);
+        continue;
+      }
+      for (int what = 0; ok && what < (kRope && a.Hq > 0 ? 3 : 2); ++what) {
+        const int heads = what == 2 ? a.Hq : H;
+        for (int h0 = 0; h0 < heads; h0 += hg) {
+          ok = ring_wait(ctl, &ctl.empty[slot], par, a.err_word);
+          if (!ok) break;
+          if (lane == 0) {
+            ctl.st[slot] = {it, what, h0};
+            mbar_arrive_expect_tx(&ctl.full[slot], C::STAGE);
+            tma_load_3d(ring + slot * C::STAGE, what == 0 ? &kmap : what == 1 ? &vmap : &qmap, 0,
+                        h0, static_cast<int>(it.row0), &ctl.full[slot], pol);
+          }
+          ++g;
+          if (++slot == NS) {
+            slot = 0;
+            par ^= 1;
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (ok) ok = ring_wait(ctl, &ctl.empty[slot], par, a.err_word);
+    if (lane == 0) {
+      if (ok) {  // nothing more
+        ctl.st[slot].what = -1;
+        mbar_arrive(&ctl.full[slot]);
+      } else {
+        // a wait gave up: the copies in flight land before the CTA's shared
+        // memory goes to another one
+        for (uint32_t k = g > NS ? g - NS : 0; k < g; ++k)
+          mbar_wait(&ctl.full[k % NS], (k / NS) & 1);
+      }
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int i = lane % kItems, r0 = lane / kItems;
+  const bool half = !kRope || a.rope.layout == KVQ_ROPE_HALF;
+  const ItemChunks ch = item_chunks(i, D, rd, half);
+  const int sub = warp % team, hw = warp / team;  // rows 16 sub .. of head hw of the stage
+  const int rbase = kRowsPerWarp * sub + r0;
+  uint32_t par = 0, phase = 0, round = 0;
+  int slot = 0;
+  while (true) {
+    if (!ring_wait(ctl, &ctl.full[slot], par, a.err_word)) return;
+    const RingStage st = ctl.st[slot];
+    if (st.what < 0) return;
+    const PageItem &it = st.it;
+    if (kRope && st.what == 0 && st.h0 == 0) {  // a page begins
+      if (!consumers_sync(ctl, phase, lane, a.err_word)) return;  // the last one's angles are read
+      fill_angles(tab, s_freq, it.first, it.nrow, rd, half, a.rope.mscale, threadIdx.x, kBcThreads);
+      if (!consumers_sync(ctl, phase, lane, a.err_word)) return;
+    }
+    const int h = st.h0 + hw;
+    const bool live = h < (st.what == 2 ? a.Hq : H);
+    uint4 w[kPasses][2];
+    const uint8_t *src = ring + slot * C::STAGE;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const uint8_t *s = src + ((rbase + p * kRpp) * hg + hw) * (2 * D);
+      w[p][0] = *reinterpret_cast<const uint4 *>(s + ch.c0 * 16);
+      w[p][1] = *reinterpret_cast<const uint4 *>(s + ch.c1 * 16);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl.empty[slot]);
+    if (++slot == NS) {
+      slot = 0;
+      par ^= 1;
+    }
+    auto item = [&](int p, float (&y)[16]) {
+      const int r = rbase + p * kRpp;
+      unpack8(w[p][0], y);
+      unpack8(w[p][1], y + 8);
+      if constexpr (kRope)
+        if (st.what != 1 && r < it.nrow) rotate_item(y, tab + r * (rd / 4), i, rd, half, ch);
+    };
+    if (kRope && st.what == 2) {
+      if (!live) continue;
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int r = rbase + p * kRpp;
+        float y[16];
+        item(p, y);
+        if (r < it.nrow)
+          store_rotated(a.q_out + (it.row0 + r) * a.q_out_stride + static_cast<int64_t>(h) * D, ch,
+                        y, w[p][0], w[p][1], i, D, rd, half);
+      }
+      continue;
+    }
+    const bool is_v = st.what == 1;
+    const int64_t blk = static_cast<int64_t>(it.page) * H + h;
+    const float s_old = live && it.slot0 > 0 ? a.c.scales[2 * blk + is_v] : 0.f;
+    float amax = 0.f;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      float y[16];
+      item(p, y);
+      if (rbase + p * kRpp < it.nrow) amax = fmaxf(amax, item_amax(y));
+    }
+    amax = warp_max(amax);
+    if (team > 1) {  // uniform over the grid
+      float *m = ctl.amax[round & 1];
+      ++round;
+      if (lane == 0) m[warp] = amax;
+      if (!consumers_sync(ctl, phase, lane, a.err_word)) return;
+      const int t0 = warp - sub;
+      amax = fmaxf(m[t0], m[t0 + 1]);
+      if (team == 4) amax = fmaxf(amax, fmaxf(m[t0 + 2], m[t0 + 3]));
+    }
+    if (!live) continue;
+    const float s_new = fmaxf(pow2(block_exponent(amax)), s_old);
+    const float inv = 1.0f / s_new;
+    uint8_t *block = (is_v ? a.c.v : a.c.k) + blk * P * D;
+    if (sub == 0) {
+      if (s_new > s_old && it.slot0 > 0) requantise_rows<D>(block, it.slot0, s_old / s_new, lane);
+      if (lane == 0) a.c.scales[2 * blk + is_v] = s_new;
+    }
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const int r = rbase + p * kRpp;
+      float y[16];
+      item(p, y);
+      if (r < it.nrow) store_codes(block + (it.slot0 + r) * D, ch, y, inv);
     }
   }
 }
@@ -272,38 +666,18 @@ __global__ void __launch_bounds__(kBcThreads) block_read_kernel(BlockReadArgs a)
   const int i = lane % kLanes, r0 = lane / kLanes;
   grid_dependency_wait();
   allow_dependents();
-  const RunStart run = find_run<kBcThreads>(
-      a.rg.B, gridDim.x, blockIdx.x, scan, [&](int b) -> int64_t {
-        const Rows r = request_rows<false>(a.rg, b);
-        if (r.err && blockIdx.x == 0) report(a.err_word, r.err);
-        return pages_touched(r, P);
-      });
-  int64_t left = min(run.per, run.total - blockIdx.x * run.per);
-  int b = run.b;
-  int64_t in = run.in;
-  while (left > 0) {
-    const Rows rq = request_rows<false>(a.rg, b);
-    const int64_t have = pages_touched(rq, P);
-    if (in >= have) {
-      ++b;
-      in = 0;
-      continue;
-    }
-    const int lp = rq.p0 / P + static_cast<int>(in);
-    ++in;
-    --left;
-    const int first = max(rq.p0, lp * P), last = min(rq.p0 + rq.n, lp * P + P);
-    const int slot0 = first - lp * P, nrow = last - first;
-    const int64_t row0 = rq.row + (first - rq.p0);
-    const int page = __ldg(a.block_table + static_cast<int64_t>(b) * a.MP + lp);
-    if (page < 0 || page >= a.c.num_pages) {
+  PageWalk walk = page_run<kBcThreads, false>(a.rg, P, 1, a.err_word, scan);
+  PageItem it;
+  while (next_page<false>(a.rg, a.block_table, a.MP, P, a.c.num_pages, 1, walk, it)) {
+    if (it.page < 0) {
       if (threadIdx.x == 0) report(a.err_word, KVQ_ERRBIT_PAGE);
       continue;
     }
+    const int slot0 = it.slot0, nrow = it.nrow;
     const int team = P / kRowsPerWarp;
     for (int u = warp; u < 2 * H * team; u += kBcWarps) {
       const int sub = u % team, h = (u / team) >> 1, is_v = (u / team) & 1;
-      const int64_t blk = static_cast<int64_t>(page) * H + h;
+      const int64_t blk = static_cast<int64_t>(it.page) * H + h;
       const uint8_t *src = (is_v ? a.c.v : a.c.k) + blk * P * D;
       uint2 w[kPasses];
 #pragma unroll
@@ -325,7 +699,7 @@ __global__ void __launch_bounds__(kBcThreads) block_read_kernel(BlockReadArgs a)
           e4m3x4_to_f32(w[p].y, x + 4);
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] *= s;
-          *reinterpret_cast<uint4 *>(dst + (row0 + slot - slot0) * stride) = pack8(x);
+          *reinterpret_cast<uint4 *>(dst + (it.row0 + slot - slot0) * stride) = pack8(x);
         }
       }
     }
@@ -339,13 +713,50 @@ BlockPool block_pool(const kvq_block_cache *c) {
           c->num_pages, c->page_size, c->num_kv_heads};
 }
 
-// CTAs for a step of n_tokens rows: it touches at most one page a row, and at
-// most n_tokens / P + 2 B pages; `per_sm` CTAs an SM at most.
-int block_ctas(int64_t n_tokens, int64_t B, int P, int per_sm, int sms) {
-  int64_t n = n_tokens / P + 2 * B;
-  n = n < n_tokens ? n : n_tokens;
+// Pages that a step of n_tokens rows touches, at most: one a row, and
+// n_tokens / P + 2 a request.
+int64_t max_pages(int64_t n_tokens, int64_t B, int P) {
+  const int64_t n = n_tokens / P + 2 * B;
+  return n < n_tokens ? n : n_tokens;
+}
+
+int block_ctas(int64_t items, int per_sm, int sms) {
   const int64_t most = static_cast<int64_t>(per_sm) * sms;
-  return static_cast<int>(n < most ? n : most);
+  return static_cast<int>(items < most ? items : most);
+}
+
+// Rows a request, on average, up to which a step takes the short kernel.
+constexpr int kShortRows = 16;
+
+// [tokens][heads][D] bf16, strided by token; a box is P rows of hg heads.
+bool rows_map(CUtensorMap *map, const void *p, int64_t stride, int64_t tokens, int heads, int D,
+              int hg, int P) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(hg),
+                             static_cast<cuuint32_t>(P)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+using RingFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, BlockAppendArgs, int);
+
+// Opt a ring kernel into its shared memory, once per device.
+bool ring_opt_in(RingFn fn, int variant) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<bool> done[kMaxDev][4];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return false;
+  if (done[dev][variant].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024) != cudaSuccess)
+    return false;
+  done[dev][variant].store(true, std::memory_order_release);
+  return true;
 }
 
 kvq_status append_impl(const kvq_block_cache *cache, const kvq_rope_desc *rope, const void *q,
@@ -386,13 +797,34 @@ kvq_status append_impl(const kvq_block_cache *cache, const kvq_rope_desc *rope, 
                 : RopeArgs{nullptr, D, KVQ_ROPE_HALF, 1.f};
   int sms = 0;
   if (device_sm_count(&sms) != KVQ_OK) return KVQ_ERR_CUDA;
-  const int ctas = block_ctas(n_tokens, B, cache->page_size, 2, sms);
-  // at most 64 rows x 32 words = 32 KB of angles
-  const size_t smem = rope ? static_cast<size_t>(cache->page_size) * rope->rotary_dim * 4 : 0;
-  const auto fn = D == 128 ? (rope ? block_append_kernel<128, true> : block_append_kernel<128, false>)
-                           : (rope ? block_append_kernel<64, true> : block_append_kernel<64, false>);
-  const cudaError_t e = launch_dependent(fn, ctas, kBcThreads, smem,
-                                         reinterpret_cast<cudaStream_t>(stream), a);
+  const int P = cache->page_size, H = cache->num_kv_heads;
+  const size_t angles = rope ? static_cast<size_t>(P) * rope->rotary_dim * 4 : 0;
+  const int64_t pages = max_pages(n_tokens, B, P);
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  const int shares = rope && Hq > 0 ? 3 : 2;
+  if (n_tokens <= kShortRows * static_cast<int64_t>(B) || pages * shares <= 4 * sms) {
+    const auto fn = D == 128 ? (rope ? block_append_short<128, true> : block_append_short<128, false>)
+                             : (rope ? block_append_short<64, true> : block_append_short<64, false>);
+    e = launch_dependent(fn, block_ctas(pages * shares, 4, sms), kBcThreads, angles, cs, a, shares);
+  } else if (H * P >= kBcWarps * kRowsPerWarp) {
+    const auto fn = D == 128 ? (rope ? block_append_ring<128, true> : block_append_ring<128, false>)
+                             : (rope ? block_append_ring<64, true> : block_append_ring<64, false>);
+    const int ns = ring_stages(D, angles), hg = kBcWarps * kRowsPerWarp / P;
+    const size_t smem = static_cast<size_t>(ns) * kBcWarps * kRowsPerWarp * D * 2 + angles;
+    if (!ring_opt_in(fn, (D == 128 ? 2 : 0) + (rope ? 1 : 0))) return KVQ_ERR_CUDA;
+    CUtensorMap km, vm, qm;
+    if (!rows_map(&km, k_new, k_stride, n_tokens, H, D, hg, P) ||
+        !rows_map(&vm, v_new, v_stride, n_tokens, H, D, hg, P))
+      return KVQ_ERR_CUDA;
+    qm = km;
+    if (Hq > 0 && !rows_map(&qm, q, q_stride, n_tokens, Hq, D, hg, P)) return KVQ_ERR_CUDA;
+    e = launch_dependent(fn, block_ctas(pages, 2, sms), kBcThreads + 32, smem, cs, km, vm, qm, a, ns);
+  } else {
+    const auto fn = D == 128 ? (rope ? block_append_wide<128, true> : block_append_wide<128, false>)
+                             : (rope ? block_append_wide<64, true> : block_append_wide<64, false>);
+    e = launch_dependent(fn, block_ctas(pages, rope ? 2 : 3, sms), kBcThreads, angles, cs, a);
+  }
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
@@ -453,7 +885,7 @@ extern "C" kvq_status kvq_block_read(const kvq_block_cache *cache, const int32_t
   a.MP = MP;
   int sms = 0;
   if (device_sm_count(&sms) != KVQ_OK) return KVQ_ERR_CUDA;
-  const int ctas = block_ctas(n_tokens, B, cache->page_size, 8, sms);
+  const int ctas = block_ctas(max_pages(n_tokens, B, cache->page_size), 8, sms);
   const cudaError_t e =
       launch_dependent(D == 128 ? block_read_kernel<128> : block_read_kernel<64>, ctas, kBcThreads,
                        0, reinterpret_cast<cudaStream_t>(stream), a);

@@ -252,6 +252,55 @@ def test_append_many_requests_and_long_prompt(kvq):
     assert_cache(c, pools, scales)
 
 
+# Prompts large enough for the staged kernel (heads times page size of 128 and
+# more) and for the one without staging: ragged, starting in the middle of pages,
+# with odd head counts, the last page of a prompt short.
+PROMPTS = [(8, 16, 128), (9, 16, 64), (2, 64, 128), (5, 32, 128), (3, 64, 64),  # staged
+           (1, 16, 128), (3, 32, 64), (1, 64, 128)]
+
+
+def prompts(rng, H, P, D, pad=5):
+    n = np.array([130 * P, 1, 9 * P + 3, 0, 200 * P + 7, P, 3])
+    return R.Step(rng, n, n + np.array([0, 5, 11, 3, 2 * P + 1, 0, P - 1]), H, P, D, pad=pad)
+
+
+@pytest.mark.parametrize("H,P,D", PROMPTS)
+def test_append_prompts(kvq, H, P, D):
+    rng = np.random.default_rng([H, P, D, 5])
+    s = prompts(rng, H, P, D)
+    (kt, kx), (vt, vx) = R.values(rng, s.N, H, D), R.values(rng, s.N, H, D)
+    pools, scales = [s.k.copy(), s.v.copy()], s.scales.copy()
+    R.append(pools, scales, [kx, vx], s.tok_start, s.lens, s.table)
+    c, err = run_append(kvq, s, (kt, vt), strided=True)
+    assert err == 0
+    assert_cache(c, pools, scales)
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("H,P,D,rd", [(8, 16, 128, 128), (3, 64, 64, 32), (4, 32, 128, 96),
+                                      (2, 64, 128, 128), (1, 16, 128, 64)])
+def test_rope_append_prompts(kvq, half, H, P, D, rd):
+    rng = np.random.default_rng([H, P, D, rd])
+    check_rope_append(kvq, prompts(rng, H, P, D), rng, 2 * H + 1 if H == 3 else 2 * H, rd, half)
+
+
+def test_append_prompts_bad_pages_and_requests(kvq):
+    """Bad entries in a prompt's table and a bad request among prompts: the others'
+    pages are written all the same."""
+    H, P, D = 8, 16, 64
+    rng = np.random.default_rng(21)
+    s = prompts(rng, H, P, D)
+    (kt, kx), (vt, vx) = R.values(rng, s.N, H, D), R.values(rng, s.N, H, D)
+    table, lens = s.table.copy(), s.lens.copy()
+    table[0, 5], table[4, 100] = s.NP, -3
+    lens[2] = 1
+    pools, scales = [s.k.copy(), s.v.copy()], s.scales.copy()
+    R.append(pools, scales, [kx, vx], s.tok_start, lens, table)
+    c, err = run_append(kvq, s, (kt, vt), lens=lens, table=table)
+    assert err == kvq.ERRBIT_SEQLEN | kvq.ERRBIT_PAGE
+    assert_cache(c, pools, scales)
+
+
 @pytest.mark.parametrize("half", [True, False])
 @pytest.mark.parametrize("H,G,P,D,rd", [(2, 4, 16, 128, 128), (8, 4, 16, 128, 64), (3, 1, 64, 128, 96),
                                         (1, 8, 32, 64, 64), (5, 2, 64, 64, 16)])
@@ -259,9 +308,13 @@ def test_rope_append(kvq, half, H, G, P, D, rd):
     """K rotated and rounded once, q beside it; V bit for bit."""
     rng = np.random.default_rng([H, G, P, rd])
     n, before = [1, 40, 0, 3, 1], [0, 10, 5, 30, 2000]
-    s = R.Step(rng, n, np.add(n, before), H, P, D, pad=2)
+    check_rope_append(kvq, R.Step(rng, n, np.add(n, before), H, P, D, pad=2), rng, G * H, rd, half)
+
+
+def check_rope_append(kvq, s, rng, Hq, rd, half):
+    H, D = s.H, s.D
     (kt, kx), (vt, vx) = R.values(rng, s.N, H, D), R.values(rng, s.N, H, D)
-    q, qx = R.values(rng, s.N, H * G, D)
+    q, qx = R.values(rng, s.N, Hq, D)
     f, m = inv_freq(rd, 500000.0), 1.1
     rope = kvq.Rope(dev(f), kvq.ROPE_HALF if half else kvq.ROPE_INTERLEAVED, m)
     c = cache_of(kvq, s)
@@ -271,7 +324,7 @@ def test_rope_append(kvq, half, H, G, P, D, rd):
                               dev(s.lens), dev(s.table), err_word=err)
     assert int(err.item()) == 0
     rows = int(s.tok_start[-1])
-    pos = np.concatenate([np.arange(b, b + k) for k, b in zip(n, before)])
+    pos = np.concatenate([np.arange(L - k, L) for k, L in zip(s.n, s.lens)])
     check_rotation(qo[:rows], qx[:rows], pos, f, half, m)
     assert (qo[rows:] == 7.0).all()
     kr = np.concatenate([R.rotate(kx[:rows], pos, f, half, m), kx[rows:]])
@@ -280,13 +333,19 @@ def test_rope_append(kvq, half, H, G, P, D, rd):
     got_k, got_s = c.k_pool.cpu().numpy(), c.scales.cpu().numpy()
     assert np.array_equal(c.v_pool.cpu().numpy(), pools[1])
     assert np.array_equal(got_s, scales)  # no amax of these inputs lies at a border
-    # half a step of e4m3 (2^-4 of the value, 2^-10 scales below 2^-6 scales) and the rotation
-    step = np.where(scales[:, :, 0] > 0, scales[:, :, 0], 0)[:, :, None, None].astype(np.float64)
-    a, b = R.decode(got_k) * step, R.decode(pools[0]) * step
+    # codes differ only where the rotation's error moves a value over a rounding
+    # border, and then by one step of e4m3 (2^-3 of the value, 2^-9 scales below
+    # 2^-6 scales)
+    step = scales[:, :, 0][:, :, None, None].astype(np.float64)
     diff = got_k != pools[0]
-    # codes differ only where the rotation's error moves a value over a rounding border
+    a, b = R.decode(got_k) * step, R.decode(pools[0]) * step
     assert diff.mean() < 1e-4
-    assert (np.abs(a - b)[diff] <= 2 * (2.0 ** -4 * np.abs(b) + 2.0 ** -10 * step + 0 * a)[diff]).all()
+    assert (np.abs(a - b)[diff] <= (2.0 ** -3 * np.abs(b) + 2.0 ** -9 * step)[diff]).all()
+    # in place: the same q
+    q2 = q.cuda()
+    kvq.kvq_rope_block_append(c, rope, q2, q2, kt.cuda(), vt.cuda(), dev(s.tok_start), dev(s.lens),
+                              dev(s.table), err_word=err)
+    assert torch.equal(q2[:rows], qo[:rows]) and np.array_equal(c.k_pool.cpu().numpy(), got_k)
 
 
 # ---------------------------------------------------------------------------
