@@ -22,6 +22,7 @@
 // shared memory.  The page's angles are computed once into shared memory and
 // used by all heads.
 #include <atomic>
+#include <type_traits>
 
 #include "block_common.cuh"
 
@@ -137,20 +138,25 @@ __device__ __forceinline__ void fill_angles(float4 *tab, const uint64_t *freq, i
   }
 }
 
+// 8 values -> their codes.
+__device__ __forceinline__ uint2 codes8(const float *v, float inv) {
+  const float2 s = make_float2(inv, inv);
+  uint32_t o[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float2 x = __fmul2_rn(make_float2(v[4 * j], v[4 * j + 1]), s);
+    const float2 y = __fmul2_rn(make_float2(v[4 * j + 2], v[4 * j + 3]), s);
+    o[j] = static_cast<uint32_t>(f32x2_to_e4m3x2(x.x, x.y)) |
+           (static_cast<uint32_t>(f32x2_to_e4m3x2(y.x, y.y)) << 16);
+  }
+  return make_uint2(o[0], o[1]);
+}
+
 // 16 values (an item) -> codes at the two chunks of a row.
 __device__ __forceinline__ void store_codes(uint8_t *row, ItemChunks ch, const float (&y)[16],
                                             float inv) {
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    uint32_t o[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float *v = y + 8 * c + 4 * j;
-      o[j] = static_cast<uint32_t>(f32x2_to_e4m3x2(v[0] * inv, v[1] * inv)) |
-             (static_cast<uint32_t>(f32x2_to_e4m3x2(v[2] * inv, v[3] * inv)) << 16);
-    }
-    *reinterpret_cast<uint2 *>(row + (c ? ch.c1 : ch.c0) * 8) = make_uint2(o[0], o[1]);
-  }
+  *reinterpret_cast<uint2 *>(row + ch.c0 * 8) = codes8(y, inv);
+  *reinterpret_cast<uint2 *>(row + ch.c1 * 8) = codes8(y + 8, inv);
 }
 
 // A rotated item -> bf16 at the two chunks; a chunk past rotary_dim as it came.
@@ -161,27 +167,55 @@ __device__ __forceinline__ void store_rotated(uint16_t *row, ItemChunks ch, cons
   *reinterpret_cast<uint4 *>(row + ch.c1 * 8) = ch.c1 < lim ? pack8(y + 8) : w1;
 }
 
-__device__ __forceinline__ float item_amax(const float (&y)[16]) {
-  float m = 0.f;
+// Largest magnitudes, as the bits of a float (their order is the magnitudes'),
+// inf and NaN included: kept as they come, since one instruction a value is
+// what there is time for.  Only when the maximum turns out not finite is it
+// taken again over the finite values (kFinite).
+template <bool kFinite>
+__device__ __forceinline__ uint32_t item_max(const float (&y)[16]) {
+  uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) m = fmaxf(m, finite_abs(y[j]));
+  for (int j = 0; j < 16; ++j) {
+    const uint32_t u = __float_as_uint(y[j]) & 0x7FFFFFFFu;
+    m = max(m, kFinite && u >= 0x7F800000u ? 0u : u);
+  }
   return m;
 }
 
-__device__ __forceinline__ float warp_max(float m) {
+template <bool kFinite>
+__device__ __forceinline__ uint32_t words_max(uint4 a, uint4 b) {  // 16 bf16
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t m = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
+  for (int j = 0; j < 8; ++j) {
+    uint32_t u = w[j] & 0x7FFF7FFFu;
+    if (kFinite) u &= ~__vcmpgeu2(u, 0x7F807F80u);
+    m = __vmaxu2(m, u);
+  }
+  return max(m & 0xFFFF0000u, m << 16);
+}
+
+// The block's amax from a function that gives a lane's maximum, whole warp.
+template <typename F>
+__device__ __forceinline__ float warp_amax(F lane_max) {
+  uint32_t m = __reduce_max_sync(0xffffffffu, lane_max(std::false_type()));
+  if (m >= 0x7F800000u) m = __reduce_max_sync(0xffffffffu, lane_max(std::true_type()));
+  return __uint_as_float(m);
 }
 
 // ---- short steps
 
+// blockIdx.x: request and share of its pages (0: K, 1: V, 2 ..: qheads heads of
+// q each); blockIdx.y: its page, counting from the first that the step
+// touches, and every gridDim.y-th one after it.  No scan over the requests: the
+// time of a decode step is a chain of loads (starts and length; table entry
+// beside the rows; old scale), and this is the shortest one.
 template <int D, bool kRope>
-__global__ void __launch_bounds__(kBcThreads, 4) block_append_short(BlockAppendArgs a, int parts) {
+__global__ void __launch_bounds__(kBcThreads, 4) block_append_short(BlockAppendArgs a, int shares,
+                                                                    int qheads) {
   constexpr int kItems = D / 16;      // lanes a row (two 8-dim chunks each)
   constexpr int kRpp = 32 / kItems;   // rows a warp pass
   extern __shared__ float4 tab[];     // kRope: [P][rd / 4] angles of the page's rows
-  __shared__ RunScan<kBcThreads> scan;
   __shared__ uint64_t s_freq[kRope ? D / 2 : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int P = a.c.P, H = a.c.H;
@@ -189,93 +223,104 @@ __global__ void __launch_bounds__(kBcThreads, 4) block_append_short(BlockAppendA
   const bool half = !kRope || a.rope.layout == KVQ_ROPE_HALF;
   const int rd = kRope ? a.rope.rd : D;
   const ItemChunks ch = item_chunks(i, D, rd, half);
+  const int b = blockIdx.x / shares, share = blockIdx.x - b * shares;
+  const bool is_v = share == 1, is_q = share > 1;
+  const int h0 = is_q ? (share - 2) * qheads : 0;
+  const int heads = is_q ? min(qheads, a.Hq - h0) : H;
+  const uint16_t *src = is_q ? a.q + static_cast<int64_t>(h0) * D : is_v ? a.v_new : a.k_new;
+  const int64_t stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
   grid_dependency_wait();
   allow_dependents();
-  double freq = 0.0;  // in flight while the requests are scanned (rd / 2 <= blockDim)
+  double freq = 0.0;
   if constexpr (kRope)
-    if (threadIdx.x < rd / 2) freq = a.rope.inv_freq[threadIdx.x];
-  PageWalk walk = page_run<kBcThreads, true>(a.rg, P, parts, a.err_word, scan);
+    if (!is_v && threadIdx.x < rd / 2) freq = a.rope.inv_freq[threadIdx.x];  // rd / 2 <= blockDim
+  const Rows rq = request_rows<true>(a.rg, b);
+  if (rq.err && blockIdx.y == 0 && share == 0 && threadIdx.x == 0) report(a.err_word, rq.err);
+  const int pages = static_cast<int>(pages_touched(rq, P));
+  if (static_cast<int>(blockIdx.y) >= pages) return;
   if constexpr (kRope)
-    if (threadIdx.x < rd / 2) s_freq[threadIdx.x] = turns_per_token(freq);
-  PageItem it;
-  while (next_page<true>(a.rg, a.block_table, a.MP, P, a.c.num_pages, parts, walk, it)) {
-    const bool is_v = it.part == 1;
+    if (!is_v && threadIdx.x < rd / 2) s_freq[threadIdx.x] = turns_per_token(freq);
+  for (int pg = blockIdx.y; pg < pages; pg += gridDim.y) {
+    const int lp = rq.p0 / P + pg;
+    const int page = __ldg(a.block_table + static_cast<int64_t>(b) * a.MP + lp);
+    const int first = max(rq.p0, lp * P), slot0 = first - lp * P;
+    const int nrow = min(rq.p0 + rq.n, lp * P + P) - first;
+    const int64_t row0 = static_cast<int64_t>(rq.row) + (first - rq.p0);
+    auto load = [&](int r, int h, uint4 (&w)[2]) {
+      w[0] = w[1] = make_uint4(0, 0, 0, 0);
+      if (r < nrow && h < heads) {
+        const uint16_t *s = src + (row0 + r) * stride + static_cast<int64_t>(h) * D;
+        w[0] = *reinterpret_cast<const uint4 *>(s + ch.c0 * 8);
+        w[1] = *reinterpret_cast<const uint4 *>(s + ch.c1 * 8);
+      }
+    };
+    // this warp's first rows, before anything that waits: head `warp` (K, V),
+    // or the (token, head) rows from `e` on (q)
+    int e = warp * kRpp + r0;
+    uint4 w[2];
+    load(is_q ? e / heads : r0, is_q ? e % heads : warp, w);
     if (kRope && !is_v) {  // uniform over the CTA
-      __syncthreads();  // the previous item's angles are no longer read (and s_freq is set)
-      fill_angles(tab, s_freq, it.first, it.nrow, rd, half, a.rope.mscale, threadIdx.x, kBcThreads);
+      __syncthreads();  // the previous page's angles are no longer read (and s_freq is set)
+      fill_angles(tab, s_freq, first, nrow, rd, half, a.rope.mscale, threadIdx.x, kBcThreads);
       __syncthreads();
     }
-    auto rotate = [&](float (&y)[16], int r) {
+    if (page < 0 || page >= a.c.num_pages) {
+      if (threadIdx.x == 0) report(a.err_word, KVQ_ERRBIT_PAGE);
+      continue;
+    }
+    auto values = [&](const uint4 (&w)[2], int r, float (&y)[16]) {
+      unpack8(w[0], y);
+      unpack8(w[1], y + 8);
       if constexpr (kRope)
-        if (!is_v && r < it.nrow) rotate_item(y, tab + r * (rd / 4), i, rd, half, ch);
+        if (!is_v && r < nrow) rotate_item(y, tab + r * (rd / 4), i, rd, half, ch);
     };
-    if (it.part == 2) {  // q: rows of (token, head)
-      if (it.page < 0) continue;
-      const int total = it.nrow * a.Hq;
-      for (int base = warp * kRpp; base < total; base += 2 * kBcWarps * kRpp) {
-        uint4 w[2][2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int e = base + j * kBcWarps * kRpp + r0, r = e / a.Hq;
-          if (e < total) {
-            const uint16_t *s = a.q + (it.row0 + r) * a.q_stride + static_cast<int64_t>(e - r * a.Hq) * D;
-            w[j][0] = *reinterpret_cast<const uint4 *>(s + ch.c0 * 8);
-            w[j][1] = *reinterpret_cast<const uint4 *>(s + ch.c1 * 8);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int e = base + j * kBcWarps * kRpp + r0, r = e / a.Hq;
-          if (e < total) {
-            float y[16];
-            unpack8(w[j][0], y);
-            unpack8(w[j][1], y + 8);
-            rotate(y, r);
-            store_rotated(a.q_out + (it.row0 + r) * a.q_out_stride + static_cast<int64_t>(e - r * a.Hq) * D,
-                          ch, y, w[j][0], w[j][1], i, D, rd, half);
-          }
-        }
+    if (is_q) {
+      const int total = nrow * heads;
+      while (e - r0 < total) {
+        const int r = e / heads, h = e - r * heads;
+        const int e2 = e + kBcWarps * kRpp;
+        uint4 w2[2];
+        load(e2 / heads, e2 % heads, w2);  // the next rows, in flight meanwhile
+        float y[16];
+        values(w, r, y);
+        if (r < nrow)
+          store_rotated(a.q_out + (row0 + r) * a.q_out_stride + static_cast<int64_t>(h0 + h) * D,
+                        ch, y, w[0], w[1], i, D, rd, half);
+        w[0] = w2[0];
+        w[1] = w2[1];
+        e = e2;
       }
       continue;
     }
     for (int h = warp; h < H; h += kBcWarps) {
-      const uint16_t *src = (is_v ? a.v_new : a.k_new) + static_cast<int64_t>(h) * D;
-      const int64_t stride = is_v ? a.v_stride : a.k_stride;
-      auto load = [&](int r, float (&y)[16]) {
-        uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-        if (r < it.nrow) {
-          const uint16_t *s = src + (it.row0 + r) * stride;
-          w0 = __ldg(reinterpret_cast<const uint4 *>(s + ch.c0 * 8));
-          w1 = __ldg(reinterpret_cast<const uint4 *>(s + ch.c1 * 8));
-        }
-        unpack8(w0, y);
-        unpack8(w1, y + 8);
-        rotate(y, r);
-      };
-      float y[16];
-      load(r0, y);  // its addresses do not need the page
-      if (it.page < 0) {
-        if (lane == 0) report(a.err_word, KVQ_ERRBIT_PAGE);
-        break;
-      }
-      const int64_t blk = static_cast<int64_t>(it.page) * H + h;
+      if (h != warp) load(r0, h, w);
+      const int64_t blk = static_cast<int64_t>(page) * H + h;
       float *scale = a.c.scales + 2 * blk + is_v;
-      const float s_old = it.slot0 > 0 ? *scale : 0.f;
-      float amax = item_amax(y);
-      for (int r = kRpp + r0; r - r0 < it.nrow; r += kRpp) {
-        load(r, y);
-        amax = fmaxf(amax, item_amax(y));
-      }
-      amax = warp_max(amax);
+      const float s_old = slot0 > 0 ? *scale : 0.f;
+      float y[16];
+      values(w, r0, y);
+      const float amax = warp_amax([&](auto finite) {
+        uint32_t m = item_max<decltype(finite)::value>(y);
+        for (int r = kRpp + r0; r - r0 < nrow; r += kRpp) {
+          uint4 v[2];
+          float z[16];
+          load(r, h, v);
+          values(v, r, z);
+          m = max(m, item_max<decltype(finite)::value>(z));
+        }
+        return m;
+      });
       const float s_new = fmaxf(pow2(block_exponent(amax)), s_old);
       const float inv = 1.0f / s_new;  // exact: a power of two
       uint8_t *block = (is_v ? a.c.v : a.c.k) + blk * P * D;
-      if (s_new > s_old && it.slot0 > 0)
-        requantise_rows<D>(block, it.slot0, s_old / s_new, lane);
+      if (s_new > s_old && slot0 > 0) requantise_rows<D>(block, slot0, s_old / s_new, lane);
       if (lane == 0) *scale = s_new;
-      for (int r = r0; r - r0 < it.nrow; r += kRpp) {
-        if (it.nrow > kRpp) load(r, y);
-        if (r < it.nrow) store_codes(block + (it.slot0 + r) * D, ch, y, inv);
+      for (int r = r0; r - r0 < nrow; r += kRpp) {
+        if (r != r0) {
+          load(r, h, w);
+          values(w, r, y);
+        }
+        if (r < nrow) store_codes(block + (slot0 + r) * D, ch, y, inv);
       }
     }
   }
@@ -350,15 +395,21 @@ __global__ void __launch_bounds__(kBcThreads, kRope ? 2 : 3) block_append_wide(B
             rotate_item(y, tab + (slot - it.slot0) * (rd / 4), i, rd, half, ch);
       };
       float amax = 0.f;
-      if (live) {
+      if (live)
+        amax = warp_amax([&](auto finite) {
+          uint32_t m = 0;
 #pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-          float y[16];
-          item(p, y);
-          amax = fmaxf(amax, item_amax(y));
-        }
-        amax = warp_max(amax);
-      }
+          for (int p = 0; p < kPasses; ++p) {
+            if (kRope && !is_v) {
+              float y[16];
+              item(p, y);
+              m = max(m, item_max<decltype(finite)::value>(y));
+            } else {
+              m = max(m, words_max<decltype(finite)::value>(w[p][0], w[p][1]));
+            }
+          }
+          return m;
+        });
       if (team > 1) {  // uniform over the CTA
         float *m = s_amax[round & 1];
         if (lane == 0) m[warp] = amax;
@@ -602,14 +653,21 @@ __global__ void __launch_bounds__(kBcThreads + 32, 2)
     const bool is_v = st.what == 1;
     const int64_t blk = static_cast<int64_t>(it.page) * H + h;
     const float s_old = live && it.slot0 > 0 ? a.c.scales[2 * blk + is_v] : 0.f;
-    float amax = 0.f;
+    float amax = warp_amax([&](auto finite) {
+      uint32_t m = 0;
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      float y[16];
-      item(p, y);
-      if (rbase + p * kRpp < it.nrow) amax = fmaxf(amax, item_amax(y));
-    }
-    amax = warp_max(amax);
+      for (int p = 0; p < kPasses; ++p) {
+        if (rbase + p * kRpp >= it.nrow) continue;  // rows of others
+        if (kRope && !is_v) {
+          float y[16];
+          item(p, y);
+          m = max(m, item_max<decltype(finite)::value>(y));
+        } else {
+          m = max(m, words_max<decltype(finite)::value>(w[p][0], w[p][1]));
+        }
+      }
+      return m;
+    });
     if (team > 1) {  // uniform over the grid
       float *m = ctl.amax[round & 1];
       ++round;
@@ -802,11 +860,23 @@ kvq_status append_impl(const kvq_block_cache *cache, const kvq_rope_desc *rope, 
   const int64_t pages = max_pages(n_tokens, B, P);
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  const int shares = rope && Hq > 0 ? 3 : 2;
-  if (n_tokens <= kShortRows * static_cast<int64_t>(B) || pages * shares <= 4 * sms) {
+  if (n_tokens <= kShortRows * static_cast<int64_t>(B) || pages <= 2 * sms) {
     const auto fn = D == 128 ? (rope ? block_append_short<128, true> : block_append_short<128, false>)
                              : (rope ? block_append_short<64, true> : block_append_short<64, false>);
-    e = launch_dependent(fn, block_ctas(pages * shares, 4, sms), kBcThreads, angles, cs, a, shares);
+    // q's heads in one share for a row a request, in shares of twice K's rows for
+    // more (256 drafts of 1-8 rows, 32 heads over 8: 9.7 us; shares of 8 and of
+    // all heads 11.3 and 10.5)
+    const int qheads = n_tokens <= 2 * static_cast<int64_t>(B) ? Hq : 2 * H;
+    const int shares = rope && Hq > 0 ? 2 + (Hq + qheads - 1) / qheads : 2;
+    if (static_cast<int64_t>(B) * shares > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
+    // pages a request that get CTAs of their own: what an average one fills,
+    // up to 16 CTAs an SM in all
+    const int64_t avg = (n_tokens + B - 1) / B;
+    int64_t gy = (avg + P - 1) / P;
+    const int64_t most = 16LL * sms / (static_cast<int64_t>(B) * shares) + 1;
+    gy = gy < most ? gy : most;
+    e = launch_dependent(fn, dim3(B * shares, static_cast<unsigned>(gy)), kBcThreads, angles, cs, a,
+                         shares, qheads);
   } else if (H * P >= kBcWarps * kRowsPerWarp) {
     const auto fn = D == 128 ? (rope ? block_append_ring<128, true> : block_append_ring<128, false>)
                              : (rope ? block_append_ring<64, true> : block_append_ring<64, false>);

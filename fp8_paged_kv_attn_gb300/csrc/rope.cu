@@ -18,13 +18,13 @@ struct RopeRows {
   int32_t heads;
 };
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 320;  // at most
 
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs r, const int32_t *pos,
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(RopeArgs r, const int32_t *pos,
                                                             RopeRows q, RopeRows k) {
   constexpr int kItems = D / 16;
-  constexpr int kStep = kRopeThreads / kItems;  // heads a pass
+  const int kStep = blockDim.x / kItems;  // heads a pass
   __shared__ float4 tab[D / 4];
   const int64_t t = blockIdx.x;
   const int i = threadIdx.x % kItems, h0 = threadIdx.x / kItems;
@@ -46,10 +46,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs r, const in
       w[j][1] = *reinterpret_cast<const uint4 *>(s + ch.c1 * 8);
     }
   }
-  if (threadIdx.x < r.rd / 4) {
-    const float2 a = rotation(p, turns_per_token(r.inv_freq[2 * threadIdx.x]), r.mscale);
-    const float2 b = rotation(p, turns_per_token(r.inv_freq[2 * threadIdx.x + 1]), r.mscale);
-    tab[angle_slot(threadIdx.x, r.rd, half)] = make_float4(a.x, a.y, b.x, b.y);
+  for (int j = threadIdx.x; j < r.rd / 4; j += blockDim.x) {
+    const float2 a = rotation(p, turns_per_token(r.inv_freq[2 * j]), r.mscale);
+    const float2 b = rotation(p, turns_per_token(r.inv_freq[2 * j + 1]), r.mscale);
+    tab[angle_slot(j, r.rd, half)] = make_float4(a.x, a.y, b.x, b.y);
   }
   __syncthreads();
   for (int hb = h0; hb < heads; hb += 2 * kStep) {
@@ -146,8 +146,12 @@ extern "C" kvq_status kvq_rope(const kvq_rope_desc *rope, const int32_t *pos, in
                     q_out_stride, n_q_heads};
   const RopeRows kr{static_cast<const uint16_t *>(k), static_cast<uint16_t *>(k_out), k_stride,
                     k_out_stride, n_k_heads};
+  // two heads a thread, or a multiple
+  const int items = (n_q_heads + n_k_heads) * (head_dim / 16);
+  const int rounds = (items + 2 * kRopeThreads - 1) / (2 * kRopeThreads);
+  const int threads = ((items + 2 * rounds - 1) / (2 * rounds) + 31) / 32 * 32;
   const cudaError_t e =
       launch_dependent(head_dim == 128 ? rope_kernel<128> : rope_kernel<64>, n_tokens,
-                       kRopeThreads, 0, reinterpret_cast<cudaStream_t>(stream), r, pos, qr, kr);
+                       threads, 0, reinterpret_cast<cudaStream_t>(stream), r, pos, qr, kr);
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
