@@ -20,7 +20,7 @@ SOURCES = ["api.cu", "append.cu", "handoff.cu", "check_tags.cu", "pages.cu", "de
            "decode_attn_static.cu", "wq_gemm.cu", "selftest.cu", "rope.cu", "block_cache.cu",
            "block_attn.cu"]
 HEADERS = ["kvq_device.cuh", "kvq_internal.h", "quant_e4m3.cuh", "check_body.cuh",
-           "decode_common.cuh", "decode_attn_mma.cuh", "block_common.cuh"]
+           "decode_common.cuh", "decode_attn_mma.cuh", "block_common.cuh", "block_attn_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--prec-div=true", "--prec-sqrt=true",
               "--ftz=false", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -37,6 +37,7 @@
 // Every wait is bounded; one that gives up raises KVQ_ERRBIT_TIMEOUT, and the
 // CTA leaves after its copies have landed.
 #include <atomic>
+#include <climits>
 
 #include "block_common.cuh"
 #include "decode_common.cuh"
@@ -54,18 +55,31 @@ constexpr int kStat = 4;                         // floats after a row's accumul
 // Row tiles: 4 (one MMA column block carries the weights and their remainders),
 // 8 or 16 rows a warp; larger row counts take RT tiles of 16.  The warps that
 // the (head, row tile) pairs leave free are further teams.
+constexpr int kTcMinRows = 9;
+
 struct BaShape {
   int rk, rt, hg, tw;   // rows a warp, row tiles, heads a stage, teams
   int rows;             // rows a row block holds: rk * rt
   int row_blocks;       // row blocks of a request of max_q rows
   int groups;           // head groups
+  bool tc;              // the tcgen05 kernel: blocks of 32 rows of one head
   int pairs() const { return hg * rt; }
   int slots() const { return pairs() * (tw - 1); }
 };
 
-inline BaShape ba_shape(int max_q, int G, int Hkv) {
+inline BaShape ba_shape(int max_q, int G, int Hkv, int D) {
   BaShape s;
   const int64_t rows = static_cast<int64_t>(max_q) * G;
+  s.tc = D == 128 && rows >= kTcMinRows;
+  if (s.tc) {
+    s.rk = 16;
+    s.rt = 2;
+    s.rows = 32;
+    s.row_blocks = static_cast<int>((rows + 31) / 32);
+    s.hg = s.tw = 1;
+    s.groups = Hkv;
+    return s;
+  }
   s.rk = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
   s.rt = 1;
   while (s.rt < kBaWarps && s.rk * s.rt < rows) s.rt *= 2;
@@ -923,6 +937,12 @@ __global__ void __launch_bounds__(kBaThreads, 1)
   }
 }
 
+}  // namespace kvq
+
+#include "block_attn_tc.cuh"
+
+namespace kvq {
+
 // ---------------------------------------------------------------------------
 // combine: rows cut across CTAs
 // ---------------------------------------------------------------------------
@@ -1063,13 +1083,13 @@ BaFn ba_kernel(int rk) {
 }
 
 // Opt a kernel into its shared memory, once per device.
-bool ba_opt_in(BaFn fn, int variant) {
+bool ba_opt_in(BaFn fn, int variant, size_t smem) {
   constexpr int kMaxDev = 64;
-  static std::atomic<bool> done[kMaxDev][6];
+  static std::atomic<bool> done[kMaxDev][7];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return false;
   if (done[dev][variant].load(std::memory_order_acquire)) return true;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kBaSmem) !=
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
       cudaSuccess)
     return false;
   done[dev][variant].store(true, std::memory_order_release);
@@ -1113,7 +1133,7 @@ extern "C" size_t kvq_block_attn_workspace_size(int32_t B, int32_t max_q, int32_
   if (static_cast<int64_t>(max_q) * (Hq / num_kv_heads) > INT32_MAX / 2) return 0;
   int sms = 0;
   if (device_sm_count(&sms) != KVQ_OK) return 0;
-  const BaShape s = ba_shape(max_q, Hq / num_kv_heads, num_kv_heads);
+  const BaShape s = ba_shape(max_q, Hq / num_kv_heads, num_kv_heads, head_dim);
   return ba_cut_bytes(sms) + ba_part_bytes(s, head_dim, sms);
 }
 
@@ -1137,7 +1157,7 @@ extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q
     return KVQ_ERR_INVALID_ARG;
   int sms = 0;
   if (device_sm_count(&sms) != KVQ_OK) return KVQ_ERR_CUDA;
-  const BaShape s = ba_shape(max_q, G, Hkv);
+  const BaShape s = ba_shape(max_q, G, Hkv, D);
   const size_t cb = ba_cut_bytes(sms);
   if (!aligned256(workspace) || workspace_bytes < cb + ba_part_bytes(s, D, sms))
     return KVQ_ERR_WORKSPACE;
@@ -1165,15 +1185,17 @@ extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q
   a.rounds = 0;
   for (int t = s.tw; t > 1; t = (t + 1) / 2) ++a.rounds;
   a.groups = s.groups;
-  a.stages = ba_stages(s, D);
+  a.stages = s.tc ? kTcStages : ba_stages(s, D);
   a.q_scale = sm_scale * kLog2e;
-  const BaFn fn = D == 128 ? ba_kernel<128>(s.rk) : ba_kernel<64>(s.rk);
-  if (!ba_opt_in(fn, (D == 128 ? 3 : 0) + (s.rk == 4 ? 0 : s.rk == 8 ? 1 : 2))) return KVQ_ERR_CUDA;
+  const BaFn fn = s.tc ? block_tc_kernel : D == 128 ? ba_kernel<128>(s.rk) : ba_kernel<64>(s.rk);
+  const size_t smem = s.tc ? tc_smem_bytes() : kBaSmem;
+  const int variant = s.tc ? 6 : (D == 128 ? 3 : 0) + (s.rk == 4 ? 0 : s.rk == 8 ? 1 : 2);
+  if (!ba_opt_in(fn, variant, smem)) return KVQ_ERR_CUDA;
   CUtensorMap kmap, vmap;
   if (!ba_map(&kmap, cache->k_pool, *cache, s.hg) || !ba_map(&vmap, cache->v_pool, *cache, s.hg))
     return KVQ_ERR_CUDA;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (launch_dependent(fn, sms, kBaThreads, kBaSmem, cs, kmap, vmap, a) != cudaSuccess)
+  if (launch_dependent(fn, sms, s.tc ? kTcThreads : kBaThreads, smem, cs, kmap, vmap, a) != cudaSuccess)
     return KVQ_ERR_CUDA;
   // fewer than a row of work for three CTAs: a row is cut into four parts or
   // more, and a CTA merges each of its output rows

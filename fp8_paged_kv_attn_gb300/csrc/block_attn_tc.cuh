@@ -1,0 +1,732 @@
+// The tcgen05 split kernel of kvq_block_attn: head_dim 128, 9 and more rows
+// (query rows times heads of a kv head).  Included by block_attn.cu.
+//
+// mma.sync would be the bound here: a warp's 16 rows need 48 MMAs a 16-token
+// tile.  On tcgen05 the 8-bit kind multiplies the cache's bytes as they are
+// (K as a K-major operand, V as an MN-major one: both are the pool's own
+// layout), so nothing of the cache is converted.  What has to be 8-bit too is
+// split into e4m3 pieces:
+//   q   a row scaled by 2^e (largest value in [224, 448)) = q1 + q2, each e4m3 (4
+//       significant bits, a bf16 has 8): exact for values down to 2^-10 of the row's
+//       largest, below that off by at most 2^-10 on that scale.  S = q1 K + q2 K
+//       in one accumulator.
+//   w   a softmax weight (times 2^4, at most 2^8) = p1 + p2/16 + p3/256 + p4/4096: each
+//       piece leaves at most a 16th (on average a 36th) of what the one before left, at
+//       most 2^-16 of w, and 2^-22 for weights below e4m3's normal range.  The pieces
+//       of 32 rows are the 128 rows of one MMA: piece p of row r is row 32 p + r, and
+//       the four sums of a row are added when a segment ends.
+// Sums are fp32 (measured: 2^-20.7 of the sum of the terms' magnitudes).
+//
+//   S[128 x 128 tokens] = Q[128 x 128] K^T   q's 32 rows four times over, so that
+//       each of a group's four warps finds them in its own TMEM lanes; warp p takes
+//       tokens 32 p .. 32 p + 31 of the tile (a row a lane, no shuffles)
+//   O[128 x 128 dims] += P[128 x 128 tokens] V
+// At 8,192 multiplications a cycle a 128-token tile of one head costs 768 cycles
+// of the tensor core, of the 1,424 that its 32 KB take from HBM.
+//
+// Roles: warps 0-3 and 4-7 two softmax groups with their own S and O (TMEM: 4 x
+// 128 columns), warp 8 issues the MMAs, warp 9 the copies.  The groups take a
+// head's tiles in turn and are merged when the segment ends.  Work is
+// scheduled, cut and combined as in the mma.sync kernel, in units of 128 tokens
+// of one head; more than 32 rows are row blocks, which follow one another so
+// that the second reads the cache from L2.
+#pragma once
+
+namespace kvq {
+
+constexpr int kTcTok = 128;                 // tokens a tile
+constexpr int kTcStages = 4;                // even: a ring slot belongs to one group within a segment
+constexpr int kTcThreads = 320;
+constexpr int kTcRows = 32;                 // rows a row block holds
+constexpr int kTcTile = kTcTok * 128;       // 16 KB: one tile of K or V, q piece, or P
+constexpr int kTcRowCost = 6;               // a row's start and end, in tiles' times
+constexpr float kTcThreshold = 4.f;         // lazy rescaling: weights stay below 2^4
+constexpr uint32_t kTcColS = 0, kTcColO = 256;
+
+struct TcSeg {
+  int b, head, rb;
+  int row0, n, L;
+  int rows;        // rows of this block that exist (1 .. 32)
+  int t_begin, tiles, part;
+};
+
+struct TcCtl {
+  TcSeg seg[kBaSegs];
+  uint64_t full[kTcStages], empty[kTcStages];
+  uint64_t segfull[kBaSegs], segempty[kBaSegs];
+  uint64_t qfull, sfull[2], sfree[2], pfull[2], pvdone[2];
+  uint64_t xch[2], epi, drain;
+  float2 sc[kTcStages][kTcTok / 16];
+  int bad[kTcStages];
+  float qk[32];                    // what undoes q's scale, times sm_scale log2(e)
+  float2 mx[2][2][4][32];          // [group][parity][warp][row]: a tile's maxima of x and x + log2 vs
+  float4 stat[2][4][32];           // [group][warp][row]: m, l, n at a segment's end
+  int nan_from[128];               // per dim: the first drafted token with a NaN code there
+  RunScan<kTcThreads> scan;
+  uint32_t tmem;
+  int fail;
+};
+
+__device__ __forceinline__ bool tc_wait(TcCtl &ctl, uint64_t *bar, uint32_t parity,
+                                        uint32_t *err_word) {
+  bool ok = false;
+  if (!*reinterpret_cast<volatile int *>(&ctl.fail)) {
+    ok = mbar_wait(bar, parity);
+    if (!ok && atomicExch(&ctl.fail, 1) == 0) report(err_word, KVQ_ERRBIT_TIMEOUT);
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Shared-memory operand of 128-byte rows, 128-byte swizzle, 8-row groups 1,024
+// bytes apart (bits 46-48: descriptor version 1; 61-63: the swizzle).
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+
+// fp32 += e4m3 * e4m3, 128 x 128; transposed: B is MN-major.
+__host__ __device__ constexpr uint32_t tc_idesc(bool transposed) {
+  return (1u << 4) | ((transposed ? 1u : 0u) << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add ? 1 : 0)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_addr(bar))
+               : "memory");
+}
+
+// 32 consecutive columns of this warp's 32 lanes.
+__device__ __forceinline__ void tc_ld32(float (&v)[32], uint32_t addr) {
+  uint32_t *r = reinterpret_cast<uint32_t *>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tc_st32(uint32_t addr, const float (&v)[32]) {
+  const uint32_t *r = reinterpret_cast<const uint32_t *>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+
+// One e4m3 piece of two values and what is left of them, times `up`.
+__device__ __forceinline__ uint32_t tc_piece(float2 &x, float up) {
+  const uint16_t c = f32x2_to_e4m3x2(x.x, x.y);
+  const float2 p = f16x2_to_f32x2(e4m3x2_to_f16x2(c));
+  x.x = (x.x - p.x) * up;
+  x.y = (x.y - p.y) * up;
+  return c;
+}
+
+// 16-byte chunk c of row r in a 128-byte-swizzled tile.
+__device__ __forceinline__ uint8_t *tc_chunk(uint8_t *tile, int r, int c) {
+  return tile + r * 128 + ((c ^ (r & 7)) * 16);
+}
+
+// q's rows into the two piece tiles, each row at 32 p + r for every p; warp
+// `quad` of four takes eight rows.
+__device__ __forceinline__ void tc_load_q(const BaArgs &a, const TcSeg &sg, uint8_t *tiles, float *qk,
+                                          int quad, int lane) {
+  const int r = 8 * quad + (lane >> 2), part = lane & 3;  // 32 dims a lane
+  const int row = sg.rb * kTcRows + r, i = row / a.G;
+  float x[32];
+  if (i < sg.n) {
+    const uint16_t *p = a.q + (static_cast<int64_t>(sg.row0) + i) * a.q_stride +
+                        static_cast<int64_t>(sg.head * a.G + row - i * a.G) * 128 + 32 * part;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) unpack8(__ldg(reinterpret_cast<const uint4 *>(p) + c), x + 8 * c);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) x[c] = 0.f;
+  }
+  float mx = 0.f;
+  bool odd = false;  // inf or NaN: the row's scores are NaN, as inf - inf would make them
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    mx = fmaxf(mx, finite_abs(x[c]));
+    odd |= !(fabsf(x[c]) < INFINITY);
+  }
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  // largest value into [224, 448): block_exponent is the smallest e with mx <= 448 2^e
+  const int e = block_exponent(mx);
+  const float up = pow2(-e);
+  const float nan = odd ? NAN : 0.f;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {  // 16 dims: one 16-byte chunk of each piece
+    uint32_t q1[4], q2[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float2 u = make_float2(x[16 * c + 4 * k] * up + nan, x[16 * c + 4 * k + 1] * up + nan);
+      float2 v = make_float2(x[16 * c + 4 * k + 2] * up + nan, x[16 * c + 4 * k + 3] * up + nan);
+      q1[k] = tc_piece(u, 1.f);
+      q1[k] |= tc_piece(v, 1.f) << 16;
+      q2[k] = tc_piece(u, 1.f);
+      q2[k] |= tc_piece(v, 1.f) << 16;
+    }
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      *reinterpret_cast<uint4 *>(tc_chunk(tiles, 32 * p + r, 2 * part + c)) =
+          make_uint4(q1[0], q1[1], q1[2], q1[3]);
+      *reinterpret_cast<uint4 *>(tc_chunk(tiles + kTcTile, 32 * p + r, 2 * part + c)) =
+          make_uint4(q2[0], q2[1], q2[2], q2[3]);
+    }
+  }
+  if (part == 0) qk[r] = a.q_scale * pow2(e);
+}
+
+__global__ void __launch_bounds__(kTcThreads, 1)
+    block_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                    BaArgs a) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  uint8_t *kv = smem;                                  // [stage][K, V]
+  uint8_t *qt = kv + kTcStages * 2 * kTcTile;          // [2 pieces]
+  uint8_t *pt = qt + 2 * kTcTile;                      // [group]
+  TcCtl &ctl = *reinterpret_cast<TcCtl *>(pt + 2 * kTcTile);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kTcStages; ++i) {
+      mbar_init(&ctl.full[i], 1 + 8);
+      mbar_init(&ctl.empty[i], 1);
+    }
+    for (int i = 0; i < kBaSegs; ++i) {
+      mbar_init(&ctl.segfull[i], 1);
+      mbar_init(&ctl.segempty[i], 9);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&ctl.sfull[g], 1);
+      mbar_init(&ctl.sfree[g], 4);
+      mbar_init(&ctl.pfull[g], 4);
+      mbar_init(&ctl.pvdone[g], 1);
+      mbar_init(&ctl.xch[g], 4);
+    }
+    mbar_init(&ctl.qfull, 4);
+    mbar_init(&ctl.epi, 8);
+    mbar_init(&ctl.drain, 1);
+    ctl.fail = 0;
+    fence_barrier_init();
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_addr(&ctl.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = ctl.tmem;
+  grid_dependency_wait();
+  const RunStart run = find_run<kTcThreads>(
+      a.rg.B, gridDim.x, blockIdx.x, ctl.scan, [&](int b) -> int64_t {
+        bool live;
+        const Rows r = ba_rows(a, b, live);
+        if (r.err && blockIdx.x == 0) report(a.err_word, r.err);
+        return live ? static_cast<int64_t>((r.p0 + r.n + kTcTok - 1) / kTcTok + kTcRowCost) * a.groups *
+                          ba_blocks(a, r, kTcRows)
+                    : 0;
+      });
+  allow_dependents();
+  const int64_t u0 = blockIdx.x * run.per;
+  const int64_t u1 = min(u0 + run.per, run.total);
+
+  if (warp == 9) {
+    // ------------------------------------------------------------ producer
+    const uint64_t once = policy_evict_first();
+    uint64_t again;  // the cache is read by several row blocks
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(again));
+    int64_t u = u0, in = run.in;
+    int b = run.b;
+    BaCut cut = {0, 0, 0, 0, 0, {0, 0, 0}};
+    uint32_t g = 0, nseg = 0, par = 1;
+    int slot = 0;
+    bool ok = true;
+    int win_b = -1, win = 0, cur = -1, nxt = -1;
+    const int32_t *bt = a.block_table;
+    auto bt_load = [&](int lp) -> int { return lp < a.MP ? __ldg(bt + lp) : -1; };
+    while (ok && u < u1) {
+      bool live;
+      const Rows rq = ba_rows(a, b, live);
+      const int tiles = live ? (rq.p0 + rq.n + kTcTok - 1) / kTcTok : 0, units = tiles + kTcRowCost;
+      const int nb = live ? ba_blocks(a, rq, kTcRows) : 0;
+      const int64_t have = static_cast<int64_t>(units) * a.groups * nb;
+      if (in >= have) {
+        ++b;
+        in = 0;
+        continue;
+      }
+      const int64_t rw = in / units;
+      const int s = static_cast<int>(in - rw * units);
+      const int head = static_cast<int>(rw / nb), rb = static_cast<int>(rw - static_cast<int64_t>(head) * nb);
+      const uint64_t pol = nb > 1 ? again : once;
+      const int span = static_cast<int>(min(static_cast<int64_t>(units - s), u1 - u));
+      const int t0 = max(0, s - kTcRowCost), take = s + span - kTcRowCost - t0;
+      const int64_t ut = u - s + kTcRowCost;
+      u += span;
+      in += span;
+      if (take <= 0) continue;
+      const int L = rq.p0 + rq.n;
+      const int64_t c_lo = ut / run.per;
+      const int nparts = static_cast<int>((ut + tiles - 1) / run.per - c_lo) + 1;
+      const int ss = nseg % kBaSegs;
+      if (nseg >= kBaSegs) ok = tc_wait(ctl, &ctl.segempty[ss], ((nseg / kBaSegs) - 1) & 1, a.err_word);
+      if (!ok) break;
+      if (lane == 0) {
+        if (t0 == 0 && nparts > 1) cut = {nparts, head, rb, rq.row, rq.n, {0, 0, 0}};
+        ctl.seg[ss] = {b, head, rb, rq.row, rq.n, L, min(rq.n * a.G - rb * kTcRows, kTcRows),
+                       t0 * kTcTok, take,
+                       nparts == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (t0 == 0 ? 1 : 0)};
+        mbar_arrive(&ctl.segfull[ss]);
+      }
+      ++nseg;
+      const int lp0 = (t0 * kTcTok) >> a.p_shift;
+      if (b != win_b || lp0 < win || lp0 >= win + 32) {
+        win_b = b;
+        win = lp0;
+        bt = a.block_table + static_cast<int64_t>(b) * a.MP;
+        cur = bt_load(win + lane);
+        nxt = bt_load(win + 32 + lane);
+      }
+      for (int st = 0, tok = t0 * kTcTok; st < take; ++st, tok += kTcTok) {
+        ok = tc_wait(ctl, &ctl.empty[slot], par, a.err_word);
+        if (!ok) break;
+        if ((tok >> a.p_shift) >= win + 32) {
+          win += 32;
+          cur = nxt;
+          nxt = bt_load(win + 32 + lane);
+        }
+        // lane j < 8: tokens tok + 16 j ..; their page lies within two windows
+        const int mine = tok + 16 * (lane & 7);
+        const int idx = (mine >> a.p_shift) - win;
+        const int from_cur = __shfl_sync(0xffffffffu, cur, idx & 31);
+        const int from_nxt = __shfl_sync(0xffffffffu, nxt, idx & 31);
+        const int page = idx < 32 ? from_cur : from_nxt;
+        const bool needed = lane < 8 && mine < L;
+        const bool good = needed && page >= 0 && page < a.num_pages;
+        const int copies = __popc(__ballot_sync(0xffffffffu, good));
+        const bool bad = __any_sync(0xffffffffu, needed && !good);
+        if (lane == 0) {
+          ctl.bad[slot] = bad;
+          if (bad) report(a.err_word, KVQ_ERRBIT_PAGE);
+          mbar_arrive_expect_tx(&ctl.full[slot], static_cast<uint32_t>(copies) * 4096u);
+        }
+        __syncwarp();
+        if (good) {
+          const int y = mine & ((1 << a.p_shift) - 1);
+          uint8_t *dst = kv + slot * 2 * kTcTile + 2048 * lane;
+          tma_load_4d(dst, &kmap, 0, y, head, page, &ctl.full[slot], pol);
+          tma_load_4d(dst + kTcTile, &vmap, 0, y, head, page, &ctl.full[slot], pol);
+          cp_async8(&ctl.sc[slot][lane], a.scales + static_cast<int64_t>(page) * a.Hkv + head);
+          cp_async_arrive(&ctl.full[slot]);
+        } else if (lane < 8) {
+          ctl.sc[slot][lane] = make_float2(1.f, 1.f);  // masked tokens
+          mbar_arrive(&ctl.full[slot]);
+        }
+        ++g;
+        if (++slot == kTcStages) {
+          slot = 0;
+          par ^= 1;
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) a.cut[blockIdx.x] = cut;
+    if (ok) {  // nothing more
+      const int ss = nseg % kBaSegs;
+      if (nseg >= kBaSegs) ok = tc_wait(ctl, &ctl.segempty[ss], ((nseg / kBaSegs) - 1) & 1, a.err_word);
+      if (ok && lane == 0) {
+        ctl.seg[ss].b = -1;
+        mbar_arrive(&ctl.segfull[ss]);
+      }
+    }
+    if (*reinterpret_cast<volatile int *>(&ctl.fail) && lane == 0)
+      for (uint32_t k = g > kTcStages ? g - kTcStages : 0; k < g; ++k)
+        mbar_wait(&ctl.full[k % kTcStages], (k / kTcStages) & 1);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ MMA issue
+    uint32_t nseg = 0, g0 = 0;
+    uint32_t ns[2] = {0, 0}, np[2] = {0, 0};  // S and P tiles so far
+    bool ok = true;
+    const uint32_t kv_a = smem_addr(kv), qt_a = smem_addr(qt), pt_a = smem_addr(pt);
+    auto issue_s = [&](int g, int slot) -> bool {
+      if (!tc_wait(ctl, &ctl.sfree[g], (ns[g] & 1) ^ 1, a.err_word)) return false;
+      ++ns[g];
+      tc_after();
+      if (lane == 0) {
+        const uint64_t kd = tc_desc(kv_a + slot * 2 * kTcTile), qd = tc_desc(qt_a);
+#pragma unroll
+        for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)  // 32 dims each: 32 bytes within the swizzled rows
+            tc_mma(tmem + kTcColS + 128 * g, qd + piece * (kTcTile >> 4) + 2 * k, kd + 2 * k, tc_idesc(false),
+                   piece + k > 0);
+        tc_commit(&ctl.sfull[g]);
+      }
+      __syncwarp();
+      return true;
+    };
+    auto issue_pv = [&](int g, int slot, bool add) {
+      if (lane == 0) {
+        const uint64_t vd = tc_desc(kv_a + slot * 2 * kTcTile + kTcTile), pd = tc_desc(pt_a + g * kTcTile);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // 32 tokens each: 32 bytes of P's rows, 32 rows of V
+          tc_mma(tmem + kTcColO + 128 * g, pd + 2 * k, vd + k * (32 * 128 >> 4), tc_idesc(true), add || k > 0);
+        tc_commit(&ctl.pvdone[g]);
+      }
+    };
+    while (ok) {
+      const int ss = nseg % kBaSegs;
+      ok = tc_wait(ctl, &ctl.segfull[ss], (nseg / kBaSegs) & 1, a.err_word);
+      if (!ok) break;
+      const TcSeg sg = ctl.seg[ss];
+      if (sg.b < 0) break;
+      ok = tc_wait(ctl, &ctl.qfull, nseg & 1, a.err_word);
+      for (int t = 0; ok && t <= sg.tiles; ++t) {
+        if (t < sg.tiles) {
+          const uint32_t gg = g0 + t;
+          const int slot = gg % kTcStages;
+          ok = tc_wait(ctl, &ctl.full[slot], (gg / kTcStages) & 1, a.err_word) && issue_s(t & 1, slot);
+        }
+        if (ok && t > 0) {  // P V of the tile before
+          const int tp = t - 1, g = tp & 1, slot = (g0 + tp) % kTcStages;
+          ok = tc_wait(ctl, &ctl.pfull[g], np[g]++ & 1, a.err_word);
+          if (ok) {
+            tc_after();
+            issue_pv(g, slot, tp >= 2);
+            if (lane == 0) tc_commit(&ctl.empty[slot]);
+            __syncwarp();
+          }
+        }
+      }
+      g0 += sg.tiles;
+      ++nseg;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.segempty[ss]);
+    }
+    if (*reinterpret_cast<volatile int *>(&ctl.fail)) {
+      // the products in flight end before the CTA's memory goes to another one
+      if (lane == 0) tc_commit(&ctl.drain);
+      mbar_wait(&ctl.drain, 0);
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    // rows of requests without work are zeros
+    for (int b = blockIdx.x; b < a.rg.B; b += gridDim.x) {
+      bool live;
+      const Rows r = ba_rows(a, b, live);
+      if (live || r.n == 0) continue;
+      float4 *o = reinterpret_cast<float4 *>(a.out + static_cast<int64_t>(r.row) * a.Hq * 128);
+      const int64_t n4 = static_cast<int64_t>(r.n) * a.Hq * 32;
+      for (int64_t k = threadIdx.x; k < n4; k += 256) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const int grp = warp >> 2, quad = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+    const uint32_t s_addr = tmem + lanes + kTcColS + 128 * grp, o_addr = tmem + lanes + kTcColO + 128 * grp;
+    uint8_t *ptile = pt + grp * kTcTile;
+    uint32_t nseg = 0, g0 = 0, nt = 0, nx = 0, ne = 0;
+    auto group_sync = [&]() -> bool {  // the group's four warps
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.xch[grp]);
+      return tc_wait(ctl, &ctl.xch[grp], nx++ & 1, a.err_word);
+    };
+    auto both_sync = [&]() -> bool {  // both groups
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.epi);
+      return tc_wait(ctl, &ctl.epi, ne++ & 1, a.err_word);
+    };
+    bool ok = true;
+    while (ok) {
+      const int ss = nseg % kBaSegs;
+      ok = tc_wait(ctl, &ctl.segfull[ss], (nseg / kBaSegs) & 1, a.err_word);
+      if (!ok) break;
+      const TcSeg sg = ctl.seg[ss];
+      if (sg.b < 0) break;
+      const int row = sg.rb * kTcRows + lane;  // of the request
+      const int my_i = row / a.G;
+      const int lim = my_i < sg.n ? sg.L - sg.n + 1 + my_i : sg.L;
+      const int min_lim = min(sg.L, sg.L - sg.n + 1 + (sg.rb * kTcRows) / a.G);
+      if (grp == 0) {
+        ctl.nan_from[threadIdx.x] = INT_MAX;  // read before the last barrier
+        tc_load_q(a, sg, qt, ctl.qk, quad, lane);
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.qfull);
+      }
+      ok = tc_wait(ctl, &ctl.qfull, nseg & 1, a.err_word);
+      if (!ok) break;
+      const float qk = ctl.qk[lane];
+      float m = -INFINITY, n = -INFINITY, l = 0.f;
+      bool seg_bad = false, any_tile = false;
+      for (int t = grp; t < sg.tiles; t += 2) {
+        const uint32_t gg = g0 + t;
+        const int slot = gg % kTcStages;
+        const int tok0 = sg.t_begin + t * kTcTok, tw = tok0 + 32 * quad;  // this warp's tokens
+        ok = tc_wait(ctl, &ctl.full[slot], (gg / kTcStages) & 1, a.err_word) &&
+             tc_wait(ctl, &ctl.sfull[grp], nt & 1, a.err_word);
+        if (!ok) break;
+        seg_bad |= ctl.bad[slot] != 0;
+        tc_after();
+        float x[32];
+        tc_ld32(x, s_addr + 32 * quad);
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.sfree[grp]);
+        const bool partial = tok0 + kTcTok > min_lim;
+        float lv[2], vm[2], mx = -INFINITY, mv = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // 16 tokens of one block
+          const float2 sc = ctl.sc[slot][2 * quad + h];
+          const uint32_t ub = __float_as_uint(sc.y);
+          const int e = static_cast<int>(ub >> 23) - 127 + ((ub & 0x7FFFFFu) ? 1 : 0);
+          lv[h] = static_cast<float>(e);
+          vm[h] = sc.y * pow2(max(-126, min(127, -e)));
+          const float f = qk * sc.x;
+          float mt = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float y = x[16 * h + c] * f;
+            if (partial && tw + 16 * h + c >= lim) y = -INFINITY;
+            x[16 * h + c] = y;
+            mt = fmaxf(mt, y);
+          }
+          mx = fmaxf(mx, mt);
+          mv = fmaxf(mv, mt + lv[h]);
+        }
+        float2(*xm)[32] = ctl.mx[grp][nt & 1];
+        xm[quad][lane] = make_float2(mx, mv);
+        ok = group_sync();
+        if (!ok) break;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float2 o = xm[w][lane];
+          mx = fmaxf(mx, o.x);
+          mv = fmaxf(mv, o.y);
+        }
+        // the row's references: the same in all four warps
+        if (mx > m + kTcThreshold) {
+          l *= exp2f(m - mx);
+          m = mx;
+        }
+        float fo = 1.f;
+        if (mv > n + kTcThreshold) {
+          fo = exp2f(n - mv);
+          n = mv;
+        }
+        // the group's product before this one has been read and summed
+        if (any_tile) {
+          ok = tc_wait(ctl, &ctl.pvdone[grp], (nt & 1) ^ 1, a.err_word);
+          if (!ok) break;
+          if (__any_sync(0xffffffffu, fo != 1.f)) {
+            tc_after();
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) {
+              float o[32];
+              tc_ld32(o, o_addr + c);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= fo;
+              tc_st32(o_addr + c, o);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          }
+        }
+        any_tile = true;
+        const bool none = n == -INFINITY;  // nothing seen yet: every x is -inf
+        const float mm = none ? 0.f : m, mn = none ? 0.f : m - n;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // vs 2^(m - n), times 2^4 (kTcThreshold keeps the weights below 2^8)
+          const float d = vm[h] * 16.f * fast_exp2(fminf(mn + lv[h], 112.f));
+          uint32_t w1[4], w2[4], w3[4], w4[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t c1 = 0, c2 = 0, c3 = 0, c4 = 0;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int c = 16 * h + 4 * k + 2 * j;
+              const float e0 = fast_exp2(x[c] - mm), e1 = fast_exp2(x[c + 1] - mm);
+              l += e0 + e1;
+              float2 w = make_float2(e0 * d, e1 * d);
+              c1 |= tc_piece(w, 16.f) << (16 * j);
+              c2 |= tc_piece(w, 16.f) << (16 * j);
+              c3 |= tc_piece(w, 16.f) << (16 * j);
+              c4 |= static_cast<uint32_t>(f32x2_to_e4m3x2(w.x, w.y)) << (16 * j);
+            }
+            w1[k] = c1;
+            w2[k] = c2;
+            w3[k] = c3;
+            w4[k] = c4;
+          }
+          const int ch = 2 * quad + h;
+          *reinterpret_cast<uint4 *>(tc_chunk(ptile, lane, ch)) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+          *reinterpret_cast<uint4 *>(tc_chunk(ptile, 32 + lane, ch)) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+          *reinterpret_cast<uint4 *>(tc_chunk(ptile, 64 + lane, ch)) = make_uint4(w3[0], w3[1], w3[2], w3[3]);
+          *reinterpret_cast<uint4 *>(tc_chunk(ptile, 96 + lane, ch)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        }
+        if (partial) {
+          // V rows past the end (whatever the slot or the cache holds) become
+          // zeros, and NaN codes of drafted tokens too: a weight of 0 does not stop
+          // a NaN.  Rows that see such a token get their NaN when they are written.
+          const int tr = 32 * quad + lane, tok = tok0 + tr;
+          uint8_t *vt = kv + slot * 2 * kTcTile + kTcTile;
+          if (tok >= sg.L) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(tc_chunk(vt, tr, c)) = make_uint4(0, 0, 0, 0);
+          } else if (tok >= min_lim) {
+            for (int c = 0; c < 8; ++c) {
+              uint4 *p = reinterpret_cast<uint4 *>(tc_chunk(vt, tr, c));
+              const uint4 v = *p;
+              if (!(has_nan(v.x) || has_nan(v.y) || has_nan(v.z) || has_nan(v.w))) continue;
+              uint32_t q[4] = {v.x, v.y, v.z, v.w};
+              for (int k = 0; k < 16; ++k)
+                if (((q[k >> 2] >> (8 * (k & 3))) & 0x7Fu) == 0x7Fu) {
+                  q[k >> 2] &= ~(0xFFu << (8 * (k & 3)));
+                  atomicMin(&ctl.nan_from[16 * c + k], tok);
+                }
+              *p = make_uint4(q[0], q[1], q[2], q[3]);
+            }
+          }
+        }
+        ++nt;
+        proxy_fence();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.pfull[grp]);
+      }
+      if (!ok) break;
+      g0 += sg.tiles;
+
+      // ---- the segment's end
+      if (any_tile) {
+        ok = tc_wait(ctl, &ctl.pvdone[grp], (nt & 1) ^ 1, a.err_word);
+        if (!ok) break;
+        tc_after();
+      }
+      ctl.stat[grp][quad][lane] = make_float4(m, seg_bad ? -1.f : l, n, 0.f);
+      ok = both_sync();
+      if (!ok) break;
+      float M = -INFINITY, N = -INFINITY, L1 = 0.f, gm[2], gn[2], gl[2], f[2];
+      bool bad = false;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        gl[k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float4 v = ctl.stat[k][w][lane];
+          bad |= v.y < 0.f;
+          gl[k] += v.y;
+          gm[k] = v.x;
+          gn[k] = v.z;
+        }
+        if (gl[k] != 0.f) {  // (also NaN); a group that saw nothing has no weight
+          M = fmaxf(M, gm[k]);
+          N = fmaxf(N, gn[k]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        f[k] = gl[k] != 0.f ? exp2f(gn[k] - N) : 0.f;
+        if (gl[k] != 0.f) L1 += gl[k] * exp2f(gm[k] - M);
+      }
+      const bool used = lane < sg.rows;
+      // a partial's row: sums, then m, l, n (n counts the 2^7 of the other kernel)
+      float *out = sg.part < 0 ? a.out + ((static_cast<int64_t>(sg.row0) + my_i) * a.Hq + sg.head * a.G +
+                                          row - my_i * a.G) * 128
+                               : a.part + (static_cast<int64_t>(sg.part) * kTcRows + lane) * (128 + kStat);
+      // out = 2^(N - M - 4) sum / l
+      const float scale = sg.part < 0 ? exp2f(N - M - 4.f) / L1 : 1.f;
+      const float down = quad == 0 ? 1.f : quad == 1 ? 1.f / 16 : quad == 2 ? 1.f / 256 : 1.f / 4096;
+      for (int c = 0; c < 128; c += 32) {
+        // 32 columns of every warp's piece into the P tiles, [warp][row][32]; then
+        // each of the eight warps sums four columns
+        float o[32];
+        if (any_tile) {
+          tc_ld32(o, o_addr + c);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<float4 *>(tc_chunk(ptile + quad * 4096, lane, k)) =
+              make_float4(o[4 * k] * down, o[4 * k + 1] * down, o[4 * k + 2] * down, o[4 * k + 3] * down);
+        ok = both_sync();
+        if (!ok) break;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (gl[s] == 0.f) continue;
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int p = 3; p >= 0; --p) {  // the smallest pieces first
+            const float4 v =
+                *reinterpret_cast<const float4 *>(tc_chunk(pt + s * kTcTile + p * 4096, lane, warp));
+            sum.x += v.x;
+            sum.y += v.y;
+            sum.z += v.z;
+            sum.w += v.w;
+          }
+          acc.x = fmaf(f[s], sum.x, acc.x);
+          acc.y = fmaf(f[s], sum.y, acc.y);
+          acc.z = fmaf(f[s], sum.z, acc.z);
+          acc.w = fmaf(f[s], sum.w, acc.w);
+        }
+        const int dim = c + 4 * warp;
+        acc.x = ctl.nan_from[dim] < lim ? NAN : acc.x * scale;
+        acc.y = ctl.nan_from[dim + 1] < lim ? NAN : acc.y * scale;
+        acc.z = ctl.nan_from[dim + 2] < lim ? NAN : acc.z * scale;
+        acc.w = ctl.nan_from[dim + 3] < lim ? NAN : acc.w * scale;
+        if (bad && sg.part < 0) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (used) *reinterpret_cast<float4 *>(out + dim) = acc;
+        ok = both_sync();  // the tiles are read (and nan_from, at the end)
+        if (!ok) break;
+      }
+      if (!ok) break;
+      if (used && sg.part >= 0 && warp == 0)
+        *reinterpret_cast<float4 *>(out + 128) = make_float4(M, bad ? -1.f : L1, N + 3.f, 0.f);
+      ++nseg;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.segempty[ss]);
+    }
+    tc_before();
+  }
+  __syncthreads();  // every role comes here, also when a wait gave up
+  if (warp == 8) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+inline size_t tc_smem_bytes() {
+  return static_cast<size_t>(kTcStages) * 2 * kTcTile + 4 * kTcTile + sizeof(TcCtl) + 1024;
+}
+
+}  // namespace kvq

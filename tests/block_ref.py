@@ -98,7 +98,7 @@ def gather(pool, scales, i, table_row, positions):
     return decode(pool[page, :, positions % P]) * scales[page, :, i].astype(np.float64)[:, :, None]
 
 
-def attend(pools, scales, q, tok_start, seq_lens, table, sm_scale, skip=()):
+def attend(pools, scales, q, tok_start, seq_lens, table, sm_scale, skip=(), max_q=1):
     """(out float64 [N, Hq, D] with NaN in rows of nobody, bound of the kernel's
     error in each value).  skip: requests whose rows are zeros.
 
@@ -111,7 +111,18 @@ def attend(pools, scales, q, tok_start, seq_lens, table, sm_scale, skip=()):
     operand of p.v is w_j s_j 2^(7 - n) (s_j the V scale, rounded up to a power
     of two) with 2^n at most twice the row's largest w_j s_j, and f16 rounds by
     at most 2^-25 near zero, so a token adds at most 2^-25 2^-7 2 max_i(w_i s_i)
-    = 2^-31 max_i(w_i s_i) times its code's magnitude."""
+    = 2^-31 max_i(w_i s_i) times its code's magnitude.
+
+    With head_dim 128 and more than 8 rows (max_q times heads a kv head) both
+    operands are sums of e4m3 pieces.  A weight's four pieces, 2^4 apart, leave at
+    most 2^-16 of it, and 2^-10 2^-12 where e4m3 is subnormal, on a scale where
+    the operand is w_j s_j 2^(4 - n): 2^-22 2^-4 2 max_i(w_i s_i) = 2^-25
+    max_i(w_i s_i) a token.  q's two pieces, on a scale where a row's largest
+    value lies in [224, 448), are exact for values of 2^-2 and more there (8
+    significant bits end at 2^-9) and else off by 2^-10: values below 2^-9.8 of the
+    largest are off by 2^-17.8 of it.  The tensor core's sums are off by at most 2^-20 of
+    the terms' magnitudes for 128 terms (scores: within the 2^-18 above; values: 2^-20
+    for each 128 tokens' sum, on top of fp32's)."""
     N, Hq, D = q.shape
     H = pools[0].shape[1]
     G = Hq // H
@@ -140,10 +151,16 @@ def attend(pools, scales, q, tok_start, seq_lens, table, sm_scale, skip=()):
                 w = np.exp(x - x.max())
                 den = w.sum()
                 out[row + i, h] = w @ v[:see, g] / den
-                score = np.max(np.abs(k[:see, g]) @ np.abs(qq)) * abs(sm_scale) * 2.0 ** -18
+                ak = np.abs(k[:see, g])
+                score = np.max(ak @ np.abs(qq)) * abs(sm_scale) * 2.0 ** -18
+                weight, floor = 2.0 ** -20, 2.0 ** -31
+                if D == 128 and max_q * G > 8:
+                    top = np.abs(qq).max()
+                    score += np.max(ak @ (np.abs(qq) < 2.0 ** -9.8 * top)) * abs(sm_scale) * top * 2.0 ** -17.8
+                    weight, floor = 2.0 ** -16 + 2.0 ** -19, 2.0 ** -25
                 s = scales[table[b, np.arange(see) // P], g, 1].astype(np.float64)
-                lost = 2.0 ** -31 * (w * s).max() / den * np.sum(np.abs(v[:see, g]) / s[:, None], 0)
-                rel = 2 * (2 * score + 2.0 ** -20 + (L / 16 + 64) * 2.0 ** -24)
+                lost = floor * (w * s).max() / den * np.sum(np.abs(v[:see, g]) / s[:, None], 0)
+                rel = 2 * (2 * score + weight + (L / 16 + 64) * 2.0 ** -24)
                 tol[row + i, h] = rel * (w @ np.abs(v[:see, g]) / den) + lost + 1e-30
     return out, tol
 

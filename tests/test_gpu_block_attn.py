@@ -48,8 +48,9 @@ def check(kvq, s, Hq, max_q=None, rng=None, **kw):
     rng = rng or np.random.default_rng(1)
     q, qx = R.values(rng, s.N, Hq, s.D)
     sm = s.D ** -0.5
-    want, tol = R.attend([s.k, s.v], s.scales, qx, s.tok_start, s.lens, s.table, sm)
-    got, err = attend(kvq, s, q, max_q or max(1, int(s.n.max())), **kw)
+    max_q = max_q or max(1, int(s.n.max()))
+    want, tol = R.attend([s.k, s.v], s.scales, qx, s.tok_start, s.lens, s.table, sm, max_q=max_q)
+    got, err = attend(kvq, s, q, max_q, **kw)
     assert err == 0
     compare(got, want, tol)
     return got
@@ -91,6 +92,23 @@ def test_long_and_cut_across_many_ctas(kvq, H, G, D, P):
     check(kvq, R.Step(rng, [1, 1, 1, 1, 1, 1], [3000, 1, 40, 5000, 17, 800], H, P, D), H * G)
 
 
+@pytest.mark.parametrize("H,G,n,P", [(8, 4, 8, 16), (2, 8, 4, 64), (3, 5, 3, 32), (1, 12, 9, 16)])
+def test_drafts_over_long_and_short_contexts(kvq, H, G, n, P):
+    """Several rows over contexts that end anywhere in a 128-token tile, cut across
+    CTAs and not, in one and in several row blocks."""
+    rng = np.random.default_rng([H, G, n])
+    lens = [n, 127, 128, 129, 255 + n, 1000, 5003, 2 * n]
+    check(kvq, R.Step(rng, [n, 1, n, n - 1, 2, n, n, n], lens, H, P, 128, pad=1), H * G)
+    check(kvq, R.Step(rng, [n], [3000 + n], H, P, 128), H * G)
+
+
+def test_many_drafts(kvq):
+    rng = np.random.default_rng(14)
+    n = rng.integers(0, 5, 700)
+    s = R.Step(rng, n, np.where(n > 0, n + rng.integers(0, 300, 700), 0), 2, 32, 128)
+    check(kvq, s, 8, max_q=4)
+
+
 def test_many_requests(kvq):
     """More requests than CTAs and than a CTA's threads, some without rows."""
     rng = np.random.default_rng(3)
@@ -99,22 +117,24 @@ def test_many_requests(kvq):
     check(kvq, s, 4, max_q=2)
 
 
-def test_scales_far_apart(kvq):
+@pytest.mark.parametrize("max_q", [1, 6])
+def test_scales_far_apart(kvq, max_q):
     """Pages whose V scales differ by 2^120, and not powers of two: a block of
     large values with little softmax weight beside one of small values."""
     rng = np.random.default_rng(4)
-    s = R.Step(rng, [1, 3, 1], [200, 90, 64], 2, 16, 128)
+    s = R.Step(rng, [1, max_q, 1], [200, 90, 640], 2, 16, 128)
     s.scales[:, :, 0] *= rng.uniform(0.6, 1.9, s.scales.shape[:2]).astype(np.float32)
     s.scales[:, :, 1] = np.exp2(rng.integers(-60, 60, s.scales.shape[:2])) * \
         rng.uniform(0.6, 1.9, s.scales.shape[:2])
     check(kvq, s, 8)
 
 
-def test_zero_blocks_keep_their_weight(kvq):
+@pytest.mark.parametrize("D", [64, 128])
+def test_zero_blocks_keep_their_weight(kvq, D):
     """V blocks of zeros carry the smallest scale, 2^-126: their tokens count in
     the denominator all the same."""
     rng = np.random.default_rng(5)
-    s = R.Step(rng, [1, 2], [100, 64], 1, 16, 64)
+    s = R.Step(rng, [1, 4], [100, 64], 1, 16, D)
     for lp in (0, 2, 3):
         for b in range(2):
             s.v[s.table[b, lp]] = 0
@@ -132,20 +152,23 @@ def test_large_scores(kvq):
     q[1] *= 2.0 ** -40
     q[2] = 0
     qx = q.double().numpy()
-    want, tol = R.attend([s.k, s.v], s.scales, qx, s.tok_start, s.lens, s.table, 0.25)
-    got, err = attend(kvq, s, q, 2, sm=0.25)
-    assert err == 0
-    compare(got, want, tol)
+    for max_q in (2, 5):
+        want, tol = R.attend([s.k, s.v], s.scales, qx, s.tok_start, s.lens, s.table, 0.25, max_q=max_q)
+        got, err = attend(kvq, s, q, max_q, sm=0.25)
+        assert err == 0
+        compare(got, want, tol)
 
 
 def test_nan_codes_stay_where_they_are_not_seen(kvq):
     """NaN codes behind a request's end, in unused pages and in drafted tokens
     that earlier rows do not see; a row that sees one is NaN."""
     rng = np.random.default_rng(7)
-    for H, G, n, D in ((2, 4, [4, 1, 6], 128), (1, 2, [2, 1, 5], 64), (8, 4, [8, 1, 3], 128)):
+    for H, G, n, D in ((2, 4, [4, 1, 6], 128), (1, 2, [2, 1, 5], 64), (8, 4, [8, 1, 3], 128),
+                       (2, 1, [3, 1, 6], 128), (1, 16, [5, 1, 7], 128)):
         s = R.Step(rng, n, [37, 21, 50], H, 16, D)
         q, qx = R.values(rng, s.N, H * G, D)
-        want, tol = R.attend([s.k, s.v], s.scales, qx, s.tok_start, s.lens, s.table, D ** -0.5)
+        want, tol = R.attend([s.k, s.v], s.scales, qx, s.tok_start, s.lens, s.table, D ** -0.5,
+                             max_q=max(n))
         for b in range(3):  # slots past the end
             L = int(s.lens[b])
             page = s.table[b, (L - 1) // 16]
@@ -177,7 +200,7 @@ def test_aborted_and_bad_requests(kvq):
     s = R.Step(rng, n, [40, 33, 60, 20, 70, 25, 90], 2, 16, 128, extra_pages=1, pad=2)
     q, qx = R.values(rng, s.N, 8, 128)
     want, tol = R.attend([s.k, s.v], s.scales, qx, s.tok_start, s.lens, s.table, 128 ** -0.5,
-                         skip=(1, 2, 3, 4, 5))
+                         skip=(1, 2, 3, 4, 5), max_q=5)
     abort = np.zeros(7, dtype=np.uint8)
     abort[1] = 1
     lens, table = s.lens.copy(), s.table.copy()
@@ -229,7 +252,8 @@ def test_strided_q_side_stream_and_graph(kvq):
     rng = np.random.default_rng(11)
     s = R.Step(rng, [3, 1, 2], [70, 5, 300], 2, 16, 128)
     wide, x = R.values(rng, s.N, 12, 128)
-    want, tol = R.attend([s.k, s.v], s.scales, x[:, 2:10], s.tok_start, s.lens, s.table, 128 ** -0.5)
+    want, tol = R.attend([s.k, s.v], s.scales, x[:, 2:10], s.tok_start, s.lens, s.table, 128 ** -0.5,
+                         max_q=3)
     w = wide.cuda()
     got, _ = attend(kvq, s, w[:, 2:10], 3)
     compare(got, want, tol)
@@ -326,7 +350,8 @@ def test_a_run_of_the_operators_together(kvq):
         torch.cuda.synchronize()
         assert int(err.item()) == 0
         pools, scales = [c.k_pool.cpu().numpy(), c.v_pool.cpu().numpy()], c.scales.cpu().numpy()
-        want, tol = R.attend(pools, scales, qr.double().cpu().numpy(), start, length + n, s.table, D ** -0.5)
+        want, tol = R.attend(pools, scales, qr.double().cpu().numpy(), start, length + n, s.table, D ** -0.5,
+                             max_q=T)
         rows = int(start[-1])
         err_ = np.abs(out.cpu().numpy()[:rows] - want[:rows]) - tol[:rows]
         assert err_.max() <= 0, t
