@@ -1185,7 +1185,7 @@ extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q
   a.rounds = 0;
   for (int t = s.tw; t > 1; t = (t + 1) / 2) ++a.rounds;
   a.groups = s.groups;
-  a.stages = s.tc ? kTcStages : ba_stages(s, D);
+  a.stages = s.tc ? 0 : ba_stages(s, D);
   a.q_scale = sm_scale * kLog2e;
   const BaFn fn = s.tc ? block_tc_kernel : D == 128 ? ba_kernel<128>(s.rk) : ba_kernel<64>(s.rk);
   const size_t smem = s.tc ? tc_smem_bytes() : kBaSmem;

@@ -10,37 +10,46 @@
 //       significant bits, a bf16 has 8): exact for values down to 2^-10 of the row's
 //       largest, below that off by at most 2^-10 on that scale.  S = q1 K + q2 K
 //       in one accumulator.
-//   w   a softmax weight (times 2^4, at most 2^8) = p1 + p2/16 + p3/256 + p4/4096: each
+//   w   a softmax weight (times 2^2, at most 2^8) = p1 + p2/16 + p3/256 + p4/4096: each
 //       piece leaves at most a 16th (on average a 36th) of what the one before left, at
 //       most 2^-16 of w, and 2^-22 for weights below e4m3's normal range.  The pieces
 //       of 32 rows are the 128 rows of one MMA: piece p of row r is row 32 p + r, and
 //       the four sums of a row are added when a segment ends.
 // Sums are fp32 (measured: 2^-20.7 of the sum of the terms' magnitudes).
 //
-//   S[128 x 128 tokens] = Q[128 x 128] K^T   q's 32 rows four times over, so that
+//   S[128 x 256 tokens] = Q[128 x 128] K^T   q's 32 rows four times over, so that
 //       each of a group's four warps finds them in its own TMEM lanes; warp p takes
-//       tokens 32 p .. 32 p + 31 of the tile (a row a lane, no shuffles)
+//       tokens 32 p .. 32 p + 31 of its tile (a row a lane, no shuffles)
 //   O[128 x 128 dims] += P[128 x 128 tokens] V
-// At 8,192 multiplications a cycle a 128-token tile of one head costs 768 cycles
-// of the tensor core, of the 1,424 that its 32 KB take from HBM.
+// An MMA of 128 rows takes 111 cycles here for 128 columns and 165 for 256, so
+// scores are issued for two 128-token tiles at once: 1,100 cycles a tile with the
+// values, of the 1,424 that its 32 KB take from HBM.  (With the cache as the operand of
+// 128 rows and the query rows as columns it would be 890, but then every softmax
+// thread holds all rows of one token and fetches each row's scale and references:
+// measured 262 us against 138 on 32 drafts of 1 - 8 rows.)
 //
 // Roles: warps 0-3 and 4-7 two softmax groups with their own S and O (TMEM: 4 x
-// 128 columns), warp 8 issues the MMAs, warp 9 the copies.  The groups take a
-// head's tiles in turn and are merged when the segment ends.  Work is
-// scheduled, cut and combined as in the mma.sync kernel, in units of 128 tokens
-// of one head; more than 32 rows are row blocks, which follow one another so
-// that the second reads the cache from L2.
+// 128 columns), warp 8 issues the MMAs, warps 9 and 10 the copies of K and of V (a
+// 16-token page is a copy of 2 KB, and issuing 16 a tile is too much for one
+// warp at HBM's rate), each into a ring of its own, since K is free after the
+// scores and V only after the values.  The groups take a head's tiles in turn and
+// are merged when the segment ends.  Work is scheduled, cut and combined as in the
+// mma.sync kernel, in units of 128 tokens of one head; more than 32 rows are row
+// blocks, which follow one another so that the second reads the cache from L2.
 #pragma once
 
 namespace kvq {
 
 constexpr int kTcTok = 128;                 // tokens a tile
-constexpr int kTcStages = 4;                // even: a ring slot belongs to one group within a segment
-constexpr int kTcThreads = 320;
+constexpr int kTcK = 4, kTcV = 4;           // ring slots: K's in pairs; V's even, so that a slot belongs to
+                                            // one group within a segment
+constexpr int kTcThreads = 352;
 constexpr int kTcRows = 32;                 // rows a row block holds
 constexpr int kTcTile = kTcTok * 128;       // 16 KB: one tile of K or V, q piece, or P
 constexpr int kTcRowCost = 6;               // a row's start and end, in tiles' times
-constexpr float kTcThreshold = 4.f;         // lazy rescaling: weights stay below 2^4
+constexpr float kTcThreshold = 6.f;         // lazy rescaling: weights stay below 2^6
+constexpr float kTcWScale = 4.f;            // and their operand, 2^2 of them, below 2^8
+constexpr float kTcFar = 64.f;              // the denominator's reference may be further off (fp32)
 constexpr uint32_t kTcColS = 0, kTcColO = 256;
 
 struct TcSeg {
@@ -52,12 +61,12 @@ struct TcSeg {
 
 struct TcCtl {
   TcSeg seg[kBaSegs];
-  uint64_t full[kTcStages], empty[kTcStages];
+  uint64_t kfull[kTcK], kempty[kTcK], vfull[kTcV], vempty[kTcV];
   uint64_t segfull[kBaSegs], segempty[kBaSegs];
   uint64_t qfull, sfull[2], sfree[2], pfull[2], pvdone[2];
   uint64_t xch[2], epi, drain;
-  float2 sc[kTcStages][kTcTok / 16];
-  int bad[kTcStages];
+  float2 sc[kTcV][kTcTok / 16];
+  int bad[kTcV];
   float qk[32];                    // what undoes q's scale, times sm_scale log2(e)
   float2 mx[2][2][4][32];          // [group][parity][warp][row]: a tile's maxima of x and x + log2 vs
   float4 stat[2][4][32];           // [group][warp][row]: m, l, n at a segment's end
@@ -67,10 +76,12 @@ struct TcCtl {
   int fail;
 };
 
+// A whole warp waits, bounded; the usual case is one try.
 __device__ __forceinline__ bool tc_wait(TcCtl &ctl, uint64_t *bar, uint32_t parity,
                                         uint32_t *err_word) {
-  bool ok = false;
-  if (!*reinterpret_cast<volatile int *>(&ctl.fail)) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  if (!ok && !*reinterpret_cast<volatile int *>(&ctl.fail)) {
     ok = mbar_wait(bar, parity);
     if (!ok && atomicExch(&ctl.fail, 1) == 0) report(err_word, KVQ_ERRBIT_TIMEOUT);
   }
@@ -88,9 +99,9 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
          (2ull << 61);
 }
 
-// fp32 += e4m3 * e4m3, 128 x 128; transposed: B is MN-major.
-__host__ __device__ constexpr uint32_t tc_idesc(bool transposed) {
-  return (1u << 4) | ((transposed ? 1u : 0u) << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+// fp32 += e4m3 * e4m3, 128 x n; transposed: B is MN-major.
+__host__ __device__ constexpr uint32_t tc_idesc(uint32_t n, bool transposed) {
+  return (1u << 4) | ((transposed ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
@@ -138,8 +149,8 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const float (&v)[32]) {
 __device__ __forceinline__ uint32_t tc_piece(float2 &x, float up) {
   const uint16_t c = f32x2_to_e4m3x2(x.x, x.y);
   const float2 p = f16x2_to_f32x2(e4m3x2_to_f16x2(c));
-  x.x = (x.x - p.x) * up;
-  x.y = (x.y - p.y) * up;
+  // (x - p) up: the products are exact, up being a power of two
+  x = __ffma2_rn(x, make_float2(up, up), __fmul2_rn(p, make_float2(-up, -up)));
   return c;
 }
 
@@ -205,19 +216,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     BaArgs a) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-  uint8_t *kv = smem;                                  // [stage][K, V]
-  uint8_t *qt = kv + kTcStages * 2 * kTcTile;          // [2 pieces]
-  uint8_t *pt = qt + 2 * kTcTile;                      // [group]
+  uint8_t *kt = smem;                       // K tiles
+  uint8_t *vtl = kt + kTcK * kTcTile;       // V tiles
+  uint8_t *qt = vtl + kTcV * kTcTile;       // q, [2 pieces]
+  uint8_t *pt = qt + 2 * kTcTile;           // weights, [group]
   TcCtl &ctl = *reinterpret_cast<TcCtl *>(pt + 2 * kTcTile);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kTcStages; ++i) {
-      mbar_init(&ctl.full[i], 1 + 8);
-      mbar_init(&ctl.empty[i], 1);
+    for (int i = 0; i < kTcK; ++i) {
+      mbar_init(&ctl.kfull[i], 1);
+      mbar_init(&ctl.kempty[i], 1);
+    }
+    for (int i = 0; i < kTcV; ++i) {
+      mbar_init(&ctl.vfull[i], 1 + 8);  // and the scales of its eight blocks
+      mbar_init(&ctl.vempty[i], 1);
     }
     for (int i = 0; i < kBaSegs; ++i) {
       mbar_init(&ctl.segfull[i], 1);
-      mbar_init(&ctl.segempty[i], 9);
+      mbar_init(&ctl.segempty[i], 9);  // the softmax warps and the MMA warp
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&ctl.sfull[g], 1);
@@ -258,16 +274,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int64_t u0 = blockIdx.x * run.per;
   const int64_t u1 = min(u0 + run.per, run.total);
 
-  if (warp == 9) {
-    // ------------------------------------------------------------ producer
+  if (warp >= 9) {
+    // ----------------------------------------------- producers: 9 K, 10 V
+    const int is_v = warp - 9;
+    const CUtensorMap *map = is_v ? &vmap : &kmap;
+    uint64_t *full = is_v ? ctl.vfull : ctl.kfull, *empty = is_v ? ctl.vempty : ctl.kempty;
+    uint8_t *tiles_at = is_v ? vtl : kt;
+    const uint32_t stages = is_v ? kTcV : kTcK;
     const uint64_t once = policy_evict_first();
     uint64_t again;  // the cache is read by several row blocks
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(again));
     int64_t u = u0, in = run.in;
     int b = run.b;
     BaCut cut = {0, 0, 0, 0, 0, {0, 0, 0}};
-    uint32_t g = 0, nseg = 0, par = 1;
-    int slot = 0;
+    uint32_t g = 0, nseg = 0, par = 1, slot = 0;
     bool ok = true;
     int win_b = -1, win = 0, cur = -1, nxt = -1;
     const int32_t *bt = a.block_table;
@@ -297,9 +317,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int64_t c_lo = ut / run.per;
       const int nparts = static_cast<int>((ut + tiles - 1) / run.per - c_lo) + 1;
       const int ss = nseg % kBaSegs;
-      if (nseg >= kBaSegs) ok = tc_wait(ctl, &ctl.segempty[ss], ((nseg / kBaSegs) - 1) & 1, a.err_word);
+      if (!is_v && nseg >= kBaSegs)
+        ok = tc_wait(ctl, &ctl.segempty[ss], ((nseg / kBaSegs) - 1) & 1, a.err_word);
       if (!ok) break;
-      if (lane == 0) {
+      if (!is_v && lane == 0) {
         if (t0 == 0 && nparts > 1) cut = {nparts, head, rb, rq.row, rq.n, {0, 0, 0}};
         ctl.seg[ss] = {b, head, rb, rq.row, rq.n, L, min(rq.n * a.G - rb * kTcRows, kTcRows),
                        t0 * kTcTok, take,
@@ -316,7 +337,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         nxt = bt_load(win + 32 + lane);
       }
       for (int st = 0, tok = t0 * kTcTok; st < take; ++st, tok += kTcTok) {
-        ok = tc_wait(ctl, &ctl.empty[slot], par, a.err_word);
+        ok = tc_wait(ctl, &empty[slot], par, a.err_word);
         if (!ok) break;
         if ((tok >> a.p_shift) >= win + 32) {
           win += 32;
@@ -334,32 +355,48 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int copies = __popc(__ballot_sync(0xffffffffu, good));
         const bool bad = __any_sync(0xffffffffu, needed && !good);
         if (lane == 0) {
-          ctl.bad[slot] = bad;
+          if (is_v) ctl.bad[slot] = bad;
           if (bad) report(a.err_word, KVQ_ERRBIT_PAGE);
-          mbar_arrive_expect_tx(&ctl.full[slot], static_cast<uint32_t>(copies) * 4096u);
+          mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(copies) * 2048u);
         }
         __syncwarp();
-        if (good) {
-          const int y = mine & ((1 << a.p_shift) - 1);
-          uint8_t *dst = kv + slot * 2 * kTcTile + 2048 * lane;
-          tma_load_4d(dst, &kmap, 0, y, head, page, &ctl.full[slot], pol);
-          tma_load_4d(dst + kTcTile, &vmap, 0, y, head, page, &ctl.full[slot], pol);
-          cp_async8(&ctl.sc[slot][lane], a.scales + static_cast<int64_t>(page) * a.Hkv + head);
-          cp_async_arrive(&ctl.full[slot]);
-        } else if (lane < 8) {
-          ctl.sc[slot][lane] = make_float2(1.f, 1.f);  // masked tokens
-          mbar_arrive(&ctl.full[slot]);
+        if (good)
+          tma_load_4d(tiles_at + slot * kTcTile + 2048 * lane, map, 0, mine & ((1 << a.p_shift) - 1), head,
+                      page, &full[slot], pol);
+        if (is_v && lane < 8) {
+          if (good) {
+            cp_async8(&ctl.sc[slot][lane], a.scales + static_cast<int64_t>(page) * a.Hkv + head);
+            cp_async_arrive(&full[slot]);
+          } else {
+            ctl.sc[slot][lane] = make_float2(1.f, 1.f);  // masked tokens
+            mbar_arrive(&full[slot]);
+          }
         }
         ++g;
-        if (++slot == kTcStages) {
+        if (++slot == stages) {
           slot = 0;
           par ^= 1;
         }
         __syncwarp();
       }
+      // K tiles come in pairs: a segment's odd last one leaves its partner's slot
+      // out, completed and emptied with nothing in it
+      if (ok && !is_v && (take & 1)) {
+        ok = tc_wait(ctl, &empty[slot], par, a.err_word);
+        if (ok && lane == 0) {
+          mbar_arrive(&full[slot]);
+          mbar_arrive(&empty[slot]);
+        }
+        __syncwarp();
+        ++g;
+        if (++slot == stages) {
+          slot = 0;
+          par ^= 1;
+        }
+      }
     }
-    if (lane == 0) a.cut[blockIdx.x] = cut;
-    if (ok) {  // nothing more
+    if (!is_v && lane == 0) a.cut[blockIdx.x] = cut;
+    if (ok && !is_v) {  // nothing more
       const int ss = nseg % kBaSegs;
       if (nseg >= kBaSegs) ok = tc_wait(ctl, &ctl.segempty[ss], ((nseg / kBaSegs) - 1) & 1, a.err_word);
       if (ok && lane == 0) {
@@ -368,40 +405,56 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
     if (*reinterpret_cast<volatile int *>(&ctl.fail) && lane == 0)
-      for (uint32_t k = g > kTcStages ? g - kTcStages : 0; k < g; ++k)
-        mbar_wait(&ctl.full[k % kTcStages], (k / kTcStages) & 1);
+      for (uint32_t k = g > stages ? g - stages : 0; k < g; ++k)
+        mbar_wait(&full[k % stages], (k / stages) & 1);
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMA issue
     uint32_t nseg = 0, g0 = 0;
     uint32_t ns[2] = {0, 0}, np[2] = {0, 0};  // S and P tiles so far
+    uint32_t kg = 0;                          // K tiles so far (pairs start at even slots)
     bool ok = true;
-    const uint32_t kv_a = smem_addr(kv), qt_a = smem_addr(qt), pt_a = smem_addr(pt);
-    auto issue_s = [&](int g, int slot) -> bool {
-      if (!tc_wait(ctl, &ctl.sfree[g], (ns[g] & 1) ^ 1, a.err_word)) return false;
-      ++ns[g];
+    const uint32_t k_a = smem_addr(kt), v_a = smem_addr(vtl), q_a = smem_addr(qt), p_a = smem_addr(pt);
+    // scores of one or two tiles, once the groups have taken the last ones
+    auto issue_s = [&](bool two) -> bool {
+      for (int g = 0; g < (two ? 2 : 1); ++g) {
+        const int slot = (kg + g) % kTcK;
+        if (!tc_wait(ctl, &ctl.kfull[slot], ((kg + g) / kTcK) & 1, a.err_word) ||
+            !tc_wait(ctl, &ctl.sfree[g], (ns[g] & 1) ^ 1, a.err_word))
+          return false;
+        ++ns[g];
+      }
       tc_after();
       if (lane == 0) {
-        const uint64_t kd = tc_desc(kv_a + slot * 2 * kTcTile), qd = tc_desc(qt_a);
+        const int slot = kg % kTcK;
+        const uint64_t kd = tc_desc(k_a + slot * kTcTile), qd = tc_desc(q_a);
+        const uint32_t id = two ? tc_idesc(256, false) : tc_idesc(128, false);
 #pragma unroll
         for (int piece = 0; piece < 2; ++piece)
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 32 dims each: 32 bytes within the swizzled rows
-            tc_mma(tmem + kTcColS + 128 * g, qd + piece * (kTcTile >> 4) + 2 * k, kd + 2 * k, tc_idesc(false),
-                   piece + k > 0);
-        tc_commit(&ctl.sfull[g]);
+            tc_mma(tmem + kTcColS, qd + piece * (kTcTile >> 4) + 2 * k, kd + 2 * k, id, piece + k > 0);
+        tc_commit(&ctl.sfull[0]);
+        tc_commit(&ctl.kempty[slot]);
+        if (two) {
+          tc_commit(&ctl.sfull[1]);
+          tc_commit(&ctl.kempty[slot + 1]);
+        }
       }
       __syncwarp();
       return true;
     };
     auto issue_pv = [&](int g, int slot, bool add) {
       if (lane == 0) {
-        const uint64_t vd = tc_desc(kv_a + slot * 2 * kTcTile + kTcTile), pd = tc_desc(pt_a + g * kTcTile);
+        const uint64_t vd = tc_desc(v_a + slot * kTcTile), pd = tc_desc(p_a + g * kTcTile);
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // 32 tokens each: 32 bytes of P's rows, 32 rows of V
-          tc_mma(tmem + kTcColO + 128 * g, pd + 2 * k, vd + k * (32 * 128 >> 4), tc_idesc(true), add || k > 0);
+          tc_mma(tmem + kTcColO + 128 * g, pd + 2 * k, vd + k * (32 * 128 >> 4), tc_idesc(128, true),
+                 add || k > 0);
         tc_commit(&ctl.pvdone[g]);
+        tc_commit(&ctl.vempty[slot]);
       }
+      __syncwarp();
     };
     while (ok) {
       const int ss = nseg % kBaSegs;
@@ -410,21 +463,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const TcSeg sg = ctl.seg[ss];
       if (sg.b < 0) break;
       ok = tc_wait(ctl, &ctl.qfull, nseg & 1, a.err_word);
-      for (int t = 0; ok && t <= sg.tiles; ++t) {
-        if (t < sg.tiles) {
-          const uint32_t gg = g0 + t;
-          const int slot = gg % kTcStages;
-          ok = tc_wait(ctl, &ctl.full[slot], (gg / kTcStages) & 1, a.err_word) && issue_s(t & 1, slot);
+      // Scores run a pair of tiles ahead of values: they are issued as soon as the
+      // groups have taken the last pair's out of TMEM, and are there when those
+      // have done their weights.
+      for (int t = -2; ok && t < sg.tiles; t += 2) {
+        if (t + 2 < sg.tiles) {
+          const bool two = t + 3 < sg.tiles;
+          ok = issue_s(two);
+          kg += 2;  // a single tile takes a pair's slots
         }
-        if (ok && t > 0) {  // P V of the tile before
-          const int tp = t - 1, g = tp & 1, slot = (g0 + tp) % kTcStages;
+        for (int g = 0; ok && g < 2; ++g) {
+          if (t + g < 0 || t + g >= sg.tiles) continue;
+          // (the group's warps have waited for the tile of V)
           ok = tc_wait(ctl, &ctl.pfull[g], np[g]++ & 1, a.err_word);
-          if (ok) {
-            tc_after();
-            issue_pv(g, slot, tp >= 2);
-            if (lane == 0) tc_commit(&ctl.empty[slot]);
-            __syncwarp();
-          }
+          if (!ok) break;
+          tc_after();
+          issue_pv(g, (g0 + t + g) % kTcV, t >= 2);
         }
       }
       g0 += sg.tiles;
@@ -488,10 +542,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bool seg_bad = false, any_tile = false;
       for (int t = grp; t < sg.tiles; t += 2) {
         const uint32_t gg = g0 + t;
-        const int slot = gg % kTcStages;
+        const int slot = gg % kTcV;
         const int tok0 = sg.t_begin + t * kTcTok, tw = tok0 + 32 * quad;  // this warp's tokens
-        ok = tc_wait(ctl, &ctl.full[slot], (gg / kTcStages) & 1, a.err_word) &&
-             tc_wait(ctl, &ctl.sfull[grp], nt & 1, a.err_word);
+        ok = tc_wait(ctl, &ctl.sfull[grp], nt & 1, a.err_word) &&
+             tc_wait(ctl, &ctl.vfull[slot], (gg / kTcV) & 1, a.err_word);
         if (!ok) break;
         seg_bad |= ctl.bad[slot] != 0;
         tc_after();
@@ -532,7 +586,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           mv = fmaxf(mv, o.y);
         }
         // the row's references: the same in all four warps
-        if (mx > m + kTcThreshold) {
+        if (mx > m + kTcFar) {
           l *= exp2f(m - mx);
           m = mx;
         }
@@ -563,8 +617,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float mm = none ? 0.f : m, mn = none ? 0.f : m - n;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          // vs 2^(m - n), times 2^4 (kTcThreshold keeps the weights below 2^8)
-          const float d = vm[h] * 16.f * fast_exp2(fminf(mn + lv[h], 112.f));
+          // vs 2^(m - n), times 2^2 (kTcThreshold keeps the operand below 2^8)
+          const float d = vm[h] * kTcWScale * fast_exp2(fminf(mn + lv[h], 112.f));
           uint32_t w1[4], w2[4], w3[4], w4[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -596,7 +650,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // zeros, and NaN codes of drafted tokens too: a weight of 0 does not stop
           // a NaN.  Rows that see such a token get their NaN when they are written.
           const int tr = 32 * quad + lane, tok = tok0 + tr;
-          uint8_t *vt = kv + slot * 2 * kTcTile + kTcTile;
+          uint8_t *vt = vtl + slot * kTcTile;
           if (tok >= sg.L) {
 #pragma unroll
             for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(tc_chunk(vt, tr, c)) = make_uint4(0, 0, 0, 0);
@@ -661,8 +715,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       float *out = sg.part < 0 ? a.out + ((static_cast<int64_t>(sg.row0) + my_i) * a.Hq + sg.head * a.G +
                                           row - my_i * a.G) * 128
                                : a.part + (static_cast<int64_t>(sg.part) * kTcRows + lane) * (128 + kStat);
-      // out = 2^(N - M - 4) sum / l
-      const float scale = sg.part < 0 ? exp2f(N - M - 4.f) / L1 : 1.f;
+      // out = 2^(N - M - 2) sum / l
+      const float scale = sg.part < 0 ? exp2f(N - M - 2.f) / L1 : 1.f;
       const float down = quad == 0 ? 1.f : quad == 1 ? 1.f / 16 : quad == 2 ? 1.f / 256 : 1.f / 4096;
       for (int c = 0; c < 128; c += 32) {
         // 32 columns of every warp's piece into the P tiles, [warp][row][32]; then
@@ -711,7 +765,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (!ok) break;
       if (used && sg.part >= 0 && warp == 0)
-        *reinterpret_cast<float4 *>(out + 128) = make_float4(M, bad ? -1.f : L1, N + 3.f, 0.f);
+        *reinterpret_cast<float4 *>(out + 128) = make_float4(M, bad ? -1.f : L1, N + 5.f, 0.f);
       ++nseg;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.segempty[ss]);
@@ -726,7 +780,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 inline size_t tc_smem_bytes() {
-  return static_cast<size_t>(kTcStages) * 2 * kTcTile + 4 * kTcTile + sizeof(TcCtl) + 1024;
+  return static_cast<size_t>(kTcK + kTcV + 4) * kTcTile + sizeof(TcCtl) + 1024;
 }
 
 }  // namespace kvq

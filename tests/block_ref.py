@@ -116,7 +116,7 @@ def attend(pools, scales, q, tok_start, seq_lens, table, sm_scale, skip=(), max_
     With head_dim 128 and more than 8 rows (max_q times heads a kv head) both
     operands are sums of e4m3 pieces.  A weight's four pieces, 2^4 apart, leave at
     most 2^-16 of it, and 2^-10 2^-12 where e4m3 is subnormal, on a scale where
-    the operand is w_j s_j 2^(4 - n): 2^-22 2^-4 2 max_i(w_i s_i) = 2^-25
+    the operand is w_j s_j 2^(2 - n): 2^-22 2^-2 2 max_i(w_i s_i) = 2^-23
     max_i(w_i s_i) a token.  q's two pieces, on a scale where a row's largest
     value lies in [224, 448), are exact for values of 2^-2 and more there (8
     significant bits end at 2^-9) and else off by 2^-10: values below 2^-9.8 of the
@@ -157,7 +157,7 @@ def attend(pools, scales, q, tok_start, seq_lens, table, sm_scale, skip=(), max_
                 if D == 128 and max_q * G > 8:
                     top = np.abs(qq).max()
                     score += np.max(ak @ (np.abs(qq) < 2.0 ** -9.8 * top)) * abs(sm_scale) * top * 2.0 ** -17.8
-                    weight, floor = 2.0 ** -16 + 2.0 ** -19, 2.0 ** -25
+                    weight, floor = 2.0 ** -16 + 2.0 ** -19, 2.0 ** -23
                 s = scales[table[b, np.arange(see) // P], g, 1].astype(np.float64)
                 lost = floor * (w * s).max() / den * np.sum(np.abs(v[:see, g]) / s[:, None], 0)
                 rel = 2 * (2 * score + weight + (L / 16 + 64) * 2.0 ** -24)
