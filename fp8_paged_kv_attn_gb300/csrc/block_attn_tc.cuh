@@ -63,14 +63,14 @@ struct TcCtl {
   TcSeg seg[kBaSegs];
   uint64_t kfull[kTcK], kempty[kTcK], vfull[kTcV], vempty[kTcV];
   uint64_t segfull[kBaSegs], segempty[kBaSegs];
-  uint64_t qfull, sfull[2], sfree[2], pfull[2], pvdone[2];
+  uint64_t qfull, qfree, sfull[2], sfree[2], pfull[2], pvdone[2];
   uint64_t xch[2], epi, drain;
   float2 sc[kTcV][kTcTok / 16];
   int bad[kTcV];
-  float qk[32];                    // what undoes q's scale, times sm_scale log2(e)
+  float qk[2][32];                 // [segment & 1]: what undoes q's scale, times sm_scale log2(e)
   float2 mx[2][2][4][32];          // [group][parity][warp][row]: a tile's maxima of x and x + log2 vs
   float4 stat[2][4][32];           // [group][warp][row]: m, l, n at a segment's end
-  int nan_from[128];               // per dim: the first drafted token with a NaN code there
+  int nan_from[2][128];            // [segment & 1], per dim: the first drafted token with a NaN code there
   RunScan<kTcThreads> scan;
   uint32_t tmem;
   int fail;
@@ -154,59 +154,60 @@ __device__ __forceinline__ uint32_t tc_piece(float2 &x, float up) {
   return c;
 }
 
+// Bit 7 of each byte that is a NaN code (0x7F or 0xFF; no carry leaves a byte).
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
 // 16-byte chunk c of row r in a 128-byte-swizzled tile.
 __device__ __forceinline__ uint8_t *tc_chunk(uint8_t *tile, int r, int c) {
   return tile + r * 128 + ((c ^ (r & 7)) * 16);
 }
 
 // q's rows into the two piece tiles, each row at 32 p + r for every p; warp
-// `quad` of four takes eight rows.
+// `warp` of eight takes four rows.
 __device__ __forceinline__ void tc_load_q(const BaArgs &a, const TcSeg &sg, uint8_t *tiles, float *qk,
-                                          int quad, int lane) {
-  const int r = 8 * quad + (lane >> 2), part = lane & 3;  // 32 dims a lane
+                                          int warp, int lane) {
+  const int r = 4 * warp + (lane >> 3), part = lane & 7;  // 16 dims a lane
   const int row = sg.rb * kTcRows + r, i = row / a.G;
-  float x[32];
+  float x[16];
   if (i < sg.n) {
-    const uint16_t *p = a.q + (static_cast<int64_t>(sg.row0) + i) * a.q_stride +
-                        static_cast<int64_t>(sg.head * a.G + row - i * a.G) * 128 + 32 * part;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) unpack8(__ldg(reinterpret_cast<const uint4 *>(p) + c), x + 8 * c);
+    const uint4 *p = reinterpret_cast<const uint4 *>(
+        a.q + (static_cast<int64_t>(sg.row0) + i) * a.q_stride +
+        static_cast<int64_t>(sg.head * a.G + row - i * a.G) * 128 + 16 * part);
+    unpack8(__ldg(p), x);
+    unpack8(__ldg(p + 1), x + 8);
   } else {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) x[c] = 0.f;
+    for (int c = 0; c < 16; ++c) x[c] = 0.f;
   }
   float mx = 0.f;
   bool odd = false;  // inf or NaN: the row's scores are NaN, as inf - inf would make them
 #pragma unroll
-  for (int c = 0; c < 32; ++c) {
+  for (int c = 0; c < 16; ++c) {
     mx = fmaxf(mx, finite_abs(x[c]));
     odd |= !(fabsf(x[c]) < INFINITY);
   }
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   // largest value into [224, 448): block_exponent is the smallest e with mx <= 448 2^e
   const int e = block_exponent(mx);
-  const float up = pow2(-e);
-  const float nan = odd ? NAN : 0.f;
+  const float up = pow2(-e), nan = odd ? NAN : 0.f;
+  uint32_t q1[4], q2[4];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {  // 16 dims: one 16-byte chunk of each piece
-    uint32_t q1[4], q2[4];
+  for (int k = 0; k < 4; ++k) {
+    float2 u = make_float2(x[4 * k] * up + nan, x[4 * k + 1] * up + nan);
+    float2 v = make_float2(x[4 * k + 2] * up + nan, x[4 * k + 3] * up + nan);
+    q1[k] = tc_piece(u, 1.f);
+    q1[k] |= tc_piece(v, 1.f) << 16;
+    q2[k] = tc_piece(u, 1.f);
+    q2[k] |= tc_piece(v, 1.f) << 16;
+  }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float2 u = make_float2(x[16 * c + 4 * k] * up + nan, x[16 * c + 4 * k + 1] * up + nan);
-      float2 v = make_float2(x[16 * c + 4 * k + 2] * up + nan, x[16 * c + 4 * k + 3] * up + nan);
-      q1[k] = tc_piece(u, 1.f);
-      q1[k] |= tc_piece(v, 1.f) << 16;
-      q2[k] = tc_piece(u, 1.f);
-      q2[k] |= tc_piece(v, 1.f) << 16;
-    }
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      *reinterpret_cast<uint4 *>(tc_chunk(tiles, 32 * p + r, 2 * part + c)) =
-          make_uint4(q1[0], q1[1], q1[2], q1[3]);
-      *reinterpret_cast<uint4 *>(tc_chunk(tiles + kTcTile, 32 * p + r, 2 * part + c)) =
-          make_uint4(q2[0], q2[1], q2[2], q2[3]);
-    }
+  for (int p = 0; p < 4; ++p) {
+    *reinterpret_cast<uint4 *>(tc_chunk(tiles, 32 * p + r, part)) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
+    *reinterpret_cast<uint4 *>(tc_chunk(tiles + kTcTile, 32 * p + r, part)) =
+        make_uint4(q2[0], q2[1], q2[2], q2[3]);
   }
   if (part == 0) qk[r] = a.q_scale * pow2(e);
 }
@@ -242,7 +243,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&ctl.pvdone[g], 1);
       mbar_init(&ctl.xch[g], 4);
     }
-    mbar_init(&ctl.qfull, 4);
+    mbar_init(&ctl.qfull, 8);
+    mbar_init(&ctl.qfree, 1);
     mbar_init(&ctl.epi, 8);
     mbar_init(&ctl.drain, 1);
     ctl.fail = 0;
@@ -471,6 +473,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const bool two = t + 3 < sg.tiles;
           ok = issue_s(two);
           kg += 2;  // a single tile takes a pair's slots
+          if (ok && lane == 0 && t + 4 >= sg.tiles) tc_commit(&ctl.qfree);  // q was read
         }
         for (int g = 0; ok && g < 2; ++g) {
           if (t + g < 0 || t + g >= sg.tiles) continue;
@@ -517,27 +520,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (lane == 0) mbar_arrive(&ctl.epi);
       return tc_wait(ctl, &ctl.epi, ne++ & 1, a.err_word);
     };
-    bool ok = true;
+    // Segment k's q, while segment k - 1 still sums its values: its scores are
+    // there when that one has been written.  A wait for the segment's descriptor holds
+    // nothing up that it needs: the copies post it when those before it are issued.
+    auto load_q = [&](uint32_t k) -> bool {
+      const int s = k % kBaSegs;
+      if (!tc_wait(ctl, &ctl.segfull[s], (k / kBaSegs) & 1, a.err_word)) return false;
+      const TcSeg next = ctl.seg[s];
+      if (next.b < 0) return true;
+      if (k > 0 && !tc_wait(ctl, &ctl.qfree, (k - 1) & 1, a.err_word)) return false;
+      if (threadIdx.x < 128) ctl.nan_from[k & 1][threadIdx.x] = INT_MAX;  // last read in segment k - 2
+      tc_load_q(a, next, qt, ctl.qk[k & 1], warp, lane);
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.qfull);
+      return true;
+    };
+    bool ok = load_q(0);
     while (ok) {
       const int ss = nseg % kBaSegs;
-      ok = tc_wait(ctl, &ctl.segfull[ss], (nseg / kBaSegs) & 1, a.err_word);
-      if (!ok) break;
       const TcSeg sg = ctl.seg[ss];
       if (sg.b < 0) break;
       const int row = sg.rb * kTcRows + lane;  // of the request
       const int my_i = row / a.G;
       const int lim = my_i < sg.n ? sg.L - sg.n + 1 + my_i : sg.L;
       const int min_lim = min(sg.L, sg.L - sg.n + 1 + (sg.rb * kTcRows) / a.G);
-      if (grp == 0) {
-        ctl.nan_from[threadIdx.x] = INT_MAX;  // read before the last barrier
-        tc_load_q(a, sg, qt, ctl.qk, quad, lane);
-        proxy_fence();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.qfull);
-      }
       ok = tc_wait(ctl, &ctl.qfull, nseg & 1, a.err_word);
       if (!ok) break;
-      const float qk = ctl.qk[lane];
+      const float qk = ctl.qk[nseg & 1][lane];
+      int *nan_from = ctl.nan_from[nseg & 1];
       float m = -INFINITY, n = -INFINITY, l = 0.f;
       bool seg_bad = false, any_tile = false;
       for (int t = grp; t < sg.tiles; t += 2) {
@@ -655,17 +666,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(tc_chunk(vt, tr, c)) = make_uint4(0, 0, 0, 0);
           } else if (tok >= min_lim) {
+            uint32_t nan = 0;
+#pragma unroll
             for (int c = 0; c < 8; ++c) {
-              uint4 *p = reinterpret_cast<uint4 *>(tc_chunk(vt, tr, c));
-              const uint4 v = *p;
-              if (!(has_nan(v.x) || has_nan(v.y) || has_nan(v.z) || has_nan(v.w))) continue;
-              uint32_t q[4] = {v.x, v.y, v.z, v.w};
-              for (int k = 0; k < 16; ++k)
-                if (((q[k >> 2] >> (8 * (k & 3))) & 0x7Fu) == 0x7Fu) {
-                  q[k >> 2] &= ~(0xFFu << (8 * (k & 3)));
-                  atomicMin(&ctl.nan_from[16 * c + k], tok);
-                }
-              *p = make_uint4(q[0], q[1], q[2], q[3]);
+              const uint4 v = *reinterpret_cast<const uint4 *>(tc_chunk(vt, tr, c));
+              nan |= nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w);
+            }
+            if (nan) {
+              for (int k = 0; k < 128; ++k) {
+                uint8_t *p = tc_chunk(vt, tr, k >> 4) + (k & 15);
+                if ((*p & 0x7F) != 0x7F) continue;
+                *p = 0;
+                atomicMin(&nan_from[k], tok);
+              }
             }
           }
         }
@@ -679,6 +692,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       g0 += sg.tiles;
 
       // ---- the segment's end
+      ok = load_q(nseg + 1);
+      if (!ok) break;
       if (any_tile) {
         ok = tc_wait(ctl, &ctl.pvdone[grp], (nt & 1) ^ 1, a.err_word);
         if (!ok) break;
@@ -754,10 +769,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           acc.w = fmaf(f[s], sum.w, acc.w);
         }
         const int dim = c + 4 * warp;
-        acc.x = ctl.nan_from[dim] < lim ? NAN : acc.x * scale;
-        acc.y = ctl.nan_from[dim + 1] < lim ? NAN : acc.y * scale;
-        acc.z = ctl.nan_from[dim + 2] < lim ? NAN : acc.z * scale;
-        acc.w = ctl.nan_from[dim + 3] < lim ? NAN : acc.w * scale;
+        acc.x = nan_from[dim] < lim ? NAN : acc.x * scale;
+        acc.y = nan_from[dim + 1] < lim ? NAN : acc.y * scale;
+        acc.z = nan_from[dim + 2] < lim ? NAN : acc.z * scale;
+        acc.w = nan_from[dim + 3] < lim ? NAN : acc.w * scale;
         if (bad && sg.part < 0) acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (used) *reinterpret_cast<float4 *>(out + dim) = acc;
         ok = both_sync();  // the tiles are read (and nan_from, at the end)
