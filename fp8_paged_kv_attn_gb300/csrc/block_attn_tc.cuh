@@ -43,7 +43,8 @@ namespace kvq {
 constexpr int kTcTok = 128;                 // tokens a tile
 constexpr int kTcK = 4, kTcV = 4;           // ring slots: K's in pairs; V's even, so that a slot belongs to
                                             // one group within a segment
-constexpr int kTcThreads = 352;
+constexpr int kTcWarps = 16;                // softmax warps, eight a group; then MMAs, K copies, V copies
+constexpr int kTcThreads = 32 * (kTcWarps + 3);
 constexpr int kTcRows = 32;                 // rows a row block holds
 constexpr int kTcTile = kTcTok * 128;       // 16 KB: one tile of K or V, q piece, or P
 constexpr int kTcRowCost = 6;               // a row's start and end, in tiles' times
@@ -59,6 +60,13 @@ struct TcSeg {
   int t_begin, tiles, part;
 };
 
+struct __align__(16) TcRow {  // of a segment that ends: the groups' factors, the row's visible tokens, its place
+  float mine, other, scale;
+  int lim;
+  int64_t at;  // -1: no such row
+  int64_t pad;
+};
+
 struct TcCtl {
   TcSeg seg[kBaSegs];
   uint64_t kfull[kTcK], kempty[kTcK], vfull[kTcV], vempty[kTcV];
@@ -68,8 +76,10 @@ struct TcCtl {
   float2 sc[kTcV][kTcTok / 16];
   int bad[kTcV];
   float qk[2][32];                 // [segment & 1]: what undoes q's scale, times sm_scale log2(e)
-  float2 mx[2][2][4][32];          // [group][parity][warp][row]: a tile's maxima of x and x + log2 vs
-  float4 stat[2][4][32];           // [group][warp][row]: m, l, n at a segment's end
+  float2 mx[2][2][8][32];          // [group][parity][warp][row]: a tile's maxima of x and x + log2 vs
+  __align__(16) float grow[kTcWarps][32];  // [warp][row]: what a rescaling multiplies by
+  __align__(16) TcRow row[kTcWarps][8];                // [warp][row]
+  float4 stat[2][8][32];           // [group][warp][row]: m, l, n at a segment's end
   int nan_from[2][128];            // [segment & 1], per dim: the first drafted token with a NaN code there
   RunScan<kTcThreads> scan;
   uint32_t tmem;
@@ -99,9 +109,18 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
          (2ull << 61);
 }
 
-// fp32 += e4m3 * e4m3, 128 x n; transposed: B is MN-major.
+// One lane of the (whole) warp, always the same.  Under this test the compiler
+// knows that a single thread issues an MMA or a copy; under `lane == 0` it issues them
+// in a loop over lanes (an MMA every 66 cycles at least, 40 here).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
+// fp32 += e4m3 * e4m3, 128 x n; transposed: A is MN-major.
 __host__ __device__ constexpr uint32_t tc_idesc(uint32_t n, bool transposed) {
-  return (1u << 4) | ((transposed ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+  return (1u << 4) | ((transposed ? 1u : 0u) << 15) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
@@ -118,30 +137,25 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
                : "memory");
 }
 
-// 32 consecutive columns of this warp's 32 lanes.
-__device__ __forceinline__ void tc_ld32(float (&v)[32], uint32_t addr) {
+// 16 consecutive columns of this warp's 32 lanes.
+__device__ __forceinline__ void tc_ld16(float (&v)[16], uint32_t addr) {
   uint32_t *r = reinterpret_cast<uint32_t *>(v);
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
+      "[%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void tc_st32(uint32_t addr, const float (&v)[32]) {
+__device__ __forceinline__ void tc_st16(uint32_t addr, const float (&v)[16]) {
   const uint32_t *r = reinterpret_cast<const uint32_t *>(v);
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
-      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
       : "memory");
 }
 
@@ -165,37 +179,36 @@ __device__ __forceinline__ uint8_t *tc_chunk(uint8_t *tile, int r, int c) {
 }
 
 // q's rows into the two piece tiles, each row at 32 p + r for every p; warp
-// `warp` of eight takes four rows.
+// `warp` of sixteen takes two rows.
 __device__ __forceinline__ void tc_load_q(const BaArgs &a, const TcSeg &sg, uint8_t *tiles, float *qk,
                                           int warp, int lane) {
-  const int r = 4 * warp + (lane >> 3), part = lane & 7;  // 16 dims a lane
+  const int r = 2 * warp + (lane >> 4), part = lane & 15;  // 8 dims a lane
   const int row = sg.rb * kTcRows + r, i = row / a.G;
-  float x[16];
+  float x[8];
   if (i < sg.n) {
-    const uint4 *p = reinterpret_cast<const uint4 *>(
-        a.q + (static_cast<int64_t>(sg.row0) + i) * a.q_stride +
-        static_cast<int64_t>(sg.head * a.G + row - i * a.G) * 128 + 16 * part);
-    unpack8(__ldg(p), x);
-    unpack8(__ldg(p + 1), x + 8);
+    unpack8(__ldg(reinterpret_cast<const uint4 *>(
+                a.q + (static_cast<int64_t>(sg.row0) + i) * a.q_stride +
+                static_cast<int64_t>(sg.head * a.G + row - i * a.G) * 128 + 8 * part)),
+            x);
   } else {
 #pragma unroll
-    for (int c = 0; c < 16; ++c) x[c] = 0.f;
+    for (int c = 0; c < 8; ++c) x[c] = 0.f;
   }
   float mx = 0.f;
   bool odd = false;  // inf or NaN: the row's scores are NaN, as inf - inf would make them
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
+  for (int c = 0; c < 8; ++c) {
     mx = fmaxf(mx, finite_abs(x[c]));
     odd |= !(fabsf(x[c]) < INFINITY);
   }
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   // largest value into [224, 448): block_exponent is the smallest e with mx <= 448 2^e
   const int e = block_exponent(mx);
   const float up = pow2(-e), nan = odd ? NAN : 0.f;
-  uint32_t q1[4], q2[4];
+  uint32_t q1[2], q2[2];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < 2; ++k) {
     float2 u = make_float2(x[4 * k] * up + nan, x[4 * k + 1] * up + nan);
     float2 v = make_float2(x[4 * k + 2] * up + nan, x[4 * k + 3] * up + nan);
     q1[k] = tc_piece(u, 1.f);
@@ -205,9 +218,10 @@ __device__ __forceinline__ void tc_load_q(const BaArgs &a, const TcSeg &sg, uint
   }
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
-    *reinterpret_cast<uint4 *>(tc_chunk(tiles, 32 * p + r, part)) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
-    *reinterpret_cast<uint4 *>(tc_chunk(tiles + kTcTile, 32 * p + r, part)) =
-        make_uint4(q2[0], q2[1], q2[2], q2[3]);
+    const int at = 8 * (part & 1);
+    *reinterpret_cast<uint2 *>(tc_chunk(tiles, 32 * p + r, part >> 1) + at) = make_uint2(q1[0], q1[1]);
+    *reinterpret_cast<uint2 *>(tc_chunk(tiles + kTcTile, 32 * p + r, part >> 1) + at) =
+        make_uint2(q2[0], q2[1]);
   }
   if (part == 0) qk[r] = a.q_scale * pow2(e);
 }
@@ -234,25 +248,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < kBaSegs; ++i) {
       mbar_init(&ctl.segfull[i], 1);
-      mbar_init(&ctl.segempty[i], 9);  // the softmax warps and the MMA warp
+      mbar_init(&ctl.segempty[i], kTcWarps + 1);  // the softmax warps and the MMA warp
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&ctl.sfull[g], 1);
-      mbar_init(&ctl.sfree[g], 4);
-      mbar_init(&ctl.pfull[g], 4);
+      mbar_init(&ctl.sfree[g], 8);
+      mbar_init(&ctl.pfull[g], 8);
       mbar_init(&ctl.pvdone[g], 1);
-      mbar_init(&ctl.xch[g], 4);
+      mbar_init(&ctl.xch[g], 8);
     }
-    mbar_init(&ctl.qfull, 8);
+    mbar_init(&ctl.qfull, kTcWarps);
     mbar_init(&ctl.qfree, 1);
-    mbar_init(&ctl.epi, 8);
+    mbar_init(&ctl.epi, kTcWarps);
     mbar_init(&ctl.drain, 1);
     ctl.fail = 0;
     fence_barrier_init();
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
   }
-  if (warp == 8) {
+  if (warp == kTcWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_addr(&ctl.tmem))
                  : "memory");
@@ -276,9 +290,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int64_t u0 = blockIdx.x * run.per;
   const int64_t u1 = min(u0 + run.per, run.total);
 
-  if (warp >= 9) {
-    // ----------------------------------------------- producers: 9 K, 10 V
-    const int is_v = warp - 9;
+  if (warp > kTcWarps) {
+    // ----------------------------------------------- producers: K, then V
+    const int is_v = warp - kTcWarps - 1;
     const CUtensorMap *map = is_v ? &vmap : &kmap;
     uint64_t *full = is_v ? ctl.vfull : ctl.kfull, *empty = is_v ? ctl.vempty : ctl.kempty;
     uint8_t *tiles_at = is_v ? vtl : kt;
@@ -354,17 +368,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int page = idx < 32 ? from_cur : from_nxt;
         const bool needed = lane < 8 && mine < L;
         const bool good = needed && page >= 0 && page < a.num_pages;
-        const int copies = __popc(__ballot_sync(0xffffffffu, good));
+        const uint32_t goods = __ballot_sync(0xffffffffu, good);
         const bool bad = __any_sync(0xffffffffu, needed && !good);
         if (lane == 0) {
           if (is_v) ctl.bad[slot] = bad;
           if (bad) report(a.err_word, KVQ_ERRBIT_PAGE);
-          mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(copies) * 2048u);
+          mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(__popc(goods)) * 2048u);
         }
         __syncwarp();
-        if (good)
-          tma_load_4d(tiles_at + slot * kTcTile + 2048 * lane, map, 0, mine & ((1 << a.p_shift) - 1), head,
-                      page, &full[slot], pol);
+        int pages[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) pages[j] = __shfl_sync(0xffffffffu, page, j);
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (goods >> j & 1)
+              tma_load_4d(tiles_at + slot * kTcTile + 2048 * j, map, 0,
+                          (tok + 16 * j) & ((1 << a.p_shift) - 1), head, pages[j], &full[slot], pol);
+        }
+        __syncwarp();
         if (is_v && lane < 8) {
           if (good) {
             cp_async8(&ctl.sc[slot][lane], a.scales + static_cast<int64_t>(page) * a.Hkv + head);
@@ -381,21 +403,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         __syncwarp();
       }
-      // K tiles come in pairs: a segment's odd last one leaves its partner's slot
-      // out, completed and emptied with nothing in it
-      if (ok && !is_v && (take & 1)) {
-        ok = tc_wait(ctl, &empty[slot], par, a.err_word);
-        if (ok && lane == 0) {
-          mbar_arrive(&full[slot]);
-          mbar_arrive(&empty[slot]);
-        }
-        __syncwarp();
-        ++g;
-        if (++slot == stages) {
-          slot = 0;
-          par ^= 1;
-        }
-      }
     }
     if (!is_v && lane == 0) a.cut[blockIdx.x] = cut;
     if (ok && !is_v) {  // nothing more
@@ -410,48 +417,42 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (uint32_t k = g > stages ? g - stages : 0; k < g; ++k)
         mbar_wait(&full[k % stages], (k / stages) & 1);
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 8) {
+  } else if (warp == kTcWarps) {
     // ------------------------------------------------------------ MMA issue
     uint32_t nseg = 0, g0 = 0;
     uint32_t ns[2] = {0, 0}, np[2] = {0, 0};  // S and P tiles so far
-    uint32_t kg = 0;                          // K tiles so far (pairs start at even slots)
+    uint32_t kg = 0;                          // K tiles so far
     bool ok = true;
     const uint32_t k_a = smem_addr(kt), v_a = smem_addr(vtl), q_a = smem_addr(qt), p_a = smem_addr(pt);
-    // scores of one or two tiles, once the groups have taken the last ones
-    auto issue_s = [&](bool two) -> bool {
-      for (int g = 0; g < (two ? 2 : 1); ++g) {
-        const int slot = (kg + g) % kTcK;
-        if (!tc_wait(ctl, &ctl.kfull[slot], ((kg + g) / kTcK) & 1, a.err_word) ||
-            !tc_wait(ctl, &ctl.sfree[g], (ns[g] & 1) ^ 1, a.err_word))
-          return false;
-        ++ns[g];
-      }
+    // a tile's scores, once its group has taken its last ones out of TMEM
+    auto issue_s = [&](int g, bool last) -> bool {
+      const int slot = kg % kTcK;
+      if (!tc_wait(ctl, &ctl.kfull[slot], (kg / kTcK) & 1, a.err_word) ||
+          !tc_wait(ctl, &ctl.sfree[g], (ns[g]++ & 1) ^ 1, a.err_word))
+        return false;
+      ++kg;
       tc_after();
-      if (lane == 0) {
-        const int slot = kg % kTcK;
+      if (elect_one()) {
         const uint64_t kd = tc_desc(k_a + slot * kTcTile), qd = tc_desc(q_a);
-        const uint32_t id = two ? tc_idesc(256, false) : tc_idesc(128, false);
 #pragma unroll
         for (int piece = 0; piece < 2; ++piece)
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 32 dims each: 32 bytes within the swizzled rows
-            tc_mma(tmem + kTcColS, qd + piece * (kTcTile >> 4) + 2 * k, kd + 2 * k, id, piece + k > 0);
-        tc_commit(&ctl.sfull[0]);
+            tc_mma(tmem + kTcColS + 128 * g, qd + piece * (kTcTile >> 4) + 2 * k, kd + 2 * k,
+                   tc_idesc(128, false), piece + k > 0);
+        tc_commit(&ctl.sfull[g]);
         tc_commit(&ctl.kempty[slot]);
-        if (two) {
-          tc_commit(&ctl.sfull[1]);
-          tc_commit(&ctl.kempty[slot + 1]);
-        }
+        if (last) tc_commit(&ctl.qfree);
       }
       __syncwarp();
       return true;
     };
     auto issue_pv = [&](int g, int slot, bool add) {
-      if (lane == 0) {
+      if (elect_one()) {
         const uint64_t vd = tc_desc(v_a + slot * kTcTile), pd = tc_desc(p_a + g * kTcTile);
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // 32 tokens each: 32 bytes of P's rows, 32 rows of V
-          tc_mma(tmem + kTcColO + 128 * g, pd + 2 * k, vd + k * (32 * 128 >> 4), tc_idesc(128, true),
+          tc_mma(tmem + kTcColO + 128 * g, vd + k * (32 * 128 >> 4), pd + 2 * k, tc_idesc(128, true),
                  add || k > 0);
         tc_commit(&ctl.pvdone[g]);
         tc_commit(&ctl.vempty[slot]);
@@ -465,24 +466,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const TcSeg sg = ctl.seg[ss];
       if (sg.b < 0) break;
       ok = tc_wait(ctl, &ctl.qfull, nseg & 1, a.err_word);
-      // Scores run a pair of tiles ahead of values: they are issued as soon as the
-      // groups have taken the last pair's out of TMEM, and are there when those
-      // have done their weights.
-      for (int t = -2; ok && t < sg.tiles; t += 2) {
-        if (t + 2 < sg.tiles) {
-          const bool two = t + 3 < sg.tiles;
-          ok = issue_s(two);
-          kg += 2;  // a single tile takes a pair's slots
-          if (ok && lane == 0 && t + 4 >= sg.tiles) tc_commit(&ctl.qfree);  // q was read
-        }
-        for (int g = 0; ok && g < 2; ++g) {
-          if (t + g < 0 || t + g >= sg.tiles) continue;
-          // (the group's warps have waited for the tile of V)
-          ok = tc_wait(ctl, &ctl.pfull[g], np[g]++ & 1, a.err_word);
-          if (!ok) break;
-          tc_after();
-          issue_pv(g, (g0 + t + g) % kTcV, t >= 2);
-        }
+      // A tile's scores are issued when its group has taken those of two tiles before
+      // out of TMEM, and are there when it has done that tile's weights.  The groups
+      // are half a tile's time apart, so that the order of their waits is this one's.
+      for (int t = -2; ok && t <= sg.tiles; ++t) {
+        if (t + 2 < sg.tiles) ok = issue_s(t & 1, t + 3 == sg.tiles);
+        const int u = t - 1;
+        if (!ok || u < 0 || u >= sg.tiles) continue;
+        // (the group's warps have waited for the tile of V)
+        const int g = u & 1;
+        ok = tc_wait(ctl, &ctl.pfull[g], np[g]++ & 1, a.err_word);
+        if (!ok) break;
+        tc_after();
+        issue_pv(g, (g0 + u) % kTcV, u >= 2);
       }
       g0 += sg.tiles;
       ++nseg;
@@ -491,7 +487,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     if (*reinterpret_cast<volatile int *>(&ctl.fail)) {
       // the products in flight end before the CTA's memory goes to another one
-      if (lane == 0) tc_commit(&ctl.drain);
+      if (elect_one()) tc_commit(&ctl.drain);
       mbar_wait(&ctl.drain, 0);
     }
   } else {
@@ -503,14 +499,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (live || r.n == 0) continue;
       float4 *o = reinterpret_cast<float4 *>(a.out + static_cast<int64_t>(r.row) * a.Hq * 128);
       const int64_t n4 = static_cast<int64_t>(r.n) * a.Hq * 32;
-      for (int64_t k = threadIdx.x; k < n4; k += 256) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int64_t k = threadIdx.x; k < n4; k += 32 * kTcWarps) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const int grp = warp >> 2, quad = warp & 3;
+    // group, TMEM lanes, and half of the lanes' 32 tokens
+    const int grp = warp >> 3, quad = warp & 3, half = (warp >> 2) & 1, gw = 2 * quad + half;
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-    const uint32_t s_addr = tmem + lanes + kTcColS + 128 * grp, o_addr = tmem + lanes + kTcColO + 128 * grp;
+    const uint32_t s_addr = tmem + lanes + kTcColS + 128 * grp + 16 * gw;
+    const uint32_t o_addr = tmem + lanes + kTcColO + 128 * grp;
     uint8_t *ptile = pt + grp * kTcTile;
     uint32_t nseg = 0, g0 = 0, nt = 0, nx = 0, ne = 0;
-    auto group_sync = [&]() -> bool {  // the group's four warps
+    auto group_sync = [&]() -> bool {  // the group's eight warps
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.xch[grp]);
       return tc_wait(ctl, &ctl.xch[grp], nx++ & 1, a.err_word);
@@ -554,49 +552,42 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int t = grp; t < sg.tiles; t += 2) {
         const uint32_t gg = g0 + t;
         const int slot = gg % kTcV;
-        const int tok0 = sg.t_begin + t * kTcTok, tw = tok0 + 32 * quad;  // this warp's tokens
+        const int tok0 = sg.t_begin + t * kTcTok, tw = tok0 + 16 * gw;  // this warp's tokens: one block
         ok = tc_wait(ctl, &ctl.sfull[grp], nt & 1, a.err_word) &&
              tc_wait(ctl, &ctl.vfull[slot], (gg / kTcV) & 1, a.err_word);
         if (!ok) break;
         seg_bad |= ctl.bad[slot] != 0;
         tc_after();
-        float x[32];
-        tc_ld32(x, s_addr + 32 * quad);
+        float x[16];
+        tc_ld16(x, s_addr);
         tc_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.sfree[grp]);
         const bool partial = tok0 + kTcTok > min_lim;
-        float lv[2], vm[2], mx = -INFINITY, mv = -INFINITY;
+        const float2 sc = ctl.sc[slot][gw];
+        const uint32_t ub = __float_as_uint(sc.y);
+        const int e = static_cast<int>(ub >> 23) - 127 + ((ub & 0x7FFFFFu) ? 1 : 0);
+        const float lv = static_cast<float>(e), vm = sc.y * pow2(max(-126, min(127, -e))), f = qk * sc.x;
+        float mx = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // 16 tokens of one block
-          const float2 sc = ctl.sc[slot][2 * quad + h];
-          const uint32_t ub = __float_as_uint(sc.y);
-          const int e = static_cast<int>(ub >> 23) - 127 + ((ub & 0x7FFFFFu) ? 1 : 0);
-          lv[h] = static_cast<float>(e);
-          vm[h] = sc.y * pow2(max(-126, min(127, -e)));
-          const float f = qk * sc.x;
-          float mt = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            float y = x[16 * h + c] * f;
-            if (partial && tw + 16 * h + c >= lim) y = -INFINITY;
-            x[16 * h + c] = y;
-            mt = fmaxf(mt, y);
-          }
-          mx = fmaxf(mx, mt);
-          mv = fmaxf(mv, mt + lv[h]);
+        for (int c = 0; c < 16; ++c) {
+          float y = x[c] * f;
+          if (partial && tw + c >= lim) y = -INFINITY;
+          x[c] = y;
+          mx = fmaxf(mx, y);
         }
+        float mv = mx + lv;
         float2(*xm)[32] = ctl.mx[grp][nt & 1];
-        xm[quad][lane] = make_float2(mx, mv);
+        xm[gw][lane] = make_float2(mx, mv);
         ok = group_sync();
         if (!ok) break;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < 8; ++w) {
           const float2 o = xm[w][lane];
           mx = fmaxf(mx, o.x);
           mv = fmaxf(mv, o.y);
         }
-        // the row's references: the same in all four warps
+        // the row's references: the same in all of the group's warps
         if (mx > m + kTcFar) {
           l *= exp2f(m - mx);
           m = mx;
@@ -611,51 +602,57 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           ok = tc_wait(ctl, &ctl.pvdone[grp], (nt & 1) ^ 1, a.err_word);
           if (!ok) break;
           if (__any_sync(0xffffffffu, fo != 1.f)) {
+            float *grow = ctl.grow[warp];
+            grow[lane] = fo;
+            __syncwarp();
             tc_after();
+#pragma unroll 1
+            for (int c = 64 * half; c < 64 * half + 64; c += 16) {  // 16 rows of a piece
+              float o[16];
+              tc_ld16(o, o_addr + c);
 #pragma unroll
-            for (int c = 0; c < 128; c += 32) {
-              float o[32];
-              tc_ld32(o, o_addr + c);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= fo;
-              tc_st32(o_addr + c, o);
+              for (int k = 0; k < 16; k += 4) {
+                const float4 g = *reinterpret_cast<const float4 *>(grow + (c & 16) + k);
+                o[k] *= g.x;
+                o[k + 1] *= g.y;
+                o[k + 2] *= g.z;
+                o[k + 3] *= g.w;
+              }
+              tc_st16(o_addr + c, o);
             }
+            __syncwarp();
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           }
         }
         any_tile = true;
         const bool none = n == -INFINITY;  // nothing seen yet: every x is -inf
         const float mm = none ? 0.f : m, mn = none ? 0.f : m - n;
+        // vs 2^(m - n), times 2^2 (kTcThreshold keeps the operand below 2^8)
+        const float d = vm * kTcWScale * fast_exp2(fminf(mn + lv, 112.f));
+        uint32_t w1[4], w2[4], w3[4], w4[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // vs 2^(m - n), times 2^2 (kTcThreshold keeps the operand below 2^8)
-          const float d = vm[h] * kTcWScale * fast_exp2(fminf(mn + lv[h], 112.f));
-          uint32_t w1[4], w2[4], w3[4], w4[4];
+        for (int k = 0; k < 4; ++k) {
+          uint32_t c1 = 0, c2 = 0, c3 = 0, c4 = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t c1 = 0, c2 = 0, c3 = 0, c4 = 0;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int c = 16 * h + 4 * k + 2 * j;
-              const float e0 = fast_exp2(x[c] - mm), e1 = fast_exp2(x[c + 1] - mm);
-              l += e0 + e1;
-              float2 w = make_float2(e0 * d, e1 * d);
-              c1 |= tc_piece(w, 16.f) << (16 * j);
-              c2 |= tc_piece(w, 16.f) << (16 * j);
-              c3 |= tc_piece(w, 16.f) << (16 * j);
-              c4 |= static_cast<uint32_t>(f32x2_to_e4m3x2(w.x, w.y)) << (16 * j);
-            }
-            w1[k] = c1;
-            w2[k] = c2;
-            w3[k] = c3;
-            w4[k] = c4;
+          for (int j = 0; j < 2; ++j) {
+            const int c = 4 * k + 2 * j;
+            const float e0 = fast_exp2(x[c] - mm), e1 = fast_exp2(x[c + 1] - mm);
+            l += e0 + e1;
+            float2 w = make_float2(e0 * d, e1 * d);
+            c1 |= tc_piece(w, 16.f) << (16 * j);
+            c2 |= tc_piece(w, 16.f) << (16 * j);
+            c3 |= tc_piece(w, 16.f) << (16 * j);
+            c4 |= static_cast<uint32_t>(f32x2_to_e4m3x2(w.x, w.y)) << (16 * j);
           }
-          const int ch = 2 * quad + h;
-          *reinterpret_cast<uint4 *>(tc_chunk(ptile, lane, ch)) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-          *reinterpret_cast<uint4 *>(tc_chunk(ptile, 32 + lane, ch)) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
-          *reinterpret_cast<uint4 *>(tc_chunk(ptile, 64 + lane, ch)) = make_uint4(w3[0], w3[1], w3[2], w3[3]);
-          *reinterpret_cast<uint4 *>(tc_chunk(ptile, 96 + lane, ch)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          w1[k] = c1;
+          w2[k] = c2;
+          w3[k] = c3;
+          w4[k] = c4;
         }
+        *reinterpret_cast<uint4 *>(tc_chunk(ptile, lane, gw)) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+        *reinterpret_cast<uint4 *>(tc_chunk(ptile, 32 + lane, gw)) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+        *reinterpret_cast<uint4 *>(tc_chunk(ptile, 64 + lane, gw)) = make_uint4(w3[0], w3[1], w3[2], w3[3]);
+        *reinterpret_cast<uint4 *>(tc_chunk(ptile, 96 + lane, gw)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
         if (partial) {
           // V rows past the end (whatever the slot or the cache holds) become
           // zeros, and NaN codes of drafted tokens too: a weight of 0 does not stop
@@ -664,16 +661,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           uint8_t *vt = vtl + slot * kTcTile;
           if (tok >= sg.L) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(tc_chunk(vt, tr, c)) = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<uint4 *>(tc_chunk(vt, tr, 4 * half + c)) = make_uint4(0, 0, 0, 0);
           } else if (tok >= min_lim) {
             uint32_t nan = 0;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const uint4 v = *reinterpret_cast<const uint4 *>(tc_chunk(vt, tr, c));
+            for (int c = 0; c < 4; ++c) {
+              const uint4 v = *reinterpret_cast<const uint4 *>(tc_chunk(vt, tr, 4 * half + c));
               nan |= nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w);
             }
             if (nan) {
-              for (int k = 0; k < 128; ++k) {
+              for (int k = 64 * half; k < 64 * half + 64; ++k) {
                 uint8_t *p = tc_chunk(vt, tr, k >> 4) + (k & 15);
                 if ((*p & 0x7F) != 0x7F) continue;
                 *p = 0;
@@ -699,7 +697,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok) break;
         tc_after();
       }
-      ctl.stat[grp][quad][lane] = make_float4(m, seg_bad ? -1.f : l, n, 0.f);
+      // this thread's dim (32 quad + lane) of 16 rows: the pieces' sum, smallest first
+      float sum[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) sum[k] = 0.f;
+      if (any_tile) {
+#pragma unroll
+        for (int p = 3; p >= 0; --p) {
+          float o[16];
+          tc_ld16(o, o_addr + 32 * p + 16 * half);
+          const float down = p == 0 ? 1.f : p == 1 ? 1.f / 16 : p == 2 ? 1.f / 256 : 1.f / 4096;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) sum[k] = fmaf(o[k], down, sum[k]);
+        }
+      }
+      // group 0 writes the first eight of them and group 1 the others; each hands the
+      // other its sums of those, [half][row][dim], in its own (free) weight tile
+      const int dim = 32 * quad + lane;
+      float *give = reinterpret_cast<float *>(ptile) + 1024 * half + dim;
+      const float *take = reinterpret_cast<const float *>(pt + (grp ^ 1) * kTcTile) + 1024 * half + dim;
+      if (grp == 0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) give[128 * k] = sum[8 + k];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          give[128 * k] = sum[k];
+          sum[k] = sum[8 + k];
+        }
+      }
+      ctl.stat[grp][gw][lane] = make_float4(m, seg_bad ? -1.f : l, n, 0.f);
       ok = both_sync();
       if (!ok) break;
       float M = -INFINITY, N = -INFINITY, L1 = 0.f, gm[2], gn[2], gl[2], f[2];
@@ -708,7 +735,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int k = 0; k < 2; ++k) {
         gl[k] = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < 8; ++w) {
           const float4 v = ctl.stat[k][w][lane];
           bad |= v.y < 0.f;
           gl[k] += v.y;
@@ -727,60 +754,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       const bool used = lane < sg.rows;
       // a partial's row: sums, then m, l, n (n counts the 2^7 of the other kernel)
-      float *out = sg.part < 0 ? a.out + ((static_cast<int64_t>(sg.row0) + my_i) * a.Hq + sg.head * a.G +
-                                          row - my_i * a.G) * 128
-                               : a.part + (static_cast<int64_t>(sg.part) * kTcRows + lane) * (128 + kStat);
-      // out = 2^(N - M - 2) sum / l
-      const float scale = sg.part < 0 ? exp2f(N - M - 2.f) / L1 : 1.f;
-      const float down = quad == 0 ? 1.f : quad == 1 ? 1.f / 16 : quad == 2 ? 1.f / 256 : 1.f / 4096;
-      for (int c = 0; c < 128; c += 32) {
-        // 32 columns of every warp's piece into the P tiles, [warp][row][32]; then
-        // each of the eight warps sums four columns
-        float o[32];
-        if (any_tile) {
-          tc_ld32(o, o_addr + c);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<float4 *>(tc_chunk(ptile + quad * 4096, lane, k)) =
-              make_float4(o[4 * k] * down, o[4 * k + 1] * down, o[4 * k + 2] * down, o[4 * k + 3] * down);
-        ok = both_sync();
-        if (!ok) break;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (gl[s] == 0.f) continue;
-          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int p = 3; p >= 0; --p) {  // the smallest pieces first
-            const float4 v =
-                *reinterpret_cast<const float4 *>(tc_chunk(pt + s * kTcTile + p * 4096, lane, warp));
-            sum.x += v.x;
-            sum.y += v.y;
-            sum.z += v.z;
-            sum.w += v.w;
-          }
-          acc.x = fmaf(f[s], sum.x, acc.x);
-          acc.y = fmaf(f[s], sum.y, acc.y);
-          acc.z = fmaf(f[s], sum.z, acc.z);
-          acc.w = fmaf(f[s], sum.w, acc.w);
-        }
-        const int dim = c + 4 * warp;
-        acc.x = nan_from[dim] < lim ? NAN : acc.x * scale;
-        acc.y = nan_from[dim + 1] < lim ? NAN : acc.y * scale;
-        acc.z = nan_from[dim + 2] < lim ? NAN : acc.z * scale;
-        acc.w = nan_from[dim + 3] < lim ? NAN : acc.w * scale;
-        if (bad && sg.part < 0) acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (used) *reinterpret_cast<float4 *>(out + dim) = acc;
-        ok = both_sync();  // the tiles are read (and nan_from, at the end)
-        if (!ok) break;
+      const int64_t at = sg.part < 0 ? ((static_cast<int64_t>(sg.row0) + my_i) * a.Hq + sg.head * a.G + row -
+                                        my_i * a.G) * 128
+                                     : (static_cast<int64_t>(sg.part) * kTcRows + lane) * (128 + kStat);
+      float *out = sg.part < 0 ? a.out : a.part;
+      {
+        // out = 2^(N - M - 2) sum / l; zeros where a page was bad
+        const float scale = sg.part < 0 ? exp2f(N - M - 2.f) / L1 : 1.f;
+        const bool zero = bad && sg.part < 0;
+        TcRow w;
+        w.mine = zero ? 0.f : f[grp];
+        w.other = zero ? 0.f : f[grp ^ 1];
+        w.scale = zero ? 0.f : scale;
+        w.lim = zero ? INT_MIN : lim;
+        w.at = used ? at : -1;
+        const int k = lane - 16 * half - 8 * grp;
+        if (k >= 0 && k < 8) ctl.row[warp][k] = w;
       }
+      __syncwarp();
+      const int nan_at = nan_from[dim];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const TcRow w = ctl.row[warp][k];
+        const float other = take[128 * k];
+        float acc = 0.f;
+        if (w.mine != 0.f) acc = w.mine * sum[k];
+        if (w.other != 0.f) acc = fmaf(w.other, other, acc);
+        acc = nan_at < w.lim ? NAN : acc * w.scale;
+        if (w.at >= 0) out[w.at + dim] = acc;
+      }
+      ok = both_sync();  // the tiles and nan_from are read
       if (!ok) break;
       if (used && sg.part >= 0 && warp == 0)
-        *reinterpret_cast<float4 *>(out + 128) = make_float4(M, bad ? -1.f : L1, N + 5.f, 0.f);
+        *reinterpret_cast<float4 *>(out + at + 128) = make_float4(M, bad ? -1.f : L1, N + 5.f, 0.f);
       ++nseg;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.segempty[ss]);
@@ -788,7 +794,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_before();
   }
   __syncthreads();  // every role comes here, also when a wait gave up
-  if (warp == 8) {
+  if (warp == kTcWarps) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
