@@ -137,7 +137,7 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
                : "memory");
 }
 
-// 16 consecutive columns of this warp's 32 lanes.
+// Consecutive columns of this warp's 32 lanes.
 __device__ __forceinline__ void tc_ld16(float (&v)[16], uint32_t addr) {
   uint32_t *r = reinterpret_cast<uint32_t *>(v);
   asm volatile(
@@ -159,13 +159,42 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const float (&v)[16]) {
       : "memory");
 }
 
-// One e4m3 piece of two values and what is left of them, times `up`.
-__device__ __forceinline__ uint32_t tc_piece(float2 &x, float up) {
+// One e4m3 piece of two values, and what is left of them (exact).
+__device__ __forceinline__ uint32_t tc_piece(float2 &x) {
   const uint16_t c = f32x2_to_e4m3x2(x.x, x.y);
   const float2 p = f16x2_to_f32x2(e4m3x2_to_f16x2(c));
-  // (x - p) up: the products are exact, up being a power of two
-  x = __ffma2_rn(x, make_float2(up, up), __fmul2_rn(p, make_float2(-up, -up)));
+  x = make_float2(x.x - p.x, x.y - p.y);
   return c;
+}
+
+// e4m3 codes of two f16 values.
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(__half2 x) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(*reinterpret_cast<uint32_t *>(&x)));
+  return c;
+}
+
+// One piece of two f16 values, and 16 times what is left of them (exact: at most the
+// value's lower seven bits).
+__device__ __forceinline__ uint32_t tc_piece16(__half2 &x) {
+  const uint32_t c = f16x2_to_e4m3x2(x), p = e4m3x2_to_f16x2(static_cast<uint16_t>(c));
+  x = __hfma2(*reinterpret_cast<const __half2 *>(&p), __float2half2_rn(-16.f),
+              __hmul2(x, __float2half2_rn(16.f)));
+  return c;
+}
+
+// Two weights' four pieces, 16 apart: their f16 roundings carry the first two, what
+// those leave of them joins with two pieces to go, on the f16's last bits (2^-19 of
+// the weight).  In fp32 throughout each piece's way back costs two more conversions.
+__device__ __forceinline__ void tc_pieces(float2 w, int shift, uint32_t &c1, uint32_t &c2, uint32_t &c3,
+                                          uint32_t &c4) {
+  __half2 x = __float22half2_rn(w);
+  const __half2 lo = __float22half2_rn(__ffma2_rn(__half22float2(x), make_float2(-1.f, -1.f), w));
+  c1 |= tc_piece16(x) << shift;
+  c2 |= tc_piece16(x) << shift;
+  x = __hfma2(lo, __float2half2_rn(256.f), x);
+  c3 |= tc_piece16(x) << shift;
+  c4 |= f16x2_to_e4m3x2(x) << shift;
 }
 
 // Bit 7 of each byte that is a NaN code (0x7F or 0xFF; no carry leaves a byte).
@@ -211,10 +240,10 @@ __device__ __forceinline__ void tc_load_q(const BaArgs &a, const TcSeg &sg, uint
   for (int k = 0; k < 2; ++k) {
     float2 u = make_float2(x[4 * k] * up + nan, x[4 * k + 1] * up + nan);
     float2 v = make_float2(x[4 * k + 2] * up + nan, x[4 * k + 3] * up + nan);
-    q1[k] = tc_piece(u, 1.f);
-    q1[k] |= tc_piece(v, 1.f) << 16;
-    q2[k] = tc_piece(u, 1.f);
-    q2[k] |= tc_piece(v, 1.f) << 16;
+    q1[k] = tc_piece(u);
+    q1[k] |= tc_piece(v) << 16;
+    q2[k] = tc_piece(u);
+    q2[k] |= tc_piece(v) << 16;
   }
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
@@ -566,8 +595,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const bool partial = tok0 + kTcTok > min_lim;
         const float2 sc = ctl.sc[slot][gw];
         const uint32_t ub = __float_as_uint(sc.y);
-        const int e = static_cast<int>(ub >> 23) - 127 + ((ub & 0x7FFFFFu) ? 1 : 0);
-        const float lv = static_cast<float>(e), vm = sc.y * pow2(max(-126, min(127, -e))), f = qk * sc.x;
+        const int e_v = static_cast<int>(ub >> 23) - 127 + ((ub & 0x7FFFFFu) ? 1 : 0);
+        const float lv = static_cast<float>(e_v), vm = sc.y * pow2(max(-126, min(127, -e_v))), f = qk * sc.x;
         float mx = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
@@ -629,6 +658,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float mm = none ? 0.f : m, mn = none ? 0.f : m - n;
         // vs 2^(m - n), times 2^2 (kTcThreshold keeps the operand below 2^8)
         const float d = vm * kTcWScale * fast_exp2(fminf(mn + lv, 112.f));
+        float2 l2 = make_float2(0.f, 0.f);
         uint32_t w1[4], w2[4], w3[4], w4[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -636,19 +666,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int c = 4 * k + 2 * j;
-            const float e0 = fast_exp2(x[c] - mm), e1 = fast_exp2(x[c + 1] - mm);
-            l += e0 + e1;
-            float2 w = make_float2(e0 * d, e1 * d);
-            c1 |= tc_piece(w, 16.f) << (16 * j);
-            c2 |= tc_piece(w, 16.f) << (16 * j);
-            c3 |= tc_piece(w, 16.f) << (16 * j);
-            c4 |= static_cast<uint32_t>(f32x2_to_e4m3x2(w.x, w.y)) << (16 * j);
+            const float2 y = __fadd2_rn(make_float2(x[c], x[c + 1]), make_float2(-mm, -mm));
+            const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            l2 = __fadd2_rn(l2, e);
+            tc_pieces(__fmul2_rn(e, make_float2(d, d)), 16 * j, c1, c2, c3, c4);
           }
           w1[k] = c1;
           w2[k] = c2;
           w3[k] = c3;
           w4[k] = c4;
         }
+        l += l2.x + l2.y;
         *reinterpret_cast<uint4 *>(tc_chunk(ptile, lane, gw)) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
         *reinterpret_cast<uint4 *>(tc_chunk(ptile, 32 + lane, gw)) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
         *reinterpret_cast<uint4 *>(tc_chunk(ptile, 64 + lane, gw)) = make_uint4(w3[0], w3[1], w3[2], w3[3]);

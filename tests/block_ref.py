@@ -157,7 +157,7 @@ def attend(pools, scales, q, tok_start, seq_lens, table, sm_scale, skip=(), max_
                 if D == 128 and max_q * G > 8:
                     top = np.abs(qq).max()
                     score += np.max(ak @ (np.abs(qq) < 2.0 ** -9.8 * top)) * abs(sm_scale) * top * 2.0 ** -17.8
-                    weight, floor = 2.0 ** -16 + 2.0 ** -19, 2.0 ** -23
+                    weight, floor = 2.0 ** -16 + 2.0 ** -18, 2.0 ** -23
                 s = scales[table[b, np.arange(see) // P], g, 1].astype(np.float64)
                 lost = floor * (w * s).max() / den * np.sum(np.abs(v[:see, g]) / s[:, None], 0)
                 rel = 2 * (2 * score + weight + (L / 16 + 64) * 2.0 ** -24)
