@@ -36,6 +36,7 @@
 //
 // Every wait is bounded; one that gives up raises KVQ_ERRBIT_TIMEOUT, and the
 // CTA leaves after its copies have landed.
+#include <algorithm>
 #include <atomic>
 #include <climits>
 
@@ -55,7 +56,6 @@ constexpr int kStat = 4;                         // floats after a row's accumul
 // Row tiles: 4 (one MMA column block carries the weights and their remainders),
 // 8 or 16 rows a warp; larger row counts take RT tiles of 16.  The warps that
 // the (head, row tile) pairs leave free are further teams.
-constexpr int kTcMinRows = 9;
 
 struct BaShape {
   int rk, rt, hg, tw;   // rows a warp, row tiles, heads a stage, teams
@@ -67,10 +67,19 @@ struct BaShape {
   int slots() const { return pairs() * (tw - 1); }
 };
 
-inline BaShape ba_shape(int max_q, int G, int Hkv, int D) {
+// The tcgen05 kernel reads a block of 32 rows in the time that the mma.sync kernel
+// takes for 12, but starts and ends a row of work more slowly.  Measured (8 kv heads
+// of 128, us, mma.sync and tcgen05): 32 requests of 1,024 - 16,384 tokens, 12 rows 103
+// and 96, 16 rows 109 and 97, 32 rows 171 and 98; 128 requests of 64 - 1,024, 16 rows
+// 45 and 57, 32 rows 74 and 59.  So it takes more than 16 rows always, and 9 - 16
+// where requests can be long: the two meet near 2,100 tokens, taken as half of what
+// the block table holds.
+constexpr int64_t kTcLong = 4096;
+
+inline BaShape ba_shape(int max_q, int G, int Hkv, int D, int64_t capacity) {
   BaShape s;
   const int64_t rows = static_cast<int64_t>(max_q) * G;
-  s.tc = D == 128 && rows >= kTcMinRows;
+  s.tc = D == 128 && (rows > 16 || (rows > 8 && capacity >= kTcLong));
   if (s.tc) {
     s.rk = 16;
     s.rt = 2;
@@ -1133,8 +1142,12 @@ extern "C" size_t kvq_block_attn_workspace_size(int32_t B, int32_t max_q, int32_
   if (static_cast<int64_t>(max_q) * (Hq / num_kv_heads) > INT32_MAX / 2) return 0;
   int sms = 0;
   if (device_sm_count(&sms) != KVQ_OK) return 0;
-  const BaShape s = ba_shape(max_q, Hq / num_kv_heads, num_kv_heads, head_dim);
-  return ba_cut_bytes(sms) + ba_part_bytes(s, head_dim, sms);
+  size_t parts = 0;  // of the larger of the kernels that a call of these sizes may take
+  for (int64_t capacity : {int64_t{0}, kTcLong}) {
+    const BaShape s = ba_shape(max_q, Hq / num_kv_heads, num_kv_heads, head_dim, capacity);
+    parts = std::max(parts, ba_part_bytes(s, head_dim, sms));
+  }
+  return ba_cut_bytes(sms) + parts;
 }
 
 extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q, int64_t q_stride,
@@ -1157,14 +1170,15 @@ extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q
     return KVQ_ERR_INVALID_ARG;
   int sms = 0;
   if (device_sm_count(&sms) != KVQ_OK) return KVQ_ERR_CUDA;
-  const BaShape s = ba_shape(max_q, G, Hkv, D);
+  const int64_t capacity = static_cast<int64_t>(MP) * cache->page_size;
+  const BaShape s = ba_shape(max_q, G, Hkv, D, capacity);
   const size_t cb = ba_cut_bytes(sms);
   if (!aligned256(workspace) || workspace_bytes < cb + ba_part_bytes(s, D, sms))
     return KVQ_ERR_WORKSPACE;
   BaArgs a;
   a.q = static_cast<const uint16_t *>(q);
   a.q_stride = q_stride;
-  a.rg = {tok_start, seq_lens, B, n_tokens, static_cast<int64_t>(MP) * cache->page_size};
+  a.rg = {tok_start, seq_lens, B, n_tokens, capacity};
   a.block_table = block_table;
   a.abort_mask = abort_mask;
   a.scales = reinterpret_cast<const float2 *>(cache->scales);

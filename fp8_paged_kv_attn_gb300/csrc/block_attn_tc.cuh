@@ -47,7 +47,7 @@ constexpr int kTcWarps = 16;                // softmax warps, eight a group; the
 constexpr int kTcThreads = 32 * (kTcWarps + 3);
 constexpr int kTcRows = 32;                 // rows a row block holds
 constexpr int kTcTile = kTcTok * 128;       // 16 KB: one tile of K or V, q piece, or P
-constexpr int kTcRowCost = 6;               // a row's start and end, in tiles' times
+constexpr int kTcRowCost = 4;               // a row's start and end, in tiles' times
 constexpr float kTcThreshold = 6.f;         // lazy rescaling: weights stay below 2^6
 constexpr float kTcWScale = 4.f;            // and their operand, 2^2 of them, below 2^8
 constexpr float kTcFar = 64.f;              // the denominator's reference may be further off (fp32)

@@ -113,9 +113,12 @@ def attend(pools, scales, q, tok_start, seq_lens, table, sm_scale, skip=(), max_
     at most 2^-25 near zero, so a token adds at most 2^-25 2^-7 2 max_i(w_i s_i)
     = 2^-31 max_i(w_i s_i) times its code's magnitude.
 
-    With head_dim 128 and more than 8 rows (max_q times heads a kv head) both
-    operands are sums of e4m3 pieces.  A weight's four pieces, 2^4 apart, leave at
-    most 2^-16 of it, and 2^-10 2^-12 where e4m3 is subnormal, on a scale where
+    With head_dim 128 and more than 16 rows (max_q times heads a kv head), or more
+    than 8 where the table holds 4,096 tokens, both operands are sums of e4m3
+    pieces.  A weight's four pieces, 2^4 apart, leave at most 2^-16 of it; the f16 that
+    holds what the first two leave is off by at most 2^-11 of 2^-8 of it, 2^-19, the
+    f16 of the weight's own remainder by 2^-22 and the exponential and the sums by 2^-20
+    and 2^-21: together at most 2^-16 + 2^-18; and 2^-10 2^-12 where e4m3 is subnormal, on a scale where
     the operand is w_j s_j 2^(2 - n): 2^-22 2^-2 2 max_i(w_i s_i) = 2^-23
     max_i(w_i s_i) a token.  q's two pieces, on a scale where a row's largest
     value lies in [224, 448), are exact for values of 2^-2 and more there (8
@@ -154,7 +157,7 @@ def attend(pools, scales, q, tok_start, seq_lens, table, sm_scale, skip=(), max_
                 ak = np.abs(k[:see, g])
                 score = np.max(ak @ np.abs(qq)) * abs(sm_scale) * 2.0 ** -18
                 weight, floor = 2.0 ** -20, 2.0 ** -31
-                if D == 128 and max_q * G > 8:
+                if D == 128 and (max_q * G > 16 or (max_q * G > 8 and MP * P >= 4096)):
                     top = np.abs(qq).max()
                     score += np.max(ak @ (np.abs(qq) < 2.0 ** -9.8 * top)) * abs(sm_scale) * top * 2.0 ** -17.8
                     weight, floor = 2.0 ** -16 + 2.0 ** -18, 2.0 ** -23

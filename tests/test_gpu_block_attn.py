@@ -53,7 +53,20 @@ def check(kvq, s, Hq, max_q=None, rng=None, **kw):
     got, err = attend(kvq, s, q, max_q, **kw)
     assert err == 0
     compare(got, want, tol)
+    if s.D == 128 and 8 < max_q * (Hq // s.H) <= 16 and s.MP * s.P < 4096:
+        # and by the kernel that such calls take where requests can be long
+        table = wide(s)
+        want, tol = R.attend([s.k, s.v], s.scales, qx, s.tok_start, s.lens, table, sm, max_q=max_q)
+        wide_got, err = attend(kvq, s, q, max_q, table=table, **kw)
+        assert err == 0
+        compare(wide_got, want, tol)
     return got
+
+
+def wide(s):
+    """The step's block table with room for 4,096 tokens."""
+    more = -(-4096 // s.P) - s.MP
+    return np.pad(s.table, ((0, 0), (0, max(0, more))), constant_values=-1)
 
 
 HEADS = [(1, 1), (1, 4), (2, 2), (4, 4), (8, 4), (8, 8), (3, 6), (5, 3), (9, 1), (2, 7), (1, 16)]
@@ -192,15 +205,16 @@ def test_nan_codes_stay_where_they_are_not_seen(kvq):
         compare(got[keep], want[keep], tol[keep])
 
 
-def test_aborted_and_bad_requests(kvq):
+@pytest.mark.parametrize("extra", [1, 250])
+def test_aborted_and_bad_requests(kvq, extra):
     """Aborted rows are zeros and their pages are not read; bad lengths, too many
     rows and bad pages zero theirs; bad starts leave theirs; others as ever."""
     rng = np.random.default_rng(8)
     n = [2, 1, 3, 1, 2, 5, 1]
-    s = R.Step(rng, n, [40, 33, 60, 20, 70, 25, 90], 2, 16, 128, extra_pages=1, pad=2)
+    s = R.Step(rng, n, [40, 33, 60, 20, 70, 25, 90], 2, 16, 128, extra_pages=extra, pad=2)
     q, qx = R.values(rng, s.N, 8, 128)
     want, tol = R.attend([s.k, s.v], s.scales, qx, s.tok_start, s.lens, s.table, 128 ** -0.5,
-                         skip=(1, 2, 3, 4, 5), max_q=5)
+                         skip=(1, 2, 3, 4, 5), max_q=4)
     abort = np.zeros(7, dtype=np.uint8)
     abort[1] = 1
     lens, table = s.lens.copy(), s.table.copy()
@@ -220,57 +234,60 @@ def test_aborted_and_bad_requests(kvq):
     assert np.array_equal(got[same], base[same])
 
 
-def test_bad_page_of_a_row_cut_across_ctas(kvq):
+@pytest.mark.parametrize("max_q", [1, 6])
+def test_bad_page_of_a_row_cut_across_ctas(kvq, max_q):
     rng = np.random.default_rng(9)
     s = R.Step(rng, [1, 1], [4000, 4000], 8, 16, 128)
     q, qx = R.values(rng, s.N, 32, 128)
-    base, _ = attend(kvq, s, q, 1)
+    base, _ = attend(kvq, s, q, max_q)
     table = s.table.copy()
     table[0, 100] = s.NP
-    got, err = attend(kvq, s, q, 1, table=table)
+    got, err = attend(kvq, s, q, max_q, table=table)
     assert err == kvq.ERRBIT_PAGE
     assert (got[0] == 0).all() and np.array_equal(got[1], base[1])
 
 
-def test_repeatable_and_page_order(kvq):
+@pytest.mark.parametrize("max_q", [1, 7])
+def test_repeatable_and_page_order(kvq, max_q):
     """The same bits every time, wherever the pages lie, and without starts."""
     rng = np.random.default_rng(10)
     s = R.Step(rng, [1] * 5, [1000, 3, 500, 77, 2048], 2, 32, 128)
     q, _ = R.values(rng, 5, 8, 128)
-    a, _ = attend(kvq, s, q, 1)
-    b, _ = attend(kvq, s, q, 1, tok_start=None)
+    a, _ = attend(kvq, s, q, max_q)
+    b, _ = attend(kvq, s, q, max_q, tok_start=None)
     perm = rng.permutation(s.NP)
     t = R.Step(rng, [1] * 5, s.lens, 2, 32, 128)
     t.k, t.v, t.scales = np.empty_like(s.k), np.empty_like(s.v), np.empty_like(s.scales)
     t.k[perm], t.v[perm], t.scales[perm] = s.k, s.v, s.scales
     t.table = np.where(s.table >= 0, perm[np.maximum(s.table, 0)], -1).astype(np.int32)
-    c, _ = attend(kvq, t, q, 1)
+    c, _ = attend(kvq, t, q, max_q)
     assert np.array_equal(a, b) and np.array_equal(a, c)
 
 
-def test_strided_q_side_stream_and_graph(kvq):
+@pytest.mark.parametrize("max_q", [3, 5])
+def test_strided_q_side_stream_and_graph(kvq, max_q):
     rng = np.random.default_rng(11)
     s = R.Step(rng, [3, 1, 2], [70, 5, 300], 2, 16, 128)
     wide, x = R.values(rng, s.N, 12, 128)
     want, tol = R.attend([s.k, s.v], s.scales, x[:, 2:10], s.tok_start, s.lens, s.table, 128 ** -0.5,
-                         max_q=3)
+                         max_q=max_q)
     w = wide.cuda()
-    got, _ = attend(kvq, s, w[:, 2:10], 3)
+    got, _ = attend(kvq, s, w[:, 2:10], max_q)
     compare(got, want, tol)
     c, ts, lens, table = cache_of(kvq, s), dev(s.tok_start), dev(s.lens), dev(s.table)
-    ws = [kvq.block_workspace(3, 3, 8, 2, 128) for _ in range(2)]
+    ws = [kvq.block_workspace(3, max_q, 8, 2, 128) for _ in range(2)]
     outs = [torch.zeros(s.N, 8, 128, device="cuda") for _ in range(2)]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     for _ in range(3):  # two calls at once, each with its workspace
         for o, k, st in zip(outs, ws, streams):
-            kvq.kvq_block_attn(c, w[:, 2:10], ts, lens, table, o, k, max_q=3, stream=st)
+            kvq.kvq_block_attn(c, w[:, 2:10], ts, lens, table, o, k, max_q=max_q, stream=st)
     torch.cuda.synchronize()
     for o in outs:
         assert np.array_equal(o.cpu().numpy(), got)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        kvq.kvq_block_attn(c, w[:, 2:10], ts, lens, table, outs[0], ws[0], max_q=3)
+        kvq.kvq_block_attn(c, w[:, 2:10], ts, lens, table, outs[0], ws[0], max_q=max_q)
     outs[0].zero_()
     for _ in range(2):
         graph.replay()
@@ -292,10 +309,11 @@ def test_offsets_past_32_bits(kvq):
     c = kvq.BlockKVCache(kp, vp, scales)
     far = np.where(s.table >= 0, s.table + off, -1).astype(np.int32)
     q, qx = R.values(rng, s.N, 16, D)
-    want, tol = R.attend([s.k, s.v], s.scales, qx, s.tok_start, s.lens, s.table, D ** -0.5)
-    got, err = attend(kvq, s, q, 2, table=far, cache=c)
-    assert err == 0
-    compare(got, want, tol)
+    for max_q in (2, 9):
+        want, tol = R.attend([s.k, s.v], s.scales, qx, s.tok_start, s.lens, s.table, D ** -0.5, max_q=max_q)
+        got, err = attend(kvq, s, q, max_q, table=far, cache=c)
+        assert err == 0
+        compare(got, want, tol)
     (kt, kx), (vt, vx) = R.values(rng, s.N, H, D), R.values(rng, s.N, H, D)
     kvq.kvq_block_append(c, kt.cuda(), vt.cuda(), dev(s.tok_start), dev(s.lens), dev(far))
     pools, sc = [s.k.copy(), s.v.copy()], s.scales.copy()
