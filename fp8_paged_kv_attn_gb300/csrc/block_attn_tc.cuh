@@ -49,7 +49,7 @@ constexpr int kTcRows = 32;                 // rows a row block holds
 constexpr int kTcTile = kTcTok * 128;       // 16 KB: one tile of K or V, q piece, or P
 constexpr int kTcRowCost = 4;               // a row's start and end, in tiles' times
 constexpr float kTcThreshold = 6.f;         // lazy rescaling: weights stay below 2^6
-constexpr float kTcWScale = 4.f;            // and their operand, 2^2 of them, below 2^8
+constexpr float kTcWScale = 2.f;            // and their operand, 2^1 of them, below 2^7
 constexpr float kTcFar = 64.f;              // the denominator's reference may be further off (fp32)
 constexpr uint32_t kTcColS = 0, kTcColO = 256;
 
@@ -118,9 +118,9 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
-// fp32 += e4m3 * e4m3, 128 x n; transposed: A is MN-major.
-__host__ __device__ constexpr uint32_t tc_idesc(uint32_t n, bool transposed) {
-  return (1u << 4) | ((transposed ? 1u : 0u) << 15) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+// fp32 += A * e4m3, 128 x n; A is e4m3 or e5m2; transposed: it is MN-major.
+__host__ __device__ constexpr uint32_t tc_idesc(uint32_t n, bool transposed, bool e5m2) {
+  return (1u << 4) | ((e5m2 ? 1u : 0u) << 7) | ((transposed ? 1u : 0u) << 15) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
@@ -159,12 +159,17 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const float (&v)[16]) {
       : "memory");
 }
 
-// One e4m3 piece of two values, and what is left of them (exact).
-__device__ __forceinline__ uint32_t tc_piece(float2 &x) {
-  const uint16_t c = f32x2_to_e4m3x2(x.x, x.y);
+// q's pieces of two values: e4m3, and e5m2 of what is left.  A bf16 value's eight bits
+// less their rounding to four are at most eight units of the last place, and e5m2's three
+// bits hold those, down to 2^-13; only a value below e4m3's smallest normal number, 2^-6,
+// is off, by at most 2^-14.
+__device__ __forceinline__ void tc_q_pieces(float x, float y, int shift, uint32_t &c1, uint32_t &c2) {
+  const uint16_t c = f32x2_to_e4m3x2(x, y);
   const float2 p = f16x2_to_f32x2(e4m3x2_to_f16x2(c));
-  x = make_float2(x.x - p.x, x.y - p.y);
-  return c;
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y - p.y), "f"(x - p.x));
+  c1 |= static_cast<uint32_t>(c) << shift;
+  c2 |= static_cast<uint32_t>(r) << shift;
 }
 
 // e4m3 codes of two f16 values.
@@ -174,25 +179,28 @@ __device__ __forceinline__ uint32_t f16x2_to_e4m3x2(__half2 x) {
   return c;
 }
 
-// One piece of two f16 values, and 16 times what is left of them (exact: at most the
-// value's lower seven bits).
+// One piece of two f16 values, and 32 times what is left of them (exact: at most the
+// value's lower seven bits).  A piece is rounded to its four bits, so that what it
+// leaves is at most 2^-4 of the value's binade, either way: 32 apart every piece starts in
+// the binade of the one before.
 __device__ __forceinline__ uint32_t tc_piece16(__half2 &x) {
   const uint32_t c = f16x2_to_e4m3x2(x), p = e4m3x2_to_f16x2(static_cast<uint16_t>(c));
-  x = __hfma2(*reinterpret_cast<const __half2 *>(&p), __float2half2_rn(-16.f),
-              __hmul2(x, __float2half2_rn(16.f)));
+  x = __hfma2(*reinterpret_cast<const __half2 *>(&p), __float2half2_rn(-32.f),
+              __hmul2(x, __float2half2_rn(32.f)));
   return c;
 }
 
-// Two weights' four pieces, 16 apart: their f16 roundings carry the first two, what
-// those leave of them joins with two pieces to go, on the f16's last bits (2^-19 of
-// the weight).  In fp32 throughout each piece's way back costs two more conversions.
+// Two weights' four pieces, which leave at most 2^-19 of a weight: its f16 rounding
+// carries the first two, what those leave of it joins with two pieces to go, on the
+// f16's last bits (2^-21).  In fp32 throughout each piece's way back costs two more
+// conversions.
 __device__ __forceinline__ void tc_pieces(float2 w, int shift, uint32_t &c1, uint32_t &c2, uint32_t &c3,
                                           uint32_t &c4) {
   __half2 x = __float22half2_rn(w);
   const __half2 lo = __float22half2_rn(__ffma2_rn(__half22float2(x), make_float2(-1.f, -1.f), w));
   c1 |= tc_piece16(x) << shift;
   c2 |= tc_piece16(x) << shift;
-  x = __hfma2(lo, __float2half2_rn(256.f), x);
+  x = __hfma2(lo, __float2half2_rn(1024.f), x);
   c3 |= tc_piece16(x) << shift;
   c4 |= f16x2_to_e4m3x2(x) << shift;
 }
@@ -235,16 +243,10 @@ __device__ __forceinline__ void tc_load_q(const BaArgs &a, const TcSeg &sg, uint
   // largest value into [224, 448): block_exponent is the smallest e with mx <= 448 2^e
   const int e = block_exponent(mx);
   const float up = pow2(-e), nan = odd ? NAN : 0.f;
-  uint32_t q1[2], q2[2];
+  uint32_t q1[2] = {0, 0}, q2[2] = {0, 0};
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    float2 u = make_float2(x[4 * k] * up + nan, x[4 * k + 1] * up + nan);
-    float2 v = make_float2(x[4 * k + 2] * up + nan, x[4 * k + 3] * up + nan);
-    q1[k] = tc_piece(u);
-    q1[k] |= tc_piece(v) << 16;
-    q2[k] = tc_piece(u);
-    q2[k] |= tc_piece(v) << 16;
-  }
+  for (int k = 0; k < 4; ++k)
+    tc_q_pieces(x[2 * k] * up + nan, x[2 * k + 1] * up + nan, 16 * (k & 1), q1[k >> 1], q2[k >> 1]);
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const int at = 8 * (part & 1);
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 32 dims each: 32 bytes within the swizzled rows
             tc_mma(tmem + kTcColS + 128 * g, qd + piece * (kTcTile >> 4) + 2 * k, kd + 2 * k,
-                   tc_idesc(128, false), piece + k > 0);
+                   tc_idesc(128, false, piece == 1), piece + k > 0);
         tc_commit(&ctl.sfull[g]);
         tc_commit(&ctl.kempty[slot]);
         if (last) tc_commit(&ctl.qfree);
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint64_t vd = tc_desc(v_a + slot * kTcTile), pd = tc_desc(p_a + g * kTcTile);
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // 32 tokens each: 32 bytes of P's rows, 32 rows of V
-          tc_mma(tmem + kTcColO + 128 * g, vd + k * (32 * 128 >> 4), pd + 2 * k, tc_idesc(128, true),
+          tc_mma(tmem + kTcColO + 128 * g, vd + k * (32 * 128 >> 4), pd + 2 * k, tc_idesc(128, true, false),
                  add || k > 0);
         tc_commit(&ctl.pvdone[g]);
         tc_commit(&ctl.vempty[slot]);
@@ -656,7 +658,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         any_tile = true;
         const bool none = n == -INFINITY;  // nothing seen yet: every x is -inf
         const float mm = none ? 0.f : m, mn = none ? 0.f : m - n;
-        // vs 2^(m - n), times 2^2 (kTcThreshold keeps the operand below 2^8)
+        // vs 2^(m - n), times 2 (kTcThreshold keeps the operand below 2^7)
         const float d = vm * kTcWScale * fast_exp2(fminf(mn + lv, 112.f));
         float2 l2 = make_float2(0.f, 0.f);
         uint32_t w1[4], w2[4], w3[4], w4[4];
@@ -734,7 +736,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int p = 3; p >= 0; --p) {
           float o[16];
           tc_ld16(o, o_addr + 32 * p + 16 * half);
-          const float down = p == 0 ? 1.f : p == 1 ? 1.f / 16 : p == 2 ? 1.f / 256 : 1.f / 4096;
+          const float down = p == 0 ? 1.f : p == 1 ? 1.f / 32 : p == 2 ? 1.f / 1024 : 1.f / 32768;
 #pragma unroll
           for (int k = 0; k < 16; ++k) sum[k] = fmaf(o[k], down, sum[k]);
         }
@@ -787,8 +789,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                      : (static_cast<int64_t>(sg.part) * kTcRows + lane) * (128 + kStat);
       float *out = sg.part < 0 ? a.out : a.part;
       {
-        // out = 2^(N - M - 2) sum / l; zeros where a page was bad
-        const float scale = sg.part < 0 ? exp2f(N - M - 2.f) / L1 : 1.f;
+        // out = 2^(N - M - 1) sum / l; zeros where a page was bad
+        const float scale = sg.part < 0 ? exp2f(N - M - 1.f) / L1 : 1.f;
         const bool zero = bad && sg.part < 0;
         TcRow w;
         w.mine = zero ? 0.f : f[grp];
@@ -814,7 +816,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ok = both_sync();  // the tiles and nan_from are read
       if (!ok) break;
       if (used && sg.part >= 0 && warp == 0)
-        *reinterpret_cast<float4 *>(out + at + 128) = make_float4(M, bad ? -1.f : L1, N + 5.f, 0.f);
+        *reinterpret_cast<float4 *>(out + at + 128) = make_float4(M, bad ? -1.f : L1, N + 6.f, 0.f);
       ++nseg;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.segempty[ss]);

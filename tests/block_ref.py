@@ -115,17 +115,18 @@ def attend(pools, scales, q, tok_start, seq_lens, table, sm_scale, skip=(), max_
 
     With head_dim 128 and more than 16 rows (max_q times heads a kv head), or more
     than 8 where the table holds 4,096 tokens, both operands are sums of e4m3
-    pieces.  A weight's four pieces, 2^4 apart, leave at most 2^-16 of it; the f16 that
-    holds what the first two leave is off by at most 2^-11 of 2^-8 of it, 2^-19, the
-    f16 of the weight's own remainder by 2^-22 and the exponential and the sums by 2^-20
-    and 2^-21: together at most 2^-16 + 2^-18; and 2^-10 2^-12 where e4m3 is subnormal, on a scale where
-    the operand is w_j s_j 2^(2 - n): 2^-22 2^-2 2 max_i(w_i s_i) = 2^-23
-    max_i(w_i s_i) a token.  q's two pieces, on a scale where a row's largest
-    value lies in [224, 448), are exact for values of 2^-2 and more there (8
-    significant bits end at 2^-9) and else off by 2^-10: values below 2^-9.8 of the
-    largest are off by 2^-17.8 of it.  The tensor core's sums are off by at most 2^-20 of
-    the terms' magnitudes for 128 terms (scores: within the 2^-18 above; values: 2^-20
-    for each 128 tokens' sum, on top of fp32's)."""
+    pieces.  A weight's four pieces, 2^5 apart, leave at most 2^-19 of it; the f16
+    that holds what the first two leave is off by at most 2^-11 of 2^-10 of it, 2^-21,
+    the f16 of the weight's own remainder by 2^-22 and the exponential and the sums by
+    2^-21 and 2^-20: together below 2^-18; and 2^-10 2^-15 where e4m3 is subnormal, on a
+    scale where the operand is w_j s_j 2^(1 - n): 2^-25 2^-1 2 max_i(w_i s_i) = 2^-25
+    max_i(w_i s_i) a token.  q's two pieces, e4m3 and e5m2 on a scale where a row's
+    largest value lies in [224, 448), are exact for values of 2^-6 and more there (what
+    four bits leave of eight is at most eight units of the last place, and e5m2
+    has three bits) and else off by 2^-14: values below 2^-13.8 of the largest are off by
+    2^-21.8 of it.  The tensor core's sums are off by at most 2^-20 of the terms'
+    magnitudes for 128 terms (scores: within the 2^-18 above; values: 2^-20 for each
+    128 tokens' sum, on top of fp32's)."""
     N, Hq, D = q.shape
     H = pools[0].shape[1]
     G = Hq // H
@@ -159,8 +160,8 @@ def attend(pools, scales, q, tok_start, seq_lens, table, sm_scale, skip=(), max_
                 weight, floor = 2.0 ** -20, 2.0 ** -31
                 if D == 128 and (max_q * G > 16 or (max_q * G > 8 and MP * P >= 4096)):
                     top = np.abs(qq).max()
-                    score += np.max(ak @ (np.abs(qq) < 2.0 ** -9.8 * top)) * abs(sm_scale) * top * 2.0 ** -17.8
-                    weight, floor = 2.0 ** -16 + 2.0 ** -18, 2.0 ** -23
+                    score += np.max(ak @ (np.abs(qq) < 2.0 ** -13.8 * top)) * abs(sm_scale) * top * 2.0 ** -21.8
+                    weight, floor = 2.0 ** -18, 2.0 ** -25
                 s = scales[table[b, np.arange(see) // P], g, 1].astype(np.float64)
                 lost = floor * (w * s).max() / den * np.sum(np.abs(v[:see, g]) / s[:, None], 0)
                 rel = 2 * (2 * score + weight + (L / 16 + 64) * 2.0 ** -24)
