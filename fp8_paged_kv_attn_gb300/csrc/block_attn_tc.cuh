@@ -466,11 +466,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (elect_one()) {
         const uint64_t kd = tc_desc(k_a + slot * kTcTile), qd = tc_desc(q_a);
 #pragma unroll
-        for (int piece = 0; piece < 2; ++piece)
+        for (int piece = 1; piece >= 0; --piece)  // the smaller first: each sum is truncated
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 32 dims each: 32 bytes within the swizzled rows
             tc_mma(tmem + kTcColS + 128 * g, qd + piece * (kTcTile >> 4) + 2 * k, kd + 2 * k,
-                   tc_idesc(128, false, piece == 1), piece + k > 0);
+                   tc_idesc(128, false, piece == 1), piece == 0 || k > 0);
         tc_commit(&ctl.sfull[g]);
         tc_commit(&ctl.kempty[slot]);
         if (last) tc_commit(&ctl.qfree);
