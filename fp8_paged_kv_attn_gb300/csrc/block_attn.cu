@@ -144,6 +144,7 @@ struct BaArgs {
   const float2 *scales;  // [num_pages][Hkv]
   BaCut *cut;            // [CTAs]
   float *part;           // [2 CTAs][hg * rt][rk][D + kStat]
+  float *kept;           // the tcgen05 kernel's flushed sums: [CTAs][kTcWarps][kTcKept]
   float *out;
   uint32_t *err_word;
   int32_t num_pages, p_shift, Hkv, Hq, G, MP, max_q;  // page size 1 << p_shift
@@ -266,8 +267,22 @@ __device__ __forceinline__ void ba_begin(BaState<D, RK> &st, const BaArgs &a, co
   }
 }
 
+// The product alone, with no sum before it.
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                                uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // p.v of one tile: words wa..wd are V rows 2t, 2t+1, 2t+8, 2t+9 at the lane's
 // D / 8 dims; hi / lo the weights' f16 and remainders per row group and n-tile.
+// The tensor core's additions truncate (towards zero), so that a long sum kept there
+// drifts: 7e-6 of it over 8,192 tokens of positive values and 1.2e-4 over 65,536,
+// measured.  So it sums a tile, and the tiles are added with rounding (5e-7 left; 1% of
+// the time at one row, 3% at eight rows of a kv head.  Flushing the sums every 16 or 32
+// turns, to shared or global memory, cost 3 - 5%).
 template <int D, int RK>
 __device__ __forceinline__ void ba_pv(float (&o)[D / 16][BaState<D, RK>::NG][4],
                                       const uint32_t (&wa)[D / 32], const uint32_t (&wb)[D / 32],
@@ -291,18 +306,31 @@ __device__ __forceinline__ void ba_pv(float (&o)[D / 16][BaState<D, RK>::NG][4],
       f[j][2] = e4m3x2_to_f16x2(y & 0xFFFFu);
       f[j][3] = e4m3x2_to_f16x2(y >> 16);
     }
+    float d[BI][NG][4];
 #pragma unroll
     for (int j = 0; j < BI; ++j)
 #pragma unroll
       for (int g = 0; g < NG; ++g)
-        mma_16816(o[i0 + j][g], f[j][0], f[j][1], f[j][2], f[j][3], hi[g][0], hi[g][1]);
+        mma_16816_first(d[j][g], f[j][0], f[j][1], f[j][2], f[j][3], RK > 4 ? lo[g][0] : hi[g][0],
+                        RK > 4 ? lo[g][1] : hi[g][1]);
     if constexpr (RK > 4) {
 #pragma unroll
       for (int j = 0; j < BI; ++j)
 #pragma unroll
         for (int g = 0; g < NG; ++g)
-          mma_16816(o[i0 + j][g], f[j][0], f[j][1], f[j][2], f[j][3], lo[g][0], lo[g][1]);
+          mma_16816(d[j][g], f[j][0], f[j][1], f[j][2], f[j][3], hi[g][0], hi[g][1]);
     }
+#pragma unroll
+    for (int j = 0; j < BI; ++j)
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          const float2 x = __fadd2_rn(make_float2(o[i0 + j][g][k], o[i0 + j][g][k + 1]),
+                                      make_float2(d[j][g][k], d[j][g][k + 1]));
+          o[i0 + j][g][k] = x.x;
+          o[i0 + j][g][k + 1] = x.y;
+        }
   }
 }
 
@@ -1113,6 +1141,10 @@ size_t ba_part_bytes(const BaShape &s, int D, int ctas) {
   return 2ull * ctas * s.hg * s.rt * s.rk * (D + kStat) * sizeof(float);
 }
 
+size_t ba_kept_bytes(const BaShape &s, int ctas) {
+  return s.tc ? sizeof(float) * ctas * kTcWarps * kTcKept : 0;
+}
+
 // [page][head][slot][dim] as a 4-D map; a box is 16 slots of hg heads.
 bool ba_map(CUtensorMap *map, const void *pool, const kvq_block_cache &c, int hg) {
   auto enc = tensor_map_encoder();
@@ -1142,10 +1174,10 @@ extern "C" size_t kvq_block_attn_workspace_size(int32_t B, int32_t max_q, int32_
   if (static_cast<int64_t>(max_q) * (Hq / num_kv_heads) > INT32_MAX / 2) return 0;
   int sms = 0;
   if (device_sm_count(&sms) != KVQ_OK) return 0;
-  size_t parts = 0;  // of the larger of the kernels that a call of these sizes may take
+  size_t parts = 0;  // the larger of the kernels' that a call of these sizes may take
   for (int64_t capacity : {int64_t{0}, kTcLong}) {
     const BaShape s = ba_shape(max_q, Hq / num_kv_heads, num_kv_heads, head_dim, capacity);
-    parts = std::max(parts, ba_part_bytes(s, head_dim, sms));
+    parts = std::max(parts, ba_part_bytes(s, head_dim, sms) + ba_kept_bytes(s, sms));
   }
   return ba_cut_bytes(sms) + parts;
 }
@@ -1173,7 +1205,7 @@ extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q
   const int64_t capacity = static_cast<int64_t>(MP) * cache->page_size;
   const BaShape s = ba_shape(max_q, G, Hkv, D, capacity);
   const size_t cb = ba_cut_bytes(sms);
-  if (!aligned256(workspace) || workspace_bytes < cb + ba_part_bytes(s, D, sms))
+  if (!aligned256(workspace) || workspace_bytes < cb + ba_part_bytes(s, D, sms) + ba_kept_bytes(s, sms))
     return KVQ_ERR_WORKSPACE;
   BaArgs a;
   a.q = static_cast<const uint16_t *>(q);
@@ -1184,6 +1216,7 @@ extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q
   a.scales = reinterpret_cast<const float2 *>(cache->scales);
   a.cut = static_cast<BaCut *>(workspace);
   a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + cb);
+  a.kept = a.part + ba_part_bytes(s, D, sms) / sizeof(float);
   a.out = out;
   a.err_word = err_word;
   a.num_pages = cache->num_pages;

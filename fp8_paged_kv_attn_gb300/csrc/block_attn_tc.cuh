@@ -48,6 +48,8 @@ constexpr int kTcThreads = 32 * (kTcWarps + 3);
 constexpr int kTcRows = 32;                 // rows a row block holds
 constexpr int kTcTile = kTcTok * 128;       // 16 KB: one tile of K or V, q piece, or P
 constexpr int kTcRowCost = 4;               // a row's start and end, in tiles' times
+constexpr int kTcFlush = 16;                // tiles whose values a group's sum in TMEM takes
+constexpr int kTcKept = 17 * 32;            // floats that a warp keeps in the workspace
 constexpr float kTcThreshold = 6.f;         // lazy rescaling: weights stay below 2^6
 constexpr float kTcWScale = 2.f;            // and their operand, 2^1 of them, below 2^7
 constexpr float kTcFar = 64.f;              // the denominator's reference may be further off (fp32)
@@ -255,6 +257,34 @@ __device__ __forceinline__ void tc_load_q(const BaArgs &a, const TcSeg &sg, uint
         make_uint2(q2[0], q2[1]);
   }
   if (part == 0) qk[r] = a.q_scale * pow2(e);
+}
+
+// Every kTcFlush tiles the sums leave TMEM, and are added with rounding to others in
+// the workspace: the tensor core's additions truncate (towards zero), and a long sum there
+// drifts, 1.3e-5 of it over 65,536 tokens, measured; 1e-7 are left, for 3% of the time.  This
+// thread's dim of 16 rows: kept times rows[row], then the pieces times grow[row].
+__device__ __forceinline__ void tc_flush(float *kept, bool first, float keep, float fo, float *rows,
+                                         uint32_t addr, int half, int lane) {
+  float acc[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) acc[k] = first ? 0.f : kept[32 * k];
+  rows[lane] = keep;
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 16; ++k) acc[k] *= rows[16 * half + k];
+  __syncwarp();
+  rows[lane] = fo;
+  __syncwarp();
+  float down = 1.f / 32768;  // the smallest pieces first
+#pragma unroll 1
+  for (int p = 3; p >= 0; --p, down *= 32.f) {
+    float o[16];
+    tc_ld16(o, addr + 32 * p);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[k] = fmaf(o[k] * down, rows[16 * half + k], acc[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < 16; ++k) kept[32 * k] = acc[k];
 }
 
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -509,7 +539,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ok = tc_wait(ctl, &ctl.pfull[g], np[g]++ & 1, a.err_word);
         if (!ok) break;
         tc_after();
-        issue_pv(g, (g0 + u) % kTcV, u >= 2);
+        issue_pv(g, (g0 + u) % kTcV, (u >> 1) % kTcFlush != 0);
       }
       g0 += sg.tiles;
       ++nseg;
@@ -632,13 +662,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (any_tile) {
           ok = tc_wait(ctl, &ctl.pvdone[grp], (nt & 1) ^ 1, a.err_word);
           if (!ok) break;
-          if (__any_sync(0xffffffffu, fo != 1.f)) {
+          const bool flush = (t >> 1) % kTcFlush == 0;
+          if (flush || __any_sync(0xffffffffu, fo != 1.f)) {
             float *grow = ctl.grow[warp];
-            grow[lane] = fo;
-            __syncwarp();
             tc_after();
+            if (flush) {
+              float *kept = a.kept + static_cast<int64_t>(blockIdx.x * kTcWarps + warp) * kTcKept + lane;
+              const bool first = (t >> 1) == kTcFlush;
+              const float kept_n = first ? n : kept[16 * 32];  // the kept sums' reference
+              kept[16 * 32] = n;
+              tc_flush(kept, first, kept_n == n ? 1.f : exp2f(kept_n - n), fo, grow, o_addr + 16 * half, half, lane);
+            } else {
+              grow[lane] = fo;
+              __syncwarp();
+            }
 #pragma unroll 1
-            for (int c = 64 * half; c < 64 * half + 64; c += 16) {  // 16 rows of a piece
+            for (int c = 64 * half; !flush && c < 64 * half + 64; c += 16) {  // 16 rows of a piece
               float o[16];
               tc_ld16(o, o_addr + c);
 #pragma unroll
@@ -740,6 +779,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int k = 0; k < 16; ++k) sum[k] = fmaf(o[k], down, sum[k]);
         }
+      }
+      if (sg.tiles > 2 * kTcFlush + grp) {  // and what was flushed
+        const float *kept = a.kept + static_cast<int64_t>(blockIdx.x * kTcWarps + warp) * kTcKept + lane;
+        float *grow = ctl.grow[warp];
+        const float kept_n = kept[16 * 32];
+        grow[lane] = kept_n == n ? 1.f : exp2f(kept_n - n);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sum[k] = fmaf(kept[32 * k], grow[16 * half + k], sum[k]);
       }
       // group 0 writes the first eight of them and group 1 the others; each hands the
       // other its sums of those, [half][row][dim], in its own (free) weight tile

@@ -115,6 +115,39 @@ def test_drafts_over_long_and_short_contexts(kvq, H, G, n, P):
     check(kvq, R.Step(rng, [n], [3000 + n], H, P, 128), H * G)
 
 
+@pytest.mark.parametrize("H,G,n,L,D", [(8, 4, 1, 2600, 128), (1, 4, 8, 9100, 128), (2, 8, 1, 5000, 128),
+                                       (8, 1, 1, 2100, 64), (1, 4, 2, 9300, 64), (2, 5, 2, 5000, 128)])
+def test_long_sums_do_not_drift(kvq, H, G, n, L, D):
+    """Values of one sign, over so many requests that a CTA sums thousands of tokens of
+    each.  All requests share one prefix."""
+    rng = np.random.default_rng([H, G, n, L])
+    s = R.Step(rng, [n], [L], H, 16, D)
+    s.v &= 0x7F
+    s.v[(s.v & 0x7F) == 0x7F] = 0x7E
+    s.k[:] = rng.integers(0x20, 0x30, s.k.shape, dtype=np.uint8) | (s.k & 0x80)
+    B, few = 160, 6
+    q, qx = R.values(rng, B * n, H * G, D)
+    ts, lens = (np.arange(B + 1) * n).astype(np.int32), np.full(B, L, dtype=np.int32)
+    s.B = B
+    got, err = attend(kvq, s, q, n, tok_start=ts, lens=lens, table=np.repeat(s.table, B, 0))
+    assert err == 0
+    rows = few * n
+    want, tol = R.attend([s.k, s.v], s.scales, qx[:rows], ts[:few + 1], lens[:few],
+                         np.repeat(s.table, few, 0), D ** -0.5, max_q=n)
+    compare(got[:rows], want, tol)
+    # no drift: roundings even out, and at most 64 additions in a row truncate, each
+    # half of 2^-23 on average: 64 2^-24 = 3.8e-6
+    rel = (got[:rows] - want) / want
+    assert abs(rel.mean()) < 4e-6
+    bad = np.repeat(s.table, B, 0)
+    bad[1, 3], bad[2, -1] = -1, s.NP  # a bad page near a row's start and at its end
+    again, err = attend(kvq, s, q, n, tok_start=ts, lens=lens, table=bad)
+    assert err == kvq.ERRBIT_PAGE
+    assert (again[n:3 * n] == 0).all()
+    keep = np.r_[0:n, 3 * n:B * n]
+    assert np.array_equal(again[keep], got[keep])
+
+
 def test_many_drafts(kvq):
     rng = np.random.default_rng(14)
     n = rng.integers(0, 5, 700)
