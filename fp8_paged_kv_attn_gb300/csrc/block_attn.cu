@@ -12,7 +12,11 @@
 // small values with a large one.  out = 2^(n - m) o / l.
 //
 // Bound: HBM.  A request's K and V are read once for all query heads of a kv
-// head and all its rows (up to 128 rows x heads a kv head).
+// head and all its rows (in blocks of up to 128 rows x heads a kv head, of 32 in the
+// tcgen05 kernel).  Measured: 64 requests of 8,193 - 9,216 tokens, 8 kv heads of 128, 4
+// heads a kv head, one row: 174 us, 97% of the measured copy rate; 8 heads a kv head,
+// 512 - 65,536 tokens, pages of 64: 294 us, 95%; 8 requests of 8,193 tokens: 31 us, 65%
+// (3 us until the first bytes are asked for, 4 for the cut rows).
 //
 //   split   persistent CTAs; the requests' (kv-head group, row block) rows, in
 //           units of 16 tokens, are laid end to end and cut into equal runs
@@ -26,7 +30,8 @@
 //           the end of a segment the teams' partials meet in shared memory.
 //   combine merges rows that were cut across CTAs.
 //
-// q.k and p.v run on mma.sync m16n8k16 (f16 in, fp32 sums): at up to 16 rows a
+// head_dim 128 with many rows takes another split kernel (block_attn_tc.cuh).  Here q.k
+// and p.v run on mma.sync m16n8k16 (f16 in, fp32 sums): at up to 16 rows a
 // tile the tensor work is about half of what the memory time allows, and the
 // operands come from registers in the layout that the byte conversion leaves
 // them in.  e4m3 is exact in f16; a row of q is scaled by a power of two into
@@ -68,11 +73,11 @@ struct BaShape {
 };
 
 // The tcgen05 kernel reads a block of 32 rows in the time that the mma.sync kernel
-// takes for 12, but starts and ends a row of work more slowly.  Measured (8 kv heads
-// of 128, us, mma.sync and tcgen05): 32 requests of 1,024 - 16,384 tokens, 12 rows 103
-// and 96, 16 rows 109 and 97, 32 rows 171 and 98; 128 requests of 64 - 1,024, 16 rows
-// 45 and 57, 32 rows 74 and 59.  So it takes more than 16 rows always, and 9 - 16
-// where requests can be long: the two meet near 2,100 tokens, taken as half of what
+// takes for 8, but starts and ends a row of work more slowly.  Measured (8 kv heads
+// of 128, us, mma.sync and tcgen05): 32 requests of 1,024 - 16,384 tokens, 12 rows 116
+// and 99, 16 rows 121 and 100, 32 rows 197 and 102; 128 requests of 64 - 1,024, 16 rows
+// 50 and 62, 32 rows 84 and 63.  So it takes more than 16 rows always, and 9 - 16
+// where requests can be long: the two meet near 1,600 tokens, taken as half of what
 // the block table holds.
 constexpr int64_t kTcLong = 4096;
 

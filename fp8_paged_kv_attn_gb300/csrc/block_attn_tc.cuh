@@ -1,52 +1,59 @@
-// The tcgen05 split kernel of kvq_block_attn: head_dim 128, 9 and more rows
-// (query rows times heads of a kv head).  Included by block_attn.cu.
+// The tcgen05 split kernel of kvq_block_attn: head_dim 128 and many rows (query
+// rows times heads of a kv head; the rule is at ba_shape).  Included by block_attn.cu.
 //
 // mma.sync would be the bound here: a warp's 16 rows need 48 MMAs a 16-token
 // tile.  On tcgen05 the 8-bit kind multiplies the cache's bytes as they are
-// (K as a K-major operand, V as an MN-major one: both are the pool's own
-// layout), so nothing of the cache is converted.  What has to be 8-bit too is
-// split into e4m3 pieces:
-//   q   a row scaled by 2^e (largest value in [224, 448)) = q1 + q2, each e4m3 (4
-//       significant bits, a bf16 has 8): exact for values down to 2^-10 of the row's
-//       largest, below that off by at most 2^-10 on that scale.  S = q1 K + q2 K
-//       in one accumulator.
-//   w   a softmax weight (times 2^2, at most 2^8) = p1 + p2/16 + p3/256 + p4/4096: each
-//       piece leaves at most a 16th (on average a 36th) of what the one before left, at
-//       most 2^-16 of w, and 2^-22 for weights below e4m3's normal range.  The pieces
-//       of 32 rows are the 128 rows of one MMA: piece p of row r is row 32 p + r, and
-//       the four sums of a row are added when a segment ends.
-// Sums are fp32 (measured: 2^-20.7 of the sum of the terms' magnitudes).
+// (both K-major K and MN-major V are the pool's own layout), so nothing of the cache
+// is converted.  What has to be 8-bit too is split into pieces:
+//   q   a row scaled by 2^e (largest value in [224, 448)) = q1 + q2, e4m3 and e5m2:
+//       exact for values down to 2^-13.8 of the row's largest (tc_q_pieces).
+//       S = q2 K + q1 K in one accumulator.
+//   w   a softmax weight (times 2, at most 2^7) = p1 + p2/2^5 + p3/2^10 + p4/2^15, e4m3
+//       (tc_pieces): off by 2^-19 of w, and by 2^-25 where e4m3 is subnormal.  The
+//       pieces of 32 rows are 128 columns of one product: piece p of row r is
+//       column 32 p + r, and a row's four sums are added when they leave TMEM.
+// Against 64 bits the result is as near as the mma.sync kernel's (1e-6 of the output's
+// norm with large scores and values).
 //
-//   S[128 x 256 tokens] = Q[128 x 128] K^T   q's 32 rows four times over, so that
-//       each of a group's four warps finds them in its own TMEM lanes; warp p takes
-//       tokens 32 p .. 32 p + 31 of its tile (a row a lane, no shuffles)
-//   O[128 x 128 dims] += P[128 x 128 tokens] V
-// An MMA of 128 rows takes 111 cycles here for 128 columns and 165 for 256, so
-// scores are issued for two 128-token tiles at once: 1,100 cycles a tile with the
-// values, of the 1,424 that its 32 KB take from HBM.  (With the cache as the operand of
-// 128 rows and the query rows as columns it would be 890, but then every softmax
-// thread holds all rows of one token and fetches each row's scale and references:
-// measured 262 us against 138 on 32 drafts of 1 - 8 rows.)
+//   S[128 x 128 tokens] = Q[128 x 128] K^T   q's 32 rows four times over, so that
+//       each of TMEM's four lane groups has them; a warp takes 16 tokens of its tile
+//       (a row a lane, no shuffles)
+//   O[128 dims x 128] += V^T[128 dims x 128 tokens] P^T   so that the pieces of a
+//       row are columns of the same lane, and their sum needs no shared memory
+//       (with dims as columns a segment's end took 18,000 cycles, now 12,000)
+// An MMA of 128 x 128 x 32 takes 64 cycles alone, 768 a tile, of the 1,424 that its
+// 32 KB take from HBM; its operands are 8 KB, all that shared memory gives in that
+// time, so in company it takes about twice as long.  (The cache as the operand of 128
+// rows in the scores too would leave every softmax thread with all rows of one
+// token: measured 262 us against 138.)
 //
-// Roles: warps 0-3 and 4-7 two softmax groups with their own S and O (TMEM: 4 x
-// 128 columns), warp 8 issues the MMAs, warps 9 and 10 the copies of K and of V (a
-// 16-token page is a copy of 2 KB, and issuing 16 a tile is too much for one
-// warp at HBM's rate), each into a ring of its own, since K is free after the
+// Roles: warps 0-7 and 8-15 two softmax groups with their own S and O (TMEM: 4 x 128
+// columns), then one warp that issues the MMAs and two that issue the copies, of
+// K and of V (a 16-token page is a copy of 2 KB, and 16 a tile are too many for
+// one warp at HBM's rate), each into a ring of its own, since K is free after the
 // scores and V only after the values.  The groups take a head's tiles in turn and
-// are merged when the segment ends.  Work is scheduled, cut and combined as in the
-// mma.sync kernel, in units of 128 tokens of one head; more than 32 rows are row
-// blocks, which follow one another so that the second reads the cache from L2.
+// are merged when the segment ends; the next segment's q and scores are made
+// meanwhile.  Work is scheduled, cut and combined as in the mma.sync kernel, in units
+// of 128 tokens of one head; more than 32 rows are row blocks, which follow one
+// another so that the second reads the cache from L2.
+//
+// Measured: 32 requests of 1,024 - 16,384 tokens, 8 kv heads, 1 - 8 rows of 4 heads: 106
+// us (mma.sync 206; HBM's floor 66).  A tile takes about 2,050 cycles of a CTA: a
+// group's own chain (scores, maxima, rescaling, 64 conversions a thread, products) is
+// 4,000 and two are in flight, TMEM being full.  Without rescaling, three of the four
+// pieces and half of the products it was 87 us, with each of them alone 96 - 100: no
+// single step is the bound any more.
 #pragma once
 
 namespace kvq {
 
 constexpr int kTcTok = 128;                 // tokens a tile
-constexpr int kTcK = 4, kTcV = 4;           // ring slots: K's in pairs; V's even, so that a slot belongs to
-                                            // one group within a segment
+constexpr int kTcK = 4, kTcV = 4;           // ring slots; V's even, so that a slot belongs to one group
+                                            // within a segment
 constexpr int kTcWarps = 16;                // softmax warps, eight a group; then MMAs, K copies, V copies
 constexpr int kTcThreads = 32 * (kTcWarps + 3);
 constexpr int kTcRows = 32;                 // rows a row block holds
-constexpr int kTcTile = kTcTok * 128;       // 16 KB: one tile of K or V, q piece, or P
+constexpr int kTcTile = kTcTok * 128;       // 16 KB: one tile of K or V, q piece, or weights
 constexpr int kTcRowCost = 4;               // a row's start and end, in tiles' times
 constexpr int kTcFlush = 16;                // tiles whose values a group's sum in TMEM takes
 constexpr int kTcKept = 17 * 32;            // floats that a warp keeps in the workspace
