@@ -9,18 +9,23 @@
 //
 // Append has three kernels, all with the maximum that sets a block's scale and
 // the conversion in one visit:
-//   short  decode and draft steps: latency counts.  K, V and q of a page go to
-//          CTAs of their own, a warp takes one head's rows, four (head_dim 128)
-//          at a time; further rows are read twice, the second time from L1.
+//   short  decode and draft steps, with parts of prompts among them or not: latency
+//          counts.  K, V and q of a page go to CTAs of their own, a warp takes one
+//          head's rows, four (head_dim 128) at a time; further rows are read twice,
+//          the second time from L1.  64 rows of 64 requests, K and V of 8 heads, q of
+//          32, rotated: 3.0 us; 256 drafts of 1 - 8 rows 10.5.
 //   ring   prompts with enough kv heads: bandwidth counts (2 D (2 + 1) bytes a
 //          token and kv head, 4 D a query head).  A producer warp stages the
 //          rows of a page and a group of heads with one TMA copy each into a
-//          shared-memory ring; a consumer warp takes 16 rows of one head.
+//          shared-memory ring; a consumer warp takes 16 rows of one head.  64
+//          prompts of 8,192 tokens: 497 us, 96% of the measured copy rate.
 //   wide   prompts with few kv heads: the same without the ring, a warp's 16
 //          rows loaded by itself.
+// Reading back has one kernel: 48 ragged prefixes 215 us, 97%.
 // In 32- and 64-token pages the warps of a block exchange their maxima through
 // shared memory.  The page's angles are computed once into shared memory and
 // used by all heads.
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -205,42 +210,111 @@ __device__ __forceinline__ float warp_amax(F lane_max) {
 
 // ---- short steps
 
-// blockIdx.x: request and share of its pages (0: K, 1: V, 2 ..: qheads heads of
-// q each); blockIdx.y: its page, counting from the first that the step
-// touches, and every gridDim.y-th one after it.  No scan over the requests: the
-// time of a decode step is a chain of loads (starts and length; table entry
-// beside the rows; old scale), and this is the shortest one.
-template <int D, bool kRope>
-__global__ void __launch_bounds__(kBcThreads, 4) block_append_short(BlockAppendArgs a, int shares,
-                                                                    int qheads) {
+template <bool kShared>
+struct SharedRun {};
+
+template <>
+struct SharedRun<true> {  // what is left of a shared CTA's run
+  RunScan<kBcThreads> scan;
+  int64_t left, in;
+  int b;
+};
+
+// blockIdx.x below B * shares: request and share of its pages (0: K, 1: V, 2 ..:
+// qheads heads of q each); blockIdx.y: its page, counting from the first that the
+// step touches, and every gridDim.y-th one after it, up to `own` pages in all.  No scan over
+// the requests: the time of a decode step is a chain of loads (starts and length;
+// table entry beside the rows; old scale), and this is the shortest one.
+// The pages beyond (a prompt's part among decode rows) are the other CTAs': they scan
+// the requests and take equal runs of them (255 requests of one row and one of 2,048: 608
+// us without them, now 26; 256 drafts of 1 - 8 rows 9.7, now 10.5).
+// kShared: the launch has such CTAs (their state costs the others registers).
+template <int D, bool kRope, bool kShared>
+__global__ void __launch_bounds__(kBcThreads, kShared ? 3 : 4) block_append_short(BlockAppendArgs a, int shares,
+                                                                    int qheads, int own) {
   constexpr int kItems = D / 16;      // lanes a row (two 8-dim chunks each)
   constexpr int kRpp = 32 / kItems;   // rows a warp pass
   extern __shared__ float4 tab[];     // kRope: [P][rd / 4] angles of the page's rows
   __shared__ uint64_t s_freq[kRope ? D / 2 : 1];
+  __shared__ SharedRun<kShared> run;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int P = a.c.P, H = a.c.H;
   const int i = lane % kItems, r0 = lane / kItems;
   const bool half = !kRope || a.rope.layout == KVQ_ROPE_HALF;
   const int rd = kRope ? a.rope.rd : D;
   const ItemChunks ch = item_chunks(i, D, rd, half);
-  const int b = blockIdx.x / shares, share = blockIdx.x - b * shares;
-  const bool is_v = share == 1, is_q = share > 1;
-  const int h0 = is_q ? (share - 2) * qheads : 0;
-  const int heads = is_q ? min(qheads, a.Hq - h0) : H;
-  const uint16_t *src = is_q ? a.q + static_cast<int64_t>(h0) * D : is_v ? a.v_new : a.k_new;
-  const int64_t stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
+  const int first_shared = a.rg.B * shares;  // CTA
+  const bool shared = kShared && static_cast<int>(blockIdx.x) >= first_shared;
+  int b = blockIdx.x / shares, share = blockIdx.x - b * shares;
+  bool is_v, is_q;
+  int h0, heads;
+  const uint16_t *src;
+  int64_t stride;
+  auto set_share = [&] {
+    is_v = share == 1;
+    is_q = share > 1;
+    h0 = is_q ? (share - 2) * qheads : 0;
+    heads = is_q ? min(qheads, a.Hq - h0) : H;
+    src = is_q ? a.q + static_cast<int64_t>(h0) * D : is_v ? a.v_new : a.k_new;
+    stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
+  };
+  set_share();
   grid_dependency_wait();
   allow_dependents();
   double freq = 0.0;
   if constexpr (kRope)
-    if (!is_v && threadIdx.x < rd / 2) freq = a.rope.inv_freq[threadIdx.x];  // rd / 2 <= blockDim
-  const Rows rq = request_rows<true>(a.rg, b);
-  if (rq.err && blockIdx.y == 0 && share == 0 && threadIdx.x == 0) report(a.err_word, rq.err);
-  const int pages = static_cast<int>(pages_touched(rq, P));
-  if (static_cast<int>(blockIdx.y) >= pages) return;
+    if ((shared || share != 1) && threadIdx.x < rd / 2) freq = a.rope.inv_freq[threadIdx.x];  // rd / 2 <= blockDim
+  Rows rq = request_rows<true>(a.rg, shared ? 0 : b);
+  int pages = INT32_MAX;  // a shared CTA's end is its run's
+  if constexpr (kShared) {
+    if (shared) {
+      const int ctas = (static_cast<int>(gridDim.x) - first_shared) * gridDim.y;
+      const int cta = (static_cast<int>(blockIdx.x) - first_shared) * gridDim.y + blockIdx.y;
+      const RunStart r = find_run<kBcThreads>(a.rg.B, ctas, cta, run.scan, [&](int k) -> int64_t {
+        return max(pages_touched(request_rows<true>(a.rg, k), P) - own, static_cast<int64_t>(0)) * shares;
+      });
+      if (threadIdx.x == 0) {
+        run.left = min(r.per, r.total - cta * r.per);
+        run.in = r.in;
+        run.b = r.b;
+      }
+    }
+  }
+  if (!shared) {
+    if (rq.err && blockIdx.y == 0 && share == 0 && threadIdx.x == 0) report(a.err_word, rq.err);
+    pages = static_cast<int>(pages_touched(rq, P));
+    if constexpr (kShared) pages = min(pages, own);
+    if (static_cast<int>(blockIdx.y) >= pages) return;
+  }
   if constexpr (kRope)
-    if (!is_v && threadIdx.x < rd / 2) s_freq[threadIdx.x] = turns_per_token(freq);
+    if ((shared || share != 1) && threadIdx.x < rd / 2) s_freq[threadIdx.x] = turns_per_token(freq);
   for (int pg = blockIdx.y; pg < pages; pg += gridDim.y) {
+    if (shared) {  // item `in` of request b: page and share
+      if constexpr (kShared) {
+        __syncthreads();
+        if (threadIdx.x == 0 && run.left > 0) {
+          while (true) {
+            const int64_t n = max(pages_touched(request_rows<true>(a.rg, run.b), P) - own,
+                                  static_cast<int64_t>(0)) * shares;
+            if (run.in < n) break;
+            run.in = 0;
+            ++run.b;
+          }
+        }
+        __syncthreads();
+        if (run.left <= 0) return;
+        b = run.b;
+        rq = request_rows<true>(a.rg, b);
+        pg = own + static_cast<int>(run.in / shares);
+        share = static_cast<int>(run.in % shares);
+        set_share();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          ++run.in;
+          --run.left;
+        }
+      }
+    }
     const int lp = rq.p0 / P + pg;
     const int page = __ldg(a.block_table + static_cast<int64_t>(b) * a.MP + lp);
     const int first = max(rq.p0, lp * P), slot0 = first - lp * P;
@@ -862,22 +936,33 @@ kvq_status append_impl(const kvq_block_cache *cache, const kvq_rope_desc *rope, 
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (n_tokens <= kShortRows * static_cast<int64_t>(B) || pages <= 2 * sms) {
-    const auto fn = D == 128 ? (rope ? block_append_short<128, true> : block_append_short<128, false>)
-                             : (rope ? block_append_short<64, true> : block_append_short<64, false>);
     // q's heads in one share for a row a request, in shares of twice K's rows for
-    // more (256 drafts of 1-8 rows, 32 heads over 8: 9.7 us; shares of 8 and of
-    // all heads 11.3 and 10.5)
+    // more (256 drafts of 1-8 rows, 32 heads over 8, no shared CTAs: 9.7 us; shares
+    // of 8 and of all heads 11.3 and 10.5)
     const int qheads = n_tokens <= 2 * static_cast<int64_t>(B) ? Hq : 2 * H;
     const int shares = rope && Hq > 0 ? 2 + (Hq + qheads - 1) / qheads : 2;
-    if (static_cast<int64_t>(B) * shares > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(B) * shares > INT32_MAX - 4 * sms) return KVQ_ERR_UNSUPPORTED;
     // pages a request that get CTAs of their own: what an average one fills,
     // up to 16 CTAs an SM in all
     const int64_t avg = (n_tokens + B - 1) / B;
     int64_t gy = (avg + P - 1) / P;
     const int64_t most = 16LL * sms / (static_cast<int64_t>(B) * shares) + 1;
     gy = gy < most ? gy : most;
-    e = launch_dependent(fn, dim3(B * shares, static_cast<unsigned>(gy)), kBcThreads, angles, cs, a,
-                         shares, qheads);
+    // a request's own CTAs do two pages each; what one can have beyond is shared
+    const int own = 2 * static_cast<int>(gy);
+    // (not in a step of a row a request, which they would slow down: 3.0 to 3.6 us)
+    const int64_t beyond = (n_tokens + P - 2) / P + 1 - own;
+    const int64_t extra = beyond <= 0 || n_tokens <= B
+                              ? 0 : (std::min<int64_t>(beyond * shares, 3 * sms) + gy - 1) / gy;
+    using ShortFn = void (*)(BlockAppendArgs, int, int, int);
+    static constexpr ShortFn kFns[2][2][2] = {
+        {{block_append_short<64, false, false>, block_append_short<64, false, true>},
+         {block_append_short<64, true, false>, block_append_short<64, true, true>}},
+        {{block_append_short<128, false, false>, block_append_short<128, false, true>},
+         {block_append_short<128, true, false>, block_append_short<128, true, true>}}};
+    e = launch_dependent(kFns[D == 128][rope != nullptr][extra > 0],
+                         dim3(static_cast<unsigned>(B * shares + extra), static_cast<unsigned>(gy)), kBcThreads,
+                         angles, cs, a, shares, qheads, own);
   } else if (H * P >= kBcWarps * kRowsPerWarp) {
     const auto fn = D == 128 ? (rope ? block_append_ring<128, true> : block_append_ring<128, false>)
                              : (rope ? block_append_ring<64, true> : block_append_ring<64, false>);

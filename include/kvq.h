@@ -3,7 +3,9 @@
  * handoff of BF16 pages, batched page-tag integrity check, the page
  * allocator that sets the tags, single-query
  * paged decode attention, and the weight-only INT4 / FP8 decode matrix
- * product, for NVIDIA GB300 (sm_103a).  Plain C ABI: pointers,
+ * product; and the block-scaled form of the cache (a scale per page and kv head):
+ * rotary positions, quantise-and-append, read-back, and causal attention of one
+ * or several rows a request.  For NVIDIA GB300 (sm_103a).  Plain C ABI: pointers,
  * sizes, a CUDA stream.  The library allocates no memory.
  *
  * Sources (web pages, cited by title and section):
@@ -72,9 +74,11 @@ typedef enum { KVQ_W_INT4 = 0, KVQ_W_E4M3 = 1 } kvq_w_dtype;
 
 /* Bits ORed into *err_word by the kernels. */
 #define KVQ_ERRBIT_PAGE    (1u << 0) /* a block-table entry the call needs is outside [0, num_pages) */
-#define KVQ_ERRBIT_SEQLEN  (1u << 1) /* seq_lens[b] < 0 or > MP * page_size */
-#define KVQ_ERRBIT_POS     (1u << 2) /* append position outside [0, MP * page_size) */
-#define KVQ_ERRBIT_REQ     (1u << 3) /* request index outside [0, B) (append, pages update) */
+#define KVQ_ERRBIT_SEQLEN  (1u << 1) /* seq_lens[b] < 0, > MP * page_size, or (ragged steps) below the
+                                        request's rows, or more rows than max_q */
+#define KVQ_ERRBIT_POS     (1u << 2) /* append or read position outside [0, MP * page_size) */
+#define KVQ_ERRBIT_REQ     (1u << 3) /* request index outside [0, B) (append, pages update); a
+                                        tok_start pair out of order or range (ragged steps) */
 #define KVQ_ERRBIT_TIMEOUT (1u << 4) /* a bounded wait inside a kernel gave up (no result) */
 #define KVQ_ERRBIT_EXHAUSTED (1u << 5) /* kvq_pages_update: an acquisition found too few free pages */
 
@@ -451,8 +455,10 @@ KVQ_API size_t kvq_block_attn_workspace_size(int32_t B, int32_t max_q, int32_t H
  * [n_tokens][Hq][head_dim], contiguous; sums and softmax statistics fp32.
  * max_q (>= 1): no request has more rows; one that does is treated as having
  * a bad length (KVQ_ERRBIT_SEQLEN).  Any number of rows is computed; the
- * kernel is built for decode and drafted tokens (up to 128 rows times heads
- * a kv head share one read of the cache).  abort_mask (uint8 [B], nullable):
+ * kernels are built for decode and drafted tokens: a request's rows, times heads
+ * a kv head, share one read of the cache in blocks of 32 (head_dim 128 and more
+ * than 16 of them, or more than 8 where MP * page_size >= 4096) or 128 (else).
+ * Against exact arithmetic the result is as near as an fp32 evaluation's.  abort_mask (uint8 [B], nullable):
  * an aborted request's pages are not read and its rows are zero.  A page
  * outside the pool raises KVQ_ERRBIT_PAGE and zeroes the request's rows that
  * would read it.  A scale is any positive finite fp32.  Values at positions

@@ -276,6 +276,34 @@ def test_append_prompts(kvq, H, P, D):
     assert_cache(c, pools, scales)
 
 
+def mixed(rng, H, P, D):
+    """Rows of decode and draft steps with parts of two prompts among them."""
+    n = np.array([1] * 30 + [9 * P + 3] + [2, 0, 5] * 5 + [1] * 25 + [4 * P, 1])
+    return R.Step(rng, n, n + rng.integers(0, 70, len(n)), H, P, D, pad=3)
+
+
+@pytest.mark.parametrize("H,P,D", [(8, 16, 128), (3, 32, 64), (1, 64, 128)])
+def test_append_prompt_parts_among_decode_rows(kvq, H, P, D):
+    rng = np.random.default_rng([H, P, D, 6])
+    s = mixed(rng, H, P, D)
+    (kt, kx), (vt, vx) = R.values(rng, s.N, H, D), R.values(rng, s.N, H, D)
+    table, lens = s.table.copy(), s.lens.copy()
+    table[30, (lens[30] - 1) // P - 1] = -1  # a bad page late in the first prompt's part
+    lens[0] = -5
+    pools, scales = [s.k.copy(), s.v.copy()], s.scales.copy()
+    R.append(pools, scales, [kx, vx], s.tok_start, lens, table)
+    c, err = run_append(kvq, s, (kt, vt), lens=lens, table=table)
+    assert err == kvq.ERRBIT_SEQLEN | kvq.ERRBIT_PAGE
+    assert_cache(c, pools, scales)
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("H,P,D,rd", [(8, 16, 128, 128), (3, 32, 64, 48), (1, 64, 128, 64)])
+def test_rope_append_prompt_parts_among_decode_rows(kvq, half, H, P, D, rd):
+    rng = np.random.default_rng([H, P, D, rd, 7])
+    check_rope_append(kvq, mixed(rng, H, P, D), rng, 5 * H, rd, half)
+
+
 @pytest.mark.parametrize("half", [True, False])
 @pytest.mark.parametrize("H,P,D,rd", [(8, 16, 128, 128), (3, 64, 64, 32), (4, 32, 128, 96),
                                       (2, 64, 128, 128), (1, 16, 128, 64)])
