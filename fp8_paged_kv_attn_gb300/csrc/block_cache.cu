@@ -951,7 +951,7 @@ kvq_status append_impl(const kvq_block_cache *cache, const kvq_rope_desc *rope, 
     // a request's own CTAs do two pages each; what one can have beyond is shared
     const int own = 2 * static_cast<int>(gy);
     // (not in a step of a row a request, which they would slow down: 3.0 to 3.6 us)
-    const int64_t beyond = (n_tokens + P - 2) / P + 1 - own;
+    const int64_t beyond = (static_cast<int64_t>(n_tokens) + P - 2) / P + 1 - own;
     const int64_t extra = beyond <= 0 || n_tokens <= B
                               ? 0 : (std::min<int64_t>(beyond * shares, 3 * sms) + gy - 1) / gy;
     using ShortFn = void (*)(BlockAppendArgs, int, int, int);

@@ -406,7 +406,8 @@ KVQ_API kvq_status kvq_rope(const kvq_rope_desc *rope, const int32_t *pos, int32
  * block, whose old scale is not read).  Slots past the request's length are
  * not written.  A table entry outside the pool raises KVQ_ERRBIT_PAGE and
  * its tokens are not written.  Appending the same rows again at the same
- * positions changes nothing. */
+ * positions changes nothing.  Requests of one call may share pages that they
+ * only read; a page that two of them write holds unspecified codes. */
 KVQ_API kvq_status kvq_block_append(const kvq_block_cache *cache, const void *k_new,
                                     int64_t k_stride, const void *v_new, int64_t v_stride,
                                     const int32_t *tok_start, int32_t n_tokens,

@@ -148,6 +148,36 @@ def test_long_sums_do_not_drift(kvq, H, G, n, L, D):
     assert np.array_equal(again[keep], got[keep])
 
 
+@pytest.mark.parametrize("n,L", [(8, 9100), (1, 9100)])
+def test_long_contexts_with_scales_far_apart(kvq, n, L):
+    """Scales that grow and shrink by 2^60 over thousands of tokens of one CTA: the
+    references move before and after long sums leave the tensor core."""
+    rng = np.random.default_rng([n, L])
+    s = R.Step(rng, [n], [L], 1, 16, 128)
+    pages = s.table[0, :-(-L // 16)]
+    at = np.arange(len(pages))
+    s.scales[pages, 0, 1] = np.exp2(np.round(30 * np.sin(at / 90.0) + rng.integers(-3, 4, len(at))))
+    s.scales[pages, 0, 0] = np.exp2(rng.integers(-9, -6, len(at)))
+    B, few = 160, 4
+    q, qx = R.values(rng, B * n, 4, 128)
+    ts, lens = (np.arange(B + 1) * n).astype(np.int32), np.full(B, L, dtype=np.int32)
+    s.B = B
+    got, err = attend(kvq, s, q, n, tok_start=ts, lens=lens, table=np.repeat(s.table, B, 0))
+    assert err == 0
+    want, tol = R.attend([s.k, s.v], s.scales, qx[:few * n], ts[:few + 1], lens[:few],
+                         np.repeat(s.table, few, 0), 128 ** -0.5, max_q=n)
+    compare(got[:few * n], want, tol)
+
+
+@pytest.mark.parametrize("H,G,D,P", [(2, 4, 128, 16), (1, 3, 64, 32), (3, 1, 128, 64)])
+def test_prompt_parts_among_decode_rows(kvq, H, G, D, P):
+    """Many row blocks of one request beside single rows."""
+    rng = np.random.default_rng([H, G, D])
+    n = [1] * 9 + [150] + [1, 3, 0, 1] + [70]
+    s = R.Step(rng, n, np.add(n, rng.integers(0, 400, len(n))), H, P, D, pad=2)
+    check(kvq, s, H * G)
+
+
 def test_many_drafts(kvq):
     rng = np.random.default_rng(14)
     n = rng.integers(0, 5, 700)
