@@ -15,7 +15,7 @@
 // head and all its rows (in blocks of up to 128 rows x heads a kv head, of 32 in the
 // tcgen05 kernel).  Measured: 64 requests of 8,193 - 9,216 tokens, 8 kv heads of 128, 4
 // heads a kv head, one row: 174 us, 97% of the measured copy rate; 8 heads a kv head,
-// 512 - 65,536 tokens, pages of 64: 294 us, 95%; 8 requests of 8,193 tokens: 31 us, 65%
+// 512 - 65,536 tokens, pages of 64: 296 us, 94%; 8 requests of 8,193 tokens: 30 us, 66%
 // (3 us until the first bytes are asked for, 4 for the cut rows).
 //
 //   split   persistent CTAs; the requests' (kv-head group, row block) rows, in
