@@ -90,25 +90,21 @@ struct PageItem {
   int first;         // position of the first row
   int slot0, nrow;   // slots [slot0, slot0 + nrow) of the page
   int64_t row0;
-  int part;          // share of the page (short kernel)
 };
 
 template <bool kLens>
 __device__ __forceinline__ bool next_page(const Ragged &rg, const int32_t *block_table, int MP,
-                                          int P, int num_pages, int parts, PageWalk &w,
-                                          PageItem &it) {
+                                          int P, int num_pages, PageWalk &w, PageItem &it) {
   if (w.left <= 0) return false;
   Rows rq = request_rows<kLens>(rg, w.b);
-  while (w.in >= pages_touched(rq, P) * parts) {
+  while (w.in >= pages_touched(rq, P)) {
     ++w.b;
     w.in = 0;
     rq = request_rows<kLens>(rg, w.b);
   }
-  const int pg = parts == 1 ? static_cast<int>(w.in) : static_cast<int>(w.in / parts);
-  it.part = static_cast<int>(w.in - static_cast<int64_t>(pg) * parts);
+  const int lp = rq.p0 / P + static_cast<int>(w.in);
   ++w.in;
   --w.left;
-  const int lp = rq.p0 / P + pg;
   const int page = __ldg(block_table + static_cast<int64_t>(w.b) * MP + lp);
   it.page = page >= 0 && page < num_pages ? page : -1;
   it.first = max(rq.p0, lp * P);
@@ -120,12 +116,12 @@ __device__ __forceinline__ bool next_page(const Ragged &rg, const int32_t *block
 
 // The CTA's run of pages (every thread calls it).
 template <int NT, bool kLens>
-__device__ __forceinline__ PageWalk page_run(const Ragged &rg, int P, int parts, uint32_t *err_word,
+__device__ __forceinline__ PageWalk page_run(const Ragged &rg, int P, uint32_t *err_word,
                                              RunScan<NT> &scan) {
   const RunStart run = find_run<NT>(rg.B, gridDim.x, blockIdx.x, scan, [&](int b) -> int64_t {
     const Rows r = request_rows<kLens>(rg, b);
     if (r.err && blockIdx.x == 0) report(err_word, r.err);
-    return pages_touched(r, P) * parts;
+    return pages_touched(r, P);
   });
   return {min(run.per, run.total - blockIdx.x * run.per), run.in, run.b};
 }
@@ -421,10 +417,10 @@ __global__ void __launch_bounds__(kBcThreads, kRope ? 2 : 3) block_append_wide(B
   allow_dependents();
   if constexpr (kRope)
     if (threadIdx.x < rd / 2) s_freq[threadIdx.x] = turns_per_token(a.rope.inv_freq[threadIdx.x]);
-  PageWalk walk = page_run<kBcThreads, true>(a.rg, P, 1, a.err_word, scan);
+  PageWalk walk = page_run<kBcThreads, true>(a.rg, P, a.err_word, scan);
   PageItem it;
   uint32_t round = 0;
-  while (next_page<true>(a.rg, a.block_table, a.MP, P, a.c.num_pages, 1, walk, it)) {  // uniform
+  while (next_page<true>(a.rg, a.block_table, a.MP, P, a.c.num_pages, walk, it)) {  // uniform
     if (it.page < 0) {
       if (threadIdx.x == 0) report(a.err_word, KVQ_ERRBIT_PAGE);
       continue;
@@ -621,7 +617,7 @@ __global__ void __launch_bounds__(kBcThreads + 32, 2)
   allow_dependents();
   if constexpr (kRope)
     if (threadIdx.x < rd / 2) s_freq[threadIdx.x] = turns_per_token(a.rope.inv_freq[threadIdx.x]);
-  PageWalk walk = page_run<kBcThreads + 32, true>(a.rg, P, 1, a.err_word, ctl.scan);  // syncs
+  PageWalk walk = page_run<kBcThreads + 32, true>(a.rg, P, a.err_word, ctl.scan);  // syncs
 
   if (warp == kBcWarps) {
     // ------------------------------------------------------------ producer
@@ -630,7 +626,7 @@ __global__ void __launch_bounds__(kBcThreads + 32, 2)
     int slot = 0;
     bool ok = true;
     PageItem it;
-    while (ok && next_page<true>(a.rg, a.block_table, a.MP, P, a.c.num_pages, 1, walk, it)) {
+    while (ok && next_page<true>(a.rg, a.block_table, a.MP, P, a.c.num_pages, walk, it)) {
       if (it.page < 0) {
         if (lane == 0) report(a.err_word, KVQ_ERRBIT_PAGE);
         continue;
@@ -798,9 +794,9 @@ __global__ void __launch_bounds__(kBcThreads) block_read_kernel(BlockReadArgs a)
   const int i = lane % kLanes, r0 = lane / kLanes;
   grid_dependency_wait();
   allow_dependents();
-  PageWalk walk = page_run<kBcThreads, false>(a.rg, P, 1, a.err_word, scan);
+  PageWalk walk = page_run<kBcThreads, false>(a.rg, P, a.err_word, scan);
   PageItem it;
-  while (next_page<false>(a.rg, a.block_table, a.MP, P, a.c.num_pages, 1, walk, it)) {
+  while (next_page<false>(a.rg, a.block_table, a.MP, P, a.c.num_pages, walk, it)) {
     if (it.page < 0) {
       if (threadIdx.x == 0) report(a.err_word, KVQ_ERRBIT_PAGE);
       continue;
