@@ -18,7 +18,7 @@
 //          token and kv head, 4 D a query head).  A producer warp stages the
 //          rows of a page and a group of heads with one TMA copy each into a
 //          shared-memory ring; a consumer warp takes 16 rows of one head.  64
-//          prompts of 8,192 tokens: 497 us, 96% of the measured copy rate.
+//          prompts of 8,192 tokens: 497 - 507 us, 94 - 96% of the measured copy rate.
 //   wide   prompts with few kv heads: the same without the ring, a warp's 16
 //          rows loaded by itself.
 // Reading back has one kernel: 48 ragged prefixes 215 us, 97%.

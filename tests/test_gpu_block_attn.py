@@ -235,6 +235,61 @@ def test_large_scores(kvq):
         compare(got, want, tol)
 
 
+@pytest.mark.parametrize("sm", [0.0, -0.05])
+def test_zero_and_negative_score_scale(kvq, sm):
+    rng = np.random.default_rng(15)
+    s = R.Step(rng, [2, 1, 3], [150, 33, 300], 2, 16, 128)
+    q, qx = R.values(rng, s.N, 8, 128)
+    for max_q in (3, 5):
+        want, tol = R.attend([s.k, s.v], s.scales, qx, s.tok_start, s.lens, s.table, sm, max_q=max_q)
+        got, err = attend(kvq, s, q, max_q, sm=sm)
+        assert err == 0
+        compare(got, want, tol)
+
+
+def test_infinite_and_nan_queries_stay_in_their_rows(kvq):
+    """A row of q with an inf or a NaN is NaN; the rows beside it are as ever."""
+    rng = np.random.default_rng(16)
+    s = R.Step(rng, [3, 2], [90, 40], 2, 16, 128)
+    q, qx = R.values(rng, s.N, 8, 128)
+    for max_q in (3, 5):
+        base, _ = attend(kvq, s, q, max_q)
+        bad = q.clone()
+        bad[1, 2, 7], bad[3, 5, 100] = float("inf"), float("nan")
+        got, err = attend(kvq, s, bad, max_q)
+        assert err == 0
+        hit = np.zeros((s.N, 8), dtype=bool)
+        hit[1, 2] = hit[3, 5] = True
+        assert np.isnan(got[hit]).all() and np.array_equal(got[~hit], base[~hit])
+
+
+def test_two_graphs_share_a_workspace(kvq):
+    """Graphs of calls of different sizes replayed in turn over one workspace."""
+    rng = np.random.default_rng(17)
+    steps = [R.Step(rng, [4, 1, 2], [700, 5, 90], 2, 16, 128), R.Step(rng, [1] * 9, [300] * 9, 2, 16, 128),
+             R.Step(rng, [8, 8], [5000, 64], 2, 16, 128)]
+    ws = torch.empty(max(kvq.kvq_block_attn_workspace_size(s.B, int(s.n.max()), 8, 2, 128) for s in steps),
+                     dtype=torch.uint8, device="cuda")
+    runs = []
+    for s in steps:
+        q, _ = R.values(rng, s.N, 8, 128)
+        n = int(s.n.max())
+        want, _ = attend(kvq, s, q, n)
+        args = (cache_of(kvq, s), q.cuda(), dev(s.tok_start), dev(s.lens), dev(s.table),
+                torch.zeros(s.N, 8, 128, device="cuda"), ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            kvq.kvq_block_attn(*args, max_q=n)
+        runs.append((graph, args, want))
+    for k in (0, 1, 2, 1, 0, 2):
+        graph, args, want = runs[k]
+        args[5].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(args[5].cpu().numpy(), want)
+
+
 def test_nan_codes_stay_where_they_are_not_seen(kvq):
     """NaN codes behind a request's end, in unused pages and in drafted tokens
     that earlier rows do not see; a row that sees one is NaN."""
