@@ -76,7 +76,7 @@ struct BaShape {
 // takes for 8, but starts and ends a row of work more slowly.  Measured (8 kv heads
 // of 128, us, mma.sync and tcgen05): 32 requests of 1,024 - 16,384 tokens, 12 rows 116
 // and 99, 16 rows 121 and 100, 32 rows 197 and 102; 128 requests of 64 - 1,024, 16 rows
-// 50 and 62, 32 rows 84 and 63.  So it takes more than 16 rows always, and 9 - 16
+// 50 and 60, 32 rows 84 and 61.  So it takes more than 16 rows always, and 9 - 16
 // where requests can be long: the two meet near 1,600 tokens, taken as half of what
 // the block table holds.
 constexpr int64_t kTcLong = 4096;
