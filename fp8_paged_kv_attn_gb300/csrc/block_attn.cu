@@ -12,8 +12,8 @@
 // small values with a large one.  out = 2^(n - m) o / l.
 //
 // Bound: HBM.  A request's K and V are read once for all query heads of a kv
-// head and all its rows (in blocks of up to 128 rows x heads a kv head, of 32 in the
-// tcgen05 kernel).  Measured: 64 requests of 8,193 - 9,216 tokens, 8 kv heads of 128, 4
+// head and all its rows, in blocks of 32 rows x heads a kv head, or 128 (ba_shape).
+// Measured: 64 requests of 8,193 - 9,216 tokens, 8 kv heads of 128, 4
 // heads a kv head, one row: 174 us, 97% of the measured copy rate; 8 heads a kv head,
 // 512 - 65,536 tokens, pages of 64: 296 us, 94%; 8 requests of 8,193 tokens: 30 us, 66%
 // (3 us until the first bytes are asked for, 4 for the cut rows).
@@ -59,8 +59,11 @@ constexpr int kBaSmem = 225 * 1024;              // ring + merge slots + control
 constexpr int kStat = 4;                         // floats after a row's accumulators: m, l, n, -
 
 // Row tiles: 4 (one MMA column block carries the weights and their remainders),
-// 8 or 16 rows a warp; larger row counts take RT tiles of 16.  The warps that
-// the (head, row tile) pairs leave free are further teams.
+// 8 or 16 rows a warp; larger row counts take RT tiles of 16: two, and beyond 128 rows
+// all eight warps.  (Blocks of 32 rows fit requests of different rows better: 24 drafts of
+// 4 - 16 rows x 6 heads, head_dim 64, 18.9 us against 20.5 with 128, 32 of 1 - 16 rows x 4
+// heads over long contexts 236 against 274; 64 rows x 4 heads 64.7 against 60.3.)  The
+// warps that the (head, row tile) pairs leave free are further teams.
 
 struct BaShape {
   int rk, rt, hg, tw;   // rows a warp, row tiles, heads a stage, teams
@@ -95,8 +98,7 @@ inline BaShape ba_shape(int max_q, int G, int Hkv, int D, int64_t capacity) {
     return s;
   }
   s.rk = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
-  s.rt = 1;
-  while (s.rt < kBaWarps && s.rk * s.rt < rows) s.rt *= 2;
+  s.rt = rows <= 16 ? 1 : rows <= 128 ? 2 : kBaWarps;
   s.rows = s.rk * s.rt;
   s.row_blocks = static_cast<int>((rows + s.rows - 1) / s.rows);
   s.hg = 1;

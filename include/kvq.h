@@ -457,8 +457,8 @@ KVQ_API size_t kvq_block_attn_workspace_size(int32_t B, int32_t max_q, int32_t H
  * max_q (>= 1): no request has more rows; one that does is treated as having
  * a bad length (KVQ_ERRBIT_SEQLEN).  Any number of rows is computed; the
  * kernels are built for decode and drafted tokens: a request's rows, times heads
- * a kv head, share one read of the cache in blocks of 32 (head_dim 128 and more
- * than 16 of them, or more than 8 where MP * page_size >= 4096) or 128 (else).
+ * a kv head, share one read of the cache in blocks of 32, or of 128 where head_dim
+ * is 64 and max_q allows more than that.
  * Against exact arithmetic the result is as near as an fp32 evaluation's.  abort_mask (uint8 [B], nullable):
  * an aborted request's pages are not read and its rows are zero.  A page
  * outside the pool raises KVQ_ERRBIT_PAGE and zeroes the request's rows that
