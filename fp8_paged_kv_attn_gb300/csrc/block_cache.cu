@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kBcThreads, kRope ? 2 : 3) block_append_wide(B
     const int sub = team == 1 ? 0 : warp % team;
     const int wbase = team == 1 ? it.slot0 : kRowsPerWarp * sub;
     const int lo = max(it.slot0, wbase), hi = min(it.slot0 + it.nrow, wbase + kRowsPerWarp);
-    for (int u0 = 0; u0 < 2 * H; u0 += kBcWarps / team, ++round) {
+    for (int u0 = 0; u0 < 2 * H; u0 += kBcWarps / team) {
       const int u = u0 + warp / team;  // (head, K or V)
       const bool live = u < 2 * H;
       const int h = u >> 1, is_v = u & 1;
@@ -481,7 +481,10 @@ __global__ void __launch_bounds__(kBcThreads, kRope ? 2 : 3) block_append_wide(B
           return m;
         });
       if (team > 1) {  // uniform over the CTA
+        // two buffers, taken in turn by the rounds that have this barrier and by no others:
+        // a warp that writes one again has passed the barrier behind its last reads
         float *m = s_amax[round & 1];
+        ++round;
         if (lane == 0) m[warp] = amax;
         __syncthreads();
         const int t0 = warp - sub;
