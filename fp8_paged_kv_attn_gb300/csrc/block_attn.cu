@@ -1207,12 +1207,14 @@ extern "C" kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q
   if (Hq <= 0 || Hq % Hkv || max_q <= 0 || !std::isfinite(sm_scale)) return KVQ_ERR_INVALID_ARG;
   const int G = Hq / Hkv;
   if (static_cast<int64_t>(max_q) * G > INT32_MAX / 2) return KVQ_ERR_INVALID_ARG;
+  // the kernels' token counters are 32 bits and run on to the end of a tile (128) and past it
+  const int64_t capacity = static_cast<int64_t>(MP) * cache->page_size;
+  if (capacity > INT32_MAX - 255) return KVQ_ERR_INVALID_ARG;
   if (n_tokens == 0 || B == 0) return KVQ_OK;
   if (!seq_lens || !out || !workspace || !aligned16(out) || !rows_ok(q, q_stride, Hq, D))
     return KVQ_ERR_INVALID_ARG;
   int sms = 0;
   if (device_sm_count(&sms) != KVQ_OK) return KVQ_ERR_CUDA;
-  const int64_t capacity = static_cast<int64_t>(MP) * cache->page_size;
   const BaShape s = ba_shape(max_q, G, Hkv, D, capacity);
   const size_t cb = ba_cut_bytes(sms);
   if (!aligned256(workspace) || workspace_bytes < cb + ba_part_bytes(s, D, sms) + ba_kept_bytes(s, sms))

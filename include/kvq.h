@@ -455,7 +455,8 @@ KVQ_API size_t kvq_block_attn_workspace_size(int32_t B, int32_t max_q, int32_t H
  * with g = h / (Hq / num_kv_heads); q bf16 strided by token, out fp32
  * [n_tokens][Hq][head_dim], contiguous; sums and softmax statistics fp32.
  * max_q (>= 1): no request has more rows; one that does is treated as having
- * a bad length (KVQ_ERRBIT_SEQLEN).  Any number of rows is computed; the
+ * a bad length (KVQ_ERRBIT_SEQLEN).  MP * page_size is at most 2^31 - 256.  Any
+ * number of rows is computed; the
  * kernels are built for decode and drafted tokens: a request's rows, times heads
  * a kv head, share one read of the cache in blocks of 32, or of 128 where head_dim
  * is 64 and max_q allows more than that.
