@@ -274,6 +274,16 @@ __device__ __forceinline__ void ba_begin(BaState<D, RK> &st, const BaArgs &a, co
   }
 }
 
+// A V scale as 2^e times a fraction in (1/2, 1] (1 for a power of two), x the fraction and y
+// e: from the bits, since 2^-e has no fp32 for the scales above 2^126, and a subnormal scale's
+// weights would sit low in f16's range with e = -126.  0 is 0 times a power of two.
+__device__ __forceinline__ float2 split_scale(float s) {
+  const bool sub = s < 0x1p-126f;
+  const uint32_t u = __float_as_uint(sub ? s * 0x1p24f : s), frac = u & 0x7FFFFFu;
+  const int e = static_cast<int>(u >> 23) - (sub ? 151 : 127) + (frac ? 1 : 0);
+  return make_float2(frac ? __uint_as_float(frac | 0x3F000000u) : u ? 1.f : 0.f, static_cast<float>(e));
+}
+
 // The product alone, with no sum before it.
 __device__ __forceinline__ void mma_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                                 uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -461,15 +471,12 @@ __device__ __forceinline__ void ba_tiles(BaState<D, RK> &st, const uint8_t *cons
                     e4m3x2_to_f16x2(kw[t][j][k] & 0xFFFFu), e4m3x2_to_f16x2(kw[t][j][k] >> 16));
   }
   const bool partial = tok0 + NT * kTile > min_lim;  // uniform over the warp
-  // log2 of the V scales, rounded up (exact for a power of two), and the
-  // scales' fractions, in (0.5, 1]
-  float lv[NT], vm[NT];
+  float lv[NT], vm[NT];  // the V scales' exponents and fractions
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const uint32_t u = __float_as_uint(sc[t].y);
-    const int e = static_cast<int>(u >> 23) - 127 + ((u & 0x7FFFFFu) ? 1 : 0);
-    lv[t] = static_cast<float>(e);
-    vm[t] = sc[t].y * pow2(max(-126, min(127, -e)));
+    const float2 v = split_scale(sc[t].y);
+    vm[t] = v.x;
+    lv[t] = v.y;
   }
   float x[NG][NT][2][2], mx[NG], mv[NG];
   bool any = false;

@@ -643,9 +643,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) mbar_arrive(&ctl.sfree[grp]);
         const bool partial = tok0 + kTcTok > min_lim;
         const float2 sc = ctl.sc[slot][gw];
-        const uint32_t ub = __float_as_uint(sc.y);
-        const int e_v = static_cast<int>(ub >> 23) - 127 + ((ub & 0x7FFFFFu) ? 1 : 0);
-        const float lv = static_cast<float>(e_v), vm = sc.y * pow2(max(-126, min(127, -e_v))), f = qk * sc.x;
+        const float2 v_scale = split_scale(sc.y);
+        const float vm = v_scale.x, lv = v_scale.y, f = qk * sc.x;
         float mx = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
