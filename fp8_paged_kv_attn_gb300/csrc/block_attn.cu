@@ -284,6 +284,16 @@ __device__ __forceinline__ float2 split_scale(float s) {
   return make_float2(frac ? __uint_as_float(frac | 0x3F000000u) : u ? 1.f : 0.f, static_cast<float>(e));
 }
 
+// 2^t / l as two factors, to be multiplied with in turn: a sum is undone by 2^t for t = n - m
+// (and the operand's scale), and neither that power nor its quotient need have an fp32 where
+// V scales are very large or small, or l is, behind a maximum that grew.  Where t is harmless
+// the second factor is the power of two in 1 / l, and nothing is rounded twice.
+__device__ __forceinline__ float2 out_scale(float t, float l) {
+  const int k = max(-126, min(126, static_cast<int>(__float_as_uint(l) >> 23) - 127));
+  const float u = fminf(fmaxf(t, -100.f), 40.f);
+  return make_float2(exp2f(u) / (l * pow2(-k)), exp2f(t - u - static_cast<float>(k)));
+}
+
 // The product alone, with no sum before it.
 __device__ __forceinline__ void mma_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                                 uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -971,13 +981,13 @@ __global__ void __launch_bounds__(kBaThreads, 1)
         const float l = e ? lb : la, m = e ? mb : ma, n = e ? nb : na;
         if (sg.part < 0) {
           // 2^(n - m) / (l 2^7); a bad row is zeros, selected and not scaled
-          const float f = l < 0.f ? 0.f : exp2f(n - m - 7.f) / l;
+          const float2 f = out_scale(n - m - 7.f, l);
           float *o = ba_out_row<D>(a, sg, kvh, row_base + r) + (D / 8) * gq;
 #pragma unroll
           for (int i = 0; i < KS; ++i)
             *reinterpret_cast<float2 *>(o + 2 * i) =
                 l < 0.f ? make_float2(0.f, 0.f)
-                        : make_float2(st.o[i][g][e] * f, st.o[i][g][2 + e] * f);
+                        : make_float2(st.o[i][g][e] * f.x * f.y, st.o[i][g][2 + e] * f.x * f.y);
         } else {
           float *o = to + r * RF;
 #pragma unroll
@@ -1094,9 +1104,9 @@ __global__ void __launch_bounds__(32 * kBcbWarps) block_combine_kernel(BaArgs a,
   const int i = r / a.G;
   float *out = a.out + ((static_cast<int64_t>(row0) + i) * a.Hq + (grp * a.hg + head) * a.G + r - i * a.G) * D;
   if constexpr (!kWide) {
-    const float f = bad ? 0.f : exp2f(N - M - 7.f) / l;
+    const float2 f = out_scale(N - M - 7.f, l);
 #pragma unroll
-    for (int k = 0; k < V; ++k) out[lane + 32 * k] = bad ? 0.f : acc[k] * f;
+    for (int k = 0; k < V; ++k) out[lane + 32 * k] = bad ? 0.f : acc[k] * f.x * f.y;
   } else {
 #pragma unroll
     for (int k = 0; k < V; ++k) s_acc[warp][lane + 32 * k] = acc[k];
@@ -1117,7 +1127,8 @@ __global__ void __launch_bounds__(32 * kBcbWarps) block_combine_kernel(BaArgs a,
         lr = fmaf(exp2f(s_st[w].x - Mr), s_st[w].y, lr);
         o = fmaf(exp2f(s_st[w].z - Nr), s_acc[w][threadIdx.x], o);
       }
-      out[threadIdx.x] = rbad ? 0.f : o * (exp2f(Nr - Mr - 7.f) / lr);
+      const float2 f = out_scale(Nr - Mr - 7.f, lr);
+      out[threadIdx.x] = rbad ? 0.f : o * f.x * f.y;
     }
   }
 }

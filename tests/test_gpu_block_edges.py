@@ -65,3 +65,80 @@ def test_largest_value_scales(kvq, D, max_q):
     got, err = attend(kvq, s, q, max_q)
     assert err == 0
     compare(got, want, tol)
+
+
+MANY = 320  # requests over the same pages: more than CTAs, so that one sums whole rows
+
+
+def one_dim(s, scores, Hq):
+    """Makes score j of every row scores[j] * ln 2, at score scale ln 2: q and K are 0 but in one dim,
+    so that a score is one exact product.  Copies the first request MANY times; returns q."""
+    s.k[:] = 0
+    codes = R.encode(scores / 16.0)
+    assert (R.decode(codes) * 16.0 == scores).all()
+    s.scales[:, :, 0] = 1.0
+    at = np.arange(len(scores))
+    s.k[s.table[0][at // s.P], :, at % s.P, 5] = codes[:, None]
+    s.B = s.N = MANY
+    s.n, s.lens = np.ones(MANY, dtype=np.int32), np.full(MANY, len(scores), dtype=np.int32)
+    s.tok_start, s.table = np.arange(MANY + 1, dtype=np.int32), np.repeat(s.table, MANY, 0)
+    q = np.zeros((MANY, Hq, s.D))
+    q[:, :, 5] = 16.0
+    return R.bf16(q)
+
+
+def exact(s, scores, G, magnitude=False):
+    """Softmax of 2^scores times the values (or their magnitudes): [heads, D]."""
+    v = R.gather(s.v & 0x7F if magnitude else s.v, s.scales, 1, s.table[0], np.arange(len(scores)))
+    w = np.exp2(scores - scores.max())
+    return np.repeat(np.einsum("j,jhd->hd", w, v) / w.sum(), G, 0)
+
+
+def roundings(top, L):
+    """Relative error of weights and sums where scores are exact products of at most `top` ln 2: a
+    score's factor is rounded three times, 3 2^-24; a weight's exponential and pieces leave 2^-21 and
+    2^-18; sums add (L / 16 + 64) 2^-24; all of it twice, for the denominator."""
+    return 2 * (top * np.log(2) * 3 * 2.0 ** -24 * 2 + 2.0 ** -21 + 2.0 ** -18 + (L / 16 + 64) * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("D,max_q", [(64, 1), (128, 1), (128, 6)])
+@pytest.mark.parametrize("L", [40, 3000])
+@pytest.mark.parametrize("top", [2.75, 11.0])
+def test_smallest_value_scales(kvq, D, max_q, L, top):
+    """Values near fp32's smallest normal number, in blocks whose scales are subnormal or the
+    library's smallest, 2^-126, among them a token with a larger score (or none) whose block's
+    scale is smaller still.  An output may also be off by 2^-149, fp32's smallest step."""
+    rng = np.random.default_rng([D, max_q, L, 33])
+    G = 4
+    s = R.Step(rng, [1], [L], 1, 16, D)
+    scores = rng.choice([0.4375, 0.8125, 2.75], L)
+    scores[3] = top
+    q = one_dim(s, scores, G)
+    s.v = (s.v & 0x87) | 0x70  # 128 .. 240
+    s.v[s.table[0, 0]] = 0
+    s.scales[:, :, 1] = 2.0 ** -126
+    s.scales[s.table[0, 1::2], :, 1] = np.float32(2.0 ** -126 * 0.8125)
+    s.scales[s.table[0, 0], :, 1] = np.float32(2.0 ** -149)
+    got, err = attend(kvq, s, q, max_q, sm=float(np.log(2.0)))
+    assert err == 0
+    tol = roundings(11, L) * exact(s, scores, G, True) + 2.0 ** -149
+    compare(got, np.broadcast_to(exact(s, scores, G), got.shape), np.broadcast_to(tol, got.shape))
+
+
+@pytest.mark.parametrize("D,max_q", [(64, 1), (128, 1), (128, 6)])
+@pytest.mark.parametrize("e", [60, 90, 110])
+def test_large_values_behind_a_growing_maximum(kvq, D, max_q, e):
+    """Scores that grow by 2^56 within a row whose V scales are 2^e: the factor that undoes the
+    references is applied without overflow."""
+    rng = np.random.default_rng([D, max_q, e, 34])
+    L, G = 700, 4
+    s = R.Step(rng, [1], [L], 1, 16, D)
+    scores = rng.choice([0.4375, 0.8125, 2.75], L)
+    scores[300] = 56.0
+    q = one_dim(s, scores, G)
+    s.v = (s.v & 0x87) | 0x30  # 0.5 .. 0.94
+    s.scales[:, :, 1] = 2.0 ** e
+    got, err = attend(kvq, s, q, max_q, sm=float(np.log(2.0)))
+    assert err == 0
+    tol = roundings(56, L) * exact(s, scores, G, True)
+    compare(got, np.broadcast_to(exact(s, scores, G), got.shape), np.broadcast_to(tol, got.shape))
