@@ -8,8 +8,10 @@
 //   q   a row scaled by 2^e (largest value in [224, 448)) = q1 + q2, e4m3 and e5m2:
 //       exact for values down to 2^-13.8 of the row's largest (tc_q_pieces).
 //       S = q2 K + q1 K in one accumulator.
-//   w   a softmax weight (times 2, at most 2^7) = p1 + p2/2^5 + p3/2^10 + p4/2^15, e4m3
-//       (tc_pieces): off by 2^-19 of w, and by 2^-25 where e4m3 is subnormal.  The
+//   w   a softmax weight (times 2^6, at most 2^7) = p1 + p2/2^5 + p3/2^10 + p4/2^15, e4m3
+//       (tc_pieces): off by 2^-19 of w, and by 2^-24 where f16 and e4m3 are subnormal, that
+//       is by 2^-30 of the row's largest weight: tokens far below an attention sink lose
+//       no more here than in the mma.sync kernel (2^-31).  The
 //       pieces of 32 rows are 128 columns of one product: piece p of row r is
 //       column 32 p + r, and a row's four sums are added when they leave TMEM.
 // Against 64 bits the result is as near as the mma.sync kernel's (1e-6 of the output's
@@ -57,8 +59,12 @@ constexpr int kTcTile = kTcTok * 128;       // 16 KB: one tile of K or V, q piec
 constexpr int kTcRowCost = 4;               // a row's start and end, in tiles' times
 constexpr int kTcFlush = 16;                // tiles whose values a group's sum in TMEM takes
 constexpr int kTcKept = 17 * 32;            // floats that a warp keeps in the workspace
-constexpr float kTcThreshold = 6.f;         // lazy rescaling: weights stay below 2^6
-constexpr float kTcWScale = 2.f;            // and their operand, 2^1 of them, below 2^7
+// Lazy rescaling: weights stay below 2^1, and their operand, 2^6 of them, below 2^7 (the third
+// piece of one above 2^7 could pass e4m3's largest value).  With 2^6 and 2^1 the row's largest
+// operand might be 2^1 only, and tokens 14 nats below a sink lost up to 2^-5 of their weights;
+// the more frequent rescaling takes 0.5% (32 drafts of 1 - 8 rows 106.8 us, so 107.4).
+constexpr float kTcThreshold = 1.f;
+constexpr float kTcWScale = 64.f;
 constexpr float kTcFar = 64.f;              // the denominator's reference may be further off (fp32)
 constexpr uint32_t kTcColS = 0, kTcColO = 256;
 
@@ -713,7 +719,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         any_tile = true;
         const bool none = n == -INFINITY;  // nothing seen yet: every x is -inf
         const float mm = none ? 0.f : m, mn = none ? 0.f : m - n;
-        // vs 2^(m - n), times 2 (kTcThreshold keeps the operand below 2^7)
+        // vs 2^(m - n), times 2^6 (kTcThreshold keeps the operand below 2^7)
         const float d = vm * kTcWScale * fast_exp2(fminf(mn + lv, 112.f));
         float2 l2 = make_float2(0.f, 0.f);
         uint32_t w1[4], w2[4], w3[4], w4[4];
@@ -847,16 +853,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (gl[k] != 0.f) L1 += gl[k] * exp2f(gm[k] - M);
       }
       const bool used = lane < sg.rows;
-      // a partial's row: sums, then m, l, n (n counts the 2^7 of the other kernel)
+      // a partial's row: sums, then m, l, n (n counts the 2^7 of the other kernel, here 2^6)
       const int64_t at = sg.part < 0 ? ((static_cast<int64_t>(sg.row0) + my_i) * a.Hq + sg.head * a.G + row -
                                         my_i * a.G) * 128
                                      : (static_cast<int64_t>(sg.part) * kTcRows + lane) * (128 + kStat);
       float *out = sg.part < 0 ? a.out : a.part;
       {
-        // out = 2^(N - M - 1) sum / l; zeros where a page was bad.  Half of a power far from
+        // out = 2^(N - M - 6) sum / l; zeros where a page was bad.  Half of a power far from
         // 1 goes to the groups' factors (out_scale says why; one more factor a value took 3%
         // of the time of 128 requests of 64 - 1,024 tokens)
-        const float t = N - M - 1.f;
+        const float t = N - M - 6.f;
         const float h = sg.part >= 0 || fabsf(t) <= 60.f ? 0.f : rintf(fminf(fmaxf(0.5f * t, -100.f), 100.f));
         const float scale = sg.part < 0 ? exp2f(t - h) / L1 : 1.f, up = pow2(static_cast<int>(h));
         const bool zero = bad && sg.part < 0;
@@ -884,7 +890,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ok = both_sync();  // the tiles and nan_from are read
       if (!ok) break;
       if (used && sg.part >= 0 && warp == 0)
-        *reinterpret_cast<float4 *>(out + at + 128) = make_float4(M, bad ? -1.f : L1, N + 6.f, 0.f);
+        *reinterpret_cast<float4 *>(out + at + 128) = make_float4(M, bad ? -1.f : L1, N + 1.f, 0.f);
       ++nseg;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.segempty[ss]);

@@ -456,11 +456,16 @@ KVQ_API size_t kvq_block_attn_workspace_size(int32_t B, int32_t max_q, int32_t H
  * [n_tokens][Hq][head_dim], contiguous; sums and softmax statistics fp32.
  * max_q (>= 1): no request has more rows; one that does is treated as having
  * a bad length (KVQ_ERRBIT_SEQLEN).  MP * page_size is at most 2^31 - 256.  Any
- * number of rows is computed; the
- * kernels are built for decode and drafted tokens: a request's rows, times heads
- * a kv head, share one read of the cache in blocks of 32, or of 128 where head_dim
- * is 64 and max_q allows more than that.
- * Against exact arithmetic the result is as near as an fp32 evaluation's.  abort_mask (uint8 [B], nullable):
+ * number of rows is computed; the kernels are built for decode and drafted tokens: a
+ * request's rows, times heads a kv head, share one read of the cache in blocks of 32, or
+ * of 128 where head_dim is 64 and max_q allows more than that.
+ * Error: scores, softmax statistics and sums are fp32; a row of q is held to 2^-21 of its
+ * largest value, a softmax weight to 2^-19 of itself, and to 2^-30 of the row's largest
+ * (each times its V scale, rounded up to a power of two) where that is more.  Against exact
+ * arithmetic that is near an fp32 evaluation's error (0.5 - 1.6 times it), except for tokens
+ * whose weights lie more than 2^11 below that of a token with values near zero (an
+ * attention sink): 2^20, or 14 nats, below it they are right to 2^-10 of themselves.
+ * abort_mask (uint8 [B], nullable):
  * an aborted request's pages are not read and its rows are zero.  A page
  * outside the pool raises KVQ_ERRBIT_PAGE and zeroes the request's rows that
  * would read it.  A scale is any positive finite fp32.  Values at positions

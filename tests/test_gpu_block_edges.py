@@ -142,3 +142,25 @@ def test_large_values_behind_a_growing_maximum(kvq, D, max_q, e):
     assert err == 0
     tol = roundings(56, L) * exact(s, scores, G, True)
     compare(got, np.broadcast_to(exact(s, scores, G), got.shape), np.broadcast_to(tol, got.shape))
+
+
+@pytest.mark.parametrize("L,max_q", [(300, 1), (300, 6), (9000, 1), (9000, 6)])
+@pytest.mark.parametrize("gap", [16, 18, 20, 22, 24])
+def test_tokens_below_a_sink_without_value(kvq, gap, L, max_q):
+    """The first token's score is about gap ln 2 above the others', its values are zero: the others'
+    weights are the output.  include/kvq.h: a weight is held to 2^-30 of the row's largest (times
+    their V scales, here equal), that is to 2^(gap - 30) of itself, beside its own roundings."""
+    rng = np.random.default_rng([gap, L, max_q, 35])
+    G, D = 4, 128
+    s = R.Step(rng, [1], [L], 1, 16, D)
+    scores = np.full(L, {16: 0.4375, 18: 0.5625, 20: 0.625, 22: 0.8125, 24: 0.875}[gap])  # fractions: weights of all bits
+    scores[0] = gap
+    q = one_dim(s, scores, G)
+    s.v = (s.v & 0x07) | 0x38  # 1 .. 1.875, one sign: equal roundings do not even out
+    s.v[s.table[0, 0], :, 0] = 0
+    s.scales[:, :, 1] = 1.0
+    got, err = attend(kvq, s, q, max_q, sm=float(np.log(2.0)))
+    assert err == 0
+    want = exact(s, scores, G)
+    tol = (2.0 ** (gap - scores[1] - 30) + roundings(gap, L)) * want
+    compare(got, np.broadcast_to(want, got.shape), np.broadcast_to(tol, got.shape))
