@@ -1202,11 +1202,16 @@ extern "C" size_t kvq_block_attn_workspace_size(int32_t B, int32_t max_q, int32_
   if (static_cast<int64_t>(max_q) * (Hq / num_kv_heads) > INT32_MAX / 2) return 0;
   int sms = 0;
   if (device_sm_count(&sms) != KVQ_OK) return 0;
-  size_t parts = 0;  // the larger of the kernels' that a call of these sizes may take
-  for (int64_t capacity : {int64_t{0}, kTcLong}) {
-    const BaShape s = ba_shape(max_q, Hq / num_kv_heads, num_kv_heads, head_dim, capacity);
-    parts = std::max(parts, ba_part_bytes(s, head_dim, sms) + ba_kept_bytes(s, sms));
-  }
+  // the largest that a call of up to max_q rows may take, by either kernel: fewer rows can need
+  // more (wider head groups, or mma.sync's partials where more rows go to tcgen05), and the
+  // tilings change after 4, 8, 16 and 128 rows (ba_shape)
+  const int rows = max_q * (Hq / num_kv_heads);
+  size_t parts = 0;
+  for (int most : {4, 8, 16, 128, INT32_MAX})
+    for (int64_t capacity : {int64_t{0}, kTcLong}) {
+      const BaShape s = ba_shape(std::min(most, rows), 1, num_kv_heads, head_dim, capacity);
+      parts = std::max(parts, ba_part_bytes(s, head_dim, sms) + ba_kept_bytes(s, sms));
+    }
   return ba_cut_bytes(sms) + parts;
 }
 

@@ -164,3 +164,24 @@ def test_tokens_below_a_sink_without_value(kvq, gap, L, max_q):
     want = exact(s, scores, G)
     tol = (2.0 ** (gap - scores[1] - 30) + roundings(gap, L)) * want
     compare(got, np.broadcast_to(want, got.shape), np.broadcast_to(tol, got.shape))
+
+
+SIZES = [(8, 4, 128), (8, 1, 128), (8, 8, 128), (5, 4, 64), (7, 2, 64), (5, 3, 128), (1, 5, 128), (3, 6, 64)]
+
+
+@pytest.mark.parametrize("H,G,D", SIZES)
+def test_a_workspace_serves_fewer_rows_and_requests(kvq, H, G, D):
+    """Sized for max_q rows of B requests it serves every smaller max_q, over narrow and wide tables."""
+    size = [kvq.kvq_block_attn_workspace_size(4, n, H * G, H, D) for n in range(1, 150)]
+    assert all(a <= b for a, b in zip(size, size[1:]))
+    assert all(kvq.kvq_block_attn_workspace_size(b, 9, H * G, H, D) <= size[8] for b in range(5))
+    most = 40
+    ws = kvq.block_workspace(4, most, H * G, H, D)
+    rng = np.random.default_rng([H, G, D, 36])
+    for n in (1, 2, 3, 4, 5, 8, 9, 16, 17, 32, 33, 40):
+        s = R.Step(rng, [n, 1], [n + 30, 50], H, 16, D)
+        q, _ = R.values(rng, s.N, H * G, D)
+        for table in (s.table, np.pad(s.table, ((0, 0), (0, 256)), constant_values=-1)):
+            got, err = attend(kvq, s, q, n, table=table, ws=ws)
+            own, _ = attend(kvq, s, q, n, table=table)
+            assert err == 0 and np.array_equal(got, own)
