@@ -214,7 +214,7 @@ struct BaState {
   uint32_t qa[NG][2][KS];                      // A fragments: rows gq (+8), words 0 and 2
   float o[KS][NG][4];
   float m[NG], l[NG], n[NG], qk[NG];
-  int lim[NG];                                 // tokens that the lane's row sees
+  int lim[NG];                                 // tokens that the lane's row sees; -1: a bad page among them
 };
 
 // The row of lane group gq in 8-row group g (copies of rows 0..3 in 4..7 for RK 4).
@@ -793,10 +793,14 @@ __global__ void __launch_bounds__(kBaThreads, 1)
           }
         }
         if (lane < a.hg) {
-          if (!bad)
+          if (!bad) {
             cp_async8(&ctl.sc[slot][lane],
                       a.scales + static_cast<int64_t>(page) * a.Hkv + grp * a.hg + lane);
-          cp_async_arrive(&ctl.full[slot]);
+            cp_async_arrive(&ctl.full[slot]);
+          } else {  // tokens that rows without a result see, and others have masked
+            ctl.sc[slot][lane] = make_float2(1.f, 1.f);
+            mbar_arrive(&ctl.full[slot]);
+          }
         }
         ++g;
         if (++slot == NS) {
@@ -851,7 +855,6 @@ __global__ void __launch_bounds__(kBaThreads, 1)
     const int row_base = sg.rb * rows + tile * RK;  // this warp's first row of the request
     ba_begin<D, RK>(st, a, sg, kvh, row_base, gq, tq);
     const int min_lim = min(sg.L, sg.L - sg.n + 1 + (sg.rb * rows) / a.G);
-    bool seg_bad = false;
     // the ring slot and phase parity of the team's first stage
     int s0 = static_cast<int>((g0 + 2 * team) % NS);
     uint32_t p0 = ((g0 + 2 * team) / NS) & 1;
@@ -862,19 +865,22 @@ __global__ void __launch_bounds__(kBaThreads, 1)
       if (two && !ba_wait_warp(ctl, &ctl.full[s1], s1 == 0 ? p0 ^ 1 : p0, a.err_word)) return;
       const int tok = sg.t_begin + k * kTile;
       const uint32_t off0 = s0 * stage_bytes + head * (kTile * D), off1 = s1 * stage_bytes + head * (kTile * D);
-      // a row that meets a bad page is zeros: its other tiles are skipped with it
-      const bool bad = ctl.bad[s0] || (two && ctl.bad[s1]);
-      seg_bad |= bad;
-      if (!bad) {
-        if (two) {
-          const uint8_t *kp[2] = {kbuf + off0, kbuf + off1}, *vp[2] = {vbuf + off0, vbuf + off1};
-          const float2 sc[2] = {ctl.sc[s0][head], ctl.sc[s1][head]};
-          ba_tiles<D, RK, 2>(st, kp, vp, sc, tok, min_lim, sg.L, gq, tq);
-        } else {
-          const uint8_t *kp[1] = {kbuf + off0}, *vp[1] = {vbuf + off0};
-          const float2 sc[1] = {ctl.sc[s0][head]};
-          ba_tiles<D, RK, 1>(st, kp, vp, sc, tok, min_lim, sg.L, gq, tq);
-        }
+      // a row that sees a bad page is zeros whatever the stage holds; rows that end before it
+      // have it masked, as any token that they do not see
+      if (ctl.bad[s0] || (two && ctl.bad[s1])) {
+        const int from = ctl.bad[s0] ? tok : tok + kTile;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          if (st.lim[g] > from) st.lim[g] = -1;
+      }
+      if (two) {
+        const uint8_t *kp[2] = {kbuf + off0, kbuf + off1}, *vp[2] = {vbuf + off0, vbuf + off1};
+        const float2 sc[2] = {ctl.sc[s0][head], ctl.sc[s1][head]};
+        ba_tiles<D, RK, 2>(st, kp, vp, sc, tok, min_lim, sg.L, gq, tq);
+      } else {
+        const uint8_t *kp[1] = {kbuf + off0}, *vp[1] = {vbuf + off0};
+        const float2 sc[1] = {ctl.sc[s0][head]};
+        ba_tiles<D, RK, 1>(st, kp, vp, sc, tok, min_lim, sg.L, gq, tq);
       }
       __syncwarp();
       if (lane == 0) {
@@ -892,12 +898,12 @@ __global__ void __launch_bounds__(kBaThreads, 1)
     if (lane == 0) mbar_arrive(&ctl.segempty[ss]);
     ++nseg;
 
-    // ---- the segment's end: the row's denominator, marked if a page was bad
+    // ---- the segment's end: the row's denominator, marked if the row sees a bad page
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       st.l[g] += __shfl_xor_sync(0xffffffffu, st.l[g], 1);
       st.l[g] += __shfl_xor_sync(0xffffffffu, st.l[g], 2);
-      if (seg_bad) st.l[g] = -1.f;
+      if (st.lim[g] < 0) st.l[g] = -1.f;
     }
     if (a.tw > 1) {
       // The teams' sums go to team 0, halving the teams each round.  Every round

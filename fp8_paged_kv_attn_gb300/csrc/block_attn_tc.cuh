@@ -89,7 +89,7 @@ struct TcCtl {
   uint64_t qfull, qfree, sfull[2], sfree[2], pfull[2], pvdone[2];
   uint64_t xch[2], epi, drain;
   float2 sc[kTcV][kTcTok / 16];
-  int bad[kTcV];
+  int bad[kTcV];                   // first token of a page outside the pool, or INT_MAX
   float qk[2][32];                 // [segment & 1]: what undoes q's scale, times sm_scale log2(e)
   float2 mx[2][2][8][32];          // [group][parity][warp][row]: a tile's maxima of x and x + log2 vs
   __align__(16) float grow[kTcWarps][32];  // [warp][row]: what a rescaling multiplies by
@@ -453,10 +453,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const bool needed = lane < 8 && mine < L;
         const bool good = needed && page >= 0 && page < a.num_pages;
         const uint32_t goods = __ballot_sync(0xffffffffu, good);
-        const bool bad = __any_sync(0xffffffffu, needed && !good);
+        const uint32_t needs = __ballot_sync(0xffffffffu, needed);
         if (lane == 0) {
-          if (is_v) ctl.bad[slot] = bad;
-          if (bad) report(a.err_word, KVQ_ERRBIT_PAGE);
+          if (is_v) ctl.bad[slot] = needs == goods ? INT_MAX : tok + 16 * (__ffs(needs ^ goods) - 1);
+          if (needs != goods) report(a.err_word, KVQ_ERRBIT_PAGE);
           mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(__popc(goods)) * 2048u);
         }
         __syncwarp();
@@ -632,7 +632,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const float qk = ctl.qk[nseg & 1][lane];
       int *nan_from = ctl.nan_from[nseg & 1];
       float m = -INFINITY, n = -INFINITY, l = 0.f;
-      bool seg_bad = false, any_tile = false;
+      bool any_tile = false;
+      int bad_from = INT_MAX;  // rows that see this token are zeros; others have it masked
       for (int t = grp; t < sg.tiles; t += 2) {
         const uint32_t gg = g0 + t;
         const int slot = gg % kTcV;
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ok = tc_wait(ctl, &ctl.sfull[grp], nt & 1, a.err_word) &&
              tc_wait(ctl, &ctl.vfull[slot], (gg / kTcV) & 1, a.err_word);
         if (!ok) break;
-        seg_bad |= ctl.bad[slot] != 0;
+        bad_from = min(bad_from, ctl.bad[slot]);
         tc_after();
         float x[16];
         tc_ld16(x, s_addr);
@@ -746,8 +747,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         *reinterpret_cast<uint4 *>(tc_chunk(ptile, 96 + lane, gw)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
         if (partial) {
           // V rows past the end (whatever the slot or the cache holds) become
-          // zeros, and NaN codes of drafted tokens too: a weight of 0 does not stop
-          // a NaN.  Rows that see such a token get their NaN when they are written.
+          // zeros, and NaN codes of drafted tokens (and of a bad page's stale rows) too: a
+          // weight of 0 does not stop a NaN.  Rows that see such a token get their NaN when they are written.
           const int tr = 32 * quad + lane, tok = tok0 + tr;
           uint8_t *vt = vtl + slot * kTcTile;
           if (tok >= sg.L) {
@@ -826,7 +827,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           sum[k] = sum[8 + k];
         }
       }
-      ctl.stat[grp][gw][lane] = make_float4(m, seg_bad ? -1.f : l, n, 0.f);
+      ctl.stat[grp][gw][lane] = make_float4(m, lim > bad_from ? -1.f : l, n, 0.f);
       ok = both_sync();
       if (!ok) break;
       float M = -INFINITY, N = -INFINITY, L1 = 0.f, gm[2], gn[2], gl[2], f[2];
@@ -859,7 +860,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                      : (static_cast<int64_t>(sg.part) * kTcRows + lane) * (128 + kStat);
       float *out = sg.part < 0 ? a.out : a.part;
       {
-        // out = 2^(N - M - 6) sum / l; zeros where a page was bad.  Half of a power far from
+        // out = 2^(N - M - 6) sum / l; zeros where the row sees a bad page.  Half of a power far from
         // 1 goes to the groups' factors (out_scale says why; one more factor a value took 3%
         // of the time of 128 requests of 64 - 1,024 tokens)
         const float t = N - M - 6.f;

@@ -185,3 +185,33 @@ def test_a_workspace_serves_fewer_rows_and_requests(kvq, H, G, D):
             got, err = attend(kvq, s, q, n, table=table, ws=ws)
             own, _ = attend(kvq, s, q, n, table=table)
             assert err == 0 and np.array_equal(got, own)
+
+
+@pytest.mark.parametrize("H,G,D,max_q", [(2, 4, 64, 8), (2, 1, 64, 70), (2, 1, 128, 8), (8, 4, 128, 8),
+                                         (1, 4, 128, 70), (1, 16, 64, 20)])
+@pytest.mark.parametrize("before", [9, 3001])
+def test_bad_page_zeroes_only_the_rows_that_see_it(kvq, H, G, D, max_q, before):
+    """Rows that end before the first token of a page outside the pool are as ever; stale NaN codes
+    of other requests do not reach them."""
+    rng = np.random.default_rng([H, G, D, before, 37])
+    n = [max_q, 2, max_q, max_q]
+    lens = [before + max_q, 40, before + max_q, 13 + max_q]
+    s = R.Step(rng, n, lens, H, 16, D)
+    q, _ = R.values(rng, s.N, H * G, D)
+    base, err = attend(kvq, s, q, max_q)
+    assert err == 0
+    s.v[s.table[1, 0]] = s.v[s.table[3, 0]] = 0x7F  # requests 1 and 3 read NaN
+    table, dead = s.table.copy(), np.zeros(s.N, dtype=bool)
+    last = (lens[0] - 1) // 16
+    for b, lp in ((0, last), (2, max(last - 1, 0))):
+        table[b, lp] = (-1, s.NP)[b == 2]
+        row = np.arange(s.tok_start[b], s.tok_start[b + 1])
+        dead[row] = lens[b] - n[b] + 1 + np.arange(n[b]) > lp * 16
+    got, err = attend(kvq, s, q, max_q, table=table)
+    assert err == kvq.ERRBIT_PAGE
+    mine = np.r_[s.tok_start[0]:s.tok_start[1], s.tok_start[2]:s.tok_start[3]]
+    assert dead[mine].any() and not dead[mine].all()
+    assert (got[dead] == 0).all()
+    keep = mine[~dead[mine]]
+    assert np.array_equal(got[keep], base[keep])
+    assert np.isnan(got[s.tok_start[1]:s.tok_start[2]]).all()
