@@ -464,6 +464,8 @@ def _arr(t, name, dtypes, shape, dev):
 
 def _rows(t, name, n, heads, D, dev):
     """(pointer, token stride) of a bf16 [n, heads, D] tensor strided by token."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
     st = t.stride()
     if t.dtype is not torch.bfloat16 or t.shape != (n, heads, D) or t.get_device() != dev or \
             st[2] != 1 or (st[1] != D and heads > 1):
@@ -576,6 +578,8 @@ def kvq_rope(rope: Rope, pos, q, q_out, k=None, k_out=None, stream=None) -> None
     dev = _device(q, "q")
     qa, qb = _rows(q, "q", N, Hq, D, dev), _rows(q_out, "q_out", N, Hq, D, dev)
     Hk, ka, kb = 0, (None, 0), (None, 0)
+    if k is None and k_out is not None:
+        raise ValueError("k is missing")
     if k is not None:
         Hk = k.shape[1]
         ka, kb = _rows(k, "k", N, Hk, D, dev), _rows(k_out, "k_out", N, Hk, D, dev)
@@ -610,11 +614,13 @@ def kvq_block_append(cache: BlockKVCache, k_new, v_new, tok_start, seq_lens, blo
 def kvq_rope_block_append(cache: BlockKVCache, rope: Rope, q, q_out, k_new, v_new, tok_start,
                           seq_lens, block_table, err_word=None, stream=None) -> None:
     """kvq_block_append with K rotated on the way in, and q rotated into q_out
-    (q and q_out may be None), in one launch."""
+    (both may be None), in one launch."""
     L = _lib or load()
     c, dev, H, D = cache.c()
     N = k_new.shape[0]
     Hq, qa, qb = 0, (None, 0), (None, 0)
+    if q is None and q_out is not None:
+        raise ValueError("q is missing")
     if q is not None:
         Hq = q.shape[1]
         qa, qb = _rows(q, "q", N, Hq, D, dev), _rows(q_out, "q_out", N, Hq, D, dev)

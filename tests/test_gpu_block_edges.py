@@ -215,3 +215,19 @@ def test_bad_page_zeroes_only_the_rows_that_see_it(kvq, H, G, D, max_q, before):
     keep = mine[~dead[mine]]
     assert np.array_equal(got[keep], base[keep])
     assert np.isnan(got[s.tok_start[1]:s.tok_start[2]]).all()
+
+
+def test_an_input_without_its_output_is_refused(kvq):
+    c = kvq.BlockKVCache.empty(4, 2, 16, 64)
+    rope = kvq.Rope(torch.ones(32, dtype=torch.float64, device="cuda"))
+    x = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    i = torch.ones(1, dtype=torch.int32, device="cuda")
+    t = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    for q, q_out in ((x, None), (None, x)):
+        with pytest.raises(ValueError):
+            kvq.kvq_rope_block_append(c, rope, q, q_out, x, x, None, i, t)
+        with pytest.raises(ValueError):
+            kvq.kvq_rope(rope, i, x, x, q, q_out)
+        if q is not None:
+            with pytest.raises(ValueError):
+                kvq.kvq_rope(rope, i, q, q_out)
