@@ -401,7 +401,10 @@ KVQ_API kvq_status kvq_rope(const kvq_rope_desc *rope, const int32_t *pos, int32
  *         tokens before this step's), at least 2^-126;
  * the block's scale becomes s, each new value e4m3_rne_satfinite(x / s) (inf
  * saturates, NaN becomes a NaN code) and, where s grew, each old code
- * e4m3_rne_satfinite(e4m3(code) * s_old / s).  Whether a block holds earlier
+ * e4m3_rne_satfinite(e4m3(code) * s_old / s).  For powers of two, the library's own scales,
+ * these are exact before they are rounded to e4m3; where a caller's old scale is another
+ * positive finite number, they are the fp32 products x * (1 / s) and e4m3(code) * (s_old / s)
+ * with the quotients rounded to fp32.  Whether a block holds earlier
  * tokens follows from the positions (slot 0 written in this step = a new
  * block, whose old scale is not read).  Slots past the request's length are
  * not written.  A table entry outside the pool raises KVQ_ERRBIT_PAGE and
@@ -432,8 +435,8 @@ KVQ_API kvq_status kvq_rope_block_append(const kvq_block_cache *cache, const kvq
 /* Reads cached tokens back: row i of request b is its position first[b] + i
  * (first int32 [B], NULL = zeros), k_out / v_out bf16
  * [n_tokens][num_kv_heads][head_dim] strided by token:
- *     bf16_rne( e4m3(code) * scale )   (exact for the library's own scales
- * unless the value is below bf16's normal range).  A range that is negative
+ *     bf16_rne( e4m3(code) * scale )   (the product in fp32; exact for the library's own
+ * scales unless the value is below bf16's normal range).  A range that is negative
  * or reaches past MP * page_size raises KVQ_ERRBIT_POS and its rows are not
  * written; a page outside the pool KVQ_ERRBIT_PAGE (its tokens' rows are not
  * written). */

@@ -231,3 +231,53 @@ def test_an_input_without_its_output_is_refused(kvq):
         if q is not None:
             with pytest.raises(ValueError):
                 kvq.kvq_rope(rope, i, q, q_out)
+
+
+# ---------------------------------------------------------------------------
+# append
+# ---------------------------------------------------------------------------
+
+def append_f32(pools, scales, new, tok_start, lens, table):
+    """R.append with the fp32 products that include/kvq.h states for scales of the caller's own."""
+    P, f = pools[0].shape[2], np.float32
+    for b in range(len(lens)):
+        row, n = int(tok_start[b]), int(tok_start[b + 1] - tok_start[b])
+        p0 = int(lens[b]) - n
+        for lp in range(p0 // P, (p0 + n - 1) // P + 1) if n else ():
+            page = int(table[b, lp])
+            lo, hi = max(p0, lp * P), min(p0 + n, lp * P + P)
+            old = lo - lp * P
+            for i in range(2):
+                x = new[i][row + lo - p0:row + hi - p0]
+                for h in range(pools[0].shape[1]):
+                    s = f(R.block_scale(float(np.abs(x[:, h]).max())))
+                    if old:
+                        was = f(scales[page, h, i])
+                        s = max(s, was)
+                        if s > was:
+                            pools[i][page, h, :old] = R.encode(
+                                R.decode(pools[i][page, h, :old]).astype(f) * (was / s))
+                    scales[page, h, i] = s
+                    pools[i][page, h, old:hi - lp * P] = R.encode(x[:, h].astype(f) * (f(1) / s))
+
+
+@pytest.mark.parametrize("H,P,D,n", [(2, 16, 128, 3), (3, 32, 64, 9), (1, 64, 128, 400), (8, 16, 64, 300),
+                                     (3, 32, 128, 200)])
+def test_append_to_blocks_with_scales_of_the_callers(kvq, H, P, D, n):
+    """Blocks whose old scales are no powers of two, ties of x / s and neighbours of ties among the
+    values, by all kernels (short, staged and wide)."""
+    rng = np.random.default_rng([H, P, D, n, 38])
+    B = 60
+    before = rng.integers(1, 2 * P, B)
+    s = R.Step(rng, [n] * B, before + n, H, P, D)
+    s.scales[:] = np.exp2(rng.integers(-9, 3, s.scales.shape)) * rng.choice(
+        [1.0, 1.25, 1.75, 1.75, 5 / 3, 1.9999999, rng.uniform(1, 2)], s.scales.shape)
+    s.scales[::7] = np.float32(3e38)
+    s.scales[3::11] = np.float32(2.0 ** -130 * 1.3)
+    kt, vt = (R.bf16(rng.integers(-255, 256, (s.N, H, D)) * np.exp2(rng.integers(-10, -4, (s.N, H, 1))))
+              for _ in range(2))
+    pools, scales = [s.k.copy(), s.v.copy()], s.scales.copy()
+    append_f32(pools, scales, [kt.double().numpy(), vt.double().numpy()], s.tok_start, s.lens, s.table)
+    c, err = run_append(kvq, s, (kt, vt))
+    assert err == 0
+    assert_cache(c, pools, scales)
