@@ -13,7 +13,7 @@
 //          counts.  K, V and q of a page go to CTAs of their own, a warp takes one
 //          head's rows, four (head_dim 128) at a time; further rows are read twice,
 //          the second time from L1.  64 rows of 64 requests, K and V of 8 heads, q of
-//          32, rotated: 3.0 us; 256 drafts of 1 - 8 rows 10.5.
+//          32, rotated: 2.75 us; 256 drafts of 1 - 8 rows 9.1.
 //   ring   prompts with enough kv heads: bandwidth counts (2 D (2 + 1) bytes a
 //          token and kv head, 4 D a query head).  A producer warp stages the
 //          rows of a page and a group of heads with one TMA copy each into a
@@ -41,6 +41,7 @@ struct BlockPool {
   uint8_t *k, *v;
   float *scales;
   int32_t num_pages, P, H;
+  int32_t ps;  // P = 1 << ps: a division by P in the chain of a decode step's loads costs 0.1 us
 };
 
 struct BlockAppendArgs {
@@ -56,8 +57,8 @@ struct BlockAppendArgs {
 };
 
 // Pages that a request's rows touch.
-__device__ __forceinline__ int64_t pages_touched(const Rows &r, int P) {
-  return r.n == 0 || r.err ? 0 : (r.p0 + r.n - 1) / P - r.p0 / P + 1;
+__device__ __forceinline__ int pages_touched(const Rows &r, int ps) {
+  return r.n == 0 || r.err ? 0 : ((r.p0 + r.n - 1) >> ps) - (r.p0 >> ps) + 1;
 }
 
 // Old codes of a block whose scale grew: rows [0, n_old) from `block` on.
@@ -94,34 +95,34 @@ struct PageItem {
 
 template <bool kLens>
 __device__ __forceinline__ bool next_page(const Ragged &rg, const int32_t *block_table, int MP,
-                                          int P, int num_pages, PageWalk &w, PageItem &it) {
+                                          int ps, int num_pages, PageWalk &w, PageItem &it) {
   if (w.left <= 0) return false;
   Rows rq = request_rows<kLens>(rg, w.b);
-  while (w.in >= pages_touched(rq, P)) {
+  while (w.in >= pages_touched(rq, ps)) {
     ++w.b;
     w.in = 0;
     rq = request_rows<kLens>(rg, w.b);
   }
-  const int lp = rq.p0 / P + static_cast<int>(w.in);
+  const int lp = (rq.p0 >> ps) + static_cast<int>(w.in);
   ++w.in;
   --w.left;
   const int page = __ldg(block_table + static_cast<int64_t>(w.b) * MP + lp);
   it.page = page >= 0 && page < num_pages ? page : -1;
-  it.first = max(rq.p0, lp * P);
-  it.slot0 = it.first - lp * P;
-  it.nrow = min(rq.p0 + rq.n, lp * P + P) - it.first;
+  it.first = max(rq.p0, lp << ps);
+  it.slot0 = it.first - (lp << ps);
+  it.nrow = min(rq.p0 + rq.n, (lp + 1) << ps) - it.first;
   it.row0 = static_cast<int64_t>(rq.row) + (it.first - rq.p0);
   return true;
 }
 
 // The CTA's run of pages (every thread calls it).
 template <int NT, bool kLens>
-__device__ __forceinline__ PageWalk page_run(const Ragged &rg, int P, uint32_t *err_word,
+__device__ __forceinline__ PageWalk page_run(const Ragged &rg, int ps, uint32_t *err_word,
                                              RunScan<NT> &scan) {
   const RunStart run = find_run<NT>(rg.B, gridDim.x, blockIdx.x, scan, [&](int b) -> int64_t {
     const Rows r = request_rows<kLens>(rg, b);
     if (r.err && blockIdx.x == 0) report(err_word, r.err);
-    return pages_touched(r, P);
+    return pages_touched(r, ps);
   });
   return {min(run.per, run.total - blockIdx.x * run.per), run.in, run.b};
 }
@@ -206,194 +207,236 @@ __device__ __forceinline__ float warp_amax(F lane_max) {
 
 // ---- short steps
 
-template <bool kShared>
-struct SharedRun {};
-
-template <>
-struct SharedRun<true> {  // what is left of a shared CTA's run
-  RunScan<kBcThreads> scan;
-  int64_t left, in;
-  int b;
-};
-
-// blockIdx.x below B * shares: request and share of its pages (0: K, 1: V, 2 ..:
-// qheads heads of q each); blockIdx.y: its page, counting from the first that the
-// step touches, and every gridDim.y-th one after it, up to `own` pages in all.  No scan over
-// the requests: the time of a decode step is a chain of loads (starts and length;
-// table entry beside the rows; old scale), and this is the shortest one.
-// The pages beyond (a prompt's part among decode rows) are the other CTAs': they scan
-// the requests and take equal runs of them (255 requests of one row and one of 2,048: 608
-// us without them, now 26; 256 drafts of 1 - 8 rows 9.7, now 10.5).
-// kShared: the launch has such CTAs (their state costs the others registers).
-template <int D, bool kRope, bool kShared>
-__global__ void __launch_bounds__(kBcThreads, kShared ? 3 : 4) block_append_short(BlockAppendArgs a, int shares,
-                                                                    int qheads, int own) {
-  constexpr int kItems = D / 16;      // lanes a row (two 8-dim chunks each)
-  constexpr int kRpp = 32 / kItems;   // rows a warp pass
-  extern __shared__ float4 tab[];     // kRope: [P][rd / 4] angles of the page's rows
-  __shared__ uint64_t s_freq[kRope ? D / 2 : 1];
-  __shared__ SharedRun<kShared> run;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int P = a.c.P, H = a.c.H;
-  const int i = lane % kItems, r0 = lane / kItems;
-  const bool half = !kRope || a.rope.layout == KVQ_ROPE_HALF;
-  const int rd = kRope ? a.rope.rd : D;
-  const ItemChunks ch = item_chunks(i, D, rd, half);
-  const int first_shared = a.rg.B * shares;  // CTA
-  const bool shared = kShared && static_cast<int>(blockIdx.x) >= first_shared;
-  int b = blockIdx.x / shares, share = blockIdx.x - b * shares;
+// A share of a page: K (0), V (1), or qheads heads of q (2 ..).
+struct ShortShare {
   bool is_v, is_q;
   int h0, heads;
   const uint16_t *src;
   int64_t stride;
-  auto set_share = [&] {
-    is_v = share == 1;
-    is_q = share > 1;
-    h0 = is_q ? (share - 2) * qheads : 0;
-    heads = is_q ? min(qheads, a.Hq - h0) : H;
-    src = is_q ? a.q + static_cast<int64_t>(h0) * D : is_v ? a.v_new : a.k_new;
-    stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
+};
+
+__device__ __forceinline__ ShortShare short_share(const BlockAppendArgs &a, int share, int qheads, int D) {
+  ShortShare s;
+  s.is_v = share == 1;
+  s.is_q = share > 1;
+  s.h0 = s.is_q ? (share - 2) * qheads : 0;
+  s.heads = s.is_q ? min(qheads, a.Hq - s.h0) : a.c.H;
+  s.src = s.is_q ? a.q + static_cast<int64_t>(s.h0) * D : s.is_v ? a.v_new : a.k_new;
+  s.stride = s.is_q ? a.q_stride : s.is_v ? a.v_stride : a.k_stride;
+  return s;
+}
+
+// A thread's place in a warp's rows.
+struct ShortLane {
+  int warp, lane, i, r0, rd;
+  bool half;
+  ItemChunks ch;
+};
+
+template <int D, bool kRope>
+__device__ __forceinline__ ShortLane short_lane(const BlockAppendArgs &a) {
+  constexpr int kItems = D / 16;  // lanes a row (two 8-dim chunks each)
+  ShortLane t;
+  t.warp = threadIdx.x >> 5;
+  t.lane = threadIdx.x & 31;
+  t.i = t.lane % kItems;
+  t.r0 = t.lane / kItems;
+  t.half = !kRope || a.rope.layout == KVQ_ROPE_HALF;
+  t.rd = kRope ? a.rope.rd : D;
+  t.ch = item_chunks(t.i, D, t.rd, t.half);
+  return t;
+}
+
+// A CTA's share of request b's page pg (counted from the first that the step touches).
+// tab: kRope: [P][rd / 4] angles of the page's rows; freq: the pairs' turns a token, set but
+// not yet synchronised.
+template <int D, bool kRope>
+__device__ __forceinline__ void append_page(const BlockAppendArgs &a, const ShortShare &sh, const ShortLane &t,
+                                            const Rows &rq, int b, int pg, float4 *tab, const uint64_t *freq) {
+  constexpr int kItems = D / 16;
+  constexpr int kRpp = 32 / kItems;   // rows a warp pass
+  const int P = a.c.P, H = a.c.H, heads = sh.heads;
+  const int warp = t.warp, lane = t.lane, i = t.i, r0 = t.r0, rd = t.rd;
+  const bool half = t.half;
+  const ItemChunks ch = t.ch;
+  const int lp = (rq.p0 >> a.c.ps) + pg;
+  const int page = __ldg(a.block_table + static_cast<int64_t>(b) * a.MP + lp);
+  const int first = max(rq.p0, lp << a.c.ps), slot0 = first - (lp << a.c.ps);
+  const int nrow = min(rq.p0 + rq.n, (lp + 1) << a.c.ps) - first;
+  const int64_t row0 = static_cast<int64_t>(rq.row) + (first - rq.p0);
+  auto load = [&](int r, int h, uint4 (&w)[2]) {
+    w[0] = w[1] = make_uint4(0, 0, 0, 0);
+    if (r < nrow && h < heads) {
+      const uint16_t *s = sh.src + (row0 + r) * sh.stride + static_cast<int64_t>(h) * D;
+      w[0] = *reinterpret_cast<const uint4 *>(s + ch.c0 * 8);
+      w[1] = *reinterpret_cast<const uint4 *>(s + ch.c1 * 8);
+    }
   };
-  set_share();
+  // this warp's first rows, before anything that waits: head `warp` (K, V),
+  // or the (token, head) rows from `e` on (q)
+  int e = warp * kRpp + r0;
+  uint4 w[2];
+  load(sh.is_q ? e / heads : r0, sh.is_q ? e % heads : warp, w);
+  if (kRope && !sh.is_v) {  // uniform over the CTA
+    __syncthreads();  // the previous page's angles are no longer read, and freq is set
+    fill_angles(tab, freq, first, nrow, rd, half, a.rope.mscale, threadIdx.x, kBcThreads);
+    __syncthreads();
+  }
+  if (page < 0 || page >= a.c.num_pages) {
+    if (threadIdx.x == 0) report(a.err_word, KVQ_ERRBIT_PAGE);
+    return;
+  }
+  auto values = [&](const uint4 (&w)[2], int r, float (&y)[16]) {
+    unpack8(w[0], y);
+    unpack8(w[1], y + 8);
+    if constexpr (kRope)
+      if (!sh.is_v && r < nrow) rotate_item(y, tab + r * (rd / 4), i, rd, half, ch);
+  };
+  if (sh.is_q) {
+    const int total = nrow * heads;
+    while (e - r0 < total) {
+      const int r = e / heads, h = e - r * heads;
+      const int e2 = e + kBcWarps * kRpp;
+      uint4 w2[2];
+      load(e2 / heads, e2 % heads, w2);  // the next rows, in flight meanwhile
+      float y[16];
+      values(w, r, y);
+      if (r < nrow)
+        store_rotated(a.q_out + (row0 + r) * a.q_out_stride + static_cast<int64_t>(sh.h0 + h) * D,
+                      ch, y, w[0], w[1], i, D, rd, half);
+      w[0] = w2[0];
+      w[1] = w2[1];
+      e = e2;
+    }
+    return;
+  }
+  for (int h = warp; h < H; h += kBcWarps) {
+    if (h != warp) load(r0, h, w);
+    const int64_t blk = static_cast<int64_t>(page) * H + h;
+    float *scale = a.c.scales + 2 * blk + sh.is_v;
+    const float s_old = slot0 > 0 ? *scale : 0.f;
+    float y[16];
+    values(w, r0, y);
+    const float amax = warp_amax([&](auto finite) {
+      uint32_t m = item_max<decltype(finite)::value>(y);
+      for (int r = kRpp + r0; r - r0 < nrow; r += kRpp) {
+        uint4 v[2];
+        float z[16];
+        load(r, h, v);
+        values(v, r, z);
+        m = max(m, item_max<decltype(finite)::value>(z));
+      }
+      return m;
+    });
+    const float s_new = fmaxf(pow2(block_exponent(amax)), s_old);
+    const float inv = 1.0f / s_new;  // exact: a power of two
+    uint8_t *block = (sh.is_v ? a.c.v : a.c.k) + blk * P * D;
+    if (s_new > s_old && slot0 > 0) requantise_rows<D>(block, slot0, s_old / s_new, lane);
+    if (lane == 0) *scale = s_new;
+    for (int r = r0; r - r0 < nrow; r += kRpp) {
+      if (r != r0) {
+        load(r, h, w);
+        values(w, r, y);
+      }
+      if (r < nrow) store_codes(block + (slot0 + r) * D, ch, y, inv);
+    }
+  }
+}
+
+// A CTA beyond the requests' own (idle_b < 0), or request idle_b's first, which has no pages: scans
+// the requests and takes an equal run of the pages that are beyond the requests' own CTAs'.
+// Out of line, so that its state costs those no registers (256 drafts 9.1 us, inlined 9.6; the
+// part of 2,048 rows below 27 and 25).
+template <int D, bool kRope>
+__device__ __noinline__ void append_shared(const BlockAppendArgs &a, int shares, int qheads, int own,
+                                           int idle_b, float4 *tab, uint64_t *freq) {
+  __shared__ RunScan<kBcThreads> scan;
+  __shared__ int idle[2];  // requests without pages: before this CTA's, and all
+  const int first_shared = a.rg.B * shares;  // CTA
+  int ctas = (static_cast<int>(gridDim.x) - first_shared) * gridDim.y;
+  int cta = (static_cast<int>(blockIdx.x) - first_shared) * gridDim.y + blockIdx.y;
+  if (idle_b >= 0) {
+    if (threadIdx.x < 2) idle[threadIdx.x] = 0;
+    bool any = false;
+    int before = 0, all = 0;
+    for (int k = threadIdx.x; k < a.rg.B; k += kBcThreads) {
+      const int n = pages_touched(request_rows<true>(a.rg, k), a.c.ps);
+      any |= n > own;
+      all += n == 0;
+      before += n == 0 && k < idle_b;
+    }
+    if (!__syncthreads_or(any)) return;
+    atomicAdd(&idle[0], before);
+    atomicAdd(&idle[1], all);
+    __syncthreads();
+    ctas = idle[1];
+    cta = idle[0];
+  }
+  if constexpr (kRope)
+    if (threadIdx.x < a.rope.rd / 2) freq[threadIdx.x] = turns_per_token(a.rope.inv_freq[threadIdx.x]);
+  auto items = [&](const Rows &rq) -> int64_t {  // (page, share) pairs
+    return static_cast<int64_t>(max(pages_touched(rq, a.c.ps) - own, 0)) * shares;
+  };
+  const RunStart r = find_run<kBcThreads>(a.rg.B, ctas, cta, scan,
+                                          [&](int k) { return items(request_rows<true>(a.rg, k)); });
+  int b = r.b;
+  int64_t in = r.in;
+  const ShortLane t = short_lane<D, kRope>(a);
+  for (int64_t left = min(r.per, r.total - cta * r.per); left > 0; --left, ++in) {
+    Rows rq = request_rows<true>(a.rg, b);
+    while (in >= items(rq)) {
+      in = 0;
+      rq = request_rows<true>(a.rg, ++b);
+    }
+    const int page = static_cast<int>(in / shares);
+    const ShortShare sh = short_share(a, static_cast<int>(in - static_cast<int64_t>(page) * shares), qheads, D);
+    append_page<D, kRope>(a, sh, t, rq, b, own + page, tab, freq);
+  }
+}
+
+// blockIdx.x below B * shares: request and share of its pages; blockIdx.y: its page, counting
+// from the first that the step touches, and every gridDim.y-th one after it, up to `own` pages in
+// all.  No scan over the requests: the time of a decode step is a chain of loads (starts and
+// length; table entry beside the rows; old scale), and this is the shortest one.
+// The pages beyond (a prompt's part among decode rows) are the other CTAs' (255 requests of one
+// row and one of 2,048: 608 us without them, now 27).  A step of no more rows than requests has
+// none; where one request has many rows all the same, others have no rows, and those requests'
+// CTAs take their place (1,024 slots, one with a part of 1,000 rows and the others idle: 482 us
+// without, now 21; 256 slots with 64 rows of decode 4.2 and 4.25).
+// Three CTAs an SM with rotation, for its registers, and four without (rotated, 64 rows of 64
+// requests 2.75 us against 3.05, 1,024 rows 16.7 against 16.3; as they come, 1,024 rows 9.4 and 7.8).
+template <int D, bool kRope>
+__global__ void __launch_bounds__(kBcThreads, kRope ? 3 : 4)
+    block_append_short(const __grid_constant__ BlockAppendArgs a, int shares, int qheads, int own) {
+  extern __shared__ float4 tab[];
+  __shared__ uint64_t s_freq[kRope ? D / 2 : 1];
+  const int rd = kRope ? a.rope.rd : D;
+  const int first_shared = a.rg.B * shares;  // CTA
+  const int b = blockIdx.x / shares, share = blockIdx.x - b * shares;
+  const ShortShare sh = short_share(a, share, qheads, D);
+  const ShortLane t = short_lane<D, kRope>(a);
   grid_dependency_wait();
   allow_dependents();
+  if (static_cast<int>(blockIdx.x) >= first_shared) {
+    append_shared<D, kRope>(a, shares, qheads, own, -1, tab, s_freq);
+    return;
+  }
   double freq = 0.0;
   if constexpr (kRope)
-    if ((shared || share != 1) && threadIdx.x < rd / 2) freq = a.rope.inv_freq[threadIdx.x];  // rd / 2 <= blockDim
-  Rows rq = request_rows<true>(a.rg, shared ? 0 : b);
-  int pages = INT32_MAX;  // a shared CTA's end is its run's
-  if constexpr (kShared) {
-    if (shared) {
-      const int ctas = (static_cast<int>(gridDim.x) - first_shared) * gridDim.y;
-      const int cta = (static_cast<int>(blockIdx.x) - first_shared) * gridDim.y + blockIdx.y;
-      const RunStart r = find_run<kBcThreads>(a.rg.B, ctas, cta, run.scan, [&](int k) -> int64_t {
-        return max(pages_touched(request_rows<true>(a.rg, k), P) - own, static_cast<int64_t>(0)) * shares;
-      });
-      if (threadIdx.x == 0) {
-        run.left = min(r.per, r.total - cta * r.per);
-        run.in = r.in;
-        run.b = r.b;
-      }
-    }
-  }
-  if (!shared) {
-    if (rq.err && blockIdx.y == 0 && share == 0 && threadIdx.x == 0) report(a.err_word, rq.err);
-    pages = static_cast<int>(pages_touched(rq, P));
-    if constexpr (kShared) pages = min(pages, own);
-    if (static_cast<int>(blockIdx.y) >= pages) return;
+    if (share != 1 && threadIdx.x < rd / 2) freq = a.rope.inv_freq[threadIdx.x];  // rd / 2 <= blockDim
+  const Rows rq = request_rows<true>(a.rg, b);
+  if (rq.err && blockIdx.y == 0 && share == 0 && threadIdx.x == 0) report(a.err_word, rq.err);
+  const int touched = pages_touched(rq, a.c.ps), pages = min(touched, own);
+  if (static_cast<int>(blockIdx.y) >= pages) {
+    if (touched == 0 && share == 0 && blockIdx.y == 0 && own < INT32_MAX &&
+        static_cast<int>(gridDim.x) == first_shared)
+      append_shared<D, kRope>(a, shares, qheads, own, b, tab, s_freq);
+    return;
   }
   if constexpr (kRope)
-    if ((shared || share != 1) && threadIdx.x < rd / 2) s_freq[threadIdx.x] = turns_per_token(freq);
-  for (int pg = blockIdx.y; pg < pages; pg += gridDim.y) {
-    if (shared) {  // item `in` of request b: page and share
-      if constexpr (kShared) {
-        __syncthreads();
-        if (threadIdx.x == 0 && run.left > 0) {
-          while (true) {
-            const int64_t n = max(pages_touched(request_rows<true>(a.rg, run.b), P) - own,
-                                  static_cast<int64_t>(0)) * shares;
-            if (run.in < n) break;
-            run.in = 0;
-            ++run.b;
-          }
-        }
-        __syncthreads();
-        if (run.left <= 0) return;
-        b = run.b;
-        rq = request_rows<true>(a.rg, b);
-        pg = own + static_cast<int>(run.in / shares);
-        share = static_cast<int>(run.in % shares);
-        set_share();
-        __syncthreads();
-        if (threadIdx.x == 0) {
-          ++run.in;
-          --run.left;
-        }
-      }
-    }
-    const int lp = rq.p0 / P + pg;
-    const int page = __ldg(a.block_table + static_cast<int64_t>(b) * a.MP + lp);
-    const int first = max(rq.p0, lp * P), slot0 = first - lp * P;
-    const int nrow = min(rq.p0 + rq.n, lp * P + P) - first;
-    const int64_t row0 = static_cast<int64_t>(rq.row) + (first - rq.p0);
-    auto load = [&](int r, int h, uint4 (&w)[2]) {
-      w[0] = w[1] = make_uint4(0, 0, 0, 0);
-      if (r < nrow && h < heads) {
-        const uint16_t *s = src + (row0 + r) * stride + static_cast<int64_t>(h) * D;
-        w[0] = *reinterpret_cast<const uint4 *>(s + ch.c0 * 8);
-        w[1] = *reinterpret_cast<const uint4 *>(s + ch.c1 * 8);
-      }
-    };
-    // this warp's first rows, before anything that waits: head `warp` (K, V),
-    // or the (token, head) rows from `e` on (q)
-    int e = warp * kRpp + r0;
-    uint4 w[2];
-    load(is_q ? e / heads : r0, is_q ? e % heads : warp, w);
-    if (kRope && !is_v) {  // uniform over the CTA
-      __syncthreads();  // the previous page's angles are no longer read (and s_freq is set)
-      fill_angles(tab, s_freq, first, nrow, rd, half, a.rope.mscale, threadIdx.x, kBcThreads);
-      __syncthreads();
-    }
-    if (page < 0 || page >= a.c.num_pages) {
-      if (threadIdx.x == 0) report(a.err_word, KVQ_ERRBIT_PAGE);
-      continue;
-    }
-    auto values = [&](const uint4 (&w)[2], int r, float (&y)[16]) {
-      unpack8(w[0], y);
-      unpack8(w[1], y + 8);
-      if constexpr (kRope)
-        if (!is_v && r < nrow) rotate_item(y, tab + r * (rd / 4), i, rd, half, ch);
-    };
-    if (is_q) {
-      const int total = nrow * heads;
-      while (e - r0 < total) {
-        const int r = e / heads, h = e - r * heads;
-        const int e2 = e + kBcWarps * kRpp;
-        uint4 w2[2];
-        load(e2 / heads, e2 % heads, w2);  // the next rows, in flight meanwhile
-        float y[16];
-        values(w, r, y);
-        if (r < nrow)
-          store_rotated(a.q_out + (row0 + r) * a.q_out_stride + static_cast<int64_t>(h0 + h) * D,
-                        ch, y, w[0], w[1], i, D, rd, half);
-        w[0] = w2[0];
-        w[1] = w2[1];
-        e = e2;
-      }
-      continue;
-    }
-    for (int h = warp; h < H; h += kBcWarps) {
-      if (h != warp) load(r0, h, w);
-      const int64_t blk = static_cast<int64_t>(page) * H + h;
-      float *scale = a.c.scales + 2 * blk + is_v;
-      const float s_old = slot0 > 0 ? *scale : 0.f;
-      float y[16];
-      values(w, r0, y);
-      const float amax = warp_amax([&](auto finite) {
-        uint32_t m = item_max<decltype(finite)::value>(y);
-        for (int r = kRpp + r0; r - r0 < nrow; r += kRpp) {
-          uint4 v[2];
-          float z[16];
-          load(r, h, v);
-          values(v, r, z);
-          m = max(m, item_max<decltype(finite)::value>(z));
-        }
-        return m;
-      });
-      const float s_new = fmaxf(pow2(block_exponent(amax)), s_old);
-      const float inv = 1.0f / s_new;  // exact: a power of two
-      uint8_t *block = (is_v ? a.c.v : a.c.k) + blk * P * D;
-      if (s_new > s_old && slot0 > 0) requantise_rows<D>(block, slot0, s_old / s_new, lane);
-      if (lane == 0) *scale = s_new;
-      for (int r = r0; r - r0 < nrow; r += kRpp) {
-        if (r != r0) {
-          load(r, h, w);
-          values(w, r, y);
-        }
-        if (r < nrow) store_codes(block + (slot0 + r) * D, ch, y, inv);
-      }
-    }
-  }
+    if (share != 1 && threadIdx.x < rd / 2) s_freq[threadIdx.x] = turns_per_token(freq);
+  for (int pg = blockIdx.y; pg < pages; pg += gridDim.y)
+    append_page<D, kRope>(a, sh, t, rq, b, pg, tab, s_freq);
 }
 
 // ---- prompts, a warp's rows loaded by itself
@@ -417,10 +460,10 @@ __global__ void __launch_bounds__(kBcThreads, kRope ? 2 : 3) block_append_wide(B
   allow_dependents();
   if constexpr (kRope)
     if (threadIdx.x < rd / 2) s_freq[threadIdx.x] = turns_per_token(a.rope.inv_freq[threadIdx.x]);
-  PageWalk walk = page_run<kBcThreads, true>(a.rg, P, a.err_word, scan);
+  PageWalk walk = page_run<kBcThreads, true>(a.rg, a.c.ps, a.err_word, scan);
   PageItem it;
   uint32_t round = 0;
-  while (next_page<true>(a.rg, a.block_table, a.MP, P, a.c.num_pages, walk, it)) {  // uniform
+  while (next_page<true>(a.rg, a.block_table, a.MP, a.c.ps, a.c.num_pages, walk, it)) {  // uniform
     if (it.page < 0) {
       if (threadIdx.x == 0) report(a.err_word, KVQ_ERRBIT_PAGE);
       continue;
@@ -620,7 +663,7 @@ __global__ void __launch_bounds__(kBcThreads + 32, 2)
   allow_dependents();
   if constexpr (kRope)
     if (threadIdx.x < rd / 2) s_freq[threadIdx.x] = turns_per_token(a.rope.inv_freq[threadIdx.x]);
-  PageWalk walk = page_run<kBcThreads + 32, true>(a.rg, P, a.err_word, ctl.scan);  // syncs
+  PageWalk walk = page_run<kBcThreads + 32, true>(a.rg, a.c.ps, a.err_word, ctl.scan);  // syncs
 
   if (warp == kBcWarps) {
     // ------------------------------------------------------------ producer
@@ -629,7 +672,7 @@ __global__ void __launch_bounds__(kBcThreads + 32, 2)
     int slot = 0;
     bool ok = true;
     PageItem it;
-    while (ok && next_page<true>(a.rg, a.block_table, a.MP, P, a.c.num_pages, walk, it)) {
+    while (ok && next_page<true>(a.rg, a.block_table, a.MP, a.c.ps, a.c.num_pages, walk, it)) {
       if (it.page < 0) {
         if (lane == 0) report(a.err_word, KVQ_ERRBIT_PAGE);
         continue;
@@ -797,9 +840,9 @@ __global__ void __launch_bounds__(kBcThreads) block_read_kernel(BlockReadArgs a)
   const int i = lane % kLanes, r0 = lane / kLanes;
   grid_dependency_wait();
   allow_dependents();
-  PageWalk walk = page_run<kBcThreads, false>(a.rg, P, a.err_word, scan);
+  PageWalk walk = page_run<kBcThreads, false>(a.rg, a.c.ps, a.err_word, scan);
   PageItem it;
-  while (next_page<false>(a.rg, a.block_table, a.MP, P, a.c.num_pages, walk, it)) {
+  while (next_page<false>(a.rg, a.block_table, a.MP, a.c.ps, a.c.num_pages, walk, it)) {
     if (it.page < 0) {
       if (threadIdx.x == 0) report(a.err_word, KVQ_ERRBIT_PAGE);
       continue;
@@ -842,7 +885,7 @@ namespace {
 
 BlockPool block_pool(const kvq_block_cache *c) {
   return {static_cast<uint8_t *>(c->k_pool), static_cast<uint8_t *>(c->v_pool), c->scales,
-          c->num_pages, c->page_size, c->num_kv_heads};
+          c->num_pages, c->page_size, c->num_kv_heads, c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : 6};
 }
 
 // Pages that a step of n_tokens rows touches, at most: one a row, and
@@ -935,9 +978,9 @@ kvq_status append_impl(const kvq_block_cache *cache, const kvq_rope_desc *rope, 
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (n_tokens <= kShortRows * static_cast<int64_t>(B) || pages <= 2 * sms) {
-    // q's heads in one share for a row a request, in shares of twice K's rows for
-    // more (256 drafts of 1-8 rows, 32 heads over 8, no shared CTAs: 9.7 us; shares
-    // of 8 and of all heads 11.3 and 10.5)
+    // q's heads in one share for up to two rows a request, in shares of twice K's rows for
+    // more (256 drafts of 1-8 rows, 32 heads over 8: 9.1 us, shares of 8 and of all heads 11.0
+    // and 8.9; four parts of 300 rows 9.8, with all heads 14.8)
     const int qheads = n_tokens <= 2 * static_cast<int64_t>(B) ? Hq : 2 * H;
     const int shares = rope && Hq > 0 ? 2 + (Hq + qheads - 1) / qheads : 2;
     if (static_cast<int64_t>(B) * shares > INT32_MAX - 4 * sms) return KVQ_ERR_UNSUPPORTED;
@@ -947,19 +990,18 @@ kvq_status append_impl(const kvq_block_cache *cache, const kvq_rope_desc *rope, 
     int64_t gy = (avg + P - 1) / P;
     const int64_t most = 16LL * sms / (static_cast<int64_t>(B) * shares) + 1;
     gy = gy < most ? gy : most;
-    // a request's own CTAs do two pages each; what one can have beyond is shared
-    const int own = 2 * static_cast<int>(gy);
-    // (not in a step of a row a request, which they would slow down: 3.0 to 3.6 us)
-    const int64_t beyond = (static_cast<int64_t>(n_tokens) + P - 2) / P + 1 - own;
-    const int64_t extra = beyond <= 0 || n_tokens <= B
-                              ? 0 : (std::min<int64_t>(beyond * shares, 3 * sms) + gy - 1) / gy;
+    // a request's own CTAs do two pages each; what one can have beyond is shared: by further
+    // CTAs, or by those of requests without rows, which there are where the rows are no more
+    // than the requests and one has many
+    const int64_t beyond = (static_cast<int64_t>(n_tokens) + P - 2) / P + 1 - 2 * gy;
+    const bool shared = beyond > 0 && tok_start;
+    const int own = shared ? 2 * static_cast<int>(gy) : INT32_MAX;
+    const int64_t extra =
+        shared && n_tokens > B ? (std::min<int64_t>(beyond * shares, 3 * sms) + gy - 1) / gy : 0;
     using ShortFn = void (*)(BlockAppendArgs, int, int, int);
-    static constexpr ShortFn kFns[2][2][2] = {
-        {{block_append_short<64, false, false>, block_append_short<64, false, true>},
-         {block_append_short<64, true, false>, block_append_short<64, true, true>}},
-        {{block_append_short<128, false, false>, block_append_short<128, false, true>},
-         {block_append_short<128, true, false>, block_append_short<128, true, true>}}};
-    e = launch_dependent(kFns[D == 128][rope != nullptr][extra > 0],
+    static constexpr ShortFn kFns[2][2] = {{block_append_short<64, false>, block_append_short<64, true>},
+                                           {block_append_short<128, false>, block_append_short<128, true>}};
+    e = launch_dependent(kFns[D == 128][rope != nullptr],
                          dim3(static_cast<unsigned>(B * shares + extra), static_cast<unsigned>(gy)), kBcThreads,
                          angles, cs, a, shares, qheads, own);
   } else if (H * P >= kBcWarps * kRowsPerWarp) {

@@ -281,3 +281,24 @@ def test_append_to_blocks_with_scales_of_the_callers(kvq, H, P, D, n):
     c, err = run_append(kvq, s, (kt, vt))
     assert err == 0
     assert_cache(c, pools, scales)
+
+
+@pytest.mark.parametrize("rope", [False, True])
+@pytest.mark.parametrize("H,P,D,B,n", [(2, 16, 128, 300, 290), (3, 32, 64, 900, 880), (8, 64, 128, 200, 150)])
+def test_append_part_of_a_prompt_among_idle_slots(kvq, H, P, D, B, n, rope):
+    """Fixed slots, most of them without rows, one with a part of a prompt: no more rows than slots."""
+    rng = np.random.default_rng([H, P, D, B, 39])
+    rows = np.zeros(B, dtype=np.int64)
+    rows[[3, B // 2, B - 1]] = 1, n, 2
+    s = R.Step(rng, rows, np.where(rows > 0, rows + rng.integers(0, 50, B), 0), H, P, D)
+    (kt, kx), (vt, vx) = R.values(rng, s.N, H, D), R.values(rng, s.N, H, D)
+    if rope:
+        from test_gpu_block_cache import check_rope_append
+        return check_rope_append(kvq, s, rng, 4 * H, D, True)
+    pools, scales = [s.k.copy(), s.v.copy()], s.scales.copy()
+    lens, table = s.lens.copy(), s.table.copy()
+    table[B // 2, 1] = s.NP
+    R.append(pools, scales, [kx, vx], s.tok_start, lens, table)
+    c, err = run_append(kvq, s, (kt, vt), table=table)
+    assert err == kvq.ERRBIT_PAGE
+    assert_cache(c, pools, scales)
