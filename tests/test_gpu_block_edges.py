@@ -302,3 +302,46 @@ def test_append_part_of_a_prompt_among_idle_slots(kvq, H, P, D, B, n, rope):
     c, err = run_append(kvq, s, (kt, vt), table=table)
     assert err == kvq.ERRBIT_PAGE
     assert_cache(c, pools, scales)
+
+
+@pytest.mark.parametrize("Hq", [1, 3, 8, 11])
+@pytest.mark.parametrize("H,P,D", [(8, 16, 128), (9, 16, 64), (2, 64, 128)])
+def test_rope_append_prompts_with_any_number_of_query_heads(kvq, H, P, D, Hq):
+    """Fewer query heads than a staged group of heads holds, and no multiple of it."""
+    from test_gpu_block_cache import check_rope_append, prompts
+    rng = np.random.default_rng([H, P, D, Hq, 40])
+    check_rope_append(kvq, prompts(rng, H, P, D), rng, Hq, D // 2, Hq % 2 == 0)
+
+
+def test_idle_slots_in_a_captured_step(kvq):
+    """A captured append of fixed slots, replayed while rows move from many requests to one and
+    back, on a stream of its own."""
+    H, P, D, B = 2, 16, 64, 80
+    rng = np.random.default_rng(41)
+    s = R.Step(rng, [0] * B, [200] * B, H, P, D)
+    c = kvq.BlockKVCache(dev(s.k), dev(s.v), dev(s.scales))
+    N = B
+    k, v = (torch.zeros(N, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ts, lens = (torch.zeros(m, dtype=torch.int32, device="cuda") for m in (B + 1, B))
+    table, err = dev(s.table), torch.zeros(1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        kvq.kvq_block_append(c, k, v, ts, lens, table, err_word=err)
+    pools, scales = [s.k.copy(), s.v.copy()], s.scales.copy()
+    length = rng.integers(0, 50, B)
+    for n in ([1] * B, [0] * 7 + [80] + [0] * 72, [0] * B, [0, 2] * 40, [35] + [0] * 78 + [45], [1] * B):
+        n = np.array(n)
+        start = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+        (kt, kx), (vt, vx) = R.values(rng, N, H, D), R.values(rng, N, H, D)
+        length += n
+        k.copy_(kt.cuda()), v.copy_(vt.cuda()), ts.copy_(dev(start))
+        lens.copy_(dev(length.astype(np.int32)))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        torch.cuda.synchronize()
+        R.append(pools, scales, [kx, vx], start, length, s.table)
+        assert int(err.item()) == 0
+        assert_cache(c, pools, scales)
