@@ -255,6 +255,9 @@ __device__ __forceinline__ void append_page(const BlockAppendArgs &a, const Shor
                                             const Rows &rq, int b, int pg, float4 *tab, const uint64_t *freq) {
   constexpr int kItems = D / 16;
   constexpr int kRpp = 32 / kItems;   // rows a warp pass
+  // passes whose rows are asked for together in the first reading (2 requests of 44 rows 5.45
+  // us, one by one 7.1); rotation has no registers for it
+  constexpr int kAhead = kRope ? 1 : 4;
   const int P = a.c.P, H = a.c.H, heads = sh.heads;
   const int warp = t.warp, lane = t.lane, i = t.i, r0 = t.r0, rd = t.rd;
   const bool half = t.half;
@@ -319,6 +322,7 @@ __device__ __forceinline__ void append_page(const BlockAppendArgs &a, const Shor
     values(w, r0, y);
     const float amax = warp_amax([&](auto finite) {
       uint32_t m = item_max<decltype(finite)::value>(y);
+#pragma unroll kAhead
       for (int r = kRpp + r0; r - r0 < nrow; r += kRpp) {
         uint4 v[2];
         float z[16];
