@@ -15,7 +15,7 @@
 // head and all its rows, in blocks of 32 rows x heads a kv head, or 128 (ba_shape).
 // Measured: 64 requests of 8,193 - 9,216 tokens, 8 kv heads of 128, 4
 // heads a kv head, one row: 174 us, 97% of the measured copy rate; 8 heads a kv head,
-// 512 - 65,536 tokens, pages of 64: 296 us, 94%; 8 requests of 8,193 tokens: 30 us, 66%
+// 512 - 65,536 tokens, pages of 64: 294 us, 95%; 8 requests of 8,193 tokens: 30 us, 66%
 // (3 us until the first bytes are asked for, 4 for the cut rows).
 //
 //   split   persistent CTAs; the requests' (kv-head group, row block) rows, in
@@ -61,8 +61,9 @@ constexpr int kStat = 4;                         // floats after a row's accumul
 // Row tiles: 4 (one MMA column block carries the weights and their remainders),
 // 8 or 16 rows a warp; larger row counts take RT tiles of 16: two, and beyond 128 rows
 // all eight warps.  (Blocks of 32 rows fit requests of different rows better: 24 drafts of
-// 4 - 16 rows x 6 heads, head_dim 64, 18.9 us against 20.5 with 128, 32 of 1 - 16 rows x 4
-// heads over long contexts 236 against 274; 64 rows x 4 heads 64.7 against 60.3.)  The
+// 4 - 16 rows x 6 heads, head_dim 64, 18.7 us against 23.9 with 64 and 20.2 with 128, 32 of
+// 1 - 16 rows x 4 heads over long contexts 231 against 268 and 521; 64 rows x 4 heads 63.9
+// against 59.2 and 59.0.)  The
 // warps that the (head, row tile) pairs leave free are further teams.
 
 struct BaShape {
@@ -77,9 +78,9 @@ struct BaShape {
 
 // The tcgen05 kernel reads a block of 32 rows in the time that the mma.sync kernel
 // takes for 8, but starts and ends a row of work more slowly.  Measured (8 kv heads
-// of 128, us, mma.sync and tcgen05): 32 requests of 1,024 - 16,384 tokens, 12 rows 116
-// and 99, 16 rows 121 and 100, 32 rows 197 and 102; 128 requests of 64 - 1,024, 16 rows
-// 50 and 60, 32 rows 84 and 61.  So it takes more than 16 rows always, and 9 - 16
+// of 128, us, mma.sync and tcgen05): 32 requests of 1,024 - 16,384 tokens, 12 rows 115
+// and 101, 16 rows 120 and 101, 32 rows 194 and 103; 128 requests of 64 - 1,024, 16 rows
+// 49 and 62, 32 rows 82 and 63.  So it takes more than 16 rows always, and 9 - 16
 // where requests can be long: the two meet near 1,600 tokens, taken as half of what
 // the block table holds.
 constexpr int64_t kTcLong = 4096;

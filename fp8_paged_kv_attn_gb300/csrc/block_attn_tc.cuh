@@ -39,12 +39,12 @@
 // of 128 tokens of one head; more than 32 rows are row blocks, which follow one
 // another so that the second reads the cache from L2.
 //
-// Measured: 32 requests of 1,024 - 16,384 tokens, 8 kv heads, 1 - 8 rows of 4 heads: 106
-// us (mma.sync 206; HBM's floor 66).  A tile takes about 2,050 cycles of a CTA: a
+// Measured: 32 requests of 1,024 - 16,384 tokens, 8 kv heads, 1 - 8 rows of 4 heads: 107.5
+// us (mma.sync 203; HBM's floor 66).  A tile takes about 2,050 cycles of a CTA: a
 // group's own chain (scores, maxima, rescaling, 64 conversions a thread, products) is
-// 4,000 and two are in flight, TMEM being full.  Without rescaling, three of the four
-// pieces and half of the products it was 87 us, with each of them alone 96 - 100: no
-// single step is the bound any more.
+// 4,000 and two are in flight; a third group would have 72 registers a thread, and shared
+// memory is full.  Without rescaling, three of the four pieces and half of the products it
+// was 87 us, with each of them alone 96 - 100: no single step is the bound any more.
 #pragma once
 
 namespace kvq {
@@ -275,8 +275,8 @@ __device__ __forceinline__ void tc_load_q(const BaArgs &a, const TcSeg &sg, uint
 // Every kTcFlush tiles the sums leave TMEM, and are added with rounding to others in
 // the workspace: the tensor core's additions truncate (towards zero), and a long sum there
 // drifts, 1.3e-5 of it over 65,536 tokens, measured; 1e-7 are left, for 3% of the time.  This
-// thread's dim of 16 rows, eight at a time (with all in registers the loop around spills:
-// 128 requests of 64 - 1,024 tokens 63.5 us, so 61.2): kept times `keep`, the pieces times `fo`.
+// thread's dim of 16 rows, eight at a time (with all in registers the loop around spills, and 128
+// requests of 64 - 1,024 tokens take 4% longer): kept times `keep`, the pieces times `fo`.
 __device__ __forceinline__ void tc_flush(float *kept, bool first, float keep, float fo, float *rows,
                                          uint32_t addr, int half, int lane) {
 #pragma unroll 1
