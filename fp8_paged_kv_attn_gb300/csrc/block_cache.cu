@@ -333,7 +333,7 @@ __device__ __forceinline__ void append_page(const BlockAppendArgs &a, const Shor
       return m;
     });
     const float s_new = fmaxf(pow2(block_exponent(amax)), s_old);
-    const float inv = 1.0f / s_new;  // exact: a power of two
+    const float inv = 1.0f / s_new;  // exact for a power of two
     uint8_t *block = (sh.is_v ? a.c.v : a.c.k) + blk * P * D;
     if (s_new > s_old && slot0 > 0) requantise_rows<D>(block, slot0, s_old / s_new, lane);
     if (lane == 0) *scale = s_new;
