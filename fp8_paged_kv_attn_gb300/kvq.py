@@ -54,7 +54,9 @@ EXPORTS = ("kvq_append", "kvq_append_check", "kvq_handoff_pages", "kvq_check_tag
            "kvq_pages_update", "kvq_decode_attn_workspace_size", "kvq_decode_attn",
            "kvq_decode_attn_static", "kvq_wq_gemm", "kvq_selftest_wait", "kvq_status_string",
            "kvq_rope_inv_freq", "kvq_rope", "kvq_block_append", "kvq_rope_block_append",
-           "kvq_block_read", "kvq_block_attn_workspace_size", "kvq_block_attn")
+           "kvq_block_read", "kvq_block_attn_workspace_size", "kvq_block_attn",
+           "kvq_pages_workspace_size", "kvq_pages_fork", "kvq_pages_release", "kvq_pages_compact",
+           "kvq_copy_pages", "kvq_block_copy_pages")
 STATIC_SCRATCH_BYTES = 64 << 20
 
 
@@ -142,6 +144,20 @@ def load(build_if_missing: bool = True):
     L.kvq_block_attn.argtypes = [bp, vp, i64, i32, vp, i32, i32, vp, vp, i32, i32, vp, f32, vp,
                                  vp, sz, vp, vp]
     L.kvq_block_attn.restype = ctypes.c_int
+    L.kvq_pages_workspace_size.argtypes = [i32, i32]
+    L.kvq_pages_workspace_size.restype = sz
+    L.kvq_pages_fork.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, i32, vp,
+                                 vp, vp, vp, sz, vp, vp]
+    L.kvq_pages_fork.restype = ctypes.c_int
+    L.kvq_pages_release.argtypes = [vp, vp, vp, i32, vp, i32, i32, vp, vp, vp, i32, vp, sz, vp, vp]
+    L.kvq_pages_release.restype = ctypes.c_int
+    L.kvq_pages_compact.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, i32, vp, vp, vp, i32, vp, vp,
+                                    sz, vp, vp]
+    L.kvq_pages_compact.restype = ctypes.c_int
+    L.kvq_copy_pages.argtypes = [cp, vp, vp, i32, vp, vp]
+    L.kvq_copy_pages.restype = ctypes.c_int
+    L.kvq_block_copy_pages.argtypes = [bp, vp, vp, i32, vp, vp]
+    L.kvq_block_copy_pages.restype = ctypes.c_int
     L.kvq_status_string.argtypes = [ctypes.c_int]
     L.kvq_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -674,3 +690,109 @@ def kvq_block_attn(cache: BlockKVCache, q, tok_start, seq_lens, block_table, out
              _arr(out, "out", _F32, (N, Hq, D), dev),
              _arr(workspace, "workspace", _BYTES, workspace.shape, dev), workspace.numel(),
              _err(err_word, dev)))
+
+
+# ----------------------------------------------------------------------------
+# pages that several requests hold (include/kvq.h).  `state` is the allocator's
+# PageState and `shares` int32 [num_pages] its count of holders beyond the first
+# (zeros at the start).  Every tensor of a call lies on one device, as above.
+# ----------------------------------------------------------------------------
+
+def kvq_pages_workspace_size(num_pages: int, B: int) -> int:
+    return int(load().kvq_pages_workspace_size(num_pages, B))
+
+
+def pages_workspace(num_pages: int, B: int, device="cuda") -> torch.Tensor:
+    """Allocate (with torch) a workspace for kvq_pages_fork, _release and _compact."""
+    n = kvq_pages_workspace_size(num_pages, B)
+    if n == 0:
+        raise ValueError("num_pages and B must be positive")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _pages(state: PageState, shares, tags=True):
+    """(device, num_pages, B, MP, pointers of the state's arrays)"""
+    dev = _device(state.block_table, "block_table")
+    n = state.free_stack.numel()
+    B, MP = state.block_table.shape
+    p = [_arr(state.free_stack, "free_stack", I32, (n,), dev),
+         _arr(state.free_count, "free_count", I32, (1,), dev)]
+    if tags:
+        p.append(_arr(state.page_tags, "page_tags", U32, (n,), dev))
+    p += [_arr(shares, "shares", I32, (n,), dev), n,
+          _arr(state.block_table, "block_table", I32, (B, MP), dev)]
+    if tags:
+        p.append(_arr(state.expected_tags, "expected_tags", U32, (B, MP), dev))
+    return dev, B, [*p, B, MP]
+
+
+def _ws(workspace, dev):
+    return _arr(workspace, "workspace", _BYTES, workspace.shape, dev), workspace.numel()
+
+
+def kvq_pages_fork(state: PageState, shares, src, dst, tokens, page_size: int, copy_src, copy_dst,
+                   fork_ok, workspace, err_word=None, stream=None) -> None:
+    """Give request dst[i] the first tokens[i] tokens of request src[i]: whole pages
+    shared, a part-filled last one replaced by a fresh page, whose copy is
+    (copy_src[i], copy_dst[i]) for kvq_copy_pages or kvq_block_copy_pages."""
+    L = _lib or load()
+    dev, _, p = _pages(state, shares)
+    n = src.shape[0]
+    _launch(L.kvq_pages_fork, "kvq_pages_fork", dev, stream,
+            (*p, page_size, _arr(src, "src", I32, (n,), dev), _arr(dst, "dst", I32, (n,), dev),
+             _arr(tokens, "tokens", I32, (n,), dev), n, _arr(copy_src, "copy_src", I32, (n,), dev),
+             _arr(copy_dst, "copy_dst", I32, (n,), dev), _arr(fork_ok, "fork_ok", U8, (n,), dev),
+             *_ws(workspace, dev), _err(err_word, dev)))
+
+
+def kvq_pages_release(state: PageState, shares, req, first, npages, workspace, err_word=None,
+                      stream=None) -> None:
+    """Request req[j] lets go of logical pages first[j] .. first[j] + npages[j] - 1 (first
+    None: from page 0); a page is free when its last holder is gone."""
+    L = _lib or load()
+    dev, _, p = _pages(state, shares, tags=False)
+    n = req.shape[0]
+    _launch(L.kvq_pages_release, "kvq_pages_release", dev, stream,
+            (*p, _arr(req, "req", I32, (n,), dev),
+             None if first is None else _arr(first, "first", I32, (n,), dev),
+             _arr(npages, "npages", I32, (n,), dev), n, *_ws(workspace, dev), _err(err_word, dev)))
+
+
+def kvq_pages_compact(state: PageState, shares, held, copy_src, copy_dst, n_moves, workspace,
+                      err_word=None, stream=None) -> None:
+    """Rename the pages in use to the lowest ids; copy_src[k] -> copy_dst[k] (the rest -1)
+    are the pages that kvq_copy_pages or kvq_block_copy_pages then moves.  held int32
+    [B]: block-table entries in use of every request; the lists have num_pages // 2
+    entries or more; n_moves int32 [1]."""
+    L = _lib or load()
+    dev, B, p = _pages(state, shares)
+    cap = copy_src.shape[0]
+    _launch(L.kvq_pages_compact, "kvq_pages_compact", dev, stream,
+            (*p, _arr(held, "held", I32, (B,), dev), _arr(copy_src, "copy_src", I32, (cap,), dev),
+             _arr(copy_dst, "copy_dst", I32, (cap,), dev), cap,
+             _arr(n_moves, "n_moves", I32, (1,), dev), *_ws(workspace, dev), _err(err_word, dev)))
+
+
+def _pairs(src, dst, dev):
+    n = src.shape[0]
+    return _arr(src, "src", I32, (n,), dev), _arr(dst, "dst", I32, (n,), dev), n
+
+
+def kvq_copy_pages(cache: KVCache, src, dst, err_word=None, stream=None) -> None:
+    """Copy whole pages of K and V: src[i] to dst[i]; pairs with a negative page are left
+    out."""
+    L = _lib or load()
+    c = cache.c()
+    dev = cache.k_pool.get_device()
+    if cache.v_pool.get_device() != dev:
+        raise ValueError("k_pool and v_pool lie on different devices")
+    _launch(L.kvq_copy_pages, "kvq_copy_pages", dev, stream,
+            (ctypes.byref(c), *_pairs(src, dst, dev), _err(err_word, dev)))
+
+
+def kvq_block_copy_pages(cache: BlockKVCache, src, dst, err_word=None, stream=None) -> None:
+    """kvq_copy_pages for the block-scaled cache: codes and scales."""
+    L = _lib or load()
+    c, dev, _, _ = cache.c()
+    _launch(L.kvq_block_copy_pages, "kvq_block_copy_pages", dev, stream,
+            (c, *_pairs(src, dst, dev), _err(err_word, dev)))

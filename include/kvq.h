@@ -216,6 +216,89 @@ KVQ_API kvq_status kvq_pages_update(int32_t *free_stack, int32_t *free_count, ui
                                     int32_t n_acq, uint8_t *acq_ok, uint32_t *err_word,
                                     kvq_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Pages that several requests hold: one prompt answered several times, a system
+ * prompt kept for many users, a search over beams.  The allocator's state as in
+ * kvq_pages_update, and page_shares int32 [num_pages]: how many block-table entries
+ * hold a page beyond the first (0 for a free page, and for one that
+ * kvq_pages_update hands out; so all zeros at the start, and acquisitions there go on
+ * as they are).  Once pages may be shared they are given back by kvq_pages_release:
+ * the releases of kvq_pages_update push a page whoever else holds it.
+ * Tags: a shared page keeps its tag, and a request that takes it expects that tag;
+ * a page that is handed out, or moved to, gets a new one.
+ * workspace: 256-byte aligned, kvq_pages_workspace_size() bytes (0: bad sizes),
+ * for the three calls alike; its contents need no preparation, and calls that can run
+ * at the same time do not share it, nor the state.
+ * ------------------------------------------------------------------------- */
+KVQ_API size_t kvq_pages_workspace_size(int32_t num_pages, int32_t B);
+
+/* Forks requests: for i = 0 .. n_fork-1, request dst_req[i] gets the first
+ * n_tokens[i] tokens of request src_req[i].  The whole pages among them are shared:
+ * dst's block-table and expected-tag entries become src's, and page_shares counts
+ * the holder.  A part-filled last page becomes a fresh one (popped off the stack, with a
+ * new tag), because both requests will write there: copy_src[i] is the page that it
+ * replaces and copy_dst[i] the fresh one, for kvq_copy_pages or
+ * kvq_block_copy_pages before either request appends; both are -1 where there is
+ * none.  fork_ok[i] (uint8) is 1 if the fork was served, else 0.
+ * A fork with a request outside [0, B), with src == dst, whose dst an earlier fork of the call
+ * has, or whose src any fork writes, raises KVQ_ERRBIT_REQ; n_tokens negative or
+ * above MP * page_size _POS; a needed entry of src that is not a page id _PAGE: these
+ * get nothing.  The others are served in order; the first that finds the stack empty
+ * and every one after it get nothing (_EXHAUSTED).  A popped entry that is not a page
+ * id is consumed unmapped (_PAGE).  A *free_count outside [0, num_pages] serves nobody
+ * (_PAGE).  dst's entries behind the pages that it gets are left as they were.
+ * Precondition (unchecked): src holds n_tokens tokens, and dst no pages. */
+KVQ_API kvq_status kvq_pages_fork(int32_t *free_stack, int32_t *free_count, uint32_t *page_tags,
+                                  int32_t *page_shares, int32_t num_pages, int32_t *block_table,
+                                  uint32_t *expected_tags, int32_t B, int32_t MP, int32_t page_size,
+                                  const int32_t *src_req, const int32_t *dst_req,
+                                  const int32_t *n_tokens, int32_t n_fork, int32_t *copy_src,
+                                  int32_t *copy_dst, uint8_t *fork_ok, void *workspace,
+                                  size_t workspace_bytes, uint32_t *err_word, kvq_stream_t stream);
+
+/* Gives pages back: for j = 0 .. n_rel-1 in order, request rel_req[j] lets go of its
+ * logical pages rel_first[j] .. rel_first[j] + rel_npages[j] - 1 in order (rel_first
+ * NULL: from page 0).  Each entry becomes -1; a page that others still hold loses
+ * one holder, and the last holder's page id is pushed on the stack.  Tags are unchanged.
+ * All or nothing: if a request is outside [0, B) or named twice (KVQ_ERRBIT_REQ), a range
+ * lies outside [0, MP] or the list has 2^31 pages (_POS), an entry is not a page id, is
+ * given back more often than it is held, the pushes would overfill the stack or
+ * *free_count is outside [0, num_pages] (_PAGE), nothing changes. */
+KVQ_API kvq_status kvq_pages_release(int32_t *free_stack, int32_t *free_count, int32_t *page_shares,
+                                     int32_t num_pages, int32_t *block_table, int32_t B, int32_t MP,
+                                     const int32_t *rel_req, const int32_t *rel_first,
+                                     const int32_t *rel_npages, int32_t n_rel, void *workspace,
+                                     size_t workspace_bytes, uint32_t *err_word,
+                                     kvq_stream_t stream);
+
+/* Moves the pool together: afterwards its pages in use are ids 0 .. live - 1, live =
+ * num_pages - *free_count, so that what lies behind can be cut off or saved apart.
+ * The k-th smallest page in use from `live` on (copy_src[k]) goes to the k-th smallest
+ * free page below (copy_dst[k]), whose tag is incremented; *n_moves (device int32) counts
+ * them, and the lists' other entries are -1.  Every request's first held[b] (int32 [B])
+ * block-table entries are renamed, and where they changed expect the new tag;
+ * page_shares moves along; the stack becomes num_pages - 1 .. live, the lowest on
+ * top.  The pages' contents are moved by kvq_copy_pages or kvq_block_copy_pages with the
+ * same lists (n = copy_cap), before anything reads or writes them.
+ * copy_cap: entries of each list, at least num_pages / 2.
+ * All or nothing: if held[b] is outside [0, MP] (KVQ_ERRBIT_POS), a stack entry is not a
+ * page id or there twice, a held entry is not a page id or is free, or *free_count is
+ * outside [0, num_pages] (_PAGE), nothing changes and the lists are all -1. */
+KVQ_API kvq_status kvq_pages_compact(int32_t *free_stack, int32_t *free_count, uint32_t *page_tags,
+                                     int32_t *page_shares, int32_t num_pages, int32_t *block_table,
+                                     uint32_t *expected_tags, int32_t B, int32_t MP,
+                                     const int32_t *held, int32_t *copy_src, int32_t *copy_dst,
+                                     int32_t copy_cap, int32_t *n_moves, void *workspace,
+                                     size_t workspace_bytes, uint32_t *err_word,
+                                     kvq_stream_t stream);
+
+/* Copies whole pages, K and V, of all kv heads: page src[i] to page dst[i] (int32
+ * [n], device).  A pair with a negative page, or of a page with itself, is left out; a
+ * page id of num_pages or more raises KVQ_ERRBIT_PAGE and its pair is left out.  No
+ * pair's dst may be another pair's src or dst (its contents are unspecified then). */
+KVQ_API kvq_status kvq_copy_pages(const kvq_cache *cache, const int32_t *src, const int32_t *dst,
+                                  int32_t n, uint32_t *err_word, kvq_stream_t stream);
+
 /* Weight-only quantised matrix product for decode ([KVQ] section "模型权重压缩":
  * the decode pool keeps the weights as 4-bit integers instead of FP8; every
  * token reads all of them, so decode is bandwidth-bound; INT4 values are
@@ -445,6 +528,11 @@ KVQ_API kvq_status kvq_block_read(const kvq_block_cache *cache, const int32_t *t
                                   const int32_t *block_table, int32_t B, int32_t MP, void *k_out,
                                   int64_t k_stride, void *v_out, int64_t v_stride,
                                   uint32_t *err_word, kvq_stream_t stream);
+
+/* kvq_copy_pages for the block-scaled cache: codes and scales. */
+KVQ_API kvq_status kvq_block_copy_pages(const kvq_block_cache *cache, const int32_t *src,
+                                        const int32_t *dst, int32_t n, uint32_t *err_word,
+                                        kvq_stream_t stream);
 
 /* Bytes of device workspace kvq_block_attn needs on the current device, for
  * at most B requests of at most max_q rows each (0: bad sizes). */
