@@ -18,7 +18,8 @@ LIB = os.path.join(OUT_DIR, "libkvq.so")
 
 SOURCES = ["api.cu", "append.cu", "handoff.cu", "check_tags.cu", "pages.cu", "decode_attn.cu",
            "decode_attn_static.cu", "wq_gemm.cu", "selftest.cu", "rope.cu", "block_cache.cu",
-           "block_attn.cu", "pages_shared.cu", "copy_pages.cu"]
+           "block_attn.cu", "pages_shared.cu", "copy_pages.cu",
+           "block_prefix.cu"]
 HEADERS = ["kvq_device.cuh", "kvq_internal.h", "quant_e4m3.cuh", "check_body.cuh",
            "decode_common.cuh", "decode_attn_mma.cuh", "block_common.cuh", "block_attn_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

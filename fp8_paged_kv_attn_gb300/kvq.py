@@ -56,7 +56,8 @@ EXPORTS = ("kvq_append", "kvq_append_check", "kvq_handoff_pages", "kvq_check_tag
            "kvq_rope_inv_freq", "kvq_rope", "kvq_block_append", "kvq_rope_block_append",
            "kvq_block_read", "kvq_block_attn_workspace_size", "kvq_block_attn",
            "kvq_pages_workspace_size", "kvq_pages_fork", "kvq_pages_release", "kvq_pages_compact",
-           "kvq_copy_pages", "kvq_block_copy_pages")
+           "kvq_copy_pages", "kvq_block_copy_pages", "kvq_block_prefix_attn_workspace_size",
+           "kvq_block_prefix_attn")
 STATIC_SCRATCH_BYTES = 64 << 20
 
 
@@ -144,6 +145,11 @@ def load(build_if_missing: bool = True):
     L.kvq_block_attn.argtypes = [bp, vp, i64, i32, vp, i32, i32, vp, vp, i32, i32, vp, f32, vp,
                                  vp, sz, vp, vp]
     L.kvq_block_attn.restype = ctypes.c_int
+    L.kvq_block_prefix_attn_workspace_size.argtypes = [i32, i32, i32, i32]
+    L.kvq_block_prefix_attn_workspace_size.restype = sz
+    L.kvq_block_prefix_attn.argtypes = [bp, vp, i64, i32, vp, i32, i32, vp, vp, i32, i32, vp, vp,
+                                        i32, vp, f32, vp, vp, sz, vp, vp]
+    L.kvq_block_prefix_attn.restype = ctypes.c_int
     L.kvq_pages_workspace_size.argtypes = [i32, i32]
     L.kvq_pages_workspace_size.restype = sz
     L.kvq_pages_fork.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, i32, vp,
@@ -690,6 +696,51 @@ def kvq_block_attn(cache: BlockKVCache, q, tok_start, seq_lens, block_table, out
              _arr(out, "out", _F32, (N, Hq, D), dev),
              _arr(workspace, "workspace", _BYTES, workspace.shape, dev), workspace.numel(),
              _err(err_word, dev)))
+
+
+def kvq_block_prefix_attn_workspace_size(n_tokens: int, Hq: int, num_kv_heads: int,
+                                         head_dim: int) -> int:
+    return int(load().kvq_block_prefix_attn_workspace_size(n_tokens, Hq, num_kv_heads, head_dim))
+
+
+def block_prefix_workspace(n_tokens: int, Hq: int, num_kv_heads: int, head_dim: int,
+                           device="cuda") -> torch.Tensor:
+    """Allocate (with torch) a workspace of the size kvq_block_prefix_attn needs for at most
+    n_tokens rows."""
+    with torch.cuda.device(device):
+        n = kvq_block_prefix_attn_workspace_size(n_tokens, Hq, num_kv_heads, head_dim)
+    if n == 0:
+        raise ValueError("kvq_block_prefix_attn does not support these sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def kvq_block_prefix_attn(cache: BlockKVCache, q, tok_start, seq_lens, block_table, group_start,
+                          prefix_pages, out, workspace, max_q: int = 1, abort_mask=None,
+                          sm_scale: Optional[float] = None, err_word=None, stream=None) -> None:
+    """Causal attention of each request's rows (at most max_q a request) over its cached tokens,
+    for requests in groups that share their first pages: requests group_start[g] ..
+    group_start[g + 1] - 1 (int32 [groups + 1]; None: no groups) hold the same prefix_pages[g]
+    pages in front (int32 [groups]), which are read once for the group.  q and out [rows, Hq,
+    D] bf16."""
+    L = _lib or load()
+    c, dev, _, D = cache.c()
+    N, Hq = q.shape[0], q.shape[1]
+    ts, sl, bt, B, MP = _step(tok_start, seq_lens, block_table, dev)
+    if group_start is None:
+        gs, pp, n_groups = None, None, 0
+        if prefix_pages is not None:
+            raise ValueError("group_start is missing")
+    else:
+        n_groups = group_start.shape[0] - 1
+        gs = _arr(group_start, "group_start", I32, (n_groups + 1,), dev)
+        if prefix_pages is None:
+            raise ValueError("prefix_pages is missing")
+        pp = _arr(prefix_pages, "prefix_pages", I32, (n_groups,), dev)
+    _launch(L.kvq_block_prefix_attn, "kvq_block_prefix_attn", dev, stream,
+            (c, *_rows(q, "q", N, Hq, D, dev), Hq, ts, N, max_q, sl, bt, B, MP, gs, pp, n_groups,
+             None if abort_mask is None else _arr(abort_mask, "abort_mask", U8, (B,), dev),
+             D ** -0.5 if sm_scale is None else sm_scale,
+             _arr(out, "out", BF16, (N, Hq, D), dev), *_ws(workspace, dev), _err(err_word, dev)))
 
 
 # ----------------------------------------------------------------------------

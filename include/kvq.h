@@ -572,6 +572,47 @@ KVQ_API kvq_status kvq_block_attn(const kvq_block_cache *cache, const void *q, i
                                   void *workspace, size_t workspace_bytes, uint32_t *err_word,
                                   kvq_stream_t stream);
 
+/* Bytes of device workspace kvq_block_prefix_attn needs on the current device, for at
+ * most n_tokens rows (0: bad sizes). */
+KVQ_API size_t kvq_block_prefix_attn_workspace_size(int32_t n_tokens, int32_t Hq,
+                                                    int32_t num_kv_heads, int32_t head_dim);
+
+/* kvq_block_attn for a batch whose requests share prefixes, with a bf16 output.  Requests
+ * group_start[g] .. group_start[g+1]-1 (int32 [n_groups+1], non-decreasing, within [0,
+ * B]) form group g, whose first prefix_pages[g] (int32 [n_groups]) logical pages are the
+ * same: forks of one request, or users of one system prompt.  They are read once for all
+ * rows of the group, through the block-table row of its first request that takes part;
+ * that the others' entries are the same is the caller's promise (unchecked).  Requests
+ * outside every group, and groups of no pages, have nothing in front of their own tokens;
+ * with n_groups 0 (both pointers may be NULL) it is causal attention as kvq_block_attn
+ * computes it.
+ *     s_j, out: as in kvq_block_attn, for every token j <= L - n_b + i; out bf16
+ *     [n_tokens][Hq][head_dim], contiguous, rounded once.
+ * Scores, softmax statistics and sums are fp32; a row of q is held to 2^-21 of its largest
+ * value and a softmax weight to 2^-11 of itself (f16), or to 2^-31 of the row's largest (each
+ * times its V scale) where that is more, so that nearly all of the output's error is its
+ * rounding to bf16.
+ * Requests are refused as in kvq_block_attn, and with KVQ_ERRBIT_SEQLEN where a prefix is
+ * negative or longer than MP pages, or reaches into a request's own rows, and with
+ * KVQ_ERRBIT_REQ where a request's rows do not lie between those of its group's ends (tok_start
+ * out of order): these requests' rows are zero.  A group_start out of order or range raises KVQ_ERRBIT_REQ, and every request's rows
+ * are zero.  An aborted request's own pages are not read and its rows are zero; its group goes
+ * on.  A page outside the pool raises KVQ_ERRBIT_PAGE and zeroes the rows that see it, in
+ * a prefix those of the whole group.  Rows of nobody are left as they were.
+ * max_q, strides, scales and limits as in kvq_block_attn; rows times heads a kv head are at most
+ * 2^30.  workspace: 256-byte aligned, kvq_block_prefix_attn_workspace_size() bytes for this many
+ * rows or more, not shared by calls that can run at the same time; its contents need no
+ * preparation. */
+KVQ_API kvq_status kvq_block_prefix_attn(const kvq_block_cache *cache, const void *q,
+                                         int64_t q_stride, int32_t Hq, const int32_t *tok_start,
+                                         int32_t n_tokens, int32_t max_q, const int32_t *seq_lens,
+                                         const int32_t *block_table, int32_t B, int32_t MP,
+                                         const int32_t *group_start, const int32_t *prefix_pages,
+                                         int32_t n_groups, const uint8_t *abort_mask,
+                                         float sm_scale, void *out, void *workspace,
+                                         size_t workspace_bytes, uint32_t *err_word,
+                                         kvq_stream_t stream);
+
 /* Self-test of a kernel failure path (no fault, no hang): one CTA starts a
  * real bulk copy of 64 bytes from src (device, 16-byte aligned) into shared
  * memory, then waits on an mbarrier that nothing ever arrives at, with the
