@@ -48,6 +48,7 @@
 #include "block_common.cuh"
 #include "decode_common.cuh"
 #include "decode_attn_mma.cuh"
+#include "tc_device.cuh"
 
 namespace kvq {
 
@@ -189,18 +190,6 @@ __device__ __forceinline__ bool ba_wait_warp(BaCtl &ctl, uint64_t *bar, uint32_t
   return __all_sync(0xffffffffu, ba_wait(ctl, bar, parity, err_word));
 }
 
-__device__ __forceinline__ void cp_async8(void *dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src)
-               : "memory");
-}
-
-// Arrives on the barrier once this thread's async copies so far have landed
-// (the arrival is one of the barrier's expected count).
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
-}
-
 // Byte offset of 16-byte chunk c of row r in a head's swizzled 16-row block.
 template <int D>
 __device__ __forceinline__ int swz(int r, int c) {
@@ -273,26 +262,6 @@ __device__ __forceinline__ void ba_begin(BaState<D, RK> &st, const BaArgs &a, co
 #pragma unroll
     for (int k = 0; k < KS; ++k) st.o[k][g][0] = st.o[k][g][1] = st.o[k][g][2] = st.o[k][g][3] = 0.f;
   }
-}
-
-// A V scale as 2^e times a fraction in (1/2, 1] (1 for a power of two), x the fraction and y
-// e: from the bits, since 2^-e has no fp32 for the scales above 2^126, and a subnormal scale's
-// weights would sit low in f16's range with e = -126.  0 is 0 times a power of two.
-__device__ __forceinline__ float2 split_scale(float s) {
-  const bool sub = s < 0x1p-126f;
-  const uint32_t u = __float_as_uint(sub ? s * 0x1p24f : s), frac = u & 0x7FFFFFu;
-  const int e = static_cast<int>(u >> 23) - (sub ? 151 : 127) + (frac ? 1 : 0);
-  return make_float2(frac ? __uint_as_float(frac | 0x3F000000u) : u ? 1.f : 0.f, static_cast<float>(e));
-}
-
-// 2^t / l as two factors, to be multiplied with in turn: a sum is undone by 2^t for t = n - m
-// (and the operand's scale), and neither that power nor its quotient need have an fp32 where
-// V scales are very large or small, or l is, behind a maximum that grew.  Where t is harmless
-// the second factor is the power of two in 1 / l, and nothing is rounded twice.
-__device__ __forceinline__ float2 out_scale(float t, float l) {
-  const int k = max(-126, min(126, static_cast<int>(__float_as_uint(l) >> 23) - 127));
-  const float u = fminf(fmaxf(t, -100.f), 40.f);
-  return make_float2(exp2f(u) / (l * pow2(-k)), exp2f(t - u - static_cast<float>(k)));
 }
 
 // The product alone, with no sum before it.

@@ -113,26 +113,6 @@ __device__ __forceinline__ bool tc_wait(TcCtl &ctl, uint64_t *bar, uint32_t pari
   return __all_sync(0xffffffffu, ok);
 }
 
-__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// Shared-memory operand of 128-byte rows, 128-byte swizzle, 8-row groups 1,024
-// bytes apart (bits 46-48: descriptor version 1; 61-63: the swizzle).
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
-  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
-         (2ull << 61);
-}
-
-// One lane of the (whole) warp, always the same.  Under this test the compiler
-// knows that a single thread issues an MMA or a copy; under `lane == 0` it issues them
-// in a loop over lanes (an MMA every 66 cycles at least, 40 here).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-  return one != 0;
-}
-
 // fp32 += A * e4m3, 128 x n; A is e4m3 or e5m2; transposed: it is MN-major.
 __host__ __device__ constexpr uint32_t tc_idesc(uint32_t n, bool transposed, bool e5m2) {
   return (1u << 4) | ((e5m2 ? 1u : 0u) << 7) | ((transposed ? 1u : 0u) << 15) | ((n >> 3) << 17) | ((128u >> 4) << 24);
@@ -144,47 +124,6 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(add ? 1 : 0)
       : "memory");
-}
-
-__device__ __forceinline__ void tc_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_addr(bar))
-               : "memory");
-}
-
-// Consecutive columns of this warp's 32 lanes.
-__device__ __forceinline__ void tc_ld16(float (&v)[16], uint32_t addr) {
-  uint32_t *r = reinterpret_cast<uint32_t *>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
-      "[%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tc_st16(uint32_t addr, const float (&v)[16]) {
-  const uint32_t *r = reinterpret_cast<const uint32_t *>(v);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
-      : "memory");
-}
-
-// q's pieces of two values: e4m3, and e5m2 of what is left.  A bf16 value's eight bits
-// less their rounding to four are at most eight units of the last place, and e5m2's three
-// bits hold those, down to 2^-13; only a value below e4m3's smallest normal number, 2^-6,
-// is off, by at most 2^-14.
-__device__ __forceinline__ void tc_q_pieces(float x, float y, int shift, uint32_t &c1, uint32_t &c2) {
-  const uint16_t c = f32x2_to_e4m3x2(x, y);
-  const float2 p = f16x2_to_f32x2(e4m3x2_to_f16x2(c));
-  uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y - p.y), "f"(x - p.x));
-  c1 |= static_cast<uint32_t>(c) << shift;
-  c2 |= static_cast<uint32_t>(r) << shift;
 }
 
 // e4m3 codes of two f16 values.
@@ -218,16 +157,6 @@ __device__ __forceinline__ void tc_pieces(float2 w, int shift, uint32_t &c1, uin
   x = __hfma2(lo, __float2half2_rn(1024.f), x);
   c3 |= tc_piece16(x) << shift;
   c4 |= f16x2_to_e4m3x2(x) << shift;
-}
-
-// Bit 7 of each byte that is a NaN code (0x7F or 0xFF; no carry leaves a byte).
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
-  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-}
-
-// 16-byte chunk c of row r in a 128-byte-swizzled tile.
-__device__ __forceinline__ uint8_t *tc_chunk(uint8_t *tile, int r, int c) {
-  return tile + r * 128 + ((c ^ (r & 7)) * 16);
 }
 
 // q's rows into the two piece tiles, each row at 32 p + r for every p; warp
