@@ -1,8 +1,13 @@
 // kvq_block_prefix_attn: causal attention over the block-scaled cache for a batch
 // whose requests form groups with a shared prefix of whole pages.
+#include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "block_common.cuh"
+#include "decode_common.cuh"
+#include "decode_attn_mma.cuh"
+#include "tc_device.cuh"
 
 namespace kvq {
 
@@ -12,8 +17,9 @@ struct PfArgs {
   Ragged rg;
   const int32_t *block_table, *group_start, *prefix_pages;
   const uint8_t *abort_mask;
-  const uint8_t *k_pool, *v_pool;
   const float2 *scales;  // [num_pages][Hkv]
+  float *rows;  // [2][n_tokens][Hq][D + kStat]: a row's prefix, and its own tokens
+  float *cut;   // [2 CTAs][kPxRows][D + kStat]: parts of rows of work that CTAs share
   uint16_t *out;
   uint32_t *err_word;
   int32_t num_pages, p_shift, Hkv, Hq, G, MP, max_q, n_groups;
@@ -72,71 +78,1008 @@ __device__ __forceinline__ bool pf_group_ok(const PfArgs &a, int g) {
   return s >= 0 && s <= e && e <= a.rg.B;
 }
 
-constexpr int kPfWarps = 8;
+// ---------------------------------------------------------------------------
+// work: items, rows of work, segments
+// ---------------------------------------------------------------------------
 
-template <int D>
-__global__ void __launch_bounds__(32 * kPfWarps) prefix_kernel(PfArgs a) {
-  constexpr int V = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x;
-  grid_dependency_wait();
-  allow_dependents();
-  bool order = true;
-  for (int g = threadIdx.x; g < a.n_groups; g += 32 * kPfWarps) order &= pf_group_ok(a, g);
-  order = __syncthreads_and(order);
-  PfReq rq = order ? pf_request(a, b) : PfReq{request_rows<true>(a.rg, b), 0, -1, false};
-  if (!order) rq.r.err |= KVQ_ERRBIT_REQ;
-  if (rq.r.err && blockIdx.y == 0 && threadIdx.x == 0) report(a.err_word, rq.r.err);
-  const bool live = rq.live && order;
-  int leader = b;
-  if (live && rq.pre > 0)
-    for (leader = __ldg(a.group_start + rq.group); leader < b && !pf_request(a, leader).live;) ++leader;
-  const int32_t *mine = a.block_table + static_cast<int64_t>(b) * a.MP;
-  const int32_t *first = a.block_table + static_cast<int64_t>(leader) * a.MP;
-  for (int u = blockIdx.y * kPfWarps + warp; u < rq.r.n * a.Hq; u += gridDim.y * kPfWarps) {
-    const int i = u / a.Hq, h = u - i * a.Hq, kvh = h / a.G;
-    uint16_t *o = a.out + ((static_cast<int64_t>(rq.r.row) + i) * a.Hq + h) * D;
-    float acc[V], q[V], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      acc[k] = 0.f;
-      q[k] = live ? __uint_as_float(static_cast<uint32_t>(a.q[(static_cast<int64_t>(rq.r.row) + i) * a.q_stride +
-                                                            h * D + lane + 32 * k]) << 16)
-                  : 0.f;
-    }
-    bool bad = !live;
-    const int L = rq.r.p0 + i + 1;
-    for (int t = 0; !bad && t < L; ++t) {
-      const int page = __ldg((t < rq.pre ? first : mine) + (t >> a.p_shift));
-      if (page < 0 || page >= a.num_pages) {
-        if (lane == 0) report(a.err_word, KVQ_ERRBIT_PAGE);
-        bad = true;
+constexpr int kPxTok = 128;         // tokens a tile
+constexpr int kPxRows = 128;        // rows a block
+constexpr int kPxRowCost = 3;       // a row of work's start and end, in tiles' times
+constexpr int kPxSegs = 8;          // segment descriptors in flight
+constexpr int kPxStats = 4;         // segments whose statistics are in flight
+constexpr int kPxScales = 8;        // tiles whose scales are in flight
+constexpr int kPxK = 4, kPxV = 3;   // tiles of K and of V in flight
+constexpr int kStat = 4;            // floats behind a row's sums
+// a row's fourth statistic: its sums lie here, in the parts of several CTAs, or it is written
+constexpr float kHere = 1.f, kCut = 2.f, kDone = 3.f;
+constexpr int kPxSoft = 8, kPxConv = 4, kPxEdge = 4;  // warps
+constexpr int kPxMma = kPxSoft + kPxConv + kPxEdge, kPxThreads = 32 * (kPxMma + 3);
+constexpr float kPxFar = 64.f;      // how far the denominator's reference may be off (fp32)
+
+// An item: the prefix of a group for all its rows, or a request's own tokens for its rows.
+struct PxItem {
+  int b;           // whose block table
+  int row0, n;     // token rows
+  int first, end;  // tokens [first, end)
+  int p0;          // position of its first row (own tokens)
+  int rows, nb;    // rows (token rows times heads a kv head), blocks of them
+  bool own, pre, live;  // pre: own tokens behind a prefix
+};
+
+__device__ __forceinline__ PxItem px_item(const PfArgs &a, int i) {
+  PxItem o;
+  o.live = false;
+  if (i < a.n_groups) {
+    const int s = __ldg(a.group_start + i), e = __ldg(a.group_start + i + 1);
+    const int pages = __ldg(a.prefix_pages + i);
+    if (s >= e || pages <= 0 || pages > a.MP) return o;
+    const int2 r = pf_group_rows(a, i);
+    o.row0 = r.x;
+    o.n = r.y - r.x;
+    for (o.b = s; o.n > 0 && o.b < e; ++o.b)
+      if (pf_request(a, o.b).live) {
+        o.live = true;
         break;
       }
-      const float2 sc = __ldg(a.scales + static_cast<int64_t>(page) * a.Hkv + kvh);
-      const int64_t at = (((static_cast<int64_t>(page) * a.Hkv + kvh) << a.p_shift) + (t & ((1 << a.p_shift) - 1))) * D;
-      float s = 0.f, v[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const uint32_t c = __ldg(a.k_pool + at + lane + 32 * k) | (__ldg(a.v_pool + at + lane + 32 * k) << 8);
-        const uint32_t f = e4m3x2_to_f16x2(static_cast<uint16_t>(c));
-        const float2 kv = __half22float2(*reinterpret_cast<const __half2 *>(&f));
-        s = fmaf(q[k], kv.x, s);
-        v[k] = kv.y * sc.y;
-      }
-#pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      s *= sc.x * a.q_scale;
-      const float M = fmaxf(m, s), f = exp2f(m - M), p = exp2f(s - M);
-      m = M;
-      l = l * f + p;
-#pragma unroll
-      for (int k = 0; k < V; ++k) acc[k] = acc[k] * f + p * v[k];
+    o.first = 0;
+    o.end = pages << a.p_shift;
+    o.own = o.pre = false;
+    o.p0 = 0;
+  } else {
+    o.b = i - a.n_groups;
+    const PfReq q = pf_request(a, o.b);
+    o.live = q.live;
+    o.row0 = q.r.row;
+    o.n = q.r.n;
+    o.p0 = q.r.p0;
+    o.first = q.pre;
+    o.end = q.r.p0 + q.r.n;
+    o.own = true;
+    o.pre = q.pre > 0;
+  }
+  o.rows = o.n * a.G;
+  o.nb = (o.rows + kPxRows - 1) / kPxRows;
+  return o;
+}
+
+// Where the tokens end that block rb of an item sees.
+__device__ __forceinline__ int px_end(const PfArgs &a, const PxItem &it, int rb) {
+  return it.own ? it.p0 + 1 + (min((rb + 1) * kPxRows, it.rows) - 1) / a.G : it.end;
+}
+__device__ __forceinline__ int px_tiles(const PfArgs &a, const PxItem &it, int rb) {
+  return (px_end(a, it, rb) - it.first + kPxTok - 1) / kPxTok;
+}
+
+// Units of one kv head of an item.
+__device__ __forceinline__ int64_t px_units(const PfArgs &a, const PxItem &it) {
+  if (!it.live) return 0;
+  if (!it.own || it.nb == 1) return static_cast<int64_t>(it.nb) * (px_tiles(a, it, 0) + kPxRowCost);
+  int64_t u = 0;
+  for (int rb = 0; rb < it.nb; ++rb) u += px_tiles(a, it, rb) + kPxRowCost;
+  return u;
+}
+
+struct PxSeg {
+  int b, head, rb;         // b -1: no more segments
+  int row0, rows;          // the item's first token row; rows of this block that exist
+  int tok, tiles, t_end;   // first token, tiles, where the block's tokens end
+  int lim0;                // tokens that the item's first token row sees, each next one more; 0: all see all
+  int part, parts;         // the slot of a row of work that CTAs share, and how many share it
+  int own, pre;
+};
+
+// A producer's way through its CTA's run; every lane of the warp keeps the same.
+struct PxWalk {
+  int64_t u, u1, in, per;
+  int i;
+  PxItem it;
+  int64_t units;
+  bool fresh;
+};
+
+// The next segment; false: the run has ended.
+__device__ __forceinline__ bool px_next(const PfArgs &a, PxWalk &w, PxSeg &sg) {
+  while (w.u < w.u1) {
+    if (w.fresh) {
+      w.it = px_item(a, w.i);
+      w.units = px_units(a, w.it);
+      w.fresh = false;
     }
+    if (w.in >= w.units * a.Hkv) {
+      ++w.i;
+      w.in = 0;
+      w.fresh = true;
+      continue;
+    }
+    const int head = static_cast<int>(w.in / w.units);  // row of work: head major
+    int64_t s = w.in - head * w.units;
+    int rb = 0, tiles;
+    if (!w.it.own) {
+      tiles = px_tiles(a, w.it, 0);
+      rb = static_cast<int>(s / (tiles + kPxRowCost));
+      s -= static_cast<int64_t>(rb) * (tiles + kPxRowCost);
+    } else {
+      for (;; ++rb) {
+        tiles = px_tiles(a, w.it, rb);
+        if (s < tiles + kPxRowCost) break;
+        s -= tiles + kPxRowCost;
+      }
+    }
+    // units [0, kPxRowCost) of a row of work stand for its start; tile t is unit kPxRowCost + t
+    const int at = static_cast<int>(s);
+    const int span = static_cast<int>(min(static_cast<int64_t>(tiles + kPxRowCost - at), w.u1 - w.u));
+    const int t0 = max(0, at - kPxRowCost), take = at + span - kPxRowCost - t0;
+    const int64_t ut = w.u - at + kPxRowCost;  // its first tile
+    w.u += span;
+    w.in += span;
+    if (take <= 0) continue;
+    const int64_t c_lo = ut / w.per;
+    sg.parts = static_cast<int>((ut + tiles - 1) / w.per - c_lo) + 1;
+    sg.part = sg.parts == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (t0 == 0 ? 1 : 0);
+    sg.b = w.it.b;
+    sg.head = head;
+    sg.rb = rb;
+    sg.row0 = w.it.row0;
+    sg.rows = min(w.it.rows - rb * kPxRows, kPxRows);
+    sg.tok = w.it.first + t0 * kPxTok;
+    sg.tiles = take;
+    sg.t_end = px_end(a, w.it, rb);
+    sg.lim0 = w.it.own ? w.it.p0 + 1 : 0;
+    sg.own = w.it.own;
+    sg.pre = w.it.pre;
+    return true;
+  }
+  return false;
+}
+
+// ---------------------------------------------------------------------------
+// shared memory and tcgen05
+// ---------------------------------------------------------------------------
+
+struct PxCtl {
+  float4 end[kPxStats][2][kPxRows];   // [segment][group]: m of its sum, l, n, how far it has come
+  PxSeg seg[kPxSegs];
+  uint64_t kfull[kPxK], kempty[kPxK], vfull[kPxV], vempty[kPxV];
+  uint64_t scfull[kPxScales], segfull[kPxSegs], segempty[kPxSegs];
+  uint64_t qfull[2], qfree[2], sfull[2], pfull[2], hfull[2], hempty[2];  // h: V in f16
+  uint64_t ref[2][4], stat[kPxStats], pvdone, odone, ofree, cv, drain;
+  float2 sc[kPxScales][kPxTok / 16];  // (K, V) scales of a tile's blocks
+  int bad[kPxScales];                 // first token of a page outside the pool, or INT_MAX
+  float qk[kPxStats][kPxRows];        // what undoes q's scale, times sm_scale log2(e)
+  float2 now[kPxRows];                // (m, n): a row's references
+  int nan_from[kPxStats][128];        // per dim: the first token with a NaN code that some row does not see
+  RunScan<kPxThreads> scan;
+  uint32_t tmem;
+  int fail;
+};
+
+constexpr uint32_t kPxS = 0, kPxO = 256, kPxQ = 384;  // TMEM columns
+
+template <int D>
+struct PxSmem {
+  static constexpr int kTile = kPxTok * D;      // a tile of K or V
+  static constexpr int kHalf = 2 * kTile;       // V in f16
+  static constexpr int kStage = 32 * 33 * 4;    // an edge warp's 32 rows and columns on their way out
+  static constexpr int k = 0, v = kPxK * kTile, h = v + kPxV * kTile, st = h + 2 * kHalf,
+                       ctl = st + kPxEdge * kStage;
+  static constexpr size_t bytes = ctl + sizeof(PxCtl) + 1024;
+  static_assert(bytes <= 227 * 1024 && ctl % 16 == 0, "shared memory of a CTA");
+};
+
+__device__ __forceinline__ bool px_wait(PxCtl &ctl, uint64_t *bar, uint32_t parity, uint32_t *err_word) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  if (!ok && !*reinterpret_cast<volatile int *>(&ctl.fail)) {
+    ok = mbar_wait(bar, parity);
+    if (!ok && atomicExch(&ctl.fail, 1) == 0) report(err_word, KVQ_ERRBIT_TIMEOUT);
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Whether a phase is over, without waiting for it; the same for the whole warp.
+__device__ __forceinline__ bool px_test(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, done != 0);
+}
+
+// Rows of D bytes: for 64 a 64-byte swizzle, 8-row groups 512 bytes apart.
+template <int D>
+__device__ __forceinline__ uint64_t px_kdesc(uint32_t addr) {
+  if (D == 128) return tc_desc(addr);
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (1ull << 16) | (32ull << 32) | (1ull << 46) | (4ull << 61);
+}
+
+// V in f16, tokens by dims, dims contiguous: 64 dims a row of 128 bytes, 128-byte swizzle;
+// 8 tokens 1,024 bytes apart, the other 64 dims 16 KB.
+__device__ __forceinline__ uint64_t px_vdesc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// fp32 += A (TMEM, 128 rows) * B (shared memory, n columns)
+__device__ __forceinline__ void px_mma8(uint32_t d, uint32_t a, uint64_t b, uint32_t n, bool e5m2, bool add) {
+  const uint32_t idesc = (1u << 4) | ((e5m2 ? 1u : 0u) << 7) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add ? 1 : 0)
+      : "memory");
+}
+
+// the same, f16 by f16, B with its columns contiguous (bit 16)
+__device__ __forceinline__ void px_mma16(uint32_t d, uint32_t a, uint64_t b, uint32_t n, bool add) {
+  const uint32_t idesc = (1u << 4) | (1u << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add ? 1 : 0)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_ld32(float (&v)[32], uint32_t addr) {
+  uint32_t *r = reinterpret_cast<uint32_t *>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tc_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------
+
+// This lane's row of a segment's q into TMEM: two pieces of D / 4 columns.
+template <int D>
+__device__ __forceinline__ void px_load_q(const PfArgs &a, const PxSeg &sg, uint32_t cols, float *qk, int r) {
+  const int row = sg.rb * kPxRows + r, i = row / a.G;
+  const uint4 *p = reinterpret_cast<const uint4 *>(a.q + (static_cast<int64_t>(sg.row0) + i) * a.q_stride +
+                                                   static_cast<int64_t>(sg.head * a.G + row - i * a.G) * D);
+  float mx = 0.f;
+  bool odd = false;  // inf or NaN: the row's scores are NaN, as inf - inf would make them
 #pragma unroll
-    for (int k = 0; k < V; ++k)
-      o[lane + 32 * k] = static_cast<uint16_t>(pack_bf16x2(bad ? 0.f : acc[k] / l, 0.f));
+  for (int c = 0; c < D / 8; ++c) {
+    float x[8];
+    unpack8(r < sg.rows ? __ldg(p + c) : make_uint4(0, 0, 0, 0), x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      mx = fmaxf(mx, finite_abs(x[k]));
+      odd |= !(fabsf(x[k]) < INFINITY);
+    }
+  }
+  const int e = block_exponent(mx);  // the largest value into [224, 448]
+  // a negative sm_scale's sign goes to q, so that a larger score is a larger product
+  const float up = copysignf(pow2(-e), a.q_scale), nan = odd ? NAN : 0.f;
+#pragma unroll 1
+  for (int c = 0; c < D / 64; ++c) {  // 64 dims: 16 columns of each piece (the row lies in L1 now)
+    float q1[16], q2[16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float x[8];
+      unpack8(r < sg.rows ? __ldg(p + 8 * c + j) : make_uint4(0, 0, 0, 0), x);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t c1 = 0, c2 = 0;
+        tc_q_pieces(x[4 * k] * up + nan, x[4 * k + 1] * up + nan, 0, c1, c2);
+        tc_q_pieces(x[4 * k + 2] * up + nan, x[4 * k + 3] * up + nan, 16, c1, c2);
+        q1[2 * j + k] = __uint_as_float(c1);
+        q2[2 * j + k] = __uint_as_float(c2);
+      }
+    }
+    tc_st16(cols + 16 * c, q1);
+    tc_st16(cols + D / 4 + 16 * c, q2);
+  }
+  qk[r] = fabsf(a.q_scale) * pow2(e);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPxThreads, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, PfArgs a) {
+  using S = PxSmem<D>;
+  constexpr int RF = D + kStat;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  PxCtl &ctl = *reinterpret_cast<PxCtl *>(smem + S::ctl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPxK; ++i) {
+      mbar_init(&ctl.kfull[i], 1);
+      mbar_init(&ctl.kempty[i], 1);
+    }
+    for (int i = 0; i < kPxV; ++i) {
+      mbar_init(&ctl.vfull[i], 1);
+      mbar_init(&ctl.vempty[i], kPxConv);
+    }
+    for (int i = 0; i < kPxScales; ++i) mbar_init(&ctl.scfull[i], 1 + kPxTok / 16);
+    for (int i = 0; i < kPxSegs; ++i) {
+      mbar_init(&ctl.segfull[i], 1);
+      mbar_init(&ctl.segempty[i], kPxMma + 1);  // everybody but the producers
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.qfull[i], kPxEdge);
+      mbar_init(&ctl.qfree[i], 1);
+      mbar_init(&ctl.sfull[i], 1);
+      mbar_init(&ctl.pfull[i], 4);
+      mbar_init(&ctl.hfull[i], kPxConv);
+      mbar_init(&ctl.hempty[i], 1);
+      for (int q = 0; q < 4; ++q) mbar_init(&ctl.ref[i][q], 1);
+    }
+    for (int i = 0; i < kPxStats; ++i) mbar_init(&ctl.stat[i], kPxSoft + kPxConv);
+    mbar_init(&ctl.pvdone, 1);
+    mbar_init(&ctl.odone, 1);
+    mbar_init(&ctl.ofree, kPxEdge);
+    mbar_init(&ctl.cv, kPxConv);
+    mbar_init(&ctl.drain, 1);
+    ctl.fail = 0;
+    fence_barrier_init();
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+  }
+  if (warp == kPxMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&ctl.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = ctl.tmem;
+  grid_dependency_wait();
+  bool order = true;
+  for (int g = threadIdx.x; g < a.n_groups; g += kPxThreads) order &= pf_group_ok(a, g);
+  order = __syncthreads_and(order);
+  if (!order && blockIdx.x == 0 && threadIdx.x == 0) report(a.err_word, KVQ_ERRBIT_REQ);
+  const RunStart run = find_run<kPxThreads>(
+      order ? a.n_groups + a.rg.B : 0, gridDim.x, blockIdx.x, ctl.scan, [&](int i) -> int64_t {
+        if (blockIdx.x == 0 && i >= a.n_groups) {
+          const uint32_t err = pf_request(a, i - a.n_groups).r.err;
+          if (err) report(a.err_word, err);
+        }
+        return px_units(a, px_item(a, i)) * a.Hkv;
+      });
+  allow_dependents();
+  const int64_t u0 = blockIdx.x * run.per;
+  const int64_t u1 = min(u0 + run.per, run.total);
+
+  if (warp > kPxMma) {
+    // ------------------------------------------------------- producers: K, then V
+    const int is_v = warp - kPxMma - 1;
+    const CUtensorMap *map = is_v ? &vmap : &kmap;
+    uint64_t *full = is_v ? ctl.vfull : ctl.kfull, *empty = is_v ? ctl.vempty : ctl.kempty;
+    uint8_t *tiles_at = smem + (is_v ? S::v : S::k);
+    const uint32_t stages = is_v ? kPxV : kPxK;
+    uint64_t again;  // a prefix is read by several row blocks and CTAs
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(again));
+    const uint64_t once = policy_evict_first();
+    const int pages_tile = kPxTok >> a.p_shift;  // a tile begins with a page
+    const uint32_t page_bytes = static_cast<uint32_t>(D) << a.p_shift;
+    uint32_t g = 0, nseg = 0, par = 1, slot = 0;
+    bool ok = true;
+    PxWalk walk = {u0, u1, run.in, run.per, run.b, {}, 0, true};
+    PxSeg sg;
+    while (ok && px_next(a, walk, sg)) {
+      const int ss = nseg % kPxSegs;
+      if (!is_v) {
+        if (nseg >= kPxSegs) ok = px_wait(ctl, &ctl.segempty[ss], ((nseg / kPxSegs) - 1) & 1, a.err_word);
+        if (!ok) break;
+        if (lane == 0) {
+          ctl.seg[ss] = sg;
+          mbar_arrive(&ctl.segfull[ss]);
+        }
+      }
+      ++nseg;
+      const int32_t *bt = a.block_table + static_cast<int64_t>(sg.b) * a.MP;
+      for (int t = 0; t < sg.tiles; ++t) {
+        const int tok = sg.tok + t * kPxTok;
+        // lane j: page j of the tile
+        const int lp = (tok >> a.p_shift) + lane;
+        const bool needed = lane < pages_tile && static_cast<int64_t>(lp) << a.p_shift < sg.t_end;
+        const int page = needed ? __ldg(bt + lp) : 0;
+        const bool good = needed && page >= 0 && page < a.num_pages;
+        const uint32_t goods = __ballot_sync(0xffffffffu, good), needs = __ballot_sync(0xffffffffu, needed);
+        ok = px_wait(ctl, &empty[slot], par, a.err_word);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(__popc(goods)) * page_bytes);
+        __syncwarp();
+        int pages[kPxTok / 16];
+#pragma unroll
+        for (int j = 0; j < kPxTok / 16; ++j) pages[j] = __shfl_sync(0xffffffffu, page, j);
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < kPxTok / 16; ++j)
+            if (goods >> j & 1)
+              tma_load_4d(tiles_at + slot * S::kTile + j * page_bytes, map, 0, 0, sg.head, pages[j], &full[slot],
+                          sg.own ? once : again);
+        }
+        __syncwarp();
+        if (!is_v) {
+          const int cs = g % kPxScales, of = lane >> (a.p_shift - 4);  // the page of block `lane`
+          const int from = __shfl_sync(0xffffffffu, page, of & 31);
+          const bool has = goods >> (of & 31) & 1;
+          if (lane == 0) {
+            ctl.bad[cs] = needs == goods ? INT_MAX : tok + ((__ffs(needs ^ goods) - 1) << a.p_shift);
+            if (needs != goods) report(a.err_word, KVQ_ERRBIT_PAGE);
+            mbar_arrive(&ctl.scfull[cs]);
+          }
+          if (lane < kPxTok / 16) {
+            if (has) {
+              cp_async8(&ctl.sc[cs][lane], a.scales + static_cast<int64_t>(from) * a.Hkv + sg.head);
+              cp_async_arrive(&ctl.scfull[cs]);
+            } else {
+              ctl.sc[cs][lane] = make_float2(1.f, 1.f);  // masked tokens
+              mbar_arrive(&ctl.scfull[cs]);
+            }
+          }
+        }
+        ++g;
+        if (++slot == stages) {
+          slot = 0;
+          par ^= 1;
+        }
+        __syncwarp();
+      }
+    }
+    if (ok && !is_v) {  // nothing more
+      const int ss = nseg % kPxSegs;
+      if (nseg >= kPxSegs) ok = px_wait(ctl, &ctl.segempty[ss], ((nseg / kPxSegs) - 1) & 1, a.err_word);
+      if (ok && lane == 0) {
+        ctl.seg[ss].b = -1;
+        mbar_arrive(&ctl.segfull[ss]);
+      }
+    }
+    if (*reinterpret_cast<volatile int *>(&ctl.fail) && lane == 0)
+      for (uint32_t k = g > stages ? g - stages : 0; k < g; ++k) mbar_wait(&full[k % stages], (k / stages) & 1);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == kPxMma) {
+    // ------------------------------------------------------------- MMA issue
+    // Scores run up to two tiles ahead of values, into the next segment too: S(t) takes the
+    // columns of S(t - 2), whose weights PV(t - 2), issued before it, reads there.
+    const uint32_t k_a = smem_addr(smem + S::k), h_a = smem_addr(smem + S::h);
+    uint32_t ks = 0, ps = 0;  // segments of the scores' and of the values' cursor
+    int kt = 0, pt = 0;       // tiles in them
+    uint32_t kg = 0, pg = 0;  // tiles so far
+    PxSeg ksg, psg;
+    bool ok = true, k_in = false, p_in = false, k_end = false;
+    auto tokens = [](const PxSeg &sg, int t) {  // of a tile, in whole chunks of 32
+      return min(kPxTok, (sg.t_end - sg.tok - t * kPxTok + 31) & ~31);
+    };
+    while (ok) {
+      while (ok && !k_end && kg - pg < 2) {
+        if (!k_in) {  // the next segment: waited for only when nothing else is to be done
+          const int ss = ks % kPxSegs;
+          const uint32_t sp = (ks / kPxSegs) & 1, qp = (ks >> 1) & 1;
+          if (kg != pg && !px_test(&ctl.segfull[ss], sp)) break;
+          ok = px_wait(ctl, &ctl.segfull[ss], sp, a.err_word);
+          if (!ok) break;
+          ksg = ctl.seg[ss];
+          if (ksg.b < 0) {
+            k_end = true;
+            break;
+          }
+          if (kg != pg && !px_test(&ctl.qfull[ks & 1], qp)) break;
+          ok = px_wait(ctl, &ctl.qfull[ks & 1], qp, a.err_word);
+          if (!ok) break;
+          k_in = true;
+          kt = 0;
+        }
+        const int slot = kg % kPxK;
+        ok = px_wait(ctl, &ctl.kfull[slot], (kg / kPxK) & 1, a.err_word);
+        if (!ok) break;
+        tc_after();
+        const bool last = kt + 1 == ksg.tiles;
+        if (elect_one()) {
+          const uint64_t kd = px_kdesc<D>(k_a + slot * S::kTile);
+          const uint32_t q = tmem + kPxQ + (ks & 1) * (D / 2), n = tokens(ksg, kt);
+#pragma unroll
+          for (int piece = 1; piece >= 0; --piece)  // the smaller first: each sum is truncated
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+              px_mma8(tmem + kPxS + 128 * (kg & 1), q + piece * (D / 4) + 8 * k, kd + 2 * k, n, piece == 1,
+                      piece == 0 || k > 0);
+          tc_commit(&ctl.sfull[kg & 1]);
+          tc_commit(&ctl.kempty[slot]);
+        }
+        __syncwarp();
+        // (a condition within the elected lane's block lost the commit: it stands around the election)
+        if (last && elect_one()) tc_commit(&ctl.qfree[ks & 1]);
+        __syncwarp();
+        ++kg;
+        ++kt;
+        if (last) {
+          k_in = false;
+          ++ks;
+        }
+      }
+      if (!ok || (k_end && kg == pg)) break;
+      if (!p_in) {
+        psg = ctl.seg[ps % kPxSegs];  // (its scores have been issued)
+        p_in = true;
+        pt = 0;
+      }
+      const int buf = pg & 1;
+      ok = px_wait(ctl, &ctl.pfull[buf], (pg >> 1) & 1, a.err_word) &&
+           px_wait(ctl, &ctl.hfull[buf], (pg >> 1) & 1, a.err_word) &&
+           (pt > 0 || ps == 0 || px_wait(ctl, &ctl.ofree, (ps - 1) & 1, a.err_word));
+      if (!ok) break;
+      tc_after();
+      const bool last = pt + 1 == psg.tiles;
+      if (elect_one()) {
+        const uint64_t vd = px_vdesc(h_a + buf * S::kHalf);
+        const int steps = tokens(psg, pt) / 16;
+        for (int k = 0; k < steps; ++k)  // 16 tokens: 8 columns of P, 16 rows of V
+          px_mma16(tmem + kPxO, tmem + kPxS + 128 * buf + 8 * k, vd + k * (16 * 128 >> 4), D, pt > 0 || k > 0);
+        tc_commit(&ctl.hempty[buf]);
+        tc_commit(&ctl.pvdone);
+      }
+      __syncwarp();
+      if (last && elect_one()) tc_commit(&ctl.odone);
+      __syncwarp();
+      ++pg;
+      ++pt;
+      if (last) {
+        if (lane == 0) mbar_arrive(&ctl.segempty[ps % kPxSegs]);
+        p_in = false;
+        ++ps;
+      }
+    }
+    if (*reinterpret_cast<volatile int *>(&ctl.fail)) {
+      // the products in flight end before the CTA's memory goes to another one
+      if (elect_one()) tc_commit(&ctl.drain);
+      mbar_wait(&ctl.drain, 0);
+    }
+  } else if (warp >= kPxSoft + kPxConv) {
+    // ---------------------------------------------- edge: q in, sums out
+    const int quad = warp & 3, r = 32 * quad + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+    float *stage = reinterpret_cast<float *>(smem + S::st + quad * S::kStage);
+    auto load_q = [&](uint32_t k) -> bool {
+      const int ss = k % kPxSegs;
+      if (!px_wait(ctl, &ctl.segfull[ss], (k / kPxSegs) & 1, a.err_word)) return false;
+      const PxSeg sg = ctl.seg[ss];
+      if (sg.b < 0) return true;
+      if (k >= 2 && !px_wait(ctl, &ctl.qfree[k & 1], ((k >> 1) - 1) & 1, a.err_word)) return false;
+      tc_after();
+      if (32 * quad < sg.rows) px_load_q<D>(a, sg, tmem + lanes + kPxQ + (k & 1) * (D / 2), ctl.qk[k % kPxStats], r);
+      tc_st_wait();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.qfull[k & 1]);
+      return true;
+    };
+    bool ok = load_q(0);
+    for (uint32_t k = 0; ok; ++k) {
+      const PxSeg sg = ctl.seg[k % kPxSegs];
+      if (sg.b < 0) break;
+      ok = load_q(k + 1) && px_wait(ctl, &ctl.stat[k % kPxStats], (k / kPxStats) & 1, a.err_word) &&
+           px_wait(ctl, &ctl.odone, k & 1, a.err_word);
+      if (!ok) break;
+      tc_after();
+      if (32 * quad < sg.rows) {
+        const int row = sg.rb * kPxRows + r, i = row / a.G;
+        const float4 e0 = ctl.end[k % kPxStats][0][r], e1 = ctl.end[k % kPxStats][1][r];
+        const float4 fin = e0.w > e1.w ? e0 : e1;  // the last references
+        const float M = fin.x, N = fin.z;
+        const bool bad = e0.y < 0.f || e1.y < 0.f;
+        float l = e0.y == 0.f ? 0.f : e0.y * exp2f(e0.x - M);
+        l += e1.y == 0.f ? 0.f : e1.y * exp2f(e1.x - M);
+        if (bad) l = -1.f;
+        const int lim = sg.lim0 ? sg.lim0 + i : INT_MAX;
+        const bool whole = sg.part < 0 && sg.own && !sg.pre;  // nothing to be merged with
+        const float2 f = whole ? out_scale(N - M - 7.f, l) : make_float2(1.f, 1.f);
+        const int64_t at = (static_cast<int64_t>(sg.row0) + i) * a.Hq + sg.head * a.G + row - i * a.G;
+        const int64_t here = (static_cast<int64_t>(sg.own) * a.rg.n_tokens * a.Hq + at) * RF;
+        const int64_t there = (static_cast<int64_t>(sg.part) * kPxRows + r) * RF;
+        float *sums = sg.part < 0 ? a.rows : a.cut;
+        if (r < sg.rows) {
+          *reinterpret_cast<float4 *>(sums + (sg.part < 0 ? here : there) + D) =
+              make_float4(M, l, N, whole ? kDone : kHere);
+          if (sg.part >= 0 && (sg.part & 1))  // the first part: where the others are
+            *reinterpret_cast<float4 *>(a.rows + here + D) =
+                make_float4(__int_as_float(sg.part >> 1), __int_as_float(sg.parts), 0.f, kCut);
+        }
+        const int *nan_from = ctl.nan_from[k % kPxStats];
+        const int64_t base = whole ? at * D : sg.part < 0 ? here : there;
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tc_ld32(o, tmem + lanes + kPxO + c);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float y = whole ? o[j] * f.x * f.y : o[j];
+            if (nan_from[c + j] < lim) y = NAN;
+            if (whole && bad) y = 0.f;
+            stage[lane * 33 + j] = y;
+          }
+          __syncwarp();
+          const int used = min(32, sg.rows - 32 * quad);
+          for (int rr = 0; rr < used; ++rr) {
+            const int64_t to = __shfl_sync(0xffffffffu, base, rr) + c + lane;
+            const float y = stage[rr * 33 + lane];
+            if (whole)
+              a.out[to] = static_cast<uint16_t>(pack_bf16x2(y, 0.f));
+            else
+              sums[to] = y;
+          }
+          __syncwarp();
+        }
+      }
+      tc_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ctl.ofree);
+        mbar_arrive(&ctl.segempty[k % kPxSegs]);
+      }
+    }
+  } else if (warp >= kPxSoft) {
+    // ------------------------------------------------ V from e4m3 to f16
+    const int quad = warp & 3;
+    constexpr int kC = D / 16, kR = 32 / kC;  // chunks of 16 codes a row; rows a pass
+    uint32_t g = 0;
+    bool ok = true;
+    for (uint32_t k = 0; ok; ++k) {
+      const int ss = k % kPxSegs;
+      ok = px_wait(ctl, &ctl.segfull[ss], (k / kPxSegs) & 1, a.err_word);
+      if (!ok) break;
+      const PxSeg sg = ctl.seg[ss];
+      if (sg.b < 0) break;
+      int *nan_from = ctl.nan_from[k % kPxStats];
+      nan_from[32 * quad + lane] = INT_MAX;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.cv);
+      ok = px_wait(ctl, &ctl.cv, k & 1, a.err_word);
+      const int min_lim = sg.lim0 ? min(sg.t_end, sg.lim0 + sg.rb * kPxRows / a.G) : sg.t_end;
+      for (int t = 0; ok && t < sg.tiles; ++t, ++g) {
+        const int slot = g % kPxV, buf = g & 1, tok = sg.tok + t * kPxTok + 32 * quad;
+        ok = px_wait(ctl, &ctl.vfull[slot], (g / kPxV) & 1, a.err_word) &&
+             px_wait(ctl, &ctl.hempty[buf], ((g >> 1) & 1) ^ 1, a.err_word);
+        if (!ok) break;
+        const uint8_t *v = smem + S::v + slot * S::kTile;
+        uint8_t *h = smem + S::h + buf * S::kHalf;
+        if (tok < sg.t_end) {
+          const bool partial = tok + 32 > min_lim;
+#pragma unroll
+          for (int it = 0; it < kC; ++it) {
+            const int row = 32 * quad + kR * it + lane / kC, j = lane % kC;
+            uint4 w;
+            if constexpr (D == 128)
+              w = *reinterpret_cast<const uint4 *>(v + row * 128 + ((j ^ (row & 7)) * 16));
+            else
+              w = *reinterpret_cast<const uint4 *>(v + row * 64 + ((j ^ ((row >> 1) & 3)) * 16));
+            uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            if (partial) {
+              const int tk = tok + kR * it + lane / kC;
+              if (tk >= sg.t_end) {
+                x[0] = x[1] = x[2] = x[3] = 0;  // cached bytes behind may be anything
+              } else if (tk >= min_lim) {
+                // a weight of 0 does not stop a NaN: it is put where its rows are written
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  uint32_t nan = nan_codes(x[q]);
+                  x[q] &= ~((nan >> 7) * 0xFFu);
+                  while (nan) {
+                    const int byte = (__ffs(nan) - 1) >> 3;
+                    nan &= nan - 1;
+                    atomicMin(&nan_from[16 * j + 4 * q + byte], tk);
+                  }
+                }
+              }
+            }
+            uint4 y[2];
+            uint32_t *o = reinterpret_cast<uint32_t *>(y);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              o[2 * q] = e4m3x2_to_f16x2(static_cast<uint16_t>(x[q] & 0xFFFFu));
+              o[2 * q + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(x[q] >> 16));
+            }
+            // 64 dims a row; the upper half's lanes store their second chunk first, so that a
+            // phase's eight lanes meet eight groups of banks
+            const int c = (2 * j) & 7, sel = D == 128 ? j >> 2 : 0;
+            uint8_t *to = h + (D == 128 ? (j >> 2) * 16384 : 0) + row * 128;
+            *reinterpret_cast<uint4 *>(to + (((c + sel) ^ (row & 7)) * 16)) = sel ? y[1] : y[0];
+            *reinterpret_cast<uint4 *>(to + (((c + 1 - sel) ^ (row & 7)) * 16)) = sel ? y[0] : y[1];
+          }
+        }
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ctl.vempty[slot]);
+          mbar_arrive(&ctl.hfull[buf]);
+        }
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ctl.stat[k % kPxStats]);
+        mbar_arrive(&ctl.segempty[ss]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int grp = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+    const uint32_t s_addr = tmem + lanes + kPxS + 128 * grp, o_addr = tmem + lanes + kPxO;
+    uint32_t g = 0;  // tiles of the CTA so far
+    bool ok = true;
+    for (uint32_t k = 0; ok; ++k) {
+      const int ss = k % kPxSegs;
+      ok = px_wait(ctl, &ctl.segfull[ss], (k / kPxSegs) & 1, a.err_word);
+      if (!ok) break;
+      const PxSeg sg = ctl.seg[ss];
+      if (sg.b < 0) break;
+      const bool act = 32 * quad < sg.rows;
+      const int lim = sg.lim0 ? min(sg.t_end, sg.lim0 + (sg.rb * kPxRows + r) / a.G) : sg.t_end;
+      const int min_lim = sg.lim0 ? min(sg.t_end, sg.lim0 + sg.rb * kPxRows / a.G) : sg.t_end;
+      float m = -INFINITY, n = -INFINITY, l = 0.f, lm = -INFINITY;
+      int bad_from = INT_MAX, come = 0;
+      for (int t = 0; t < sg.tiles; ++t, ++g) {
+        if ((g & 1) != static_cast<uint32_t>(grp)) continue;
+        const int cs = g % kPxScales, tok = sg.tok + t * kPxTok;
+        ok = px_wait(ctl, &ctl.sfull[grp], (g >> 1) & 1, a.err_word) &&
+             px_wait(ctl, &ctl.scfull[cs], (g / kPxScales) & 1, a.err_word);
+        if (!ok) break;
+        tc_after();
+        come = t + 1;
+        const int chunks = (min(kPxTok, sg.t_end - tok) + 31) >> 5;
+        const bool partial = tok + kPxTok > min_lim;
+        const float qk = act ? ctl.qk[k % kPxStats][r] : 0.f;
+        float mx = -INFINITY, mv = -INFINITY;
+        if (act) {
+          bad_from = min(bad_from, ctl.bad[cs]);
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            float x[32];
+            tc_ld32(x, s_addr + 32 * c);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float2 sc = ctl.sc[cs][2 * c + h];
+              float mt = -INFINITY;
+              if (partial) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  if (tok + 32 * c + 16 * h + j < lim) mt = fmaxf(mt, x[16 * h + j]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) mt = fmaxf(mt, x[16 * h + j]);
+              }
+              if (mt > -INFINITY) {  // (0 times -inf is no maximum)
+                const float y = mt * (qk * sc.x);
+                mx = fmaxf(mx, y);
+                mv = fmaxf(mv, y + split_scale(sc.y).y);
+              }
+            }
+          }
+        }
+        // the references, which the groups hand one another
+        if (g > 0) {
+          ok = px_wait(ctl, &ctl.ref[grp ^ 1][quad], ((g - 1) >> 1) & 1, a.err_word);
+          if (!ok) break;
+        }
+        float fo = 1.f;
+        if (act) {
+          if (t > 0) {
+            const float2 now = ctl.now[r];
+            m = now.x;
+            n = now.y;
+          }
+          if (m == -INFINITY || mx > m + kPxFar) m = mx;
+          if (n == -INFINITY) {
+            n = mv;
+          } else if (mv > n + kRescaleThreshold) {
+            fo = exp2f(n - mv);
+            n = mv;
+          }
+          ctl.now[r] = make_float2(m, n);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.ref[grp][quad]);
+        if (act) {
+          if (lm != m) {
+            l = l == 0.f ? 0.f : l * exp2f(lm - m);
+            lm = m;
+          }
+          if (t > 0 && __any_sync(0xffffffffu, fo != 1.f)) {
+            ok = px_wait(ctl, &ctl.pvdone, (g - 1) & 1, a.err_word);
+            if (!ok) break;
+            tc_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
+              tc_ld16(o, o_addr + c);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] *= fo;
+              tc_st16(o_addr + c, o);
+            }
+          }
+          const bool none = n == -INFINITY;  // nothing seen yet: every x is -inf
+          const float mm = none ? 0.f : m, mn = none ? 0.f : m - n;
+          float2 l2 = make_float2(0.f, 0.f);
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            float x[32], p[16];
+            tc_ld32(x, s_addr + 32 * c);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float2 sc = ctl.sc[cs][2 * c + h];
+              const float2 vs = split_scale(sc.y);
+              const float f = qk * sc.x;
+              // vs 2^(m - n), with kPScale (2^7) so that the largest weights sit high in f16's range
+              const float d = vs.x * kPScale * fast_exp2(fminf(mn + vs.y, 112.f));
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                float2 y = __ffma2_rn(make_float2(x[16 * h + j], x[16 * h + j + 1]), make_float2(f, f),
+                                      make_float2(-mm, -mm));
+                if (partial) {
+                  const int tk = tok + 32 * c + 16 * h + j;
+                  if (tk >= lim) y.x = -INFINITY;
+                  if (tk + 1 >= lim) y.y = -INFINITY;
+                }
+                const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                l2 = __fadd2_rn(l2, e);
+                const float2 w = __fmul2_rn(e, make_float2(d, d));
+                p[8 * h + j / 2] = __uint_as_float(f32x2_to_f16x2(w.x, w.y));
+              }
+            }
+            tc_st16(s_addr + 16 * c, p);
+          }
+          l += l2.x + l2.y;
+          tc_st_wait();
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.pfull[grp]);
+      }
+      if (!ok) break;
+      ctl.end[k % kPxStats][grp][r] = make_float4(lm, lim > bad_from ? -1.f : l, n, static_cast<float>(come));
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ctl.stat[k % kPxStats]);
+        mbar_arrive(&ctl.segempty[ss]);
+      }
+    }
+    tc_before();
+  }
+  __syncthreads();  // every role comes here, also when a wait gave up
+  if (warp == kPxMma) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
 }
+
+// ---------------------------------------------------------------------------
+// merge: a row's prefix and own tokens, each here or in the parts of several CTAs
+// ---------------------------------------------------------------------------
+
+constexpr int kPxMergeWarps = 8;
+
+template <int D>
+struct PxSum {
+  float M, N, l, acc[D / 32];
+  bool bad;
+};
+
+template <int D>
+__device__ __forceinline__ void px_add(PxSum<D> &s, const float *row, int lane) {
+  const float4 e = __ldcg(reinterpret_cast<const float4 *>(row + D));
+  float v[D / 32];
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) v[k] = __ldcg(row + lane + 32 * k);
+  s.bad |= e.y < 0.f;
+  if (e.y == 0.f) return;  // saw nothing
+  const float M = fmaxf(s.M, e.x), N = fmaxf(s.N, e.z);
+  const float fm = s.M == -INFINITY ? 0.f : exp2f(s.M - M), fn = s.N == -INFINITY ? 0.f : exp2f(s.N - N);
+  const float gm = exp2f(e.x - M), gn = exp2f(e.z - N);
+  s.l = fmaf(gm, e.y, s.l * fm);
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) s.acc[k] = fmaf(gn, v[k], s.acc[k] * fn);
+  s.M = M;
+  s.N = N;
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kPxMergeWarps) prefix_merge_kernel(PfArgs a) {
+  constexpr int RF = D + kStat;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x;
+  // the inputs were written before the kernel ahead began; its results come after the wait
+  bool order = true;
+  for (int g = threadIdx.x; g < a.n_groups; g += 32 * kPxMergeWarps) order &= pf_group_ok(a, g);
+  order = __syncthreads_and(order);
+  const PfReq rq = order ? pf_request(a, b) : PfReq{request_rows<true>(a.rg, b), 0, -1, false};
+  const int row_pre = rq.group >= 0 && rq.pre > 0 ? pf_group_rows(a, rq.group).x : 0;
+  grid_dependency_wait();
+  allow_dependents();
+  for (int64_t u = blockIdx.y * kPxMergeWarps + warp; u < static_cast<int64_t>(rq.r.n) * a.Hq;
+       u += gridDim.y * kPxMergeWarps) {
+    const int i = static_cast<int>(u / a.Hq), h = static_cast<int>(u - static_cast<int64_t>(i) * a.Hq);
+    const int token = rq.r.row + i, kvh = h / a.G;
+    const int64_t at = static_cast<int64_t>(token) * a.Hq + h;
+    uint16_t *o = a.out + at * D;
+    if (!rq.live) {
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) o[lane + 32 * k] = 0;
+      continue;
+    }
+    PxSum<D> s;
+    s.M = s.N = -INFINITY;
+    s.l = 0.f;
+    s.bad = false;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) s.acc[k] = 0.f;
+    bool done = false;
+    for (int own = rq.pre > 0 ? 0 : 1; own < 2; ++own) {
+      const float *row = a.rows + (static_cast<int64_t>(own) * a.rg.n_tokens * a.Hq + at) * RF;
+      const float4 e = __ldcg(reinterpret_cast<const float4 *>(row + D));
+      if (e.w == kDone) {
+        done = true;
+      } else if (e.w == kHere) {
+        px_add<D>(s, row, lane);
+      } else {
+        // part p lies in the p-th CTA from here on: the first in slot 1, others in slot 0
+        const int cta = __float_as_int(e.x), parts = __float_as_int(e.y);
+        const int r = ((token - (own ? rq.r.row : row_pre)) * a.G + h - kvh * a.G) % kPxRows;
+        for (int p = 0; p < parts; ++p)
+          px_add<D>(s, a.cut + (static_cast<int64_t>(2 * (cta + p) + (p == 0)) * kPxRows + r) * RF, lane);
+      }
+    }
+    if (done) continue;
+    const float2 f = out_scale(s.N - s.M - 7.f, s.l);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k)
+      o[lane + 32 * k] = static_cast<uint16_t>(pack_bf16x2(s.bad ? 0.f : s.acc[k] * f.x * f.y, 0.f));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+namespace {
+
+size_t px_up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+size_t px_rows_bytes(int64_t n_tokens, int Hq, int D) {
+  return px_up256(2ull * n_tokens * Hq * (D + kStat) * sizeof(float));
+}
+size_t px_cut_bytes(int ctas, int D) { return px_up256(2ull * ctas * kPxRows * (D + kStat) * sizeof(float)); }
+
+using PxFn = void (*)(CUtensorMap, CUtensorMap, PfArgs);
+
+// Opt the kernel into its shared memory, once per device.
+bool px_opt_in(PxFn fn, int variant, size_t smem) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<bool> done[kMaxDev][2];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return false;
+  if (done[dev][variant].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return false;
+  done[dev][variant].store(true, std::memory_order_release);
+  return true;
+}
+
+// [page][head][slot][dim] as a 4-D map; a box is one head's page.
+bool px_map(CUtensorMap *map, const void *pool, const kvq_block_cache &c) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t D = c.head_dim, P = c.page_size, H = c.num_kv_heads, NP = c.num_pages;
+  const cuuint64_t dims[4] = {D, P, H, NP};
+  const cuuint64_t strides[3] = {D, P * D, H * P * D};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(P), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(pool), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
 
 }  // namespace kvq
 
@@ -146,7 +1089,9 @@ extern "C" size_t kvq_block_prefix_attn_workspace_size(int32_t n_tokens, int32_t
                                                        int32_t num_kv_heads, int32_t head_dim) {
   if (n_tokens < 0 || Hq <= 0 || num_kv_heads <= 0 || Hq % num_kv_heads) return 0;
   if (head_dim != 64 && head_dim != 128) return 0;
-  return 256;
+  int sms = 0;
+  if (device_sm_count(&sms) != KVQ_OK) return 0;
+  return px_rows_bytes(n_tokens, Hq, head_dim) + px_cut_bytes(sms, head_dim);
 }
 
 extern "C" kvq_status kvq_block_prefix_attn(
@@ -168,8 +1113,10 @@ extern "C" kvq_status kvq_block_prefix_attn(
   if (n_tokens == 0 || B == 0) return KVQ_OK;
   if (!seq_lens || !out || !workspace || !aligned16(out) || !rows_ok(q, q_stride, Hq, D)) return KVQ_ERR_INVALID_ARG;
   if (n_groups > 0 && (!group_start || !prefix_pages)) return KVQ_ERR_INVALID_ARG;
-  if (!aligned256(workspace) || workspace_bytes < kvq_block_prefix_attn_workspace_size(n_tokens, Hq, Hkv, D))
-    return KVQ_ERR_WORKSPACE;
+  int sms = 0;
+  if (device_sm_count(&sms) != KVQ_OK) return KVQ_ERR_CUDA;
+  const size_t rows_bytes = px_rows_bytes(n_tokens, Hq, D);
+  if (!aligned256(workspace) || workspace_bytes < rows_bytes + px_cut_bytes(sms, D)) return KVQ_ERR_WORKSPACE;
   PfArgs a;
   a.q = static_cast<const uint16_t *>(q);
   a.q_stride = q_stride;
@@ -178,8 +1125,8 @@ extern "C" kvq_status kvq_block_prefix_attn(
   a.group_start = group_start;
   a.prefix_pages = prefix_pages;
   a.abort_mask = abort_mask;
-  a.k_pool = static_cast<const uint8_t *>(cache->k_pool);
-  a.v_pool = static_cast<const uint8_t *>(cache->v_pool);
+  a.rows = static_cast<float *>(workspace);
+  a.cut = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + rows_bytes);
   a.scales = reinterpret_cast<const float2 *>(cache->scales);
   a.out = static_cast<uint16_t *>(out);
   a.err_word = err_word;
@@ -191,9 +1138,19 @@ extern "C" kvq_status kvq_block_prefix_attn(
   a.MP = MP;
   a.max_q = max_q;
   a.n_groups = n_groups;
-  a.q_scale = sm_scale * 1.4426950408889634f;
-  const dim3 grid(static_cast<unsigned>(B), static_cast<unsigned>((Hq + kPfWarps - 1) / kPfWarps));
-  const cudaError_t e = launch_dependent(D == 128 ? prefix_kernel<128> : prefix_kernel<64>, grid, 32 * kPfWarps, 0,
-                                         reinterpret_cast<cudaStream_t>(stream), a);
-  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  a.q_scale = sm_scale * kLog2e;
+  const PxFn fn = D == 128 ? prefix_kernel<128> : prefix_kernel<64>;
+  const size_t smem = D == 128 ? PxSmem<128>::bytes : PxSmem<64>::bytes;
+  if (!px_opt_in(fn, D == 128, smem)) return KVQ_ERR_CUDA;
+  CUtensorMap kmap, vmap;
+  if (!px_map(&kmap, cache->k_pool, *cache) || !px_map(&vmap, cache->v_pool, *cache)) return KVQ_ERR_CUDA;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (launch_dependent(fn, sms, kPxThreads, smem, cs, kmap, vmap, a) != cudaSuccess) return KVQ_ERR_CUDA;
+  // a warp a row and head, up to 64 CTAs a request
+  const int64_t most = (static_cast<int64_t>(std::min(max_q, n_tokens)) * Hq + kPxMergeWarps - 1) / kPxMergeWarps;
+  const dim3 grid(static_cast<unsigned>(B), static_cast<unsigned>(std::min<int64_t>(64, most)));
+  if (launch_dependent(D == 128 ? prefix_merge_kernel<128> : prefix_merge_kernel<64>, grid, 32 * kPxMergeWarps, 0, cs,
+                       a) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  return KVQ_OK;
 }
