@@ -14,6 +14,8 @@ namespace kvq {
 struct PfArgs {
   const uint16_t *q;
   int64_t q_stride;
+  uint8_t *qp;  // [n_tokens][Hq][2][D]: q's two pieces
+  float *qk;    // [n_tokens][Hq]: what undoes their scale, times |sm_scale| log2(e)
   Ragged rg;
   const int32_t *block_table, *group_start, *prefix_pages;
   const uint8_t *abort_mask;
@@ -56,7 +58,7 @@ __device__ __forceinline__ int2 pf_group_rows(const PfArgs &a, int g) {
   return make_int2(max(x, 0), min(y, a.rg.n_tokens));
 }
 
-__device__ __forceinline__ PfReq pf_request(const PfArgs &a, int b) {
+__device__ __noinline__ PfReq pf_request(const PfArgs &a, int b) {
   PfReq o;
   o.r = request_rows<true>(a.rg, b);
   o.group = pf_group(a, b);
@@ -88,12 +90,14 @@ constexpr int kPxRowCost = 3;       // a row of work's start and end, in tiles' 
 constexpr int kPxSegs = 8;          // segment descriptors in flight
 constexpr int kPxStats = 4;         // segments whose statistics are in flight
 constexpr int kPxScales = 8;        // tiles whose scales are in flight
-constexpr int kPxK = 4, kPxV = 3;   // tiles of K and of V in flight
+constexpr int kPxK = 4, kPxV = 4;   // tiles of K and of V in flight
 constexpr int kStat = 4;            // floats behind a row's sums
 // a row's fourth statistic: its sums lie here, in the parts of several CTAs, or it is written
 constexpr float kHere = 1.f, kCut = 2.f, kDone = 3.f;
-constexpr int kPxSoft = 8, kPxConv = 4, kPxEdge = 4;  // warps
-constexpr int kPxMma = kPxSoft + kPxConv + kPxEdge, kPxThreads = 32 * (kPxMma + 3);
+// warps: softmax (two groups of four), sides (V's conversion, q in, sums out); then MMAs, copies
+// of K, of V, scales
+constexpr int kPxSoft = 8, kPxSide = 4;
+constexpr int kPxMma = kPxSoft + kPxSide, kPxThreads = 32 * (kPxMma + 4);
 constexpr float kPxFar = 64.f;      // how far the denominator's reference may be off (fp32)
 
 // An item: the prefix of a group for all its rows, or a request's own tokens for its rows.
@@ -106,7 +110,7 @@ struct PxItem {
   bool own, pre, live;  // pre: own tokens behind a prefix
 };
 
-__device__ __forceinline__ PxItem px_item(const PfArgs &a, int i) {
+__device__ __noinline__ PxItem px_item(const PfArgs &a, int i) {
   PxItem o;
   o.live = false;
   if (i < a.n_groups) {
@@ -151,7 +155,7 @@ __device__ __forceinline__ int px_tiles(const PfArgs &a, const PxItem &it, int r
 }
 
 // Units of one kv head of an item.
-__device__ __forceinline__ int64_t px_units(const PfArgs &a, const PxItem &it) {
+__device__ __noinline__ int64_t px_units(const PfArgs &a, const PxItem &it) {
   if (!it.live) return 0;
   if (!it.own || it.nb == 1) return static_cast<int64_t>(it.nb) * (px_tiles(a, it, 0) + kPxRowCost);
   int64_t u = 0;
@@ -168,66 +172,74 @@ struct PxSeg {
   int own, pre;
 };
 
-// A producer's way through its CTA's run; every lane of the warp keeps the same.
+// A producer's way through its CTA's run [u0, u1); every lane of the warp keeps the same.  Where
+// it stands: tile or start unit `at` of the row of work (head, rb), which has `tiles`.
 struct PxWalk {
-  int64_t u, u1, in, per;
-  int i;
+  int64_t u, u0, u1, per;
+  int i, head, rb, tiles, at;
   PxItem it;
-  int64_t units;
-  bool fresh;
 };
 
+__device__ __noinline__ void px_start(const PfArgs &a, PxWalk &w, int64_t in) {
+  w.it = px_item(a, w.i);
+  const int64_t units = px_units(a, w.it);
+  w.head = static_cast<int>(in / units);  // row of work: head major
+  int64_t s = in - w.head * units;
+  w.rb = 0;
+  w.tiles = px_tiles(a, w.it, 0);
+  if (!w.it.own) {
+    w.rb = static_cast<int>(s / (w.tiles + kPxRowCost));
+    s -= static_cast<int64_t>(w.rb) * (w.tiles + kPxRowCost);
+  } else {
+    while (s >= w.tiles + kPxRowCost) {
+      s -= w.tiles + kPxRowCost;
+      w.tiles = px_tiles(a, w.it, ++w.rb);
+    }
+  }
+  w.at = static_cast<int>(s);
+}
+
 // The next segment; false: the run has ended.
-__device__ __forceinline__ bool px_next(const PfArgs &a, PxWalk &w, PxSeg &sg) {
+__device__ __noinline__ bool px_next(const PfArgs &a, PxWalk &w, PxSeg &sg) {
   while (w.u < w.u1) {
-    if (w.fresh) {
-      w.it = px_item(a, w.i);
-      w.units = px_units(a, w.it);
-      w.fresh = false;
-    }
-    if (w.in >= w.units * a.Hkv) {
-      ++w.i;
-      w.in = 0;
-      w.fresh = true;
-      continue;
-    }
-    const int head = static_cast<int>(w.in / w.units);  // row of work: head major
-    int64_t s = w.in - head * w.units;
-    int rb = 0, tiles;
-    if (!w.it.own) {
-      tiles = px_tiles(a, w.it, 0);
-      rb = static_cast<int>(s / (tiles + kPxRowCost));
-      s -= static_cast<int64_t>(rb) * (tiles + kPxRowCost);
-    } else {
-      for (;; ++rb) {
-        tiles = px_tiles(a, w.it, rb);
-        if (s < tiles + kPxRowCost) break;
-        s -= tiles + kPxRowCost;
-      }
+    if (w.head == a.Hkv) {
+      do {
+        if (++w.i >= a.n_groups + a.rg.B) return false;
+        w.it = px_item(a, w.i);
+      } while (!w.it.live);
+      w.head = w.rb = w.at = 0;
+      w.tiles = px_tiles(a, w.it, 0);
     }
     // units [0, kPxRowCost) of a row of work stand for its start; tile t is unit kPxRowCost + t
-    const int at = static_cast<int>(s);
-    const int span = static_cast<int>(min(static_cast<int64_t>(tiles + kPxRowCost - at), w.u1 - w.u));
-    const int t0 = max(0, at - kPxRowCost), take = at + span - kPxRowCost - t0;
-    const int64_t ut = w.u - at + kPxRowCost;  // its first tile
-    w.u += span;
-    w.in += span;
-    if (take <= 0) continue;
-    const int64_t c_lo = ut / w.per;
-    sg.parts = static_cast<int>((ut + tiles - 1) / w.per - c_lo) + 1;
+    const int span = static_cast<int>(min(static_cast<int64_t>(w.tiles + kPxRowCost - w.at), w.u1 - w.u));
+    const int t0 = max(0, w.at - kPxRowCost), take = w.at + span - kPxRowCost - t0;
+    const int64_t ut = w.u - w.at + kPxRowCost;  // its first tile
+    sg.parts = 1;
+    if (ut < w.u0 || ut + w.tiles > w.u0 + w.per)
+      sg.parts = static_cast<int>((ut + w.tiles - 1) / w.per - ut / w.per) + 1;
     sg.part = sg.parts == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (t0 == 0 ? 1 : 0);
     sg.b = w.it.b;
-    sg.head = head;
-    sg.rb = rb;
+    sg.head = w.head;
+    sg.rb = w.rb;
     sg.row0 = w.it.row0;
-    sg.rows = min(w.it.rows - rb * kPxRows, kPxRows);
+    sg.rows = min(w.it.rows - w.rb * kPxRows, kPxRows);
     sg.tok = w.it.first + t0 * kPxTok;
     sg.tiles = take;
-    sg.t_end = px_end(a, w.it, rb);
+    sg.t_end = px_end(a, w.it, w.rb);
     sg.lim0 = w.it.own ? w.it.p0 + 1 : 0;
     sg.own = w.it.own;
     sg.pre = w.it.pre;
-    return true;
+    w.u += span;
+    w.at += span;
+    if (w.at == w.tiles + kPxRowCost) {
+      w.at = 0;
+      if (++w.rb == w.it.nb) {
+        w.rb = 0;
+        ++w.head;
+      }
+      if (w.it.nb > 1) w.tiles = px_tiles(a, w.it, w.rb);
+    }
+    if (take > 0) return true;
   }
   return false;
 }
@@ -237,21 +249,29 @@ __device__ __forceinline__ bool px_next(const PfArgs &a, PxWalk &w, PxSeg &sg) {
 // ---------------------------------------------------------------------------
 
 struct PxCtl {
-  float4 end[kPxStats][2][kPxRows];   // [segment][group]: m of its sum, l, n, how far it has come
+  float4 sc[kPxScales][kPxTok / 16];  // of a tile's blocks: K scale; V scale's fraction times 2^7, exponent
+  float4 end[kPxStats][2][kPxRows];   // [segment][group]: m that its l stands on, l, n, -
+  float2 now[kPxRows];                // (m, n): a row's references
+  float qk[kPxStats][kPxRows];
+  unsigned long long nan_from[kPxStats][128];  // per dim: px_nan of a token with a NaN code that some row
+                                               // does not see, the first of the last segment that had one
+  int nan_seg[kPxStats];              // 1 + the last segment that had one
+  int come[kPxStats][2];              // [segment][group]: tiles of the segment up to the group's last
+  int bad[kPxScales];                 // first token of a page outside the pool, or INT_MAX
   PxSeg seg[kPxSegs];
   uint64_t kfull[kPxK], kempty[kPxK], vfull[kPxV], vempty[kPxV];
-  uint64_t scfull[kPxScales], segfull[kPxSegs], segempty[kPxSegs];
+  uint64_t scfull[kPxScales], scempty[kPxScales], segfull[kPxSegs], segempty[kPxSegs];
   uint64_t qfull[2], qfree[2], sfull[2], pfull[2], hfull[2], hempty[2];  // h: V in f16
-  uint64_t ref[2][4], stat[kPxStats], pvdone, odone, ofree, cv, drain;
-  float2 sc[kPxScales][kPxTok / 16];  // (K, V) scales of a tile's blocks
-  int bad[kPxScales];                 // first token of a page outside the pool, or INT_MAX
-  float qk[kPxStats][kPxRows];        // what undoes q's scale, times sm_scale log2(e)
-  float2 now[kPxRows];                // (m, n): a row's references
-  int nan_from[kPxStats][128];        // per dim: the first token with a NaN code that some row does not see
+  uint64_t stat[kPxStats], qready[kPxStats], pvdone, odone, ofree, drain;
   RunScan<kPxThreads> scan;
   uint32_t tmem;
   int fail;
 };
+
+// A later segment's is smaller than an earlier one's, so that nothing needs to be cleared.
+__device__ __forceinline__ unsigned long long px_nan(uint32_t seg, int tok) {
+  return (static_cast<unsigned long long>(~seg) << 32) | static_cast<uint32_t>(tok);
+}
 
 constexpr uint32_t kPxS = 0, kPxO = 256, kPxQ = 384;  // TMEM columns
 
@@ -259,21 +279,26 @@ template <int D>
 struct PxSmem {
   static constexpr int kTile = kPxTok * D;      // a tile of K or V
   static constexpr int kHalf = 2 * kTile;       // V in f16
-  static constexpr int kStage = 32 * 33 * 4;    // an edge warp's 32 rows and columns on their way out
-  static constexpr int k = 0, v = kPxK * kTile, h = v + kPxV * kTile, st = h + 2 * kHalf,
-                       ctl = st + kPxEdge * kStage;
+  static constexpr int k = 0, v = kPxK * kTile, h = v + kPxV * kTile, ctl = h + 2 * kHalf;
   static constexpr size_t bytes = ctl + sizeof(PxCtl) + 1024;
   static_assert(bytes <= 227 * 1024 && ctl % 16 == 0, "shared memory of a CTA");
 };
 
-__device__ __forceinline__ bool px_wait(PxCtl &ctl, uint64_t *bar, uint32_t parity, uint32_t *err_word) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (__all_sync(0xffffffffu, ok)) return true;
-  if (!ok && !*reinterpret_cast<volatile int *>(&ctl.fail)) {
+// A whole warp waits, bounded.  The wait itself is out of line, as the schedule's walk is: with both
+// inlined at each place the kernel was 173 KB of code for five roles at once, and instruction
+// fetches were its bound.
+__device__ __noinline__ bool px_wait_long(int *fail, uint64_t *bar, uint32_t parity, uint32_t *err_word) {
+  bool ok = false;
+  if (!*reinterpret_cast<volatile int *>(fail)) {
     ok = mbar_wait(bar, parity);
-    if (!ok && atomicExch(&ctl.fail, 1) == 0) report(err_word, KVQ_ERRBIT_TIMEOUT);
+    if (!ok && atomicExch(fail, 1) == 0) report(err_word, KVQ_ERRBIT_TIMEOUT);
   }
   return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ bool px_wait(PxCtl &ctl, uint64_t *bar, uint32_t parity, uint32_t *err_word) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return px_wait_long(&ctl.fail, bar, parity, err_word);
 }
 
 // Whether a phase is over, without waiting for it; the same for the whole warp.
@@ -321,6 +346,7 @@ __device__ __forceinline__ void px_mma16(uint32_t d, uint32_t a, uint64_t b, uin
       : "memory");
 }
 
+// 32 consecutive columns of this warp's lanes; the values are there after tc_ld_wait.
 __device__ __forceinline__ void tc_ld32(float (&v)[32], uint32_t addr) {
   uint32_t *r = reinterpret_cast<uint32_t *>(v);
   asm volatile(
@@ -331,56 +357,167 @@ __device__ __forceinline__ void tc_ld32(float (&v)[32], uint32_t addr) {
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Waits for this thread's loads; the values pass through it, so that no use moves ahead of it.
+__device__ __forceinline__ void tc_ld_wait(float (&v)[32]) {
+  uint32_t *r = reinterpret_cast<uint32_t *>(v);
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+        "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+        "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+      :: "memory");
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
 }
 
 __device__ __forceinline__ void tc_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
-// the kernel
+// q's pieces
 // ---------------------------------------------------------------------------
 
-// This lane's row of a segment's q into TMEM: two pieces of D / 4 columns.
+constexpr int kPxQThreads = 256;
+
+// Four dims a lane; each row scaled by 2^e, its largest value into [224, 448], and split into an
+// e4m3 and an e5m2 piece (tc_q_pieces).  Done once a call, since every CTA that works on a part of a
+// row's tokens needs them.
 template <int D>
-__device__ __forceinline__ void px_load_q(const PfArgs &a, const PxSeg &sg, uint32_t cols, float *qk, int r) {
-  const int row = sg.rb * kPxRows + r, i = row / a.G;
-  const uint4 *p = reinterpret_cast<const uint4 *>(a.q + (static_cast<int64_t>(sg.row0) + i) * a.q_stride +
-                                                   static_cast<int64_t>(sg.head * a.G + row - i * a.G) * D);
+__global__ void __launch_bounds__(kPxQThreads) prefix_q_kernel(PfArgs a) {
+  grid_dependency_wait();
+  allow_dependents();
+  const int64_t idx = (static_cast<int64_t>(blockIdx.x) * kPxQThreads + threadIdx.x) / (D / 4);  // (token, head)
+  const int part = threadIdx.x % (D / 4);
+  const bool has = idx < static_cast<int64_t>(a.rg.n_tokens) * a.Hq;
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  if (has) {
+    const int64_t t = idx / a.Hq, h = idx - t * a.Hq;
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(a.q + t * a.q_stride + h * D + 4 * part));
+    bf16x2_to_f32(w.x, x);
+    bf16x2_to_f32(w.y, x + 2);
+  }
   float mx = 0.f;
   bool odd = false;  // inf or NaN: the row's scores are NaN, as inf - inf would make them
 #pragma unroll
-  for (int c = 0; c < D / 8; ++c) {
-    float x[8];
-    unpack8(r < sg.rows ? __ldg(p + c) : make_uint4(0, 0, 0, 0), x);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      mx = fmaxf(mx, finite_abs(x[k]));
-      odd |= !(fabsf(x[k]) < INFINITY);
-    }
+  for (int k = 0; k < 4; ++k) {
+    mx = fmaxf(mx, finite_abs(x[k]));
+    odd |= !(fabsf(x[k]) < INFINITY);
   }
-  const int e = block_exponent(mx);  // the largest value into [224, 448]
+#pragma unroll
+  for (int o = 1; o < D / 4; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (!has) return;
+  const int e = block_exponent(mx);
   // a negative sm_scale's sign goes to q, so that a larger score is a larger product
   const float up = copysignf(pow2(-e), a.q_scale), nan = odd ? NAN : 0.f;
-#pragma unroll 1
-  for (int c = 0; c < D / 64; ++c) {  // 64 dims: 16 columns of each piece (the row lies in L1 now)
-    float q1[16], q2[16];
+  uint32_t c1 = 0, c2 = 0;
+  tc_q_pieces(x[0] * up + nan, x[1] * up + nan, 0, c1, c2);
+  tc_q_pieces(x[2] * up + nan, x[3] * up + nan, 16, c1, c2);
+  uint32_t *to = reinterpret_cast<uint32_t *>(a.qp + idx * (2 * D)) + part;
+  to[0] = c1;
+  to[D / 4] = c2;
+  if (part == 0) a.qk[idx] = fabsf(a.q_scale) * pow2(e);
+}
+
+// ---------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------
+
+// A segment's q into TMEM, a row a lane: D / 4 columns of each piece.
+template <int D>
+__device__ __forceinline__ void px_load_q(const PfArgs &a, const PxSeg &sg, uint32_t cols, float *qk, int r) {
+  const int row = sg.rb * kPxRows + r, i = row / a.G;
+  const int64_t at = (static_cast<int64_t>(sg.row0) + i) * a.Hq + sg.head * a.G + row - i * a.G;
+  const bool has = r < sg.rows;
+  const uint4 *p = reinterpret_cast<const uint4 *>(a.qp + (has ? at : 0) * (2 * D));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float x[8];
-      unpack8(r < sg.rows ? __ldg(p + 8 * c + j) : make_uint4(0, 0, 0, 0), x);
+  for (int c = 0; c < 2 * D / 64; ++c) {
+    float w[16];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t c1 = 0, c2 = 0;
-        tc_q_pieces(x[4 * k] * up + nan, x[4 * k + 1] * up + nan, 0, c1, c2);
-        tc_q_pieces(x[4 * k + 2] * up + nan, x[4 * k + 3] * up + nan, 16, c1, c2);
-        q1[2 * j + k] = __uint_as_float(c1);
-        q2[2 * j + k] = __uint_as_float(c2);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const uint4 x = has ? __ldcg(p + 4 * c + j) : make_uint4(0, 0, 0, 0);
+      w[4 * j] = __uint_as_float(x.x);
+      w[4 * j + 1] = __uint_as_float(x.y);
+      w[4 * j + 2] = __uint_as_float(x.z);
+      w[4 * j + 3] = __uint_as_float(x.w);
     }
-    tc_st16(cols + 16 * c, q1);
-    tc_st16(cols + D / 4 + 16 * c, q2);
+    tc_st16(cols + 16 * c, w);
   }
-  qk[r] = fabsf(a.q_scale) * pow2(e);
+  qk[r] = has ? __ldcg(a.qk + at) : 0.f;
+}
+
+// Chunk j (16 codes) of a row of a tile as the copy left it.
+template <int D>
+__device__ __forceinline__ const uint8_t *px_codes(const uint8_t *v, int row, int j) {
+  return D == 128 ? v + row * 128 + ((j ^ (row & 7)) * 16) : v + row * 64 + ((j ^ ((row >> 1) & 3)) * 16);
+}
+
+// The same in f16: 64 dims a row of 128 bytes.  The upper half's lanes store their second eight
+// first, so that the eight lanes of a store's phase meet eight groups of banks.
+template <int D>
+__device__ __forceinline__ void px_store_half(uint8_t *h, int row, int j, uint4 w) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    o[2 * q] = e4m3x2_to_f16x2(static_cast<uint16_t>(x[q] & 0xFFFFu));
+    o[2 * q + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(x[q] >> 16));
+  }
+  const uint4 y0 = make_uint4(o[0], o[1], o[2], o[3]), y1 = make_uint4(o[4], o[5], o[6], o[7]);
+  const int c = (2 * j) & 7;
+  const bool up = D == 128 && j >= 4;
+  uint8_t *to = h + (up ? 16384 : 0) + row * 128;
+  *reinterpret_cast<uint4 *>(to + (((c + up) ^ (row & 7)) * 16)) = up ? y1 : y0;
+  *reinterpret_cast<uint4 *>(to + (((c + 1 - up) ^ (row & 7)) * 16)) = up ? y0 : y1;
+}
+
+// One chunk of 32 tokens of a row's scores: the maxima of x and of x + log2 vs.
+__device__ __forceinline__ void px_max(const float (&x)[32], const float4 *sc, float qk, float &mx, float &mv) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float4 b = sc[h];
+    const float *y = x + 16 * h;
+    const float u0 = max3(y[0], y[1], y[2]), u1 = max3(y[3], y[4], y[5]), u2 = max3(y[6], y[7], y[8]);
+    const float u3 = max3(y[9], y[10], y[11]), u4 = max3(y[12], y[13], y[14]);
+    const float mt = max3(max3(u0, u1, u2), fmaxf(u3, y[15]), u4);
+    const float z = mt > -INFINITY ? mt * (qk * b.x) : -INFINITY;  // (0 times -inf is no maximum)
+    mx = fmaxf(mx, z);
+    mv = fmaxf(mv, z + b.z);
+  }
+}
+
+// Its weights: e = 2^(x - m) for the sum l, and e vs 2^(m - n) 2^7 in f16.
+template <bool kMasked>
+__device__ __forceinline__ void px_weights(const float (&x)[32], const float4 *sc, float qk, float m, float mn,
+                                           float2 &l, float (&p)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float4 b = sc[h];
+    const float f = qk * b.x, d = b.y * fast_exp2(fminf(mn + b.z, 112.f));
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      float2 y = make_float2(x[16 * h + j], x[16 * h + j + 1]);
+      y = __ffma2_rn(y, make_float2(f, f), make_float2(-m, -m));
+      if (kMasked) {  // (0 times -inf is no score)
+        if (x[16 * h + j] == -INFINITY) y.x = -INFINITY;
+        if (x[16 * h + j + 1] == -INFINITY) y.y = -INFINITY;
+      }
+      const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+      l = __fadd2_rn(l, e);
+      const float2 w = __fmul2_rn(e, make_float2(d, d));
+      p[8 * h + j / 2] = __uint_as_float(f32x2_to_f16x2(w.x, w.y));
+    }
+  }
+}
+
+__device__ __forceinline__ void px_mask(float (&x)[32], int see) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (j >= see) x[j] = -INFINITY;
 }
 
 template <int D>
@@ -399,33 +536,39 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     }
     for (int i = 0; i < kPxV; ++i) {
       mbar_init(&ctl.vfull[i], 1);
-      mbar_init(&ctl.vempty[i], kPxConv);
+      mbar_init(&ctl.vempty[i], kPxSide);
     }
-    for (int i = 0; i < kPxScales; ++i) mbar_init(&ctl.scfull[i], 1 + kPxTok / 16);
+    for (int i = 0; i < kPxScales; ++i) {
+      mbar_init(&ctl.scfull[i], 1);
+      mbar_init(&ctl.scempty[i], 1);
+    }
     for (int i = 0; i < kPxSegs; ++i) {
       mbar_init(&ctl.segfull[i], 1);
-      mbar_init(&ctl.segempty[i], kPxMma + 1);  // everybody but the producers
+      mbar_init(&ctl.segempty[i], kPxMma + 2);  // everybody but the copies
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.qfull[i], kPxEdge);
+      mbar_init(&ctl.qfull[i], kPxSide);
       mbar_init(&ctl.qfree[i], 1);
       mbar_init(&ctl.sfull[i], 1);
       mbar_init(&ctl.pfull[i], 4);
-      mbar_init(&ctl.hfull[i], kPxConv);
+      mbar_init(&ctl.hfull[i], kPxSide);
       mbar_init(&ctl.hempty[i], 1);
-      for (int q = 0; q < 4; ++q) mbar_init(&ctl.ref[i][q], 1);
     }
-    for (int i = 0; i < kPxStats; ++i) mbar_init(&ctl.stat[i], kPxSoft + kPxConv);
+    for (int i = 0; i < kPxStats; ++i) {
+      mbar_init(&ctl.stat[i], kPxSoft + kPxSide);
+      mbar_init(&ctl.qready[i], kPxSide);
+      ctl.nan_seg[i] = 0;
+    }
     mbar_init(&ctl.pvdone, 1);
     mbar_init(&ctl.odone, 1);
-    mbar_init(&ctl.ofree, kPxEdge);
-    mbar_init(&ctl.cv, kPxConv);
+    mbar_init(&ctl.ofree, kPxSide);
     mbar_init(&ctl.drain, 1);
     ctl.fail = 0;
     fence_barrier_init();
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
   }
+  for (int i = threadIdx.x; i < kPxStats * 128; i += kPxThreads) ctl.nan_from[0][i] = ~0ull;
   if (warp == kPxMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&ctl.tmem))
                  : "memory");
@@ -435,7 +578,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = ctl.tmem;
-  grid_dependency_wait();
+  // The kernel ahead (q's pieces) let this one start when everything before it was complete; only its
+  // own results are waited for, where they are read.
   bool order = true;
   for (int g = threadIdx.x; g < a.n_groups; g += kPxThreads) order &= pf_group_ok(a, g);
   order = __syncthreads_and(order);
@@ -452,7 +596,45 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   const int64_t u0 = blockIdx.x * run.per;
   const int64_t u1 = min(u0 + run.per, run.total);
 
-  if (warp > kPxMma) {
+  if (warp == kPxMma + 3) {
+    // --------------------------------------------- scales, four tiles at a time
+    uint32_t g = 0;
+    bool ok = true;
+    for (uint32_t k = 0; ok; ++k) {
+      const int ss = k % kPxSegs;
+      ok = px_wait(ctl, &ctl.segfull[ss], (k / kPxSegs) & 1, a.err_word);
+      if (!ok) break;
+      const PxSeg sg = ctl.seg[ss];
+      if (sg.b < 0) break;
+      const int32_t *bt = a.block_table + static_cast<int64_t>(sg.b) * a.MP;
+      for (int t0 = 0; ok && t0 < sg.tiles; t0 += 4) {
+        const int mine = t0 + (lane >> 3), tok = sg.tok + mine * kPxTok + 16 * (lane & 7);
+        const bool needed = mine < sg.tiles && tok < sg.t_end;
+        const int page = needed ? __ldg(bt + (tok >> a.p_shift)) : -1;
+        const bool good = page >= 0 && page < a.num_pages;
+        // tokens without a page are masked
+        const float2 x = good ? __ldg(a.scales + static_cast<int64_t>(page) * a.Hkv + sg.head) : make_float2(1.f, 1.f);
+        const float2 vs = split_scale(x.y);
+        const uint32_t bads = __ballot_sync(0xffffffffu, needed && !good);
+#pragma unroll 1
+        for (int j = 0; ok && j < 4 && t0 + j < sg.tiles; ++j, ++g) {
+          const int cs = g % kPxScales;
+          ok = px_wait(ctl, &ctl.scempty[cs], ((g / kPxScales) & 1) ^ 1, a.err_word);
+          if (!ok) break;
+          // the weights' operand: kPScale (2^7), so that the largest sit high in f16's range
+          if (lane >> 3 == j) ctl.sc[cs][lane & 7] = make_float4(x.x, vs.x * kPScale, vs.y, 0.f);
+          if (lane == 0) {
+            const uint32_t bad = bads >> (8 * j) & 0xFFu;
+            ctl.bad[cs] = bad ? sg.tok + (t0 + j) * kPxTok + 16 * (__ffs(bad) - 1) : INT_MAX;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.scfull[cs]);
+        }
+      }
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&ctl.segempty[ss]);
+    }
+  } else if (warp > kPxMma) {
     // ------------------------------------------------------- producers: K, then V
     const int is_v = warp - kPxMma - 1;
     const CUtensorMap *map = is_v ? &vmap : &kmap;
@@ -466,7 +648,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     const uint32_t page_bytes = static_cast<uint32_t>(D) << a.p_shift;
     uint32_t g = 0, nseg = 0, par = 1, slot = 0;
     bool ok = true;
-    PxWalk walk = {u0, u1, run.in, run.per, run.b, {}, 0, true};
+    PxWalk walk = {u0, u0, u1, run.per, run.b, 0, 0, 0, 0, {}};
+    if (u0 < u1) px_start(a, walk, run.in);
     PxSeg sg;
     while (ok && px_next(a, walk, sg)) {
       const int ss = nseg % kPxSegs;
@@ -503,25 +686,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                           sg.own ? once : again);
         }
         __syncwarp();
-        if (!is_v) {
-          const int cs = g % kPxScales, of = lane >> (a.p_shift - 4);  // the page of block `lane`
-          const int from = __shfl_sync(0xffffffffu, page, of & 31);
-          const bool has = goods >> (of & 31) & 1;
-          if (lane == 0) {
-            ctl.bad[cs] = needs == goods ? INT_MAX : tok + ((__ffs(needs ^ goods) - 1) << a.p_shift);
-            if (needs != goods) report(a.err_word, KVQ_ERRBIT_PAGE);
-            mbar_arrive(&ctl.scfull[cs]);
-          }
-          if (lane < kPxTok / 16) {
-            if (has) {
-              cp_async8(&ctl.sc[cs][lane], a.scales + static_cast<int64_t>(from) * a.Hkv + sg.head);
-              cp_async_arrive(&ctl.scfull[cs]);
-            } else {
-              ctl.sc[cs][lane] = make_float2(1.f, 1.f);  // masked tokens
-              mbar_arrive(&ctl.scfull[cs]);
-            }
-          }
-        }
+        if (!is_v && lane == 0 && needs != goods) report(a.err_word, KVQ_ERRBIT_PAGE);
         ++g;
         if (++slot == stages) {
           slot = 0;
@@ -540,7 +705,6 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     }
     if (*reinterpret_cast<volatile int *>(&ctl.fail) && lane == 0)
       for (uint32_t k = g > stages ? g - stages : 0; k < g; ++k) mbar_wait(&full[k % stages], (k / stages) & 1);
-    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == kPxMma) {
     // ------------------------------------------------------------- MMA issue
     // Scores run up to two tiles ahead of values, into the next segment too: S(t) takes the
@@ -612,13 +776,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
            px_wait(ctl, &ctl.hfull[buf], (pg >> 1) & 1, a.err_word) &&
            (pt > 0 || ps == 0 || px_wait(ctl, &ctl.ofree, (ps - 1) & 1, a.err_word));
       if (!ok) break;
+      if (lane == 0) mbar_arrive(&ctl.scempty[pg % kPxScales]);
       tc_after();
       const bool last = pt + 1 == psg.tiles;
       if (elect_one()) {
         const uint64_t vd = px_vdesc(h_a + buf * S::kHalf);
         const int steps = tokens(psg, pt) / 16;
         for (int k = 0; k < steps; ++k)  // 16 tokens: 8 columns of P, 16 rows of V
-          px_mma16(tmem + kPxO, tmem + kPxS + 128 * buf + 8 * k, vd + k * (16 * 128 >> 4), D, pt > 0 || k > 0);
+          px_mma16(tmem + kPxO, tmem + kPxS + 128 * buf + 32 * (k >> 1) + 8 * (k & 1), vd + k * (16 * 128 >> 4), D, pt > 0 || k > 0);
         tc_commit(&ctl.hempty[buf]);
         tc_commit(&ctl.pvdone);
       }
@@ -638,79 +803,93 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       if (elect_one()) tc_commit(&ctl.drain);
       mbar_wait(&ctl.drain, 0);
     }
-  } else if (warp >= kPxSoft + kPxConv) {
-    // ---------------------------------------------- edge: q in, sums out
+  } else if (warp >= kPxSoft) {
+    // ------------------------- sides: q in, V from e4m3 to f16, sums out
     const int quad = warp & 3, r = 32 * quad + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-    float *stage = reinterpret_cast<float *>(smem + S::st + quad * S::kStage);
-    auto load_q = [&](uint32_t k) -> bool {
-      const int ss = k % kPxSegs;
-      if (!px_wait(ctl, &ctl.segfull[ss], (k / kPxSegs) & 1, a.err_word)) return false;
-      const PxSeg sg = ctl.seg[ss];
-      if (sg.b < 0) return true;
+    constexpr int kC = D / 16, kR = 32 / kC;  // chunks of 16 codes a row of V; rows a pass
+    const int row0 = 32 * quad + lane / kC, chunk = lane % kC;  // this lane's rows, kR apart, and chunk
+    uint32_t g = 0, nq = 0;  // tiles, and segments whose q is in
+    bool ok = true, ended = false;
+    // The next segment's q; its descriptor is posted when the copies of the one before are issued.
+    auto load_q = [&]() -> bool {
+      const uint32_t k = nq;
+      if (!px_wait(ctl, &ctl.segfull[k % kPxSegs], (k / kPxSegs) & 1, a.err_word)) return false;
+      const PxSeg &sg = ctl.seg[k % kPxSegs];
+      ended = sg.b < 0;
+      if (ended) return true;
       if (k >= 2 && !px_wait(ctl, &ctl.qfree[k & 1], ((k >> 1) - 1) & 1, a.err_word)) return false;
       tc_after();
-      if (32 * quad < sg.rows) px_load_q<D>(a, sg, tmem + lanes + kPxQ + (k & 1) * (D / 2), ctl.qk[k % kPxStats], r);
-      tc_st_wait();
+      if (32 * quad < sg.rows) {
+        px_load_q<D>(a, sg, tmem + lanes + kPxQ + (k & 1) * (D / 2), ctl.qk[k % kPxStats], r);
+        tc_st_wait();
+      }
       tc_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.qfull[k & 1]);
+      if (lane == 0) {
+        mbar_arrive(&ctl.qfull[k & 1]);
+        mbar_arrive(&ctl.qready[k % kPxStats]);
+      }
+      ++nq;
       return true;
     };
-    bool ok = load_q(0);
-    for (uint32_t k = 0; ok; ++k) {
-      const PxSeg sg = ctl.seg[k % kPxSegs];
-      if (sg.b < 0) break;
-      ok = load_q(k + 1) && px_wait(ctl, &ctl.stat[k % kPxStats], (k / kPxStats) & 1, a.err_word) &&
-           px_wait(ctl, &ctl.odone, k & 1, a.err_word);
-      if (!ok) break;
+    // Segment k's sums: a row to the output, or with its statistics to where the merge finds it.
+    auto put = [&](uint32_t k) -> bool {
+      const int ks = k % kPxStats;
+      if (!px_wait(ctl, &ctl.stat[ks], (k / kPxStats) & 1, a.err_word) ||
+          !px_wait(ctl, &ctl.odone, k & 1, a.err_word))
+        return false;
+      const PxSeg &sg = ctl.seg[k % kPxSegs];
       tc_after();
       if (32 * quad < sg.rows) {
         const int row = sg.rb * kPxRows + r, i = row / a.G;
-        const float4 e0 = ctl.end[k % kPxStats][0][r], e1 = ctl.end[k % kPxStats][1][r];
-        const float4 fin = e0.w > e1.w ? e0 : e1;  // the last references
-        const float M = fin.x, N = fin.z;
+        const int fin = ctl.come[ks][1] > ctl.come[ks][0];  // who had the last tile
+        const float4 e0 = ctl.end[ks][fin][r], e1 = ctl.end[ks][fin ^ 1][r];
+        const float M = e0.x, N = e0.z;
         const bool bad = e0.y < 0.f || e1.y < 0.f;
-        float l = e0.y == 0.f ? 0.f : e0.y * exp2f(e0.x - M);
-        l += e1.y == 0.f ? 0.f : e1.y * exp2f(e1.x - M);
+        float l = e0.y;
+        if (e1.y != 0.f) l += e1.y * exp2f(e1.x - M);
         if (bad) l = -1.f;
-        const int lim = sg.lim0 ? sg.lim0 + i : INT_MAX;
         const bool whole = sg.part < 0 && sg.own && !sg.pre;  // nothing to be merged with
-        const float2 f = whole ? out_scale(N - M - 7.f, l) : make_float2(1.f, 1.f);
         const int64_t at = (static_cast<int64_t>(sg.row0) + i) * a.Hq + sg.head * a.G + row - i * a.G;
-        const int64_t here = (static_cast<int64_t>(sg.own) * a.rg.n_tokens * a.Hq + at) * RF;
-        const int64_t there = (static_cast<int64_t>(sg.part) * kPxRows + r) * RF;
-        float *sums = sg.part < 0 ? a.rows : a.cut;
-        if (r < sg.rows) {
-          *reinterpret_cast<float4 *>(sums + (sg.part < 0 ? here : there) + D) =
-              make_float4(M, l, N, whole ? kDone : kHere);
+        float *here = a.rows + (static_cast<int64_t>(sg.own) * a.rg.n_tokens * a.Hq + at) * RF;
+        float *to = sg.part < 0 ? here : a.cut + (static_cast<int64_t>(sg.part) * kPxRows + r) * RF;
+        const bool has = r < sg.rows;
+        if (has) {
+          *reinterpret_cast<float4 *>(to + D) = make_float4(M, l, N, whole ? kDone : kHere);
           if (sg.part >= 0 && (sg.part & 1))  // the first part: where the others are
-            *reinterpret_cast<float4 *>(a.rows + here + D) =
+            *reinterpret_cast<float4 *>(here + D) =
                 make_float4(__int_as_float(sg.part >> 1), __int_as_float(sg.parts), 0.f, kCut);
         }
-        const int *nan_from = ctl.nan_from[k % kPxStats];
-        const int64_t base = whole ? at * D : sg.part < 0 ? here : there;
+        float2 f = make_float2(1.f, 1.f);
+        if (whole) f = bad ? make_float2(0.f, 0.f) : out_scale(N - M - 7.f, l);
+        const bool nan = ctl.nan_seg[ks] == static_cast<int>(k) + 1;
+        const int lim = sg.lim0 ? sg.lim0 + i : INT_MAX;
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
           tc_ld32(o, tmem + lanes + kPxO + c);
+          tc_ld_wait(o);
+          if (nan) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float y = whole ? o[j] * f.x * f.y : o[j];
-            if (nan_from[c + j] < lim) y = NAN;
-            if (whole && bad) y = 0.f;
-            stage[lane * 33 + j] = y;
+            for (int j = 0; j < 32; ++j)
+              if (ctl.nan_from[ks][c + j] < px_nan(k, lim)) o[j] = NAN;
           }
-          __syncwarp();
-          const int used = min(32, sg.rows - 32 * quad);
-          for (int rr = 0; rr < used; ++rr) {
-            const int64_t to = __shfl_sync(0xffffffffu, base, rr) + c + lane;
-            const float y = stage[rr * 33 + lane];
-            if (whole)
-              a.out[to] = static_cast<uint16_t>(pack_bf16x2(y, 0.f));
-            else
-              sums[to] = y;
+          if (!has) continue;
+          if (whole) {
+            uint4 w[4];
+            uint32_t *u = reinterpret_cast<uint32_t *>(w);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              u[j] = bad ? 0u : pack_bf16x2(o[2 * j] * f.x * f.y, o[2 * j + 1] * f.x * f.y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(a.out + at * D + c + 8 * j) = w[j];
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4 *>(to + c + 4 * j) =
+                  make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           }
-          __syncwarp();
         }
       }
       tc_before();
@@ -719,74 +898,55 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         mbar_arrive(&ctl.ofree);
         mbar_arrive(&ctl.segempty[k % kPxSegs]);
       }
-    }
-  } else if (warp >= kPxSoft) {
-    // ------------------------------------------------ V from e4m3 to f16
-    const int quad = warp & 3;
-    constexpr int kC = D / 16, kR = 32 / kC;  // chunks of 16 codes a row; rows a pass
-    uint32_t g = 0;
-    bool ok = true;
-    for (uint32_t k = 0; ok; ++k) {
-      const int ss = k % kPxSegs;
-      ok = px_wait(ctl, &ctl.segfull[ss], (k / kPxSegs) & 1, a.err_word);
-      if (!ok) break;
-      const PxSeg sg = ctl.seg[ss];
-      if (sg.b < 0) break;
-      int *nan_from = ctl.nan_from[k % kPxStats];
-      nan_from[32 * quad + lane] = INT_MAX;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.cv);
-      ok = px_wait(ctl, &ctl.cv, k & 1, a.err_word);
-      const int min_lim = sg.lim0 ? min(sg.t_end, sg.lim0 + sg.rb * kPxRows / a.G) : sg.t_end;
-      for (int t = 0; ok && t < sg.tiles; ++t, ++g) {
+      return true;
+    };
+    grid_dependency_wait();  // q's pieces
+    ok = load_q();
+    uint32_t k = 0;
+    for (; ok && !(ended && k == nq); ++k) {
+      const PxSeg &sg = ctl.seg[k % kPxSegs];
+      const int tiles = sg.tiles, t_end = sg.t_end;
+      const int min_lim = sg.lim0 ? min(t_end, sg.lim0 + sg.rb * kPxRows / a.G) : t_end;
+      for (int t = 0; t < tiles; ++t, ++g) {
         const int slot = g % kPxV, buf = g & 1, tok = sg.tok + t * kPxTok + 32 * quad;
         ok = px_wait(ctl, &ctl.vfull[slot], (g / kPxV) & 1, a.err_word) &&
              px_wait(ctl, &ctl.hempty[buf], ((g >> 1) & 1) ^ 1, a.err_word);
         if (!ok) break;
         const uint8_t *v = smem + S::v + slot * S::kTile;
         uint8_t *h = smem + S::h + buf * S::kHalf;
-        if (tok < sg.t_end) {
-          const bool partial = tok + 32 > min_lim;
+        if (tok + 32 <= min_lim) {
 #pragma unroll
+          for (int it = 0; it < kC; it += 4) {
+            uint4 w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              w[q] = *reinterpret_cast<const uint4 *>(px_codes<D>(v, row0 + kR * (it + q), chunk));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) px_store_half<D>(h, row0 + kR * (it + q), chunk, w[q]);
+          }
+        } else if (tok < t_end) {
+#pragma unroll 1
           for (int it = 0; it < kC; ++it) {
-            const int row = 32 * quad + kR * it + lane / kC, j = lane % kC;
-            uint4 w;
-            if constexpr (D == 128)
-              w = *reinterpret_cast<const uint4 *>(v + row * 128 + ((j ^ (row & 7)) * 16));
-            else
-              w = *reinterpret_cast<const uint4 *>(v + row * 64 + ((j ^ ((row >> 1) & 3)) * 16));
-            uint32_t x[4] = {w.x, w.y, w.z, w.w};
-            if (partial) {
-              const int tk = tok + kR * it + lane / kC;
-              if (tk >= sg.t_end) {
-                x[0] = x[1] = x[2] = x[3] = 0;  // cached bytes behind may be anything
-              } else if (tk >= min_lim) {
-                // a weight of 0 does not stop a NaN: it is put where its rows are written
+            const int row = row0 + kR * it, tk = tok + row - 32 * quad;
+            uint4 w = *reinterpret_cast<const uint4 *>(px_codes<D>(v, row, chunk));
+            uint32_t *x = reinterpret_cast<uint32_t *>(&w);
+            if (tk >= t_end) {
+              w = make_uint4(0, 0, 0, 0);  // cached bytes behind may be anything
+            } else if (tk >= min_lim) {
+              // a weight of 0 does not stop a NaN: it is put where its rows are written
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  uint32_t nan = nan_codes(x[q]);
-                  x[q] &= ~((nan >> 7) * 0xFFu);
-                  while (nan) {
-                    const int byte = (__ffs(nan) - 1) >> 3;
-                    nan &= nan - 1;
-                    atomicMin(&nan_from[16 * j + 4 * q + byte], tk);
-                  }
+              for (int q = 0; q < 4; ++q) {
+                uint32_t nan = nan_codes(x[q]);
+                x[q] &= ~((nan >> 7) * 0xFFu);
+                while (nan) {
+                  const int byte = (__ffs(nan) - 1) >> 3;
+                  nan &= nan - 1;
+                  atomicMin(&ctl.nan_from[k % kPxStats][16 * chunk + 4 * q + byte], px_nan(k, tk));
+                  ctl.nan_seg[k % kPxStats] = static_cast<int>(k) + 1;
                 }
               }
             }
-            uint4 y[2];
-            uint32_t *o = reinterpret_cast<uint32_t *>(y);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              o[2 * q] = e4m3x2_to_f16x2(static_cast<uint16_t>(x[q] & 0xFFFFu));
-              o[2 * q + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(x[q] >> 16));
-            }
-            // 64 dims a row; the upper half's lanes store their second chunk first, so that a
-            // phase's eight lanes meet eight groups of banks
-            const int c = (2 * j) & 7, sel = D == 128 ? j >> 2 : 0;
-            uint8_t *to = h + (D == 128 ? (j >> 2) * 16384 : 0) + row * 128;
-            *reinterpret_cast<uint4 *>(to + (((c + sel) ^ (row & 7)) * 16)) = sel ? y[1] : y[0];
-            *reinterpret_cast<uint4 *>(to + (((c + 1 - sel) ^ (row & 7)) * 16)) = sel ? y[0] : y[1];
+            px_store_half<D>(h, row, chunk, w);
           }
         }
         proxy_fence();
@@ -795,82 +955,91 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           mbar_arrive(&ctl.vempty[slot]);
           mbar_arrive(&ctl.hfull[buf]);
         }
+        if (t == 0 && k > 0) {  // the sums before, once this segment's first values are on their way
+          ok = put(k - 1);
+          if (!ok) break;
+        }
       }
       if (!ok) break;
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&ctl.stat[k % kPxStats]);
-        mbar_arrive(&ctl.segempty[ss]);
-      }
+      if (lane == 0) mbar_arrive(&ctl.stat[k % kPxStats]);
+      ok = load_q();
     }
+    if (ok && k > 0) put(k - 1);
   } else {
-    // ------------------------------------------------------------- softmax
+    // ------------------------------------------------------- softmax, a row a lane
     const int grp = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
     const uint32_t s_addr = tmem + lanes + kPxS + 128 * grp, o_addr = tmem + lanes + kPxO;
     uint32_t g = 0;  // tiles of the CTA so far
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
-      const int ss = k % kPxSegs;
+      const int ss = k % kPxSegs, ks = k % kPxStats;
       ok = px_wait(ctl, &ctl.segfull[ss], (k / kPxSegs) & 1, a.err_word);
       if (!ok) break;
-      const PxSeg sg = ctl.seg[ss];
+      const PxSeg &sg = ctl.seg[ss];
       if (sg.b < 0) break;
+      const int tiles = sg.tiles, t_end = sg.t_end, tok0 = sg.tok;
       const bool act = 32 * quad < sg.rows;
-      const int lim = sg.lim0 ? min(sg.t_end, sg.lim0 + (sg.rb * kPxRows + r) / a.G) : sg.t_end;
-      const int min_lim = sg.lim0 ? min(sg.t_end, sg.lim0 + sg.rb * kPxRows / a.G) : sg.t_end;
-      float m = -INFINITY, n = -INFINITY, l = 0.f, lm = -INFINITY;
+      const int lim = sg.lim0 ? min(t_end, sg.lim0 + (sg.rb * kPxRows + r) / a.G) : t_end;
+      const int min_lim = sg.lim0 ? min(t_end, sg.lim0 + sg.rb * kPxRows / a.G) : t_end;
+      float m = -INFINITY, n = -INFINITY, l = 0.f, lm = -INFINITY, qk = 0.f;
       int bad_from = INT_MAX, come = 0;
-      for (int t = 0; t < sg.tiles; ++t, ++g) {
-        if ((g & 1) != static_cast<uint32_t>(grp)) continue;
-        const int cs = g % kPxScales, tok = sg.tok + t * kPxTok;
-        ok = px_wait(ctl, &ctl.sfull[grp], (g >> 1) & 1, a.err_word) &&
-             px_wait(ctl, &ctl.scfull[cs], (g / kPxScales) & 1, a.err_word);
+      const int first = (g & 1) != static_cast<uint32_t>(grp);  // the group's first tile
+      if (first < tiles) {
+        ok = px_wait(ctl, &ctl.qready[ks], (k / kPxStats) & 1, a.err_word);
+        if (!ok) break;
+        qk = ctl.qk[ks][r];  // (of a row that exists)
+      }
+      for (int t = first; t < tiles; t += 2) {
+        const uint32_t gt = g + t;
+        const int cs = gt % kPxScales, tok = tok0 + t * kPxTok;
+        ok = px_wait(ctl, &ctl.sfull[grp], (gt >> 1) & 1, a.err_word) &&
+             px_wait(ctl, &ctl.scfull[cs], (gt / kPxScales) & 1, a.err_word);
         if (!ok) break;
         tc_after();
         come = t + 1;
-        const int chunks = (min(kPxTok, sg.t_end - tok) + 31) >> 5;
-        const bool partial = tok + kPxTok > min_lim;
-        const float qk = act ? ctl.qk[k % kPxStats][r] : 0.f;
-        float mx = -INFINITY, mv = -INFINITY;
+        const float4 *sc = ctl.sc[cs];
+        float mx = -INFINITY, mv = -INFINITY, xa[32], xb[32];
+        const bool full = tok + kPxTok <= min_lim;  // everybody sees all of it
+        const int chunks = (min(kPxTok, t_end - tok) + 31) >> 5;  // of 32 tokens
         if (act) {
           bad_from = min(bad_from, ctl.bad[cs]);
+          if (full) {
+            tc_ld32(xa, s_addr);
+            tc_ld_wait(xa);
+            tc_ld32(xb, s_addr + 32);
+            px_max(xa, sc, qk, mx, mv);
+            tc_ld_wait(xb);
+            tc_ld32(xa, s_addr + 64);
+            px_max(xb, sc + 2, qk, mx, mv);
+            tc_ld_wait(xa);
+            tc_ld32(xb, s_addr + 96);
+            px_max(xa, sc + 4, qk, mx, mv);
+            tc_ld_wait(xb);
+            px_max(xb, sc + 6, qk, mx, mv);
+          } else {
 #pragma unroll 1
-          for (int c = 0; c < chunks; ++c) {
-            float x[32];
-            tc_ld32(x, s_addr + 32 * c);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float2 sc = ctl.sc[cs][2 * c + h];
-              float mt = -INFINITY;
-              if (partial) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if (tok + 32 * c + 16 * h + j < lim) mt = fmaxf(mt, x[16 * h + j]);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) mt = fmaxf(mt, x[16 * h + j]);
-              }
-              if (mt > -INFINITY) {  // (0 times -inf is no maximum)
-                const float y = mt * (qk * sc.x);
-                mx = fmaxf(mx, y);
-                mv = fmaxf(mv, y + split_scale(sc.y).y);
-              }
+            for (int c = 0; c < chunks; ++c) {
+              tc_ld32(xa, s_addr + 32 * c);
+              tc_ld_wait(xa);
+              px_mask(xa, lim - tok - 32 * c);
+              px_max(xa, sc + 2 * c, qk, mx, mv);
             }
           }
         }
-        // the references, which the groups hand one another
-        if (g > 0) {
-          ok = px_wait(ctl, &ctl.ref[grp ^ 1][quad], ((g - 1) >> 1) & 1, a.err_word);
+        // the references, which the groups hand one another with their weights
+        if (gt > 0) {
+          ok = px_wait(ctl, &ctl.pfull[grp ^ 1], ((gt - 1) >> 1) & 1, a.err_word);
           if (!ok) break;
         }
-        float fo = 1.f;
         if (act) {
           if (t > 0) {
             const float2 now = ctl.now[r];
             m = now.x;
             n = now.y;
           }
+          float fo = 1.f;
           if (m == -INFINITY || mx > m + kPxFar) m = mx;
           if (n == -INFINITY) {
             n = mv;
@@ -879,16 +1048,42 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             n = mv;
           }
           ctl.now[r] = make_float2(m, n);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.ref[grp][quad]);
-        if (act) {
           if (lm != m) {
             l = l == 0.f ? 0.f : l * exp2f(lm - m);
             lm = m;
           }
+          const bool none = n == -INFINITY;  // nothing seen yet: every x is -inf
+          const float mm = none ? 0.f : m, mn = none ? 0.f : m - n;
+          float2 l2 = make_float2(0.f, 0.f);
+          float p[16];
+          if (full) {  // the last two chunks' scores are still here
+            px_weights<false>(xa, sc + 4, qk, mm, mn, l2, p);
+            tc_st16(s_addr + 64, p);  // in the chunk's own columns
+            tc_ld32(xa, s_addr);
+            px_weights<false>(xb, sc + 6, qk, mm, mn, l2, p);
+            tc_st16(s_addr + 96, p);
+            tc_ld_wait(xa);
+            tc_ld32(xb, s_addr + 32);
+            px_weights<false>(xa, sc, qk, mm, mn, l2, p);
+            tc_st16(s_addr, p);
+            tc_ld_wait(xb);
+            px_weights<false>(xb, sc + 2, qk, mm, mn, l2, p);
+            tc_st16(s_addr + 32, p);
+          } else {
+#pragma unroll 1
+            for (int c = chunks - 1; c >= 0; --c) {
+              if (c != chunks - 1) {
+                tc_ld32(xa, s_addr + 32 * c);
+                tc_ld_wait(xa);
+                px_mask(xa, lim - tok - 32 * c);
+              }
+              px_weights<true>(xa, sc + 2 * c, qk, mm, mn, l2, p);
+              tc_st16(s_addr + 32 * c, p);
+            }
+          }
+          l += l2.x + l2.y;
           if (t > 0 && __any_sync(0xffffffffu, fo != 1.f)) {
-            ok = px_wait(ctl, &ctl.pvdone, (g - 1) & 1, a.err_word);
+            ok = px_wait(ctl, &ctl.pvdone, (gt - 1) & 1, a.err_word);
             if (!ok) break;
             tc_after();
 #pragma unroll 1
@@ -900,38 +1095,6 @@ __global__ void __launch_bounds__(kPxThreads, 1)
               tc_st16(o_addr + c, o);
             }
           }
-          const bool none = n == -INFINITY;  // nothing seen yet: every x is -inf
-          const float mm = none ? 0.f : m, mn = none ? 0.f : m - n;
-          float2 l2 = make_float2(0.f, 0.f);
-#pragma unroll 1
-          for (int c = 0; c < chunks; ++c) {
-            float x[32], p[16];
-            tc_ld32(x, s_addr + 32 * c);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float2 sc = ctl.sc[cs][2 * c + h];
-              const float2 vs = split_scale(sc.y);
-              const float f = qk * sc.x;
-              // vs 2^(m - n), with kPScale (2^7) so that the largest weights sit high in f16's range
-              const float d = vs.x * kPScale * fast_exp2(fminf(mn + vs.y, 112.f));
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                float2 y = __ffma2_rn(make_float2(x[16 * h + j], x[16 * h + j + 1]), make_float2(f, f),
-                                      make_float2(-mm, -mm));
-                if (partial) {
-                  const int tk = tok + 32 * c + 16 * h + j;
-                  if (tk >= lim) y.x = -INFINITY;
-                  if (tk + 1 >= lim) y.y = -INFINITY;
-                }
-                const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                l2 = __fadd2_rn(l2, e);
-                const float2 w = __fmul2_rn(e, make_float2(d, d));
-                p[8 * h + j / 2] = __uint_as_float(f32x2_to_f16x2(w.x, w.y));
-              }
-            }
-            tc_st16(s_addr + 16 * c, p);
-          }
-          l += l2.x + l2.y;
           tc_st_wait();
         }
         tc_before();
@@ -939,10 +1102,12 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         if (lane == 0) mbar_arrive(&ctl.pfull[grp]);
       }
       if (!ok) break;
-      ctl.end[k % kPxStats][grp][r] = make_float4(lm, lim > bad_from ? -1.f : l, n, static_cast<float>(come));
+      g += tiles;
+      ctl.end[ks][grp][r] = make_float4(lm, lim > bad_from ? -1.f : l, n, 0.f);
+      if (quad == 0 && lane == 0) ctl.come[ks][grp] = come;
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&ctl.stat[k % kPxStats]);
+        mbar_arrive(&ctl.stat[ks]);
         mbar_arrive(&ctl.segempty[ss]);
       }
     }
@@ -1050,6 +1215,13 @@ size_t px_rows_bytes(int64_t n_tokens, int Hq, int D) {
 }
 size_t px_cut_bytes(int ctas, int D) { return px_up256(2ull * ctas * kPxRows * (D + kStat) * sizeof(float)); }
 
+size_t px_q_bytes(int64_t n_tokens, int Hq, int D) { return px_up256(2ull * n_tokens * Hq * D); }
+size_t px_qk_bytes(int64_t n_tokens, int Hq) { return px_up256(4ull * n_tokens * Hq); }
+size_t px_bytes(int64_t n_tokens, int Hq, int D, int ctas) {
+  return px_rows_bytes(n_tokens, Hq, D) + px_cut_bytes(ctas, D) + px_q_bytes(n_tokens, Hq, D) +
+         px_qk_bytes(n_tokens, Hq);
+}
+
 using PxFn = void (*)(CUtensorMap, CUtensorMap, PfArgs);
 
 // Opt the kernel into its shared memory, once per device.
@@ -1091,7 +1263,7 @@ extern "C" size_t kvq_block_prefix_attn_workspace_size(int32_t n_tokens, int32_t
   if (head_dim != 64 && head_dim != 128) return 0;
   int sms = 0;
   if (device_sm_count(&sms) != KVQ_OK) return 0;
-  return px_rows_bytes(n_tokens, Hq, head_dim) + px_cut_bytes(sms, head_dim);
+  return px_bytes(n_tokens, Hq, head_dim, sms);
 }
 
 extern "C" kvq_status kvq_block_prefix_attn(
@@ -1115,8 +1287,7 @@ extern "C" kvq_status kvq_block_prefix_attn(
   if (n_groups > 0 && (!group_start || !prefix_pages)) return KVQ_ERR_INVALID_ARG;
   int sms = 0;
   if (device_sm_count(&sms) != KVQ_OK) return KVQ_ERR_CUDA;
-  const size_t rows_bytes = px_rows_bytes(n_tokens, Hq, D);
-  if (!aligned256(workspace) || workspace_bytes < rows_bytes + px_cut_bytes(sms, D)) return KVQ_ERR_WORKSPACE;
+  if (!aligned256(workspace) || workspace_bytes < px_bytes(n_tokens, Hq, D, sms)) return KVQ_ERR_WORKSPACE;
   PfArgs a;
   a.q = static_cast<const uint16_t *>(q);
   a.q_stride = q_stride;
@@ -1125,8 +1296,13 @@ extern "C" kvq_status kvq_block_prefix_attn(
   a.group_start = group_start;
   a.prefix_pages = prefix_pages;
   a.abort_mask = abort_mask;
-  a.rows = static_cast<float *>(workspace);
-  a.cut = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + rows_bytes);
+  uint8_t *at = static_cast<uint8_t *>(workspace);
+  a.rows = reinterpret_cast<float *>(at);
+  at += px_rows_bytes(n_tokens, Hq, D);
+  a.cut = reinterpret_cast<float *>(at);
+  at += px_cut_bytes(sms, D);
+  a.qp = at;
+  a.qk = reinterpret_cast<float *>(at + px_q_bytes(n_tokens, Hq, D));
   a.scales = reinterpret_cast<const float2 *>(cache->scales);
   a.out = static_cast<uint16_t *>(out);
   a.err_word = err_word;
@@ -1145,6 +1321,10 @@ extern "C" kvq_status kvq_block_prefix_attn(
   CUtensorMap kmap, vmap;
   if (!px_map(&kmap, cache->k_pool, *cache) || !px_map(&vmap, cache->v_pool, *cache)) return KVQ_ERR_CUDA;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t q_ctas = (static_cast<int64_t>(n_tokens) * Hq * (D / 4) + kPxQThreads - 1) / kPxQThreads;
+  if (launch_dependent(D == 128 ? prefix_q_kernel<128> : prefix_q_kernel<64>, static_cast<unsigned>(q_ctas),
+                       kPxQThreads, 0, cs, a) != cudaSuccess)
+    return KVQ_ERR_CUDA;
   if (launch_dependent(fn, sms, kPxThreads, smem, cs, kmap, vmap, a) != cudaSuccess) return KVQ_ERR_CUDA;
   // a warp a row and head, up to 64 CTAs a request
   const int64_t most = (static_cast<int64_t>(std::min(max_q, n_tokens)) * Hq + kPxMergeWarps - 1) / kPxMergeWarps;
