@@ -870,11 +870,6 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           float o[32];
           tc_ld32(o, tmem + lanes + kPxO + c);
           tc_ld_wait(o);
-          if (nan) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (ctl.nan_from[ks][c + j] < px_nan(k, lim)) o[j] = NAN;
-          }
           if (!has) continue;
           if (whole) {
             uint4 w[4];
@@ -891,6 +886,15 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                   make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           }
         }
+        if (nan && has && !(whole && bad))
+#pragma unroll 1
+          for (int c = 0; c < D; ++c)
+            if (ctl.nan_from[ks][c] < px_nan(k, lim)) {
+              if (whole)
+                a.out[at * D + c] = 0x7FFF;
+              else
+                to[c] = NAN;
+            }
       }
       tc_before();
       __syncwarp();
@@ -901,13 +905,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       return true;
     };
     grid_dependency_wait();  // q's pieces
-    ok = load_q();
-    uint32_t k = 0;
-    for (; ok && !(ended && k == nq); ++k) {
+    for (uint32_t k = 0; ok; ++k) {
+      ok = load_q();
+      if (!ok) break;
       const PxSeg &sg = ctl.seg[k % kPxSegs];
-      const int tiles = sg.tiles, t_end = sg.t_end;
+      const int tiles = ended ? 0 : sg.tiles, t_end = sg.t_end;
       const int min_lim = sg.lim0 ? min(t_end, sg.lim0 + sg.rb * kPxRows / a.G) : t_end;
-      for (int t = 0; t < tiles; ++t, ++g) {
+      for (int t = 0; t < max(tiles, 1); ++t) {
+        if (t < tiles) {
         const int slot = g % kPxV, buf = g & 1, tok = sg.tok + t * kPxTok + 32 * quad;
         ok = px_wait(ctl, &ctl.vfull[slot], (g / kPxV) & 1, a.err_word) &&
              px_wait(ctl, &ctl.hempty[buf], ((g >> 1) & 1) ^ 1, a.err_word);
@@ -915,7 +920,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const uint8_t *v = smem + S::v + slot * S::kTile;
         uint8_t *h = smem + S::h + buf * S::kHalf;
         if (tok + 32 <= min_lim) {
-#pragma unroll
+#pragma unroll 1
           for (int it = 0; it < kC; it += 4) {
             uint4 w[4];
 #pragma unroll
@@ -955,17 +960,17 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           mbar_arrive(&ctl.vempty[slot]);
           mbar_arrive(&ctl.hfull[buf]);
         }
+        ++g;
+        }
         if (t == 0 && k > 0) {  // the sums before, once this segment's first values are on their way
           ok = put(k - 1);
           if (!ok) break;
         }
       }
-      if (!ok) break;
+      if (!ok || ended) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.stat[k % kPxStats]);
-      ok = load_q();
     }
-    if (ok && k > 0) put(k - 1);
   } else {
     // ------------------------------------------------------- softmax, a row a lane
     const int grp = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
@@ -1000,31 +1005,27 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         tc_after();
         come = t + 1;
         const float4 *sc = ctl.sc[cs];
-        float mx = -INFINITY, mv = -INFINITY, xa[32], xb[32];
+        float mx = -INFINITY, mv = -INFINITY, x[32];
         const bool full = tok + kPxTok <= min_lim;  // everybody sees all of it
         const int chunks = (min(kPxTok, t_end - tok) + 31) >> 5;  // of 32 tokens
         if (act) {
           bad_from = min(bad_from, ctl.bad[cs]);
+          // (rolled loops: with the chunks laid out one after another the roles' code did not fit the
+          // instruction caches, and its fetching took twice the time of the work)
           if (full) {
-            tc_ld32(xa, s_addr);
-            tc_ld_wait(xa);
-            tc_ld32(xb, s_addr + 32);
-            px_max(xa, sc, qk, mx, mv);
-            tc_ld_wait(xb);
-            tc_ld32(xa, s_addr + 64);
-            px_max(xb, sc + 2, qk, mx, mv);
-            tc_ld_wait(xa);
-            tc_ld32(xb, s_addr + 96);
-            px_max(xa, sc + 4, qk, mx, mv);
-            tc_ld_wait(xb);
-            px_max(xb, sc + 6, qk, mx, mv);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              tc_ld32(x, s_addr + 32 * c);
+              tc_ld_wait(x);
+              px_max(x, sc + 2 * c, qk, mx, mv);
+            }
           } else {
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
-              tc_ld32(xa, s_addr + 32 * c);
-              tc_ld_wait(xa);
-              px_mask(xa, lim - tok - 32 * c);
-              px_max(xa, sc + 2 * c, qk, mx, mv);
+              tc_ld32(x, s_addr + 32 * c);
+              tc_ld_wait(x);
+              px_mask(x, lim - tok - 32 * c);
+              px_max(x, sc + 2 * c, qk, mx, mv);
             }
           }
         }
@@ -1056,28 +1057,21 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           const float mm = none ? 0.f : m, mn = none ? 0.f : m - n;
           float2 l2 = make_float2(0.f, 0.f);
           float p[16];
-          if (full) {  // the last two chunks' scores are still here
-            px_weights<false>(xa, sc + 4, qk, mm, mn, l2, p);
-            tc_st16(s_addr + 64, p);  // in the chunk's own columns
-            tc_ld32(xa, s_addr);
-            px_weights<false>(xb, sc + 6, qk, mm, mn, l2, p);
-            tc_st16(s_addr + 96, p);
-            tc_ld_wait(xa);
-            tc_ld32(xb, s_addr + 32);
-            px_weights<false>(xa, sc, qk, mm, mn, l2, p);
-            tc_st16(s_addr, p);
-            tc_ld_wait(xb);
-            px_weights<false>(xb, sc + 2, qk, mm, mn, l2, p);
-            tc_st16(s_addr + 32, p);
+          if (full) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              tc_ld32(x, s_addr + 32 * c);
+              tc_ld_wait(x);
+              px_weights<false>(x, sc + 2 * c, qk, mm, mn, l2, p);
+              tc_st16(s_addr + 32 * c, p);  // in the chunk's own columns
+            }
           } else {
 #pragma unroll 1
-            for (int c = chunks - 1; c >= 0; --c) {
-              if (c != chunks - 1) {
-                tc_ld32(xa, s_addr + 32 * c);
-                tc_ld_wait(xa);
-                px_mask(xa, lim - tok - 32 * c);
-              }
-              px_weights<true>(xa, sc + 2 * c, qk, mm, mn, l2, p);
+            for (int c = 0; c < chunks; ++c) {
+              tc_ld32(x, s_addr + 32 * c);
+              tc_ld_wait(x);
+              px_mask(x, lim - tok - 32 * c);
+              px_weights<true>(x, sc + 2 * c, qk, mm, mn, l2, p);
               tc_st16(s_addr + 32 * c, p);
             }
           }
