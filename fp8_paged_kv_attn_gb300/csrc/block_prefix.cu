@@ -14,8 +14,11 @@ namespace kvq {
 struct PfArgs {
   const uint16_t *q;
   int64_t q_stride;
-  uint8_t *qp;  // [n_tokens][Hq][2][D]: q's two pieces
-  float *qk;    // [n_tokens][Hq]: what undoes their scale, times |sm_scale| log2(e)
+  uint8_t *qp;    // [n_tokens][Hq][2][D]: q's two pieces
+  float *qk;      // [n_tokens][Hq]: what undoes their scale, times |sm_scale| log2(e)
+  struct PxPlan *plan;
+  struct PxItem *items;  // [2 n_tokens]: groups' prefixes, then requests
+  int64_t *units;        // [2 n_tokens + 1]: units before each item
   Ragged rg;
   const int32_t *block_table, *group_start, *prefix_pages;
   const uint8_t *abort_mask;
@@ -58,7 +61,7 @@ __device__ __forceinline__ int2 pf_group_rows(const PfArgs &a, int g) {
   return make_int2(max(x, 0), min(y, a.rg.n_tokens));
 }
 
-__device__ __noinline__ PfReq pf_request(const PfArgs &a, int b) {
+__device__ __forceinline__ PfReq pf_request(const PfArgs &a, int b) {
   PfReq o;
   o.r = request_rows<true>(a.rg, b);
   o.group = pf_group(a, b);
@@ -94,57 +97,29 @@ constexpr int kPxK = 4, kPxV = 4;   // tiles of K and of V in flight
 constexpr int kStat = 4;            // floats behind a row's sums
 // a row's fourth statistic: its sums lie here, in the parts of several CTAs, or it is written
 constexpr float kHere = 1.f, kCut = 2.f, kDone = 3.f;
-// warps: softmax (two groups of four), sides (V's conversion, q in, sums out); then MMAs, copies
-// of K, of V, scales
-constexpr int kPxSoft = 8, kPxSide = 4;
-constexpr int kPxMma = kPxSoft + kPxSide, kPxThreads = 32 * (kPxMma + 4);
+// warps: softmax (two groups of four), V's conversion, q in, sums out; then MMAs, copies of K, of V,
+// scales
+constexpr int kPxSoft = 8, kPxConv = 4, kPxQ4 = 4, kPxPut = 4;
+constexpr int kPxMma = kPxSoft + kPxConv + kPxQ4 + kPxPut, kPxThreads = 32 * (kPxMma + 4);
 constexpr float kPxFar = 64.f;      // how far the denominator's reference may be off (fp32)
 
 // An item: the prefix of a group for all its rows, or a request's own tokens for its rows.
-struct PxItem {
+struct __align__(16) PxItem {
   int b;           // whose block table
   int row0, n;     // token rows
+  int rows;        // rows: token rows times heads a kv head
   int first, end;  // tokens [first, end)
   int p0;          // position of its first row (own tokens)
-  int rows, nb;    // rows (token rows times heads a kv head), blocks of them
-  bool own, pre, live;  // pre: own tokens behind a prefix
+  int nb;          // blocks of rows
+  int own, pre;    // pre: own tokens behind a prefix
+  int live;        // 0: a request whose rows are zeros
+  int row_pre;     // the first row of its group
 };
 
-__device__ __noinline__ PxItem px_item(const PfArgs &a, int i) {
-  PxItem o;
-  o.live = false;
-  if (i < a.n_groups) {
-    const int s = __ldg(a.group_start + i), e = __ldg(a.group_start + i + 1);
-    const int pages = __ldg(a.prefix_pages + i);
-    if (s >= e || pages <= 0 || pages > a.MP) return o;
-    const int2 r = pf_group_rows(a, i);
-    o.row0 = r.x;
-    o.n = r.y - r.x;
-    for (o.b = s; o.n > 0 && o.b < e; ++o.b)
-      if (pf_request(a, o.b).live) {
-        o.live = true;
-        break;
-      }
-    o.first = 0;
-    o.end = pages << a.p_shift;
-    o.own = o.pre = false;
-    o.p0 = 0;
-  } else {
-    o.b = i - a.n_groups;
-    const PfReq q = pf_request(a, o.b);
-    o.live = q.live;
-    o.row0 = q.r.row;
-    o.n = q.r.n;
-    o.p0 = q.r.p0;
-    o.first = q.pre;
-    o.end = q.r.p0 + q.r.n;
-    o.own = true;
-    o.pre = q.pre > 0;
-  }
-  o.rows = o.n * a.G;
-  o.nb = (o.rows + kPxRows - 1) / kPxRows;
-  return o;
-}
+struct PxPlan {
+  int64_t total, per;  // units, and units a CTA
+  int n_grp, n_req;    // items
+};
 
 // Where the tokens end that block rb of an item sees.
 __device__ __forceinline__ int px_end(const PfArgs &a, const PxItem &it, int rb) {
@@ -155,12 +130,18 @@ __device__ __forceinline__ int px_tiles(const PfArgs &a, const PxItem &it, int r
 }
 
 // Units of one kv head of an item.
-__device__ __noinline__ int64_t px_units(const PfArgs &a, const PxItem &it) {
+__device__ __forceinline__ int64_t px_units(const PfArgs &a, const PxItem &it) {
   if (!it.live) return 0;
   if (!it.own || it.nb == 1) return static_cast<int64_t>(it.nb) * (px_tiles(a, it, 0) + kPxRowCost);
   int64_t u = 0;
   for (int rb = 0; rb < it.nb; ++rb) u += px_tiles(a, it, rb) + kPxRowCost;
   return u;
+}
+
+// 64-bit division of numbers that are usually small.
+__device__ __forceinline__ int64_t px_div(int64_t x, int64_t y) {
+  if (((x | y) >> 31) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
 }
 
 struct PxSeg {
@@ -176,19 +157,29 @@ struct PxSeg {
 // it stands: tile or start unit `at` of the row of work (head, rb), which has `tiles`.
 struct PxWalk {
   int64_t u, u0, u1, per;
-  int i, head, rb, tiles, at;
+  int i, n, head, rb, tiles, at;
   PxItem it;
 };
 
-__device__ __noinline__ void px_start(const PfArgs &a, PxWalk &w, int64_t in) {
-  w.it = px_item(a, w.i);
+__device__ __forceinline__ PxItem px_load_item(const PfArgs &a, int i) {
+  PxItem o;
+  const int4 *p = reinterpret_cast<const int4 *>(a.items + i);
+  int4 *q = reinterpret_cast<int4 *>(&o);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) q[k] = __ldcg(p + k);
+  return o;
+}
+
+// in: the unit of item w.i that the run begins with.
+__device__ __forceinline__ void px_start(const PfArgs &a, PxWalk &w, int64_t in) {
+  w.it = px_load_item(a, w.i);
   const int64_t units = px_units(a, w.it);
-  w.head = static_cast<int>(in / units);  // row of work: head major
+  w.head = static_cast<int>(px_div(in, units));  // row of work: head major
   int64_t s = in - w.head * units;
   w.rb = 0;
   w.tiles = px_tiles(a, w.it, 0);
   if (!w.it.own) {
-    w.rb = static_cast<int>(s / (w.tiles + kPxRowCost));
+    w.rb = static_cast<int>(px_div(s, w.tiles + kPxRowCost));
     s -= static_cast<int64_t>(w.rb) * (w.tiles + kPxRowCost);
   } else {
     while (s >= w.tiles + kPxRowCost) {
@@ -199,13 +190,13 @@ __device__ __noinline__ void px_start(const PfArgs &a, PxWalk &w, int64_t in) {
   w.at = static_cast<int>(s);
 }
 
-// The next segment; false: the run has ended.
+// The next segment; false: the run has ended.  Out of line: two roles call it.
 __device__ __noinline__ bool px_next(const PfArgs &a, PxWalk &w, PxSeg &sg) {
   while (w.u < w.u1) {
     if (w.head == a.Hkv) {
       do {
-        if (++w.i >= a.n_groups + a.rg.B) return false;
-        w.it = px_item(a, w.i);
+        if (++w.i >= w.n) return false;
+        w.it = px_load_item(a, w.i);
       } while (!w.it.live);
       w.head = w.rb = w.at = 0;
       w.tiles = px_tiles(a, w.it, 0);
@@ -216,7 +207,7 @@ __device__ __noinline__ bool px_next(const PfArgs &a, PxWalk &w, PxSeg &sg) {
     const int64_t ut = w.u - w.at + kPxRowCost;  // its first tile
     sg.parts = 1;
     if (ut < w.u0 || ut + w.tiles > w.u0 + w.per)
-      sg.parts = static_cast<int>((ut + w.tiles - 1) / w.per - ut / w.per) + 1;
+      sg.parts = static_cast<int>(px_div(ut + w.tiles - 1, w.per) - px_div(ut, w.per)) + 1;
     sg.part = sg.parts == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (t0 == 0 ? 1 : 0);
     sg.b = w.it.b;
     sg.head = w.head;
@@ -248,6 +239,31 @@ __device__ __noinline__ bool px_next(const PfArgs &a, PxWalk &w, PxSeg &sg) {
 // shared memory and tcgen05
 // ---------------------------------------------------------------------------
 
+// Barriers, those that expect as many arrivals together: 1, 4, 12, 22.
+enum : int {
+  kKFull = 0,
+  kKEmpty = kKFull + kPxK,
+  kVFull = kKEmpty + kPxK,
+  kScFull = kVFull + kPxV,
+  kScEmpty = kScFull + kPxScales,
+  kSegFull = kScEmpty + kPxScales,
+  kQFree = kSegFull + kPxSegs,
+  kSFull = kQFree + 2,
+  kHEmpty = kSFull + 2,
+  kPvDone = kHEmpty + 2,
+  kODone,
+  kDrain,
+  kVEmpty,  // four warps each from here
+  kQFull = kVEmpty + kPxV,
+  kQReady = kQFull + 2,
+  kPFull = kQReady + kPxStats,
+  kHFull = kPFull + 2,
+  kOFree = kHFull + 2,
+  kStatFull,  // softmax and conversion
+  kSegEmpty = kStatFull + kPxStats,  // everybody but the copies
+  kBars = kSegEmpty + kPxSegs
+};
+
 struct PxCtl {
   float4 sc[kPxScales][kPxTok / 16];  // of a tile's blocks: K scale; V scale's fraction times 2^7, exponent
   float4 end[kPxStats][2][kPxRows];   // [segment][group]: m that its l stands on, l, n, -
@@ -255,15 +271,13 @@ struct PxCtl {
   float qk[kPxStats][kPxRows];
   unsigned long long nan_from[kPxStats][128];  // per dim: px_nan of a token with a NaN code that some row
                                                // does not see, the first of the last segment that had one
+  uint64_t bar[kBars];
+  int64_t run_in;                     // where the CTA's run begins: unit of item run_i
+  int run_i;
   int nan_seg[kPxStats];              // 1 + the last segment that had one
   int come[kPxStats][2];              // [segment][group]: tiles of the segment up to the group's last
   int bad[kPxScales];                 // first token of a page outside the pool, or INT_MAX
   PxSeg seg[kPxSegs];
-  uint64_t kfull[kPxK], kempty[kPxK], vfull[kPxV], vempty[kPxV];
-  uint64_t scfull[kPxScales], scempty[kPxScales], segfull[kPxSegs], segempty[kPxSegs];
-  uint64_t qfull[2], qfree[2], sfull[2], pfull[2], hfull[2], hempty[2];  // h: V in f16
-  uint64_t stat[kPxStats], qready[kPxStats], pvdone, odone, ofree, drain;
-  RunScan<kPxThreads> scan;
   uint32_t tmem;
   int fail;
 };
@@ -284,31 +298,49 @@ struct PxSmem {
   static_assert(bytes <= 227 * 1024 && ctl % 16 == 0, "shared memory of a CTA");
 };
 
-// A whole warp waits, bounded.  The wait itself is out of line, as the schedule's walk is: with both
-// inlined at each place the kernel was 173 KB of code for five roles at once, and instruction
-// fetches were its bound.
-__device__ __noinline__ bool px_wait_long(int *fail, uint64_t *bar, uint32_t parity, uint32_t *err_word) {
+// Barriers by their shared-memory address.
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void bar_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// A whole warp waits, bounded.  The wait itself is out of line: inlined at each place, with the schedule's
+// walk, the kernel was 173 KB of code for five roles at once, and instruction fetches were its bound.
+__device__ __noinline__ bool px_wait_long(int *fail, uint32_t bar, uint32_t parity, uint32_t *err_word) {
   bool ok = false;
   if (!*reinterpret_cast<volatile int *>(fail)) {
-    ok = mbar_wait(bar, parity);
+    const long long t0 = clock64();
+    for (uint32_t i = 0; i < kWaitPolls; ++i) {
+      ok = bar_try(bar, parity);
+      if (ok || clock64() - t0 > kWaitCycles) break;
+    }
     if (!ok && atomicExch(fail, 1) == 0) report(err_word, KVQ_ERRBIT_TIMEOUT);
   }
   return __all_sync(0xffffffffu, ok);
 }
 
-__device__ __forceinline__ bool px_wait(PxCtl &ctl, uint64_t *bar, uint32_t parity, uint32_t *err_word) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return px_wait_long(&ctl.fail, bar, parity, err_word);
-}
-
 // Whether a phase is over, without waiting for it; the same for the whole warp.
-__device__ __forceinline__ bool px_test(uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ bool px_test(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
+      : "r"(bar), "r"(parity)
       : "memory");
   return __all_sync(0xffffffffu, done != 0);
 }
@@ -382,16 +414,122 @@ __device__ __forceinline__ void tc_st_wait() { asm volatile("tcgen05.wait::st.sy
 // q's pieces
 // ---------------------------------------------------------------------------
 
-constexpr int kPxQThreads = 256;
+constexpr int kPxQThreads = 1024;
 
-// Four dims a lane; each row scaled by 2^e, its largest value into [224, 448], and split into an
-// e4m3 and an e5m2 piece (tc_q_pieces).  Done once a call, since every CTA that works on a part of a
-// row's tokens needs them.
+// Exclusive scan of v over the CTA; *total = the sum.
+__device__ __forceinline__ int64_t px_scan(int64_t v, int64_t *warps, int64_t *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  __syncthreads();  // the scratch may be read
+  if (lane == 31) warps[warp] = incl;
+  __syncthreads();
+  int64_t w = warps[lane], wi = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, wi, o);
+    if (lane >= o) wi += u;
+  }
+  *total = __shfl_sync(0xffffffffu, wi, 31);
+  return __shfl_sync(0xffffffffu, wi - w, warp) + incl - v;
+}
+
+// One CTA: the items with work, or with rows to be zeroed, and the units before each.  (Worked out by
+// every CTA of the next kernel for itself, as kvq_block_attn does, it took them 6.4 us: groups make a
+// request three dependent reads, and the code is long.)
+__device__ __forceinline__ void px_plan(const PfArgs &a, int ctas) {
+  __shared__ int64_t warps[32];
+  bool order = true;
+  for (int g = threadIdx.x; g < a.n_groups; g += kPxQThreads) order &= pf_group_ok(a, g);
+  order = __syncthreads_and(order);
+  if (!order && threadIdx.x == 0) report(a.err_word, KVQ_ERRBIT_REQ);
+  const int groups = order ? a.n_groups : 0, all = groups + a.rg.B;
+  const int64_t room = 2 * static_cast<int64_t>(a.rg.n_tokens);
+  int64_t units = 0, count = 0;
+  int n_grp = 0;
+  // groups in rounds of their own, so that the requests' items follow theirs
+  for (int i0 = 0; i0 < all; i0 += i0 < groups ? min(kPxQThreads, groups - i0) : kPxQThreads) {
+    const int i = i0 + threadIdx.x;
+    const bool grp = i0 < groups;
+    PxItem o = {};
+    bool has = false;
+    if (grp && i < groups) {
+      const int s = __ldg(a.group_start + i), e = __ldg(a.group_start + i + 1);
+      const int pages = __ldg(a.prefix_pages + i);
+      if (s < e && pages > 0 && pages <= a.MP) {
+        const int2 r = pf_group_rows(a, i);
+        o.row0 = r.x;
+        o.n = r.y - r.x;
+        o.end = pages << a.p_shift;
+        for (o.b = s; o.n > 0 && o.b < e; ++o.b)
+          if (pf_request(a, o.b).live) {
+            o.live = has = true;
+            break;
+          }
+      }
+    } else if (!grp && i < all) {
+      o.b = i - groups;
+      PfReq q;
+      if (order) {
+        q = pf_request(a, o.b);
+      } else {
+        q.r = request_rows<true>(a.rg, o.b);
+        q.pre = 0;
+        q.group = -1;
+        q.live = false;
+      }
+      if (q.r.err) report(a.err_word, q.r.err);
+      has = q.r.n > 0;
+      o.row0 = q.r.row;
+      o.n = q.r.n;
+      o.p0 = q.r.p0;
+      o.first = q.pre;
+      o.end = q.r.p0 + q.r.n;
+      o.own = 1;
+      o.pre = q.pre > 0;
+      o.live = q.live;
+      o.row_pre = q.live && q.pre > 0 ? pf_group_rows(a, q.group).x : 0;
+    }
+    o.rows = o.n * a.G;
+    o.nb = (o.rows + kPxRows - 1) / kPxRows;
+    const int64_t u = has ? px_units(a, o) * a.Hkv : 0;
+    int64_t n_all, u_all;
+    const int64_t at = count + px_scan(has, warps, &n_all);
+    const int64_t before = units + px_scan(u, warps, &u_all);
+    if (has && at < room) a.items[at] = o;
+    if (has && at <= room) a.units[at] = before;
+    if (has && at >= room) report(a.err_word, KVQ_ERRBIT_REQ);  // requests that own the same rows
+    count += n_all;
+    units += u_all;
+    if (grp) n_grp = static_cast<int>(min(count, room));
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const int64_t n = min(count, room), total = count > room ? a.units[room] : units;
+    a.units[n] = total;
+    a.plan->total = total;
+    a.plan->per = max(static_cast<int64_t>(1), px_div(total + ctas - 1, ctas));
+    a.plan->n_grp = n_grp;
+    a.plan->n_req = static_cast<int>(n) - n_grp;
+  }
+}
+
+// Block 0 makes the plan.  The others: four dims a lane; each row scaled by 2^e, its largest value into
+// [224, 448], and split into an e4m3 and an e5m2 piece (tc_q_pieces).  Done once a call, since every
+// CTA that works on a part of a row's tokens needs them.
 template <int D>
-__global__ void __launch_bounds__(kPxQThreads) prefix_q_kernel(PfArgs a) {
+__global__ void __launch_bounds__(kPxQThreads) prefix_plan_kernel(PfArgs a, int ctas) {
   grid_dependency_wait();
   allow_dependents();
-  const int64_t idx = (static_cast<int64_t>(blockIdx.x) * kPxQThreads + threadIdx.x) / (D / 4);  // (token, head)
+  if (blockIdx.x == 0) {
+    px_plan(a, ctas);
+    return;
+  }
+  const int64_t idx = (static_cast<int64_t>(blockIdx.x - 1) * kPxQThreads + threadIdx.x) / (D / 4);  // (token, head)
   const int part = threadIdx.x % (D / 4);
   const bool has = idx < static_cast<int64_t>(a.rg.n_tokens) * a.Hq;
   float x[4] = {0.f, 0.f, 0.f, 0.f};
@@ -529,42 +667,20 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   PxCtl &ctl = *reinterpret_cast<PxCtl *>(smem + S::ctl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kPxK; ++i) {
-      mbar_init(&ctl.kfull[i], 1);
-      mbar_init(&ctl.kempty[i], 1);
-    }
-    for (int i = 0; i < kPxV; ++i) {
-      mbar_init(&ctl.vfull[i], 1);
-      mbar_init(&ctl.vempty[i], kPxSide);
-    }
-    for (int i = 0; i < kPxScales; ++i) {
-      mbar_init(&ctl.scfull[i], 1);
-      mbar_init(&ctl.scempty[i], 1);
-    }
-    for (int i = 0; i < kPxSegs; ++i) {
-      mbar_init(&ctl.segfull[i], 1);
-      mbar_init(&ctl.segempty[i], kPxMma + 2);  // everybody but the copies
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.qfull[i], kPxSide);
-      mbar_init(&ctl.qfree[i], 1);
-      mbar_init(&ctl.sfull[i], 1);
-      mbar_init(&ctl.pfull[i], 4);
-      mbar_init(&ctl.hfull[i], kPxSide);
-      mbar_init(&ctl.hempty[i], 1);
-    }
-    for (int i = 0; i < kPxStats; ++i) {
-      mbar_init(&ctl.stat[i], kPxSoft + kPxSide);
-      mbar_init(&ctl.qready[i], kPxSide);
-      ctl.nan_seg[i] = 0;
-    }
-    mbar_init(&ctl.pvdone, 1);
-    mbar_init(&ctl.odone, 1);
-    mbar_init(&ctl.ofree, kPxSide);
-    mbar_init(&ctl.drain, 1);
-    ctl.fail = 0;
+  const uint32_t bars = smem_addr(ctl.bar);
+  auto bar = [&](int i) -> uint32_t { return bars + 8u * i; };
+  auto wait = [&](int i, uint32_t parity) -> bool {
+    if (__all_sync(0xffffffffu, bar_try(bars + 8u * i, parity))) return true;
+    return px_wait_long(&ctl.fail, bars + 8u * i, parity, a.err_word);
+  };
+  if (threadIdx.x < kBars) {
+    const int i = threadIdx.x;
+    mbar_init(&ctl.bar[i], i < kVEmpty ? 1 : i < kStatFull ? 4 : i < kSegEmpty ? kPxSoft + kPxConv : kPxMma + 2);
     fence_barrier_init();
+  }
+  if (threadIdx.x < kPxStats) ctl.nan_seg[threadIdx.x] = 0;
+  if (threadIdx.x == 0) {
+    ctl.fail = 0;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
   }
@@ -574,27 +690,23 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  grid_dependency_wait();  // the plan and q's pieces
+  allow_dependents();
+  const int64_t per = __ldcg(&a.plan->per), total = __ldcg(&a.plan->total);
+  const int n_items = __ldcg(&a.plan->n_grp) + __ldcg(&a.plan->n_req);
+  const int64_t u0 = blockIdx.x * per, u1 = min(u0 + per, total);
+  if (u0 < u1)
+    for (int i = threadIdx.x; i < n_items; i += kPxThreads) {
+      const int64_t lo = __ldcg(a.units + i), hi = __ldcg(a.units + i + 1);
+      if (lo <= u0 && u0 < hi) {
+        ctl.run_i = i;
+        ctl.run_in = u0 - lo;
+      }
+    }
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = ctl.tmem;
-  // The kernel ahead (q's pieces) let this one start when everything before it was complete; only its
-  // own results are waited for, where they are read.
-  bool order = true;
-  for (int g = threadIdx.x; g < a.n_groups; g += kPxThreads) order &= pf_group_ok(a, g);
-  order = __syncthreads_and(order);
-  if (!order && blockIdx.x == 0 && threadIdx.x == 0) report(a.err_word, KVQ_ERRBIT_REQ);
-  const RunStart run = find_run<kPxThreads>(
-      order ? a.n_groups + a.rg.B : 0, gridDim.x, blockIdx.x, ctl.scan, [&](int i) -> int64_t {
-        if (blockIdx.x == 0 && i >= a.n_groups) {
-          const uint32_t err = pf_request(a, i - a.n_groups).r.err;
-          if (err) report(a.err_word, err);
-        }
-        return px_units(a, px_item(a, i)) * a.Hkv;
-      });
-  allow_dependents();
-  const int64_t u0 = blockIdx.x * run.per;
-  const int64_t u1 = min(u0 + run.per, run.total);
 
   if (warp == kPxMma + 3) {
     // --------------------------------------------- scales, four tiles at a time
@@ -602,7 +714,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       const int ss = k % kPxSegs;
-      ok = px_wait(ctl, &ctl.segfull[ss], (k / kPxSegs) & 1, a.err_word);
+      ok = wait(kSegFull + ss, (k / kPxSegs) & 1);
       if (!ok) break;
       const PxSeg sg = ctl.seg[ss];
       if (sg.b < 0) break;
@@ -619,7 +731,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll 1
         for (int j = 0; ok && j < 4 && t0 + j < sg.tiles; ++j, ++g) {
           const int cs = g % kPxScales;
-          ok = px_wait(ctl, &ctl.scempty[cs], ((g / kPxScales) & 1) ^ 1, a.err_word);
+          ok = wait(kScEmpty + cs, ((g / kPxScales) & 1) ^ 1);
           if (!ok) break;
           // the weights' operand: kPScale (2^7), so that the largest sit high in f16's range
           if (lane >> 3 == j) ctl.sc[cs][lane & 7] = make_float4(x.x, vs.x * kPScale, vs.y, 0.f);
@@ -628,17 +740,17 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             ctl.bad[cs] = bad ? sg.tok + (t0 + j) * kPxTok + 16 * (__ffs(bad) - 1) : INT_MAX;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.scfull[cs]);
+          if (lane == 0) bar_arrive(bar(kScFull + cs));
         }
       }
       __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&ctl.segempty[ss]);
+      if (ok && lane == 0) bar_arrive(bar(kSegEmpty + ss));
     }
   } else if (warp > kPxMma) {
     // ------------------------------------------------------- producers: K, then V
     const int is_v = warp - kPxMma - 1;
     const CUtensorMap *map = is_v ? &vmap : &kmap;
-    uint64_t *full = is_v ? ctl.vfull : ctl.kfull, *empty = is_v ? ctl.vempty : ctl.kempty;
+    const int full = is_v ? kVFull : kKFull, empty = is_v ? kVEmpty : kKEmpty;
     uint8_t *tiles_at = smem + (is_v ? S::v : S::k);
     const uint32_t stages = is_v ? kPxV : kPxK;
     uint64_t again;  // a prefix is read by several row blocks and CTAs
@@ -648,17 +760,17 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     const uint32_t page_bytes = static_cast<uint32_t>(D) << a.p_shift;
     uint32_t g = 0, nseg = 0, par = 1, slot = 0;
     bool ok = true;
-    PxWalk walk = {u0, u0, u1, run.per, run.b, 0, 0, 0, 0, {}};
-    if (u0 < u1) px_start(a, walk, run.in);
+    PxWalk walk = {u0, u0, u1, per, ctl.run_i, n_items, 0, 0, 0, 0, {}};
+    if (u0 < u1) px_start(a, walk, ctl.run_in);
     PxSeg sg;
     while (ok && px_next(a, walk, sg)) {
       const int ss = nseg % kPxSegs;
       if (!is_v) {
-        if (nseg >= kPxSegs) ok = px_wait(ctl, &ctl.segempty[ss], ((nseg / kPxSegs) - 1) & 1, a.err_word);
+        if (nseg >= kPxSegs) ok = wait(kSegEmpty + ss, ((nseg / kPxSegs) - 1) & 1);
         if (!ok) break;
         if (lane == 0) {
           ctl.seg[ss] = sg;
-          mbar_arrive(&ctl.segfull[ss]);
+          bar_arrive(bar(kSegFull + ss));
         }
       }
       ++nseg;
@@ -671,9 +783,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const int page = needed ? __ldg(bt + lp) : 0;
         const bool good = needed && page >= 0 && page < a.num_pages;
         const uint32_t goods = __ballot_sync(0xffffffffu, good), needs = __ballot_sync(0xffffffffu, needed);
-        ok = px_wait(ctl, &empty[slot], par, a.err_word);
+        ok = wait(empty + slot, par);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(__popc(goods)) * page_bytes);
+        if (lane == 0) mbar_arrive_expect_tx(&ctl.bar[full + slot], static_cast<uint32_t>(__popc(goods)) * page_bytes);
         __syncwarp();
         int pages[kPxTok / 16];
 #pragma unroll
@@ -682,7 +794,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll
           for (int j = 0; j < kPxTok / 16; ++j)
             if (goods >> j & 1)
-              tma_load_4d(tiles_at + slot * S::kTile + j * page_bytes, map, 0, 0, sg.head, pages[j], &full[slot],
+              tma_load_4d(tiles_at + slot * S::kTile + j * page_bytes, map, 0, 0, sg.head, pages[j], &ctl.bar[full + slot],
                           sg.own ? once : again);
         }
         __syncwarp();
@@ -697,14 +809,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     }
     if (ok && !is_v) {  // nothing more
       const int ss = nseg % kPxSegs;
-      if (nseg >= kPxSegs) ok = px_wait(ctl, &ctl.segempty[ss], ((nseg / kPxSegs) - 1) & 1, a.err_word);
+      if (nseg >= kPxSegs) ok = wait(kSegEmpty + ss, ((nseg / kPxSegs) - 1) & 1);
       if (ok && lane == 0) {
         ctl.seg[ss].b = -1;
-        mbar_arrive(&ctl.segfull[ss]);
+        bar_arrive(bar(kSegFull + ss));
       }
     }
     if (*reinterpret_cast<volatile int *>(&ctl.fail) && lane == 0)
-      for (uint32_t k = g > stages ? g - stages : 0; k < g; ++k) mbar_wait(&full[k % stages], (k / stages) & 1);
+      for (uint32_t k = g > stages ? g - stages : 0; k < g; ++k) mbar_wait(&ctl.bar[full + k % stages], (k / stages) & 1);
   } else if (warp == kPxMma) {
     // ------------------------------------------------------------- MMA issue
     // Scores run up to two tiles ahead of values, into the next segment too: S(t) takes the
@@ -723,22 +835,22 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         if (!k_in) {  // the next segment: waited for only when nothing else is to be done
           const int ss = ks % kPxSegs;
           const uint32_t sp = (ks / kPxSegs) & 1, qp = (ks >> 1) & 1;
-          if (kg != pg && !px_test(&ctl.segfull[ss], sp)) break;
-          ok = px_wait(ctl, &ctl.segfull[ss], sp, a.err_word);
+          if (kg != pg && !px_test(bar(kSegFull + ss), sp)) break;
+          ok = wait(kSegFull + ss, sp);
           if (!ok) break;
           ksg = ctl.seg[ss];
           if (ksg.b < 0) {
             k_end = true;
             break;
           }
-          if (kg != pg && !px_test(&ctl.qfull[ks & 1], qp)) break;
-          ok = px_wait(ctl, &ctl.qfull[ks & 1], qp, a.err_word);
+          if (kg != pg && !px_test(bar(kQFull + (ks & 1)), qp)) break;
+          ok = wait(kQFull + (ks & 1), qp);
           if (!ok) break;
           k_in = true;
           kt = 0;
         }
         const int slot = kg % kPxK;
-        ok = px_wait(ctl, &ctl.kfull[slot], (kg / kPxK) & 1, a.err_word);
+        ok = wait(kKFull + slot, (kg / kPxK) & 1);
         if (!ok) break;
         tc_after();
         const bool last = kt + 1 == ksg.tiles;
@@ -751,12 +863,12 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             for (int k = 0; k < D / 32; ++k)
               px_mma8(tmem + kPxS + 128 * (kg & 1), q + piece * (D / 4) + 8 * k, kd + 2 * k, n, piece == 1,
                       piece == 0 || k > 0);
-          tc_commit(&ctl.sfull[kg & 1]);
-          tc_commit(&ctl.kempty[slot]);
+          bar_commit(bar(kSFull + (kg & 1)));
+          bar_commit(bar(kKEmpty + slot));
         }
         __syncwarp();
         // (a condition within the elected lane's block lost the commit: it stands around the election)
-        if (last && elect_one()) tc_commit(&ctl.qfree[ks & 1]);
+        if (last && elect_one()) bar_commit(bar(kQFree + (ks & 1)));
         __syncwarp();
         ++kg;
         ++kt;
@@ -772,11 +884,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         pt = 0;
       }
       const int buf = pg & 1;
-      ok = px_wait(ctl, &ctl.pfull[buf], (pg >> 1) & 1, a.err_word) &&
-           px_wait(ctl, &ctl.hfull[buf], (pg >> 1) & 1, a.err_word) &&
-           (pt > 0 || ps == 0 || px_wait(ctl, &ctl.ofree, (ps - 1) & 1, a.err_word));
+      ok = wait(kPFull + buf, (pg >> 1) & 1) && wait(kHFull + buf, (pg >> 1) & 1) &&
+           (pt > 0 || ps == 0 || wait(kOFree, (ps - 1) & 1));
       if (!ok) break;
-      if (lane == 0) mbar_arrive(&ctl.scempty[pg % kPxScales]);
+      if (lane == 0) bar_arrive(bar(kScEmpty + pg % kPxScales));
       tc_after();
       const bool last = pt + 1 == psg.tiles;
       if (elect_one()) {
@@ -784,62 +895,38 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const int steps = tokens(psg, pt) / 16;
         for (int k = 0; k < steps; ++k)  // 16 tokens: 8 columns of P, 16 rows of V
           px_mma16(tmem + kPxO, tmem + kPxS + 128 * buf + 32 * (k >> 1) + 8 * (k & 1), vd + k * (16 * 128 >> 4), D, pt > 0 || k > 0);
-        tc_commit(&ctl.hempty[buf]);
-        tc_commit(&ctl.pvdone);
+        bar_commit(bar(kHEmpty + buf));
+        bar_commit(bar(kPvDone));
       }
       __syncwarp();
-      if (last && elect_one()) tc_commit(&ctl.odone);
+      if (last && elect_one()) bar_commit(bar(kODone));
       __syncwarp();
       ++pg;
       ++pt;
       if (last) {
-        if (lane == 0) mbar_arrive(&ctl.segempty[ps % kPxSegs]);
+        if (lane == 0) bar_arrive(bar(kSegEmpty + ps % kPxSegs));
         p_in = false;
         ++ps;
       }
     }
     if (*reinterpret_cast<volatile int *>(&ctl.fail)) {
       // the products in flight end before the CTA's memory goes to another one
-      if (elect_one()) tc_commit(&ctl.drain);
-      mbar_wait(&ctl.drain, 0);
+      if (elect_one()) bar_commit(bar(kDrain));
+      mbar_wait(&ctl.bar[kDrain], 0);
     }
-  } else if (warp >= kPxSoft) {
-    // ------------------------- sides: q in, V from e4m3 to f16, sums out
+  } else if (warp >= kPxSoft + kPxConv + kPxQ4) {
+    // ------------- sums out: to the output, or with their statistics to where the merge finds them
     const int quad = warp & 3, r = 32 * quad + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-    constexpr int kC = D / 16, kR = 32 / kC;  // chunks of 16 codes a row of V; rows a pass
-    const int row0 = 32 * quad + lane / kC, chunk = lane % kC;  // this lane's rows, kR apart, and chunk
-    uint32_t g = 0, nq = 0;  // tiles, and segments whose q is in
-    bool ok = true, ended = false;
-    // The next segment's q; its descriptor is posted when the copies of the one before are issued.
-    auto load_q = [&]() -> bool {
-      const uint32_t k = nq;
-      if (!px_wait(ctl, &ctl.segfull[k % kPxSegs], (k / kPxSegs) & 1, a.err_word)) return false;
-      const PxSeg &sg = ctl.seg[k % kPxSegs];
-      ended = sg.b < 0;
-      if (ended) return true;
-      if (k >= 2 && !px_wait(ctl, &ctl.qfree[k & 1], ((k >> 1) - 1) & 1, a.err_word)) return false;
-      tc_after();
-      if (32 * quad < sg.rows) {
-        px_load_q<D>(a, sg, tmem + lanes + kPxQ + (k & 1) * (D / 2), ctl.qk[k % kPxStats], r);
-        tc_st_wait();
-      }
-      tc_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&ctl.qfull[k & 1]);
-        mbar_arrive(&ctl.qready[k % kPxStats]);
-      }
-      ++nq;
-      return true;
-    };
-    // Segment k's sums: a row to the output, or with its statistics to where the merge finds it.
-    auto put = [&](uint32_t k) -> bool {
-      const int ks = k % kPxStats;
-      if (!px_wait(ctl, &ctl.stat[ks], (k / kPxStats) & 1, a.err_word) ||
-          !px_wait(ctl, &ctl.odone, k & 1, a.err_word))
-        return false;
-      const PxSeg &sg = ctl.seg[k % kPxSegs];
+    bool ok = true;
+    for (uint32_t k = 0; ok; ++k) {
+      const int ss = k % kPxSegs, ks = k % kPxStats;
+      ok = wait(kSegFull + ss, (k / kPxSegs) & 1);
+      if (!ok) break;
+      const PxSeg &sg = ctl.seg[ss];
+      if (sg.b < 0) break;
+      ok = wait(kStatFull + ks, (k / kPxStats) & 1) && wait(kODone, k & 1);
+      if (!ok) break;
       tc_after();
       if (32 * quad < sg.rows) {
         const int row = sg.rb * kPxRows + r, i = row / a.G;
@@ -899,23 +986,54 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       tc_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&ctl.ofree);
-        mbar_arrive(&ctl.segempty[k % kPxSegs]);
+        bar_arrive(bar(kOFree));
+        bar_arrive(bar(kSegEmpty + ss));
       }
-      return true;
-    };
-    grid_dependency_wait();  // q's pieces
+    }
+  } else if (warp >= kPxSoft + kPxConv) {
+    // ------------------------------------------------------------------- q in
+    const int quad = warp & 3, r = 32 * quad + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+    bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
-      ok = load_q();
+      const int ss = k % kPxSegs;
+      ok = wait(kSegFull + ss, (k / kPxSegs) & 1);
       if (!ok) break;
-      const PxSeg &sg = ctl.seg[k % kPxSegs];
-      const int tiles = ended ? 0 : sg.tiles, t_end = sg.t_end;
+      const PxSeg &sg = ctl.seg[ss];
+      if (sg.b < 0) break;
+      ok = k < 2 || wait(kQFree + (k & 1), ((k >> 1) - 1) & 1);
+      if (!ok) break;
+      tc_after();
+      if (32 * quad < sg.rows) {
+        px_load_q<D>(a, sg, tmem + lanes + kPxQ + (k & 1) * (D / 2), ctl.qk[k % kPxStats], r);
+        tc_st_wait();
+      }
+      tc_before();
+      __syncwarp();
+      if (lane == 0) {
+        bar_arrive(bar(kQFull + (k & 1)));
+        bar_arrive(bar(kQReady + k % kPxStats));
+        bar_arrive(bar(kSegEmpty + ss));
+      }
+    }
+  } else if (warp >= kPxSoft) {
+    // ------------------------------------------------------ V from e4m3 to f16
+    const int quad = warp & 3;
+    constexpr int kC = D / 16, kR = 32 / kC;  // chunks of 16 codes a row of V; rows a pass
+    const int row0 = 32 * quad + lane / kC, chunk = lane % kC;  // this lane's rows, kR apart, and chunk
+    uint32_t g = 0;
+    bool ok = true;
+    for (uint32_t k = 0; ok; ++k) {
+      const int ss = k % kPxSegs;
+      ok = wait(kSegFull + ss, (k / kPxSegs) & 1);
+      if (!ok) break;
+      const PxSeg &sg = ctl.seg[ss];
+      if (sg.b < 0) break;
+      const int tiles = sg.tiles, t_end = sg.t_end, tok0 = sg.tok;
       const int min_lim = sg.lim0 ? min(t_end, sg.lim0 + sg.rb * kPxRows / a.G) : t_end;
-      for (int t = 0; t < max(tiles, 1); ++t) {
-        if (t < tiles) {
-        const int slot = g % kPxV, buf = g & 1, tok = sg.tok + t * kPxTok + 32 * quad;
-        ok = px_wait(ctl, &ctl.vfull[slot], (g / kPxV) & 1, a.err_word) &&
-             px_wait(ctl, &ctl.hempty[buf], ((g >> 1) & 1) ^ 1, a.err_word);
+      for (int t = 0; t < tiles; ++t, ++g) {
+        const int slot = g % kPxV, buf = g & 1, tok = tok0 + t * kPxTok + 32 * quad;
+        ok = wait(kVFull + slot, (g / kPxV) & 1) && wait(kHEmpty + buf, ((g >> 1) & 1) ^ 1);
         if (!ok) break;
         const uint8_t *v = smem + S::v + slot * S::kTile;
         uint8_t *h = smem + S::h + buf * S::kHalf;
@@ -957,19 +1075,16 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         proxy_fence();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&ctl.vempty[slot]);
-          mbar_arrive(&ctl.hfull[buf]);
-        }
-        ++g;
-        }
-        if (t == 0 && k > 0) {  // the sums before, once this segment's first values are on their way
-          ok = put(k - 1);
-          if (!ok) break;
+          bar_arrive(bar(kVEmpty + slot));
+          bar_arrive(bar(kHFull + buf));
         }
       }
-      if (!ok || ended) break;
+      if (!ok) break;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.stat[k % kPxStats]);
+      if (lane == 0) {
+        bar_arrive(bar(kStatFull + k % kPxStats));
+        bar_arrive(bar(kSegEmpty + ss));
+      }
     }
   } else {
     // ------------------------------------------------------- softmax, a row a lane
@@ -980,7 +1095,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       const int ss = k % kPxSegs, ks = k % kPxStats;
-      ok = px_wait(ctl, &ctl.segfull[ss], (k / kPxSegs) & 1, a.err_word);
+      ok = wait(kSegFull + ss, (k / kPxSegs) & 1);
       if (!ok) break;
       const PxSeg &sg = ctl.seg[ss];
       if (sg.b < 0) break;
@@ -992,15 +1107,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       int bad_from = INT_MAX, come = 0;
       const int first = (g & 1) != static_cast<uint32_t>(grp);  // the group's first tile
       if (first < tiles) {
-        ok = px_wait(ctl, &ctl.qready[ks], (k / kPxStats) & 1, a.err_word);
+        ok = wait(kQReady + ks, (k / kPxStats) & 1);
         if (!ok) break;
         qk = ctl.qk[ks][r];  // (of a row that exists)
       }
       for (int t = first; t < tiles; t += 2) {
         const uint32_t gt = g + t;
         const int cs = gt % kPxScales, tok = tok0 + t * kPxTok;
-        ok = px_wait(ctl, &ctl.sfull[grp], (gt >> 1) & 1, a.err_word) &&
-             px_wait(ctl, &ctl.scfull[cs], (gt / kPxScales) & 1, a.err_word);
+        ok = wait(kSFull + grp, (gt >> 1) & 1) && wait(kScFull + cs, (gt / kPxScales) & 1);
         if (!ok) break;
         tc_after();
         come = t + 1;
@@ -1031,7 +1145,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         }
         // the references, which the groups hand one another with their weights
         if (gt > 0) {
-          ok = px_wait(ctl, &ctl.pfull[grp ^ 1], ((gt - 1) >> 1) & 1, a.err_word);
+          ok = wait(kPFull + (grp ^ 1), ((gt - 1) >> 1) & 1);
           if (!ok) break;
         }
         if (act) {
@@ -1077,7 +1191,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           }
           l += l2.x + l2.y;
           if (t > 0 && __any_sync(0xffffffffu, fo != 1.f)) {
-            ok = px_wait(ctl, &ctl.pvdone, (gt - 1) & 1, a.err_word);
+            ok = wait(kPvDone, (gt - 1) & 1);
             if (!ok) break;
             tc_after();
 #pragma unroll 1
@@ -1093,7 +1207,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         }
         tc_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.pfull[grp]);
+        if (lane == 0) bar_arrive(bar(kPFull + grp));
       }
       if (!ok) break;
       g += tiles;
@@ -1101,8 +1215,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       if (quad == 0 && lane == 0) ctl.come[ks][grp] = come;
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&ctl.stat[ks]);
-        mbar_arrive(&ctl.segempty[ss]);
+        bar_arrive(bar(kStatFull + ks));
+        bar_arrive(bar(kSegEmpty + ss));
       }
     }
     tc_before();
@@ -1120,80 +1234,96 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 
 constexpr int kPxMergeWarps = 8;
 
-template <int D>
-struct PxSum {
-  float M, N, l, acc[D / 32];
-  bool bad;
-};
-
-template <int D>
-__device__ __forceinline__ void px_add(PxSum<D> &s, const float *row, int lane) {
-  const float4 e = __ldcg(reinterpret_cast<const float4 *>(row + D));
-  float v[D / 32];
-#pragma unroll
-  for (int k = 0; k < D / 32; ++k) v[k] = __ldcg(row + lane + 32 * k);
-  s.bad |= e.y < 0.f;
-  if (e.y == 0.f) return;  // saw nothing
-  const float M = fmaxf(s.M, e.x), N = fmaxf(s.N, e.z);
-  const float fm = s.M == -INFINITY ? 0.f : exp2f(s.M - M), fn = s.N == -INFINITY ? 0.f : exp2f(s.N - N);
-  const float gm = exp2f(e.x - M), gn = exp2f(e.z - N);
-  s.l = fmaf(gm, e.y, s.l * fm);
-#pragma unroll
-  for (int k = 0; k < D / 32; ++k) s.acc[k] = fmaf(gn, v[k], s.acc[k] * fn);
-  s.M = M;
-  s.N = N;
-}
-
+// One request of the plan, a warp a row and head, the lanes its dims; four parts' loads in flight.
+//   out = 2^(N - M) sum_p 2^(n_p - N) o_p / sum_p 2^(m_p - M) l_p
 template <int D>
 __global__ void __launch_bounds__(32 * kPxMergeWarps) prefix_merge_kernel(PfArgs a) {
-  constexpr int RF = D + kStat;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x;
-  // the inputs were written before the kernel ahead began; its results come after the wait
-  bool order = true;
-  for (int g = threadIdx.x; g < a.n_groups; g += 32 * kPxMergeWarps) order &= pf_group_ok(a, g);
-  order = __syncthreads_and(order);
-  const PfReq rq = order ? pf_request(a, b) : PfReq{request_rows<true>(a.rg, b), 0, -1, false};
-  const int row_pre = rq.group >= 0 && rq.pre > 0 ? pf_group_rows(a, rq.group).x : 0;
+  constexpr int RF = D + kStat, V = D / 32, kBatch = 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the kernel ahead began, and let this one start, when the plan was complete)
+  const int n_grp = __ldcg(&a.plan->n_grp), n_req = __ldcg(&a.plan->n_req);
+  const PxItem it = px_load_item(a, n_grp + min(static_cast<int>(blockIdx.x), max(n_req - 1, 0)));
   grid_dependency_wait();
   allow_dependents();
-  for (int64_t u = blockIdx.y * kPxMergeWarps + warp; u < static_cast<int64_t>(rq.r.n) * a.Hq;
+  if (static_cast<int>(blockIdx.x) >= n_req) return;
+  for (int64_t u = blockIdx.y * kPxMergeWarps + warp; u < static_cast<int64_t>(it.n) * a.Hq;
        u += gridDim.y * kPxMergeWarps) {
-    const int i = static_cast<int>(u / a.Hq), h = static_cast<int>(u - static_cast<int64_t>(i) * a.Hq);
-    const int token = rq.r.row + i, kvh = h / a.G;
-    const int64_t at = static_cast<int64_t>(token) * a.Hq + h;
-    uint16_t *o = a.out + at * D;
-    if (!rq.live) {
+    const int i = static_cast<int>(px_div(u, a.Hq)), h = static_cast<int>(u - static_cast<int64_t>(i) * a.Hq);
+    const int64_t at = (static_cast<int64_t>(it.row0) + i) * a.Hq + h;
+    uint16_t *o = a.out + at * D + V * lane;
+    const float *rows = a.rows + at * RF, *own_rows = rows + static_cast<int64_t>(a.rg.n_tokens) * a.Hq * RF;
+    float M = -INFINITY, N = -INFINITY, l = 0.f, acc[V];
+    bool bad = !it.live;
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) o[lane + 32 * k] = 0;
-      continue;
+    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+    // where the sums lie: the prefix's, then those of its own tokens
+    float4 where[2];
+    where[0] = where[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (it.live) {
+      if (it.pre) where[0] = __ldcg(reinterpret_cast<const float4 *>(rows + D));
+      where[1] = __ldcg(reinterpret_cast<const float4 *>(own_rows + D));
+      if (where[1].w == kDone) continue;
     }
-    PxSum<D> s;
-    s.M = s.N = -INFINITY;
-    s.l = 0.f;
-    s.bad = false;
+#pragma unroll 1
+    for (int own = 0; own < 2; ++own) {
+      const float4 e = own ? where[1] : where[0];
+      if (e.w == 0.f) continue;
+      // part p lies in the p-th CTA from here on: the first in slot 1, others in slot 0
+      const bool cut = e.w == kCut;
+      const int parts = cut ? __float_as_int(e.y) : 1;
+      const int r = ((it.row0 + i - (own ? it.row0 : it.row_pre)) * a.G + h % a.G) % kPxRows;
+      const float *base = cut ? a.cut + (static_cast<int64_t>(2 * __float_as_int(e.x)) * kPxRows + r) * RF
+                              : own ? own_rows : rows;
+      for (int p0 = 0; p0 < parts; p0 += kBatch) {
+        float4 s[kBatch];
+        float v[kBatch][V];
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) s.acc[k] = 0.f;
-    bool done = false;
-    for (int own = rq.pre > 0 ? 0 : 1; own < 2; ++own) {
-      const float *row = a.rows + (static_cast<int64_t>(own) * a.rg.n_tokens * a.Hq + at) * RF;
-      const float4 e = __ldcg(reinterpret_cast<const float4 *>(row + D));
-      if (e.w == kDone) {
-        done = true;
-      } else if (e.w == kHere) {
-        px_add<D>(s, row, lane);
-      } else {
-        // part p lies in the p-th CTA from here on: the first in slot 1, others in slot 0
-        const int cta = __float_as_int(e.x), parts = __float_as_int(e.y);
-        const int r = ((token - (own ? rq.r.row : row_pre)) * a.G + h - kvh * a.G) % kPxRows;
-        for (int p = 0; p < parts; ++p)
-          px_add<D>(s, a.cut + (static_cast<int64_t>(2 * (cta + p) + (p == 0)) * kPxRows + r) * RF, lane);
+        for (int j = 0; j < kBatch; ++j) {
+          s[j] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+          if (p0 + j < parts) {
+            const float *q = base + (cut ? static_cast<int64_t>(2 * (p0 + j) + (p0 + j == 0)) * kPxRows * RF : 0);
+            s[j] = __ldcg(reinterpret_cast<const float4 *>(q + D));
+            if constexpr (V == 4) {
+              const float4 x = __ldcg(reinterpret_cast<const float4 *>(q) + lane);
+              v[j][0] = x.x;
+              v[j][1] = x.y;
+              v[j][2] = x.z;
+              v[j][3] = x.w;
+            } else {
+              const float2 x = __ldcg(reinterpret_cast<const float2 *>(q) + lane);
+              v[j][0] = x.x;
+              v[j][1] = x.y;
+            }
+          }
+        }
+        float Mb = M, Nb = N;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          Mb = fmaxf(Mb, s[j].x);
+          Nb = fmaxf(Nb, s[j].z);
+          bad |= s[j].y < 0.f;
+        }
+        const float fl = M == -INFINITY ? 0.f : exp2f(M - Mb), fo = N == -INFINITY ? 0.f : exp2f(N - Nb);
+        l *= fl;
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] *= fo;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          if (s[j].y == 0.f) continue;  // saw nothing
+          l = fmaf(exp2f(s[j].x - Mb), s[j].y, l);
+          const float f = exp2f(s[j].z - Nb);
+#pragma unroll
+          for (int k = 0; k < V; ++k) acc[k] = fmaf(f, v[j][k], acc[k]);
+        }
+        M = Mb;
+        N = Nb;
       }
     }
-    if (done) continue;
-    const float2 f = out_scale(s.N - s.M - 7.f, s.l);
+    const float2 f = bad ? make_float2(0.f, 0.f) : out_scale(N - M - 7.f, l);
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k)
-      o[lane + 32 * k] = static_cast<uint16_t>(pack_bf16x2(s.bad ? 0.f : s.acc[k] * f.x * f.y, 0.f));
+    for (int k = 0; k < V; k += 2)
+      *reinterpret_cast<uint32_t *>(o + k) =
+          bad ? 0u : pack_bf16x2(acc[k] * f.x * f.y, acc[k + 1] * f.x * f.y);
   }
 }
 
@@ -1211,9 +1341,12 @@ size_t px_cut_bytes(int ctas, int D) { return px_up256(2ull * ctas * kPxRows * (
 
 size_t px_q_bytes(int64_t n_tokens, int Hq, int D) { return px_up256(2ull * n_tokens * Hq * D); }
 size_t px_qk_bytes(int64_t n_tokens, int Hq) { return px_up256(4ull * n_tokens * Hq); }
+size_t px_plan_bytes(int64_t n_tokens) {
+  return 256 + px_up256(2 * n_tokens * sizeof(PxItem)) + px_up256((2 * n_tokens + 1) * sizeof(int64_t));
+}
 size_t px_bytes(int64_t n_tokens, int Hq, int D, int ctas) {
-  return px_rows_bytes(n_tokens, Hq, D) + px_cut_bytes(ctas, D) + px_q_bytes(n_tokens, Hq, D) +
-         px_qk_bytes(n_tokens, Hq);
+  return px_plan_bytes(n_tokens) + px_rows_bytes(n_tokens, Hq, D) + px_cut_bytes(ctas, D) +
+         px_q_bytes(n_tokens, Hq, D) + px_qk_bytes(n_tokens, Hq);
 }
 
 using PxFn = void (*)(CUtensorMap, CUtensorMap, PfArgs);
@@ -1291,6 +1424,10 @@ extern "C" kvq_status kvq_block_prefix_attn(
   a.prefix_pages = prefix_pages;
   a.abort_mask = abort_mask;
   uint8_t *at = static_cast<uint8_t *>(workspace);
+  a.plan = reinterpret_cast<PxPlan *>(at);
+  a.items = reinterpret_cast<PxItem *>(at + 256);
+  a.units = reinterpret_cast<int64_t *>(at + 256 + px_up256(2ull * n_tokens * sizeof(PxItem)));
+  at += px_plan_bytes(n_tokens);
   a.rows = reinterpret_cast<float *>(at);
   at += px_rows_bytes(n_tokens, Hq, D);
   a.cut = reinterpret_cast<float *>(at);
@@ -1316,13 +1453,13 @@ extern "C" kvq_status kvq_block_prefix_attn(
   if (!px_map(&kmap, cache->k_pool, *cache) || !px_map(&vmap, cache->v_pool, *cache)) return KVQ_ERR_CUDA;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const int64_t q_ctas = (static_cast<int64_t>(n_tokens) * Hq * (D / 4) + kPxQThreads - 1) / kPxQThreads;
-  if (launch_dependent(D == 128 ? prefix_q_kernel<128> : prefix_q_kernel<64>, static_cast<unsigned>(q_ctas),
-                       kPxQThreads, 0, cs, a) != cudaSuccess)
+  if (launch_dependent(D == 128 ? prefix_plan_kernel<128> : prefix_plan_kernel<64>, static_cast<unsigned>(1 + q_ctas),
+                       kPxQThreads, 0, cs, a, sms) != cudaSuccess)
     return KVQ_ERR_CUDA;
   if (launch_dependent(fn, sms, kPxThreads, smem, cs, kmap, vmap, a) != cudaSuccess) return KVQ_ERR_CUDA;
   // a warp a row and head, up to 64 CTAs a request
   const int64_t most = (static_cast<int64_t>(std::min(max_q, n_tokens)) * Hq + kPxMergeWarps - 1) / kPxMergeWarps;
-  const dim3 grid(static_cast<unsigned>(B), static_cast<unsigned>(std::min<int64_t>(64, most)));
+  const dim3 grid(static_cast<unsigned>(std::min(B, n_tokens)), static_cast<unsigned>(std::min<int64_t>(64, most)));
   if (launch_dependent(D == 128 ? prefix_merge_kernel<128> : prefix_merge_kernel<64>, grid, 32 * kPxMergeWarps, 0, cs,
                        a) != cudaSuccess)
     return KVQ_ERR_CUDA;
