@@ -97,10 +97,10 @@ constexpr int kPxK = 4, kPxV = 4;   // tiles of K and of V in flight
 constexpr int kStat = 4;            // floats behind a row's sums
 // a row's fourth statistic: its sums lie here, in the parts of several CTAs, or it is written
 constexpr float kHere = 1.f, kCut = 2.f, kDone = 3.f;
-// warps: softmax (two groups of four), V's conversion, q in, sums out; then MMAs, copies of K, of V,
-// scales
-constexpr int kPxSoft = 8, kPxConv = 4, kPxQ4 = 4, kPxPut = 4;
-constexpr int kPxMma = kPxSoft + kPxConv + kPxQ4 + kPxPut, kPxThreads = 32 * (kPxMma + 4);
+// warps: softmax (two groups of eight), V's conversion, edges (q in, sums out); then MMAs, copies of K,
+// of V, scales
+constexpr int kPxSoft = 16, kPxConv = 4, kPxEdge = 4;
+constexpr int kPxMma = kPxSoft + kPxConv + kPxEdge, kPxThreads = 32 * (kPxMma + 4);
 constexpr float kPxFar = 64.f;      // how far the denominator's reference may be off (fp32)
 
 // An item: the prefix of a group for all its rows, or a request's own tokens for its rows.
@@ -239,7 +239,7 @@ __device__ __noinline__ bool px_next(const PfArgs &a, PxWalk &w, PxSeg &sg) {
 // shared memory and tcgen05
 // ---------------------------------------------------------------------------
 
-// Barriers, those that expect as many arrivals together: 1, 4, 12, 22.
+// Barriers, those that expect as many arrivals together: 1, 2, 4, 8, 20, 26.
 enum : int {
   kKFull = 0,
   kKEmpty = kKFull + kPxK,
@@ -253,21 +253,30 @@ enum : int {
   kPvDone = kHEmpty + 2,
   kODone,
   kDrain,
-  kVEmpty,  // four warps each from here
+  kPair,  // [group][quarter of the rows]: two warps each
+  kRef = kPair + 8,
+  kVEmpty = kRef + 8,  // four warps each from here
   kQFull = kVEmpty + kPxV,
   kQReady = kQFull + 2,
-  kPFull = kQReady + kPxStats,
-  kHFull = kPFull + 2,
+  kHFull = kQReady + kPxStats,
   kOFree = kHFull + 2,
-  kStatFull,  // softmax and conversion
+  kPFull,  // a group
+  kStatFull = kPFull + 2,  // softmax and conversion
   kSegEmpty = kStatFull + kPxStats,  // everybody but the copies
   kBars = kSegEmpty + kPxSegs
 };
 
+__device__ __forceinline__ int px_arrivals(int bar) {
+  return bar < kPair ? 1 : bar < kVEmpty ? 2 : bar < kPFull ? 4 : bar < kStatFull ? 8
+         : bar < kSegEmpty ? kPxSoft + kPxConv : kPxMma + 2;
+}
+
 struct PxCtl {
   float4 sc[kPxScales][kPxTok / 16];  // of a tile's blocks: K scale; V scale's fraction times 2^7, exponent
-  float4 end[kPxStats][2][kPxRows];   // [segment][group]: m that its l stands on, l, n, -
-  float2 now[kPxRows];                // (m, n): a row's references
+  float2 end_mn[kPxStats][2][kPxRows];   // [segment][group]: m that its l stands on, n
+  float end_l[kPxStats][2][2][kPxRows];  // [segment][group][half]
+  float2 mx[2][2][kPxRows];           // [group][half]: a tile's maxima of x and x + log2 vs
+  float2 now[2][kPxRows];             // [group]: (m, n), a row's references
   float qk[kPxStats][kPxRows];
   unsigned long long nan_from[kPxStats][128];  // per dim: px_nan of a token with a NaN code that some row
                                                // does not see, the first of the last segment that had one
@@ -675,7 +684,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   };
   if (threadIdx.x < kBars) {
     const int i = threadIdx.x;
-    mbar_init(&ctl.bar[i], i < kVEmpty ? 1 : i < kStatFull ? 4 : i < kSegEmpty ? kPxSoft + kPxConv : kPxMma + 2);
+    mbar_init(&ctl.bar[i], px_arrivals(i));
     fence_barrier_init();
   }
   if (threadIdx.x < kPxStats) ctl.nan_seg[threadIdx.x] = 0;
@@ -914,28 +923,50 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       if (elect_one()) bar_commit(bar(kDrain));
       mbar_wait(&ctl.bar[kDrain], 0);
     }
-  } else if (warp >= kPxSoft + kPxConv + kPxQ4) {
-    // ------------- sums out: to the output, or with their statistics to where the merge finds them
+  } else if (warp >= kPxSoft + kPxConv) {
+    // ----- edges: q in; sums out, to the output, or with their statistics to where the merge finds them
     const int quad = warp & 3, r = 32 * quad + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
     bool ok = true;
-    for (uint32_t k = 0; ok; ++k) {
-      const int ss = k % kPxSegs, ks = k % kPxStats;
-      ok = wait(kSegFull + ss, (k / kPxSegs) & 1);
+    for (uint32_t j = 0; ok; ++j) {  // segment j's q, then the sums of the one before
+      ok = wait(kSegFull + j % kPxSegs, (j / kPxSegs) & 1);
       if (!ok) break;
+      const PxSeg &next = ctl.seg[j % kPxSegs];
+      const bool ended = next.b < 0;
+      if (!ended) {
+        ok = j < 2 || wait(kQFree + (j & 1), ((j >> 1) - 1) & 1);
+        if (!ok) break;
+        tc_after();
+        if (32 * quad < next.rows) {
+          px_load_q<D>(a, next, tmem + lanes + kPxQ + (j & 1) * (D / 2), ctl.qk[j % kPxStats], r);
+          tc_st_wait();
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(bar(kQFull + (j & 1)));
+          bar_arrive(bar(kQReady + j % kPxStats));
+        }
+      }
+      if (j == 0) {
+        if (ended) break;
+        continue;
+      }
+      const uint32_t k = j - 1;
+      const int ss = k % kPxSegs, ks = k % kPxStats;
       const PxSeg &sg = ctl.seg[ss];
-      if (sg.b < 0) break;
       ok = wait(kStatFull + ks, (k / kPxStats) & 1) && wait(kODone, k & 1);
       if (!ok) break;
       tc_after();
       if (32 * quad < sg.rows) {
         const int row = sg.rb * kPxRows + r, i = row / a.G;
         const int fin = ctl.come[ks][1] > ctl.come[ks][0];  // who had the last tile
-        const float4 e0 = ctl.end[ks][fin][r], e1 = ctl.end[ks][fin ^ 1][r];
-        const float M = e0.x, N = e0.z;
-        const bool bad = e0.y < 0.f || e1.y < 0.f;
-        float l = e0.y;
-        if (e1.y != 0.f) l += e1.y * exp2f(e1.x - M);
+        const float M = ctl.end_mn[ks][fin][r].x, N = ctl.end_mn[ks][fin][r].y;
+        const float l0 = ctl.end_l[ks][fin][0][r], l1 = ctl.end_l[ks][fin][1][r];
+        const float l2 = ctl.end_l[ks][fin ^ 1][0][r], l3 = ctl.end_l[ks][fin ^ 1][1][r];
+        const bool bad = l0 < 0.f || l1 < 0.f || l2 < 0.f || l3 < 0.f;
+        float l = l0 + l1;
+        if (l2 + l3 != 0.f) l += (l2 + l3) * exp2f(ctl.end_mn[ks][fin ^ 1][r].x - M);
         if (bad) l = -1.f;
         const bool whole = sg.part < 0 && sg.own && !sg.pre;  // nothing to be merged with
         const int64_t at = (static_cast<int64_t>(sg.row0) + i) * a.Hq + sg.head * a.G + row - i * a.G;
@@ -989,32 +1020,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         bar_arrive(bar(kOFree));
         bar_arrive(bar(kSegEmpty + ss));
       }
-    }
-  } else if (warp >= kPxSoft + kPxConv) {
-    // ------------------------------------------------------------------- q in
-    const int quad = warp & 3, r = 32 * quad + lane;
-    const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-    bool ok = true;
-    for (uint32_t k = 0; ok; ++k) {
-      const int ss = k % kPxSegs;
-      ok = wait(kSegFull + ss, (k / kPxSegs) & 1);
-      if (!ok) break;
-      const PxSeg &sg = ctl.seg[ss];
-      if (sg.b < 0) break;
-      ok = k < 2 || wait(kQFree + (k & 1), ((k >> 1) - 1) & 1);
-      if (!ok) break;
-      tc_after();
-      if (32 * quad < sg.rows) {
-        px_load_q<D>(a, sg, tmem + lanes + kPxQ + (k & 1) * (D / 2), ctl.qk[k % kPxStats], r);
-        tc_st_wait();
-      }
-      tc_before();
-      __syncwarp();
-      if (lane == 0) {
-        bar_arrive(bar(kQFull + (k & 1)));
-        bar_arrive(bar(kQReady + k % kPxStats));
-        bar_arrive(bar(kSegEmpty + ss));
-      }
+      if (ended) break;
     }
   } else if (warp >= kPxSoft) {
     // ------------------------------------------------------ V from e4m3 to f16
@@ -1087,11 +1093,13 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       }
     }
   } else {
-    // ------------------------------------------------------- softmax, a row a lane
-    const int grp = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
+    // ------------------------------------------------------------- softmax
+    // A row a lane, twice: `half` takes every other 32 tokens of a tile.
+    const int grp = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, r = 32 * quad + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-    const uint32_t s_addr = tmem + lanes + kPxS + 128 * grp, o_addr = tmem + lanes + kPxO;
-    uint32_t g = 0;  // tiles of the CTA so far
+    const uint32_t s_addr = tmem + lanes + kPxS + 128 * grp, o_addr = tmem + lanes + kPxO + half * (D / 2);
+    const int pair = kPair + 4 * grp + quad, ref_mine = kRef + 4 * grp + quad, ref_other = kRef + 4 * (grp ^ 1) + quad;
+    uint32_t g = 0, np = 0;  // tiles of the CTA so far, exchanges
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       const int ss = k % kPxSegs, ks = k % kPxStats;
@@ -1126,68 +1134,61 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           bad_from = min(bad_from, ctl.bad[cs]);
           // (rolled loops: with the chunks laid out one after another the roles' code did not fit the
           // instruction caches, and its fetching took twice the time of the work)
-          if (full) {
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              tc_ld32(x, s_addr + 32 * c);
-              tc_ld_wait(x);
-              px_max(x, sc + 2 * c, qk, mx, mv);
-            }
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
-              tc_ld32(x, s_addr + 32 * c);
-              tc_ld_wait(x);
-              px_mask(x, lim - tok - 32 * c);
-              px_max(x, sc + 2 * c, qk, mx, mv);
-            }
+          for (int c = half; c < chunks; c += 2) {
+            tc_ld32(x, s_addr + 32 * c);
+            tc_ld_wait(x);
+            if (!full) px_mask(x, lim - tok - 32 * c);
+            px_max(x, sc + 2 * c, qk, mx, mv);
           }
+          ctl.mx[grp][half][r] = make_float2(mx, mv);
         }
-        // the references, which the groups hand one another with their weights
-        if (gt > 0) {
-          ok = wait(kPFull + (grp ^ 1), ((gt - 1) >> 1) & 1);
-          if (!ok) break;
-        }
+        // the row's other half, and the references that the groups hand one another
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(pair));
+        ok = wait(pair, np++ & 1) && (gt == 0 || wait(ref_other, ((gt - 1) >> 1) & 1));
+        if (!ok) break;
+        float fo = 1.f;
         if (act) {
+          const float2 other = ctl.mx[grp][half ^ 1][r];
+          mx = fmaxf(mx, other.x);
+          mv = fmaxf(mv, other.y);
           if (t > 0) {
-            const float2 now = ctl.now[r];
+            const float2 now = ctl.now[grp ^ 1][r];
             m = now.x;
             n = now.y;
           }
-          float fo = 1.f;
           if (m == -INFINITY || mx > m + kPxFar) m = mx;
           if (n == -INFINITY) {
             n = mv;
           } else if (mv > n + kRescaleThreshold) {
-            fo = exp2f(n - mv);
+            fo = fast_exp2(n - mv);
             n = mv;
           }
-          ctl.now[r] = make_float2(m, n);
+          if (half == 0) ctl.now[grp][r] = make_float2(m, n);
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(ref_mine));
+        if (act) {
           if (lm != m) {
-            l = l == 0.f ? 0.f : l * exp2f(lm - m);
+            l = l == 0.f ? 0.f : l * fast_exp2(lm - m);
             lm = m;
           }
           const bool none = n == -INFINITY;  // nothing seen yet: every x is -inf
           const float mm = none ? 0.f : m, mn = none ? 0.f : m - n;
           float2 l2 = make_float2(0.f, 0.f);
           float p[16];
-          if (full) {
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              tc_ld32(x, s_addr + 32 * c);
-              tc_ld_wait(x);
+          for (int c = half; c < chunks; c += 2) {
+            tc_ld32(x, s_addr + 32 * c);
+            tc_ld_wait(x);
+            if (full) {
               px_weights<false>(x, sc + 2 * c, qk, mm, mn, l2, p);
-              tc_st16(s_addr + 32 * c, p);  // in the chunk's own columns
-            }
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
-              tc_ld32(x, s_addr + 32 * c);
-              tc_ld_wait(x);
+            } else {
               px_mask(x, lim - tok - 32 * c);
               px_weights<true>(x, sc + 2 * c, qk, mm, mn, l2, p);
-              tc_st16(s_addr + 32 * c, p);
             }
+            tc_st16(s_addr + 32 * c, p);  // in the chunk's own columns
           }
           l += l2.x + l2.y;
           if (t > 0 && __any_sync(0xffffffffu, fo != 1.f)) {
@@ -1195,7 +1196,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             if (!ok) break;
             tc_after();
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
+            for (int c = 0; c < D / 2; c += 16) {
               float o[16];
               tc_ld16(o, o_addr + c);
 #pragma unroll
@@ -1211,8 +1212,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       }
       if (!ok) break;
       g += tiles;
-      ctl.end[ks][grp][r] = make_float4(lm, lim > bad_from ? -1.f : l, n, 0.f);
-      if (quad == 0 && lane == 0) ctl.come[ks][grp] = come;
+      if (half == 0) ctl.end_mn[ks][grp][r] = make_float2(lm, n);
+      ctl.end_l[ks][grp][half][r] = lim > bad_from ? -1.f : l;
+      if (half == 0 && quad == 0 && lane == 0) ctl.come[ks][grp] = come;
       __syncwarp();
       if (lane == 0) {
         bar_arrive(bar(kStatFull + ks));
