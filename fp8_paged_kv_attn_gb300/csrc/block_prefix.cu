@@ -308,13 +308,15 @@ struct PxSmem {
 };
 
 // Barriers by their shared-memory address.
+// A try sleeps until the phase ends, for up to a millisecond (left to its own, it comes back after a short
+// time, and the waiting warps' polls were a fifth of all instructions).
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(1000000)
       : "memory");
   return done != 0;
 }
@@ -387,28 +389,20 @@ __device__ __forceinline__ void px_mma16(uint32_t d, uint32_t a, uint64_t b, uin
       : "memory");
 }
 
-// 32 consecutive columns of this warp's lanes; the values are there after tc_ld_wait.
+// 32 consecutive columns of this warp's lanes, loaded and waited for in one statement, so that no use
+// moves between.
 __device__ __forceinline__ void tc_ld32(float (&v)[32], uint32_t addr) {
   uint32_t *r = reinterpret_cast<uint32_t *>(v);
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr));
-}
-
-// Waits for this thread's loads; the values pass through it, so that no use moves ahead of it.
-__device__ __forceinline__ void tc_ld_wait(float (&v)[32]) {
-  uint32_t *r = reinterpret_cast<uint32_t *>(v);
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-        "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-        "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-      :: "memory");
+      : "r"(addr)
+      : "memory");
 }
 
 __device__ __forceinline__ float max3(float x, float y, float z) {
@@ -603,8 +597,7 @@ __device__ __forceinline__ const uint8_t *px_codes(const uint8_t *v, int row, in
   return D == 128 ? v + row * 128 + ((j ^ (row & 7)) * 16) : v + row * 64 + ((j ^ ((row >> 1) & 3)) * 16);
 }
 
-// The same in f16: 64 dims a row of 128 bytes.  The upper half's lanes store their second eight
-// first, so that the eight lanes of a store's phase meet eight groups of banks.
+// The same in f16: 64 dims a row of 128 bytes.
 template <int D>
 __device__ __forceinline__ void px_store_half(uint8_t *h, int row, int j, uint4 w) {
   const uint32_t x[4] = {w.x, w.y, w.z, w.w};
@@ -614,12 +607,10 @@ __device__ __forceinline__ void px_store_half(uint8_t *h, int row, int j, uint4 
     o[2 * q] = e4m3x2_to_f16x2(static_cast<uint16_t>(x[q] & 0xFFFFu));
     o[2 * q + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(x[q] >> 16));
   }
-  const uint4 y0 = make_uint4(o[0], o[1], o[2], o[3]), y1 = make_uint4(o[4], o[5], o[6], o[7]);
   const int c = (2 * j) & 7;
-  const bool up = D == 128 && j >= 4;
-  uint8_t *to = h + (up ? 16384 : 0) + row * 128;
-  *reinterpret_cast<uint4 *>(to + (((c + up) ^ (row & 7)) * 16)) = up ? y1 : y0;
-  *reinterpret_cast<uint4 *>(to + (((c + 1 - up) ^ (row & 7)) * 16)) = up ? y0 : y1;
+  uint8_t *to = h + (D == 128 && j >= 4 ? 16384 : 0) + row * 128;
+  *reinterpret_cast<uint4 *>(to + ((c ^ (row & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+  *reinterpret_cast<uint4 *>(to + (((c + 1) ^ (row & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 // One chunk of 32 tokens of a row's scores: the maxima of x and of x + log2 vs.
@@ -893,8 +884,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         pt = 0;
       }
       const int buf = pg & 1;
-      ok = wait(kPFull + buf, (pg >> 1) & 1) && wait(kHFull + buf, (pg >> 1) & 1) &&
-           (pt > 0 || ps == 0 || wait(kOFree, (ps - 1) & 1));
+      ok = wait(kHFull + buf, (pg >> 1) & 1) && (pt > 0 || ps == 0 || wait(kOFree, (ps - 1) & 1)) &&
+           wait(kPFull + buf, (pg >> 1) & 1);
       if (!ok) break;
       if (lane == 0) bar_arrive(bar(kScEmpty + pg % kPxScales));
       tc_after();
@@ -987,7 +978,6 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         for (int c = 0; c < D; c += 32) {
           float o[32];
           tc_ld32(o, tmem + lanes + kPxO + c);
-          tc_ld_wait(o);
           if (!has) continue;
           if (whole) {
             uint4 w[4];
@@ -1025,8 +1015,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   } else if (warp >= kPxSoft) {
     // ------------------------------------------------------ V from e4m3 to f16
     const int quad = warp & 3;
-    constexpr int kC = D / 16, kR = 32 / kC;  // chunks of 16 codes a row of V; rows a pass
-    const int row0 = 32 * quad + lane / kC, chunk = lane % kC;  // this lane's rows, kR apart, and chunk
+    // This lane's chunk of 16 codes, and rows, kR apart.  With head_dim 128 the lanes of the upper 64 dims
+    // take the neighbouring row, so that the eight lanes of a store's phase meet eight groups of banks.
+    constexpr int kC = D / 16, kR = 32 / kC;
+    const int chunk = lane % kC, row0 = (32 * quad + lane / kC) ^ (D == 128 ? chunk >> 2 : 0);
     uint32_t g = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
@@ -1044,14 +1036,28 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const uint8_t *v = smem + S::v + slot * S::kTile;
         uint8_t *h = smem + S::h + buf * S::kHalf;
         if (tok + 32 <= min_lim) {
+          // rows eight apart have the same swizzle: the addresses are two and constants
+          const uint8_t *va = px_codes<D>(v, row0, chunk), *vb = px_codes<D>(v, row0 + 4, chunk);
+          uint8_t *ha = h, *hb = h;
 #pragma unroll 1
-          for (int it = 0; it < kC; it += 4) {
-            uint4 w[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              w[q] = *reinterpret_cast<const uint4 *>(px_codes<D>(v, row0 + kR * (it + q), chunk));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) px_store_half<D>(h, row0 + kR * (it + q), chunk, w[q]);
+          for (int q = 0; q < 4; q += 2) {
+            constexpr int kS = 8 * D;
+            if constexpr (D == 128) {
+              const uint4 w0 = *reinterpret_cast<const uint4 *>(va), w1 = *reinterpret_cast<const uint4 *>(vb);
+              const uint4 w2 = *reinterpret_cast<const uint4 *>(va + kS), w3 = *reinterpret_cast<const uint4 *>(vb + kS);
+              px_store_half<D>(ha, row0, chunk, w0);
+              px_store_half<D>(hb, row0 + 4, chunk, w1);
+              px_store_half<D>(ha + 1024, row0, chunk, w2);
+              px_store_half<D>(hb + 1024, row0 + 4, chunk, w3);
+              vb += 2 * kS;
+              hb += 2048;
+            } else {
+              const uint4 w0 = *reinterpret_cast<const uint4 *>(va), w2 = *reinterpret_cast<const uint4 *>(va + kS);
+              px_store_half<D>(ha, row0, chunk, w0);
+              px_store_half<D>(ha + 1024, row0, chunk, w2);
+            }
+            va += 2 * kS;
+            ha += 2048;
           }
         } else if (tok < t_end) {
 #pragma unroll 1
@@ -1122,7 +1128,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       for (int t = first; t < tiles; t += 2) {
         const uint32_t gt = g + t;
         const int cs = gt % kPxScales, tok = tok0 + t * kPxTok;
-        ok = wait(kSFull + grp, (gt >> 1) & 1) && wait(kScFull + cs, (gt / kPxScales) & 1);
+        ok = wait(kScFull + cs, (gt / kPxScales) & 1) && wait(kSFull + grp, (gt >> 1) & 1);
         if (!ok) break;
         tc_after();
         come = t + 1;
@@ -1137,7 +1143,6 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll 1
           for (int c = half; c < chunks; c += 2) {
             tc_ld32(x, s_addr + 32 * c);
-            tc_ld_wait(x);
             if (!full) px_mask(x, lim - tok - 32 * c);
             px_max(x, sc + 2 * c, qk, mx, mv);
           }
@@ -1181,7 +1186,6 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll 1
           for (int c = half; c < chunks; c += 2) {
             tc_ld32(x, s_addr + 32 * c);
-            tc_ld_wait(x);
             if (full) {
               px_weights<false>(x, sc + 2 * c, qk, mm, mn, l2, p);
             } else {
