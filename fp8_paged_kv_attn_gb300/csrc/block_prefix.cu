@@ -405,6 +405,36 @@ __device__ __forceinline__ void tc_ld32(float (&v)[32], uint32_t addr) {
       : "memory");
 }
 
+__device__ __forceinline__ void tc_st32(uint32_t addr, const float (&v)[32]) {
+  const uint32_t *r = reinterpret_cast<const uint32_t *>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(addr)
+               : "memory");
+}
+
+// 16 columns, loaded and waited for in one statement as well.
+__device__ __forceinline__ void tc_ld16w(float (&v)[16], uint32_t addr) {
+  uint32_t *r = reinterpret_cast<uint32_t *>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
@@ -613,48 +643,39 @@ __device__ __forceinline__ void px_store_half(uint8_t *h, int row, int j, uint4 
   *reinterpret_cast<uint4 *>(to + (((c + 1) ^ (row & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// One chunk of 32 tokens of a row's scores: the maxima of x and of x + log2 vs.
-__device__ __forceinline__ void px_max(const float (&x)[32], const float4 *sc, float qk, float &mx, float &mv) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float4 b = sc[h];
-    const float *y = x + 16 * h;
-    const float u0 = max3(y[0], y[1], y[2]), u1 = max3(y[3], y[4], y[5]), u2 = max3(y[6], y[7], y[8]);
-    const float u3 = max3(y[9], y[10], y[11]), u4 = max3(y[12], y[13], y[14]);
-    const float mt = max3(max3(u0, u1, u2), fmaxf(u3, y[15]), u4);
-    const float z = mt > -INFINITY ? mt * (qk * b.x) : -INFINITY;  // (0 times -inf is no maximum)
-    mx = fmaxf(mx, z);
-    mv = fmaxf(mv, z + b.z);
-  }
+// A block of 16 tokens of a row's scores: the maxima of x and of x + log2 vs.
+__device__ __forceinline__ void px_max(const float (&y)[16], const float4 &b, float qk, float &mx, float &mv) {
+  const float u0 = max3(y[0], y[1], y[2]), u1 = max3(y[3], y[4], y[5]), u2 = max3(y[6], y[7], y[8]);
+  const float u3 = max3(y[9], y[10], y[11]), u4 = max3(y[12], y[13], y[14]);
+  const float mt = max3(max3(u0, u1, u2), fmaxf(u3, y[15]), u4);
+  const float z = mt > -INFINITY ? mt * (qk * b.x) : -INFINITY;  // (0 times -inf is no maximum)
+  mx = fmaxf(mx, z);
+  mv = fmaxf(mv, z + b.z);
 }
 
 // Its weights: e = 2^(x - m) for the sum l, and e vs 2^(m - n) 2^7 in f16.
 template <bool kMasked>
-__device__ __forceinline__ void px_weights(const float (&x)[32], const float4 *sc, float qk, float m, float mn,
-                                           float2 &l, float (&p)[16]) {
+__device__ __forceinline__ void px_weights(const float (&x)[16], const float4 &b, float qk, float m, float mn,
+                                           float2 &l, uint32_t (&p)[8]) {
+  const float f = qk * b.x, d = b.y * fast_exp2(fminf(mn + b.z, 112.f));
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float4 b = sc[h];
-    const float f = qk * b.x, d = b.y * fast_exp2(fminf(mn + b.z, 112.f));
-#pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-      float2 y = make_float2(x[16 * h + j], x[16 * h + j + 1]);
-      y = __ffma2_rn(y, make_float2(f, f), make_float2(-m, -m));
-      if (kMasked) {  // (0 times -inf is no score)
-        if (x[16 * h + j] == -INFINITY) y.x = -INFINITY;
-        if (x[16 * h + j + 1] == -INFINITY) y.y = -INFINITY;
-      }
-      const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-      l = __fadd2_rn(l, e);
-      const float2 w = __fmul2_rn(e, make_float2(d, d));
-      p[8 * h + j / 2] = __uint_as_float(f32x2_to_f16x2(w.x, w.y));
+  for (int j = 0; j < 16; j += 2) {
+    float2 y = make_float2(x[j], x[j + 1]);
+    y = __ffma2_rn(y, make_float2(f, f), make_float2(-m, -m));
+    if (kMasked) {  // (0 times -inf is no score)
+      if (x[j] == -INFINITY) y.x = -INFINITY;
+      if (x[j + 1] == -INFINITY) y.y = -INFINITY;
     }
+    const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+    l = __fadd2_rn(l, e);
+    const float2 w = __fmul2_rn(e, make_float2(d, d));
+    p[j / 2] = f32x2_to_f16x2(w.x, w.y);
   }
 }
 
-__device__ __forceinline__ void px_mask(float (&x)[32], int see) {
+__device__ __forceinline__ void px_mask(float (&x)[16], int see) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
+  for (int j = 0; j < 16; ++j)
     if (j >= see) x[j] = -INFINITY;
 }
 
@@ -827,8 +848,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     uint32_t kg = 0, pg = 0;  // tiles so far
     PxSeg ksg, psg;
     bool ok = true, k_in = false, p_in = false, k_end = false;
-    auto tokens = [](const PxSeg &sg, int t) {  // of a tile, in whole chunks of 32
-      return min(kPxTok, (sg.t_end - sg.tok - t * kPxTok + 31) & ~31);
+    auto tokens = [](const PxSeg &sg, int t) {  // of a tile, in whole blocks of 16
+      return min(kPxTok, (sg.t_end - sg.tok - t * kPxTok + 15) & ~15);
     };
     while (ok) {
       while (ok && !k_end && kg - pg < 2) {
@@ -894,7 +915,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const uint64_t vd = px_vdesc(h_a + buf * S::kHalf);
         const int steps = tokens(psg, pt) / 16;
         for (int k = 0; k < steps; ++k)  // 16 tokens: 8 columns of P, 16 rows of V
-          px_mma16(tmem + kPxO, tmem + kPxS + 128 * buf + 32 * (k >> 1) + 8 * (k & 1), vd + k * (16 * 128 >> 4), D, pt > 0 || k > 0);
+          px_mma16(tmem + kPxO, tmem + kPxS + 128 * buf + 16 * k, vd + k * (16 * 128 >> 4), D, pt > 0 || k > 0);
         bar_commit(bar(kHEmpty + buf));
         bar_commit(bar(kPvDone));
       }
@@ -1100,7 +1121,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     }
   } else {
     // ------------------------------------------------------------- softmax
-    // A row a lane, twice: `half` takes every other 32 tokens of a tile.
+    // A row a lane, twice: `half` takes every other block of 16 tokens.
     const int grp = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, r = 32 * quad + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
     const uint32_t s_addr = tmem + lanes + kPxS + 128 * grp, o_addr = tmem + lanes + kPxO + half * (D / 2);
@@ -1133,18 +1154,26 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         tc_after();
         come = t + 1;
         const float4 *sc = ctl.sc[cs];
-        float mx = -INFINITY, mv = -INFINITY, x[32];
+        float mx = -INFINITY, mv = -INFINITY, x[16];
         const bool full = tok + kPxTok <= min_lim;  // everybody sees all of it
-        const int chunks = (min(kPxTok, t_end - tok) + 31) >> 5;  // of 32 tokens
+        const int blocks = (min(kPxTok, t_end - tok) + 15) >> 4;
         if (act) {
           bad_from = min(bad_from, ctl.bad[cs]);
           // (rolled loops: with the chunks laid out one after another the roles' code did not fit the
           // instruction caches, and its fetching took twice the time of the work)
+          if (full) {
 #pragma unroll 1
-          for (int c = half; c < chunks; c += 2) {
-            tc_ld32(x, s_addr + 32 * c);
-            if (!full) px_mask(x, lim - tok - 32 * c);
-            px_max(x, sc + 2 * c, qk, mx, mv);
+            for (int c = half; c < kPxTok / 16; c += 2) {
+              tc_ld16w(x, s_addr + 16 * c);
+              px_max(x, sc[c], qk, mx, mv);
+            }
+          } else {
+#pragma unroll 1
+            for (int c = half; c < blocks; c += 2) {
+              tc_ld16w(x, s_addr + 16 * c);
+              px_mask(x, lim - tok - 16 * c);
+              px_max(x, sc[c], qk, mx, mv);
+            }
           }
           ctl.mx[grp][half][r] = make_float2(mx, mv);
         }
@@ -1182,17 +1211,22 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           const bool none = n == -INFINITY;  // nothing seen yet: every x is -inf
           const float mm = none ? 0.f : m, mn = none ? 0.f : m - n;
           float2 l2 = make_float2(0.f, 0.f);
-          float p[16];
+          uint32_t p[8];
+          if (full) {
 #pragma unroll 1
-          for (int c = half; c < chunks; c += 2) {
-            tc_ld32(x, s_addr + 32 * c);
-            if (full) {
-              px_weights<false>(x, sc + 2 * c, qk, mm, mn, l2, p);
-            } else {
-              px_mask(x, lim - tok - 32 * c);
-              px_weights<true>(x, sc + 2 * c, qk, mm, mn, l2, p);
+            for (int c = half; c < kPxTok / 16; c += 2) {
+              tc_ld16w(x, s_addr + 16 * c);
+              px_weights<false>(x, sc[c], qk, mm, mn, l2, p);
+              tc_st8(s_addr + 16 * c, p);  // in the block's own columns
             }
-            tc_st16(s_addr + 32 * c, p);  // in the chunk's own columns
+          } else {
+#pragma unroll 1
+            for (int c = half; c < blocks; c += 2) {
+              tc_ld16w(x, s_addr + 16 * c);
+              px_mask(x, lim - tok - 16 * c);
+              px_weights<true>(x, sc[c], qk, mm, mn, l2, p);
+              tc_st8(s_addr + 16 * c, p);
+            }
           }
           l += l2.x + l2.y;
           if (t > 0 && __any_sync(0xffffffffu, fo != 1.f)) {
@@ -1200,12 +1234,12 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             if (!ok) break;
             tc_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 2; c += 16) {
-              float o[16];
-              tc_ld16(o, o_addr + c);
+            for (int c = 0; c < D / 2; c += 32) {
+              float o[32];
+              tc_ld32(o, o_addr + c);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] *= fo;
-              tc_st16(o_addr + c, o);
+              for (int j = 0; j < 32; ++j) o[j] *= fo;
+              tc_st32(o_addr + c, o);
             }
           }
           tc_st_wait();
