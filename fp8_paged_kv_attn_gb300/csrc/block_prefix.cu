@@ -8,6 +8,7 @@
 #include "decode_common.cuh"
 #include "decode_attn_mma.cuh"
 #include "tc_device.cuh"
+#include "block_attn_split.cuh"
 
 namespace kvq {
 
@@ -16,8 +17,8 @@ struct PfArgs {
   int64_t q_stride;
   uint8_t *qp;    // [n_tokens][Hq][2][D]: q's two pieces
   float *qk;      // [n_tokens][Hq]: what undoes their scale, times |sm_scale| log2(e)
-  struct PxPlan *plan;
-  struct PxItem *items;  // [2 n_tokens]: groups' prefixes, then requests
+  PxPlan *plan;
+  PxItem *items;         // [2 n_tokens]: groups' prefixes, then requests
   int64_t *units;        // [2 n_tokens + 1]: units before each item
   Ragged rg;
   const int32_t *block_table, *group_start, *prefix_pages;
@@ -28,6 +29,9 @@ struct PfArgs {
   uint16_t *out;
   uint32_t *err_word;
   int32_t num_pages, p_shift, Hkv, Hq, G, MP, max_q, n_groups;
+  int32_t own_split;  // own tokens are attended to by the mma.sync kernel; its shape:
+  int32_t hg, rt, rk;
+  const float *own_cut;
   float q_scale;  // sm_scale * log2(e)
 };
 
@@ -94,32 +98,11 @@ constexpr int kPxSegs = 8;          // segment descriptors in flight
 constexpr int kPxStats = 4;         // segments whose statistics are in flight
 constexpr int kPxScales = 8;        // tiles whose scales are in flight
 constexpr int kPxK = 4, kPxV = 4;   // tiles of K and of V in flight
-constexpr int kStat = 4;            // floats behind a row's sums
-// a row's fourth statistic: its sums lie here, in the parts of several CTAs, or it is written
-constexpr float kHere = 1.f, kCut = 2.f, kDone = 3.f;
 // warps: softmax (two groups of eight), V's conversion, edges (q in, sums out); then MMAs, copies of K,
 // of V, scales
 constexpr int kPxSoft = 16, kPxConv = 4, kPxEdge = 4;
 constexpr int kPxMma = kPxSoft + kPxConv + kPxEdge, kPxThreads = 32 * (kPxMma + 4);
 constexpr float kPxFar = 64.f;      // how far the denominator's reference may be off (fp32)
-
-// An item: the prefix of a group for all its rows, or a request's own tokens for its rows.
-struct __align__(16) PxItem {
-  int b;           // whose block table
-  int row0, n;     // token rows
-  int rows;        // rows: token rows times heads a kv head
-  int first, end;  // tokens [first, end)
-  int p0;          // position of its first row (own tokens)
-  int nb;          // blocks of rows
-  int own, pre;    // pre: own tokens behind a prefix
-  int live;        // 0: a request whose rows are zeros
-  int row_pre;     // the first row of its group
-};
-
-struct PxPlan {
-  int64_t total, per;  // units, and units a CTA
-  int n_grp, n_req;    // items
-};
 
 // Where the tokens end that block rb of an item sees.
 __device__ __forceinline__ int px_end(const PfArgs &a, const PxItem &it, int rb) {
@@ -161,18 +144,9 @@ struct PxWalk {
   PxItem it;
 };
 
-__device__ __forceinline__ PxItem px_load_item(const PfArgs &a, int i) {
-  PxItem o;
-  const int4 *p = reinterpret_cast<const int4 *>(a.items + i);
-  int4 *q = reinterpret_cast<int4 *>(&o);
-#pragma unroll
-  for (int k = 0; k < 3; ++k) q[k] = __ldcg(p + k);
-  return o;
-}
-
 // in: the unit of item w.i that the run begins with.
 __device__ __forceinline__ void px_start(const PfArgs &a, PxWalk &w, int64_t in) {
-  w.it = px_load_item(a, w.i);
+  w.it = px_load_item(a.items + w.i);
   const int64_t units = px_units(a, w.it);
   w.head = static_cast<int>(px_div(in, units));  // row of work: head major
   int64_t s = in - w.head * units;
@@ -196,8 +170,8 @@ __device__ __noinline__ bool px_next(const PfArgs &a, PxWalk &w, PxSeg &sg) {
     if (w.head == a.Hkv) {
       do {
         if (++w.i >= w.n) return false;
-        w.it = px_load_item(a, w.i);
-      } while (!w.it.live);
+        w.it = px_load_item(a.items + w.i);
+      } while (!w.it.live || (w.it.own && a.own_split));
       w.head = w.rb = w.at = 0;
       w.tiles = px_tiles(a, w.it, 0);
     }
@@ -529,7 +503,7 @@ __device__ __forceinline__ void px_plan(const PfArgs &a, int ctas) {
     }
     o.rows = o.n * a.G;
     o.nb = (o.rows + kPxRows - 1) / kPxRows;
-    const int64_t u = has ? px_units(a, o) * a.Hkv : 0;
+    const int64_t u = has && (grp || !a.own_split) ? px_units(a, o) * a.Hkv : 0;
     int64_t n_all, u_all;
     const int64_t at = count + px_scan(has, warps, &n_all);
     const int64_t before = units + px_scan(u, warps, &u_all);
@@ -1282,7 +1256,7 @@ __global__ void __launch_bounds__(32 * kPxMergeWarps) prefix_merge_kernel(PfArgs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // (the kernel ahead began, and let this one start, when the plan was complete)
   const int n_grp = __ldcg(&a.plan->n_grp), n_req = __ldcg(&a.plan->n_req);
-  const PxItem it = px_load_item(a, n_grp + min(static_cast<int>(blockIdx.x), max(n_req - 1, 0)));
+  const PxItem it = px_load_item(a.items + n_grp + min(static_cast<int>(blockIdx.x), max(n_req - 1, 0)));
   grid_dependency_wait();
   allow_dependents();
   if (static_cast<int>(blockIdx.x) >= n_req) return;
@@ -1311,9 +1285,16 @@ __global__ void __launch_bounds__(32 * kPxMergeWarps) prefix_merge_kernel(PfArgs
       // part p lies in the p-th CTA from here on: the first in slot 1, others in slot 0
       const bool cut = e.w == kCut;
       const int parts = cut ? __float_as_int(e.y) : 1;
-      const int r = ((it.row0 + i - (own ? it.row0 : it.row_pre)) * a.G + h % a.G) % kPxRows;
-      const float *base = cut ? a.cut + (static_cast<int64_t>(2 * __float_as_int(e.x)) * kPxRows + r) * RF
-                              : own ? own_rows : rows;
+      const int row = (it.row0 + i - (own ? it.row0 : it.row_pre)) * a.G + h % a.G;
+      const float *base = own ? own_rows : rows;
+      int64_t slot = kPxRows;  // rows of a part's slot
+      if (cut && own && a.own_split) {
+        const int in = row % (a.rt * a.rk), kvh = h / a.G;
+        slot = a.hg * a.rt * a.rk;
+        base = a.own_cut + (2 * __float_as_int(e.x) * slot + (kvh % a.hg * a.rt + in / a.rk) * a.rk + in % a.rk) * RF;
+      } else if (cut) {
+        base = a.cut + (static_cast<int64_t>(2 * __float_as_int(e.x)) * kPxRows + row % kPxRows) * RF;
+      }
       for (int p0 = 0; p0 < parts; p0 += kBatch) {
         float4 s[kBatch];
         float v[kBatch][V];
@@ -1321,7 +1302,7 @@ __global__ void __launch_bounds__(32 * kPxMergeWarps) prefix_merge_kernel(PfArgs
         for (int j = 0; j < kBatch; ++j) {
           s[j] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
           if (p0 + j < parts) {
-            const float *q = base + (cut ? static_cast<int64_t>(2 * (p0 + j) + (p0 + j == 0)) * kPxRows * RF : 0);
+            const float *q = base + (cut ? (2 * (p0 + j) + (p0 + j == 0)) * slot * RF : 0);
             s[j] = __ldcg(reinterpret_cast<const float4 *>(q + D));
             if constexpr (V == 4) {
               const float4 x = __ldcg(reinterpret_cast<const float4 *>(q) + lane);
@@ -1384,17 +1365,19 @@ size_t px_qk_bytes(int64_t n_tokens, int Hq) { return px_up256(4ull * n_tokens *
 size_t px_plan_bytes(int64_t n_tokens) {
   return 256 + px_up256(2 * n_tokens * sizeof(PxItem)) + px_up256((2 * n_tokens + 1) * sizeof(int64_t));
 }
-size_t px_bytes(int64_t n_tokens, int Hq, int D, int ctas) {
-  return px_plan_bytes(n_tokens) + px_rows_bytes(n_tokens, Hq, D) + px_cut_bytes(ctas, D) +
+size_t px_own_cut_bytes(int Hq, int Hkv, int D, int ctas);
+size_t px_bytes(int64_t n_tokens, int Hq, int Hkv, int D, int ctas) {
+  return px_own_cut_bytes(Hq, Hkv, D, ctas) + px_plan_bytes(n_tokens) + px_rows_bytes(n_tokens, Hq, D) + px_cut_bytes(ctas, D) +
          px_q_bytes(n_tokens, Hq, D) + px_qk_bytes(n_tokens, Hq);
 }
 
 using PxFn = void (*)(CUtensorMap, CUtensorMap, PfArgs);
 
 // Opt the kernel into its shared memory, once per device.
-bool px_opt_in(PxFn fn, int variant, size_t smem) {
+template <typename Fn>
+bool px_opt_in(Fn fn, int variant, size_t smem) {
   constexpr int kMaxDev = 64;
-  static std::atomic<bool> done[kMaxDev][2];
+  static std::atomic<bool> done[kMaxDev][6];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return false;
   if (done[dev][variant].load(std::memory_order_acquire)) return true;
@@ -1404,18 +1387,38 @@ bool px_opt_in(PxFn fn, int variant, size_t smem) {
   return true;
 }
 
-// [page][head][slot][dim] as a 4-D map; a box is one head's page.
-bool px_map(CUtensorMap *map, const void *pool, const kvq_block_cache &c) {
+// [page][head][slot][dim] as a 4-D map; a box is `slots` slots of `heads` heads.
+bool px_map(CUtensorMap *map, const void *pool, const kvq_block_cache &c, int slots, int heads) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t D = c.head_dim, P = c.page_size, H = c.num_kv_heads, NP = c.num_pages;
   const cuuint64_t dims[4] = {D, P, H, NP};
   const cuuint64_t strides[3] = {D, P * D, H * P * D};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(P), 1, 1};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(slots),
+                             static_cast<cuuint32_t>(heads), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(pool), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Own tokens: the mma.sync kernel where a request has few rows.
+using BaFn = void (*)(CUtensorMap, CUtensorMap, BaArgs);
+
+template <int D>
+BaFn px_own_kernel(int rk) {
+  return rk == 4 ? block_split_kernel<D, 4, true>
+                 : rk == 8 ? block_split_kernel<D, 8, true> : block_split_kernel<D, 16, true>;
+}
+
+constexpr int kPxOwnRows = 16;  // rows (times heads a kv head) of a request that it takes
+
+// The slots of its parts, for every number of rows that a call may allow.
+size_t px_own_cut_bytes(int Hq, int Hkv, int D, int ctas) {
+  size_t most = 0;
+  for (int rows : {4, 8, 16})
+    if (rows >= Hq / Hkv) most = std::max(most, ba_part_bytes(ba_shape(rows, 1, Hkv, D, 0), D, ctas));
+  return px_up256(most);
 }
 
 }  // namespace
@@ -1430,7 +1433,7 @@ extern "C" size_t kvq_block_prefix_attn_workspace_size(int32_t n_tokens, int32_t
   if (head_dim != 64 && head_dim != 128) return 0;
   int sms = 0;
   if (device_sm_count(&sms) != KVQ_OK) return 0;
-  return px_bytes(n_tokens, Hq, head_dim, sms);
+  return px_bytes(n_tokens, Hq, num_kv_heads, head_dim, sms);
 }
 
 extern "C" kvq_status kvq_block_prefix_attn(
@@ -1454,7 +1457,7 @@ extern "C" kvq_status kvq_block_prefix_attn(
   if (n_groups > 0 && (!group_start || !prefix_pages)) return KVQ_ERR_INVALID_ARG;
   int sms = 0;
   if (device_sm_count(&sms) != KVQ_OK) return KVQ_ERR_CUDA;
-  if (!aligned256(workspace) || workspace_bytes < px_bytes(n_tokens, Hq, D, sms)) return KVQ_ERR_WORKSPACE;
+  if (!aligned256(workspace) || workspace_bytes < px_bytes(n_tokens, Hq, Hkv, D, sms)) return KVQ_ERR_WORKSPACE;
   PfArgs a;
   a.q = static_cast<const uint16_t *>(q);
   a.q_stride = q_stride;
@@ -1473,7 +1476,15 @@ extern "C" kvq_status kvq_block_prefix_attn(
   a.cut = reinterpret_cast<float *>(at);
   at += px_cut_bytes(sms, D);
   a.qp = at;
-  a.qk = reinterpret_cast<float *>(at + px_q_bytes(n_tokens, Hq, D));
+  at += px_q_bytes(n_tokens, Hq, D);
+  a.qk = reinterpret_cast<float *>(at);
+  at += px_qk_bytes(n_tokens, Hq);
+  const BaShape shape = ba_shape(max_q, G, Hkv, D, 0);
+  a.own_split = static_cast<int64_t>(max_q) * G <= kPxOwnRows;
+  a.hg = shape.hg;
+  a.rt = shape.rt;
+  a.rk = shape.rk;
+  a.own_cut = reinterpret_cast<float *>(at);
   a.scales = reinterpret_cast<const float2 *>(cache->scales);
   a.out = static_cast<uint16_t *>(out);
   a.err_word = err_word;
@@ -1490,13 +1501,49 @@ extern "C" kvq_status kvq_block_prefix_attn(
   const size_t smem = D == 128 ? PxSmem<128>::bytes : PxSmem<64>::bytes;
   if (!px_opt_in(fn, D == 128, smem)) return KVQ_ERR_CUDA;
   CUtensorMap kmap, vmap;
-  if (!px_map(&kmap, cache->k_pool, *cache) || !px_map(&vmap, cache->v_pool, *cache)) return KVQ_ERR_CUDA;
+  if (!px_map(&kmap, cache->k_pool, *cache, cache->page_size, 1) ||
+      !px_map(&vmap, cache->v_pool, *cache, cache->page_size, 1))
+    return KVQ_ERR_CUDA;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const int64_t q_ctas = (static_cast<int64_t>(n_tokens) * Hq * (D / 4) + kPxQThreads - 1) / kPxQThreads;
   if (launch_dependent(D == 128 ? prefix_plan_kernel<128> : prefix_plan_kernel<64>, static_cast<unsigned>(1 + q_ctas),
                        kPxQThreads, 0, cs, a, sms) != cudaSuccess)
     return KVQ_ERR_CUDA;
   if (launch_dependent(fn, sms, kPxThreads, smem, cs, kmap, vmap, a) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (a.own_split) {
+    BaArgs o = {};
+    o.q = a.q;
+    o.q_stride = q_stride;
+    o.rg = a.rg;
+    o.block_table = block_table;
+    o.scales = a.scales;
+    o.part = reinterpret_cast<float *>(at);
+    o.err_word = err_word;
+    o.num_pages = a.num_pages;
+    o.p_shift = a.p_shift;
+    o.Hkv = Hkv;
+    o.Hq = Hq;
+    o.G = G;
+    o.MP = MP;
+    o.max_q = max_q;
+    o.hg = shape.hg;
+    o.rt = shape.rt;
+    o.tw = shape.tw;
+    for (int t = shape.tw; t > 1; t = (t + 1) / 2) ++o.rounds;
+    o.groups = shape.groups;
+    o.stages = ba_stages(shape, D);
+    o.q_scale = a.q_scale;
+    o.plan = a.plan;
+    o.items = a.items;
+    o.rows = a.rows;
+    const BaFn own = D == 128 ? px_own_kernel<128>(shape.rk) : px_own_kernel<64>(shape.rk);
+    const int variant = shape.rk == 4 ? 0 : shape.rk == 8 ? 1 : 2;
+    if (!(D == 128 ? px_opt_in<BaFn>(own, 3 + variant, kBaSmem) : px_opt_in<BaFn>(own, variant, kBaSmem)))
+      return KVQ_ERR_CUDA;
+    if (!px_map(&kmap, cache->k_pool, *cache, kTile, shape.hg) || !px_map(&vmap, cache->v_pool, *cache, kTile, shape.hg))
+      return KVQ_ERR_CUDA;
+    if (launch_dependent(own, sms, kBaThreads, kBaSmem, cs, kmap, vmap, o) != cudaSuccess) return KVQ_ERR_CUDA;
+  }
   // a warp a row and head, up to 64 CTAs a request
   const int64_t most = (static_cast<int64_t>(std::min(max_q, n_tokens)) * Hq + kPxMergeWarps - 1) / kPxMergeWarps;
   const dim3 grid(static_cast<unsigned>(std::min(B, n_tokens)), static_cast<unsigned>(std::min<int64_t>(64, most)));
