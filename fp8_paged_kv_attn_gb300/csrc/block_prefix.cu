@@ -98,10 +98,10 @@ constexpr int kPxSegs = 8;          // segment descriptors in flight
 constexpr int kPxStats = 4;         // segments whose statistics are in flight
 constexpr int kPxScales = 8;        // tiles whose scales are in flight
 constexpr int kPxK = 4, kPxV = 4;   // tiles of K and of V in flight
-// warps: softmax (two groups of eight), V's conversion, edges (q in, sums out); then MMAs, copies of K,
+// warps: softmax (two groups of four), sides (q in, V's conversion, sums out); then MMAs, copies of K,
 // of V, scales
-constexpr int kPxSoft = 16, kPxConv = 4, kPxEdge = 4;
-constexpr int kPxMma = kPxSoft + kPxConv + kPxEdge, kPxThreads = 32 * (kPxMma + 4);
+constexpr int kPxSoft = 8, kPxSide = 4;
+constexpr int kPxMma = kPxSoft + kPxSide, kPxThreads = 32 * (kPxMma + 4);
 constexpr float kPxFar = 64.f;      // how far the denominator's reference may be off (fp32)
 
 // Where the tokens end that block rb of an item sees.
@@ -213,7 +213,7 @@ __device__ __noinline__ bool px_next(const PfArgs &a, PxWalk &w, PxSeg &sg) {
 // shared memory and tcgen05
 // ---------------------------------------------------------------------------
 
-// Barriers, those that expect as many arrivals together: 1, 2, 4, 8, 20, 26.
+// Barriers, those that expect as many arrivals together: 1, 4, 12, 14.
 enum : int {
   kKFull = 0,
   kKEmpty = kKFull + kPxK,
@@ -227,29 +227,26 @@ enum : int {
   kPvDone = kHEmpty + 2,
   kODone,
   kDrain,
-  kPair,  // [group][quarter of the rows]: two warps each
-  kRef = kPair + 8,
+  kRef,  // [group][quarter of the rows]
   kVEmpty = kRef + 8,  // four warps each from here
   kQFull = kVEmpty + kPxV,
   kQReady = kQFull + 2,
   kHFull = kQReady + kPxStats,
   kOFree = kHFull + 2,
-  kPFull,  // a group
-  kStatFull = kPFull + 2,  // softmax and conversion
+  kPHalf,  // a group's weights for the first 64 tokens of a tile
+  kPFull = kPHalf + 2,
+  kStatFull = kPFull + 2,  // softmax and sides
   kSegEmpty = kStatFull + kPxStats,  // everybody but the copies
   kBars = kSegEmpty + kPxSegs
 };
 
 __device__ __forceinline__ int px_arrivals(int bar) {
-  return bar < kPair ? 1 : bar < kVEmpty ? 2 : bar < kPFull ? 4 : bar < kStatFull ? 8
-         : bar < kSegEmpty ? kPxSoft + kPxConv : kPxMma + 2;
+  return bar < kVEmpty ? 1 : bar < kStatFull ? 4 : bar < kSegEmpty ? kPxSoft + kPxSide : kPxMma + 2;
 }
 
 struct PxCtl {
   float4 sc[kPxScales][kPxTok / 16];  // of a tile's blocks: K scale; V scale's fraction times 2^7, exponent
-  float2 end_mn[kPxStats][2][kPxRows];   // [segment][group]: m that its l stands on, n
-  float end_l[kPxStats][2][2][kPxRows];  // [segment][group][half]
-  float2 mx[2][2][kPxRows];           // [group][half]: a tile's maxima of x and x + log2 vs
+  float4 end[kPxStats][2][kPxRows];   // [segment][group]: m that its l stands on, l, n, -
   float2 now[2][kPxRows];             // [group]: (m, n), a row's references
   float qk[kPxStats][kPxRows];
   unsigned long long nan_from[kPxStats][128];  // per dim: px_nan of a token with a NaN code that some row
@@ -617,39 +614,47 @@ __device__ __forceinline__ void px_store_half(uint8_t *h, int row, int j, uint4 
   *reinterpret_cast<uint4 *>(to + (((c + 1) ^ (row & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// A block of 16 tokens of a row's scores: the maxima of x and of x + log2 vs.
-__device__ __forceinline__ void px_max(const float (&y)[16], const float4 &b, float qk, float &mx, float &mv) {
-  const float u0 = max3(y[0], y[1], y[2]), u1 = max3(y[3], y[4], y[5]), u2 = max3(y[6], y[7], y[8]);
-  const float u3 = max3(y[9], y[10], y[11]), u4 = max3(y[12], y[13], y[14]);
-  const float mt = max3(max3(u0, u1, u2), fmaxf(u3, y[15]), u4);
-  const float z = mt > -INFINITY ? mt * (qk * b.x) : -INFINITY;  // (0 times -inf is no maximum)
-  mx = fmaxf(mx, z);
-  mv = fmaxf(mv, z + b.z);
+// A chunk of 32 tokens of a row's scores: the maxima of x and of x + log2 vs.
+__device__ __forceinline__ void px_max(const float (&x)[32], const float4 *sc, float qk, float &mx, float &mv) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float4 b = sc[h];
+    const float *y = x + 16 * h;
+    const float u0 = max3(y[0], y[1], y[2]), u1 = max3(y[3], y[4], y[5]), u2 = max3(y[6], y[7], y[8]);
+    const float u3 = max3(y[9], y[10], y[11]), u4 = max3(y[12], y[13], y[14]);
+    const float z = max3(max3(u0, u1, u2), fmaxf(u3, y[15]), u4) * (qk * b.x);  // (0 times -inf: no maximum)
+    mx = fmaxf(mx, z);
+    mv = fmaxf(mv, z + b.z);
+  }
 }
 
 // Its weights: e = 2^(x - m) for the sum l, and e vs 2^(m - n) 2^7 in f16.
 template <bool kMasked>
-__device__ __forceinline__ void px_weights(const float (&x)[16], const float4 &b, float qk, float m, float mn,
-                                           float2 &l, uint32_t (&p)[8]) {
-  const float f = qk * b.x, d = b.y * fast_exp2(fminf(mn + b.z, 112.f));
+__device__ __forceinline__ void px_weights(const float (&x)[32], const float4 *sc, float qk, float m, float mn,
+                                           float2 (&l)[2], float (&p)[16]) {
 #pragma unroll
-  for (int j = 0; j < 16; j += 2) {
-    float2 y = make_float2(x[j], x[j + 1]);
-    y = __ffma2_rn(y, make_float2(f, f), make_float2(-m, -m));
-    if (kMasked) {  // (0 times -inf is no score)
-      if (x[j] == -INFINITY) y.x = -INFINITY;
-      if (x[j + 1] == -INFINITY) y.y = -INFINITY;
+  for (int h = 0; h < 2; ++h) {
+    const float4 b = sc[h];
+    const float f = qk * b.x, d = b.y * fast_exp2(fminf(mn + b.z, 112.f));
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      float2 y = make_float2(x[16 * h + j], x[16 * h + j + 1]);
+      y = __ffma2_rn(y, make_float2(f, f), make_float2(-m, -m));
+      if (kMasked) {  // (0 times -inf is no score)
+        if (x[16 * h + j] == -INFINITY) y.x = -INFINITY;
+        if (x[16 * h + j + 1] == -INFINITY) y.y = -INFINITY;
+      }
+      const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+      l[h] = __fadd2_rn(l[h], e);
+      const float2 w = __fmul2_rn(e, make_float2(d, d));
+      p[8 * h + j / 2] = __uint_as_float(f32x2_to_f16x2(w.x, w.y));
     }
-    const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-    l = __fadd2_rn(l, e);
-    const float2 w = __fmul2_rn(e, make_float2(d, d));
-    p[j / 2] = f32x2_to_f16x2(w.x, w.y);
   }
 }
 
-__device__ __forceinline__ void px_mask(float (&x)[16], int see) {
+__device__ __forceinline__ void px_mask(float (&x)[32], int see) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
+  for (int j = 0; j < 32; ++j)
     if (j >= see) x[j] = -INFINITY;
 }
 
@@ -822,8 +827,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     uint32_t kg = 0, pg = 0;  // tiles so far
     PxSeg ksg, psg;
     bool ok = true, k_in = false, p_in = false, k_end = false;
-    auto tokens = [](const PxSeg &sg, int t) {  // of a tile, in whole blocks of 16
-      return min(kPxTok, (sg.t_end - sg.tok - t * kPxTok + 15) & ~15);
+    auto tokens = [](const PxSeg &sg, int t) {  // of a tile, in whole chunks of 32
+      return min(kPxTok, (sg.t_end - sg.tok - t * kPxTok + 31) & ~31);
     };
     while (ok) {
       while (ok && !k_end && kg - pg < 2) {
@@ -880,16 +885,25 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       }
       const int buf = pg & 1;
       ok = wait(kHFull + buf, (pg >> 1) & 1) && (pt > 0 || ps == 0 || wait(kOFree, (ps - 1) & 1)) &&
-           wait(kPFull + buf, (pg >> 1) & 1);
+           wait(kPHalf + buf, (pg >> 1) & 1);
+      if (!ok) break;
+      tc_after();
+      const bool last = pt + 1 == psg.tiles;
+      // 16 tokens a step: 8 columns of P, 16 rows of V; the first four while the others' weights are made
+      const int steps = tokens(psg, pt) / 16;
+      const uint64_t vd = px_vdesc(h_a + buf * S::kHalf);
+      if (elect_one())
+        for (int k = 0; k < min(steps, 4); ++k)
+          px_mma16(tmem + kPxO, tmem + kPxS + 128 * buf + 32 * (k >> 1) + 8 * (k & 1), vd + k * (16 * 128 >> 4), D,
+                   pt > 0 || k > 0);
+      __syncwarp();
+      ok = wait(kPFull + buf, (pg >> 1) & 1);
       if (!ok) break;
       if (lane == 0) bar_arrive(bar(kScEmpty + pg % kPxScales));
       tc_after();
-      const bool last = pt + 1 == psg.tiles;
       if (elect_one()) {
-        const uint64_t vd = px_vdesc(h_a + buf * S::kHalf);
-        const int steps = tokens(psg, pt) / 16;
-        for (int k = 0; k < steps; ++k)  // 16 tokens: 8 columns of P, 16 rows of V
-          px_mma16(tmem + kPxO, tmem + kPxS + 128 * buf + 16 * k, vd + k * (16 * 128 >> 4), D, pt > 0 || k > 0);
+        for (int k = 4; k < steps; ++k)
+          px_mma16(tmem + kPxO, tmem + kPxS + 128 * buf + 32 * (k >> 1) + 8 * (k & 1), vd + k * (16 * 128 >> 4), D, true);
         bar_commit(bar(kHEmpty + buf));
         bar_commit(bar(kPvDone));
       }
@@ -909,50 +923,27 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       if (elect_one()) bar_commit(bar(kDrain));
       mbar_wait(&ctl.bar[kDrain], 0);
     }
-  } else if (warp >= kPxSoft + kPxConv) {
-    // ----- edges: q in; sums out, to the output, or with their statistics to where the merge finds them
+  } else if (warp >= kPxSoft) {
+    // ---------- sides: q in; V from e4m3 to f16; sums out, to the output or to where the merge finds them
     const int quad = warp & 3, r = 32 * quad + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-    bool ok = true;
-    for (uint32_t j = 0; ok; ++j) {  // segment j's q, then the sums of the one before
-      ok = wait(kSegFull + j % kPxSegs, (j / kPxSegs) & 1);
-      if (!ok) break;
-      const PxSeg &next = ctl.seg[j % kPxSegs];
-      const bool ended = next.b < 0;
-      if (!ended) {
-        ok = j < 2 || wait(kQFree + (j & 1), ((j >> 1) - 1) & 1);
-        if (!ok) break;
-        tc_after();
-        if (32 * quad < next.rows) {
-          px_load_q<D>(a, next, tmem + lanes + kPxQ + (j & 1) * (D / 2), ctl.qk[j % kPxStats], r);
-          tc_st_wait();
-        }
-        tc_before();
-        __syncwarp();
-        if (lane == 0) {
-          bar_arrive(bar(kQFull + (j & 1)));
-          bar_arrive(bar(kQReady + j % kPxStats));
-        }
-      }
-      if (j == 0) {
-        if (ended) break;
-        continue;
-      }
-      const uint32_t k = j - 1;
+    // This lane's chunk of 16 codes, and rows, kR apart.  With head_dim 128 the lanes of the upper 64 dims
+    // take the neighbouring row, so that the eight lanes of a store's phase meet eight groups of banks.
+    constexpr int kC = D / 16, kR = 32 / kC;
+    const int chunk = lane % kC, row0 = (32 * quad + lane / kC) ^ (D == 128 ? chunk >> 2 : 0);
+    auto px_put = [&](uint32_t k) -> bool {  // segment k's sums
       const int ss = k % kPxSegs, ks = k % kPxStats;
       const PxSeg &sg = ctl.seg[ss];
-      ok = wait(kStatFull + ks, (k / kPxStats) & 1) && wait(kODone, k & 1);
-      if (!ok) break;
+      if (!wait(kStatFull + ks, (k / kPxStats) & 1) || !wait(kODone, k & 1)) return false;
       tc_after();
       if (32 * quad < sg.rows) {
         const int row = sg.rb * kPxRows + r, i = row / a.G;
         const int fin = ctl.come[ks][1] > ctl.come[ks][0];  // who had the last tile
-        const float M = ctl.end_mn[ks][fin][r].x, N = ctl.end_mn[ks][fin][r].y;
-        const float l0 = ctl.end_l[ks][fin][0][r], l1 = ctl.end_l[ks][fin][1][r];
-        const float l2 = ctl.end_l[ks][fin ^ 1][0][r], l3 = ctl.end_l[ks][fin ^ 1][1][r];
-        const bool bad = l0 < 0.f || l1 < 0.f || l2 < 0.f || l3 < 0.f;
-        float l = l0 + l1;
-        if (l2 + l3 != 0.f) l += (l2 + l3) * exp2f(ctl.end_mn[ks][fin ^ 1][r].x - M);
+        const float4 e0 = ctl.end[ks][fin][r], e1 = ctl.end[ks][fin ^ 1][r];
+        const float M = e0.x, N = e0.z;
+        const bool bad = e0.y < 0.f || e1.y < 0.f;
+        float l = e0.y;
+        if (e1.y != 0.f) l += e1.y * exp2f(e1.x - M);
         if (bad) l = -1.f;
         const bool whole = sg.part < 0 && sg.own && !sg.pre;  // nothing to be merged with
         const int64_t at = (static_cast<int64_t>(sg.row0) + i) * a.Hq + sg.head * a.G + row - i * a.G;
@@ -1005,102 +996,113 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         bar_arrive(bar(kOFree));
         bar_arrive(bar(kSegEmpty + ss));
       }
-      if (ended) break;
-    }
-  } else if (warp >= kPxSoft) {
-    // ------------------------------------------------------ V from e4m3 to f16
-    const int quad = warp & 3;
-    // This lane's chunk of 16 codes, and rows, kR apart.  With head_dim 128 the lanes of the upper 64 dims
-    // take the neighbouring row, so that the eight lanes of a store's phase meet eight groups of banks.
-    constexpr int kC = D / 16, kR = 32 / kC;
-    const int chunk = lane % kC, row0 = (32 * quad + lane / kC) ^ (D == 128 ? chunk >> 2 : 0);
+      return true;
+    };
     uint32_t g = 0;
     bool ok = true;
-    for (uint32_t k = 0; ok; ++k) {
+    for (uint32_t k = 0; ok; ++k) {  // segment k's q and first tile of V, the sums of the one before, the rest
       const int ss = k % kPxSegs;
       ok = wait(kSegFull + ss, (k / kPxSegs) & 1);
       if (!ok) break;
-      const PxSeg &sg = ctl.seg[ss];
-      if (sg.b < 0) break;
-      const int tiles = sg.tiles, t_end = sg.t_end, tok0 = sg.tok;
-      const int min_lim = sg.lim0 ? min(t_end, sg.lim0 + sg.rb * kPxRows / a.G) : t_end;
-      for (int t = 0; t < tiles; ++t, ++g) {
-        const int slot = g % kPxV, buf = g & 1, tok = tok0 + t * kPxTok + 32 * quad;
-        ok = wait(kVFull + slot, (g / kPxV) & 1) && wait(kHEmpty + buf, ((g >> 1) & 1) ^ 1);
+      const PxSeg &next = ctl.seg[ss];
+      const bool ended = next.b < 0;
+      const int tiles = ended ? 0 : next.tiles, t_end = next.t_end, tok0 = next.tok;
+      const int min_lim = next.lim0 ? min(t_end, next.lim0 + next.rb * kPxRows / a.G) : t_end;
+      if (!ended) {
+        ok = k < 2 || wait(kQFree + (k & 1), ((k >> 1) - 1) & 1);
         if (!ok) break;
-        const uint8_t *v = smem + S::v + slot * S::kTile;
-        uint8_t *h = smem + S::h + buf * S::kHalf;
-        if (tok + 32 <= min_lim) {
-          // rows eight apart have the same swizzle: the addresses are two and constants
-          const uint8_t *va = px_codes<D>(v, row0, chunk), *vb = px_codes<D>(v, row0 + 4, chunk);
-          uint8_t *ha = h, *hb = h;
-#pragma unroll 1
-          for (int q = 0; q < 4; q += 2) {
-            constexpr int kS = 8 * D;
-            if constexpr (D == 128) {
-              const uint4 w0 = *reinterpret_cast<const uint4 *>(va), w1 = *reinterpret_cast<const uint4 *>(vb);
-              const uint4 w2 = *reinterpret_cast<const uint4 *>(va + kS), w3 = *reinterpret_cast<const uint4 *>(vb + kS);
-              px_store_half<D>(ha, row0, chunk, w0);
-              px_store_half<D>(hb, row0 + 4, chunk, w1);
-              px_store_half<D>(ha + 1024, row0, chunk, w2);
-              px_store_half<D>(hb + 1024, row0 + 4, chunk, w3);
-              vb += 2 * kS;
-              hb += 2048;
-            } else {
-              const uint4 w0 = *reinterpret_cast<const uint4 *>(va), w2 = *reinterpret_cast<const uint4 *>(va + kS);
-              px_store_half<D>(ha, row0, chunk, w0);
-              px_store_half<D>(ha + 1024, row0, chunk, w2);
-            }
-            va += 2 * kS;
-            ha += 2048;
-          }
-        } else if (tok < t_end) {
-#pragma unroll 1
-          for (int it = 0; it < kC; ++it) {
-            const int row = row0 + kR * it, tk = tok + row - 32 * quad;
-            uint4 w = *reinterpret_cast<const uint4 *>(px_codes<D>(v, row, chunk));
-            uint32_t *x = reinterpret_cast<uint32_t *>(&w);
-            if (tk >= t_end) {
-              w = make_uint4(0, 0, 0, 0);  // cached bytes behind may be anything
-            } else if (tk >= min_lim) {
-              // a weight of 0 does not stop a NaN: it is put where its rows are written
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                uint32_t nan = nan_codes(x[q]);
-                x[q] &= ~((nan >> 7) * 0xFFu);
-                while (nan) {
-                  const int byte = (__ffs(nan) - 1) >> 3;
-                  nan &= nan - 1;
-                  atomicMin(&ctl.nan_from[k % kPxStats][16 * chunk + 4 * q + byte], px_nan(k, tk));
-                  ctl.nan_seg[k % kPxStats] = static_cast<int>(k) + 1;
-                }
-              }
-            }
-            px_store_half<D>(h, row, chunk, w);
-          }
+        tc_after();
+        if (32 * quad < next.rows) {
+          px_load_q<D>(a, next, tmem + lanes + kPxQ + (k & 1) * (D / 2), ctl.qk[k % kPxStats], r);
+          tc_st_wait();
         }
-        proxy_fence();
+        tc_before();
         __syncwarp();
         if (lane == 0) {
-          bar_arrive(bar(kVEmpty + slot));
-          bar_arrive(bar(kHFull + buf));
+          bar_arrive(bar(kQFull + (k & 1)));
+          bar_arrive(bar(kQReady + k % kPxStats));
         }
       }
-      if (!ok) break;
-      __syncwarp();
-      if (lane == 0) {
-        bar_arrive(bar(kStatFull + k % kPxStats));
-        bar_arrive(bar(kSegEmpty + ss));
+      for (int t = 0; t < max(tiles, 1); ++t) {
+        if (t < tiles) {
+          const int slot = g % kPxV, buf = g & 1, tok = tok0 + t * kPxTok + 32 * quad;
+          ok = wait(kVFull + slot, (g / kPxV) & 1) && wait(kHEmpty + buf, ((g >> 1) & 1) ^ 1);
+          if (!ok) break;
+          const uint8_t *v = smem + S::v + slot * S::kTile;
+          uint8_t *h = smem + S::h + buf * S::kHalf;
+          if (tok + 32 <= min_lim) {
+            // rows eight apart have the same swizzle: the addresses are two and constants
+            const uint8_t *va = px_codes<D>(v, row0, chunk), *vb = px_codes<D>(v, row0 + 4, chunk);
+            uint8_t *ha = h, *hb = h;
+#pragma unroll 1
+            for (int q = 0; q < 4; q += 2) {
+              constexpr int kS = 8 * D;
+              if constexpr (D == 128) {
+                const uint4 w0 = *reinterpret_cast<const uint4 *>(va), w1 = *reinterpret_cast<const uint4 *>(vb);
+                const uint4 w2 = *reinterpret_cast<const uint4 *>(va + kS), w3 = *reinterpret_cast<const uint4 *>(vb + kS);
+                px_store_half<D>(ha, row0, chunk, w0);
+                px_store_half<D>(hb, row0 + 4, chunk, w1);
+                px_store_half<D>(ha + 1024, row0, chunk, w2);
+                px_store_half<D>(hb + 1024, row0 + 4, chunk, w3);
+                vb += 2 * kS;
+                hb += 2048;
+              } else {
+                const uint4 w0 = *reinterpret_cast<const uint4 *>(va), w2 = *reinterpret_cast<const uint4 *>(va + kS);
+                px_store_half<D>(ha, row0, chunk, w0);
+                px_store_half<D>(ha + 1024, row0, chunk, w2);
+              }
+              va += 2 * kS;
+              ha += 2048;
+            }
+          } else if (tok < t_end) {
+#pragma unroll 1
+            for (int it = 0; it < kC; ++it) {
+              const int row = row0 + kR * it, tk = tok + row - 32 * quad;
+              uint4 w = *reinterpret_cast<const uint4 *>(px_codes<D>(v, row, chunk));
+              uint32_t *x = reinterpret_cast<uint32_t *>(&w);
+              if (tk >= t_end) {
+                w = make_uint4(0, 0, 0, 0);  // cached bytes behind may be anything
+              } else if (tk >= min_lim) {
+                // a weight of 0 does not stop a NaN: it is put where its rows are written
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  uint32_t nan = nan_codes(x[q]);
+                  x[q] &= ~((nan >> 7) * 0xFFu);
+                  while (nan) {
+                    const int byte = (__ffs(nan) - 1) >> 3;
+                    nan &= nan - 1;
+                    atomicMin(&ctl.nan_from[k % kPxStats][16 * chunk + 4 * q + byte], px_nan(k, tk));
+                    ctl.nan_seg[k % kPxStats] = static_cast<int>(k) + 1;
+                  }
+                }
+              }
+              px_store_half<D>(h, row, chunk, w);
+            }
+          }
+          proxy_fence();
+          __syncwarp();
+          if (lane == 0) {
+            bar_arrive(bar(kVEmpty + slot));
+            bar_arrive(bar(kHFull + buf));
+          }
+          ++g;
+        }
+        if (t == 0 && k > 0) {
+          ok = px_put(k - 1);
+          if (!ok) break;
+        }
       }
+      if (!ok || ended) break;
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(kStatFull + k % kPxStats));
     }
   } else {
-    // ------------------------------------------------------------- softmax
-    // A row a lane, twice: `half` takes every other block of 16 tokens.
-    const int grp = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, r = 32 * quad + lane;
+    // ------------------------------------------------------- softmax, a row a lane
+    const int grp = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-    const uint32_t s_addr = tmem + lanes + kPxS + 128 * grp, o_addr = tmem + lanes + kPxO + half * (D / 2);
-    const int pair = kPair + 4 * grp + quad, ref_mine = kRef + 4 * grp + quad, ref_other = kRef + 4 * (grp ^ 1) + quad;
-    uint32_t g = 0, np = 0;  // tiles of the CTA so far, exchanges
+    const uint32_t s_addr = tmem + lanes + kPxS + 128 * grp, o_addr = tmem + lanes + kPxO;
+    const int ref_mine = kRef + 4 * grp + quad, ref_other = kRef + 4 * (grp ^ 1) + quad;
+    uint32_t g = 0;  // tiles of the CTA so far
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       const int ss = k % kPxSegs, ks = k % kPxStats;
@@ -1128,39 +1130,35 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         tc_after();
         come = t + 1;
         const float4 *sc = ctl.sc[cs];
-        float mx = -INFINITY, mv = -INFINITY, x[16];
+        float mx = -INFINITY, mv = -INFINITY, x[32];
         const bool full = tok + kPxTok <= min_lim;  // everybody sees all of it
-        const int blocks = (min(kPxTok, t_end - tok) + 15) >> 4;
+        const int chunks = full ? 4 : (min(kPxTok, t_end - tok) + 31) >> 5;  // of 32 tokens
         if (act) {
           bad_from = min(bad_from, ctl.bad[cs]);
           // (rolled loops: with the chunks laid out one after another the roles' code did not fit the
           // instruction caches, and its fetching took twice the time of the work)
           if (full) {
 #pragma unroll 1
-            for (int c = half; c < kPxTok / 16; c += 2) {
-              tc_ld16w(x, s_addr + 16 * c);
-              px_max(x, sc[c], qk, mx, mv);
+            for (int c = 0; c < 4; ++c) {
+              tc_ld32(x, s_addr + 32 * c);
+              px_max(x, sc + 2 * c, qk, mx, mv);
             }
           } else {
 #pragma unroll 1
-            for (int c = half; c < blocks; c += 2) {
-              tc_ld16w(x, s_addr + 16 * c);
-              px_mask(x, lim - tok - 16 * c);
-              px_max(x, sc[c], qk, mx, mv);
+            for (int c = 0; c < chunks; ++c) {
+              tc_ld32(x, s_addr + 32 * c);
+              px_mask(x, lim - tok - 32 * c);
+              px_max(x, sc + 2 * c, qk, mx, mv);
             }
           }
-          ctl.mx[grp][half][r] = make_float2(mx, mv);
         }
-        // the row's other half, and the references that the groups hand one another
-        __syncwarp();
-        if (lane == 0) bar_arrive(bar(pair));
-        ok = wait(pair, np++ & 1) && (gt == 0 || wait(ref_other, ((gt - 1) >> 1) & 1));
-        if (!ok) break;
+        // the references, which the groups hand one another
+        if (gt > 0) {
+          ok = wait(ref_other, ((gt - 1) >> 1) & 1);
+          if (!ok) break;
+        }
         float fo = 1.f;
         if (act) {
-          const float2 other = ctl.mx[grp][half ^ 1][r];
-          mx = fmaxf(mx, other.x);
-          mv = fmaxf(mv, other.y);
           if (t > 0) {
             const float2 now = ctl.now[grp ^ 1][r];
             m = now.x;
@@ -1173,7 +1171,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             fo = fast_exp2(n - mv);
             n = mv;
           }
-          if (half == 0) ctl.now[grp][r] = make_float2(m, n);
+          ctl.now[grp][r] = make_float2(m, n);
         }
         __syncwarp();
         if (lane == 0) bar_arrive(bar(ref_mine));
@@ -1184,49 +1182,59 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           }
           const bool none = n == -INFINITY;  // nothing seen yet: every x is -inf
           const float mm = none ? 0.f : m, mn = none ? 0.f : m - n;
-          float2 l2 = make_float2(0.f, 0.f);
-          uint32_t p[8];
-          if (full) {
+          float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          float p[16];
 #pragma unroll 1
-            for (int c = half; c < kPxTok / 16; c += 2) {
-              tc_ld16w(x, s_addr + 16 * c);
-              px_weights<false>(x, sc[c], qk, mm, mn, l2, p);
-              tc_st8(s_addr + 16 * c, p);  // in the block's own columns
+          for (int h = 0; h < 2; ++h) {  // 64 tokens
+            if (full) {
+#pragma unroll 1
+              for (int c = 2 * h; c < 2 * h + 2; ++c) {
+                tc_ld32(x, s_addr + 32 * c);
+                px_weights<false>(x, sc + 2 * c, qk, mm, mn, l2, p);
+                tc_st16(s_addr + 32 * c, p);  // in the chunk's own columns
+              }
+            } else {
+#pragma unroll 1
+              for (int c = 2 * h; c < min(2 * h + 2, chunks); ++c) {
+                tc_ld32(x, s_addr + 32 * c);
+                px_mask(x, lim - tok - 32 * c);
+                px_weights<true>(x, sc + 2 * c, qk, mm, mn, l2, p);
+                tc_st16(s_addr + 32 * c, p);
+              }
             }
-          } else {
+            if (h == 0 && t > 0 && __any_sync(0xffffffffu, fo != 1.f)) {  // before any of the tile's products
+              ok = wait(kPvDone, (gt - 1) & 1);
+              if (!ok) break;
+              tc_after();
 #pragma unroll 1
-            for (int c = half; c < blocks; c += 2) {
-              tc_ld16w(x, s_addr + 16 * c);
-              px_mask(x, lim - tok - 16 * c);
-              px_weights<true>(x, sc[c], qk, mm, mn, l2, p);
-              tc_st8(s_addr + 16 * c, p);
-            }
-          }
-          l += l2.x + l2.y;
-          if (t > 0 && __any_sync(0xffffffffu, fo != 1.f)) {
-            ok = wait(kPvDone, (gt - 1) & 1);
-            if (!ok) break;
-            tc_after();
-#pragma unroll 1
-            for (int c = 0; c < D / 2; c += 32) {
-              float o[32];
-              tc_ld32(o, o_addr + c);
+              for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tc_ld32(o, o_addr + c);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] *= fo;
-              tc_st32(o_addr + c, o);
+                for (int j = 0; j < 32; ++j) o[j] *= fo;
+                tc_st32(o_addr + c, o);
+              }
             }
+            tc_st_wait();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(h ? kPFull + grp : kPHalf + grp));
           }
-          tc_st_wait();
+          if (!ok) break;
+          l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+        } else {
+          tc_before();
+          __syncwarp();
+          if (lane == 0) {
+            bar_arrive(bar(kPHalf + grp));
+            bar_arrive(bar(kPFull + grp));
+          }
         }
-        tc_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(bar(kPFull + grp));
       }
       if (!ok) break;
       g += tiles;
-      if (half == 0) ctl.end_mn[ks][grp][r] = make_float2(lm, n);
-      ctl.end_l[ks][grp][half][r] = lim > bad_from ? -1.f : l;
-      if (half == 0 && quad == 0 && lane == 0) ctl.come[ks][grp] = come;
+      ctl.end[ks][grp][r] = make_float4(lm, lim > bad_from ? -1.f : l, n, 0.f);
+      if (quad == 0 && lane == 0) ctl.come[ks][grp] = come;
       __syncwarp();
       if (lane == 0) {
         bar_arrive(bar(kStatFull + ks));
