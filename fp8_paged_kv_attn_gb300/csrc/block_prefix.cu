@@ -224,8 +224,7 @@ enum : int {
   kQFree = kSegFull + kPxSegs,
   kSFull = kQFree + 2,
   kHEmpty = kSFull + 2,
-  kPvDone = kHEmpty + 2,
-  kODone,
+  kODone = kHEmpty + 2,
   kDrain,
   kRef,  // [group][quarter of the rows]
   kVEmpty = kRef + 8,  // four warps each from here
@@ -267,7 +266,12 @@ __device__ __forceinline__ unsigned long long px_nan(uint32_t seg, int tok) {
   return (static_cast<unsigned long long>(~seg) << 32) | static_cast<uint32_t>(tok);
 }
 
-constexpr uint32_t kPxS = 0, kPxO = 256, kPxQ = 384;  // TMEM columns
+// TMEM columns: scores, a ring of five halves of a tile (64 tokens), from 0 on; q; sums.
+constexpr uint32_t kPxQ = 320, kPxO = 384;
+template <int D>
+constexpr int kPxQs = 128 / D;  // segments' q
+__device__ __forceinline__ uint32_t px_scol(uint32_t g, int half) { return 64 * ((2 * g + half) % 5); }
+
 
 template <int D>
 struct PxSmem {
@@ -315,8 +319,8 @@ __device__ __noinline__ bool px_wait_long(int *fail, uint32_t bar, uint32_t pari
   return __all_sync(0xffffffffu, ok);
 }
 
-// Whether a phase is over, without waiting for it; the same for the whole warp.
-__device__ __forceinline__ bool px_test(uint32_t bar, uint32_t parity) {
+// Whether a phase is over, without waiting for it.
+__device__ __forceinline__ uint32_t bar_test(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
@@ -324,7 +328,7 @@ __device__ __forceinline__ bool px_test(uint32_t bar, uint32_t parity) {
       : "=r"(done)
       : "r"(bar), "r"(parity)
       : "memory");
-  return __all_sync(0xffffffffu, done != 0);
+  return done;
 }
 
 // Rows of D bytes: for 64 a 64-byte swizzle, 8-row groups 512 bytes apart.
@@ -673,6 +677,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     if (__all_sync(0xffffffffu, bar_try(bars + 8u * i, parity))) return true;
     return px_wait_long(&ctl.fail, bars + 8u * i, parity, a.err_word);
   };
+  auto test = [&](int i, uint32_t parity) { return bar_test(bars + 8u * i, parity); };  // (a lane's)
   if (threadIdx.x < kBars) {
     const int i = threadIdx.x;
     mbar_init(&ctl.bar[i], px_arrivals(i));
@@ -819,96 +824,127 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       for (uint32_t k = g > stages ? g - stages : 0; k < g; ++k) mbar_wait(&ctl.bar[full + k % stages], (k / stages) & 1);
   } else if (warp == kPxMma) {
     // ------------------------------------------------------------- MMA issue
-    // Scores run up to two tiles ahead of values, into the next segment too: S(t) takes the
-    // columns of S(t - 2), whose weights PV(t - 2), issued before it, reads there.
+    // Scores run two tiles ahead of values, into the next segment too.  S(t + 2) takes the columns of the
+    // second half of S(t - 1) and of the first of S(t), whose weights the products issued before it read
+    // there: it is made while the softmax ends the weights of t.
     const uint32_t k_a = smem_addr(smem + S::k), h_a = smem_addr(smem + S::h);
     uint32_t ks = 0, ps = 0;  // segments of the scores' and of the values' cursor
     int kt = 0, pt = 0;       // tiles in them
     uint32_t kg = 0, pg = 0;  // tiles so far
-    PxSeg ksg, psg;
+    int k_tiles = 0, k_len = 0, p_tiles = 0, p_len = 0;  // their segments' tiles and tokens
     bool ok = true, k_in = false, p_in = false, k_end = false;
-    auto tokens = [](const PxSeg &sg, int t) {  // of a tile, in whole chunks of 32
-      return min(kPxTok, (sg.t_end - sg.tok - t * kPxTok + 31) & ~31);
+    auto tokens = [](int len, int t) {  // of a tile, in whole chunks of 32
+      return min(kPxTok, (len - t * kPxTok + 31) & ~31);
     };
-    while (ok) {
-      while (ok && !k_end && kg - pg < 2) {
-        if (!k_in) {  // the next segment: waited for only when nothing else is to be done
-          const int ss = ks % kPxSegs;
-          const uint32_t sp = (ks / kPxSegs) & 1, qp = (ks >> 1) & 1;
-          if (kg != pg && !px_test(bar(kSegFull + ss), sp)) break;
-          ok = wait(kSegFull + ss, sp);
-          if (!ok) break;
-          ksg = ctl.seg[ss];
-          if (ksg.b < 0) {
-            k_end = true;
-            break;
-          }
-          if (kg != pg && !px_test(bar(kQFull + (ks & 1)), qp)) break;
-          ok = wait(kQFull + (ks & 1), qp);
-          if (!ok) break;
-          k_in = true;
-          kt = 0;
-        }
-        const int slot = kg % kPxK;
-        ok = wait(kKFull + slot, (kg / kPxK) & 1);
-        if (!ok) break;
-        tc_after();
-        const bool last = kt + 1 == ksg.tiles;
-        if (elect_one()) {
-          const uint64_t kd = px_kdesc<D>(k_a + slot * S::kTile);
-          const uint32_t q = tmem + kPxQ + (ks & 1) * (D / 2), n = tokens(ksg, kt);
+    // the scores' next segment; not if it is not there, unless `must`
+    auto next = [&](bool must) {
+      const int ss = ks % kPxSegs, qs = ks % kPxQs<D>;
+      const uint32_t sp = (ks / kPxSegs) & 1, qp = (ks / kPxQs<D>) & 1;
+      if (!must && !__all_sync(0xffffffffu, test(kSegFull + ss, sp))) return false;
+      if (!(ok = wait(kSegFull + ss, sp))) return false;
+      const PxSeg &sg = ctl.seg[ss];
+      k_tiles = sg.tiles;
+      k_len = sg.t_end - sg.tok;
+      if (sg.b < 0) {
+        k_end = true;
+        return false;
+      }
+      if (!must && !__all_sync(0xffffffffu, test(kQFull + qs, qp))) return false;
+      if (!(ok = wait(kQFull + qs, qp))) return false;
+      kt = 0;
+      return k_in = true;
+    };
+    // a tile's scores, whose K is there
+    auto scores = [&]() {
+      const int slot = kg % kPxK, qs = ks % kPxQs<D>, n = tokens(k_len, kt);
+      const bool last = kt + 1 == k_tiles;
+      const uint64_t kd = px_kdesc<D>(k_a + slot * S::kTile);
+      const uint32_t q = tmem + kPxQ + qs * (D / 2), to = tmem + px_scol(kg, 0);
+      auto mma = [&](uint32_t at, uint64_t rows, int cols) {
+        if (elect_one())
 #pragma unroll
           for (int piece = 1; piece >= 0; --piece)  // the smaller first: each sum is truncated
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
-              px_mma8(tmem + kPxS + 128 * (kg & 1), q + piece * (D / 4) + 8 * k, kd + 2 * k, n, piece == 1,
-                      piece == 0 || k > 0);
-          bar_commit(bar(kSFull + (kg & 1)));
-          bar_commit(bar(kKEmpty + slot));
-        }
+              px_mma8(at, q + piece * (D / 4) + 8 * k, rows + 2 * k, cols, piece == 1, piece == 0 || k > 0);
         __syncwarp();
-        // (a condition within the elected lane's block lost the commit: it stands around the election)
-        if (last && elect_one()) bar_commit(bar(kQFree + (ks & 1)));
-        __syncwarp();
-        ++kg;
-        ++kt;
-        if (last) {
-          k_in = false;
-          ++ks;
-        }
+      };
+      if (to - tmem != 256) {
+        mma(to, kd, n);
+      } else {  // the ring's end (half a tile's product takes as long as a whole one's: one tile in five)
+        mma(to, kd, min(n, 64));
+        if (n > 64) mma(tmem, kd + (S::kTile / 2 >> 4), n - 64);
+      }
+      if (elect_one()) {
+        bar_commit(bar(kSFull + (kg & 1)));
+        bar_commit(bar(kKEmpty + slot));
+      }
+      __syncwarp();
+      // (a condition within the elected lane's block lost the commit: it stands around the election)
+      if (last && elect_one()) bar_commit(bar(kQFree + qs));
+      __syncwarp();
+      ++kg;
+      ++kt;
+      if (last) {
+        k_in = false;
+        ++ks;
+      }
+    };
+    while (ok) {
+      while (ok && !k_end && kg - pg < 2) {
+        if (!k_in && !next(kg == pg)) break;
+        ok = wait(kKFull + kg % kPxK, (kg / kPxK) & 1);
+        if (!ok) break;
+        tc_after();
+        scores();
       }
       if (!ok || (k_end && kg == pg)) break;
       if (!p_in) {
-        psg = ctl.seg[ps % kPxSegs];  // (its scores have been issued)
+        const PxSeg &sg = ctl.seg[ps % kPxSegs];  // (its scores have been issued)
+        p_tiles = sg.tiles;
+        p_len = sg.t_end - sg.tok;
         p_in = true;
         pt = 0;
+        ok = ps == 0 || wait(kOFree, (ps - 1) & 1);
+        if (!ok) break;
       }
       const int buf = pg & 1;
-      ok = wait(kHFull + buf, (pg >> 1) & 1) && (pt > 0 || ps == 0 || wait(kOFree, (ps - 1) & 1)) &&
-           wait(kPHalf + buf, (pg >> 1) & 1);
+      const uint32_t par = (pg >> 1) & 1;
+      const bool last = pt + 1 == p_tiles, ahead = !k_end && kg - pg == 2 && (k_in || next(false));
       if (!ok) break;
-      tc_after();
-      const bool last = pt + 1 == psg.tiles;
-      // 16 tokens a step: 8 columns of P, 16 rows of V; the first four while the others' weights are made
-      const int steps = tokens(psg, pt) / 16;
-      const uint64_t vd = px_vdesc(h_a + buf * S::kHalf);
-      if (elect_one())
-        for (int k = 0; k < min(steps, 4); ++k)
-          px_mma16(tmem + kPxO, tmem + kPxS + 128 * buf + 32 * (k >> 1) + 8 * (k & 1), vd + k * (16 * 128 >> 4), D,
-                   pt > 0 || k > 0);
-      __syncwarp();
-      ok = wait(kPFull + buf, (pg >> 1) & 1);
-      if (!ok) break;
-      if (lane == 0) bar_arrive(bar(kScEmpty + pg % kPxScales));
-      tc_after();
-      if (elect_one()) {
-        for (int k = 4; k < steps; ++k)
-          px_mma16(tmem + kPxO, tmem + kPxS + 128 * buf + 32 * (k >> 1) + 8 * (k & 1), vd + k * (16 * 128 >> 4), D, true);
-        bar_commit(bar(kHEmpty + buf));
-        bar_commit(bar(kPvDone));
+      {  // a round trip is some 150 cycles beside the tiles' traffic: the tests go out together
+        const int kb = ahead ? kKFull + kg % kPxK : kHFull + buf;
+        const uint32_t kp = ahead ? (kg / kPxK) & 1 : par;
+        const uint32_t x = test(kb, kp), y = test(kHFull + buf, par), z = test(kPHalf + buf, par);
+        ok = __all_sync(0xffffffffu, x & y & z) ||
+             (wait(kb, kp) && wait(kHFull + buf, par) && wait(kPHalf + buf, par));
       }
+      if (!ok) break;
+      tc_after();
+      // 16 tokens a step: 8 columns of P, 16 rows of V
+      const int steps = tokens(p_len, pt) / 16;
+      const uint64_t vd = px_vdesc(h_a + buf * S::kHalf);
+      auto values = [&](int half) {
+        const uint32_t p = tmem + px_scol(pg, half);
+        const uint64_t rows = vd + half * (64 * 128 >> 4);
+        const int n = min(steps - 4 * half, 4);
+        if (elect_one())
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < n)
+              px_mma16(tmem + kPxO, p + 32 * (k >> 1) + 8 * (k & 1), rows + k * (16 * 128 >> 4), D, pt + half + k > 0);
+        __syncwarp();
+      };
+      values(0);
+      if (ahead) scores();
+      ok = wait(kPFull + buf, par);
+      if (!ok) break;
+      tc_after();
+      values(1);
+      if (elect_one()) bar_commit(bar(kHEmpty + buf));
       __syncwarp();
       if (last && elect_one()) bar_commit(bar(kODone));
+      if (lane == 0) bar_arrive(bar(kScEmpty + pg % kPxScales));
       __syncwarp();
       ++pg;
       ++pt;
@@ -1009,17 +1045,18 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       const int tiles = ended ? 0 : next.tiles, t_end = next.t_end, tok0 = next.tok;
       const int min_lim = next.lim0 ? min(t_end, next.lim0 + next.rb * kPxRows / a.G) : t_end;
       if (!ended) {
-        ok = k < 2 || wait(kQFree + (k & 1), ((k >> 1) - 1) & 1);
+        constexpr uint32_t kQs = kPxQs<D>;
+        ok = k < kQs || wait(kQFree + k % kQs, (k / kQs - 1) & 1);
         if (!ok) break;
         tc_after();
         if (32 * quad < next.rows) {
-          px_load_q<D>(a, next, tmem + lanes + kPxQ + (k & 1) * (D / 2), ctl.qk[k % kPxStats], r);
+          px_load_q<D>(a, next, tmem + lanes + kPxQ + k % kQs * (D / 2), ctl.qk[k % kPxStats], r);
           tc_st_wait();
         }
         tc_before();
         __syncwarp();
         if (lane == 0) {
-          bar_arrive(bar(kQFull + (k & 1)));
+          bar_arrive(bar(kQFull + k % kQs));
           bar_arrive(bar(kQReady + k % kPxStats));
         }
       }
@@ -1100,7 +1137,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     // ------------------------------------------------------- softmax, a row a lane
     const int grp = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-    const uint32_t s_addr = tmem + lanes + kPxS + 128 * grp, o_addr = tmem + lanes + kPxO;
+    const uint32_t o_addr = tmem + lanes + kPxO;
     const int ref_mine = kRef + 4 * grp + quad, ref_other = kRef + 4 * (grp ^ 1) + quad;
     uint32_t g = 0;  // tiles of the CTA so far
     bool ok = true;
@@ -1130,6 +1167,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         tc_after();
         come = t + 1;
         const float4 *sc = ctl.sc[cs];
+        const uint32_t s0 = tmem + lanes + px_scol(gt, 0), s1 = tmem + lanes + px_scol(gt, 1) - 64;
         float mx = -INFINITY, mv = -INFINITY, x[32];
         const bool full = tok + kPxTok <= min_lim;  // everybody sees all of it
         const int chunks = full ? 4 : (min(kPxTok, t_end - tok) + 31) >> 5;  // of 32 tokens
@@ -1140,13 +1178,13 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           if (full) {
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-              tc_ld32(x, s_addr + 32 * c);
+              tc_ld32(x, (c < 2 ? s0 : s1) + 32 * c);
               px_max(x, sc + 2 * c, qk, mx, mv);
             }
           } else {
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
-              tc_ld32(x, s_addr + 32 * c);
+              tc_ld32(x, (c < 2 ? s0 : s1) + 32 * c);
               px_mask(x, lim - tok - 32 * c);
               px_max(x, sc + 2 * c, qk, mx, mv);
             }
@@ -1189,21 +1227,21 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             if (full) {
 #pragma unroll 1
               for (int c = 2 * h; c < 2 * h + 2; ++c) {
-                tc_ld32(x, s_addr + 32 * c);
+                tc_ld32(x, (c < 2 ? s0 : s1) + 32 * c);
                 px_weights<false>(x, sc + 2 * c, qk, mm, mn, l2, p);
-                tc_st16(s_addr + 32 * c, p);  // in the chunk's own columns
+                tc_st16((h ? s1 : s0) + 32 * c, p);  // in the chunk's own columns
               }
             } else {
 #pragma unroll 1
               for (int c = 2 * h; c < min(2 * h + 2, chunks); ++c) {
-                tc_ld32(x, s_addr + 32 * c);
+                tc_ld32(x, (c < 2 ? s0 : s1) + 32 * c);
                 px_mask(x, lim - tok - 32 * c);
                 px_weights<true>(x, sc + 2 * c, qk, mm, mn, l2, p);
-                tc_st16(s_addr + 32 * c, p);
+                tc_st16((h ? s1 : s0) + 32 * c, p);
               }
             }
             if (h == 0 && t > 0 && __any_sync(0xffffffffu, fo != 1.f)) {  // before any of the tile's products
-              ok = wait(kPvDone, (gt - 1) & 1);
+              ok = wait(kHEmpty + (grp ^ 1), ((gt - 1) >> 1) & 1);
               if (!ok) break;
               tc_after();
 #pragma unroll 1
