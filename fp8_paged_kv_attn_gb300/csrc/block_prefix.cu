@@ -1324,67 +1324,74 @@ __global__ void __launch_bounds__(32 * kPxMergeWarps) prefix_merge_kernel(PfArgs
       where[1] = __ldcg(reinterpret_cast<const float4 *>(own_rows + D));
       if (where[1].w == kDone) continue;
     }
-#pragma unroll 1
-    for (int own = 0; own < 2; ++own) {
-      const float4 e = own ? where[1] : where[0];
-      if (e.w == 0.f) continue;
-      // part p lies in the p-th CTA from here on: the first in slot 1, others in slot 0
-      const bool cut = e.w == kCut;
-      const int parts = cut ? __float_as_int(e.y) : 1;
-      const int row = (it.row0 + i - (own ? it.row0 : it.row_pre)) * a.G + h % a.G;
-      const float *base = own ? own_rows : rows;
-      int64_t slot = kPxRows;  // rows of a part's slot
-      if (cut && own && a.own_split) {
-        const int in = row % (a.rt * a.rk), kvh = h / a.G;
-        slot = a.hg * a.rt * a.rk;
-        base = a.own_cut + (2 * __float_as_int(e.x) * slot + (kvh % a.hg * a.rt + in / a.rk) * a.rk + in % a.rk) * RF;
-      } else if (cut) {
-        base = a.cut + (static_cast<int64_t>(2 * __float_as_int(e.x)) * kPxRows + row % kPxRows) * RF;
-      }
-      for (int p0 = 0; p0 < parts; p0 += kBatch) {
-        float4 s[kBatch];
-        float v[kBatch][V];
+    // The parts of both in one list.  Part p lies in the p-th CTA from here on: the first in slot 1, others in
+    // slot 0.
+    const float *base[2] = {rows, own_rows};
+    int parts[2];
+    int64_t slot[2];  // from one CTA's slot to the next; 0: not cut
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          s[j] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-          if (p0 + j < parts) {
-            const float *q = base + (cut ? (2 * (p0 + j) + (p0 + j == 0)) * slot * RF : 0);
-            s[j] = __ldcg(reinterpret_cast<const float4 *>(q + D));
-            if constexpr (V == 4) {
-              const float4 x = __ldcg(reinterpret_cast<const float4 *>(q) + lane);
-              v[j][0] = x.x;
-              v[j][1] = x.y;
-              v[j][2] = x.z;
-              v[j][3] = x.w;
-            } else {
-              const float2 x = __ldcg(reinterpret_cast<const float2 *>(q) + lane);
-              v[j][0] = x.x;
-              v[j][1] = x.y;
-            }
+    for (int own = 0; own < 2; ++own) {
+      const float4 e = where[own];
+      parts[own] = e.w == 0.f ? 0 : 1;
+      slot[own] = 0;
+      if (e.w != kCut) continue;
+      parts[own] = __float_as_int(e.y);
+      const int row = (it.row0 + i - (own ? it.row0 : it.row_pre)) * a.G + h % a.G;
+      int64_t at_row = row % kPxRows, rows_slot = kPxRows;
+      if (own && a.own_split) {
+        const int in = row % (a.rt * a.rk), kvh = h / a.G;
+        rows_slot = a.hg * a.rt * a.rk;
+        at_row = (kvh % a.hg * a.rt + in / a.rk) * a.rk + in % a.rk;
+      }
+      slot[own] = rows_slot * RF;
+      base[own] = (own && a.own_split ? a.own_cut : a.cut) + (2 * __float_as_int(e.x) * rows_slot + at_row) * RF;
+    }
+    const int all = parts[0] + parts[1];
+    for (int p0 = 0; p0 < all; p0 += kBatch) {
+      float4 s[kBatch];
+      float v[kBatch][V];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        s[j] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        if (p0 + j < all) {
+          const bool own = p0 + j >= parts[0];
+          const int p = p0 + j - (own ? parts[0] : 0);
+          const float *q = (own ? base[1] : base[0]) + (2 * p + (p == 0)) * (own ? slot[1] : slot[0]);
+          s[j] = __ldcg(reinterpret_cast<const float4 *>(q + D));
+          if constexpr (V == 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(q) + lane);
+            v[j][0] = x.x;
+            v[j][1] = x.y;
+            v[j][2] = x.z;
+            v[j][3] = x.w;
+          } else {
+            const float2 x = __ldcg(reinterpret_cast<const float2 *>(q) + lane);
+            v[j][0] = x.x;
+            v[j][1] = x.y;
           }
         }
-        float Mb = M, Nb = N;
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          Mb = fmaxf(Mb, s[j].x);
-          Nb = fmaxf(Nb, s[j].z);
-          bad |= s[j].y < 0.f;
-        }
-        const float fl = M == -INFINITY ? 0.f : exp2f(M - Mb), fo = N == -INFINITY ? 0.f : exp2f(N - Nb);
-        l *= fl;
-#pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] *= fo;
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          if (s[j].y == 0.f) continue;  // saw nothing
-          l = fmaf(exp2f(s[j].x - Mb), s[j].y, l);
-          const float f = exp2f(s[j].z - Nb);
-#pragma unroll
-          for (int k = 0; k < V; ++k) acc[k] = fmaf(f, v[j][k], acc[k]);
-        }
-        M = Mb;
-        N = Nb;
       }
+      float Mb = M, Nb = N;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        Mb = fmaxf(Mb, s[j].x);
+        Nb = fmaxf(Nb, s[j].z);
+        bad |= s[j].y < 0.f;
+      }
+      const float fl = M == -INFINITY ? 0.f : exp2f(M - Mb), fo = N == -INFINITY ? 0.f : exp2f(N - Nb);
+      l *= fl;
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[k] *= fo;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (s[j].y == 0.f) continue;  // saw nothing
+        l = fmaf(exp2f(s[j].x - Mb), s[j].y, l);
+        const float f = exp2f(s[j].z - Nb);
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = fmaf(f, v[j][k], acc[k]);
+      }
+      M = Mb;
+      N = Nb;
     }
     const float2 f = bad ? make_float2(0.f, 0.f) : out_scale(N - M - 7.f, l);
 #pragma unroll
