@@ -35,8 +35,8 @@ struct ShSmem {
   int base[kShThreads];  // the entry's first logical page
   int req[kShThreads], other[kShThreads];
   uint8_t on[kShThreads];
-  unsigned int bits;
-  long long sum;
+  unsigned int bits[4];      // the cluster's error bits, a word a check
+  long long sums[kShCtas];   // its CTAs' sums
 };
 
 // Exclusive scan of v over the CTA; *total = the sum.
@@ -81,20 +81,51 @@ __device__ __forceinline__ int sh_owner(const ShSmem &sm, int m, long long e) {
   return lo;
 }
 
-// The cluster's error bits together; every thread of the cluster calls it.
-__device__ __forceinline__ unsigned int sh_bits(cg::cluster_group &cl, ShSmem &sm) {
-  cl.sync();
-  unsigned int all = 0;
-  for (unsigned int r = 0; r < cl.num_blocks(); ++r)
-    all |= *cl.map_shared_rank(&sm.bits, r);
-  cl.sync();  // nobody's bits change, or go with their CTA, before all have read them
-  return all;
+// The same, from the owner `o` of an item a little before e.
+__device__ __forceinline__ int sh_owner_from(const ShSmem &sm, int m, long long e, int o) {
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    if (o + 1 >= m || sm.pre[o + 1] > e) return o;
+    ++o;
+  }
+  return sh_owner(sm, m, e);
 }
 
-// Memory that other CTAs of the cluster write: never through the read-only path.
+// The cluster's error bits up to check c; every thread of the cluster calls it.  Who has bits hands them to
+// every CTA (reading the others' words took longer than a phase: 32 warps, eight remote loads each).  A
+// check's word is its own: a later one's bits cannot come in while it is read.
+__device__ __forceinline__ unsigned int sh_bits(cg::cluster_group &cl, ShSmem &sm, int c, unsigned int bits) {
+  if (bits)
+    for (unsigned int r = 0; r < cl.num_blocks(); ++r) atomicOr(cl.map_shared_rank(&sm.bits[c], r), bits);
+  cl.sync();
+  return sm.bits[c];
+}
+
+// A sum of this CTA for every CTA, read behind the next barrier of the cluster.
+__device__ __forceinline__ void sh_sum(cg::cluster_group &cl, ShSmem &sm, long long sum) {
+  if (threadIdx.x < cl.num_blocks()) *cl.map_shared_rank(&sm.sums[cl.block_rank()], threadIdx.x) = sum;
+}
+
+// Memory that other CTAs of the cluster write, read behind a barrier of the cluster: never through the
+// read-only path.
 template <typename T>
 __device__ __forceinline__ T vol(const T *p) {
   return __ldcg(p);
+}
+
+// A warp takes kShBatch times 32 items in a row.  This thread's first, where the cluster's thread `at` begins;
+__device__ __forceinline__ long long sh_first(int at) {
+  return static_cast<long long>(at & ~31) * kShBatch + (at & 31);
+}
+// and the owners of its items e0, e0 + 32, .. below `to` (-1: there is none).
+__device__ __forceinline__ void sh_batch(const ShSmem &sm, int m, long long e0, long long to, int (&o)[kShBatch]) {
+  int from = sh_owner(sm, m, e0 & ~31ll);
+#pragma unroll
+  for (int k = 0; k < kShBatch; ++k) {
+    const long long e = e0 + 32 * k;
+    o[k] = -1;
+    if (e < to) o[k] = from = sh_owner_from(sm, m, e, from);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -121,7 +152,6 @@ __global__ void __launch_bounds__(kShThreads, 1) fork_kernel(ForkArgs a) {
   const int at = cta * kShThreads + tid, threads = ctas * kShThreads;
   grid_dependency_wait();
   allow_dependents();
-  if (tid == 0) sm.bits = 0;
   const int count = *a.count;
   if (count < 0 || count > a.num_pages) {  // every CTA alike
     for (int i = at; i < a.n; i += threads) {
@@ -170,13 +200,18 @@ __global__ void __launch_bounds__(kShThreads, 1) fork_kernel(ForkArgs a) {
     }
     sm.pre[tid] = sh_scan(pages, sm, &total);
     __syncthreads();
-    for (long long e = at; e < total; e += threads) {
-      const int o = sh_owner(sm, m, e);
-      const int page = a.table[static_cast<int64_t>(sm.req[o]) * a.MP + (e - sm.pre[o])];
-      if (page < 0 || page >= a.num_pages) {
-        a.ok[r0 + o] = 0;
-        bits |= KVQ_ERRBIT_PAGE;
-      }
+    for (long long e0 = sh_first(at); e0 < total; e0 += static_cast<long long>(kShBatch) * threads) {
+      int o[kShBatch], page[kShBatch];
+      sh_batch(sm, m, e0, total, o);
+#pragma unroll
+      for (int k = 0; k < kShBatch; ++k)
+        page[k] = o[k] < 0 ? 0 : a.table[static_cast<int64_t>(sm.req[o[k]]) * a.MP + (e0 + 32 * k - sm.pre[o[k]])];
+#pragma unroll
+      for (int k = 0; k < kShBatch; ++k)
+        if (page[k] < 0 || page[k] >= a.num_pages) {
+          a.ok[r0 + o[k]] = 0;
+          bits |= KVQ_ERRBIT_PAGE;
+        }
     }
     __syncthreads();
   }
@@ -221,18 +256,17 @@ __global__ void __launch_bounds__(kShThreads, 1) fork_kernel(ForkArgs a) {
       a.copy_src[i] = from;
       a.copy_dst[i] = to;
     }
-    for (long long e0 = at; e0 < total; e0 += static_cast<long long>(kShBatch) * threads) {
+    for (long long e0 = sh_first(at); e0 < total; e0 += static_cast<long long>(kShBatch) * threads) {
       int64_t to[kShBatch];
-      int page[kShBatch];
+      int o[kShBatch], page[kShBatch];
       uint32_t tag[kShBatch];
+      sh_batch(sm, m, e0, total, o);
 #pragma unroll
       for (int k = 0; k < kShBatch; ++k) {
-        const long long e = e0 + static_cast<long long>(k) * threads;
         page[k] = -1;
-        if (e < total) {
-          const int o = sh_owner(sm, m, e);
-          const int64_t col = e - sm.pre[o], from = static_cast<int64_t>(sm.req[o]) * a.MP + col;
-          to[k] = static_cast<int64_t>(sm.other[o]) * a.MP + col;
+        if (o[k] >= 0) {
+          const int64_t col = e0 + 32 * k - sm.pre[o[k]], from = static_cast<int64_t>(sm.req[o[k]]) * a.MP + col;
+          to[k] = static_cast<int64_t>(sm.other[o[k]]) * a.MP + col;
           page[k] = a.table[from];
           tag[k] = a.expected[from];
         }
@@ -267,29 +301,37 @@ struct ReleaseArgs {
   int32_t num_pages, B, MP, n;
 };
 
-// Calls f(item, its table entry) for the items [from, to) of the list.  Every thread of the CTA
-// calls f together, with a null entry where it has no item.
+// Calls f(first item, the table entries of kShBatch items in a row) for the items [from, to) of the list.
+// Every thread of the CTA calls f together, with null entries where it has no item.
 template <typename F>
-__device__ __forceinline__ void sh_items(const ReleaseArgs &a, ShSmem &sm, long long from, long long to, F f) {
+__device__ __forceinline__ void sh_items(const ReleaseArgs &a, ShSmem &sm, long long from, long long to,
+                                         long long items, F f) {
   const int tid = threadIdx.x;
   long long carry = 0;
   for (int r0 = 0; r0 < a.n && carry < to; r0 += kShThreads) {
     const int j = r0 + tid, m = min(kShThreads, a.n - r0);
-    long long total;
-    const long long pre = sh_scan(j < a.n ? a.npages[j] : 0, sm, &total);
-    sm.pre[tid] = pre;
-    if (j < a.n) {
-      sm.req[tid] = a.req[j];
-      sm.base[tid] = a.first ? a.first[j] : 0;
+    long long total = items;
+    if (a.n > kShThreads) {  // a single round is still there
+      const long long pre = sh_scan(j < a.n ? a.npages[j] : 0, sm, &total);
+      sm.pre[tid] = pre;
+      if (j < a.n) {
+        sm.req[tid] = a.req[j];
+        sm.base[tid] = a.first ? a.first[j] : 0;
+      }
+      __syncthreads();
     }
-    __syncthreads();
     const long long lo = max(from, carry), hi = min(to, carry + total);
-    for (long long e0 = lo; e0 < hi; e0 += kShThreads) {
-      const long long e = e0 + tid;
-      int32_t *entry = nullptr;
-      if (e < hi) {
-        const int o = sh_owner(sm, m, e - carry);
-        entry = a.table + static_cast<int64_t>(sm.req[o]) * a.MP + sm.base[o] + (e - carry - sm.pre[o]);
+    for (long long e0 = lo; e0 < hi; e0 += kShBatch * kShThreads) {
+      const long long e = e0 + kShBatch * tid;
+      int32_t *entry[kShBatch];
+      int o = e < hi ? sh_owner(sm, m, e - carry) : 0;
+#pragma unroll
+      for (int k = 0; k < kShBatch; ++k) {
+        entry[k] = nullptr;
+        if (e + k < hi) {
+          o = sh_owner_from(sm, m, e + k - carry, o);
+          entry[k] = a.table + static_cast<int64_t>(sm.req[o]) * a.MP + sm.base[o] + (e + k - carry - sm.pre[o]);
+        }
       }
       f(static_cast<int>(e), entry);
     }
@@ -305,11 +347,8 @@ __global__ void __launch_bounds__(kShThreads, 1) release_kernel(ReleaseArgs a) {
   const int at = cta * kShThreads + tid, threads = ctas * kShThreads;
   grid_dependency_wait();
   allow_dependents();
-  if (tid == 0) {
-    sm.bits = 0;
-    sm.sum = 0;
-  }
-  __syncthreads();
+  if (tid < 4) sm.bits[tid] = 0;
+  cl.barrier_arrive();
   const int count = *a.count;
   unsigned int bits = count < 0 || count > a.num_pages ? KVQ_ERRBIT_PAGE : 0;
   // ---- the list: requests named once, pages within their rows
@@ -319,8 +358,10 @@ __global__ void __launch_bounds__(kShThreads, 1) release_kernel(ReleaseArgs a) {
     long long n = 0, total;
     if (j < a.n) {
       const int b = a.req[j];
-      const long long f = a.first ? a.first[j] : 0;
+      const int f = a.first ? a.first[j] : 0;
       n = a.npages[j];
+      sm.req[tid] = b;
+      sm.base[tid] = f;
       if (b < 0 || b >= a.B)
         bits |= KVQ_ERRBIT_REQ;
       else if (j % ctas == cta)
@@ -330,87 +371,123 @@ __global__ void __launch_bounds__(kShThreads, 1) release_kernel(ReleaseArgs a) {
         n = 0;
       }
     }
-    sh_scan(n, sm, &total);
+    sm.pre[tid] = sh_scan(n, sm, &total);
     items += total;
   }
   if (items > INT_MAX) bits |= KVQ_ERRBIT_POS;
-  if (bits) atomicOr(&sm.bits, bits);
-  if (sh_bits(cl, sm)) {
+  cl.barrier_wait();  // every CTA's words are there
+  if (sh_bits(cl, sm, 0, bits)) {
     if (bits) report(a.err_word, bits);
     return;
   }
   for (int j = at; j < a.n; j += threads) atomicMin(a.claim + a.req[j], j);
-  cl.sync();
-  for (int j = at; j < a.n; j += threads)
-    if (vol(a.claim + a.req[j]) != j) bits |= KVQ_ERRBIT_REQ;
   // ---- the items: pages, and their counters cleared
   const long long per = (items + ctas - 1) / ctas;
   const long long from = min(items, cta * per), to = min(items, from + per);
-  sh_items(a, sm, from, to, [&](int, const int32_t *entry) {
-    if (!entry) return;
-    const int page = *entry;
-    if (page < 0 || page >= a.num_pages) {
-      bits |= KVQ_ERRBIT_PAGE;
-    } else {
-      a.gone[page] = 0;
-      a.last[page] = -1;
+  auto pages = [](int32_t *const(&entry)[kShBatch], int (&page)[kShBatch]) {
+#pragma unroll
+    for (int k = 0; k < kShBatch; ++k) page[k] = entry[k] ? *entry[k] : 0;
+  };
+  sh_items(a, sm, from, to, items, [&](int, int32_t *const(&entry)[kShBatch]) {
+    int page[kShBatch];
+    pages(entry, page);
+#pragma unroll
+    for (int k = 0; k < kShBatch; ++k) {
+      if (page[k] < 0 || page[k] >= a.num_pages) {
+        bits |= KVQ_ERRBIT_PAGE;
+      } else if (entry[k]) {
+        a.gone[page[k]] = 0;
+        a.last[page[k]] = -1;
+      }
     }
   });
-  if (bits) atomicOr(&sm.bits, bits);
-  if (sh_bits(cl, sm)) {
+  if (sh_bits(cl, sm, 1, bits)) {
     if (bits) report(a.err_word, bits);
     return;
   }
-  sh_items(a, sm, from, to, [&](int e, const int32_t *entry) {
-    if (!entry) return;
-    const int page = *entry;
-    atomicAdd(a.gone + page, 1);
-    atomicMax(a.last + page, e);
+  for (int j = at; j < a.n; j += threads)  // (a request named twice spoils scratch alone)
+    if (vol(a.claim + a.req[j]) != j) bits |= KVQ_ERRBIT_REQ;
+  sh_items(a, sm, from, to, items, [&](int e, int32_t *const(&entry)[kShBatch]) {
+    int page[kShBatch];
+    pages(entry, page);
+#pragma unroll
+    for (int k = 0; k < kShBatch; ++k)
+      if (entry[k]) {
+        atomicAdd(a.gone + page[k], 1);
+        atomicMax(a.last + page[k], e + k);
+      }
   });
-  cl.sync();
+  if (sh_bits(cl, sm, 2, bits)) {
+    if (bits) report(a.err_word, bits);
+    return;
+  }
   // ---- a page whose last holder goes is free, and lies on the stack where its last item stands
   int frees = 0;
-  sh_items(a, sm, from, to, [&](int e, const int32_t *entry) {
-    if (!entry) return;
-    const int page = *entry;
-    if (vol(a.last + page) != e) return;
-    const int gone = vol(a.gone + page), shares = a.shares[page];
-    if (shares < 0 || gone - 1 > shares) bits |= KVQ_ERRBIT_PAGE;  // more often than it is held
-    frees += gone - 1 == shares;
+  // (of an item: whether it is its page's last, how many entries hold the page, its counter)
+  struct Held {
+    int page[kShBatch], last[kShBatch], gone[kShBatch], shares[kShBatch];
+  };
+  auto look = [&](int32_t *const(&entry)[kShBatch], Held &h) {
+    pages(entry, h.page);
+#pragma unroll
+    for (int k = 0; k < kShBatch; ++k) {
+      h.last[k] = -1;
+      h.gone[k] = h.shares[k] = 0;
+      if (entry[k]) {
+        h.last[k] = vol(a.last + h.page[k]);
+        h.gone[k] = vol(a.gone + h.page[k]);
+        h.shares[k] = vol(a.shares + h.page[k]);
+      }
+    }
+  };
+  sh_items(a, sm, from, to, items, [&](int e, int32_t *const(&entry)[kShBatch]) {
+    Held h;
+    look(entry, h);
+#pragma unroll
+    for (int k = 0; k < kShBatch; ++k)
+      if (entry[k] && h.last[k] == e + k) {
+        if (h.shares[k] < 0 || h.gone[k] - 1 > h.shares[k]) bits |= KVQ_ERRBIT_PAGE;  // more often than it is held
+        frees += h.gone[k] - 1 == h.shares[k];
+      }
   });
   long long freed;
   sh_scan(frees, sm, &freed);
-  if (tid == 0) sm.sum = freed;
-  if (bits) atomicOr(&sm.bits, bits);
-  cl.sync();
+  sh_sum(cl, sm, freed);
+  unsigned int any = sh_bits(cl, sm, 3, bits);
   long long before = 0, all = 0;
-  unsigned int any = 0;
   for (int r = 0; r < ctas; ++r) {
-    const long long f = *cl.map_shared_rank(&sm.sum, r);
-    any |= *cl.map_shared_rank(&sm.bits, r);
+    const long long f = sm.sums[r];
     before += r < cta ? f : 0;
     all += f;
   }
-  cl.sync();
   if (!any && count + all > a.num_pages) any = bits = KVQ_ERRBIT_PAGE;
   if (any) {
     if (bits) report(a.err_word, bits);
     return;
   }
-  sh_items(a, sm, from, to, [&](int e, int32_t *entry) {
-    int push = -1;
-    if (entry) {
-      const int page = *entry;
-      *entry = -1;
-      if (vol(a.last + page) == e) {
-        const int left = a.shares[page] - vol(a.gone + page);
-        a.shares[page] = max(left, 0);
-        if (left < 0) push = page;
+  sh_items(a, sm, from, to, items, [&](int e, int32_t *const(&entry)[kShBatch]) {
+    Held h;
+    look(entry, h);
+    int free[kShBatch], pushes = 0;
+#pragma unroll
+    for (int k = 0; k < kShBatch; ++k) {
+      free[k] = -1;
+      if (!entry[k]) continue;
+      *entry[k] = -1;
+      if (h.last[k] == e + k) {  // (the page's counter is read here alone)
+        const int left = h.shares[k] - h.gone[k];
+        a.shares[h.page[k]] = max(left, 0);
+        if (left < 0) {
+          free[k] = h.page[k];
+          ++pushes;
+        }
       }
     }
     long long total;
-    const long long pre = sh_scan(push >= 0, sm, &total);
-    if (push >= 0) a.stack[count + before + pre] = push;
+    long long to_stack = count + before + sh_scan(pushes, sm, &total);
+#pragma unroll
+    for (int k = 0; k < kShBatch; ++k)
+      if (free[k] >= 0) a.stack[to_stack++] = free[k];
     before += total;
   });
   if (at == 0) *a.count = count + static_cast<int>(all);
@@ -433,6 +510,30 @@ struct CompactArgs {
   int32_t num_pages, B, MP, cap;
 };
 
+// Calls f(indexes of kShBatch table entries, -1 for none) over the entries that requests hold, spread over
+// the cluster.
+template <typename F>
+__device__ __forceinline__ void sh_held(const CompactArgs &a, ShSmem &sm, int at, int threads, F f) {
+  const int tid = threadIdx.x;
+  for (int r0 = 0; r0 < a.B; r0 += kShThreads) {
+    const int b = r0 + tid, m = min(kShThreads, a.B - r0);
+    long long total;
+    const long long pre = sh_scan(b < a.B ? a.held[b] : 0, sm, &total);
+    sm.pre[tid] = pre;
+    __syncthreads();
+    for (long long e0 = sh_first(at); e0 < total; e0 += static_cast<long long>(kShBatch) * threads) {
+      int o[kShBatch];
+      int64_t idx[kShBatch];
+      sh_batch(sm, m, e0, total, o);
+#pragma unroll
+      for (int k = 0; k < kShBatch; ++k)
+        idx[k] = o[k] < 0 ? -1 : static_cast<int64_t>(r0 + o[k]) * a.MP + (e0 + 32 * k - sm.pre[o[k]]);
+      f(idx);
+    }
+    __syncthreads();
+  }
+}
+
 __global__ void __launch_bounds__(kShThreads, 1) compact_kernel(CompactArgs a) {
   __shared__ ShSmem sm;
   __shared__ int s_base[kShCtas];
@@ -441,24 +542,33 @@ __global__ void __launch_bounds__(kShThreads, 1) compact_kernel(CompactArgs a) {
   const int at = cta * kShThreads + tid, threads = ctas * kShThreads;
   grid_dependency_wait();
   allow_dependents();
-  if (tid == 0) sm.bits = 0;
+  if (tid < 4) sm.bits[tid] = 0;
   const int words = (a.num_pages + 31) / 32, count = *a.count;
   const int share = (words + ctas - 1) / ctas;  // words a CTA scans
   for (int w = at; w < words; w += threads) a.words[w] = 0;
   unsigned int bits = count < 0 || count > a.num_pages ? KVQ_ERRBIT_PAGE : 0;
   cl.sync();
   if (!bits)
-    for (int i = at; i < count; i += threads) {
-      const int page = a.stack[i];
-      if (page < 0 || page >= a.num_pages)
-        bits |= KVQ_ERRBIT_PAGE;
-      else if (atomicOr(a.words + (page >> 5), 1u << (page & 31)) >> (page & 31) & 1)
-        bits |= KVQ_ERRBIT_PAGE;  // free twice
+    for (int i0 = at; i0 < count; i0 += kShBatch * threads) {
+      int page[kShBatch];
+#pragma unroll
+      for (int k = 0; k < kShBatch; ++k) page[k] = i0 < count - k * threads ? a.stack[i0 + k * threads] : INT_MAX;
+      uint32_t was[kShBatch];
+#pragma unroll
+      for (int k = 0; k < kShBatch; ++k) {
+        was[k] = 0;
+        if (page[k] >= 0 && page[k] < a.num_pages)
+          was[k] = atomicOr(a.words + (page[k] >> 5), 1u << (page[k] & 31)) >> (page[k] & 31) & 1;
+        else if (i0 < count - k * threads)
+          bits |= KVQ_ERRBIT_PAGE;
+      }
+#pragma unroll
+      for (int k = 0; k < kShBatch; ++k)
+        if (was[k]) bits |= KVQ_ERRBIT_PAGE;  // free twice
     }
   for (int b = at; b < a.B; b += threads)
     if (a.held[b] < 0 || a.held[b] > a.MP) bits |= KVQ_ERRBIT_POS;
-  if (bits) atomicOr(&sm.bits, bits);
-  unsigned int any = sh_bits(cl, sm);
+  unsigned int any = sh_bits(cl, sm, 0, bits);
   if (!any) {
     // ---- free pages before each word, and held pages that are none or free
     const int w0 = min(words, cta * share), w1 = min(words, w0 + share);
@@ -470,26 +580,27 @@ __global__ void __launch_bounds__(kShThreads, 1) compact_kernel(CompactArgs a) {
       if (w < w1) a.pre[w] = static_cast<int>(carry + pre);
       carry += total;
     }
-    if (tid == 0) sm.sum = carry;
-    for (int b = cta; b < a.B; b += ctas) {
-      const int32_t *row = a.table + static_cast<int64_t>(b) * a.MP;
-      const int held = a.held[b];
-      for (int j = tid; j < held; j += kShThreads) {
-        const int page = row[j];
-        if (page < 0 || page >= a.num_pages || (vol(a.words + (page >> 5)) >> (page & 31) & 1))
+    sh_sum(cl, sm, carry);
+    sh_held(a, sm, at, threads, [&](const int64_t(&idx)[kShBatch]) {
+      int page[kShBatch];
+#pragma unroll
+      for (int k = 0; k < kShBatch; ++k) page[k] = idx[k] < 0 ? INT_MIN : a.table[idx[k]];
+#pragma unroll
+      for (int k = 0; k < kShBatch; ++k) {
+        if (idx[k] < 0) continue;
+        if (page[k] < 0 || page[k] >= a.num_pages || (a.words[page[k] >> 5] >> (page[k] & 31) & 1))
           bits |= KVQ_ERRBIT_PAGE;
       }
-    }
-    if (bits) atomicOr(&sm.bits, bits);
-    any = sh_bits(cl, sm);
+    });
+    any = sh_bits(cl, sm, 1, bits);
     if (tid == 0) {
       int base = 0;
       for (int r = 0; r < ctas; ++r) {
         s_base[r] = base;
-        base += static_cast<int>(*cl.map_shared_rank(&sm.sum, r));
+        base += static_cast<int>(sm.sums[r]);
       }
     }
-    cl.sync();
+    __syncthreads();
   }
   if (any) {  // nothing changes
     for (int k = at; k < a.cap; k += threads) a.copy_src[k] = a.copy_dst[k] = -1;
@@ -501,43 +612,72 @@ __global__ void __launch_bounds__(kShThreads, 1) compact_kernel(CompactArgs a) {
   // free pages below id, and whether id is one
   auto free_below = [&](int id, bool &is_free) {
     const int w = id >> 5;
-    const uint32_t word = vol(a.words + w);
+    const uint32_t word = a.words[w];
     is_free = word >> (id & 31) & 1;
-    return s_base[w / share] + vol(a.pre + w) + __popc(word & ((1u << (id & 31)) - 1));
+    return s_base[w / share] + a.pre[w] + __popc(word & ((1u << (id & 31)) - 1));
   };
   bool unused;
   const int holes = live < a.num_pages ? free_below(live, unused) : count;
   const int stay = live - holes;  // live pages below `live`
-  for (int id = at; id < a.num_pages; id += threads) {
-    bool is_free;
-    const int f = free_below(id, is_free);
-    if (is_free && id < live) {
-      a.copy_dst[f] = id;
-      a.tags[id] += 1u;
-    } else if (!is_free && id >= live) {
-      a.copy_src[id - f - stay] = id;
+  for (int w = at; w < words; w += threads) {
+    const uint32_t word = a.words[w];
+    int f = s_base[w / share] + a.pre[w];  // free pages below
+    const int first = 32 * w, here = min(32, a.num_pages - first), low = min(max(live - first, 0), here);
+    const uint32_t below = low == 32 ? ~0u : (1u << low) - 1, all = here == 32 ? ~0u : (1u << here) - 1;
+    for (uint32_t x = word & below; x; x &= x - 1) {
+      const int id = first + __ffs(x) - 1;
+      a.copy_dst[f++] = id;
+      atomicAdd(a.tags + id, 1u);
+    }
+    for (uint32_t x = ~word & ~below & all; x; x &= x - 1) {
+      const int bit = __ffs(x) - 1;
+      a.copy_src[first + bit - (f + __popc(word & ~below & ((1u << bit) - 1))) - stay] = first + bit;
     }
   }
   for (int i = at; i < count; i += threads) a.stack[i] = a.num_pages - 1 - i;
   for (int k = holes + at; k < a.cap; k += threads) a.copy_src[k] = a.copy_dst[k] = -1;
   cl.sync();
-  for (int k = at; k < holes; k += threads) {
-    const int from = vol(a.copy_src + k), to = vol(a.copy_dst + k);
-    a.shares[to] = a.shares[from];
-    a.shares[from] = 0;
+  for (int i0 = at; i0 < holes; i0 += kShBatch * threads) {
+    int from[kShBatch], to[kShBatch], held[kShBatch];
+#pragma unroll
+    for (int k = 0; k < kShBatch; ++k)
+      if (i0 < holes - k * threads) {
+        from[k] = a.copy_src[i0 + k * threads];
+        to[k] = a.copy_dst[i0 + k * threads];
+      }
+#pragma unroll
+    for (int k = 0; k < kShBatch; ++k)
+      if (i0 < holes - k * threads) held[k] = a.shares[from[k]];
+#pragma unroll
+    for (int k = 0; k < kShBatch; ++k)
+      if (i0 < holes - k * threads) {
+        a.shares[to[k]] = held[k];
+        a.shares[from[k]] = 0;
+      }
   }
-  for (int b = cta; b < a.B; b += ctas) {
-    const int64_t row = static_cast<int64_t>(b) * a.MP;
-    const int held = a.held[b];
-    for (int j = tid; j < held; j += kShThreads) {
-      const int page = a.table[row + j];
-      if (page < live) continue;
+  sh_held(a, sm, at, threads, [&](const int64_t(&idx)[kShBatch]) {
+    int page[kShBatch], to[kShBatch];
+    uint32_t tag[kShBatch];
+#pragma unroll
+    for (int k = 0; k < kShBatch; ++k) page[k] = idx[k] < 0 ? -1 : a.table[idx[k]];
+#pragma unroll
+    for (int k = 0; k < kShBatch; ++k) {
+      to[k] = -1;
+      if (page[k] < live) continue;
       bool is_free;
-      const int to = vol(a.copy_dst + (page - free_below(page, is_free) - stay));
-      a.table[row + j] = to;
-      a.expected[row + j] = vol(a.tags + to);
+      const int f = free_below(page[k], is_free);
+      to[k] = a.copy_dst[page[k] - f - stay];
     }
-  }
+#pragma unroll
+    for (int k = 0; k < kShBatch; ++k)
+      if (to[k] >= 0) tag[k] = a.tags[to[k]];
+#pragma unroll
+    for (int k = 0; k < kShBatch; ++k)
+      if (to[k] >= 0) {
+        a.table[idx[k]] = to[k];
+        a.expected[idx[k]] = tag[k];
+      }
+  });
   if (at == 0) *a.moves = holes;
 }
 
