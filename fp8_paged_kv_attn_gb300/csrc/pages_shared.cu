@@ -4,17 +4,22 @@
 // shares[p] counts the block-table entries that hold page p beyond the first, so
 // a page that kvq_pages_update hands out needs no entry written: 0 is right.
 //
-// Each call is one cluster of up to 8 CTAs of 1,024 threads.  Its phases depend on
+// Each call is one cluster of up to 16 CTAs of 1,024 threads.  Its phases depend on
 // one another (a fork's pages on the forks before it, a page's place on the stack on
 // its last holder in the list) and are ordered by the cluster's hardware barrier, so that a
-// call is one launch, whatever its sizes, and its work spreads over 8,192 threads.  What
-// bounds it: a launch and a barrier a phase for short lists (5 - 9 us), and then the
-// latency of its scattered accesses (holders of a page), of which a thread has several in flight.
+// call is one launch, whatever its sizes.  What bounds it: for short lists a chain of four to
+// seven phases, each a barrier and one or two loads that wait for one another (4 forks of 700
+// tokens 9 us, 3 requests released 14, a pool of 2,048 pages moved together 15); for long ones
+// the rate at which an SM takes scattered accesses, a 32-byte sector each for 4 or 8 bytes (200
+// requests with 36,000 entries released: 47 us on 8 SMs, 25 on 16; a pool of 300,000 pages: 92
+// and 54).  A thread has four entries in flight, a warp neighbouring ones (a request's entries a
+// CTA at a time, one row behind the other, took 61 us for the pool of 2,048 pages).
 //
 // Lists are taken in rounds of 1,024 entries: every CTA scans a round's page counts, and
 // the round's pages ("items", in list order) are spread over the cluster by a binary
-// search of the scan.
+// search of the scan, once a warp's batch.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -26,7 +31,7 @@ namespace kvq {
 namespace cg = cooperative_groups;
 
 constexpr int kShThreads = 1024;
-constexpr int kShCtas = 8;
+constexpr int kShCtas = 16;
 constexpr int kShBatch = 4;  // items a thread has in flight
 
 struct ShSmem {
@@ -296,7 +301,7 @@ struct ReleaseArgs {
   int32_t *stack, *count, *shares, *table;
   const int32_t *req, *first, *npages;
   int32_t *claim;         // [B]
-  int32_t *gone, *last;   // [num_pages]: how many entries of the list hold a page, and the last one
+  int2 *gone;             // [num_pages]: how many entries of the list hold a page, and the last one
   uint32_t *err_word;
   int32_t num_pages, B, MP, n;
 };
@@ -396,8 +401,7 @@ __global__ void __launch_bounds__(kShThreads, 1) release_kernel(ReleaseArgs a) {
       if (page[k] < 0 || page[k] >= a.num_pages) {
         bits |= KVQ_ERRBIT_PAGE;
       } else if (entry[k]) {
-        a.gone[page[k]] = 0;
-        a.last[page[k]] = -1;
+        a.gone[page[k]] = make_int2(0, -1);
       }
     }
   });
@@ -413,8 +417,8 @@ __global__ void __launch_bounds__(kShThreads, 1) release_kernel(ReleaseArgs a) {
 #pragma unroll
     for (int k = 0; k < kShBatch; ++k)
       if (entry[k]) {
-        atomicAdd(a.gone + page[k], 1);
-        atomicMax(a.last + page[k], e + k);
+        atomicAdd(&a.gone[page[k]].x, 1);
+        atomicMax(&a.gone[page[k]].y, e + k);
       }
   });
   if (sh_bits(cl, sm, 2, bits)) {
@@ -434,8 +438,9 @@ __global__ void __launch_bounds__(kShThreads, 1) release_kernel(ReleaseArgs a) {
       h.last[k] = -1;
       h.gone[k] = h.shares[k] = 0;
       if (entry[k]) {
-        h.last[k] = vol(a.last + h.page[k]);
-        h.gone[k] = vol(a.gone + h.page[k]);
+        const int2 g = vol(a.gone + h.page[k]);
+        h.gone[k] = g.x;
+        h.last[k] = g.y;
         h.shares[k] = vol(a.shares + h.page[k]);
       }
     }
@@ -689,11 +694,44 @@ namespace {
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-// One cluster: a single CTA where a few thousand items at most are in hand (its barriers cost
-// less), else eight.
+// The largest cluster of the current device: 16 CTAs have to be asked for, and may not fit.
+template <typename Args>
+unsigned cluster_ctas(void (*kernel)(Args)) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<unsigned> most[kMaxDev];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 8;
+  unsigned ctas = most[dev].load(std::memory_order_acquire);
+  if (ctas) return ctas;
+  ctas = 8;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = kShCtas;
+    cfg.blockDim = kShThreads;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kShCtas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    if (cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) != cudaSuccess)
+      cudaGetLastError();
+    else if (fit > 0)
+      ctas = kShCtas;
+  } else {
+    cudaGetLastError();
+  }
+  most[dev].store(ctas, std::memory_order_release);
+  return ctas;
+}
+
+// One cluster: a single CTA where a few thousand items at most are in hand, else the largest (16 CTAs
+// against one: 176 entries forked 11.0 us and 9.0, 8,000 12.3 and 17.0, 32,000 15 and 40; 2,048 pages moved
+// together 16 and 14.5, 8,192 18 and 20.5).
 template <typename Args>
 cudaError_t launch_cluster(void (*kernel)(Args), int64_t items, cudaStream_t stream, const Args &args) {
-  const unsigned ctas = items <= 4 * kShThreads ? 1 : kShCtas;
+  const unsigned ctas = items <= 4 * kShThreads ? 1 : cluster_ctas(kernel);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = ctas;
   cfg.blockDim = kShThreads;
@@ -758,9 +796,9 @@ extern "C" kvq_status kvq_pages_release(int32_t *free_stack, int32_t *free_count
   if (!aligned256(workspace) || workspace_bytes < kvq_pages_workspace_size(num_pages, B))
     return KVQ_ERR_WORKSPACE;
   int32_t *claim = static_cast<int32_t *>(workspace);
-  int32_t *gone = claim + up256(4ull * B) / 4, *last = gone + up256(4ull * num_pages) / 4;
+  int2 *gone = reinterpret_cast<int2 *>(claim + up256(4ull * B) / 4);
   const ReleaseArgs args{free_stack, free_count, page_shares, block_table, rel_req, rel_first,
-                         rel_npages, claim,      gone,        last,        err_word, num_pages,
+                         rel_npages, claim,      gone,        err_word,    num_pages,
                          B,          MP,         n_rel};
   const cudaError_t e = launch_cluster(release_kernel, static_cast<int64_t>(n_rel) * MP,
                                        reinterpret_cast<cudaStream_t>(stream), args);
