@@ -459,13 +459,14 @@ __device__ __forceinline__ void px_plan(const PfArgs &a, int ctas) {
   const int64_t room = 2 * static_cast<int64_t>(a.rg.n_tokens);
   int64_t units = 0, count = 0;
   int n_grp = 0;
-  // groups in rounds of their own, so that the requests' items follow theirs
-  for (int i0 = 0; i0 < all; i0 += i0 < groups ? min(kPxQThreads, groups - i0) : kPxQThreads) {
+  // groups' items, then requests', in one list (in rounds of their own they cost a chain of loads each:
+  // 40 requests of five groups took 1.6 us more)
+  for (int i0 = 0; i0 < all; i0 += kPxQThreads) {
     const int i = i0 + threadIdx.x;
-    const bool grp = i0 < groups;
+    const bool grp = i < groups;
     PxItem o = {};
     bool has = false;
-    if (grp && i < groups) {
+    if (grp) {
       const int s = __ldg(a.group_start + i), e = __ldg(a.group_start + i + 1);
       const int pages = __ldg(a.prefix_pages + i);
       if (s < e && pages > 0 && pages <= a.MP) {
@@ -479,7 +480,7 @@ __device__ __forceinline__ void px_plan(const PfArgs &a, int ctas) {
             break;
           }
       }
-    } else if (!grp && i < all) {
+    } else if (i < all) {
       o.b = i - groups;
       PfReq q;
       if (order) {
@@ -513,7 +514,7 @@ __device__ __forceinline__ void px_plan(const PfArgs &a, int ctas) {
     if (has && at >= room) report(a.err_word, KVQ_ERRBIT_REQ);  // requests that own the same rows
     count += n_all;
     units += u_all;
-    if (grp) n_grp = static_cast<int>(min(count, room));
+    if (i0 < groups) n_grp += __syncthreads_count(has && grp);
   }
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -521,8 +522,8 @@ __device__ __forceinline__ void px_plan(const PfArgs &a, int ctas) {
     a.units[n] = total;
     a.plan->total = total;
     a.plan->per = max(static_cast<int64_t>(1), px_div(total + ctas - 1, ctas));
-    a.plan->n_grp = n_grp;
-    a.plan->n_req = static_cast<int>(n) - n_grp;
+    a.plan->n_grp = min(n_grp, static_cast<int>(n));
+    a.plan->n_req = max(static_cast<int>(n) - n_grp, 0);
   }
 }
 
