@@ -1533,7 +1533,7 @@ extern "C" kvq_status kvq_block_prefix_attn(
   at += px_q_bytes(n_tokens, Hq, D);
   a.qk = reinterpret_cast<float *>(at);
   at += px_qk_bytes(n_tokens, Hq);
-  const BaShape shape = ba_shape(max_q, G, Hkv, D, 0);
+  const BaShape shape = ba_shape(std::min(max_q, kPxOwnRows), G, Hkv, D, 0);
   a.own_split = static_cast<int64_t>(max_q) * G <= kPxOwnRows;
   a.hg = shape.hg;
   a.rt = shape.rt;

@@ -482,3 +482,142 @@ def test_a_run_of_forked_answers(kvq):
     kvq.kvq_pages_release(st, shares, i32(left), None, i32([-(-int(lens[b]) // P) for b in left]), ws, err_word=err)
     torch.cuda.synchronize()
     assert int(err.item()) == 0 and int(st.free_count.item()) == NP and not shares.any()
+
+
+def shared(s, G):
+    """Both of the kernels that attend to own tokens: a row a request, and more than they take at once."""
+    return ({}, {"max_q": 16 // G + 1})
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_largest_value_scales(kvq, D):
+    """Up to the largest fp32, with codes so small that the values are finite."""
+    rng = np.random.default_rng([24, D])
+    s = X.Step(rng, [(9, [(1, 200), (1, 3), (1, 90)]), (0, [(1, 640)])], 2, 16, D)
+    s.v &= 0x87  # at most 7 2^-9
+    e = rng.integers(124, 128, s.scales.shape[:2])
+    s.scales[:, :, 1] = np.ldexp(rng.integers(4, 8, e.shape) / 4.0, e)
+    s.scales[::3, :, 1] = np.float32(2.0 ** 127)
+    s.scales[1::5, :, 1] = np.finfo(np.float32).max
+    for kw in shared(s, 4):
+        check(kvq, s, 8, **kw)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_smallest_value_scales(kvq, D):
+    """Values near fp32's smallest normal number; scales that are subnormal.  An output may also be off
+    by a step of a subnormal bf16, 2^-133."""
+    rng = np.random.default_rng([25, D])
+    s = X.Step(rng, [(9, [(1, 200), (1, 3)]), (0, [(1, 300)])], 2, 16, D)
+    s.v = (s.v & 0x87) | 0x70  # 128 .. 240
+    s.scales[:, :, 1] = 2.0 ** -126
+    s.scales[1::2, :, 1] = np.float32(2.0 ** -126 * 0.8125)
+    s.scales[2::5, :, 1] = np.float32(2.0 ** -149)
+    q = R.values(rng, s.N, 8, D)
+    want, tol = X.attend([s.k, s.v], s.scales, q[1], s.tok_start, s.lens, s.table, D ** -0.5)
+    for kw in shared(s, 4):
+        out, err = attend(kvq, s, q[0], **kw)
+        assert err == 0
+        compare(out, want, tol - 1e-37 + 2.0 ** -133)
+
+
+def scored(rng, scores, pages, reqs, D, scale):
+    """A step of one group whose token j scores scores[j] ln 2 (at score scale ln 2) for every row: q and K are
+    zeros but in one dim, so that a score is one exact product."""
+    s = X.Step(rng, [(pages, reqs)], 1, 16, D)
+    s.k[:] = 0
+    s.scales[:, :, 0] = 1.0
+    s.scales[:, :, 1] = scale
+    codes = R.encode(scores / 16.0)
+    assert (R.decode(codes) * 16.0 == scores).all()
+    for b in range(s.B):
+        at = np.arange(int(s.lens[b]))
+        s.k[s.table[b, at // 16], 0, at % 16, 5] = codes[at]
+    q = np.zeros((s.N, 4, D))
+    q[:, :, 5] = 16.0
+    return s, R.bf16(q), (R.bf16(q).float().numpy().astype(np.float64))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("e,jump", [(0, 56.0), (60, 56.0), (110, 56.0), (110, 112.0), (-60, 224.0)])
+def test_large_values_behind_a_growing_maximum(kvq, D, e, jump):
+    """Scores that grow by 2^56 and more within a row, in the prefix and in own tokens: the references
+    are undone without overflow, whatever the V scales."""
+    rng = np.random.default_rng([26, D, abs(e)])
+    scores = rng.choice([0.4375, 0.8125, 2.75], 1000)
+    scores[300], scores[700] = jump, jump + (8 if jump < 112 else 16)
+    s, q, x = scored(rng, scores, 600 // 16, [(1, 408 - 8), (1, 30), (1, 300)], D, 2.0 ** e)
+    s.v = (s.v & 0x87) | 0x30  # 0.5 .. 0.94
+    for kw in shared(s, 4):
+        check(kvq, s, 4, q=(q, x), sm=float(np.log(2.0)), **kw)
+
+
+@pytest.mark.parametrize("gap", [16, 18, 20, 22, 24])
+def test_tokens_below_a_sink_without_value(kvq, gap):
+    """The first token's score is some `gap` ln 2 above the others', its values are zero: the others'
+    weights, all alike, are the output."""
+    rng = np.random.default_rng([27, gap])
+    scores = np.full(2000, {16: 0.4375, 18: 0.5625, 20: 0.625, 22: 0.8125, 24: 0.875}[gap])
+    scores[0] = gap
+    s, q, x = scored(rng, scores, 100, [(1, 300), (1, 9)], 128, 1.0)
+    s.v = (s.v & 0x07) | 0x38  # 1 .. 1.875, one sign: equal roundings do not even out
+    s.v[s.table[0, 0], :, 0] = 0
+    for kw in shared(s, 4):
+        check(kvq, s, 4, q=(q, x), sm=float(np.log(2.0)), **kw)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_sums_of_one_sign(kvq, D):
+    """Every weight alike and every value positive, so that what the tensor cores' additions lose adds up;
+    requests enough that one CTA sums whole prefixes."""
+    rng = np.random.default_rng([28, D])
+    s = X.Step(rng, [(40000 // 64, [(1, 20), (1, 1)])], 1, 64, D)
+    s.v &= 0x7F
+    q = np.zeros((s.N, 4, D))
+    check(kvq, s, 4, q=(R.bf16(q), q))
+    B = 160  # groups of one, the same pages: 160 rows of work for as many CTAs or fewer
+    s.B = s.N = B
+    s.n, s.lens = np.ones(B, dtype=np.int32), np.full(B, s.lens[1], dtype=np.int32)
+    s.table = np.repeat(s.table[1:], B, 0)
+    s.tok_start = s.group_start = np.arange(B + 1, dtype=np.int32)
+    s.pre = np.full(B, s.pre[0], dtype=np.int32)
+    one, tol = X.attend([s.k, s.v], s.scales, q[:1], s.tok_start[:2], s.lens[:1], s.table[:1], D ** -0.5)
+    q = np.zeros((B, 4, D))
+    out, err = attend(kvq, s, R.bf16(q))
+    assert err == 0
+    compare(out, np.repeat(one, B, 0), np.repeat(tol, B, 0))
+
+
+def test_the_largest_max_q_and_its_workspace(kvq):
+    """max_q is a limit, not a size; a workspace that is too small, or not aligned, is refused."""
+    rng = np.random.default_rng(29)
+    s = X.Step(rng, [(3, [(1, 20), (6, 9)])], 2, 16, 64)
+    check(kvq, s, 4, max_q=2 ** 31 - 1)
+    q = R.values(rng, s.N, 4, 64)[0]
+    ws = kvq.block_prefix_workspace(s.N, 4, 2, 64)
+    for bad in (ws[:-1], ws[16:]):
+        with pytest.raises(kvq.KvqError):
+            attend(kvq, s, q, ws=bad)
+
+
+def test_binding_refuses_other_shapes(kvq):
+    rng = np.random.default_rng(31)
+    s = X.Step(rng, [(3, [(1, 20), (1, 9)])], 2, 16, 64)
+    q = R.values(rng, s.N, 4, 64)[0]
+    one = np.array([1], dtype=np.int32)
+    for groups in ((None, s.pre), (s.group_start, None), (s.group_start, s.pre[:0]), (s.group_start.astype(np.int64), s.pre)):
+        with pytest.raises(ValueError):
+            attend(kvq, s, q, groups=groups)
+    with pytest.raises(ValueError):
+        attend(kvq, s, q, abort=np.zeros(3, dtype=np.uint8))
+    with pytest.raises(ValueError):
+        attend(kvq, s, q.float())
+    with pytest.raises(ValueError):
+        attend(kvq, s, q, lens=one)
+
+
+def test_many_groups_of_one(kvq):
+    """More groups than the plan takes at once, a request each, and empty ones in between."""
+    rng = np.random.default_rng(30)
+    s = X.Step(rng, [(1, [(1, int(rng.integers(1, 40)))]) if g % 3 else (2, []) for g in range(1700)], 1, 16, 64)
+    check(kvq, s, 4)
