@@ -1,5 +1,25 @@
 // kvq_block_prefix_attn: causal attention over the block-scaled cache for a batch
 // whose requests form groups with a shared prefix of whole pages.
+//
+// Softmax over a row's tokens in any number of parts: with m, a reference of the scores x (base 2), and
+// n, one of x + log2 v for the V scales v, a part is
+//   l = sum 2^(x - m),   O = sum (2^(x - m) v 2^(m - n) 2^7) c   (c a token's V code),
+// and parts are joined as  out = 2^(N - M - 7) sum_p 2^(n_p - N) O_p / sum_p 2^(m_p - M) l_p.
+// The two references keep the operand of the second product in f16's range however far apart the V
+// scales are; both follow their maxima lazily.  A prefix is a part of every row of its group, read once for
+// 128 rows of it (times heads a kv head); a request's own tokens are another.
+//
+// Four launches: the plan and q's pieces; prefixes (prefix_kernel, tcgen05); own tokens (the mma.sync kernel
+// of kvq_block_attn, where a request has few rows); the merge.  Measured on 256 requests of 64 heads over 8
+// behind 32,768 tokens: 6, 270, 28 and 15 us, which overlap to 317 in all (kvq_block_attn, which reads
+// the prefix for every request: 2,556).
+//
+// What bounds prefix_kernel: a tile (128 rows, 128 tokens, head_dim 128) is 1,080 cycles of the tensor core (8 of
+// its steps for the scores, q being two 8-bit pieces, 8 in f16 for the values) and some 1,150 of shared
+// memory (V goes through it a second time, as f16), and takes 2,380: tensor pipe 43%, issue slots 50%.  The softmax
+// groups need 3,500 - 4,000 cycles a tile each, two in turn, and the MMA warp's own instructions
+// and waits beside the softmax's take 1,300 a tile.  Weights are f16 (2^-11), not kvq_block_attn's four
+// 8-bit pieces (2^-19), since the output is bf16 (2^-8): a quarter of the products.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -93,7 +113,7 @@ __device__ __forceinline__ bool pf_group_ok(const PfArgs &a, int g) {
 
 constexpr int kPxTok = 128;         // tokens a tile
 constexpr int kPxRows = 128;        // rows a block
-constexpr int kPxRowCost = 3;       // a row of work's start and end, in tiles' times
+constexpr int kPxRowCost = 2;       // a row of work's start and end, in tiles' times (1 - 6: within 3%)
 constexpr int kPxSegs = 8;          // segment descriptors in flight
 constexpr int kPxStats = 4;         // segments whose statistics are in flight
 constexpr int kPxScales = 8;        // tiles whose scales are in flight
@@ -398,18 +418,6 @@ __device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t (&r)[8]) {
                : "memory");
 }
 
-// 16 columns, loaded and waited for in one statement as well.
-__device__ __forceinline__ void tc_ld16w(float (&v)[16], uint32_t addr) {
-  uint32_t *r = reinterpret_cast<uint32_t *>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr)
-      : "memory");
-}
-
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
@@ -663,6 +671,15 @@ __device__ __forceinline__ void px_mask(float (&x)[32], int see) {
     if (j >= see) x[j] = -INFINITY;
 }
 
+// One CTA an SM, each with its run of tiles; a tile passes, in turn,
+//   copies (a warp each for K and V, rings of four tiles; a warp for scales, eight tiles ahead),
+//   the MMA warp: S = q K^T into TMEM,
+//   a group of four softmax warps, a row a thread: maximum, references, weights into S's own columns in
+//     f16; tiles alternate between two groups, which hand the references on before they make the weights,
+//   the MMA warp: O += P V,
+// and beside them four side warps turn V's codes into f16, bring q in and take finished sums out.  A row a
+// thread: with two threads a row and 28 warps, 128 registers did not fit, and the exchange of maxima cost more
+// than it saved (256 requests behind 32k: 355 us, and 332).
 template <int D>
 __global__ void __launch_bounds__(kPxThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, PfArgs a) {
@@ -1465,7 +1482,10 @@ BaFn px_own_kernel(int rk) {
                  : rk == 8 ? block_split_kernel<D, 8, true> : block_split_kernel<D, 16, true>;
 }
 
-constexpr int kPxOwnRows = 16;  // rows (times heads a kv head) of a request that it takes
+// Rows (times heads a kv head) of a request that it takes, the most that its warps hold at once.  Both sides, us, it
+// and prefix_kernel: 256 requests of 1 - 700 own tokens, 4 rows 37 and 139, 8 rows 47 and 139, 16 rows 78 and 150;
+// 64 of 8,193, 8 rows 185 and 287, 16 rows 308 and 291.
+constexpr int kPxOwnRows = 16;
 
 // The slots of its parts, for every number of rows that a call may allow.
 size_t px_own_cut_bytes(int Hq, int Hkv, int D, int ctas) {

@@ -5,7 +5,8 @@
  * paged decode attention, and the weight-only INT4 / FP8 decode matrix
  * product; and the block-scaled form of the cache (a scale per page and kv head):
  * rotary positions, quantise-and-append, read-back, and causal attention of one
- * or several rows a request.  For NVIDIA GB300 (sm_103a).  Plain C ABI: pointers,
+ * or several rows a request, over a prefix that requests share or not; and pages that
+ * several requests hold: forked, released, moved together, copied.  For NVIDIA GB300 (sm_103a).  Plain C ABI: pointers,
  * sizes, a CUDA stream.  The library allocates no memory.
  *
  * Sources (web pages, cited by title and section):
@@ -590,14 +591,18 @@ KVQ_API size_t kvq_block_prefix_attn_workspace_size(int32_t n_tokens, int32_t Hq
  *     [n_tokens][Hq][head_dim], contiguous, rounded once.
  * Scores, softmax statistics and sums are fp32; a row of q is held to 2^-21 of its largest
  * value and a softmax weight to 2^-11 of itself (f16), or to 2^-31 of the row's largest (each
- * times its V scale) where that is more, so that nearly all of the output's error is its
- * rounding to bf16.
+ * times its V scale) where that is more; the tensor cores' additions truncate, which takes up to
+ * 2^-27 a token off a sum of one sign (2^-12 for 32k tokens).  So nearly all of the output's
+ * error is its rounding to bf16.  Own tokens of requests with at most 16 rows (times heads a kv
+ * head) are computed as kvq_block_attn computes them.  The call pays where requests share long
+ * prefixes; few requests behind a short one are served sooner by kvq_block_attn (4 behind 1,040
+ * tokens: 16 us, and 27 here).
  * Requests are refused as in kvq_block_attn, and with KVQ_ERRBIT_SEQLEN where a prefix is
  * negative or longer than MP pages, or reaches into a request's own rows, and with
  * KVQ_ERRBIT_REQ where a request's rows do not lie between those of its group's ends (tok_start
- * out of order): these requests' rows are zero.  A group_start out of order or range raises KVQ_ERRBIT_REQ, and every request's rows
- * are zero.  An aborted request's own pages are not read and its rows are zero; its group goes
- * on.  A page outside the pool raises KVQ_ERRBIT_PAGE and zeroes the rows that see it, in
+ * out of order): these requests' rows are zero.  A group_start out of order or range raises
+ * KVQ_ERRBIT_REQ, and every request's rows are zero.  An aborted request's own pages are not
+ * read and its rows are zero; its group goes on.  A page outside the pool raises KVQ_ERRBIT_PAGE and zeroes the rows that see it, in
  * a prefix those of the whole group.  Rows of nobody are left as they were.
  * max_q, strides, scales and limits as in kvq_block_attn; rows times heads a kv head are at most
  * 2^30.  workspace: 256-byte aligned, kvq_block_prefix_attn_workspace_size() bytes for this many
