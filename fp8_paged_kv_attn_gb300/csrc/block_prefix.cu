@@ -1314,6 +1314,7 @@ constexpr int kPxMergeWarps = 8;
 
 // One request of the plan, a warp a row and head, the lanes its dims; four parts' loads in flight.
 //   out = 2^(N - M) sum_p 2^(n_p - N) o_p / sum_p 2^(m_p - M) l_p
+// (a part 2^126 below the largest adds nothing: weights are held to 2^-31 of that)
 template <int D>
 __global__ void __launch_bounds__(32 * kPxMergeWarps) prefix_merge_kernel(PfArgs a) {
   constexpr int RF = D + kStat, V = D / 32, kBatch = 4;
@@ -1396,15 +1397,15 @@ __global__ void __launch_bounds__(32 * kPxMergeWarps) prefix_merge_kernel(PfArgs
         Nb = fmaxf(Nb, s[j].z);
         bad |= s[j].y < 0.f;
       }
-      const float fl = M == -INFINITY ? 0.f : exp2f(M - Mb), fo = N == -INFINITY ? 0.f : exp2f(N - Nb);
+      const float fl = M == -INFINITY ? 0.f : fast_exp2(M - Mb), fo = N == -INFINITY ? 0.f : fast_exp2(N - Nb);
       l *= fl;
 #pragma unroll
       for (int k = 0; k < V; ++k) acc[k] *= fo;
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         if (s[j].y == 0.f) continue;  // saw nothing
-        l = fmaf(exp2f(s[j].x - Mb), s[j].y, l);
-        const float f = exp2f(s[j].z - Nb);
+        l = fmaf(fast_exp2(s[j].x - Mb), s[j].y, l);
+        const float f = fast_exp2(s[j].z - Nb);
 #pragma unroll
         for (int k = 0; k < V; ++k) acc[k] = fmaf(f, v[j][k], acc[k]);
       }
