@@ -434,3 +434,49 @@ def test_decode_goes_on_after_fork_and_compaction(kvq):
     # alone, by one rounding of a code (2^-4) at most in K or V
     assert torch.equal(out[[0, 1, 3]], want[[0, 1, 3]])
     assert float((out[2] - want[2]).norm() / want[2].norm()) < 0.1
+
+
+def test_refusals_that_one_of_many_blocks_sees(kvq):
+    """Long lists, of more requests than a round takes, with one mistake at either end or in the middle: all
+    or nothing for the whole cluster, and it goes on afterwards."""
+    rng = np.random.default_rng(14)
+    B, MP = 1500, 24
+    held = rng.integers(0, MP + 1, B)
+    held[[0, 700, B - 1]] = 20
+    x = started(kvq, rng, int(held.sum()) + 900, B, MP, held)
+    order = rng.permutation(B)
+    order = np.r_[0, order[(order != 0) & (order != 700) & (order != B - 1)], 700, B - 1]
+    for b in (0, 700, B - 1):
+        for j, entry, shares in ((19, -1, None), (0, x.h.num_pages, None), (7, None, -1)):
+            page = x.h.block_table[b, j]
+            if shares is not None:
+                x.h.shares[page] = shares
+            else:
+                x.h.block_table[b, j] = entry
+            x.upload()
+            assert x.release(order, None, held[order]) == S.PAGE
+            if shares is None:
+                assert x.compact(held)[3] == S.PAGE
+            x.h.shares[page], x.h.block_table[b, j] = 0, page
+            x.upload()
+        assert x.release(np.r_[order, b], None, np.r_[held[order], 1]) & S.REQ
+        at = int(np.flatnonzero(order == b)[0])
+        n = held[order]
+        n[at] = MP + 1
+        assert x.release(order, None, n) == S.POS
+        assert x.compact(np.where(np.arange(B) == b, MP + 1, held))[3] == S.POS
+    for at in (0, int(x.h.free_count[0]) - 1):
+        was = x.h.free_stack[at]
+        for bad in (x.h.num_pages, x.h.free_stack[at - 1] if at else x.h.free_stack[1]):
+            x.h.free_stack[at] = bad
+            x.upload()
+            assert x.compact(held)[3] == S.PAGE
+        x.h.free_stack[at] = was
+        x.upload()
+    assert x.release(order[1:1200], None, held[order[1:1200]]) == 0
+    gone = np.zeros(B, dtype=bool)
+    gone[order[1:1200]] = True
+    held[gone] = 0
+    x.compact(held)
+    src = rng.choice(np.flatnonzero(held), 1100)
+    x.fork(src, np.flatnonzero(gone)[:1100], (held[src] * 16 * rng.random(1100)).astype(int), 16)
