@@ -11,7 +11,7 @@
 //
 // Four launches: the plan and q's pieces; prefixes (prefix_kernel, tcgen05); own tokens (the mma.sync kernel
 // of kvq_block_attn, where a request has few rows); the merge.  Measured on 256 requests of 64 heads over 8
-// behind 32,768 tokens: 6, 270, 28 and 15 us, which overlap to 317 in all (kvq_block_attn, which reads
+// behind 32,768 tokens: 10, 274, 28 and 20 us one by one and cold, 316 in all (kvq_block_attn, which reads
 // the prefix for every request: 2,556).
 //
 // What bounds prefix_kernel: a tile (128 rows, 128 tokens, head_dim 128) is 1,080 cycles of the tensor core (8 of
@@ -678,8 +678,8 @@ __device__ __forceinline__ void px_mask(float (&x)[32], int see) {
 //     f16; tiles alternate between two groups, which hand the references on before they make the weights,
 //   the MMA warp: O += P V,
 // and beside them four side warps turn V's codes into f16, bring q in and take finished sums out.  A row a
-// thread: with two threads a row and 28 warps, 128 registers did not fit, and the exchange of maxima cost more
-// than it saved (256 requests behind 32k: 355 us, and 332).
+// thread: with two (16 softmax warps of 80 registers, which exchange their maxima) 256 requests behind 32k take 326
+// us, and 316 with one.
 template <int D>
 __global__ void __launch_bounds__(kPxThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, PfArgs a) {
@@ -872,52 +872,15 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       kt = 0;
       return k_in = true;
     };
-    // a tile's scores, whose K is there
-    auto scores = [&]() {
-      const int slot = kg % kPxK, qs = ks % kPxQs<D>, n = tokens(k_len, kt);
-      const bool last = kt + 1 == k_tiles;
-      const uint64_t kd = px_kdesc<D>(k_a + slot * S::kTile);
-      const uint32_t q = tmem + kPxQ + qs * (D / 2), to = tmem + px_scol(kg, 0);
-      auto mma = [&](uint32_t at, uint64_t rows, int cols) {
-        if (elect_one())
-#pragma unroll
-          for (int piece = 1; piece >= 0; --piece)  // the smaller first: each sum is truncated
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-              px_mma8(at, q + piece * (D / 4) + 8 * k, rows + 2 * k, cols, piece == 1, piece == 0 || k > 0);
-        __syncwarp();
-      };
-      if (to - tmem != 256) {
-        mma(to, kd, n);
-      } else {  // the ring's end (half a tile's product takes as long as a whole one's: one tile in five)
-        mma(to, kd, min(n, 64));
-        if (n > 64) mma(tmem, kd + (S::kTile / 2 >> 4), n - 64);
-      }
-      if (elect_one()) {
-        bar_commit(bar(kSFull + (kg & 1)));
-        bar_commit(bar(kKEmpty + slot));
-      }
-      __syncwarp();
-      // (a condition within the elected lane's block lost the commit: it stands around the election)
-      if (last && elect_one()) bar_commit(bar(kQFree + qs));
-      __syncwarp();
-      ++kg;
-      ++kt;
-      if (last) {
-        k_in = false;
-        ++ks;
-      }
-    };
+    // Each turn: the first half of a tile's values, then the scores two tiles on, if they can be, then the other
+    // half; scores alone where they are not that far ahead.
     while (ok) {
-      while (ok && !k_end && kg - pg < 2) {
-        if (!k_in && !next(kg == pg)) break;
-        ok = wait(kKFull + kg % kPxK, (kg / kPxK) & 1);
-        if (!ok) break;
-        tc_after();
-        scores();
-      }
-      if (!ok || (k_end && kg == pg)) break;
-      if (!p_in) {
+      const bool more = !k_end && (k_in || next(kg == pg));  // the next scores' segment is here
+      if (!ok || (!more && kg == pg)) break;
+      const bool pv = kg - pg == 2 || !more;
+      const int buf = pg & 1, slot = kg % kPxK;
+      const uint32_t par = (pg >> 1) & 1, kpar = (kg / kPxK) & 1;
+      if (pv && !p_in) {
         const PxSeg &sg = ctl.seg[ps % kPxSegs];  // (its scores have been issued)
         p_tiles = sg.tiles;
         p_len = sg.t_end - sg.tok;
@@ -926,16 +889,13 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         ok = ps == 0 || wait(kOFree, (ps - 1) & 1);
         if (!ok) break;
       }
-      const int buf = pg & 1;
-      const uint32_t par = (pg >> 1) & 1;
-      const bool last = pt + 1 == p_tiles, ahead = !k_end && kg - pg == 2 && (k_in || next(false));
-      if (!ok) break;
       {  // a round trip is some 150 cycles beside the tiles' traffic: the tests go out together
-        const int kb = ahead ? kKFull + kg % kPxK : kHFull + buf;
-        const uint32_t kp = ahead ? (kg / kPxK) & 1 : par;
-        const uint32_t x = test(kb, kp), y = test(kHFull + buf, par), z = test(kPHalf + buf, par);
-        ok = __all_sync(0xffffffffu, x & y & z) ||
-             (wait(kb, kp) && wait(kHFull + buf, par) && wait(kPHalf + buf, par));
+        const int kb = more ? kKFull + slot : kHFull + buf, vb = pv ? kHFull + buf : kb;
+        const uint32_t kp = more ? kpar : par, vp = pv ? par : kp;
+        const int hb = pv ? kPHalf + buf : kb;
+        const uint32_t hp = pv ? par : kp;
+        const uint32_t x = test(kb, kp), y = test(vb, vp), z = test(hb, hp);
+        ok = __all_sync(0xffffffffu, x & y & z) || (wait(kb, kp) && wait(vb, vp) && wait(hb, hp));
       }
       if (!ok) break;
       tc_after();
@@ -953,12 +913,47 @@ __global__ void __launch_bounds__(kPxThreads, 1)
               px_mma16(tmem + kPxO, p + 32 * (k >> 1) + 8 * (k & 1), rows + k * (16 * 128 >> 4), D, pt + half + k > 0);
         __syncwarp();
       };
-      values(0);
-      if (ahead) scores();
+      if (pv) values(0);
+      if (more) {
+        const int n = tokens(k_len, kt), qs = ks % kPxQs<D>;
+        const uint32_t q = tmem + kPxQ + qs * (D / 2);
+        uint32_t to = px_scol(kg, 0);
+        // at the ring's end in two (half a tile's product takes 0.65 of a whole one's: one tile in five)
+        const int wide = to == 256 ? 64 : kPxTok;
+#pragma unroll 1
+        for (int at = 0; at < n; at += wide, to = 0) {
+          const uint64_t kd = px_kdesc<D>(k_a + slot * S::kTile) + (at * D >> 4);
+          const int cols = min(n - at, wide);
+          if (elect_one())
+#pragma unroll
+            for (int piece = 1; piece >= 0; --piece)  // the smaller first: each sum is truncated
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k)
+                px_mma8(tmem + to, q + piece * (D / 4) + 8 * k, kd + 2 * k, cols, piece == 1, piece == 0 || k > 0);
+          __syncwarp();
+        }
+        const bool last = kt + 1 == k_tiles;
+        if (elect_one()) {
+          bar_commit(bar(kSFull + (kg & 1)));
+          bar_commit(bar(kKEmpty + slot));
+        }
+        __syncwarp();
+        // (a condition within the elected lane's block lost the commit: it stands around the election)
+        if (last && elect_one()) bar_commit(bar(kQFree + qs));
+        __syncwarp();
+        ++kg;
+        ++kt;
+        if (last) {
+          k_in = false;
+          ++ks;
+        }
+      }
+      if (!pv) continue;
       ok = wait(kPFull + buf, par);
       if (!ok) break;
       tc_after();
       values(1);
+      const bool last = pt + 1 == p_tiles;
       if (elect_one()) bar_commit(bar(kHEmpty + buf));
       __syncwarp();
       if (last && elect_one()) bar_commit(bar(kODone));
