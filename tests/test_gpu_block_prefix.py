@@ -621,3 +621,19 @@ def test_many_groups_of_one(kvq):
     rng = np.random.default_rng(30)
     s = X.Step(rng, [(1, [(1, int(rng.integers(1, 40)))]) if g % 3 else (2, []) for g in range(1700)], 1, 16, 64)
     check(kvq, s, 4)
+
+
+@pytest.mark.parametrize("max_q", [1, 9])
+def test_nobody_takes_part(kvq, max_q):
+    """Every request aborted, or without rows, or refused: zeros, and rows of nobody left as they were."""
+    rng = np.random.default_rng(32)
+    s = X.Step(rng, [(3, [(1, 20), (1, 9)]), (1, [(1, 30)])], 2, 16, 128, pad=2)
+    check(kvq, s, 8, max_q=max_q, skip=(0, 1, 2), abort=np.ones(3, dtype=np.uint8))
+    lens = s.lens.copy()
+    s.lens[:] = [0, -1, 1 << 30]
+    check(kvq, s, 8, max_q=max_q, skip=(0, 1, 2), bits=2)  # KVQ_ERRBIT_SEQLEN
+    s.lens = lens
+    s.tok_start[:] = 0
+    check(kvq, s, 8, max_q=max_q)
+    s.tok_start[:] = [0, 0, 0, s.N]  # one request has all the rows
+    check(kvq, s, 8, max_q=9)
