@@ -253,8 +253,12 @@ enum : int {
   kHFull = kQReady + kPxStats,
   kOFree = kHFull + 2,
   kPHalf,  // a group's weights for the first 64 tokens of a tile
+  // All of a tile's weights.  Four in turn: the scores two tiles on come once a tile's first half is there, so
+  // that a warp that is ahead (one without rows has nothing else to wait for) ends the group's next tile while
+  // another is still at this one.  On one barrier a group its second arrival stood for the other's, and scores
+  // were taken for weights.  The scores four tiles on come behind all arrivals for this tile.
   kPFull = kPHalf + 2,
-  kStatFull = kPFull + 2,  // softmax and sides
+  kStatFull = kPFull + 4,  // softmax and sides
   kSegEmpty = kStatFull + kPxStats,  // everybody but the copies
   kBars = kSegEmpty + kPxSegs
 };
@@ -949,7 +953,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         }
       }
       if (!pv) continue;
-      ok = wait(kPFull + buf, par);
+      ok = wait(kPFull + (pg & 3), (pg >> 2) & 1);
       if (!ok) break;
       tc_after();
       values(1);
@@ -1269,7 +1273,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             tc_st_wait();
             tc_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(bar(h ? kPFull + grp : kPHalf + grp));
+            if (lane == 0) bar_arrive(bar(h ? kPFull + (gt & 3) : kPHalf + grp));
           }
           if (!ok) break;
           l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
@@ -1278,7 +1282,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           __syncwarp();
           if (lane == 0) {
             bar_arrive(bar(kPHalf + grp));
-            bar_arrive(bar(kPFull + grp));
+            bar_arrive(bar(kPFull + (gt & 3)));
           }
         }
       }
