@@ -150,6 +150,8 @@ struct ForkArgs {
   int32_t num_pages, B, MP, page_size, n;
 };
 
+constexpr uint8_t kForkBad = 2;  // fork_ok while the call runs: 1 or this, for a fork with an entry that is no page
+
 __global__ void __launch_bounds__(kShThreads, 1) fork_kernel(ForkArgs a) {
   __shared__ ShSmem sm;
   cg::cluster_group cl = cg::this_cluster();
@@ -195,7 +197,8 @@ __global__ void __launch_bounds__(kShThreads, 1) fork_kernel(ForkArgs a) {
     a.ok[i] = valid;
   }
   cl.sync();
-  // ---- every page that a fork takes, or copies, is a page
+  // ---- every page that a fork takes, or copies, is a page.  A fork that is found bad keeps a mark other than 0: the
+  // CTAs lay a round's items out by its flags, each at its own time, and have to find the same ones.
   for (int r0 = 0; r0 < a.n; r0 += kShThreads) {
     const int i = r0 + tid, m = min(kShThreads, a.n - r0);
     long long pages = 0, total;
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(kShThreads, 1) fork_kernel(ForkArgs a) {
 #pragma unroll
       for (int k = 0; k < kShBatch; ++k)
         if (page[k] < 0 || page[k] >= a.num_pages) {
-          a.ok[r0 + o[k]] = 0;
+          a.ok[r0 + o[k]] = kForkBad;
           bits |= KVQ_ERRBIT_PAGE;
         }
     }
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(kShThreads, 1) fork_kernel(ForkArgs a) {
   long long wanted = 0, taken = 0;
   for (int r0 = 0; r0 < a.n; r0 += kShThreads) {
     const int i = r0 + tid, m = min(kShThreads, a.n - r0);
-    const bool valid = i < a.n && vol(a.ok + i) != 0;
+    const bool valid = i < a.n && vol(a.ok + i) == 1;
     int s = 0, d = 0, full = 0, cut = 0;
     if (valid) {
       s = a.src[i];
@@ -278,7 +281,7 @@ __global__ void __launch_bounds__(kShThreads, 1) fork_kernel(ForkArgs a) {
       }
 #pragma unroll
       for (int k = 0; k < kShBatch; ++k)
-        if (page[k] >= 0) {
+        if (page[k] >= 0 && page[k] < a.num_pages) {
           a.table[to[k]] = page[k];
           a.expected[to[k]] = tag[k];
           atomicAdd(a.shares + page[k], 1);
