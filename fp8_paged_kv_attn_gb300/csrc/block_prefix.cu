@@ -113,6 +113,11 @@ __device__ __forceinline__ bool pf_group_ok(const PfArgs &a, int g) {
 
 constexpr int kPxTok = 128;         // tokens a tile
 constexpr int kPxRows = 128;        // rows a block
+// Tiles of a row of work that the tensor core sums before the sums are taken out and added with rounding.  Its
+// additions truncate, up to 2^-27 of a sum of one sign for each token: 2^-12 for these 32,768, and half a bf16
+// step for 262,144 (summed without a limit, a million tokens' means that stand 2^-11 above a rounding's
+// border came out a bf16 step too small).
+constexpr int kPxSumTiles = 256;
 constexpr int kPxRowCost = 2;       // a row of work's start and end, in tiles' times (1 - 6: within 3%)
 constexpr int kPxSegs = 8;          // segment descriptors in flight
 constexpr int kPxStats = 4;         // segments whose statistics are in flight
@@ -154,6 +159,7 @@ struct PxSeg {
   int lim0;                // tokens that the item's first token row sees, each next one more; 0: all see all
   int part, parts;         // the slot of a row of work that CTAs share, and how many share it
   int own, pre;
+  int again, more;         // the row of work has earlier, further segments in this CTA (kPxSumTiles)
 };
 
 // A producer's way through its CTA's run [u0, u1); every lane of the warp keeps the same.  Where
@@ -196,13 +202,20 @@ __device__ __noinline__ bool px_next(const PfArgs &a, PxWalk &w, PxSeg &sg) {
       w.tiles = px_tiles(a, w.it, 0);
     }
     // units [0, kPxRowCost) of a row of work stand for its start; tile t is unit kPxRowCost + t
-    const int span = static_cast<int>(min(static_cast<int64_t>(w.tiles + kPxRowCost - w.at), w.u1 - w.u));
-    const int t0 = max(0, w.at - kPxRowCost), take = w.at + span - kPxRowCost - t0;
+    int span = static_cast<int>(min(static_cast<int64_t>(w.tiles + kPxRowCost - w.at), w.u1 - w.u));
+    const int t0 = max(0, w.at - kPxRowCost);
+    int take = w.at + span - kPxRowCost - t0;
     const int64_t ut = w.u - w.at + kPxRowCost;  // its first tile
+    sg.again = t0 > 0 && w.u > w.u0;
+    sg.more = take > kPxSumTiles;
+    if (sg.more) {
+      span -= take - kPxSumTiles;
+      take = kPxSumTiles;
+    }
     sg.parts = 1;
     if (ut < w.u0 || ut + w.tiles > w.u0 + w.per)
       sg.parts = static_cast<int>(px_div(ut + w.tiles - 1, w.per) - px_div(ut, w.per)) + 1;
-    sg.part = sg.parts == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (t0 == 0 ? 1 : 0);
+    sg.part = sg.parts == 1 ? -1 : 2 * static_cast<int>(blockIdx.x) + (ut >= w.u0 ? 1 : 0);
     sg.b = w.it.b;
     sg.head = w.head;
     sg.rb = w.rb;
@@ -675,6 +688,44 @@ __device__ __forceinline__ void px_mask(float (&x)[32], int see) {
     if (j >= see) x[j] = -INFINITY;
 }
 
+// A further segment of a row of work (kPxSumTiles): its sums O and statistics (m, l, n) are added to what lies
+// in `to`, which this lane wrote, or with `out` the joined row is written.  The joined statistics.  Out of line,
+// since segments that long are few: within the sides' loop it took 256 requests behind 32k from 314 to 329 us.
+template <int D>
+__device__ __noinline__ float4 px_join(uint32_t o_addr, float *to, float4 s, bool has, uint16_t *out) {
+  float4 was = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+  if (has) was = *reinterpret_cast<const float4 *>(to + D);
+  const float M = fmaxf(was.x, s.x), N = fmaxf(was.z, s.z);
+  const bool bad = was.y < 0.f || s.y < 0.f;
+  // who saw nothing (l = 0) has no maximum and no weight
+  const float x = was.y == 0.f ? 0.f : exp2f(was.z - N), y = s.y == 0.f ? 0.f : exp2f(s.z - N);
+  const float l = bad ? -1.f
+                      : (was.y == 0.f ? 0.f : was.y * exp2f(was.x - M)) + (s.y == 0.f ? 0.f : s.y * exp2f(s.x - M));
+  const float2 f = bad ? make_float2(0.f, 0.f) : out_scale(N - M - 7.f, l);
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    float o[16];
+    tc_ld16(o, o_addr + c);
+    if (!has) continue;
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float4 v = *reinterpret_cast<const float4 *>(to + c + 4 * j);
+      v = make_float4(v.x * x + o[4 * j] * y, v.y * x + o[4 * j + 1] * y, v.z * x + o[4 * j + 2] * y,
+                      v.w * x + o[4 * j + 3] * y);
+      if (!out) *reinterpret_cast<float4 *>(to + c + 4 * j) = v;
+      w[2 * j] = bad ? 0u : pack_bf16x2(v.x * f.x * f.y, v.y * f.x * f.y);
+      w[2 * j + 1] = bad ? 0u : pack_bf16x2(v.z * f.x * f.y, v.w * f.x * f.y);
+    }
+    if (out) {
+      *reinterpret_cast<uint4 *>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4 *>(out + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+  if (has) *reinterpret_cast<float4 *>(to + D) = make_float4(M, l, N, out ? kDone : kHere);
+  return make_float4(M, l, N, 0.f);
+}
+
 // One CTA an SM, each with its run of tiles; a tile passes, in turn,
 //   copies (a warp each for K and V, rings of four tiles; a warp for scales, eight tiles ahead),
 //   the MMA warp: S = q K^T into TMEM,
@@ -994,16 +1045,20 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const int fin = ctl.come[ks][1] > ctl.come[ks][0];  // who had the last tile
         const float4 e0 = ctl.end[ks][fin][r], e1 = ctl.end[ks][fin ^ 1][r];
         const float M = e0.x, N = e0.z;
-        const bool bad = e0.y < 0.f || e1.y < 0.f;
+        bool bad = e0.y < 0.f || e1.y < 0.f;
         float l = e0.y;
         if (e1.y != 0.f) l += e1.y * exp2f(e1.x - M);
-        if (bad) l = -1.f;
-        const bool whole = sg.part < 0 && sg.own && !sg.pre;  // nothing to be merged with
+        const bool whole = sg.part < 0 && sg.own && !sg.pre && !sg.more;  // nothing to be merged with
         const int64_t at = (static_cast<int64_t>(sg.row0) + i) * a.Hq + sg.head * a.G + row - i * a.G;
         float *here = a.rows + (static_cast<int64_t>(sg.own) * a.rg.n_tokens * a.Hq + at) * RF;
         float *to = sg.part < 0 ? here : a.cut + (static_cast<int64_t>(sg.part) * kPxRows + r) * RF;
         const bool has = r < sg.rows;
-        if (has) {
+        if (bad) l = -1.f;
+        if (sg.again) {
+          const float4 all = px_join<D>(tmem + lanes + kPxO, to, make_float4(M, l, N, 0.f), has, whole ? a.out + at * D : nullptr);
+          bad = all.y < 0.f;
+        }
+        if (has && !sg.again) {
           *reinterpret_cast<float4 *>(to + D) = make_float4(M, l, N, whole ? kDone : kHere);
           if (sg.part >= 0 && (sg.part & 1))  // the first part: where the others are
             *reinterpret_cast<float4 *>(here + D) =
@@ -1014,7 +1069,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const bool nan = ctl.nan_seg[ks] == static_cast<int>(k) + 1;
         const int lim = sg.lim0 ? sg.lim0 + i : INT_MAX;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = sg.again ? D : 0; c < D; c += 32) {
           float o[32];
           tc_ld32(o, tmem + lanes + kPxO + c);
           if (!has) continue;

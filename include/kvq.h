@@ -592,8 +592,9 @@ KVQ_API size_t kvq_block_prefix_attn_workspace_size(int32_t n_tokens, int32_t Hq
  * Scores, softmax statistics and sums are fp32; a row of q is held to 2^-21 of its largest
  * value and a softmax weight to 2^-11 of itself (f16), or to 2^-31 of the row's largest (each
  * times its V scale) where that is more; the tensor cores' additions truncate, which takes up to
- * 2^-27 a token off a sum of one sign (2^-12 for 32k tokens).  So nearly all of the output's
- * error is its rounding to bf16.  Own tokens of requests with at most 16 rows (times heads a kv
+ * 2^-27 a token off a sum of one sign, for at most 32,768 tokens (2^-12): longer ones are summed
+ * in parts, joined in fp32.  So nearly all of the output's error is its rounding to bf16, however
+ * long the prefix.  Own tokens of requests with at most 16 rows (times heads a kv
  * head) are computed as kvq_block_attn computes them.  The call pays where requests share long
  * prefixes; few requests behind a short one are served sooner by kvq_block_attn (4 behind 1,040
  * tokens: 16 us, and 27 here).

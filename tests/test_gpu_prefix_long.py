@@ -5,6 +5,8 @@ import pytest
 import torch
 
 import block_ref as R
+import prefix_ref as X
+from test_gpu_block_prefix import attend, compare
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +81,57 @@ def test_long_sums_are_rounded_between(kvq, D, tokens, B, own, G):
     got = out.double().cpu()
     wrong = got != want
     assert not wrong.any(), (float(wrong.double().mean()), got[wrong][0], want.expand_as(got)[wrong][0])
+
+
+def repeated(s, B):
+    """The step's one request B times, each a group of its own: rows of work enough that a CTA has whole ones."""
+    n = int(s.n[0])
+    s.B, s.N = B, B * n
+    s.n, s.lens, s.table = np.repeat(s.n, B), np.repeat(s.lens, B), np.repeat(s.table, B, 0)
+    s.tok_start = np.arange(0, (B + 1) * n, n, dtype=np.int32)
+    s.group_start, s.pre = np.arange(B + 1, dtype=np.int32), np.repeat(s.pre, B)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("own", [False, True])
+def test_joined_sums(kvq, D, own):
+    """Sums that are taken out in between and joined: maxima that rise and fall, V scales 2^60 apart from one
+    stretch of the prefix to the next, NaN codes and pages outside the pool in the first or the last of them."""
+    rng = np.random.default_rng([41, D, own])
+    s = X.Step(rng, [(0, [(3, 90001)])] if own else [(90001 // P, [(3, 7)])], 1, P, D)
+    at = np.arange(s.MP) * P
+    for stretch, (k, v) in enumerate(((-2, 20), (1, -40), (0, 0), (2, 20))):
+        pages = s.table[0, (at >= 25000 * stretch) & (at < 25000 * (stretch + 1))]
+        pages = pages[pages >= 0]
+        s.scales[pages, :, 0] *= np.float32(2.0 ** k)
+        s.scales[pages, :, 1] *= np.float32(2.0 ** v)
+    G, B = 2, 160
+    q = R.values(rng, s.N, G, D)
+    want, tol = X.attend([s.k, s.v], s.scales, q[1], s.tok_start, s.lens, s.table, D ** -0.5)
+    n = s.N
+    repeated(s, B)
+    want, tol, qs = np.tile(want, (B, 1, 1)), np.tile(tol, (B, 1, 1)), q[0].repeat(B, 1, 1)
+    kw = dict(max_q=9)
+    if own:
+        kw["groups"] = (None, None)
+    out, err = attend(kvq, s, qs, **kw)
+    assert err == 0
+    compare(out, want, tol)
+    for token in (100, 40000, 89000):
+        page, slot = s.table[0, token // P], token % P
+        was = s.v[page, 0, slot, 3]
+        s.v[page, 0, slot, 3] = 0x7F
+        out, err = attend(kvq, s, qs, **kw)
+        s.v[page, 0, slot, 3] = was
+        assert err == 0 and bool(out[:, :, 3].isnan().all())
+        out[:, :, 3] = 0
+        other = want.copy()
+        other[:, :, 3] = 0
+        compare(out, other, tol)
+        table = s.table.copy()
+        table[::2, token // P] = s.NP
+        out, err = attend(kvq, s, qs, table=table, **kw)
+        assert err == kvq.ERRBIT_PAGE
+        other, none = want.reshape(B, n, G, D).copy(), tol.reshape(B, n, G, D).copy()
+        other[::2], none[::2] = 0, 0
+        compare(out, other.reshape(want.shape), none.reshape(tol.shape))
