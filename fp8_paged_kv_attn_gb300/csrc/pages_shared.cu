@@ -695,6 +695,11 @@ __global__ void __launch_bounds__(kShThreads, 1) compact_kernel(CompactArgs a) {
 
 namespace {
 
+// The kernels step through their lists with 32-bit counters, up to 65,536 ahead.
+bool sh_sizes_ok(int32_t num_pages, int32_t B, int32_t list) {
+  return std::max({num_pages, B, list}) <= 1 << 30;
+}
+
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // The largest cluster of the current device: 16 CTAs have to be asked for, and may not fit.
@@ -757,7 +762,7 @@ cudaError_t launch_cluster(void (*kernel)(Args), int64_t items, cudaStream_t str
 using namespace kvq;
 
 extern "C" size_t kvq_pages_workspace_size(int32_t num_pages, int32_t B) {
-  if (num_pages <= 0 || B <= 0) return 0;
+  if (num_pages <= 0 || B <= 0 || !sh_sizes_ok(num_pages, B, 0)) return 0;
   return up256(4ull * B) + 2 * up256(4ull * num_pages);
 }
 
@@ -769,7 +774,8 @@ extern "C" kvq_status kvq_pages_fork(int32_t *free_stack, int32_t *free_count, u
                                      int32_t n_fork, int32_t *copy_src, int32_t *copy_dst,
                                      uint8_t *fork_ok, void *workspace, size_t workspace_bytes,
                                      uint32_t *err_word, kvq_stream_t stream) {
-  if (num_pages <= 0 || B <= 0 || MP <= 0 || page_size <= 0 || n_fork < 0) return KVQ_ERR_INVALID_ARG;
+  if (num_pages <= 0 || B <= 0 || MP <= 0 || page_size <= 0 || n_fork < 0 || !sh_sizes_ok(num_pages, B, n_fork))
+    return KVQ_ERR_INVALID_ARG;
   if (!free_stack || !free_count || !page_tags || !page_shares || !block_table || !expected_tags)
     return KVQ_ERR_INVALID_ARG;
   if (n_fork == 0) return KVQ_OK;
@@ -792,7 +798,7 @@ extern "C" kvq_status kvq_pages_release(int32_t *free_stack, int32_t *free_count
                                         const int32_t *rel_npages, int32_t n_rel, void *workspace,
                                         size_t workspace_bytes, uint32_t *err_word,
                                         kvq_stream_t stream) {
-  if (num_pages <= 0 || B <= 0 || MP <= 0 || n_rel < 0) return KVQ_ERR_INVALID_ARG;
+  if (num_pages <= 0 || B <= 0 || MP <= 0 || n_rel < 0 || !sh_sizes_ok(num_pages, B, n_rel)) return KVQ_ERR_INVALID_ARG;
   if (!free_stack || !free_count || !page_shares || !block_table) return KVQ_ERR_INVALID_ARG;
   if (n_rel == 0) return KVQ_OK;
   if (!rel_req || !rel_npages || !workspace) return KVQ_ERR_INVALID_ARG;
@@ -816,7 +822,8 @@ extern "C" kvq_status kvq_pages_compact(int32_t *free_stack, int32_t *free_count
                                         int32_t copy_cap, int32_t *n_moves, void *workspace,
                                         size_t workspace_bytes, uint32_t *err_word,
                                         kvq_stream_t stream) {
-  if (num_pages <= 0 || B <= 0 || MP <= 0 || copy_cap < num_pages / 2) return KVQ_ERR_INVALID_ARG;
+  if (num_pages <= 0 || B <= 0 || MP <= 0 || copy_cap < num_pages / 2 || !sh_sizes_ok(num_pages, B, copy_cap))
+    return KVQ_ERR_INVALID_ARG;
   if (!free_stack || !free_count || !page_tags || !page_shares || !block_table || !expected_tags)
     return KVQ_ERR_INVALID_ARG;
   if (!held || !n_moves || !workspace || (copy_cap > 0 && (!copy_src || !copy_dst)))

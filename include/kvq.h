@@ -227,6 +227,7 @@ KVQ_API kvq_status kvq_pages_update(int32_t *free_stack, int32_t *free_count, ui
  * the releases of kvq_pages_update push a page whoever else holds it.
  * Tags: a shared page keeps its tag, and a request that takes it expects that tag;
  * a page that is handed out, or moved to, gets a new one.
+ * num_pages, B and the lists' lengths are at most 2^30 (KVQ_ERR_INVALID_ARG).
  * workspace: 256-byte aligned, kvq_pages_workspace_size() bytes (0: bad sizes),
  * for the three calls alike; its contents need no preparation, and calls that can run
  * at the same time do not share it, nor the state.
