@@ -1579,6 +1579,7 @@ extern "C" kvq_status kvq_block_prefix_attn(
   if (Hq <= 0 || Hq % Hkv || max_q <= 0 || n_groups < 0 || !std::isfinite(sm_scale)) return KVQ_ERR_INVALID_ARG;
   const int G = Hq / Hkv;
   if (static_cast<int64_t>(n_tokens) * G > INT32_MAX / 2) return KVQ_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(n_groups) + B > 1 << 30) return KVQ_ERR_INVALID_ARG;  // px_plan walks both as one list
   const int64_t capacity = static_cast<int64_t>(MP) * cache->page_size;
   if (capacity > INT32_MAX - 255) return KVQ_ERR_INVALID_ARG;
   if (n_tokens == 0 || B == 0) return KVQ_OK;

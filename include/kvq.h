@@ -606,10 +606,10 @@ KVQ_API size_t kvq_block_prefix_attn_workspace_size(int32_t n_tokens, int32_t Hq
  * KVQ_ERRBIT_REQ, and every request's rows are zero.  An aborted request's own pages are not
  * read and its rows are zero; its group goes on.  A page outside the pool raises KVQ_ERRBIT_PAGE and zeroes the rows that see it, in
  * a prefix those of the whole group.  Rows of nobody are left as they were.
- * max_q, strides, scales and limits as in kvq_block_attn; rows times heads a kv head are at most
- * 2^30.  workspace: 256-byte aligned, kvq_block_prefix_attn_workspace_size() bytes for this many
- * rows or more, not shared by calls that can run at the same time; its contents need no
- * preparation. */
+ * max_q, strides, scales and limits as in kvq_block_attn; rows times heads a kv head, and
+ * requests and groups together, are at most 2^30.  workspace: 256-byte aligned,
+ * kvq_block_prefix_attn_workspace_size() bytes for this many rows or more, not shared by calls
+ * that can run at the same time; its contents need no preparation. */
 KVQ_API kvq_status kvq_block_prefix_attn(const kvq_block_cache *cache, const void *q,
                                          int64_t q_stride, int32_t Hq, const int32_t *tok_start,
                                          int32_t n_tokens, int32_t max_q, const int32_t *seq_lens,
