@@ -1,10 +1,11 @@
-"""kvq_pages_fork over a cluster of CTAs with forks that get nothing among those that are served, against
-pages_ref.py, every array equal."""
+"""kvq_pages_fork over a cluster of CTAs with forks that get nothing among those that are served, and sequences of
+forks, acquisitions, releases and compactions, against pages_ref.py, every array equal."""
 import numpy as np
 import pytest
+import torch
 
 import pages_ref as S
-from test_gpu_pages_shared import Both
+from test_gpu_pages_shared import Both, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +45,57 @@ def test_forks_of_many_blocks_that_get_nothing(kvq, seed):
     # and the state goes on: what was served is given back
     served = np.flatnonzero(ok)
     assert x.release(dst[served], None, -(-tok[served] // P)) == 0
+
+
+def grow(kvq, x, req, first, n):
+    """Pages for several requests by kvq_pages_update; those behind the first that does not fit get none."""
+    ok, err = torch.full((len(req),), 9, dtype=torch.uint8, device="cuda"), i32([0])
+    kvq.kvq_pages_update(x.state, acq_req=i32(req), acq_first=i32(first), acq_npages=i32(n), acq_ok=ok, err_word=err)
+    want = np.cumsum(n) <= x.h.free_count[0]
+    for b, f, m, w in zip(req, first, n, want):
+        if w:
+            S.acquire(x.h, b, f, m)
+    x.same("acquire")
+    assert np.array_equal(ok.cpu().numpy(), want) and (int(err.item()) == 0) == bool(want.all())
+    return want
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_sequences_with_acquisitions(kvq, seed):
+    """A run as a serving program makes it: prompts get pages, are forked, grow by pages of their own, end, and
+    the pool is moved together; on one CTA and on many.  Acquisitions know nothing of holders."""
+    rng = np.random.default_rng([51, seed])
+    B, MP = ((12, 20), (40, 9), (300, 40), (25, 400), (900, 12), (60, 64))[seed]
+    h = S.State(rng, B * MP // 3, B, MP)
+    x = Both(kvq, h)
+    tokens = np.zeros(B, dtype=np.int64)
+    did = dict.fromkeys(("grow", "fork", "release"), 0)
+    for step in range(16):
+        pages = -(-tokens // P)
+        idle, live = np.flatnonzero(pages == 0), np.flatnonzero(pages > 0)
+        what = ("grow", "fork", "grow", "release")[step % 4]
+        if what == "grow":
+            req = rng.permutation(B)[:max(1, B // 4)]
+            n = np.minimum(rng.integers(0, 1 + max(1, MP // 6), len(req)), MP - pages[req])
+            got = grow(kvq, x, req, pages[req], n)
+            tokens[req] = np.where(got & (n > 0), (pages[req] + n) * P - rng.integers(0, P, len(req)), tokens[req])
+        elif what == "fork" and len(live) and len(idle):
+            dst = rng.permutation(idle)[:max(1, len(idle) // 2)]
+            src = rng.choice(live, len(dst))
+            tok = (tokens[src] * rng.random(len(dst))).astype(np.int64)
+            tok[::2] = tokens[src[::2]]
+            got = x.fork(src, dst, tok, P)[2]
+            tokens[dst] = np.where(got, tok, 0)
+        elif what == "release" and len(live):
+            req = rng.permutation(live)[:max(1, len(live) // 2)]
+            keep = np.where(rng.random(len(req)) < 0.5, 0, pages[req] // 2)
+            assert x.release(req, keep, pages[req] - keep) == 0
+            tokens[req] = np.minimum(tokens[req], keep * P)
+        did[what] += 1
+        if step % 5 == 4:
+            x.compact(-(-tokens // P))
+        assert np.array_equal(x.h.shares, np.maximum(S.holders(x.h) - 1, 0))
+    assert all(did.values())
+    left = np.flatnonzero(tokens)
+    assert x.release(left, None, -(-tokens[left] // P)) == 0
+    assert x.h.free_count[0] == x.h.num_pages and not x.h.shares.any()
