@@ -17,6 +17,8 @@ CASES = {
     "three_rows": ([(900, [(1, 16), (1, 16), (1, 16)])], 8, 16, 64, 8, 1),
     "rows_of_a_warp_and_one": ([(9, [(6, 1 + 37 * (b % 6) + 5) for b in range(18)]) for _ in range(6)], 8, 64, 128, 6, 6),
     "own_tokens_of_few_rows": ([(0, [(1, 700), (3, 1500), (2, 90), (4, 4000)])], 2, 16, 128, 8, 33),
+    "prompts": ([(37, [(300, 300), (129, 700), (1, 40)]), (5, [(33, 33), (260, 261)])], 2, 32, 128, 3, 300),
+    "prompts_of_a_small_model": ([(50, [(200, 230), (31, 900), (65, 65)])], 3, 16, 64, 6, 200),
     "full_blocks": ([(300, [(1, 30)] * 64)], 2, 16, 128, 4, 17),
 }
 
