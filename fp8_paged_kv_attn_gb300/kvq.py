@@ -757,7 +757,7 @@ def pages_workspace(num_pages: int, B: int, device="cuda") -> torch.Tensor:
     """Allocate (with torch) a workspace for kvq_pages_fork, _release and _compact."""
     n = kvq_pages_workspace_size(num_pages, B)
     if n == 0:
-        raise ValueError("num_pages and B must be positive")
+        raise ValueError("num_pages and B must lie between 1 and 2^30")
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
