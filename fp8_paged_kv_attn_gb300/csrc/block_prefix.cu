@@ -698,24 +698,24 @@ __device__ __noinline__ float4 px_join(uint32_t o_addr, float *to, float4 s, boo
                       : (was.y == 0.f ? 0.f : was.y * exp2f(was.x - M)) + (s.y == 0.f ? 0.f : s.y * exp2f(s.x - M));
   const float2 f = bad ? make_float2(0.f, 0.f) : out_scale(N - M - 7.f, l);
 #pragma unroll 1
-  for (int c = 0; c < D; c += 16) {
-    float o[16];
-    tc_ld16(o, o_addr + c);
+  for (int c = 0; c < D; c += 32) {
+    float o[32];
+    tc_ld32(o, o_addr + c);
     if (!has) continue;
-    uint32_t w[8];
+    uint4 w[4];
+    uint32_t *u = reinterpret_cast<uint32_t *>(w);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       float4 v = *reinterpret_cast<const float4 *>(to + c + 4 * j);
       v = make_float4(v.x * x + o[4 * j] * y, v.y * x + o[4 * j + 1] * y, v.z * x + o[4 * j + 2] * y,
                       v.w * x + o[4 * j + 3] * y);
       if (!out) *reinterpret_cast<float4 *>(to + c + 4 * j) = v;
-      w[2 * j] = bad ? 0u : pack_bf16x2(v.x * f.x * f.y, v.y * f.x * f.y);
-      w[2 * j + 1] = bad ? 0u : pack_bf16x2(v.z * f.x * f.y, v.w * f.x * f.y);
+      u[2 * j] = bad ? 0u : pack_bf16x2(v.x * f.x * f.y, v.y * f.x * f.y);
+      u[2 * j + 1] = bad ? 0u : pack_bf16x2(v.z * f.x * f.y, v.w * f.x * f.y);
     }
-    if (out) {
-      *reinterpret_cast<uint4 *>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
-      *reinterpret_cast<uint4 *>(out + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-    }
+    if (out)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(out + c + 8 * j) = w[j];
   }
   if (has) *reinterpret_cast<float4 *>(to + D) = make_float4(M, l, N, out ? kDone : kHere);
   return make_float4(M, l, N, 0.f);
