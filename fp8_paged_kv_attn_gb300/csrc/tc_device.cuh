@@ -63,16 +63,17 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
                : "memory");
 }
 
-// Consecutive columns of this warp's 32 lanes.
+// Consecutive columns of this warp's 32 lanes, loaded and waited for in one statement, so that no use of
+// theirs moves between.
 __device__ __forceinline__ void tc_ld16(float (&v)[16], uint32_t addr) {
   uint32_t *r = reinterpret_cast<uint32_t *>(v);
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
-      "[%16];"
+      "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+      : "r"(addr)
+      : "memory");
 }
 
 __device__ __forceinline__ void tc_st16(uint32_t addr, const float (&v)[16]) {
